@@ -28,6 +28,7 @@ F8_ERR_TIMEOUT = 5
 F8_ERR_NONFINITE = 6
 F8_ERR_UNSUPPORTED = 7
 F8_ERR_BOUNDS = 8
+F8_ERR_INDEX = 9
 
 # every symbol include/f8.h declares
 EXPORTS = ("f8_amax", "f8_cast_transpose", "f8_gemm", "f8_linear_workspace_bytes",
@@ -39,7 +40,10 @@ EXPORTS = ("f8_amax", "f8_cast_transpose", "f8_gemm", "f8_linear_workspace_bytes
            "f8_quantize_swiglu_bwd", "f8_kernel_launches", "f8_selftest_bounds",
            "f8_gemm_grouped", "f8_quantize_multi", "f8_quantize_multi_workspace_bytes",
            "f8_linear_group_workspace_bytes", "f8_linear_fwd_group", "f8_linear_bwd_group",
-           "f8_transpose_u8", "f8_linear_fwd_qw", "f8_linear_fwd_qw_workspace_bytes")
+           "f8_transpose_u8", "f8_linear_fwd_qw", "f8_linear_fwd_qw_workspace_bytes",
+           "f8_norm_fwd", "f8_norm_bwd", "f8_norm_bwd_workspace_bytes", "f8_quantize_norm",
+           "f8_token_logprobs", "f8_token_logprobs_bwd", "f8_distill_fwd", "f8_distill_bwd",
+           "f8_distill_fwd_bwd")
 
 F8_MAX_GROUPED_GEMMS = 8
 F8_MAX_MULTI_TENSORS = 8
@@ -47,6 +51,13 @@ F8_MAX_GROUP_LINEARS = 4
 
 F8_E4M3 = 0
 F8_E5M2 = 1
+
+F8_BF16 = 0
+F8_F32 = 1
+F8_LAYER_NORM = 0
+F8_RMS_NORM = 1
+F8_MAX_TOP = 256
+F8_MAX_VOCAB = 1 << 22
 
 
 class F8Error(RuntimeError):
@@ -174,6 +185,29 @@ def lib() -> ctypes.CDLL:
         L.f8_linear_fwd_qw.argtypes = [vp, vp, i64, i64, i64, vp, ctypes.POINTER(_Saved), vp,
                                        ctypes.c_size_t, vp]
         L.f8_linear_fwd_qw.restype = st
+        f32, ci, sz = ctypes.c_float, ctypes.c_int, ctypes.c_size_t
+        L.f8_norm_fwd.argtypes = [vp, ci, vp, vp, ci, ci, i64, i64, f32, vp, vp, vp, vp, vp]
+        L.f8_norm_fwd.restype = st
+        L.f8_norm_bwd_workspace_bytes.argtypes = [i64, i64]
+        L.f8_norm_bwd_workspace_bytes.restype = sz
+        L.f8_norm_bwd.argtypes = [vp, vp, ci, vp, ci, vp, vp, ci, i64, i64, vp, vp, vp, vp, sz, vp]
+        L.f8_norm_bwd.restype = st
+        L.f8_quantize_norm.argtypes = [vp, vp, vp, ci, ci, i64, i64, f32, vp, vp, vp, vp, vp, vp, vp,
+                                       vp, sz, vp]
+        L.f8_quantize_norm.restype = st
+        L.f8_token_logprobs.argtypes = [vp, ci, i64, i64, i64, vp, f32, ci, vp, vp, vp, vp, vp, vp]
+        L.f8_token_logprobs.restype = st
+        L.f8_token_logprobs_bwd.argtypes = [vp, ci, i64, i64, i64, vp, vp, vp, vp, vp, f32, vp, i64,
+                                            vp, vp]
+        L.f8_token_logprobs_bwd.restype = st
+        L.f8_distill_fwd.argtypes = [vp, ci, i64, i64, i64, vp, vp, ci, f32, ci, vp, vp, vp, vp]
+        L.f8_distill_fwd.restype = st
+        L.f8_distill_bwd.argtypes = [vp, ci, i64, i64, i64, vp, vp, ci, f32, ci, vp, vp, vp, vp, i64,
+                                     vp, vp]
+        L.f8_distill_bwd.restype = st
+        L.f8_distill_fwd_bwd.argtypes = [vp, ci, i64, i64, i64, vp, vp, ci, f32, ci, vp, vp, vp, i64,
+                                         vp, vp]
+        L.f8_distill_fwd_bwd.restype = st
         _lib = L
         return L
 

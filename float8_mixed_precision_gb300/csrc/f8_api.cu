@@ -31,17 +31,6 @@ DeviceInfo g_dev[kMaxDevices];
 bool g_dev_ready[kMaxDevices];
 std::atomic<uint64_t> g_wait_limit_ns{kDefaultWaitLimitNs};
 
-bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
-f8_status from_cuda(cudaError_t e)
-{
-    if (e == cudaSuccess)
-        return F8_OK;
-    if (e == cudaErrorNotSupported)
-        return F8_ERR_UNSUPPORTED;
-    return F8_ERR_CUDA;
-}
-
 size_t round256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 // The GEMM kernels number the output tiles of a launch (128 x 256 at the
@@ -261,18 +250,6 @@ using namespace f8;
 
 namespace {
 
-// The kernels are built for sm_103a only; refuse anything else up front.
-f8_status get_device(const DeviceInfo **out)
-{
-    const DeviceInfo *d = device_info();
-    if (d == nullptr)
-        return F8_ERR_CUDA;
-    if (d->cc_major != 10 || d->cc_minor != 3)
-        return F8_ERR_UNSUPPORTED;
-    *out = d;
-    return F8_OK;
-}
-
 f8_status check_cast_args(const void *x, int64_t rows, int64_t cols, const float *amax,
                           const float *scale_out, const uint8_t *q, const uint8_t *q_t)
 {
@@ -304,15 +281,6 @@ f8_status check_gemm_args(const uint8_t *a, const uint8_t *b, int64_t M, int64_t
         return F8_ERR_ALIGN;
     return F8_OK;
 }
-
-#define F8_TRY(expr)                                                                               \
-    do {                                                                                           \
-        f8_status st_ = (expr);                                                                    \
-        if (st_ != F8_OK)                                                                          \
-            return st_;                                                                            \
-    } while (0)
-
-#define F8_TRY_CUDA(expr) F8_TRY(from_cuda(expr))
 
 } // namespace
 
@@ -356,6 +324,7 @@ const char *f8_status_string(f8_status s)
     case F8_ERR_NONFINITE: return "F8_ERR_NONFINITE: non-finite value in an amax input";
     case F8_ERR_UNSUPPORTED: return "F8_ERR_UNSUPPORTED: needs an sm_103 device and driver";
     case F8_ERR_BOUNDS: return "F8_ERR_BOUNDS: an index left its buffer (checked build)";
+    case F8_ERR_INDEX: return "F8_ERR_INDEX: a token id lies outside the vocabulary";
     }
     return "F8_ERR_UNKNOWN";
 }
@@ -968,6 +937,8 @@ f8_status f8_last_device_status(void *stream)
         return F8_ERR_BOUNDS;
     if (word & kStatusTimeout)
         return F8_ERR_TIMEOUT;
+    if (word & kStatusIndex)
+        return F8_ERR_INDEX;
     if (word & kStatusNonfinite)
         return F8_ERR_NONFINITE;
     return F8_OK;

@@ -25,6 +25,43 @@ struct DeviceInfo {
 // Returns nullptr if the device cannot be queried.
 const DeviceInfo *device_info();
 
+// What the entry points share: pointer alignment (a a power of two), the
+// status of a CUDA error, early return on a status, and the current device
+// (the kernels are built for sm_103a only; anything else is refused up front).
+inline bool aligned(const void *p, uintptr_t a)
+{
+    return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0;
+}
+
+inline f8_status from_cuda(cudaError_t e)
+{
+    if (e == cudaSuccess)
+        return F8_OK;
+    if (e == cudaErrorNotSupported)
+        return F8_ERR_UNSUPPORTED;
+    return F8_ERR_CUDA;
+}
+
+#define F8_TRY(expr)                                                                               \
+    do {                                                                                           \
+        f8_status st_ = (expr);                                                                    \
+        if (st_ != F8_OK)                                                                          \
+            return st_;                                                                            \
+    } while (0)
+
+#define F8_TRY_CUDA(expr) F8_TRY(f8::from_cuda(expr))
+
+inline f8_status get_device(const DeviceInfo **out)
+{
+    const DeviceInfo *d = device_info();
+    if (d == nullptr)
+        return F8_ERR_CUDA;
+    if (d->cc_major != 10 || d->cc_minor != 3)
+        return F8_ERR_UNSUPPORTED;
+    *out = d;
+    return F8_OK;
+}
+
 // Time limit of the GEMM pipeline's device waits.
 uint64_t wait_limit_ns();
 

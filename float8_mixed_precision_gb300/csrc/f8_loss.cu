@@ -1,0 +1,1692 @@
+// What stands behind a head linear: log probabilities of given tokens with
+// entropy and top alternatives, and the distillation loss against a teacher's
+// top logits, forward and backward.
+//
+// Every kernel walks rows of the logits [rows, vocab], z = logits / T, and is
+// bound by HBM: one value read per element forward, one more written backward.
+// A row is walked in 16-byte chunks on 16-byte boundaries.  The loops take the
+// whole ones; the first and the last chunk of a row that starts or ends inside
+// one (the edges) are read element by element by one thread each.
+//
+// Softmax statistics, one pass: a thread keeps (m, s, h) with m the largest
+// logit so far, s = sum e^((x - m) / T) and, for the entropy, h = sum e^d d (d
+// in units of log 2), rescaled when m grows.  Pairs join as
+//   M = max(m1, m2), f_i = 2^((m_i - M) c), s = s1 f1 + s2 f2,
+//   h = f1 (h1 + s1 (m1 - M) c) + f2 (...),   c = log2(e) / T,
+// in a fixed order (lanes, warps, blocks of a cluster): equal inputs give
+// equal bits.  Then lse = M / T + ln s and entropy = ln s - ln 2 h / s, sums of
+// terms of one sign.
+//
+// A row goes to one block, or where there are fewer rows than keep the SMs busy
+// to a cluster of up to eight, each with a stretch of it, joined in the first
+// block's shared memory.
+#include <cooperative_groups.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+#include <mutex>
+
+#include "f8_internal.h"
+#include "f8_ptx.cuh"
+
+namespace f8 {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kMaxCluster = 8;
+constexpr float kLn2 = 0.693147180559945309f;
+constexpr double kLog2e = 1.44269504088896340736;
+// below any exponent that 2^x tells from 0 in fp32; keeps 0 * d finite
+constexpr float kFloor2 = -1.0e4f;
+// past this an fp32 log-sum-exp no longer tells a row's tokens apart
+constexpr float kMaxLse = 16777216.0f;
+#define F8_NEG_INF __int_as_float(0xff800000)
+#define F8_POS_INF __int_as_float(0x7f800000)
+#define F8_NAN __int_as_float(0x7fffffff)
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// ------------------------------------------------------------ rows in chunks
+template <typename T>
+struct Chunk {
+    static constexpr int E = 16 / static_cast<int>(sizeof(T));  // elements
+};
+
+// One row as 16-byte chunks: chunk c holds elements c * E - off + [0, E).
+template <typename T>
+struct Row {
+    const T *base;    // chunk 0, on a 16-byte boundary
+    int64_t at;       // the row's first element in the whole buffer
+    int off, vocab;
+    int nch, w0, w1;  // chunks, and the whole ones among them: [w0, w1)
+
+    __device__ __forceinline__ Row(const T *p, int64_t row, int64_t ld, int v)
+    {
+        const T *r = p + row * ld;
+        constexpr int E = Chunk<T>::E;
+        off = static_cast<int>((reinterpret_cast<uintptr_t>(r) & 15u) / sizeof(T));
+        base = r - off;
+        at = row * ld;
+        vocab = v;
+        nch = (off + v + E - 1) / E;
+        w0 = off > 0 ? 1 : 0;
+        w1 = max(w0, (off + v) / E);
+    }
+    __device__ __forceinline__ bool whole(int c) const { return c >= w0 && c < w1; }
+    // edge i (0: the first chunk, 1: the last) that lies in chunks [c0, c1), or -1
+    __device__ __forceinline__ int edge(int i, int c0, int c1) const
+    {
+        const int c = i == 0 ? 0 : nch - 1;
+        const bool is = i < 2 && !whole(c) && (i == 0 || c > 0);
+        return is && c >= c0 && c < c1 ? c : -1;
+    }
+};
+
+// Threads that take the edges of their block's stretch: lane 0 of two warps.
+__device__ __forceinline__ int edge_of_thread()
+{
+    return (threadIdx.x & 31) == 0 ? static_cast<int>(threadIdx.x >> 5) : 2;
+}
+
+__device__ __forceinline__ uint4 neg_inf_chunk(__nv_bfloat16)
+{
+    return make_uint4(0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u);
+}
+__device__ __forceinline__ uint4 neg_inf_chunk(float)
+{
+    return make_uint4(0xFF800000u, 0xFF800000u, 0xFF800000u, 0xFF800000u);
+}
+
+// Chunk c if it is a whole one below `end`, else -inf.
+template <typename T>
+__device__ __forceinline__ uint4 load_chunk(const Row<T> &r, int c, int end, int64_t total,
+                                            unsigned *status)
+{
+    constexpr int E = Chunk<T>::E;
+    uint4 v = neg_inf_chunk(T());
+    if (c >= r.w0 && c < min(end, r.w1) &&
+        in_range(r.at - r.off + static_cast<int64_t>(c) * E, E, total, status))
+        v = *reinterpret_cast<const uint4 *>(r.base + static_cast<int64_t>(c) * E);
+    return v;
+}
+
+template <typename T>
+__device__ __forceinline__ float as_float(T x);
+template <>
+__device__ __forceinline__ float as_float<__nv_bfloat16>(__nv_bfloat16 x)
+{
+    return __bfloat162float(x);
+}
+template <>
+__device__ __forceinline__ float as_float<float>(float x)
+{
+    return x;
+}
+
+// An edge chunk's elements inside the row, -inf elsewhere.
+template <typename T>
+__device__ __forceinline__ void load_edge(const Row<T> &r, int c, float (&f)[Chunk<T>::E],
+                                          int64_t total, unsigned *status)
+{
+    constexpr int E = Chunk<T>::E;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        const int v = c * E + e - r.off;
+        f[e] = F8_NEG_INF;
+        if (v >= 0 && v < r.vocab && in_range(r.at + v, 1, total, status))
+            f[e] = as_float(r.base[r.off + v]);
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ void unpack(uint4 v, float (&f)[Chunk<T>::E]);
+template <>
+__device__ __forceinline__ void unpack<__nv_bfloat16>(uint4 v, float (&f)[8])
+{
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f[2 * i] = __uint_as_float(w[i] << 16);
+        f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+}
+template <>
+__device__ __forceinline__ void unpack<float>(uint4 v, float (&f)[4])
+{
+    f[0] = __uint_as_float(v.x), f[1] = __uint_as_float(v.y);
+    f[2] = __uint_as_float(v.z), f[3] = __uint_as_float(v.w);
+}
+
+template <typename T>
+__device__ __forceinline__ uint4 pack(const float (&f)[Chunk<T>::E]);
+template <>
+__device__ __forceinline__ uint4 pack<__nv_bfloat16>(const float (&f)[8])
+{
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        __nv_bfloat162 h = __float22bfloat162_rn(make_float2(f[2 * i], f[2 * i + 1]));
+        w[i] = *reinterpret_cast<uint32_t *>(&h);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+template <>
+__device__ __forceinline__ uint4 pack<float>(const float (&f)[4])
+{
+    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
+                      __float_as_uint(f[3]));
+}
+
+template <int E>
+__device__ __forceinline__ float max_of(const float (&f)[E])
+{
+    float m = f[0];
+#pragma unroll
+    for (int e = 1; e < E; ++e)
+        m = fmaxf(m, f[e]);
+    return m;
+}
+
+// ------------------------------------------------------------ softmax sums
+struct Stats {
+    float m, s, h;  // h only where the entropy is wanted
+};
+
+__device__ __forceinline__ Stats stats_empty() { return Stats{F8_NEG_INF, 0.0f, 0.0f}; }
+
+template <bool ENT>
+__device__ __forceinline__ Stats join(Stats a, Stats b, float c)
+{
+    const float M = fmaxf(a.m, b.m);
+    // -inf - -inf is NaN here, which fmaxf turns into the floor: factor 0
+    const float da = fmaxf((a.m - M) * c, kFloor2), db = fmaxf((b.m - M) * c, kFloor2);
+    const float fa = ex2(da), fb = ex2(db);
+    Stats r;
+    r.m = M;
+    r.s = a.s * fa + b.s * fb;
+    r.h = ENT ? fa * fmaf(a.s, da, a.h) + fb * fmaf(b.s, db, b.h) : 0.0f;
+    return r;
+}
+
+// Adds N values to the running sums.
+template <bool ENT, int N>
+__device__ __forceinline__ void add_values(Stats &t, const float (&f)[N], float c)
+{
+    const float bm = max_of(f);
+    if (bm > t.m) {
+        const float d = fmaxf((t.m - bm) * c, kFloor2);
+        const float r = ex2(d);
+        if (ENT)
+            t.h = r * fmaf(t.s, d, t.h);
+        t.s *= r;
+        t.m = bm;
+    }
+    const float m = t.m == F8_NEG_INF ? 0.0f : t.m;
+    float s0 = 0.0f, s1 = 0.0f, h0 = 0.0f, h1 = 0.0f;
+#pragma unroll
+    for (int e = 0; e < N; e += 2) {
+        const float d0 = (f[e] - m) * c, d1 = (f[e + 1] - m) * c;
+        const float e0 = ex2(d0), e1 = ex2(d1);
+        s0 += e0;
+        s1 += e1;
+        if (ENT) {
+            h0 = fmaf(e0, fmaxf(d0, kFloor2), h0);
+            h1 = fmaf(e1, fmaxf(d1, kFloor2), h1);
+        }
+    }
+    t.s += s0 + s1;
+    if (ENT)
+        t.h += h0 + h1;
+}
+
+// The block's sums, in every thread.  `red`: one Stats per warp.
+template <bool ENT, int WARPS>
+__device__ __forceinline__ Stats block_join(Stats t, float c, Stats *red)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        Stats u;
+        u.m = __shfl_xor_sync(0xFFFFFFFFu, t.m, o);
+        u.s = __shfl_xor_sync(0xFFFFFFFFu, t.s, o);
+        u.h = ENT ? __shfl_xor_sync(0xFFFFFFFFu, t.h, o) : 0.0f;
+        // lower lane first on both sides, so that all lanes get equal bits
+        t = (threadIdx.x & o) ? join<ENT>(u, t, c) : join<ENT>(t, u, c);
+    }
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0)
+        red[threadIdx.x >> 5] = t;
+    __syncthreads();
+    t = red[0];
+#pragma unroll 1
+    for (int w = 1; w < WARPS; ++w)
+        t = join<ENT>(t, red[w], c);
+    return t;
+}
+
+// Sum, or maximum, of one value per thread, in every thread, in a fixed order.
+template <int WARPS>
+__device__ __forceinline__ float block_sum(float v, float *red)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0)
+        red[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = 0.0f;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w)
+        v += red[w];
+    return v;
+}
+
+template <int WARPS>
+__device__ __forceinline__ float block_max(float v, float *red)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0)
+        red[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = red[0];
+#pragma unroll
+    for (int w = 1; w < WARPS; ++w)
+        v = fmaxf(v, red[w]);
+    return v;
+}
+
+// ------------------------------------------------------------ clusters
+// A block of a cluster may write another's shared memory once that block has
+// started (cluster_started, an arrive at the kernel's start and a wait before
+// the first write) and until cluster_join, after which the writes can be read.
+__device__ __forceinline__ void cluster_start()
+{
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_started()
+{
+    __syncwarp();
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_join()
+{
+    __syncwarp();
+    cluster_sync();
+}
+// The same shared variable in block `rank` of the cluster.
+template <typename P>
+__device__ __forceinline__ P *peer(P *p, unsigned rank)
+{
+    return cooperative_groups::this_cluster().map_shared_rank(p, rank);
+}
+
+// ------------------------------------------------------------ top k
+// fp32 values as unsigned keys of the same order, never 0; -0 counts as +0.
+__device__ __forceinline__ uint32_t order_key(float x)
+{
+    const uint32_t b = __float_as_uint(x + 0.0f);
+    const uint32_t k = b ^ ((b >> 31) ? 0xFFFFFFFFu : 0x80000000u);
+    return k ? k : 1u;
+}
+__device__ __forceinline__ float key_value(uint32_t k)
+{
+    return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xFFFFFFFFu));
+}
+
+// How many of the n keys are >= t; `red`: one word per warp.
+__device__ __forceinline__ int count_from(const uint32_t *keys, int n, uint32_t t, int *red)
+{
+    int c = 0;
+    for (int i0 = 0; i0 < n; i0 += kThreads) {
+        const int i = i0 + static_cast<int>(threadIdx.x);
+        c += __popc(__ballot_sync(0xFFFFFFFFu, i < n && keys[i] >= t));
+    }
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0)
+        red[threadIdx.x >> 5] = c;
+    __syncthreads();
+    c = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w)
+        c += red[w];
+    return c;
+}
+
+// The positions of the k largest of n keys in shared memory (equal keys: the
+// lower positions), ascending, in out[0 .. min(k, n)).  The threshold is found
+// by bisection over the key range; n < 2^16.
+__device__ __forceinline__ void block_select(const uint32_t *keys, int n, int k, int *out, int *red)
+{
+    const int tid = threadIdx.x, lane = tid & 31;
+    if (n <= k) {
+        for (int i = tid; i < n; i += kThreads)
+            out[i] = i;
+        __syncthreads();
+        return;
+    }
+    uint32_t lo = 0xFFFFFFFFu, hi = 0;
+    for (int i = tid; i < n; i += kThreads) {
+        lo = min(lo, keys[i]);
+        hi = max(hi, keys[i]);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        lo = min(lo, __shfl_xor_sync(0xFFFFFFFFu, lo, o));
+        hi = max(hi, __shfl_xor_sync(0xFFFFFFFFu, hi, o));
+    }
+    __syncthreads();
+    if (lane == 0) {
+        red[tid >> 5] = static_cast<int>(lo);
+        red[kWarps + (tid >> 5)] = static_cast<int>(hi);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        lo = min(lo, static_cast<uint32_t>(red[w]));
+        hi = max(hi, static_cast<uint32_t>(red[kWarps + w]));
+    }
+    // at least k keys are >= lo, fewer than k are > hi
+    while (lo < hi) {
+        const uint32_t mid = lo + (hi - lo) / 2 + 1;
+        const int c = count_from(keys, n, mid, red);
+        if (c >= k)
+            lo = mid;
+        else
+            hi = mid - 1;
+        if (c == k)
+            break;
+    }
+    // every key > lo, and the first of those == lo until k are found
+    const int per = (n + kThreads - 1) / kThreads;
+    const int i0 = min(n, tid * per), i1 = min(n, i0 + per);
+    int gt = 0, eq = 0;
+#pragma unroll 1
+    for (int i = i0; i < i1; ++i) {
+        gt += keys[i] > lo ? 1 : 0;
+        eq += keys[i] == lo ? 1 : 0;
+    }
+    const int packed = (gt << 16) | eq;  // exclusive sums over the block
+    int incl = packed;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+        incl += lane >= o ? u : 0;
+    }
+    __syncthreads();
+    if (lane == 31)
+        red[tid >> 5] = incl;
+    __syncthreads();
+    int before = incl - packed, all = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        before += w < (tid >> 5) ? red[w] : 0;
+        all += red[w];
+    }
+    const int need = k - (all >> 16);
+    int a = before >> 16, b = before & 0xFFFF;
+#pragma unroll 1
+    for (int i = i0; i < i1; ++i) {
+        if (keys[i] > lo) {
+            out[a + min(b, need)] = i;
+            ++a;
+        } else if (keys[i] == lo) {
+            if (b < need)
+                out[a + b] = i;
+            ++b;
+        }
+    }
+    __syncthreads();
+}
+
+// Shared memory of the top-k stage, in 4-byte words; every part starts on a
+// 16-byte boundary.
+struct TopLayout {
+    int groups, list, keys, pick, merge_key, merge_id, words;
+};
+__host__ __device__ inline int words4(int n) { return (n + 3) & ~3; }
+__host__ __device__ inline TopLayout top_layout(int ngroups, int k, int cluster)
+{
+    TopLayout l;
+    l.groups = 0;                         // one key per group of 32 chunks
+    l.list = l.groups + words4(ngroups);  // k positions
+    l.keys = l.list + words4(k);          // 32 k chunk keys, then E k element keys
+    l.pick = l.keys + 32 * k;             // k chunks
+    l.merge_key = l.pick + words4(k);
+    l.merge_id = l.merge_key + words4(cluster * k);
+    l.words = l.merge_id + words4(cluster * k);
+    return l;
+}
+
+// ------------------------------------------------------------ log probabilities
+struct LogprobArgs {
+    const void *logits;
+    int64_t rows, ld;
+    int vocab, top_k, cluster;
+    const int64_t *tokens;
+    float inv_t, c;  // 1 / T, log2(e) / T
+    float *logp, *entropy, *lse;
+    int32_t *top_ids;
+    float *top_logp;
+    unsigned *status;
+};
+
+constexpr int kUnroll = 4;  // chunks in flight per thread
+
+// TOP: the maximum of every 32 consecutive chunks (what one warp loads at once)
+// is kept in shared memory.  The k largest elements of a row lie in the k
+// groups with the largest maxima (equal ones: the lower groups), so the second
+// step looks at 32 k chunks, the third at the k best of those: exact for any
+// input, and the row is read once plus k groups from L2.
+template <typename T, bool TOP>
+__global__ void __launch_bounds__(kThreads)
+logprobs_kernel(const __grid_constant__ LogprobArgs a)
+{
+    constexpr int E = Chunk<T>::E;
+    extern __shared__ __align__(16) uint32_t dyn[];
+    __shared__ Stats red[kWarps];
+    __shared__ Stats parts[kMaxCluster];
+    __shared__ int sred[2 * kWarps];
+    griddep_wait();
+    griddep_launch_dependents();
+    const int C = a.cluster;
+    const int64_t row = blockIdx.x / C;
+    const int rank = static_cast<int>(blockIdx.x % C);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int64_t tok = a.tokens != nullptr ? a.tokens[row] : 0;
+    if (tok < 0) {  // the whole cluster leaves
+        if (rank == 0) {
+            if (tid == 0) {
+                if (a.logp != nullptr)
+                    a.logp[row] = 0.0f;
+                if (a.entropy != nullptr)
+                    a.entropy[row] = 0.0f;
+                if (a.lse != nullptr)
+                    a.lse[row] = 0.0f;
+            }
+            if (TOP && tid < a.top_k) {
+                a.top_ids[row * a.top_k + tid] = -1;
+                a.top_logp[row * a.top_k + tid] = F8_NEG_INF;
+            }
+        }
+        return;
+    }
+    if (C > 1)
+        cluster_start();
+    const Row<T> r(static_cast<const T *>(a.logits), row, a.ld, a.vocab);
+    const int64_t total = (a.rows - 1) * a.ld + a.vocab;
+    // groups of 32 chunks, dealt to the cluster's blocks in stretches
+    const int ngroups = (r.nch + 31) / 32;
+    const int per = (ngroups + C - 1) / C;
+    const int g0 = min(ngroups, rank * per), g1 = min(ngroups, g0 + per);
+    const int per_max = ((r.vocab + E - 1 + E) / E + 31) / 32;  // any row offset
+    const TopLayout lay = top_layout((per_max + C - 1) / C, a.top_k, C);
+    uint32_t *gkeys = dyn + lay.groups;
+
+    Stats t = stats_empty();
+    for (int g = g0 + warp * kUnroll; g < g1; g += kWarps * kUnroll) {
+        uint4 v[kUnroll];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u)
+            v[u] = load_chunk(r, (g + u) * 32 + lane, g1 * 32, total, a.status);
+        float f[kUnroll * E];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            float x[E];
+            unpack<T>(v[u], x);
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                f[u * E + e] = x[e];
+            if (TOP) {
+                const uint32_t key = __reduce_max_sync(0xFFFFFFFFu, order_key(max_of(x)));
+                if (lane == 0 && g + u < g1)
+                    gkeys[g + u - g0] = key;
+            }
+        }
+        add_values<true>(t, f, a.c);
+    }
+    if (TOP)
+        __syncthreads();
+    const int ec = r.edge(edge_of_thread(), g0 * 32, g1 * 32);
+    if (ec >= 0) {
+        float x[E];
+        load_edge(r, ec, x, total, a.status);
+        add_values<true>(t, x, a.c);
+        if (TOP)
+            atomicMax(&gkeys[ec / 32 - g0], order_key(max_of(x)));
+    }
+    t = block_join<true, kWarps>(t, a.c, red);
+
+    // the block's own k best: ids and keys into the leader's merge arrays
+    if (TOP) {
+        int *list = reinterpret_cast<int *>(dyn + lay.list);
+        uint32_t *keys = dyn + lay.keys;
+        const int k = a.top_k;
+        const int v0 = g0 * 32 * E - r.off, v1 = min(g1 * 32 * E - r.off, r.vocab);
+        const int have = max(0, min(k, v1 - max(v0, 0)));
+        __syncthreads();
+        block_select(gkeys, g1 - g0, k, list, sred);
+        const int ng = min(k, g1 - g0);
+        for (int i = tid; i < ng * 32; i += kThreads) {
+            const int ch = (g0 + list[i >> 5]) * 32 + (i & 31);
+            uint32_t key = 0;
+            if (ch < r.nch) {
+                float x[E];
+                if (r.whole(ch))
+                    unpack<T>(load_chunk(r, ch, r.nch, total, a.status), x);
+                else
+                    load_edge(r, ch, x, total, a.status);
+                key = order_key(max_of(x));
+            }
+            keys[i] = key;
+        }
+        __syncthreads();
+        // positions among the candidate chunks, then their chunk numbers
+        int *pick = reinterpret_cast<int *>(dyn + lay.pick);
+        block_select(keys, ng * 32, k, pick, sred);
+        const int nc = min(k, ng * 32);
+        for (int i = tid; i < nc; i += kThreads)
+            pick[i] = (g0 + list[pick[i] >> 5]) * 32 + (pick[i] & 31);
+        __syncthreads();
+        for (int i = tid; i < nc * E; i += kThreads) {
+            const int v = pick[i / E] * E + i % E - r.off;
+            keys[i] = v >= 0 && v < r.vocab
+                          ? order_key(as_float(r.base[pick[i / E] * static_cast<int64_t>(E) + i % E]))
+                          : 0u;
+        }
+        __syncthreads();
+        block_select(keys, nc * E, have, list, sred);
+        uint32_t *mk = dyn + lay.merge_key + rank * k, *mi = dyn + lay.merge_id + rank * k;
+        if (C > 1) {
+            cluster_started();
+            mk = peer(mk, 0);
+            mi = peer(mi, 0);
+        }
+        for (int i = tid; i < k; i += kThreads) {
+            uint32_t key = 0, id = 0x7FFFFFFFu;
+            if (i < have) {
+                key = keys[list[i]];
+                id = pick[list[i] / E] * E + list[i] % E - r.off;
+            }
+            mk[i] = key;
+            mi[i] = id;
+        }
+    } else if (C > 1) {
+        cluster_started();
+    }
+    if (C > 1) {
+        if (tid == 0)
+            *peer(&parts[rank], 0) = t;
+        cluster_join();
+        if (rank != 0)
+            return;
+        t = parts[0];
+        for (int i = 1; i < C; ++i)
+            t = join<true>(t, parts[i], a.c);
+    } else {
+        __syncthreads();
+    }
+
+    const bool none = t.m == F8_NEG_INF && t.s == 0.0f;
+    const float ls = logf(t.s);
+    float lse = fmaf(t.m, a.inv_t, ls);
+    if (t.s != t.s || t.m == F8_POS_INF) {
+        lse = F8_NAN;
+        if (tid == 0)
+            atomicOr(a.status, kStatusNonfinite);
+    }
+    if (none)
+        lse = F8_NEG_INF;
+    if (tid == 0) {
+        if (a.lse != nullptr)
+            a.lse[row] = lse;
+        if (a.entropy != nullptr)
+            a.entropy[row] = none ? 0.0f : (lse != lse ? F8_NAN : ls - kLn2 * t.h / t.s);
+        if (a.logp != nullptr) {
+            // from the difference to the maximum: |logits| does not cancel
+            float lp = F8_NAN;
+            if (tok >= r.vocab)
+                atomicOr(a.status, kStatusIndex);
+            else if (none)
+                lp = F8_NEG_INF;
+            else if (lse == lse)
+                lp = (as_float(r.base[r.off + tok]) - t.m) * a.inv_t - ls;
+            a.logp[row] = lp;
+        }
+    }
+    if (TOP) {
+        const int k = a.top_k;
+        int *list = reinterpret_cast<int *>(dyn + lay.list);
+        const uint32_t *mk = dyn + lay.merge_key;
+        const uint32_t *mi = dyn + lay.merge_id;
+        __syncthreads();
+        block_select(mk, C * k, k, list, sred);
+        // descending order: the rank of each among the k
+        for (int i = tid; i < k; i += kThreads) {
+            const uint32_t key = mk[list[i]];
+            int place = 0;
+            for (int j = 0; j < k; ++j) {
+                const uint32_t o = mk[list[j]];
+                place += (o > key || (o == key && j < i)) ? 1 : 0;
+            }
+            a.top_ids[row * k + place] = static_cast<int32_t>(mi[list[i]]);
+            a.top_logp[row * k + place] =
+                none ? F8_NEG_INF
+                     : (lse != lse ? F8_NAN : (key_value(key) - t.m) * a.inv_t - ls);
+        }
+    }
+}
+
+// ------------------------------------------------------------ gradients' output
+struct OutArgs {
+    void *p;
+    int64_t ld;
+    unsigned *amax;
+};
+
+// Elements of chunk c that lie in the row, one by one.
+template <typename T>
+__device__ __forceinline__ uint32_t store_elements(const Row<T> &r, T *out, int c,
+                                                   const float (&f)[Chunk<T>::E], int64_t out_at,
+                                                   int64_t out_total, unsigned *status)
+{
+    constexpr int E = Chunk<T>::E;
+    uint32_t m2 = 0;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        const int i = c * E + e - r.off;
+        const T v = static_cast<T>(f[e]);
+        if (i >= 0 && i < r.vocab && in_range(out_at + i, 1, out_total, status)) {
+            out[i] = v;
+            if (sizeof(T) == 2)
+                m2 = __vmaxu2(m2, (__float_as_uint(as_float(v)) >> 16) & 0x7FFFu);
+        }
+    }
+    return m2;
+}
+
+// Writes a whole chunk of a row's gradient: one vector where the output row
+// has the input row's offset, else element by element.  Returns the magnitude
+// bits of the stored bf16 values as a maximum over u16 pairs.
+template <typename T>
+__device__ __forceinline__ uint32_t store_chunk(const Row<T> &r, T *out, bool same, int c,
+                                                const float (&f)[Chunk<T>::E], int64_t out_at,
+                                                int64_t out_total, unsigned *status)
+{
+    constexpr int E = Chunk<T>::E;
+    if (!same)
+        return store_elements(r, out, c, f, out_at, out_total, status);
+    const uint4 v = pack<T>(f);
+    const int64_t i = static_cast<int64_t>(c) * E - r.off;
+    if (in_range(out_at + i, E, out_total, status))
+        *reinterpret_cast<uint4 *>(out + i) = v;
+    if (sizeof(T) != 2)
+        return 0;
+    return __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu),
+                    __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu));
+}
+
+// Zeros in columns [from, to) of an output row, by the threads of one block.
+template <typename T>
+__device__ __forceinline__ void zero_columns(T *out, int64_t from, int64_t to, int64_t out_at,
+                                             int64_t out_total, unsigned *status)
+{
+    for (int64_t i = from + threadIdx.x; i < to; i += blockDim.x)
+        if (in_range(out_at + i, 1, out_total, status))
+            out[i] = T(0.0f);
+}
+
+// One atomicMax per block on the fp32 pattern of a zeroed word (the result
+// does not depend on the order).
+__device__ __forceinline__ void block_amax(uint32_t m2, unsigned *amax, unsigned *status)
+{
+    __shared__ unsigned blk;
+    if (amax == nullptr)
+        return;
+    __syncthreads();
+    if (threadIdx.x == 0)
+        blk = 0;
+    __syncthreads();
+    const unsigned m = __reduce_max_sync(0xFFFFFFFFu, max(m2 & 0xFFFFu, m2 >> 16));
+    if ((threadIdx.x & 31) == 0)
+        atomicMax(&blk, m);
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        if (blk >= 0x7F80u)
+            atomicOr(status, kStatusNonfinite);
+        atomicMax(amax, blk << 16);
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ bool same_offset(const Row<T> &r, const T *out)
+{
+    return static_cast<int>((reinterpret_cast<uintptr_t>(out) & 15u) / sizeof(T)) == r.off;
+}
+
+// Chunks per block of the backward kernels.
+constexpr int kBwdChunks = 8 * kThreads;
+
+// ------------------------------------------------------------ log probabilities, backward
+struct LogprobBwdArgs {
+    const void *logits;
+    int64_t rows, ld;
+    int vocab, blocks_per_row;
+    const int64_t *tokens;
+    const float *lse, *entropy, *dlogp, *dentropy;
+    float inv_t;
+    OutArgs out;
+    unsigned *status;
+};
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads)
+logprobs_bwd_kernel(const __grid_constant__ LogprobBwdArgs a)
+{
+    constexpr int E = Chunk<T>::E;
+    griddep_wait();
+    griddep_launch_dependents();
+    const int64_t row = blockIdx.x / a.blocks_per_row;
+    const int part = static_cast<int>(blockIdx.x % a.blocks_per_row);
+    const Row<T> r(static_cast<const T *>(a.logits), row, a.ld, a.vocab);
+    const int64_t total = (a.rows - 1) * a.ld + a.vocab;
+    T *out = static_cast<T *>(a.out.p) + row * a.out.ld;
+    const int64_t out_at = row * a.out.ld, out_total = a.rows * a.out.ld;
+    const int64_t tok = a.tokens != nullptr ? a.tokens[row] : -1;
+    const float ga = a.dlogp != nullptr && a.tokens != nullptr ? a.dlogp[row] : 0.0f;
+    const float gh = a.dentropy != nullptr ? a.dentropy[row] : 0.0f;
+    const float lse = a.lse[row];
+    const bool skip = (a.tokens != nullptr && tok < 0) || (ga == 0.0f && gh == 0.0f) ||
+                      fabsf(lse) >= kMaxLse;
+    const bool same = same_offset(r, out);
+    const float H = gh != 0.0f ? a.entropy[row] : 0.0f;
+    const float fa = ga * a.inv_t, fh = gh * a.inv_t;
+    uint32_t m2 = 0;
+    if (tok >= r.vocab && threadIdx.x == 0)
+        atomicOr(a.status, kStatusIndex);
+    const int c0 = part * kBwdChunks, c1 = min(r.nch, c0 + kBwdChunks);
+    // the gradient of one chunk in place of its logits
+    auto gradient = [&](int ch, float (&f)[E]) {
+        const int64_t first = static_cast<int64_t>(ch) * E - r.off;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const float lp = fmaf(f[e], a.inv_t, -lse);
+            const float p = ex2(lp * static_cast<float>(kLog2e));
+            // p (lp + H) is 0 for a masked token, whose lp is -inf
+            const float q = p * (fmaxf(lp, kFloor2) + H);
+            const float g = (tok == first + e ? fa : 0.0f) - fmaf(fa, p, fh * q);
+            f[e] = skip ? 0.0f : g;
+        }
+    };
+    for (int cb = max(c0, r.w0) + static_cast<int>(threadIdx.x); cb < min(c1, r.w1);
+         cb += kUnroll * kThreads) {
+        uint4 v[kUnroll];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u)
+            v[u] = load_chunk(r, cb + u * kThreads, skip ? 0 : c1, total, a.status);
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            const int ch = cb + u * kThreads;
+            if (ch < min(c1, r.w1)) {
+                float f[E];
+                unpack<T>(v[u], f);
+                gradient(ch, f);
+                m2 = __vmaxu2(m2, store_chunk(r, out, same, ch, f, out_at, out_total, a.status));
+            }
+        }
+    }
+    const int ec = r.edge(edge_of_thread(), c0, c1);
+    if (ec >= 0) {
+        float f[E];
+        if (skip) {
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                f[e] = 0.0f;
+        } else {
+            load_edge(r, ec, f, total, a.status);
+        }
+        gradient(ec, f);
+        m2 = __vmaxu2(m2, store_elements(r, out, ec, f, out_at, out_total, a.status));
+    }
+    if (part == a.blocks_per_row - 1)
+        zero_columns(out, r.vocab, a.out.ld, out_at, out_total, a.status);
+    block_amax(m2, a.out.amax, a.status);
+}
+
+// ------------------------------------------------------------ distillation
+struct DistillArgs {
+    const void *logits;
+    int64_t rows, ld;
+    int vocab, k, cluster, blocks_per_row;
+    const int32_t *ids;
+    const float *values;
+    float inv_t, c;
+    float *loss, *lse, *rest;      // written by the forward, read by the backward
+    const float *dloss;
+    OutArgs out;
+    unsigned *status;
+};
+
+// The row's slots in shared memory.  A table keyed by chunk number finds the
+// slots that name an element of a chunk: head[chunk % kHeads] starts a list
+// of slots.  Of equal ids only the first slot is listed; it carries their
+// summed q.
+constexpr int kHeads = 2048;
+struct Slots {
+    int head[kHeads];
+    int next[F8_MAX_TOP];
+    int id[F8_MAX_TOP];     // -1: empty
+    float q[F8_MAX_TOP];    // the slot's own q
+    float qsum[F8_MAX_TOP]; // of all slots with this id, at the first of them; else unused
+    float logq[F8_MAX_TOP];
+    float z[F8_MAX_TOP];    // the student's logit at id
+    uint8_t first[F8_MAX_TOP];
+    float red[32];
+  };
+
+struct SlotSums {
+    bool any;     // the row has a slot
+    float total;  // sum q (1 without the tail class)
+    float left;   // q_r
+};
+
+// Reads the row's slots; all threads of the block.
+template <typename T, bool TAIL, int WARPS>
+__device__ __forceinline__ SlotSums load_slots(const DistillArgs &a, const Row<T> &r, int64_t row,
+                                               Slots &s, bool table, bool logits)
+{
+    constexpr int N = WARPS * 32;
+    const int tid = threadIdx.x, k = a.k;
+    if (table) {
+        for (int i = tid; i < kHeads / 4; i += N)
+            reinterpret_cast<uint4 *>(s.head)[i] =
+                make_uint4(0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu);
+    }
+    const bool mine = tid < k;
+    int id = -1;
+    float t = F8_NEG_INF;
+    if (mine) {
+        id = a.ids[row * k + tid];
+        t = a.values[row * k + tid];
+        if (id >= r.vocab) {
+            atomicOr(a.status, kStatusIndex);
+            id = -1;
+        }
+        if (t == F8_NEG_INF)
+            id = -1;
+        if (id < 0)
+            t = F8_NEG_INF;
+        s.id[tid] = id < 0 ? -1 : id;
+    }
+    SlotSums out;
+    out.any = __syncthreads_or(mine && id >= 0) != 0;
+    out.total = 1.0f;
+    out.left = 0.0f;
+    if (!out.any)
+        return out;
+    float q = 0.0f, logq = 0.0f;
+    if (TAIL) {
+        q = id >= 0 ? expf(t) : 0.0f;
+        logq = t;
+        out.total = block_sum<WARPS>(q, s.red);
+        out.left = fmaxf(1.0f - out.total, 0.0f);
+    } else {
+        const float m = block_max<WARPS>(t, s.red);
+        const float d = (t - m) * a.inv_t;
+        const float e = id >= 0 ? expf(d) : 0.0f;
+        const float sum = block_sum<WARPS>(e, s.red);
+        q = e / sum;
+        logq = d - logf(sum);
+    }
+    if (mine) {
+        s.q[tid] = q;
+        s.logq[tid] = logq;
+        if (logits)
+            s.z[tid] = id >= 0 ? as_float(r.base[r.off + id]) : 0.0f;
+    }
+    __syncthreads();
+    bool first = id >= 0;
+    float qs = 0.0f;
+    if (id >= 0) {
+        for (int j = 0; j < k; ++j) {
+            if (s.id[j] == id) {
+                qs += s.q[j];
+                first = first && j >= tid;
+            }
+        }
+    }
+    if (mine) {
+        s.first[tid] = first;
+        s.qsum[tid] = qs;
+    }
+    // a list's order is free: its slots name different elements
+    if (table && first)
+        s.next[tid] = atomicExch(&s.head[((id + r.off) / Chunk<T>::E) % kHeads], tid);
+    __syncthreads();
+    return out;
+}
+
+// -inf in the elements of chunk ch that a slot names.
+template <typename T>
+__device__ __forceinline__ void drop_slots(const Slots &s, const Row<T> &r, int ch,
+                                           float (&f)[Chunk<T>::E])
+{
+    constexpr int E = Chunk<T>::E;
+    for (int j = s.head[ch % kHeads]; j >= 0; j = s.next[j]) {
+        const int d = s.id[j] + r.off - ch * E;
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            if (d == e)
+                f[e] = F8_NEG_INF;
+    }
+}
+
+// The loss of a row from the slots and the student's statistics over the
+// whole vocabulary (TAIL: over the tokens outside the slots' ids); all threads
+// of the block.  Gives lse and the student's mass outside.
+struct RowLoss {
+    float loss, lse, rest;
+    float m, inv_s;  // p = 2^((x - m) c) inv_s
+    bool none;       // every token is masked
+    bool bad;        // NaN or +inf
+};
+
+template <bool TAIL, int WARPS>
+__device__ __forceinline__ RowLoss row_loss(const DistillArgs &a, Slots &s, const SlotSums &q,
+                                            Stats t, bool want)
+{
+    const int tid = threadIdx.x;
+    const bool mine = tid < a.k && s.id[tid] >= 0;
+    const float z = mine ? s.z[tid] : F8_NEG_INF;
+    RowLoss o;
+    o.rest = 0.0f;
+    float outside = t.s, m = t.m;
+    if (TAIL) {
+        m = fmaxf(t.m, block_max<WARPS>(z, s.red));
+        // a NaN is no maximum; it reaches the sum
+        const float mm = m == F8_NEG_INF ? 0.0f : m;
+        outside = t.s * ex2(fmaxf((t.m - m) * a.c, kFloor2));
+        const float in = mine && s.first[tid] ? ex2((z - mm) * a.c) : 0.0f;
+        t.s = outside + block_sum<WARPS>(in, s.red);
+        t.m = m;
+    }
+    o.bad = t.s != t.s || m == F8_POS_INF;
+    o.none = !o.bad && t.s == 0.0f;
+    o.m = m == F8_NEG_INF ? 0.0f : m;
+    o.inv_s = o.none ? 0.0f : 1.0f / t.s;
+    const float ls = logf(t.s);
+    o.lse = o.bad ? F8_NAN : (o.none ? F8_NEG_INF : fmaf(m, a.inv_t, ls));
+    if (TAIL)
+        o.rest = o.bad ? F8_NAN : outside * o.inv_s;
+    o.loss = 0.0f;
+    if (want) {
+        float term = 0.0f;
+        if (mine && s.q[tid] > 0.0f) {
+            // log p from the difference to the maximum; -inf for a masked token
+            const float lp = o.none ? F8_NEG_INF : fmaf(z - o.m, a.inv_t, -ls);
+            term = s.q[tid] * (s.logq[tid] - lp);
+        } else if (mine && s.q[tid] != s.q[tid]) {
+            term = F8_NAN;
+        }
+        o.loss = block_sum<WARPS>(term, s.red);
+        if (TAIL && o.rest > 0.0f && q.left > 0.0f)
+            o.loss += q.left * (logf(q.left) - logf(o.rest));
+        if (o.bad)
+            o.loss = F8_NAN;
+    }
+    return o;
+}
+
+template <typename T, bool TAIL>
+__global__ void __launch_bounds__(kThreads)
+distill_fwd_kernel(const __grid_constant__ DistillArgs a)
+{
+    constexpr int E = Chunk<T>::E;
+    __shared__ __align__(16) Slots slots;
+    __shared__ Stats red[kWarps];
+    __shared__ Stats parts[kMaxCluster];
+    griddep_wait();
+    griddep_launch_dependents();
+    const int C = a.cluster;
+    const int64_t row = blockIdx.x / C;
+    const int rank = static_cast<int>(blockIdx.x % C);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const Row<T> r(static_cast<const T *>(a.logits), row, a.ld, a.vocab);
+    const int64_t total = (a.rows - 1) * a.ld + a.vocab;
+    if (C > 1)
+        cluster_start();
+    const SlotSums q = load_slots<T, TAIL, kWarps>(a, r, row, slots, TAIL, true);
+    if (!q.any) {
+        if (C > 1)
+            cluster_started();
+        if (rank == 0 && tid == 0) {
+            a.loss[row] = 0.0f;
+            a.lse[row] = 0.0f;
+            if (TAIL)
+                a.rest[row] = 0.0f;
+        }
+        return;
+    }
+    const int ngroups = (r.nch + 31) / 32;
+    const int per = (ngroups + C - 1) / C;
+    const int g0 = min(ngroups, rank * per), g1 = min(ngroups, g0 + per);
+    Stats t = stats_empty();
+    for (int g = g0 + warp * kUnroll; g < g1; g += kWarps * kUnroll) {
+        uint4 v[kUnroll];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u)
+            v[u] = load_chunk(r, (g + u) * 32 + lane, g1 * 32, total, a.status);
+        float f[kUnroll * E];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            float x[E];
+            unpack<T>(v[u], x);
+            if (TAIL)
+                drop_slots(slots, r, (g + u) * 32 + lane, x);
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                f[u * E + e] = x[e];
+        }
+        add_values<false>(t, f, a.c);
+    }
+    const int ec = r.edge(edge_of_thread(), g0 * 32, g1 * 32);
+    if (ec >= 0) {
+        float x[E];
+        load_edge(r, ec, x, total, a.status);
+        if (TAIL)
+            drop_slots(slots, r, ec, x);
+        add_values<false>(t, x, a.c);
+    }
+    t = block_join<false, kWarps>(t, a.c, red);
+    if (C > 1) {
+        cluster_started();
+        if (tid == 0)
+            *peer(&parts[rank], 0) = t;
+        cluster_join();
+        if (rank != 0)
+            return;
+        t = parts[0];
+        for (int i = 1; i < C; ++i)
+            t = join<false>(t, parts[i], a.c);
+    }
+    const RowLoss o = row_loss<TAIL, kWarps>(a, slots, q, t, true);
+    if (tid == 0) {
+        a.loss[row] = o.loss;
+        a.lse[row] = o.lse;
+        if (TAIL)
+            a.rest[row] = o.rest;
+        if (o.bad || o.loss != o.loss)
+            atomicOr(a.status, kStatusNonfinite);
+    }
+}
+
+// dlogits of one chunk: dense * p, and at the slots' ids scale (total p - q).
+template <typename T>
+__device__ __forceinline__ void slot_gradient(const Slots &s, const Row<T> &r, int ch,
+                                              const float (&p)[Chunk<T>::E], float scale,
+                                              float total, float (&g)[Chunk<T>::E])
+{
+    constexpr int E = Chunk<T>::E;
+    for (int j = s.head[ch % kHeads]; j >= 0; j = s.next[j]) {
+        const int d = s.id[j] + r.off - ch * E;
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            if (d == e)
+                g[e] = scale * fmaf(total, p[e], -s.qsum[j]);
+    }
+}
+
+template <typename T, bool TAIL>
+__global__ void __launch_bounds__(kThreads)
+distill_bwd_kernel(const __grid_constant__ DistillArgs a)
+{
+    constexpr int E = Chunk<T>::E;
+    __shared__ __align__(16) Slots slots;
+    griddep_wait();
+    griddep_launch_dependents();
+    const int64_t row = blockIdx.x / a.blocks_per_row;
+    const int part = static_cast<int>(blockIdx.x % a.blocks_per_row);
+    const Row<T> r(static_cast<const T *>(a.logits), row, a.ld, a.vocab);
+    const int64_t total = (a.rows - 1) * a.ld + a.vocab;
+    T *out = static_cast<T *>(a.out.p) + row * a.out.ld;
+    const int64_t out_at = row * a.out.ld, out_total = a.rows * a.out.ld;
+    const bool same = same_offset(r, out);
+    const float scale = a.dloss[row] * a.inv_t;
+    const float lse = a.lse[row];
+    SlotSums q = load_slots<T, TAIL, kWarps>(a, r, row, slots, true, false);
+    const bool skip = !q.any || a.dloss[row] == 0.0f || fabsf(lse) >= kMaxLse;
+    float mass = q.total, dense = q.total;
+    if (TAIL) {
+        const float rest = a.rest[row];
+        if (rest > 0.0f) {
+            mass = q.total + q.left;
+            dense = mass - q.left / rest;
+        }
+    }
+    uint32_t m2 = 0;
+    const int c0 = part * kBwdChunks, c1 = min(r.nch, c0 + kBwdChunks);
+    auto gradient = [&](int ch, float (&f)[E]) {
+        float g[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            f[e] = ex2(fmaf(f[e], a.inv_t, -lse) * static_cast<float>(kLog2e));
+            g[e] = skip ? 0.0f : scale * dense * f[e];
+        }
+        if (!skip)
+            slot_gradient(slots, r, ch, f, scale, mass, g);
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            f[e] = g[e];
+    };
+    for (int cb = max(c0, r.w0) + static_cast<int>(threadIdx.x); cb < min(c1, r.w1);
+         cb += kUnroll * kThreads) {
+        uint4 v[kUnroll];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u)
+            v[u] = load_chunk(r, cb + u * kThreads, skip ? 0 : c1, total, a.status);
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            const int ch = cb + u * kThreads;
+            if (ch < min(c1, r.w1)) {
+                float f[E];
+                unpack<T>(v[u], f);
+                gradient(ch, f);
+                m2 = __vmaxu2(m2, store_chunk(r, out, same, ch, f, out_at, out_total, a.status));
+            }
+        }
+    }
+    const int ec = r.edge(edge_of_thread(), c0, c1);
+    if (ec >= 0) {
+        float f[E];
+        if (skip) {
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                f[e] = 0.0f;
+        } else {
+            load_edge(r, ec, f, total, a.status);
+        }
+        gradient(ec, f);
+        m2 = __vmaxu2(m2, store_elements(r, out, ec, f, out_at, out_total, a.status));
+    }
+    if (part == a.blocks_per_row - 1)
+        zero_columns(out, r.vocab, a.out.ld, out_at, out_total, a.status);
+    block_amax(m2, a.out.amax, a.status);
+}
+
+// Loss and gradient together.  A cluster of C blocks shares a row, each thread
+// holding up to NV of its chunks in registers between the two phases, so a row
+// that fits is read once; a longer one is walked in stretches and read again
+// (from L2 where it still holds it).
+constexpr int kNV = 8;
+
+template <typename T, bool TAIL, int WARPS>
+__global__ void __launch_bounds__(WARPS * 32)
+distill_fused_kernel(const __grid_constant__ DistillArgs a)
+{
+    constexpr int E = Chunk<T>::E;
+    constexpr int N = WARPS * 32;
+    __shared__ __align__(16) Slots slots;
+    __shared__ Stats red[WARPS];
+    __shared__ Stats parts[kMaxCluster];
+    griddep_wait();
+    griddep_launch_dependents();
+    const int C = a.cluster;
+    const int64_t row = blockIdx.x / C;
+    const int rank = static_cast<int>(blockIdx.x % C);
+    const int tid = threadIdx.x;
+    const Row<T> r(static_cast<const T *>(a.logits), row, a.ld, a.vocab);
+    const int64_t total = (a.rows - 1) * a.ld + a.vocab;
+    T *out = static_cast<T *>(a.out.p) + row * a.out.ld;
+    const int64_t out_at = row * a.out.ld, out_total = a.rows * a.out.ld;
+    const bool same = same_offset(r, out);
+    if (C > 1)
+        cluster_start();
+    const SlotSums q = load_slots<T, TAIL, WARPS>(a, r, row, slots, true, true);
+    const int per = (r.nch + C - 1) / C;
+    const int c0 = min(r.nch, rank * per), c1 = min(r.nch, c0 + per);
+    const float dl = a.dloss[row];
+    uint32_t m2 = 0;
+    const int ec = r.edge(edge_of_thread(), c0, c1);
+    const int wb = max(c0, r.w0), we = min(c1, r.w1);  // this block's whole chunks
+    if (q.any) {
+        uint4 v[kNV];
+        float edge[E];
+        Stats t = stats_empty();
+        if (ec >= 0) {
+            load_edge(r, ec, edge, total, a.status);
+            float x[E];
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                x[e] = edge[e];
+            if (TAIL)
+                drop_slots(slots, r, ec, x);
+            add_values<false>(t, x, a.c);
+        }
+        for (int cb = wb; cb < we; cb += kNV * N) {
+#pragma unroll
+            for (int u = 0; u < kNV; ++u)
+                v[u] = load_chunk(r, cb + u * N + tid, we, total, a.status);
+#pragma unroll
+            for (int h = 0; h < kNV; h += kUnroll) {
+                float f[kUnroll * E];
+#pragma unroll
+                for (int u = 0; u < kUnroll; ++u) {
+                    float x[E];
+                    unpack<T>(v[h + u], x);
+                    if (TAIL)
+                        drop_slots(slots, r, cb + (h + u) * N + tid, x);
+#pragma unroll
+                    for (int e = 0; e < E; ++e)
+                        f[u * E + e] = x[e];
+                }
+                add_values<false>(t, f, a.c);
+            }
+        }
+        t = block_join<false, WARPS>(t, a.c, red);
+        if (C > 1) {
+            cluster_started();
+            if (tid < C)
+                *peer(&parts[rank], tid) = t;
+            cluster_join();
+            t = parts[0];
+            for (int i = 1; i < C; ++i)
+                t = join<false>(t, parts[i], a.c);
+        }
+        const RowLoss o = row_loss<TAIL, WARPS>(a, slots, q, t, rank == 0);
+        if (rank == 0 && tid == 0) {
+            a.loss[row] = o.loss;
+            if (o.bad || o.loss != o.loss)
+                atomicOr(a.status, kStatusNonfinite);
+        }
+        float mass = q.total, dense = q.total;
+        if (TAIL && o.rest > 0.0f) {
+            mass = q.total + q.left;
+            dense = mass - q.left / o.rest;
+        }
+        const bool zero = dl == 0.0f || o.none;
+        const float scale = dl * a.inv_t, inv_s = o.bad ? F8_NAN : o.inv_s;
+        auto gradient = [&](int ch, float (&f)[E]) {
+            float g[E];
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                f[e] = ex2((f[e] - o.m) * a.c) * inv_s;
+                g[e] = zero ? 0.0f : scale * dense * f[e];
+            }
+            if (!zero)
+                slot_gradient(slots, r, ch, f, scale, mass, g);
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                f[e] = g[e];
+        };
+        for (int cb = wb; cb < we; cb += kNV * N) {
+            if (we - wb > kNV * N) {
+#pragma unroll
+                for (int u = 0; u < kNV; ++u)
+                    v[u] = load_chunk(r, cb + u * N + tid, we, total, a.status);
+            }
+#pragma unroll
+            for (int u = 0; u < kNV; ++u) {
+                const int ch = cb + u * N + tid;
+                if (ch < we) {
+                    float f[E];
+                    unpack<T>(v[u], f);
+                    gradient(ch, f);
+                    m2 = __vmaxu2(m2, store_chunk(r, out, same, ch, f, out_at, out_total, a.status));
+                }
+            }
+        }
+        if (ec >= 0) {
+            gradient(ec, edge);
+            m2 = __vmaxu2(m2, store_elements(r, out, ec, edge, out_at, out_total, a.status));
+        }
+    } else {
+        if (C > 1)
+            cluster_started();
+        if (rank == 0 && tid == 0)
+            a.loss[row] = 0.0f;
+        float g[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            g[e] = 0.0f;
+        for (int ch = wb + tid; ch < we; ch += N)
+            store_chunk(r, out, same, ch, g, out_at, out_total, a.status);
+        if (ec >= 0)
+            store_elements(r, out, ec, g, out_at, out_total, a.status);
+    }
+    if (rank == C - 1)
+        zero_columns(out, r.vocab, a.out.ld, out_at, out_total, a.status);
+    block_amax(m2, a.out.amax, a.status);
+}
+
+// ------------------------------------------------------------ launches
+// Blocks per row: one where the rows alone keep every SM busy, up to eight
+// where they do not, none with less than a group of chunks for each warp.
+int cluster_for(int64_t rows, int64_t chunks, const DeviceInfo &dev)
+{
+    int c = 1;
+    while (c < kMaxCluster && rows * c < 2 * dev.sm_count && chunks / (2 * c) >= kWarps * 32)
+        c *= 2;
+    return c;
+}
+
+template <typename F>
+cudaError_t allow_smem(F *kernel, size_t bytes)
+{
+    if (bytes <= 48 * 1024)
+        return cudaSuccess;
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                static_cast<int>(bytes));
+}
+
+template <typename T>
+cudaError_t logprobs(LogprobArgs a, const DeviceInfo &dev, cudaStream_t st)
+{
+    constexpr int E = Chunk<T>::E;
+    const int64_t chunks = (static_cast<int64_t>(a.vocab) + E - 1 + E) / E;
+    a.cluster = cluster_for(a.rows, chunks, dev);
+    const int ngroups = static_cast<int>((chunks + 31) / 32);
+    size_t smem = 0;
+    if (a.top_k > 0)
+        smem = 4u * top_layout((ngroups + a.cluster - 1) / a.cluster, a.top_k, a.cluster).words;
+    const dim3 grid(static_cast<unsigned>(a.rows * a.cluster));
+    if (a.top_k > 0) {
+        const cudaError_t e = allow_smem(logprobs_kernel<T, true>, smem);
+        if (e != cudaSuccess)
+            return e;
+        return launch_pdl_cluster(logprobs_kernel<T, true>, grid, dim3(kThreads), smem, st,
+                                  static_cast<unsigned>(a.cluster), a);
+    }
+    return launch_pdl_cluster(logprobs_kernel<T, false>, grid, dim3(kThreads), 0, st,
+                              static_cast<unsigned>(a.cluster), a);
+}
+
+template <typename T>
+int bwd_blocks(int64_t vocab)
+{
+    const int64_t chunks = (vocab + 2 * Chunk<T>::E - 2) / Chunk<T>::E;
+    return static_cast<int>((chunks + kBwdChunks - 1) / kBwdChunks);
+}
+
+template <typename T>
+cudaError_t logprobs_bwd(LogprobBwdArgs a, const DeviceInfo &, cudaStream_t st)
+{
+    a.blocks_per_row = bwd_blocks<T>(a.vocab);
+    return launch_pdl(logprobs_bwd_kernel<T>, dim3(static_cast<unsigned>(a.rows * a.blocks_per_row)),
+                      dim3(kThreads), 0, st, a);
+}
+
+template <typename T, bool TAIL>
+cudaError_t distill_fwd(DistillArgs a, const DeviceInfo &dev, cudaStream_t st)
+{
+    const int64_t chunks = (static_cast<int64_t>(a.vocab) + 2 * Chunk<T>::E - 2) / Chunk<T>::E;
+    a.cluster = cluster_for(a.rows, chunks, dev);
+    return launch_pdl_cluster(distill_fwd_kernel<T, TAIL>,
+                              dim3(static_cast<unsigned>(a.rows * a.cluster)), dim3(kThreads), 0, st,
+                              static_cast<unsigned>(a.cluster), a);
+}
+
+template <typename T, bool TAIL>
+cudaError_t distill_bwd(DistillArgs a, const DeviceInfo &, cudaStream_t st)
+{
+    a.blocks_per_row = bwd_blocks<T>(a.vocab);
+    return launch_pdl(distill_bwd_kernel<T, TAIL>,
+                      dim3(static_cast<unsigned>(a.rows * a.blocks_per_row)), dim3(kThreads), 0, st,
+                      a);
+}
+
+template <typename T, bool TAIL>
+cudaError_t distill_fused(DistillArgs a, const DeviceInfo &dev, cudaStream_t st)
+{
+    // as few blocks as hold the row in registers, more where rows are few
+    const int64_t chunks = (static_cast<int64_t>(a.vocab) + 2 * Chunk<T>::E - 2) / Chunk<T>::E;
+    int c = 1;
+    while (c < kMaxCluster && (chunks + c - 1) / c > kNV * kThreads)
+        c *= 2;
+    a.cluster = std::max(c, cluster_for(a.rows, chunks, dev));
+    const dim3 grid(static_cast<unsigned>(a.rows * a.cluster));
+    if ((chunks + a.cluster - 1) / a.cluster > kNV * kThreads)
+        return launch_pdl_cluster(distill_fused_kernel<T, TAIL, 2 * kWarps>, grid,
+                                  dim3(2 * kThreads), 0, st, static_cast<unsigned>(a.cluster), a);
+    return launch_pdl_cluster(distill_fused_kernel<T, TAIL, kWarps>, grid, dim3(kThreads), 0, st,
+                              static_cast<unsigned>(a.cluster), a);
+}
+
+// What every call of this file asks of its logits.
+f8_status check_logits(const void *logits, f8_dtype type, int64_t rows, int64_t vocab, int64_t ld,
+                       float temperature)
+{
+    if ((type != F8_BF16 && type != F8_F32) || rows < 0 || vocab < 0 || ld < vocab)
+        return F8_ERR_INVALID;
+    if (!(temperature > 0.0f) || !std::isfinite(temperature) || !std::isfinite(1.0f / temperature))
+        return F8_ERR_INVALID;
+    if (rows > 0 && (vocab == 0 || logits == nullptr))
+        return F8_ERR_INVALID;
+    // blocks are numbered in 32 bits: at most kMaxCluster, or the backward's share, per row
+    if (vocab > F8_MAX_VOCAB || ld > INT32_MAX || rows > INT32_MAX / 1024)
+        return F8_ERR_SHAPE;
+    if (!aligned(logits, 16))
+        return F8_ERR_ALIGN;
+    return F8_OK;
+}
+
+f8_status check_out(const void *dlogits, f8_dtype type, int64_t rows, int64_t vocab, int64_t ld,
+                    const void *logits, int64_t ldd, const float *amax_out)
+{
+    if (ldd < vocab || (rows > 0 && dlogits == nullptr))
+        return F8_ERR_INVALID;
+    if (dlogits != nullptr && dlogits == logits && ldd != ld)
+        return F8_ERR_INVALID;
+    if (amax_out != nullptr && type != F8_BF16)
+        return F8_ERR_INVALID;
+    if (ldd > INT32_MAX)
+        return F8_ERR_SHAPE;
+    if (!aligned(dlogits, 16) || !aligned(amax_out, 4))
+        return F8_ERR_ALIGN;
+    return F8_OK;
+}
+
+f8_status check_slots(const int32_t *ids, const float *values, int k, int tail, int64_t rows)
+{
+    if (k < 1 || (tail != 0 && tail != 1) || (rows > 0 && (ids == nullptr || values == nullptr)))
+        return F8_ERR_INVALID;
+    if (k > F8_MAX_TOP)
+        return F8_ERR_SHAPE;
+    if (!aligned(ids, 4) || !aligned(values, 4))
+        return F8_ERR_ALIGN;
+    return F8_OK;
+}
+
+DistillArgs distill_args(const void *logits, int64_t rows, int64_t vocab, int64_t ld,
+                         const int32_t *ids, const float *values, int k, float temperature,
+                         float *loss, float *lse, float *rest, const float *dloss, void *dlogits,
+                         int64_t ldd, float *amax_out, const DeviceInfo &dev)
+{
+    DistillArgs a = {};
+    a.logits = logits;
+    a.rows = rows;
+    a.ld = ld;
+    a.vocab = static_cast<int>(vocab);
+    a.k = k;
+    a.ids = ids;
+    a.values = values;
+    a.inv_t = 1.0f / temperature;
+    a.c = static_cast<float>(kLog2e / static_cast<double>(temperature));
+    a.loss = loss;
+    a.lse = lse;
+    a.rest = rest;
+    a.dloss = dloss;
+    a.out = OutArgs{dlogits, ldd, reinterpret_cast<unsigned *>(amax_out)};
+    a.status = dev.status;
+    return a;
+}
+
+} // namespace
+} // namespace f8
+
+using namespace f8;
+
+#define F8_BY_TYPE(fn, type, tail, ...)                                                            \
+    ((type) == F8_BF16 ? ((tail) ? fn<__nv_bfloat16, true>(__VA_ARGS__)                            \
+                                 : fn<__nv_bfloat16, false>(__VA_ARGS__))                          \
+                       : ((tail) ? fn<float, true>(__VA_ARGS__) : fn<float, false>(__VA_ARGS__)))
+
+extern "C" {
+
+f8_status f8_token_logprobs(const void *logits, f8_dtype type, int64_t rows, int64_t vocab,
+                            int64_t ld, const int64_t *tokens, float temperature, int top_k,
+                            float *logp, float *entropy, float *lse, int32_t *top_ids,
+                            float *top_logp, void *stream)
+{
+    F8_TRY(check_logits(logits, type, rows, vocab, ld, temperature));
+    if (top_k < 0 || (top_k > 0 && rows > 0 && (top_ids == nullptr || top_logp == nullptr)) ||
+        (tokens == nullptr && logp != nullptr))
+        return F8_ERR_INVALID;
+    if (top_k > F8_MAX_TOP || (rows > 0 && top_k > vocab))
+        return F8_ERR_SHAPE;
+    if (!aligned(tokens, 8) || !aligned(logp, 4) || !aligned(entropy, 4) || !aligned(lse, 4) ||
+        !aligned(top_ids, 4) || !aligned(top_logp, 4))
+        return F8_ERR_ALIGN;
+    const DeviceInfo *dev;
+    F8_TRY(get_device(&dev));
+    if (rows == 0)
+        return F8_OK;
+    LogprobArgs a = {};
+    a.logits = logits;
+    a.rows = rows;
+    a.ld = ld;
+    a.vocab = static_cast<int>(vocab);
+    a.top_k = top_k;
+    a.tokens = tokens;
+    a.inv_t = 1.0f / temperature;
+    a.c = static_cast<float>(kLog2e / static_cast<double>(temperature));
+    a.logp = logp;
+    a.entropy = entropy;
+    a.lse = lse;
+    a.top_ids = top_ids;
+    a.top_logp = top_logp;
+    a.status = dev->status;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return from_cuda(type == F8_BF16 ? logprobs<__nv_bfloat16>(a, *dev, st)
+                                     : logprobs<float>(a, *dev, st));
+}
+
+f8_status f8_token_logprobs_bwd(const void *logits, f8_dtype type, int64_t rows, int64_t vocab,
+                                int64_t ld, const int64_t *tokens, const float *lse,
+                                const float *entropy, const float *dlogp, const float *dentropy,
+                                float temperature, void *dlogits, int64_t ldd, float *amax_out,
+                                void *stream)
+{
+    F8_TRY(check_logits(logits, type, rows, vocab, ld, temperature));
+    F8_TRY(check_out(dlogits, type, rows, vocab, ld, logits, ldd, amax_out));
+    if (rows > 0 && (lse == nullptr || (dentropy != nullptr && entropy == nullptr) ||
+                     (dlogp != nullptr && tokens == nullptr)))
+        return F8_ERR_INVALID;
+    if (!aligned(tokens, 8) || !aligned(lse, 4) || !aligned(entropy, 4) || !aligned(dlogp, 4) ||
+        !aligned(dentropy, 4))
+        return F8_ERR_ALIGN;
+    const DeviceInfo *dev;
+    F8_TRY(get_device(&dev));
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (amax_out != nullptr)
+        F8_TRY_CUDA(cudaMemsetAsync(amax_out, 0, sizeof(float), st));
+    if (rows == 0)
+        return F8_OK;
+    LogprobBwdArgs a = {};
+    a.logits = logits;
+    a.rows = rows;
+    a.ld = ld;
+    a.vocab = static_cast<int>(vocab);
+    a.tokens = tokens;
+    a.lse = lse;
+    a.entropy = entropy;
+    a.dlogp = dlogp;
+    a.dentropy = dentropy;
+    a.inv_t = 1.0f / temperature;
+    a.out = OutArgs{dlogits, ldd, reinterpret_cast<unsigned *>(amax_out)};
+    a.status = dev->status;
+    return from_cuda(type == F8_BF16 ? logprobs_bwd<__nv_bfloat16>(a, *dev, st)
+                                     : logprobs_bwd<float>(a, *dev, st));
+}
+
+f8_status f8_distill_fwd(const void *logits, f8_dtype type, int64_t rows, int64_t vocab, int64_t ld,
+                         const int32_t *ids, const float *values, int k, float temperature,
+                         int tail, float *loss, float *lse, float *rest, void *stream)
+{
+    F8_TRY(check_logits(logits, type, rows, vocab, ld, temperature));
+    F8_TRY(check_slots(ids, values, k, tail, rows));
+    if (rows > 0 && (loss == nullptr || lse == nullptr || (tail && rest == nullptr)))
+        return F8_ERR_INVALID;
+    if (!aligned(loss, 4) || !aligned(lse, 4) || !aligned(rest, 4))
+        return F8_ERR_ALIGN;
+    const DeviceInfo *dev;
+    F8_TRY(get_device(&dev));
+    if (rows == 0)
+        return F8_OK;
+    const DistillArgs a = distill_args(logits, rows, vocab, ld, ids, values, k, temperature, loss,
+                                       lse, rest, nullptr, nullptr, 0, nullptr, *dev);
+    return from_cuda(F8_BY_TYPE(f8::distill_fwd, type, tail, a, *dev,
+                                static_cast<cudaStream_t>(stream)));
+}
+
+f8_status f8_distill_bwd(const void *logits, f8_dtype type, int64_t rows, int64_t vocab, int64_t ld,
+                         const int32_t *ids, const float *values, int k, float temperature,
+                         int tail, const float *lse, const float *rest, const float *dloss,
+                         void *dlogits, int64_t ldd, float *amax_out, void *stream)
+{
+    F8_TRY(check_logits(logits, type, rows, vocab, ld, temperature));
+    F8_TRY(check_slots(ids, values, k, tail, rows));
+    F8_TRY(check_out(dlogits, type, rows, vocab, ld, logits, ldd, amax_out));
+    if (rows > 0 && (lse == nullptr || dloss == nullptr || (tail && rest == nullptr)))
+        return F8_ERR_INVALID;
+    if (!aligned(lse, 4) || !aligned(rest, 4) || !aligned(dloss, 4))
+        return F8_ERR_ALIGN;
+    const DeviceInfo *dev;
+    F8_TRY(get_device(&dev));
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (amax_out != nullptr)
+        F8_TRY_CUDA(cudaMemsetAsync(amax_out, 0, sizeof(float), st));
+    if (rows == 0)
+        return F8_OK;
+    const DistillArgs a =
+        distill_args(logits, rows, vocab, ld, ids, values, k, temperature, nullptr,
+                     const_cast<float *>(lse), const_cast<float *>(rest), dloss, dlogits, ldd,
+                     amax_out, *dev);
+    return from_cuda(F8_BY_TYPE(f8::distill_bwd, type, tail, a, *dev, st));
+}
+
+f8_status f8_distill_fwd_bwd(const void *logits, f8_dtype type, int64_t rows, int64_t vocab,
+                             int64_t ld, const int32_t *ids, const float *values, int k,
+                             float temperature, int tail, const float *dloss, float *loss,
+                             void *dlogits, int64_t ldd, float *amax_out, void *stream)
+{
+    F8_TRY(check_logits(logits, type, rows, vocab, ld, temperature));
+    F8_TRY(check_slots(ids, values, k, tail, rows));
+    F8_TRY(check_out(dlogits, type, rows, vocab, ld, logits, ldd, amax_out));
+    if (rows > 0 && (loss == nullptr || dloss == nullptr))
+        return F8_ERR_INVALID;
+    if (!aligned(loss, 4) || !aligned(dloss, 4))
+        return F8_ERR_ALIGN;
+    const DeviceInfo *dev;
+    F8_TRY(get_device(&dev));
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (amax_out != nullptr)
+        F8_TRY_CUDA(cudaMemsetAsync(amax_out, 0, sizeof(float), st));
+    if (rows == 0)
+        return F8_OK;
+    const DistillArgs a = distill_args(logits, rows, vocab, ld, ids, values, k, temperature, loss,
+                                       nullptr, nullptr, dloss, dlogits, ldd, amax_out, *dev);
+    return from_cuda(F8_BY_TYPE(f8::distill_fused, type, tail, a, *dev, st));
+}
+
+} // extern "C"

@@ -12,6 +12,7 @@ namespace f8 {
 constexpr unsigned kStatusNonfinite = 1u << 0;
 constexpr unsigned kStatusTimeout = 1u << 1;
 constexpr unsigned kStatusBounds = 1u << 2;
+constexpr unsigned kStatusIndex = 1u << 3;
 
 // Bounds checks of the manual global-memory indexing, compiled in only with
 // -DF8_BOUNDS_CHECK (the checked build).  In that build an access of `len`

@@ -33,9 +33,10 @@
  *     are returned as a non-zero f8_status; nothing is enqueued then.
  *     Pointers to bf16 or E4M3 tensors must be 16-byte aligned; pointers to
  *     fp32 scalars 4-byte aligned.
- *   - Errors found on the device (a non-finite amax, a wait that ran past its
- *     time limit, in the checked build an index outside its buffer) are
- *     recorded in a per-device status word;
+ *   - Errors found on the device (a non-finite amax or log-sum-exp, a token id
+ *     outside the vocabulary, a wait that ran past its time limit, in the
+ *     checked build an index outside its buffer) are recorded in a per-device
+ *     status word;
  *     f8_last_device_status() reports and clears it.
  */
 #ifndef F8_H_
@@ -57,7 +58,8 @@ typedef enum {
     F8_ERR_TIMEOUT = 5,     /* a device-side wait exceeded its time limit     */
     F8_ERR_NONFINITE = 6,   /* an amax input held +-inf or NaN                */
     F8_ERR_UNSUPPORTED = 7, /* not an sm_103 device, or no driver entry point */
-    F8_ERR_BOUNDS = 8       /* checked build only: an index left its buffer   */
+    F8_ERR_BOUNDS = 8,      /* checked build only: an index left its buffer   */
+    F8_ERR_INDEX = 9        /* a token id outside the vocabulary (device-side) */
 } f8_status;
 
 /*
@@ -573,6 +575,175 @@ f8_status f8_gemm_w13_swiglu(const uint8_t *x_q, const uint8_t *w13_q, int64_t M
                              void *h, float *amax_h, void *stream);
 
 /*
+ * The operators on both sides of a Float8 linear: the norm that produces its
+ * input, and what stands behind the head linear in training and scoring
+ * (log probabilities, and the distillation loss).  The torchtitan pages name
+ * neither an interface nor a kernel for them; the formulas below are the
+ * definitions, evaluated in fp32 with one rounding to the output's type.
+ *
+ * Element type of a tensor that may be bf16 or fp32.
+ */
+typedef enum { F8_BF16 = 0, F8_F32 = 1 } f8_dtype;
+
+/*
+ * The norm of a row x[0..C):
+ *   F8_LAYER_NORM  mu = sum x / C,  r = 1 / sqrt(sum (x - mu)^2 / C + eps)
+ *   F8_RMS_NORM    mu = 0,          r = 1 / sqrt(sum x^2 / C + eps)
+ *   y = (x - mu) r w + b
+ */
+typedef enum { F8_LAYER_NORM = 0, F8_RMS_NORM = 1 } f8_norm;
+
+/*
+ * Forward of the norm.
+ *   x, y:   device [rows, cols] of type x_type, dense; y may be x.
+ *   w, b:   device [cols] of type w_type; b may be NULL (no bias; an RMS norm
+ *           usually has none).
+ *   mean, rstd: device fp32 [rows], mu and r for the backward pass; either may
+ *           be NULL (mean is not written for F8_RMS_NORM).
+ *   amax_out: device fp32 receiving max |y| of the values as stored, ready for
+ *           f8_cast_transpose, or NULL; needs x_type F8_BF16.  The call zeroes
+ *           it first.  A non-finite y then sets F8_ERR_NONFINITE.
+ * rows, cols >= 0 (nothing is done for 0; amax_out is then 0); eps >= 0.
+ * x, y, w, b 16-byte aligned, mean, rstd, amax_out 4-byte aligned.  Any cols is
+ * taken; rows of whole 16-byte vectors (cols a multiple of 8 for bf16, of 4
+ * for fp32) and cols <= 16384 take the fastest path.
+ */
+f8_status f8_norm_fwd(const void *x, f8_dtype x_type, const void *w, const void *b,
+                      f8_dtype w_type, f8_norm kind, int64_t rows, int64_t cols, float eps,
+                      void *y, float *mean, float *rstd, float *amax_out, void *stream);
+
+/*
+ * Backward of the norm, for the gradient dy of y and the forward's statistics:
+ *   xh = (x - mu) r,  g = dy w,  c1 = sum g xh / C,  c2 = sum g / C (0 for RMS)
+ *   dx = r (g - c2 - xh c1),   dw = sum over rows of dy xh,   db = sum of dy
+ *   dy, x, dx: device [rows, cols] of type x_type; dx may be dy or x.
+ *   w, dw, db: device [cols] of type w_type.  dx, dw and db may each be NULL.
+ *   mean:   NULL for F8_RMS_NORM.
+ *   workspace: f8_norm_bwd_workspace_bytes(rows, cols) bytes, 16-byte aligned
+ *           (partial sums of dw and db; contents need not be initialised);
+ *           may be NULL if dw and db are.
+ * The sums over rows are formed in a fixed order: equal inputs give equal bits.
+ */
+size_t f8_norm_bwd_workspace_bytes(int64_t rows, int64_t cols);
+f8_status f8_norm_bwd(const void *dy, const void *x, f8_dtype x_type, const void *w,
+                      f8_dtype w_type, const float *mean, const float *rstd, f8_norm kind,
+                      int64_t rows, int64_t cols, void *dx, void *dw, void *db, void *workspace,
+                      size_t workspace_bytes, void *stream);
+
+/*
+ * The input of a Float8 linear produced by a norm and quantised to E4M3 with
+ * its amax taken in the producing pass (as f8_quantize_swiglu does for the w2
+ * input): launch one is f8_norm_fwd with one partial maximum of |y| per CTA,
+ * launch two f8_quantize's cast of y.  Against f8_norm_fwd followed by
+ * f8_quantize, the amax re-read of y (2 B per element) is gone.
+ *   x, y: device bf16 [rows, cols]; w, b, mean, rstd as for f8_norm_fwd.
+ *   amax_out, scale_out, q, q_t, workspace: as for f8_quantize.
+ */
+f8_status f8_quantize_norm(const void *x, const void *w, const void *b, f8_dtype w_type,
+                           f8_norm kind, int64_t rows, int64_t cols, float eps, void *y,
+                           float *mean, float *rstd, float *amax_out, float *scale_out, uint8_t *q,
+                           uint8_t *q_t, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Most alternatives of f8_token_logprobs, and slots of f8_distill_*. */
+#define F8_MAX_TOP 256
+/* Largest vocabulary of the calls below. */
+#define F8_MAX_VOCAB (1 << 22)
+
+/*
+ * Log probabilities of given tokens under z = logits / temperature, row by row:
+ *   lse = log sum_v exp z_v,  logp = z_token - lse,  entropy = -sum p log p,
+ * and the top_k largest logits in descending order (equal ones by ascending
+ * id) with their log probabilities.
+ *   logits: device [rows, vocab] of type `type`, row r at logits + r * ld
+ *           elements (ld >= vocab; columns vocab .. ld are not read), 16-byte
+ *           aligned.  Rows that start off a 16-byte boundary are taken.
+ *   tokens: device int64 [rows] or NULL (then logp must be NULL).  A negative
+ *           token marks a row that is ignored: its logits are not read, logp,
+ *           entropy and lse are 0, top_ids -1 and top_logp -inf.  A token >=
+ *           vocab sets F8_ERR_INDEX and its logp is NaN.
+ *   logp, entropy, lse: device fp32 [rows]; each may be NULL.
+ *   top_ids, top_logp: device int32 / fp32 [rows, top_k], or NULL for top_k 0.
+ * -inf logits are masked tokens (p = 0).  A row without any other has lse,
+ * logp and top_logp -inf and entropy 0.  A NaN or +inf logit makes its row's
+ * results NaN (top_ids then are distinct ids, not otherwise specified) and
+ * sets F8_ERR_NONFINITE.
+ * temperature > 0; 0 <= top_k <= min(vocab, F8_MAX_TOP); vocab <= F8_MAX_VOCAB.
+ */
+f8_status f8_token_logprobs(const void *logits, f8_dtype type, int64_t rows, int64_t vocab,
+                            int64_t ld, const int64_t *tokens, float temperature, int top_k,
+                            float *logp, float *entropy, float *lse, int32_t *top_ids,
+                            float *top_logp, void *stream);
+
+/*
+ * Backward of logp and entropy to the logits, for upstream gradients dlogp
+ * (a) and dentropy (h) per row and the forward's lse and entropy:
+ *   dlogits_v = ( a (1[v = token] - p_v) - h p_v (log p_v + entropy) ) / temperature
+ *   dlogp, dentropy: device fp32 [rows]; each may be NULL (zero).
+ *   entropy: needed with dentropy only.
+ *   dlogits: device [rows, ldd] of type `type`, row r at dlogits + r * ldd;
+ *           columns vocab .. ldd are set to zero (the padding of a head whose
+ *           width is rounded up).  May be the logits buffer itself if ldd = ld.
+ *   amax_out: device fp32 receiving max |dlogits| as stored, ready for
+ *           f8_cast_transpose, or NULL; needs type F8_BF16.
+ * Ignored rows (negative token), rows whose upstream gradients are both 0, and
+ * rows of |lse| >= 2^24 (every token masked by -inf or by the type's lowest
+ * value: an fp32 lse no longer holds the row's sum) are not read and get zeros.
+ * Without tokens (NULL) only the entropy has a gradient.
+ */
+f8_status f8_token_logprobs_bwd(const void *logits, f8_dtype type, int64_t rows, int64_t vocab,
+                                int64_t ld, const int64_t *tokens, const float *lse,
+                                const float *entropy, const float *dlogp, const float *dentropy,
+                                float temperature, void *dlogits, int64_t ldd, float *amax_out,
+                                void *stream);
+
+/*
+ * Distillation from a teacher's top logits.  Each row has k slots (id_j, t_j);
+ * a slot with id < 0 or t = -inf is empty, and a row without a slot is ignored
+ * (loss 0, zero gradient, its logits are not read).  With z = logits /
+ * temperature, p = softmax(z) over the whole vocabulary:
+ *   tail = 0: q = softmax(t / temperature) over the row's slots;
+ *             loss = sum_j q_j (log q_j - log p_id_j)
+ *   tail = 1: t are log probabilities at this temperature (f8_token_logprobs'
+ *             top_logp), q_j = exp t_j; what they leave, q_r = max(0, 1 - sum q),
+ *             is the mass of one more class, "any other token", of which the
+ *             student holds p_r = the sum of p outside the slots' ids;
+ *             loss = sum_j q_j (log q_j - log p_id_j) + q_r (log q_r - log p_r),
+ *             the last term dropped where p_r = 0.
+ *   dlogits_v = dloss / temperature *
+ *               (m p_v - sum_{j: id_j = v} q_j - [tail, v outside] p_v q_r / p_r),
+ *               m = sum q + q_r
+ * No factor temperature^2 is applied.
+ *   logits, type, rows, vocab, ld: as for f8_token_logprobs.
+ *   ids:    device int32 [rows, k]; an id >= vocab sets F8_ERR_INDEX and its
+ *           slot counts as empty.  Equal ids in a row add up.
+ *   values: device fp32 [rows, k].
+ *   loss:   device fp32 [rows].  +inf where a slot with q > 0 names a masked
+ *           token; a row of masked tokens only gets zero gradient.
+ *   lse:    device fp32 [rows];  rest: device fp32 [rows] receiving p_r, needed
+ *           with tail = 1 and NULL otherwise.
+ *   dloss:  device fp32 [rows].  Rows with dloss = 0 get zero gradient (and
+ *           are not read by f8_distill_bwd, nor are rows of |lse| >= 2^24, which
+ *           it gives zeros as f8_token_logprobs_bwd does).
+ *   dlogits, ldd, amax_out: as for f8_token_logprobs_bwd.
+ * NaN or +inf in a row that is not ignored makes its loss and gradient NaN and
+ * sets F8_ERR_NONFINITE.
+ * f8_distill_fwd_bwd is both passes for callers that know dloss beforehand
+ * (e.g. 1 / tokens): the logits are read once.
+ * 1 <= k <= F8_MAX_TOP; temperature > 0; vocab <= F8_MAX_VOCAB.
+ */
+f8_status f8_distill_fwd(const void *logits, f8_dtype type, int64_t rows, int64_t vocab, int64_t ld,
+                         const int32_t *ids, const float *values, int k, float temperature,
+                         int tail, float *loss, float *lse, float *rest, void *stream);
+f8_status f8_distill_bwd(const void *logits, f8_dtype type, int64_t rows, int64_t vocab, int64_t ld,
+                         const int32_t *ids, const float *values, int k, float temperature,
+                         int tail, const float *lse, const float *rest, const float *dloss,
+                         void *dlogits, int64_t ldd, float *amax_out, void *stream);
+f8_status f8_distill_fwd_bwd(const void *logits, f8_dtype type, int64_t rows, int64_t vocab,
+                             int64_t ld, const int32_t *ids, const float *values, int k,
+                             float temperature, int tail, const float *dloss, float *loss,
+                             void *dlogits, int64_t ldd, float *amax_out, void *stream);
+
+/*
  * Number of kernels this library has launched (enqueued) in this process so
  * far, over all devices and streams; host-side, no synchronisation.  The
  * difference across a sequence of calls is the number of GPU kernels those
@@ -595,9 +766,9 @@ f8_status f8_selftest_bounds(void *stream);
 
 /*
  * Synchronises `stream`, then reads and clears the current device's status
- * word.  Returns F8_OK, F8_ERR_NONFINITE, F8_ERR_TIMEOUT or F8_ERR_BOUNDS
- * (the most severe bit set, BOUNDS over TIMEOUT over NONFINITE), or
- * F8_ERR_CUDA if the synchronisation itself failed.
+ * word.  Returns F8_OK, F8_ERR_NONFINITE, F8_ERR_INDEX, F8_ERR_TIMEOUT or
+ * F8_ERR_BOUNDS (the most severe bit set, BOUNDS over TIMEOUT over INDEX over
+ * NONFINITE), or F8_ERR_CUDA if the synchronisation itself failed.
  */
 f8_status f8_last_device_status(void *stream);
 
