@@ -196,6 +196,63 @@ __device__ __forceinline__ float max_of(const float (&f)[E])
     return m;
 }
 
+// Two bf16 at a time: the larger of each pair, without (max2) and with
+// (max2_nan) a NaN that either holds.
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t max2_nan(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b)
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+// The largest element of a chunk (a NaN only if all are).
+template <typename T>
+__device__ __forceinline__ float chunk_max(uint4 v);
+template <>
+__device__ __forceinline__ float chunk_max<__nv_bfloat16>(uint4 v)
+{
+    const uint32_t m = max2(max2(v.x, v.y), max2(v.z, v.w));
+    return fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xFFFF0000u));
+}
+template <>
+__device__ __forceinline__ float chunk_max<float>(uint4 v)
+{
+    return fmaxf(fmaxf(__uint_as_float(v.x), __uint_as_float(v.y)),
+                 fmaxf(__uint_as_float(v.z), __uint_as_float(v.w)));
+}
+
+// No element of a chunk below `low` (elements pairwise in one register for
+// bf16, whose `low` then is rounded to bf16).
+template <typename T>
+__device__ __forceinline__ uint4 chunk_floor(uint4 v, float low);
+template <>
+__device__ __forceinline__ uint4 chunk_floor<__nv_bfloat16>(uint4 v, float low)
+{
+    const __nv_bfloat162 h = __float22bfloat162_rn(make_float2(low, low));
+    const uint32_t l = *reinterpret_cast<const uint32_t *>(&h);
+    return make_uint4(max2_nan(v.x, l), max2_nan(v.y, l), max2_nan(v.z, l), max2_nan(v.w, l));
+}
+template <>
+__device__ __forceinline__ uint4 chunk_floor<float>(uint4 v, float low)
+{
+    return make_uint4(__float_as_uint(max_nan(__uint_as_float(v.x), low)),
+                      __float_as_uint(max_nan(__uint_as_float(v.y), low)),
+                      __float_as_uint(max_nan(__uint_as_float(v.z), low)),
+                      __float_as_uint(max_nan(__uint_as_float(v.w), low)));
+}
+
 // ------------------------------------------------------------ softmax sums
 struct Stats {
     float m, s, h;  // h only where the entropy is wanted
@@ -217,11 +274,10 @@ __device__ __forceinline__ Stats join(Stats a, Stats b, float c)
     return r;
 }
 
-// Adds N values to the running sums.
-template <bool ENT, int N>
-__device__ __forceinline__ void add_values(Stats &t, const float (&f)[N], float c)
+// The sums' reference grows to bm.
+template <bool ENT>
+__device__ __forceinline__ void raise_max(Stats &t, float bm, float c)
 {
-    const float bm = max_of(f);
     if (bm > t.m) {
         const float d = fmaxf((t.m - bm) * c, kFloor2);
         const float r = ex2(d);
@@ -230,22 +286,81 @@ __device__ __forceinline__ void add_values(Stats &t, const float (&f)[N], float 
         t.s *= r;
         t.m = bm;
     }
+}
+
+// Adds N values to the running sums, whatever they are.
+template <bool ENT, int N>
+__device__ __forceinline__ void add_values(Stats &t, const float (&f)[N], float c)
+{
+    raise_max<ENT>(t, max_of(f), c);
     const float m = t.m == F8_NEG_INF ? 0.0f : t.m;
-    float s0 = 0.0f, s1 = 0.0f, h0 = 0.0f, h1 = 0.0f;
 #pragma unroll
-    for (int e = 0; e < N; e += 2) {
-        const float d0 = (f[e] - m) * c, d1 = (f[e + 1] - m) * c;
-        const float e0 = ex2(d0), e1 = ex2(d1);
-        s0 += e0;
-        s1 += e1;
-        if (ENT) {
-            h0 = fmaf(e0, fmaxf(d0, kFloor2), h0);
-            h1 = fmaf(e1, fmaxf(d1, kFloor2), h1);
+    for (int e = 0; e < N; ++e) {
+        const float d = (f[e] - m) * c;
+        const float x = ex2(d);
+        t.s += x;
+        if (ENT)
+            t.h = fmaf(x, fmaxf(d, kFloor2), t.h);
+    }
+}
+
+// Past this m c (in units of log 2) the sums take add_values' steps.
+constexpr float kFastRange = 4096.0f;
+
+// Adds U chunks.  Where the maximum is of ordinary size the exponent is one
+// fused multiply-add, x c - mc with mc = fl(m c), two elements per
+// instruction; r = m c - mc, which every term then carries as a factor 2^r, is
+// taken out of the sums at the end.  For the entropy the elements are first
+// raised to 200 / c below the maximum, which leaves their 2^d at 0 and keeps
+// 0 * d finite for masked tokens.
+template <typename T, bool ENT, int U>
+__device__ __forceinline__ void add_chunks(Stats &t, const uint4 (&v)[U], float c, float inv_c)
+{
+    constexpr int E = Chunk<T>::E;
+    float bm = chunk_max<T>(v[0]);
+#pragma unroll
+    for (int u = 1; u < U; ++u)
+        bm = fmaxf(bm, chunk_max<T>(v[u]));
+    raise_max<ENT>(t, bm, c);
+    const float mc = t.m * c;
+    if (!(fabsf(mc) < kFastRange)) {
+#pragma unroll 1
+        for (int u = 0; u < U; ++u) {
+            uint4 w = v[0];
+#pragma unroll
+            for (int j = 1; j < U; ++j)
+                w = u == j ? v[j] : w;
+            float f[E];
+            unpack<T>(w, f);
+            add_values<ENT>(t, f, c);
+        }
+        return;
+    }
+    const float r = fmaf(t.m, c, -mc);
+    const float low = t.m - 200.0f * inv_c;
+    const float2 c2 = make_float2(c, c), n2 = make_float2(-mc, -mc);
+    float2 s[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+    float2 h[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        float f[E];
+        unpack<T>(ENT ? chunk_floor<T>(v[u], low) : v[u], f);
+#pragma unroll
+        for (int e = 0; e < E; e += 2) {
+            const float2 d = __ffma2_rn(make_float2(f[e], f[e + 1]), c2, n2);
+            const float2 x = make_float2(ex2(d.x), ex2(d.y));
+            s[(e >> 1) & 1] = __fadd2_rn(s[(e >> 1) & 1], x);
+            if (ENT)
+                h[(e >> 1) & 1] = __ffma2_rn(x, d, h[(e >> 1) & 1]);
         }
     }
-    t.s += s0 + s1;
-    if (ENT)
-        t.h += h0 + h1;
+    const float bs = (s[0].x + s[0].y) + (s[1].x + s[1].y);
+    const float corr = fmaf(-r, kLn2, 1.0f);
+    t.s = fmaf(bs, corr, t.s);
+    if (ENT) {
+        const float bh = (h[0].x + h[0].y) + (h[1].x + h[1].y);
+        t.h = fmaf(fmaf(-r, bs, bh), corr, t.h);
+    }
 }
 
 // The block's sums, in every thread.  `red`: one Stats per warp.
@@ -475,7 +590,7 @@ struct LogprobArgs {
     int64_t rows, ld;
     int vocab, top_k, cluster;
     const int64_t *tokens;
-    float inv_t, c;  // 1 / T, log2(e) / T
+    float inv_t, c, inv_c;  // 1 / T, log2(e) / T, T / log2(e)
     float *logp, *entropy, *lse;
     int32_t *top_ids;
     float *top_logp;
@@ -540,21 +655,15 @@ logprobs_kernel(const __grid_constant__ LogprobArgs a)
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u)
             v[u] = load_chunk(r, (g + u) * 32 + lane, g1 * 32, total, a.status);
-        float f[kUnroll * E];
+        if (TOP) {
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            float x[E];
-            unpack<T>(v[u], x);
-#pragma unroll
-            for (int e = 0; e < E; ++e)
-                f[u * E + e] = x[e];
-            if (TOP) {
-                const uint32_t key = __reduce_max_sync(0xFFFFFFFFu, order_key(max_of(x)));
+            for (int u = 0; u < kUnroll; ++u) {
+                const uint32_t key = __reduce_max_sync(0xFFFFFFFFu, order_key(chunk_max<T>(v[u])));
                 if (lane == 0 && g + u < g1)
                     gkeys[g + u - g0] = key;
             }
         }
-        add_values<true>(t, f, a.c);
+        add_chunks<T, true>(t, v, a.c, a.inv_c);
     }
     if (TOP)
         __syncthreads();
@@ -652,7 +761,8 @@ logprobs_kernel(const __grid_constant__ LogprobArgs a)
         if (a.lse != nullptr)
             a.lse[row] = lse;
         if (a.entropy != nullptr)
-            a.entropy[row] = none ? 0.0f : (lse != lse ? F8_NAN : ls - kLn2 * t.h / t.s);
+            // both are of one sign by definition, also where they round to 0
+            a.entropy[row] = none ? 0.0f : (lse != lse ? F8_NAN : fmaxf(ls - kLn2 * t.h / t.s, 0.0f));
         if (a.logp != nullptr) {
             // from the difference to the maximum: |logits| does not cancel
             float lp = F8_NAN;
@@ -661,7 +771,7 @@ logprobs_kernel(const __grid_constant__ LogprobArgs a)
             else if (none)
                 lp = F8_NEG_INF;
             else if (lse == lse)
-                lp = (as_float(r.base[r.off + tok]) - t.m) * a.inv_t - ls;
+                lp = fminf((as_float(r.base[r.off + tok]) - t.m) * a.inv_t - ls, 0.0f);
             a.logp[row] = lp;
         }
     }
@@ -683,7 +793,7 @@ logprobs_kernel(const __grid_constant__ LogprobArgs a)
             a.top_ids[row * k + place] = static_cast<int32_t>(mi[list[i]]);
             a.top_logp[row * k + place] =
                 none ? F8_NEG_INF
-                     : (lse != lse ? F8_NAN : (key_value(key) - t.m) * a.inv_t - ls);
+                     : (lse != lse ? F8_NAN : fminf((key_value(key) - t.m) * a.inv_t - ls, 0.0f));
         }
     }
 }
@@ -992,6 +1102,18 @@ __device__ __forceinline__ void drop_slots(const Slots &s, const Row<T> &r, int 
     }
 }
 
+template <typename T>
+__device__ __forceinline__ uint4 without_slots(const Slots &s, const Row<T> &r, int ch, uint4 v)
+{
+    if (s.head[ch % kHeads] >= 0) {
+        float f[Chunk<T>::E];
+        unpack<T>(v, f);
+        drop_slots(s, r, ch, f);
+        v = pack<T>(f);  // exact: the values are the chunk's own
+    }
+    return v;
+}
+
 // The loss of a row from the slots and the student's statistics over the
 // whole vocabulary (TAIL: over the tokens outside the slots' ids); all threads
 // of the block.  Gives lse and the student's mass outside.
@@ -1087,18 +1209,12 @@ distill_fwd_kernel(const __grid_constant__ DistillArgs a)
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u)
             v[u] = load_chunk(r, (g + u) * 32 + lane, g1 * 32, total, a.status);
-        float f[kUnroll * E];
+        if (TAIL) {
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            float x[E];
-            unpack<T>(v[u], x);
-            if (TAIL)
-                drop_slots(slots, r, (g + u) * 32 + lane, x);
-#pragma unroll
-            for (int e = 0; e < E; ++e)
-                f[u * E + e] = x[e];
+            for (int u = 0; u < kUnroll; ++u)
+                v[u] = without_slots(slots, r, (g + u) * 32 + lane, v[u]);
         }
-        add_values<false>(t, f, a.c);
+        add_chunks<T, false>(t, v, a.c, 0.0f);
     }
     const int ec = r.edge(edge_of_thread(), g0 * 32, g1 * 32);
     if (ec >= 0) {
@@ -1279,18 +1395,12 @@ distill_fused_kernel(const __grid_constant__ DistillArgs a)
                 v[u] = load_chunk(r, cb + u * N + tid, we, total, a.status);
 #pragma unroll
             for (int h = 0; h < kNV; h += kUnroll) {
-                float f[kUnroll * E];
+                uint4 w[kUnroll];
 #pragma unroll
-                for (int u = 0; u < kUnroll; ++u) {
-                    float x[E];
-                    unpack<T>(v[h + u], x);
-                    if (TAIL)
-                        drop_slots(slots, r, cb + (h + u) * N + tid, x);
-#pragma unroll
-                    for (int e = 0; e < E; ++e)
-                        f[u * E + e] = x[e];
-                }
-                add_values<false>(t, f, a.c);
+                for (int u = 0; u < kUnroll; ++u)
+                    w[u] = TAIL ? without_slots(slots, r, cb + (h + u) * N + tid, v[h + u])
+                                : v[h + u];
+                add_chunks<T, false>(t, w, a.c, 0.0f);
             }
         }
         t = block_join<false, WARPS>(t, a.c, red);
@@ -1570,6 +1680,7 @@ f8_status f8_token_logprobs(const void *logits, f8_dtype type, int64_t rows, int
     a.tokens = tokens;
     a.inv_t = 1.0f / temperature;
     a.c = static_cast<float>(kLog2e / static_cast<double>(temperature));
+    a.inv_c = static_cast<float>(static_cast<double>(temperature) / kLog2e);
     a.logp = logp;
     a.entropy = entropy;
     a.lse = lse;

@@ -26,6 +26,7 @@
 
 #include <algorithm>
 #include <cstdint>
+#include <mutex>
 
 #include "f8_internal.h"
 #include "f8_ptx.cuh"
@@ -225,6 +226,329 @@ __device__ __forceinline__ void block_amax(uint32_t m2, int mode, unsigned *amax
 
 __host__ __device__ constexpr int block_threads(int tpr) { return tpr < 256 ? 256 : tpr; }
 
+// ------------------------------------------------------------ rows by bulk copies
+// The ring kernels bring rows into shared memory with bulk copies, several
+// rows ahead, so that the loads in flight do not depend on how many threads
+// the registers leave room for: a group of TPR threads walks its rows (stride:
+// all groups of the grid) over `stages` slots, and its thread 0 refills a slot
+// once the group has taken the row into registers.  A copy covers the row's
+// 16-byte pieces, so a row may start inside one (widths that are no multiple
+// of 8); the piece that would reach past the last row's end is read directly.
+constexpr int kMaxStages = 8;
+
+struct RowCopy {
+    int64_t first;   // element at the slot's start
+    int shift;       // elements before the row in the slot
+    uint32_t bytes;  // copied
+    int tail;        // elements of the row past the copied ones
+};
+
+template <typename T>
+__device__ __forceinline__ RowCopy row_copy(int64_t row, int64_t rows, int64_t cols)
+{
+    constexpr int64_t P = 16 / sizeof(T);
+    const int64_t b = row * cols, e = b + cols, total = rows * cols;
+    RowCopy c;
+    c.first = b / P * P;
+    c.shift = static_cast<int>(b - c.first);
+    const int64_t stop = min((e + P - 1) / P * P, total / P * P);
+    c.bytes = static_cast<uint32_t>((stop - c.first) * static_cast<int64_t>(sizeof(T)));
+    c.tail = static_cast<int>(max(e - max(stop, b), static_cast<int64_t>(0)));
+    return c;
+}
+
+// N tensors' rows in one slot, each `pitch` bytes.
+template <typename T, int N>
+struct Ring {
+    uint8_t *slots;
+    uint64_t *full;
+    int stages;
+    uint32_t pitch;
+    int64_t rows, cols;
+    const T *src[N];
+    bool ok;  // no wait has run out
+
+    __device__ __forceinline__ T *row(int slot, int which) const
+    {
+        return reinterpret_cast<T *>(slots + (slot * N + which) * pitch);
+    }
+    __device__ __forceinline__ void fill(int slot, int64_t r) const
+    {
+        const RowCopy c = row_copy<T>(r, rows, cols);
+        mbar_arrive_expect_tx(&full[slot], N * c.bytes);
+        if (c.bytes > 0) {
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                bulk_load(row(slot, i), src[i] + c.first, c.bytes, &full[slot]);
+        }
+    }
+    __device__ __forceinline__ void wait(int slot, uint32_t parity, uint64_t limit_ns,
+                                         unsigned *status)
+    {
+        if (ok && !mbar_wait(&full[slot], parity, nullptr, limit_ns)) {
+            ok = false;  // go on without waiting: every thread keeps to the barriers
+            atomicOr(status, kStatusTimeout);
+        }
+    }
+};
+
+template <int TPR>
+__device__ __forceinline__ void group_sync(int group)
+{
+    asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "n"(TPR) : "memory");
+}
+
+// The row's elements past the copied ones (of the tensor's last row only),
+// into the slot by the group's first threads.
+template <typename T, int N, int TPR>
+__device__ __forceinline__ void fill_tail(const Ring<T, N> &ring, int slot, int64_t r, int group,
+                                          int t)
+{
+    const RowCopy c = row_copy<T>(r, ring.rows, ring.cols);
+    if (c.tail == 0)
+        return;
+    if (t < c.tail) {
+        const int64_t at = (r + 1) * ring.cols - c.tail + t;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            ring.row(slot, i)[at - c.first] = ring.src[i][at];
+    }
+    group_sync<TPR>(group);
+}
+
+// Sum of a, and of b with PAIR, over the group, in a fixed order; two floats
+// per warp and use in `red`, the uses alternating between two halves, so one
+// barrier each.
+template <int TPR, bool PAIR>
+__device__ __forceinline__ float2 ring_sum(float a, float b, float *red, int group, int &buf)
+{
+    constexpr int W = TPR / 32;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
+        if (PAIR)
+            b += __shfl_xor_sync(0xFFFFFFFFu, b, o);
+    }
+    float *r = red + (group * 2 + buf) * 2 * W;
+    buf ^= 1;
+    const int t = static_cast<int>(threadIdx.x) % TPR;
+    if ((t & 31) == 0) {
+        r[t >> 5] = a;
+        if (PAIR)
+            r[W + (t >> 5)] = b;
+    }
+    group_sync<TPR>(group);
+    a = b = 0.0f;
+#pragma unroll
+    for (int w = 0; w < W; w += 4) {
+        const float4 v = *reinterpret_cast<const float4 *>(r + w);
+        a += (v.x + v.y) + (v.z + v.w);
+        if (PAIR) {
+            const float4 u = *reinterpret_cast<const float4 *>(r + W + w);
+            b += (u.x + u.y) + (u.z + u.w);
+        }
+    }
+    return make_float2(a, b);
+}
+
+// The slot's columns of one thread as VEC-wide vectors u * TPR + t.
+template <typename T, int VEC, int NV, int TPR>
+__device__ __forceinline__ void take(const T *row, int shift, int nvec, int t,
+                                     typename Raw<T, VEC>::type (&v)[NV])
+{
+    using R = typename Raw<T, VEC>::type;
+#pragma unroll
+    for (int u = 0; u < NV; ++u) {
+        const int i = u * TPR + t;
+        v[u] = R{};
+        if (i < nvec)
+            v[u] = VEC == 1 ? reinterpret_cast<const R *>(row + shift)[i]
+                            : reinterpret_cast<const R *>(row)[i];
+    }
+}
+
+// Values in pairs: two neighbouring elements of a vector, or (VEC 1) the
+// elements of two vectors.
+template <typename T, int VEC, int NV>
+__device__ __forceinline__ void to_pairs(const typename Raw<T, VEC>::type (&v)[NV],
+                                         float2 (&f)[NV * VEC / 2])
+{
+#pragma unroll
+    for (int u = 0; u < NV; ++u) {
+        float x[VEC];
+        unpack<T>(v[u], x);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+            const int i = u * VEC + e;
+            if (i & 1)
+                f[i / 2].y = x[e];
+            else
+                f[i / 2].x = x[e];
+        }
+    }
+}
+
+template <int VEC, int NV, int TPR>
+__device__ __forceinline__ void param_pairs(const void *p, int type, int cols, int t,
+                                            float2 (&f)[NV * VEC / 2], unsigned *status)
+{
+#pragma unroll
+    for (int u = 0; u < NV; ++u) {
+        float x[VEC];
+        const int i = u * TPR + t;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+            x[e] = 0.0f;
+        if (p != nullptr && i < cols / VEC)
+            load_param<VEC>(p, type, i * VEC, cols, x, status);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+            const int k = u * VEC + e;
+            if (k & 1)
+                f[k / 2].y = x[e];
+            else
+                f[k / 2].x = x[e];
+        }
+    }
+}
+
+// The pairs of vector u as an array of VEC floats.
+template <int VEC, int NV>
+__device__ __forceinline__ void pair_vector(const float2 (&f)[NV * VEC / 2], int u, float (&x)[VEC])
+{
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+        const int k = u * VEC + e;
+        x[e] = (k & 1) ? f[k / 2].y : f[k / 2].x;
+    }
+}
+
+// Forward on the ring.  w and b stay in registers as fp32; the arithmetic takes
+// two elements per instruction.
+template <typename T, int VEC, int NV, int TPR>
+__global__ void __launch_bounds__(block_threads(TPR), 768 / block_threads(TPR))
+norm_fwd_ring_kernel(const T *x, const void *__restrict__ w, const void *__restrict__ b, int w_type,
+                     int rms, int64_t rows, int cols, float eps, T *y, float *__restrict__ mean,
+                     float *__restrict__ rstd, unsigned *amax, int amax_mode, int stages,
+                     uint32_t pitch, uint64_t limit_ns, unsigned *status)
+{
+    using R = typename Raw<T, VEC>::type;
+    constexpr int kGroups = block_threads(TPR) / TPR;
+    constexpr int P = NV * VEC / 2;
+    extern __shared__ __align__(16) uint8_t dyn[];
+    __shared__ __align__(16) float red[4 * block_threads(TPR) / 32];
+    __shared__ __align__(8) uint64_t full[kGroups * kMaxStages];
+    const int group = threadIdx.x / TPR, t = threadIdx.x % TPR;
+    Ring<T, 1> ring{dyn + static_cast<size_t>(group) * stages * pitch,
+                    full + group * kMaxStages, stages, pitch, rows, cols, {x}, true};
+    if (t == 0) {
+        for (int i = 0; i < stages; ++i)
+            mbar_init(&ring.full[i], 1);
+        fence_mbar_init();
+    }
+    griddep_wait();
+    griddep_launch_dependents();
+    const int64_t step = static_cast<int64_t>(gridDim.x) * kGroups;
+    const int64_t row0 = static_cast<int64_t>(blockIdx.x) * kGroups + group;
+    __syncthreads();
+    if (t == 0)
+        for (int i = 0; i < stages; ++i)
+            if (row0 + i * step < rows)
+                ring.fill(i, row0 + i * step);
+    float2 fw[P], fb[P];
+    param_pairs<VEC, NV, TPR>(w, w_type, cols, t, fw, status);
+    param_pairs<VEC, NV, TPR>(b, w_type, cols, t, fb, status);
+    const int nvec = cols / VEC;
+    const float inv_c = 1.0f / static_cast<float>(cols);
+    const int64_t total = rows * cols;
+    uint32_t m2 = 0;
+    int buf = 0, slot = 0;
+    uint32_t parity = 0;
+    for (int64_t row = row0; row < rows; row += step) {
+        ring.wait(slot, parity, limit_ns, status);
+        int shift = 0;
+        if (VEC == 1) {
+            shift = row_copy<T>(row, rows, cols).shift;
+            fill_tail<T, 1, TPR>(ring, slot, row, group, t);
+        }
+        R v[NV];
+        take<T, VEC, NV, TPR>(ring.row(slot, 0), shift, nvec, t, v);
+        float2 f[P];
+        to_pairs<T, VEC, NV>(v, f);
+        // elements past the row are 0 and take part in the first sum only
+        float mu = 0.0f;
+        if (!rms) {
+            float2 s = f[0];
+#pragma unroll
+            for (int i = 1; i < P; ++i)
+                s = __fadd2_rn(s, f[i]);
+            mu = ring_sum<TPR, false>(s.x + s.y, 0.0f, red, group, buf).x * inv_c;
+        }
+        float2 q = make_float2(0.0f, 0.0f);
+        const float2 nmu = make_float2(-mu, -mu);
+#pragma unroll
+        for (int u = 0; u < NV; ++u) {
+            if (u * TPR + t < nvec) {
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    const int k = u * VEC + e;
+                    if (VEC > 1) {
+                        if ((k & 1) == 0) {
+                            f[k / 2] = __fadd2_rn(f[k / 2], nmu);
+                            q = __ffma2_rn(f[k / 2], f[k / 2], q);
+                        }
+                    } else if (k & 1) {
+                        f[k / 2].y -= mu;
+                        q.y = fmaf(f[k / 2].y, f[k / 2].y, q.y);
+                    } else {
+                        f[k / 2].x -= mu;
+                        q.x = fmaf(f[k / 2].x, f[k / 2].x, q.x);
+                    }
+                }
+            }
+        }
+        const float r =
+            1.0f / sqrtf(ring_sum<TPR, false>(q.x + q.y, 0.0f, red, group, buf).x * inv_c + eps);
+        // every thread has taken its part of the row: the slot can be refilled
+        if (t == 0) {
+            if (row + stages * step < rows)
+                ring.fill(slot, row + stages * step);
+            if (mean != nullptr && !rms)
+                mean[row] = mu;
+            if (rstd != nullptr)
+                rstd[row] = r;
+        }
+        const float2 r2 = make_float2(r, r);
+#pragma unroll
+        for (int i = 0; i < P; ++i)
+            f[i] = __ffma2_rn(__fmul2_rn(f[i], r2), fw[i], fb[i]);
+        const int64_t at = row * cols;
+#pragma unroll
+        for (int u = 0; u < NV; ++u) {
+            const int64_t i = u * TPR + t;
+            if (i < nvec) {
+                float o[VEC];
+                pair_vector<VEC, NV>(f, u, o);
+                R p;
+                pack<T>(o, p);
+                m2 = abs_max2(m2, p);
+                if (in_range(at + i * VEC, VEC, total, status))
+                    *reinterpret_cast<R *>(y + at + i * VEC) = p;
+            }
+        }
+        if (++slot == stages) {
+            slot = 0;
+            parity ^= 1u;
+        }
+    }
+    // copies that a wait gave up on land before the block leaves
+    if (!ring.ok && t == 0)
+        for (int i = 0; i < stages; ++i)
+            mbar_wait(&ring.full[i], parity ^ (i < slot ? 1u : 0u), nullptr, limit_ns);
+    if (amax_mode != kAmaxNone)
+        block_amax(m2, amax_mode, amax, status);
+}
+
 // ------------------------------------------------------------ forward
 template <typename T, int VEC, int NV, int TPR>
 __global__ void __launch_bounds__(block_threads(TPR))
@@ -384,6 +708,167 @@ norm_fwd_wide_kernel(const T *x, const void *__restrict__ w, const void *__restr
     }
     if (amax_mode != kAmaxNone)
         block_amax(m2, amax_mode, amax, status);
+}
+
+// ------------------------------------------------------------ backward on the ring
+// As the forward, with rows of dy beside those of x in a slot.  A block has
+// 512 threads in as many groups as its rows' width leaves; their column sums
+// are joined in shared memory at the end, so there is one partial row per
+// block.  Elements past the row are 0 and add nothing anywhere.
+constexpr int kBwdThreads = 512;
+
+template <typename T, int VEC, int NV, int TPR>
+__global__ void __launch_bounds__(kBwdThreads, 1)
+norm_bwd_ring_kernel(const T *dy, const T *x, const void *__restrict__ w, int w_type,
+                     const float *__restrict__ mean, const float *__restrict__ rstd, int rms,
+                     int64_t rows, int cols, T *dx, float *__restrict__ parts, int stages,
+                     uint32_t pitch, uint64_t limit_ns, unsigned *status)
+{
+    using R = typename Raw<T, VEC>::type;
+    constexpr int kGroups = kBwdThreads / TPR;
+    constexpr int P = NV * VEC / 2;
+    extern __shared__ __align__(16) uint8_t dyn[];
+    __shared__ __align__(16) float red[4 * kBwdThreads / 32];
+    __shared__ __align__(8) uint64_t full[kGroups * kMaxStages];
+    const int group = threadIdx.x / TPR, t = threadIdx.x % TPR;
+    Ring<T, 2> ring{dyn + static_cast<size_t>(group) * stages * 2 * pitch,
+                    full + group * kMaxStages, stages, pitch, rows, cols, {x, dy}, true};
+    if (t == 0) {
+        for (int i = 0; i < stages; ++i)
+            mbar_init(&ring.full[i], 1);
+        fence_mbar_init();
+    }
+    griddep_wait();
+    griddep_launch_dependents();
+    const int64_t step = static_cast<int64_t>(gridDim.x) * kGroups;
+    const int64_t row0 = static_cast<int64_t>(blockIdx.x) * kGroups + group;
+    __syncthreads();
+    if (t == 0)
+        for (int i = 0; i < stages; ++i)
+            if (row0 + i * step < rows)
+                ring.fill(i, row0 + i * step);
+    float2 fw[P], aw[P], ab[P];
+    param_pairs<VEC, NV, TPR>(w, w_type, cols, t, fw, status);
+#pragma unroll
+    for (int i = 0; i < P; ++i)
+        aw[i] = ab[i] = make_float2(0.0f, 0.0f);
+    const int nvec = cols / VEC;
+    const float inv_c = 1.0f / static_cast<float>(cols);
+    const int64_t total = rows * cols;
+    int buf = 0, slot = 0;
+    uint32_t parity = 0;
+    // the next row's statistics are on their way while a row is worked on
+    float mu_next = 0.0f, r_next = 0.0f;
+    if (row0 < rows) {
+        mu_next = rms ? 0.0f : mean[row0];
+        r_next = rstd[row0];
+    }
+    for (int64_t row = row0; row < rows; row += step) {
+        const float mu = mu_next, r = r_next;
+        if (row + step < rows) {
+            mu_next = rms ? 0.0f : mean[row + step];
+            r_next = rstd[row + step];
+        }
+        ring.wait(slot, parity, limit_ns, status);
+        int shift = 0;
+        if (VEC == 1) {
+            shift = row_copy<T>(row, rows, cols).shift;
+            fill_tail<T, 2, TPR>(ring, slot, row, group, t);
+        }
+        R vx[NV], vd[NV];
+        take<T, VEC, NV, TPR>(ring.row(slot, 0), shift, nvec, t, vx);
+        take<T, VEC, NV, TPR>(ring.row(slot, 1), shift, nvec, t, vd);
+        float2 xh[P], g[P];
+        to_pairs<T, VEC, NV>(vx, xh);
+        to_pairs<T, VEC, NV>(vd, g);
+        const float2 r2 = make_float2(r, r), nmu = make_float2(-mu, -mu);
+        float2 s1 = make_float2(0.0f, 0.0f), s2 = s1;
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            xh[i] = __fmul2_rn(__fadd2_rn(xh[i], nmu), r2);
+            aw[i] = __ffma2_rn(g[i], xh[i], aw[i]);
+            ab[i] = __fadd2_rn(ab[i], g[i]);
+            g[i] = __fmul2_rn(g[i], fw[i]);
+            s1 = __ffma2_rn(g[i], xh[i], s1);
+            s2 = __fadd2_rn(s2, g[i]);
+        }
+        const float2 c = ring_sum<TPR, true>(s1.x + s1.y, s2.x + s2.y, red, group, buf);
+        if (t == 0 && row + stages * step < rows)
+            ring.fill(slot, row + stages * step);
+        if (dx != nullptr) {
+            const float k1 = -r * (c.x * inv_c), k2 = rms ? 0.0f : -r * (c.y * inv_c);
+            const float2 n1 = make_float2(k1, k1), n2 = make_float2(k2, k2);
+            const int64_t at = row * cols;
+#pragma unroll
+            for (int i = 0; i < P; ++i)
+                g[i] = __ffma2_rn(g[i], r2, __ffma2_rn(xh[i], n1, n2));
+#pragma unroll
+            for (int u = 0; u < NV; ++u) {
+                const int64_t i = u * TPR + t;
+                if (i < nvec) {
+                    float o[VEC];
+                    pair_vector<VEC, NV>(g, u, o);
+                    R p;
+                    pack<T>(o, p);
+                    if (in_range(at + i * VEC, VEC, total, status))
+                        *reinterpret_cast<R *>(dx + at + i * VEC) = p;
+                }
+            }
+        }
+        if (++slot == stages) {
+            slot = 0;
+            parity ^= 1u;
+        }
+    }
+    if (!ring.ok && t == 0)
+        for (int i = 0; i < stages; ++i)
+            mbar_wait(&ring.full[i], parity ^ (i < slot ? 1u : 0u), nullptr, limit_ns);
+    if (parts == nullptr)
+        return;
+    // the groups' sums joined in group order, two floats per thread at a time
+    if (kGroups > 1) {
+        float2 *ex = reinterpret_cast<float2 *>(dyn);
+#pragma unroll 1
+        for (int i = 0; i < 2 * P; ++i) {
+            float2 v = make_float2(0.0f, 0.0f);
+#pragma unroll
+            for (int k = 0; k < P; ++k) {
+                v = i == k ? aw[k] : v;
+                v = i == P + k ? ab[k] : v;
+            }
+            __syncthreads();
+            ex[threadIdx.x] = v;
+            __syncthreads();
+            if (group == 0) {
+#pragma unroll
+                for (int j = 1; j < kGroups; ++j)
+                    v = __fadd2_rn(v, ex[j * TPR + t]);
+#pragma unroll
+                for (int k = 0; k < P; ++k) {
+                    aw[k] = i == k ? v : aw[k];
+                    ab[k] = i == P + k ? v : ab[k];
+                }
+            }
+        }
+    }
+    if (group == 0) {
+        float *p = parts + static_cast<int64_t>(blockIdx.x) * 2 * cols;
+#pragma unroll
+        for (int u = 0; u < NV; ++u) {
+            const int i = u * TPR + t;
+            if (i < nvec) {
+                float o[VEC];
+                pair_vector<VEC, NV>(aw, u, o);
+#pragma unroll
+                for (int e = 0; e < VEC; ++e)
+                    p[i * VEC + e] = o[e];
+                pair_vector<VEC, NV>(ab, u, o);
+#pragma unroll
+                for (int e = 0; e < VEC; ++e)
+                    p[cols + i * VEC + e] = o[e];
+            }
+        }
+    }
 }
 
 // ------------------------------------------------------------ backward
@@ -554,9 +1039,11 @@ norm_cols_wide_kernel(const T *__restrict__ dy, const T *__restrict__ x,
     p[cols + c] = ab;
 }
 
-// dw and db from the partial rows, added in order: 32 columns per block, 8
-// threads per column, each every eighth partial row.
-__global__ void __launch_bounds__(256)
+// dw and db from the partial rows, in a fixed order: 32 columns per block, 32
+// threads per column, each every 32nd partial row.
+constexpr int kReduceThreads = 1024;
+
+__global__ void __launch_bounds__(kReduceThreads)
 norm_reduce_kernel(const float *__restrict__ parts, int nparts, int64_t cols, int w_type,
                    void *__restrict__ dw, void *__restrict__ db, unsigned *status)
 {
@@ -565,27 +1052,29 @@ norm_reduce_kernel(const float *__restrict__ parts, int nparts, int64_t cols, in
     void *out = blockIdx.y == 0 ? dw : db;
     if (out == nullptr)
         return;
-    __shared__ float acc[8][33];
+    __shared__ float acc[32][33];
     const int lane = threadIdx.x & 31, k = threadIdx.x >> 5;
     const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + lane;
     float s = 0.0f;
     if (c < cols) {
         const float *p = parts + static_cast<int64_t>(blockIdx.y) * cols + c;
-#pragma unroll 4
-        for (int i = k; i < nparts; i += 8)
+#pragma unroll 8
+        for (int i = k; i < nparts; i += 32)
             s += p[static_cast<int64_t>(i) * 2 * cols];
     }
     acc[k][lane] = s;
     __syncthreads();
-    if (k == 0 && c < cols && in_range(c, 1, cols, status)) {
-        s = 0.0f;
+    // warp k adds the 32 sums of column k
+    s = acc[lane][k];
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            s += acc[i][lane];
+    for (int o = 16; o > 0; o >>= 1)
+        s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+    const int64_t col = static_cast<int64_t>(blockIdx.x) * 32 + k;
+    if (lane == 0 && col < cols && in_range(col, 1, cols, status)) {
         if (w_type == kBf16)
-            static_cast<__nv_bfloat16 *>(out)[c] = __float2bfloat16_rn(s);
+            static_cast<__nv_bfloat16 *>(out)[col] = __float2bfloat16_rn(s);
         else
-            static_cast<float *>(out)[c] = s;
+            static_cast<float *>(out)[col] = s;
     }
 }
 
@@ -630,6 +1119,82 @@ cudaError_t fwd_launch(const FwdArgs &a, const DeviceInfo &dev, cudaStream_t st,
                       static_cast<T *>(a.y), a.mean, a.rstd, a.amax, a.amax_mode, dev.status);
 }
 
+// Ring launches.  Shared memory for the rows: what leaves room for the blocks
+// that the registers allow per SM.
+constexpr int kRingBytes = 200 * 1024;
+
+template <auto Kernel>
+cudaError_t allow_ring(const DeviceInfo &dev)
+{
+    static std::once_flag once[64];
+    static cudaError_t err[64];
+    const int d = dev.ordinal & 63;
+    std::call_once(once[d], [&] {
+        err[d] = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
+    });
+    return err[d];
+}
+
+struct RingPlan {
+    int grid, stages;
+    uint32_t pitch;
+    size_t smem;
+};
+
+// Blocks and slots for `groups` groups a block, `per_sm` blocks an SM and
+// `tensors` rows a slot.
+RingPlan ring_plan(int64_t rows, int64_t cols, int esize, int groups, int per_sm, int tensors,
+                   const DeviceInfo &dev)
+{
+    RingPlan p;
+    p.grid = static_cast<int>(std::max<int64_t>(
+        1, std::min<int64_t>((rows + groups - 1) / groups,
+                             static_cast<int64_t>(dev.sm_count) * per_sm)));
+    // up to 15 bytes before and after the row
+    p.pitch = static_cast<uint32_t>((cols * esize + 15 + 15) / 16 * 16);
+    const int64_t per_group = (rows + static_cast<int64_t>(p.grid) * groups - 1) /
+                              (static_cast<int64_t>(p.grid) * groups);
+    const int64_t fit = kRingBytes / per_sm / (static_cast<int64_t>(groups) * tensors * p.pitch);
+    p.stages = static_cast<int>(std::min<int64_t>(std::min<int64_t>(fit, kMaxStages), per_group));
+    p.smem = static_cast<size_t>(groups) * p.stages * tensors * p.pitch;
+    return p;
+}
+
+constexpr int fwd_blocks(int tpr) { return 768 / block_threads(tpr); }
+
+template <typename T, int VEC, int NV, int TPR>
+cudaError_t fwd_ring(const FwdArgs &a, const DeviceInfo &dev, cudaStream_t st, int *nparts)
+{
+    const RingPlan p = ring_plan(a.rows, a.cols, sizeof(T), block_threads(TPR) / TPR,
+                                 fwd_blocks(TPR), 1, dev);
+    const cudaError_t e = allow_ring<norm_fwd_ring_kernel<T, VEC, NV, TPR>>(dev);
+    if (e != cudaSuccess)
+        return e;
+    if (nparts != nullptr)
+        *nparts = p.grid;
+    return launch_pdl(norm_fwd_ring_kernel<T, VEC, NV, TPR>, dim3(p.grid), dim3(block_threads(TPR)),
+                      p.smem, st, static_cast<const T *>(a.x), a.w, a.b, a.w_type, a.rms, a.rows,
+                      static_cast<int>(a.cols), a.eps, static_cast<T *>(a.y), a.mean, a.rstd, a.amax,
+                      a.amax_mode, p.stages, p.pitch, wait_limit_ns(), dev.status);
+}
+
+template <typename T, int VEC, int NV, int TPR>
+cudaError_t bwd_ring(const BwdArgs &a, const DeviceInfo &dev, cudaStream_t st, int *nparts)
+{
+    const RingPlan p = ring_plan(a.rows, a.cols, sizeof(T), kBwdThreads / TPR, 1, 2, dev);
+    const cudaError_t e = allow_ring<norm_bwd_ring_kernel<T, VEC, NV, TPR>>(dev);
+    if (e != cudaSuccess)
+        return e;
+    *nparts = p.grid;
+    // the join at the end needs a float2 per thread
+    const size_t smem = std::max<size_t>(p.smem, sizeof(float2) * kBwdThreads);
+    return launch_pdl(norm_bwd_ring_kernel<T, VEC, NV, TPR>, dim3(p.grid), dim3(kBwdThreads), smem,
+                      st, static_cast<const T *>(a.dy), static_cast<const T *>(a.x), a.w, a.w_type,
+                      a.mean, a.rstd, a.rms, a.rows, static_cast<int>(a.cols),
+                      static_cast<T *>(a.dx), a.parts, p.stages, p.pitch, wait_limit_ns(),
+                      dev.status);
+}
+
 constexpr int kMaxBwdBlocksPerSm = 4;
 constexpr int kMaxWideParts = 64;
 
@@ -645,47 +1210,47 @@ cudaError_t bwd_launch(const BwdArgs &a, const DeviceInfo &dev, cudaStream_t st,
                       static_cast<int>(a.cols), static_cast<T *>(a.dx), a.parts, dev.status);
 }
 
-// Threads per row by the row's vectors: the smallest group whose registers
-// hold the row.
-template <typename T, int VEC, int NV>
+// Threads per row by its width: the smallest group that holds the row at 16
+// elements a thread (32 in the forward's widest).
+template <typename T, int VEC>
 cudaError_t fwd_pick(const FwdArgs &a, const DeviceInfo &dev, cudaStream_t st, int *nparts)
 {
-    const int64_t n = a.cols / VEC;
-    if (n <= 32 * NV)
+    constexpr int NV = 16 / VEC;
+    if (a.cols <= 512)
         return fwd_launch<T, VEC, NV, 32>(a, dev, st, nparts);
-    if (n <= 128 * NV)
-        return fwd_launch<T, VEC, NV, 128>(a, dev, st, nparts);
-    if (n <= 256 * NV)
-        return fwd_launch<T, VEC, NV, 256>(a, dev, st, nparts);
-    if (n <= 512 * NV)
-        return fwd_launch<T, VEC, NV, 512>(a, dev, st, nparts);
-    return fwd_launch<T, VEC, NV, 1024>(a, dev, st, nparts);
+    if (a.cols <= 2048)
+        return fwd_ring<T, VEC, NV, 128>(a, dev, st, nparts);
+    if (a.cols <= 4096)
+        return fwd_ring<T, VEC, NV, 256>(a, dev, st, nparts);
+    if (a.cols <= 8192)
+        return fwd_ring<T, VEC, NV, 512>(a, dev, st, nparts);
+    return fwd_ring<T, VEC, 2 * NV, 512>(a, dev, st, nparts);
 }
 
-template <typename T, int VEC, int NV>
+template <typename T, int VEC>
 cudaError_t bwd_pick(const BwdArgs &a, const DeviceInfo &dev, cudaStream_t st, int *nparts)
 {
-    const int64_t n = a.cols / VEC;
-    if (n <= 32 * NV)
+    constexpr int NV = 16 / VEC;
+    if (a.cols <= 512)
         return bwd_launch<T, VEC, NV, 32>(a, dev, st, nparts);
-    if (n <= 128 * NV)
-        return bwd_launch<T, VEC, NV, 128>(a, dev, st, nparts);
-    if (n <= 256 * NV)
-        return bwd_launch<T, VEC, NV, 256>(a, dev, st, nparts);
-    if (n <= 512 * NV)
-        return bwd_launch<T, VEC, NV, 512>(a, dev, st, nparts);
+    if (a.cols <= 2048)
+        return bwd_ring<T, VEC, NV, 128>(a, dev, st, nparts);
+    if (a.cols <= 4096)
+        return bwd_ring<T, VEC, NV, 256>(a, dev, st, nparts);
+    if (a.cols <= 8192)
+        return bwd_ring<T, VEC, NV, 512>(a, dev, st, nparts);
     return bwd_launch<T, VEC, NV, 1024>(a, dev, st, nparts);
 }
 
-constexpr int64_t kRegCols = 16384;  // 16 elements in each of 1024 threads
+constexpr int64_t kRegCols = 16384;  // 16 elements in each of 1024 threads, 32 in each of 512
 
 template <typename T>
 cudaError_t fwd_type(const FwdArgs &a, const DeviceInfo &dev, cudaStream_t st, int *nparts)
 {
     constexpr int VEC = 16 / sizeof(T);
     if (a.cols <= kRegCols)
-        return a.cols % VEC == 0 ? fwd_pick<T, VEC, 16 / VEC>(a, dev, st, nparts)
-                                 : fwd_pick<T, 1, 16>(a, dev, st, nparts);
+        return a.cols % VEC == 0 ? fwd_pick<T, VEC>(a, dev, st, nparts)
+                                 : fwd_pick<T, 1>(a, dev, st, nparts);
     const int64_t grid = std::min<int64_t>(a.rows, 2 * dev.sm_count);
     if (nparts != nullptr)
         *nparts = static_cast<int>(grid);
@@ -701,8 +1266,8 @@ cudaError_t bwd_type(const BwdArgs &a, const DeviceInfo &dev, cudaStream_t st)
     int nparts = 0;
     cudaError_t e = cudaSuccess;
     if (a.cols <= kRegCols) {
-        e = a.cols % VEC == 0 ? bwd_pick<T, VEC, 16 / VEC>(a, dev, st, &nparts)
-                              : bwd_pick<T, 1, 16>(a, dev, st, &nparts);
+        e = a.cols % VEC == 0 ? bwd_pick<T, VEC>(a, dev, st, &nparts)
+                              : bwd_pick<T, 1>(a, dev, st, &nparts);
     } else {
         // the column sums first: dx may be one of the inputs
         if (a.parts != nullptr) {
@@ -722,7 +1287,7 @@ cudaError_t bwd_type(const BwdArgs &a, const DeviceInfo &dev, cudaStream_t st)
     if (e != cudaSuccess || a.parts == nullptr)
         return e;
     return launch_pdl(norm_reduce_kernel, dim3(static_cast<unsigned>((a.cols + 31) / 32), 2),
-                      dim3(256), 0, st, static_cast<const float *>(a.parts), nparts, a.cols,
+                      dim3(kReduceThreads), 0, st, static_cast<const float *>(a.parts), nparts, a.cols,
                       a.w_type, a.dw, a.db, dev.status);
 }
 
