@@ -387,6 +387,33 @@ __device__ __forceinline__ Stats block_join(Stats t, float c, Stats *red)
     return t;
 }
 
+// The joined sums of the lanes of a warp, in every lane; without the entropy.
+__device__ __forceinline__ Stats warp_stats(Stats t, float c)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        Stats u;
+        u.m = __shfl_xor_sync(0xFFFFFFFFu, t.m, o);
+        u.s = __shfl_xor_sync(0xFFFFFFFFu, t.s, o);
+        u.h = 0.0f;
+        t = (threadIdx.x & o) ? join<false>(u, t, c) : join<false>(t, u, c);
+    }
+    return t;
+}
+// The same where lanes 16 .. 31 repeat lanes 0 .. 15.
+__device__ __forceinline__ Stats warp_stats_16(Stats t, float c)
+{
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) {
+        Stats u;
+        u.m = __shfl_xor_sync(0xFFFFFFFFu, t.m, o);
+        u.s = __shfl_xor_sync(0xFFFFFFFFu, t.s, o);
+        u.h = 0.0f;
+        t = (threadIdx.x & o) ? join<false>(u, t, c) : join<false>(t, u, c);
+    }
+    return t;
+}
+
 // Sum, or maximum, of one value per thread, in every thread, in a fixed order.
 template <int WARPS>
 __device__ __forceinline__ float block_sum(float v, float *red)
@@ -847,12 +874,25 @@ __device__ __forceinline__ uint32_t store_chunk(const Row<T> &r, T *out, bool sa
                     __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu));
 }
 
-// Zeros in columns [from, to) of an output row, by the threads of one block.
+// Zeros in columns [from, to) of an output row, by n threads of which this is
+// number t: 16-byte pieces, and single elements at the ends.
 template <typename T>
 __device__ __forceinline__ void zero_columns(T *out, int64_t from, int64_t to, int64_t out_at,
-                                             int64_t out_total, unsigned *status)
+                                             int64_t out_total, unsigned *status, int t, int n)
 {
-    for (int64_t i = from + threadIdx.x; i < to; i += blockDim.x)
+    constexpr int64_t E = Chunk<T>::E;
+    if (from >= to)
+        return;
+    const int64_t lead = (E - static_cast<int64_t>((reinterpret_cast<uintptr_t>(out + from) & 15u) /
+                                                   sizeof(T))) % E;
+    const int64_t v0 = min(from + lead, to), nv = (to - v0) / E;
+    for (int64_t i = from + t; i < v0; i += n)
+        if (in_range(out_at + i, 1, out_total, status))
+            out[i] = T(0.0f);
+    for (int64_t i = t; i < nv; i += n)
+        if (in_range(out_at + v0 + i * E, E, out_total, status))
+            *reinterpret_cast<uint4 *>(out + v0 + i * E) = make_uint4(0, 0, 0, 0);
+    for (int64_t i = v0 + nv * E + t; i < to; i += n)
         if (in_range(out_at + i, 1, out_total, status))
             out[i] = T(0.0f);
 }
@@ -970,7 +1010,8 @@ logprobs_bwd_kernel(const __grid_constant__ LogprobBwdArgs a)
         m2 = __vmaxu2(m2, store_elements(r, out, ec, f, out_at, out_total, a.status));
     }
     if (part == a.blocks_per_row - 1)
-        zero_columns(out, r.vocab, a.out.ld, out_at, out_total, a.status);
+        zero_columns(out, r.vocab, a.out.ld, out_at, out_total, a.status,
+                     static_cast<int>(threadIdx.x), static_cast<int>(blockDim.x));
     block_amax(m2, a.out.amax, a.status);
 }
 
@@ -990,15 +1031,16 @@ struct DistillArgs {
 
 // The row's slots in shared memory.  A table keyed by chunk number finds the
 // slots that name an element of a chunk: head[chunk % kHeads] starts a list
-// of slots.  Of equal ids only the first slot is listed; it carries their
-// summed q.
+// of slots.  Slots of equal ids each carry their summed q.
 constexpr int kHeads = 2048;
-struct Slots {
+struct SlotTable {
     int head[kHeads];
     int next[F8_MAX_TOP];
     int id[F8_MAX_TOP];     // -1: empty
     float q[F8_MAX_TOP];    // the slot's own q
-    float qsum[F8_MAX_TOP]; // of all slots with this id, at the first of them; else unused
+    float qsum[F8_MAX_TOP]; // of all slots with this id
+};
+struct Slots : SlotTable {
     float logq[F8_MAX_TOP];
     float z[F8_MAX_TOP];    // the student's logit at id
     uint8_t first[F8_MAX_TOP];
@@ -1080,8 +1122,8 @@ __device__ __forceinline__ SlotSums load_slots(const DistillArgs &a, const Row<T
         s.first[tid] = first;
         s.qsum[tid] = qs;
     }
-    // a list's order is free: its slots name different elements
-    if (table && first)
+    // a list's order is free: of slots with one id each gives the same values
+    if (table && id >= 0)
         s.next[tid] = atomicExch(&s.head[((id + r.off) / Chunk<T>::E) % kHeads], tid);
     __syncthreads();
     return out;
@@ -1089,7 +1131,7 @@ __device__ __forceinline__ SlotSums load_slots(const DistillArgs &a, const Row<T
 
 // -inf in the elements of chunk ch that a slot names.
 template <typename T>
-__device__ __forceinline__ void drop_slots(const Slots &s, const Row<T> &r, int ch,
+__device__ __forceinline__ void drop_slots(const SlotTable &s, const Row<T> &r, int ch,
                                            float (&f)[Chunk<T>::E])
 {
     constexpr int E = Chunk<T>::E;
@@ -1103,7 +1145,7 @@ __device__ __forceinline__ void drop_slots(const Slots &s, const Row<T> &r, int 
 }
 
 template <typename T>
-__device__ __forceinline__ uint4 without_slots(const Slots &s, const Row<T> &r, int ch, uint4 v)
+__device__ __forceinline__ uint4 without_slots(const SlotTable &s, const Row<T> &r, int ch, uint4 v)
 {
     if (s.head[ch % kHeads] >= 0) {
         float f[Chunk<T>::E];
@@ -1249,7 +1291,7 @@ distill_fwd_kernel(const __grid_constant__ DistillArgs a)
 
 // dlogits of one chunk: dense * p, and at the slots' ids scale (total p - q).
 template <typename T>
-__device__ __forceinline__ void slot_gradient(const Slots &s, const Row<T> &r, int ch,
+__device__ __forceinline__ void slot_gradient(const SlotTable &s, const Row<T> &r, int ch,
                                               const float (&p)[Chunk<T>::E], float scale,
                                               float total, float (&g)[Chunk<T>::E])
 {
@@ -1336,24 +1378,25 @@ distill_bwd_kernel(const __grid_constant__ DistillArgs a)
         m2 = __vmaxu2(m2, store_elements(r, out, ec, f, out_at, out_total, a.status));
     }
     if (part == a.blocks_per_row - 1)
-        zero_columns(out, r.vocab, a.out.ld, out_at, out_total, a.status);
+        zero_columns(out, r.vocab, a.out.ld, out_at, out_total, a.status,
+                     static_cast<int>(threadIdx.x), static_cast<int>(blockDim.x));
     block_amax(m2, a.out.amax, a.status);
 }
 
-// Loss and gradient together.  A cluster of C blocks shares a row, each thread
-// holding up to NV of its chunks in registers between the two phases, so a row
-// that fits is read once; a longer one is walked in stretches and read again
-// (from L2 where it still holds it).
+// Loss and gradient together, for short rows and for few.  A block, or a cluster
+// of C blocks, takes a row, each thread holding up to NV of its chunks in
+// registers between the two passes, so a row that fits is read once; a longer
+// one is walked in stretches and read again (from L2).
 constexpr int kNV = 8;
 
-template <typename T, bool TAIL, int WARPS>
-__global__ void __launch_bounds__(WARPS * 32)
+template <typename T, bool TAIL>
+__global__ void __launch_bounds__(kThreads)
 distill_fused_kernel(const __grid_constant__ DistillArgs a)
 {
     constexpr int E = Chunk<T>::E;
-    constexpr int N = WARPS * 32;
+    constexpr int N = kThreads;
     __shared__ __align__(16) Slots slots;
-    __shared__ Stats red[WARPS];
+    __shared__ Stats red[kWarps];
     __shared__ Stats parts[kMaxCluster];
     griddep_wait();
     griddep_launch_dependents();
@@ -1368,7 +1411,7 @@ distill_fused_kernel(const __grid_constant__ DistillArgs a)
     const bool same = same_offset(r, out);
     if (C > 1)
         cluster_start();
-    const SlotSums q = load_slots<T, TAIL, WARPS>(a, r, row, slots, true, true);
+    const SlotSums q = load_slots<T, TAIL, kWarps>(a, r, row, slots, true, true);
     const int per = (r.nch + C - 1) / C;
     const int c0 = min(r.nch, rank * per), c1 = min(r.nch, c0 + per);
     const float dl = a.dloss[row];
@@ -1403,7 +1446,7 @@ distill_fused_kernel(const __grid_constant__ DistillArgs a)
                 add_chunks<T, false>(t, w, a.c, 0.0f);
             }
         }
-        t = block_join<false, WARPS>(t, a.c, red);
+        t = block_join<false, kWarps>(t, a.c, red);
         if (C > 1) {
             cluster_started();
             if (tid < C)
@@ -1413,7 +1456,7 @@ distill_fused_kernel(const __grid_constant__ DistillArgs a)
             for (int i = 1; i < C; ++i)
                 t = join<false>(t, parts[i], a.c);
         }
-        const RowLoss o = row_loss<TAIL, WARPS>(a, slots, q, t, rank == 0);
+        const RowLoss o = row_loss<TAIL, kWarps>(a, slots, q, t, rank == 0);
         if (rank == 0 && tid == 0) {
             a.loss[row] = o.loss;
             if (o.bad || o.loss != o.loss)
@@ -1475,7 +1518,493 @@ distill_fused_kernel(const __grid_constant__ DistillArgs a)
             store_elements(r, out, ec, g, out_at, out_total, a.status);
     }
     if (rank == C - 1)
-        zero_columns(out, r.vocab, a.out.ld, out_at, out_total, a.status);
+        zero_columns(out, r.vocab, a.out.ld, out_at, out_total, a.status,
+                     static_cast<int>(threadIdx.x), static_cast<int>(blockDim.x));
+    block_amax(m2, a.out.amax, a.status);
+}
+
+// Loss and gradient together, for many long rows.  A row of the logits is
+// needed twice, for its sums and for its gradient, and the blocks of all SMs
+// together hold more than L2 does, so a block keeps what it can: one persistent
+// block per SM takes whole rows through a ring of 16 KB pieces in shared
+// memory that bulk copies fill.
+//   warp 16      reads the next row's slots (two buffers) and sums them up;
+//   warp 17      issues the copies: a row's pieces 0 .. n-1, then again those
+//                that the ring could not keep, then the next row's;
+//   warps 0..15  first pass: running sums over the pieces, releasing all but
+//                the last `keep`; the block's join (one barrier); second pass:
+//                the gradient of the kept pieces, then of those copied again
+//                (from L2, which they have just passed), released one by one.
+// The pieces are released in the order of their copies, so the ring is a queue
+// and the next row's copies run during the second pass.
+constexpr int kRingWarps = 16;
+constexpr int kRingConsumers = kRingWarps * 32;
+constexpr int kRingThreads = kRingConsumers + 64;
+constexpr int kPieceChunks = 1024;
+constexpr int kPieceBytes = kPieceChunks * 16;
+constexpr int kPieces = 12;
+constexpr int kKeep = 9;  // the other three are under way
+constexpr int kPerThread = kPieceChunks / kRingConsumers;
+constexpr uint64_t kDrainLimitNs = 1000000000ull;
+
+struct RingSlots : SlotTable {
+    int any;        // the row has a slot
+    int used;       // some slot has q > 0
+    int masked;     // such a slot names a masked token
+    float dloss;
+    float total;    // sum q (1 without the tail class)
+    float qall;     // sum q as it came out
+    float left;     // q_r
+    float plogp;    // sum q log q
+    float zref;     // the largest logit of a slot with q > 0
+    float zmean;    // sum q (z - zref)
+    float zmax;     // the largest logit of the slots' ids
+    float inside;   // sum over these ids of 2^((z - zmax) c)
+};
+
+constexpr size_t kRingSmem = static_cast<size_t>(kPieces) * kPieceBytes + 2 * sizeof(RingSlots);
+
+template <typename V, typename F>
+__device__ __forceinline__ V warp_all(V v, F f)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        const V u = __shfl_xor_sync(0xFFFFFFFFu, v, o);
+        // lower lane first on both sides, so that all lanes get equal bits
+        v = (threadIdx.x & o) ? f(u, v) : f(v, u);
+    }
+    return v;
+}
+__device__ __forceinline__ float warp_sum(float v)
+{
+    return warp_all(v, [](float a, float b) { return a + b; });
+}
+__device__ __forceinline__ float warp_max(float v)
+{
+    return warp_all(v, [](float a, float b) { return fmaxf(a, b); });
+}
+
+// One row's slots, by one warp: slot lane + 32 i in register i.
+template <typename T, bool TAIL>
+__device__ __forceinline__ void ring_slots(const DistillArgs &a, int64_t row, RingSlots &s)
+{
+    constexpr int N = F8_MAX_TOP / 32;
+    const int lane = threadIdx.x & 31, k = a.k;
+    const Row<T> r(static_cast<const T *>(a.logits), row, a.ld, a.vocab);
+    for (int i = lane; i < kHeads / 4; i += 32)
+        reinterpret_cast<int4 *>(s.head)[i] = make_int4(-1, -1, -1, -1);
+    int id[N];
+    float t[N], z[N];
+    bool any = false, outside = false;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const int j = lane + 32 * i;
+        id[i] = -1;
+        t[i] = F8_NEG_INF;
+        z[i] = F8_NEG_INF;
+        if (j < k) {
+            id[i] = a.ids[row * k + j];
+            t[i] = a.values[row * k + j];
+        }
+        outside |= id[i] >= r.vocab;
+        if (id[i] >= r.vocab || t[i] == F8_NEG_INF)
+            id[i] = -1;
+        if (id[i] < 0)
+            t[i] = F8_NEG_INF;
+        any |= id[i] >= 0;
+    }
+    if (outside)
+        atomicOr(a.status, kStatusIndex);
+    any = __any_sync(0xFFFFFFFFu, any);
+    if (any) {
+        float zm = F8_NEG_INF, tm = F8_NEG_INF;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            if (id[i] >= 0)
+                z[i] = as_float(r.base[r.off + id[i]]);
+            tm = fmaxf(tm, t[i]);
+        }
+        float q[N], logq[N], sum = 0.0f;
+        if (!TAIL)
+            tm = warp_max(tm);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            logq[i] = TAIL ? t[i] : (t[i] - tm) * a.inv_t;
+            q[i] = id[i] >= 0 ? expf(logq[i]) : 0.0f;
+            sum += q[i];
+        }
+        sum = warp_sum(sum);
+        if (!TAIL) {
+            const float ls = logf(sum), inv = 1.0f / sum;
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                q[i] *= inv;
+                logq[i] -= ls;
+            }
+        }
+        // the table, and each id's summed q
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int j = lane + 32 * i;
+            if (j < k) {
+                s.id[j] = id[i];
+                s.q[j] = q[i];
+            }
+        }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (id[i] >= 0)
+                s.next[lane + 32 * i] =
+                    atomicExch(&s.head[((id[i] + r.off) / Chunk<T>::E) % kHeads], lane + 32 * i);
+        __syncwarp();
+        bool first[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int j = lane + 32 * i;
+            first[i] = id[i] >= 0;
+            int same = 0;
+            if (id[i] >= 0) {
+                for (int p = s.head[((id[i] + r.off) / Chunk<T>::E) % kHeads]; p >= 0; p = s.next[p]) {
+                    if (s.id[p] == id[i]) {
+                        ++same;
+                        first[i] = first[i] && p >= j;
+                    }
+                }
+                float qs = q[i];
+                if (same > 1) {  // in slot order
+                    qs = 0.0f;
+                    for (int p = 0; p < k; ++p)
+                        qs += s.id[p] == id[i] ? s.q[p] : 0.0f;
+                }
+                s.qsum[j] = qs;
+            }
+        }
+        float zref = F8_NEG_INF, plogp = 0.0f;
+        bool used = false, masked = false;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const bool u = q[i] > 0.0f || q[i] != q[i];
+            used |= u;
+            masked |= u && z[i] == F8_NEG_INF;
+            if (u) {
+                plogp = fmaf(q[i], logq[i], plogp);
+                zref = fmaxf(zref, z[i]);
+            }
+            zm = fmaxf(zm, z[i]);
+        }
+        zref = warp_max(zref);
+        plogp = warp_sum(plogp);
+        used = __any_sync(0xFFFFFFFFu, used);
+        masked = __any_sync(0xFFFFFFFFu, masked);
+        zm = warp_max(zm);
+        float zmean = 0.0f, inside = 0.0f, total = 0.0f;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            total += q[i];
+            if (q[i] > 0.0f && z[i] != F8_NEG_INF)
+                zmean = fmaf(q[i], z[i] - zref, zmean);
+            if (TAIL && first[i] && zm != F8_NEG_INF)
+                inside += ex2((z[i] - zm) * a.c);
+        }
+        zmean = warp_sum(zmean);
+        total = TAIL ? sum : warp_sum(total);
+        if (TAIL)
+            inside = warp_sum(inside);
+        if (lane == 0) {
+            s.used = used;
+            s.masked = masked;
+            s.total = TAIL ? total : 1.0f;
+            s.qall = total;
+            s.left = TAIL ? fmaxf(1.0f - total, 0.0f) : 0.0f;
+            s.plogp = plogp;
+            s.zref = zref;
+            s.zmean = zmean;
+            s.zmax = zm;
+            s.inside = inside;
+        }
+    }
+    if (lane == 0) {
+        s.any = any;
+        s.dloss = a.dloss[row];
+    }
+    __syncwarp();
+}
+
+// Piece of position `seq` in the queue: its slot, and the parity of its phase.
+__device__ __forceinline__ int ring_slot(uint32_t seq) { return static_cast<int>(seq % kPieces); }
+__device__ __forceinline__ uint32_t ring_parity(uint32_t seq) { return (seq / kPieces) & 1u; }
+
+template <typename T, bool TAIL>
+__global__ void __launch_bounds__(kRingThreads, 1)
+distill_ring_kernel(const __grid_constant__ DistillArgs a, uint64_t limit_ns)
+{
+    constexpr int E = Chunk<T>::E;
+    extern __shared__ __align__(128) uint8_t pieces[];
+    __shared__ __align__(8) uint64_t full[kPieces];
+    __shared__ __align__(8) uint64_t empty[kPieces];
+    __shared__ __align__(8) uint64_t sfull[2];
+    __shared__ __align__(8) uint64_t sempty[2];
+    __shared__ Stats parts[2][kRingWarps];
+    __shared__ int abort_word;
+    volatile int *abort_flag = &abort_word;
+    RingSlots *slots = reinterpret_cast<RingSlots *>(pieces + static_cast<size_t>(kPieces) * kPieceBytes);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid == 0) {
+        for (int i = 0; i < kPieces; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], kRingWarps);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sfull[i], 1);
+            mbar_init(&sempty[i], kRingWarps + 1);
+        }
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    griddep_wait();
+    griddep_launch_dependents();
+    __syncthreads();
+    const int64_t total = (a.rows - 1) * a.ld + a.vocab;
+    auto wait = [&](uint64_t *bar, uint32_t parity) {
+        if (mbar_wait(bar, parity, abort_flag, limit_ns))
+            return true;
+        *abort_flag = 1;
+        atomicOr(a.status, kStatusTimeout);
+        return false;
+    };
+    uint32_t m2 = 0;
+
+    if (warp == kRingWarps) {
+        // ---------------------------------------------------- the rows' slots
+        int i = 0;
+        for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, ++i) {
+            const int b = i & 1;
+            const bool ok = wait(&sempty[b], ((i >> 1) & 1) ^ 1u);
+            if (!__all_sync(0xFFFFFFFFu, ok))
+                break;
+            ring_slots<T, TAIL>(a, row, slots[b]);
+            if (lane == 0)
+                mbar_arrive(&sfull[b]);
+        }
+    } else if (warp == kRingWarps + 1) {
+        // ---------------------------------------------------- copies
+        if (lane == 0) {
+            uint32_t seq = 0;
+            int i = 0;
+            bool stop = false;
+            for (int64_t row = blockIdx.x; row < a.rows && !stop; row += gridDim.x, ++i) {
+                const int b = i & 1;
+                if (!wait(&sfull[b], (i >> 1) & 1)) {
+                    stop = true;
+                    break;
+                }
+                const bool any = slots[b].any != 0;
+                mbar_arrive(&sempty[b]);
+                if (!any)
+                    continue;
+                const Row<T> r(static_cast<const T *>(a.logits), row, a.ld, a.vocab);
+                const int n = r.w1 - r.w0;
+                const int np = (n + kPieceChunks - 1) / kPieceChunks;
+                const int again = np - min(np, kKeep);
+                for (int j = 0; j < np + again; ++j, ++seq) {
+                    const int piece = j < np ? j : j - np;
+                    const int slot = ring_slot(seq);
+                    if (!wait(&empty[slot], ring_parity(seq) ^ 1u)) {
+                        stop = true;
+                        break;
+                    }
+                    const int c0 = piece * kPieceChunks;
+                    const uint32_t bytes = 16u * static_cast<uint32_t>(min(kPieceChunks, n - c0));
+                    mbar_arrive_expect_tx(&full[slot], bytes);
+                    bulk_load(pieces + slot * kPieceBytes,
+                              r.base + static_cast<int64_t>(r.w0 + c0) * E, bytes, &full[slot]);
+                }
+            }
+            if (*abort_flag) {  // copies still under way land before the block leaves
+                const uint32_t first = seq > kPieces ? seq - kPieces : 0;
+                for (uint32_t p = first; p < seq; ++p)
+                    mbar_wait(&full[ring_slot(p)], ring_parity(p), nullptr, kDrainLimitNs);
+            }
+        }
+        __syncwarp();
+    } else {
+        // ---------------------------------------------------- sums and gradient
+        uint32_t seq = 0;
+        int i = 0;
+        bool alive = true;
+        for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, ++i) {
+            const int b = i & 1;
+            alive = alive && __all_sync(0xFFFFFFFFu, wait(&sfull[b], (i >> 1) & 1));
+            const RingSlots &s = slots[b];
+            const bool any = alive && s.any != 0;
+            const Row<T> r(static_cast<const T *>(a.logits), row, a.ld, a.vocab);
+            const int n = r.w1 - r.w0;
+            const int np = any ? (n + kPieceChunks - 1) / kPieceChunks : 0;
+            const int keep = min(np, kKeep), again = np - keep;
+            auto arrived = [&](uint32_t q) {
+                alive = alive && __all_sync(0xFFFFFFFFu, wait(&full[ring_slot(q)], ring_parity(q)));
+            };
+            auto release = [&](uint32_t q) {
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&empty[ring_slot(q)]);
+            };
+            // this thread's chunk u of a piece
+            auto chunk = [&](uint32_t q, int piece, int u) {
+                const int c = u * kRingConsumers + tid;
+                uint4 v = neg_inf_chunk(T());
+                if (piece * kPieceChunks + c < n)
+                    v = reinterpret_cast<const uint4 *>(pieces + ring_slot(q) * kPieceBytes)[c];
+                return v;
+            };
+            Stats t = stats_empty();
+            for (int j = 0; j < np; ++j) {
+                arrived(seq + j);
+                uint4 v[kPerThread];
+#pragma unroll
+                for (int u = 0; u < kPerThread; ++u)
+                    v[u] = chunk(seq + j, j, u);
+                if (j < again)
+                    release(seq + j);
+                if (TAIL) {
+#pragma unroll
+                    for (int u = 0; u < kPerThread; ++u)
+                        v[u] = without_slots(
+                            s, r, r.w0 + j * kPieceChunks + u * kRingConsumers + tid, v[u]);
+                }
+                add_chunks<T, false>(t, v, a.c, 0.0f);
+            }
+            const int ec = any ? r.edge(edge_of_thread(), 0, r.nch) : -1;
+            float edge[E];
+            if (ec >= 0) {
+                load_edge(r, ec, edge, total, a.status);
+                float x[E];
+#pragma unroll
+                for (int e = 0; e < E; ++e)
+                    x[e] = edge[e];
+                if (TAIL)
+                    drop_slots(s, r, ec, x);
+                add_values<false>(t, x, a.c);
+            }
+            // the block's sums: warps' in shared memory, two sets in turn
+            const float c = a.c;
+            t = warp_stats(t, c);
+            if (lane == 0)
+                parts[b][warp] = t;
+            asm volatile("bar.sync 1, %0;" ::"n"(kRingConsumers) : "memory");
+            t = parts[b][lane & (kRingWarps - 1)];
+            t = warp_stats_16(t, c);
+
+            T *out = static_cast<T *>(a.out.p) + row * a.out.ld;
+            const int64_t out_at = row * a.out.ld, out_total = a.rows * a.out.ld;
+            const bool same = same_offset(r, out);
+            if (any) {
+                float m = t.m, outside = t.s, sum = t.s, rest = 0.0f;
+                if (TAIL) {
+                    m = fmaxf(t.m, s.zmax);
+                    outside = t.s * ex2(fmaxf((t.m - m) * c, kFloor2));
+                    sum = outside + s.inside * ex2(fmaxf((s.zmax - m) * c, kFloor2));
+                }
+                const bool bad = sum != sum || m == F8_POS_INF;
+                const bool none = !bad && sum == 0.0f;
+                const float inv_s = none ? 0.0f : (bad ? F8_NAN : 1.0f / sum);
+                if (TAIL)
+                    rest = outside * inv_s;
+                if (tid == 0) {
+                    float loss = 0.0f;
+                    if (s.used) {
+                        loss = s.masked || none
+                                   ? F8_POS_INF
+                                   : s.plogp - s.zmean * a.inv_t +
+                                         s.qall * fmaf(m - s.zref, a.inv_t, logf(sum));
+                    }
+                    if (TAIL && rest > 0.0f && s.left > 0.0f)
+                        loss += s.left * (logf(s.left) - logf(rest));
+                    if (bad || s.plogp != s.plogp || s.zmean != s.zmean)
+                        loss = F8_NAN;
+                    a.loss[row] = loss;
+                    if (loss != loss)
+                        atomicOr(a.status, kStatusNonfinite);
+                }
+                float mass = s.total, dense = s.total;
+                if (TAIL && rest > 0.0f) {
+                    mass = s.total + s.left;
+                    dense = mass - s.left / rest;
+                }
+                const bool zero = s.dloss == 0.0f || none;
+                const float scale = zero ? 0.0f : s.dloss * a.inv_t;
+                const float mm = m == F8_NEG_INF ? 0.0f : m;
+                const float2 nm = make_float2(-mm, -mm), c2 = make_float2(c, c);
+                const float fac = zero ? 0.0f : scale * dense * inv_s;
+                const float2 f2 = make_float2(fac, fac);
+                // the gradient of chunk ch in place of its logits
+                auto gradient = [&](int ch, float (&f)[E]) {
+                    if (zero) {
+#pragma unroll
+                        for (int e = 0; e < E; ++e)
+                            f[e] = 0.0f;
+                        return;
+                    }
+                    float p[E];
+#pragma unroll
+                    for (int e = 0; e < E; e += 2) {
+                        const float2 d =
+                            __fmul2_rn(__fadd2_rn(make_float2(f[e], f[e + 1]), nm), c2);
+                        const float2 x = make_float2(ex2(d.x), ex2(d.y));
+                        p[e] = x.x;
+                        p[e + 1] = x.y;
+                        const float2 g = __fmul2_rn(x, f2);
+                        f[e] = g.x;
+                        f[e + 1] = g.y;
+                    }
+                    if (s.head[ch % kHeads] >= 0) {
+#pragma unroll
+                        for (int e = 0; e < E; ++e)
+                            p[e] *= inv_s;
+                        slot_gradient(s, r, ch, p, scale, mass, f);
+                    }
+                };
+                // the kept pieces, then the first ones again
+                for (int j = 0; j < np; ++j) {
+                    const int piece = j < keep ? again + j : j - keep;
+                    const uint32_t q = seq + again + j;
+                    if (j >= keep)
+                        arrived(q);
+                    uint4 v[kPerThread];
+#pragma unroll
+                    for (int u = 0; u < kPerThread; ++u)
+                        v[u] = chunk(q, piece, u);
+                    release(q);
+#pragma unroll
+                    for (int u = 0; u < kPerThread; ++u) {
+                        const int k = piece * kPieceChunks + u * kRingConsumers + tid;
+                        if (k < n) {
+                            float f[E];
+                            unpack<T>(v[u], f);
+                            gradient(r.w0 + k, f);
+                            m2 = __vmaxu2(m2, store_chunk(r, out, same, r.w0 + k, f, out_at,
+                                                          out_total, a.status));
+                        }
+                    }
+                }
+                if (ec >= 0) {
+                    gradient(ec, edge);
+                    m2 = __vmaxu2(m2, store_elements(r, out, ec, edge, out_at, out_total, a.status));
+                }
+                seq += np + again;
+            } else if (alive) {
+                if (tid == 0)
+                    a.loss[row] = 0.0f;
+                zero_columns(out, 0, r.vocab, out_at, out_total, a.status, tid, kRingConsumers);
+            }
+            if (alive)
+                zero_columns(out, r.vocab, a.out.ld, out_at, out_total, a.status, tid, kRingConsumers);
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&sempty[b]);
+        }
+    }
     block_amax(m2, a.out.amax, a.status);
 }
 
@@ -1558,17 +2087,27 @@ cudaError_t distill_bwd(DistillArgs a, const DeviceInfo &, cudaStream_t st)
 template <typename T, bool TAIL>
 cudaError_t distill_fused(DistillArgs a, const DeviceInfo &dev, cudaStream_t st)
 {
-    // as few blocks as hold the row in registers, more where rows are few
     const int64_t chunks = (static_cast<int64_t>(a.vocab) + 2 * Chunk<T>::E - 2) / Chunk<T>::E;
-    int c = 1;
-    while (c < kMaxCluster && (chunks + c - 1) / c > kNV * kThreads)
-        c *= 2;
-    a.cluster = std::max(c, cluster_for(a.rows, chunks, dev));
-    const dim3 grid(static_cast<unsigned>(a.rows * a.cluster));
-    if ((chunks + a.cluster - 1) / a.cluster > kNV * kThreads)
-        return launch_pdl_cluster(distill_fused_kernel<T, TAIL, 2 * kWarps>, grid,
-                                  dim3(2 * kThreads), 0, st, static_cast<unsigned>(a.cluster), a);
-    return launch_pdl_cluster(distill_fused_kernel<T, TAIL, kWarps>, grid, dim3(kThreads), 0, st,
+    // the ring where a row does not fit one block's registers and there is at
+    // least a row for every second SM
+    if (chunks > kNV * kThreads && 2 * a.rows >= dev.sm_count) {
+        static std::once_flag once[64];
+        static cudaError_t err[64];
+        const int d = dev.ordinal & 63;
+        std::call_once(once[d], [&] {
+            err[d] = cudaFuncSetAttribute(distill_ring_kernel<T, TAIL>,
+                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                          static_cast<int>(kRingSmem));
+        });
+        if (err[d] != cudaSuccess)
+            return err[d];
+        return launch_pdl(distill_ring_kernel<T, TAIL>,
+                          dim3(static_cast<unsigned>(std::min<int64_t>(a.rows, dev.sm_count))),
+                          dim3(kRingThreads), kRingSmem, st, a, wait_limit_ns());
+    }
+    a.cluster = cluster_for(a.rows, chunks, dev);
+    return launch_pdl_cluster(distill_fused_kernel<T, TAIL>,
+                              dim3(static_cast<unsigned>(a.rows * a.cluster)), dim3(kThreads), 0, st,
                               static_cast<unsigned>(a.cluster), a);
 }
 

@@ -98,6 +98,21 @@ def test_rows_longer_than_the_registers(f8, dtype, vocab, tail):
     assert f8.f8_last_device_status() == 0
 
 
+@pytest.mark.parametrize("tail", [False, True], ids=["top", "tail"])
+@pytest.mark.parametrize("dtype,vocab,pad", [(torch.bfloat16, 140003, 13), (torch.bfloat16, 20480, 0),
+                                             (torch.float32, 65001, 3)])
+def test_many_long_rows(f8, dtype, vocab, pad, tail):
+    """Several rows per SM, some of them ignored, longer than what one block
+    keeps of a row."""
+    full, logits, ids, values, dloss = _case(400, vocab, 40, dtype, tail, 22, pad)
+    ids[5::17] = -1
+    full[5::17] = float("nan")
+    dloss[3::50] = 0.0
+    clean = torch.where(torch.isnan(logits), torch.zeros_like(logits), logits)
+    _check(f8, full, vocab, ids, values, dloss, 0.9, tail, f"many {dtype} {vocab}", clean)
+    assert f8.f8_last_device_status() == 0
+
+
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
 @pytest.mark.parametrize("tail", [False, True], ids=["top", "tail"])
 @pytest.mark.parametrize("vocab", [300, 4001, 70000])
