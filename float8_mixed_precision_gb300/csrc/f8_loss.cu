@@ -147,6 +147,34 @@ __device__ __forceinline__ void load_edge(const Row<T> &r, int c, float (&f)[Chu
     }
 }
 
+// Walks whole chunks [c0, c1) of a row by N threads, U at a time: body(v, c)
+// gets the thread's chunks c + u * N, -inf where that is c1 or past it.
+template <typename T, int N, int U, typename F>
+__device__ __forceinline__ void walk_chunks(const Row<T> &r, int c0, int c1, int64_t total,
+                                            unsigned *status, F body)
+{
+    constexpr int E = Chunk<T>::E;
+    const uint4 *p = reinterpret_cast<const uint4 *>(r.base);
+    int c = c0 + static_cast<int>(threadIdx.x) % N;
+    for (; c + (U - 1) * N < c1; c += U * N) {
+        uint4 v[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            v[u] = neg_inf_chunk(T());
+            if (in_range(r.at - r.off + static_cast<int64_t>(c + u * N) * E, E, total, status))
+                v[u] = p[c + u * N];
+        }
+        body(v, c);
+    }
+    if (c < c1) {
+        uint4 v[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            v[u] = load_chunk(r, c + u * N, c1, total, status);
+        body(v, c);
+    }
+}
+
 template <typename T>
 __device__ __forceinline__ void unpack(uint4 v, float (&f)[Chunk<T>::E]);
 template <>
@@ -184,6 +212,43 @@ __device__ __forceinline__ uint4 pack<float>(const float (&f)[4])
 {
     return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
                       __float_as_uint(f[3]));
+}
+
+// A chunk's elements in pairs, for arithmetic on two at a time.
+template <typename T>
+__device__ __forceinline__ void unpack2(uint4 v, float2 (&f)[Chunk<T>::E / 2]);
+template <>
+__device__ __forceinline__ void unpack2<__nv_bfloat16>(uint4 v, float2 (&f)[4])
+{
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        f[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+}
+template <>
+__device__ __forceinline__ void unpack2<float>(uint4 v, float2 (&f)[2])
+{
+    f[0] = make_float2(__uint_as_float(v.x), __uint_as_float(v.y));
+    f[1] = make_float2(__uint_as_float(v.z), __uint_as_float(v.w));
+}
+template <typename T>
+__device__ __forceinline__ uint4 pack2(const float2 (&f)[Chunk<T>::E / 2]);
+template <>
+__device__ __forceinline__ uint4 pack2<__nv_bfloat16>(const float2 (&f)[4])
+{
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        __nv_bfloat162 h = __float22bfloat162_rn(f[i]);
+        w[i] = *reinterpret_cast<uint32_t *>(&h);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+template <>
+__device__ __forceinline__ uint4 pack2<float>(const float2 (&f)[2])
+{
+    return make_uint4(__float_as_uint(f[0].x), __float_as_uint(f[0].y), __float_as_uint(f[1].x),
+                      __float_as_uint(f[1].y));
 }
 
 template <int E>
@@ -343,15 +408,15 @@ __device__ __forceinline__ void add_chunks(Stats &t, const uint4 (&v)[U], float 
     float2 h[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        float f[E];
-        unpack<T>(ENT ? chunk_floor<T>(v[u], low) : v[u], f);
+        float2 f[E / 2];
+        unpack2<T>(ENT ? chunk_floor<T>(v[u], low) : v[u], f);
 #pragma unroll
-        for (int e = 0; e < E; e += 2) {
-            const float2 d = __ffma2_rn(make_float2(f[e], f[e + 1]), c2, n2);
+        for (int e = 0; e < E / 2; ++e) {
+            const float2 d = __ffma2_rn(f[e], c2, n2);
             const float2 x = make_float2(ex2(d.x), ex2(d.y));
-            s[(e >> 1) & 1] = __fadd2_rn(s[(e >> 1) & 1], x);
+            s[e & 1] = __fadd2_rn(s[e & 1], x);
             if (ENT)
-                h[(e >> 1) & 1] = __ffma2_rn(x, d, h[(e >> 1) & 1]);
+                h[e & 1] = __ffma2_rn(x, d, h[e & 1]);
         }
     }
     const float bs = (s[0].x + s[0].y) + (s[1].x + s[1].y);
@@ -364,7 +429,7 @@ __device__ __forceinline__ void add_chunks(Stats &t, const uint4 (&v)[U], float 
 }
 
 // The block's sums, in every thread.  `red`: one Stats per warp.
-template <bool ENT, int WARPS>
+template <bool ENT>
 __device__ __forceinline__ Stats block_join(Stats t, float c, Stats *red)
 {
 #pragma unroll
@@ -382,9 +447,17 @@ __device__ __forceinline__ Stats block_join(Stats t, float c, Stats *red)
     __syncthreads();
     t = red[0];
 #pragma unroll 1
-    for (int w = 1; w < WARPS; ++w)
+    for (int w = 1; w < kWarps; ++w)
         t = join<ENT>(t, red[w], c);
     return t;
+}
+
+// The largest value of a warp's lanes (a NaN only if all are).
+__device__ __forceinline__ float warp_max_of(float v)
+{
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
 }
 
 // The joined sums of the lanes of a warp, in every lane; without the entropy.
@@ -414,41 +487,6 @@ __device__ __forceinline__ Stats warp_stats_16(Stats t, float c)
     return t;
 }
 
-// Sum, or maximum, of one value per thread, in every thread, in a fixed order.
-template <int WARPS>
-__device__ __forceinline__ float block_sum(float v, float *red)
-{
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-        v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0)
-        red[threadIdx.x >> 5] = v;
-    __syncthreads();
-    v = 0.0f;
-#pragma unroll
-    for (int w = 0; w < WARPS; ++w)
-        v += red[w];
-    return v;
-}
-
-template <int WARPS>
-__device__ __forceinline__ float block_max(float v, float *red)
-{
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-        v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0)
-        red[threadIdx.x >> 5] = v;
-    __syncthreads();
-    v = red[0];
-#pragma unroll
-    for (int w = 1; w < WARPS; ++w)
-        v = fmaxf(v, red[w]);
-    return v;
-}
-
 // ------------------------------------------------------------ clusters
 // A block of a cluster may write another's shared memory once that block has
 // started (cluster_started, an arrive at the kernel's start and a wait before
@@ -475,12 +513,13 @@ __device__ __forceinline__ P *peer(P *p, unsigned rank)
 }
 
 // ------------------------------------------------------------ top k
-// fp32 values as unsigned keys of the same order, never 0; -0 counts as +0.
+// fp32 values as unsigned keys of the same order, never 0; -0 counts as +0,
+// any NaN as the largest.
 __device__ __forceinline__ uint32_t order_key(float x)
 {
     const uint32_t b = __float_as_uint(x + 0.0f);
     const uint32_t k = b ^ ((b >> 31) ? 0xFFFFFFFFu : 0x80000000u);
-    return k ? k : 1u;
+    return x != x ? 0xFFFFFFFFu : k;
 }
 __device__ __forceinline__ float key_value(uint32_t k)
 {
@@ -507,8 +546,8 @@ __device__ __forceinline__ int count_from(const uint32_t *keys, int n, uint32_t 
 }
 
 // The positions of the k largest of n keys in shared memory (equal keys: the
-// lower positions), ascending, in out[0 .. min(k, n)).  The threshold is found
-// by bisection over the key range; n < 2^16.
+// lower positions), ascending, in out[0 .. min(k, n)), by bisection over the
+// key range; n < 2^16.
 __device__ __forceinline__ void block_select(const uint32_t *keys, int n, int k, int *out, int *red)
 {
     const int tid = threadIdx.x, lane = tid & 31;
@@ -592,10 +631,89 @@ __device__ __forceinline__ void block_select(const uint32_t *keys, int n, int k,
     __syncthreads();
 }
 
+// The k-th largest of n > k keys in shared memory, by seven pivots a round: the
+// largest t with at least k keys >= t, or a lower one with exactly k.  `cnt`:
+// three sets of eight counters, zero at the start and at the end.
+__device__ __forceinline__ uint32_t block_threshold(const uint32_t *keys, int n, int k, int *red,
+                                                    int *cnt)
+{
+    const int tid = threadIdx.x, lane = tid & 31;
+    uint32_t lo = 0xFFFFFFFFu, hi = 0;
+    for (int i = tid; i < n; i += kThreads) {
+        lo = min(lo, keys[i]);
+        hi = max(hi, keys[i]);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        lo = min(lo, __shfl_xor_sync(0xFFFFFFFFu, lo, o));
+        hi = max(hi, __shfl_xor_sync(0xFFFFFFFFu, hi, o));
+    }
+    __syncthreads();
+    if (lane == 0) {
+        red[tid >> 5] = static_cast<int>(lo);
+        red[kWarps + (tid >> 5)] = static_cast<int>(hi);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        lo = min(lo, static_cast<uint32_t>(red[w]));
+        hi = max(hi, static_cast<uint32_t>(red[kWarps + w]));
+    }
+    // at least k keys are >= lo, fewer than k are > hi
+    int set = 0;
+    while (lo < hi) {
+        const uint32_t step = (hi - lo) / 8 + 1;
+        uint32_t pivot[7];
+#pragma unroll
+        for (int p = 0; p < 7; ++p)  // past hi: nothing to count
+            pivot[p] = (hi - lo) / step >= p + 1u ? lo + (p + 1) * step : 0xFFFFFFFFu;
+        int c[7] = {0, 0, 0, 0, 0, 0, 0};
+        for (int i0 = 0; i0 < n; i0 += kThreads) {
+            const uint32_t key = i0 + tid < n ? keys[i0 + tid] : 0u;
+#pragma unroll
+            for (int p = 0; p < 7; ++p)
+                c[p] += __popc(__ballot_sync(0xFFFFFFFFu, key >= pivot[p]));
+        }
+        int mine = 0;
+#pragma unroll
+        for (int p = 0; p < 7; ++p)
+            mine = lane == p ? c[p] : mine;
+        if (lane < 7 && mine > 0)
+            atomicAdd(&cnt[8 * set + lane], mine);
+        const int next = set == 2 ? 0 : set + 1;
+        if (tid < 8)
+            cnt[8 * next + tid] = 0;
+        __syncthreads();
+        uint32_t nlo = lo, nhi = min(hi, pivot[0] - 1);
+        int at = 0;
+#pragma unroll
+        for (int p = 0; p < 7; ++p) {
+            const bool in = (hi - lo) / step >= p + 1u;
+            const int have = cnt[8 * set + p];
+            if (in && have >= k) {
+                nlo = pivot[p];
+                nhi = p == 6 || (hi - lo) / step < p + 2u ? hi : pivot[p < 6 ? p + 1 : 6] - 1;
+                at = have;
+            }
+        }
+        lo = nlo;
+        hi = nhi;
+        set = next;
+        if (at == k)
+            break;
+    }
+    __syncthreads();
+    if (tid < 24)
+        cnt[tid] = 0;
+    __syncthreads();
+    return lo;
+}
+
 // Shared memory of the top-k stage, in 4-byte words; every part starts on a
 // 16-byte boundary.
+constexpr int kCandidates = 2048;
 struct TopLayout {
-    int groups, list, keys, pick, merge_key, merge_id, words;
+    int groups, list, keys, pick, cand_key, cand_id, best_key, best_id, merge_key, merge_id, words;
 };
 __host__ __device__ inline int words4(int n) { return (n + 3) & ~3; }
 __host__ __device__ inline TopLayout top_layout(int ngroups, int k, int cluster)
@@ -605,10 +723,128 @@ __host__ __device__ inline TopLayout top_layout(int ngroups, int k, int cluster)
     l.list = l.groups + words4(ngroups);  // k positions
     l.keys = l.list + words4(k);          // 32 k chunk keys, then E k element keys
     l.pick = l.keys + 32 * k;             // k chunks
-    l.merge_key = l.pick + words4(k);
-    l.merge_id = l.merge_key + words4(cluster * k);
-    l.words = l.merge_id + words4(cluster * k);
+    l.cand_key = l.pick + words4(k);
+    l.cand_id = l.cand_key + kCandidates;
+    l.best_key = l.cand_id + kCandidates;  // the block's k best, in order
+    l.best_id = l.best_key + words4(k);
+    l.merge_key = l.best_id + words4(k);
+    l.merge_id = l.merge_key + (cluster > 1 ? words4(cluster * k) : 0);
+    l.words = l.merge_id + (cluster > 1 ? words4(cluster * k) : 0);
     return l;
+}
+
+// The k largest elements of chunks [32 g0, 32 g1) of a row, in order, in
+// best_key / best_id of `lay`; gkeys holds the groups' largest keys.  Every
+// element among the k largest is >= the k-th largest maximum of any k or more
+// disjoint parts of the row.  So: the threshold over the groups' maxima (over
+// the chunks' where there are too few groups), a look at the parts that reach
+// it, and their elements >= it ranked against one another.  Where many values
+// are equal to the threshold or one part holds very many large ones, the
+// candidates may not fit; then parts are chosen exactly (k parts hold all, by
+// maximum and position), groups, chunks, elements in turn.
+template <typename T>
+__device__ __forceinline__ void block_top(const Row<T> &r, int g0, int g1, int k, int have,
+                                          uint32_t *dyn, const TopLayout &lay, int *red, int *cnt,
+                                          int *ncand, int64_t total, unsigned *status)
+{
+    constexpr int E = Chunk<T>::E;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    uint32_t *gkeys = dyn + lay.groups, *keys = dyn + lay.keys;
+    uint32_t *ck = dyn + lay.cand_key, *bk = dyn + lay.best_key;
+    int *ci = reinterpret_cast<int *>(dyn + lay.cand_id);
+    int *bi = reinterpret_cast<int *>(dyn + lay.best_id);
+    int *list = reinterpret_cast<int *>(dyn + lay.list);
+    const int ng = g1 - g0;
+    auto load = [&](int ch, float (&x)[E]) {
+        if (r.whole(ch))
+            unpack<T>(load_chunk(r, ch, r.nch, total, status), x);
+        else
+            load_edge(r, ch, x, total, status);
+    };
+    auto offer = [&](int ch, uint32_t t) {
+        float x[E];
+        load(ch, x);
+        if (order_key(max_of(x)) < t && t > 1)
+            return;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const int v = ch * E + e - r.off;
+            const uint32_t key = order_key(x[e]);
+            if (v >= 0 && v < r.vocab && key >= t) {
+                const int at = atomicAdd(ncand, 1);
+                if (at < kCandidates) {
+                    ck[at] = key;
+                    ci[at] = v;
+                }
+            }
+        }
+    };
+    auto chunk_keys = [&](const int *groups, int n) {  // of n groups (all from g0 if groups is null)
+        for (int i = tid; i < n * 32; i += kThreads) {
+            const int ch = (g0 + (groups != nullptr ? groups[i >> 5] : i >> 5)) * 32 + (i & 31);
+            uint32_t key = 0;
+            if (ch < r.nch) {
+                float x[E];
+                load(ch, x);
+                key = order_key(max_of(x));
+            }
+            keys[i] = key;
+        }
+        __syncthreads();
+    };
+    if (ng > k) {
+        const uint32_t t = block_threshold(gkeys, ng, k, red, cnt);
+        for (int g = warp; g < ng; g += kWarps) {
+            const int ch = (g0 + g) * 32 + lane;
+            if (gkeys[g] >= t && ch < r.nch)
+                offer(ch, t);
+        }
+    } else {
+        chunk_keys(nullptr, ng);
+        const int nch = min(32 * ng, r.nch - 32 * g0);
+        const uint32_t t = nch > k ? block_threshold(keys, nch, k, red, cnt) : 1u;
+        for (int i = tid; i < nch; i += kThreads)
+            if (keys[i] >= t)
+                offer(g0 * 32 + i, t);
+    }
+    __syncthreads();
+    int n = *ncand;
+    if (n > kCandidates) {
+        block_select(gkeys, ng, k, list, red);
+        const int kg = min(k, ng);
+        chunk_keys(list, kg);
+        int *pick = reinterpret_cast<int *>(dyn + lay.pick);
+        block_select(keys, kg * 32, k, pick, red);
+        const int kc = min(k, kg * 32);
+        for (int i = tid; i < kc; i += kThreads)
+            pick[i] = (g0 + list[pick[i] >> 5]) * 32 + (pick[i] & 31);
+        __syncthreads();
+        for (int i = tid; i < kc * E; i += kThreads) {
+            const int v = pick[i / E] * E + i % E - r.off;
+            const bool in = v >= 0 && v < r.vocab;
+            ck[i] = in ? order_key(as_float(r.base[r.off + v])) : 0u;
+            ci[i] = in ? v : 0x7FFFFFFF;
+        }
+        __syncthreads();
+        n = kc * E;
+    }
+    // each candidate's rank among them
+    for (int i = tid; i < n; i += kThreads) {
+        const uint32_t key = ck[i];
+        const int id = ci[i];
+        int place = 0;
+        for (int j = 0; j < n; ++j)
+            place += ck[j] > key || (ck[j] == key && ci[j] < id) ? 1 : 0;
+        if (place < have) {
+            bk[place] = key;
+            bi[place] = id;
+        }
+    }
+    for (int i = have + tid; i < k; i += kThreads) {
+        bk[i] = 0;
+        bi[i] = 0x7FFFFFFF;
+    }
+    __syncthreads();
 }
 
 // ------------------------------------------------------------ log probabilities
@@ -626,11 +862,9 @@ struct LogprobArgs {
 
 constexpr int kUnroll = 4;  // chunks in flight per thread
 
-// TOP: the maximum of every 32 consecutive chunks (what one warp loads at once)
-// is kept in shared memory.  The k largest elements of a row lie in the k
-// groups with the largest maxima (equal ones: the lower groups), so the second
-// step looks at 32 k chunks, the third at the k best of those: exact for any
-// input, and the row is read once plus k groups from L2.
+// TOP: the largest of every 32 consecutive chunks (what one warp loads at once)
+// is kept in shared memory, so the row is read once plus the few groups that
+// block_top looks at again, from L2.
 template <typename T, bool TOP>
 __global__ void __launch_bounds__(kThreads)
 logprobs_kernel(const __grid_constant__ LogprobArgs a)
@@ -640,6 +874,12 @@ logprobs_kernel(const __grid_constant__ LogprobArgs a)
     __shared__ Stats red[kWarps];
     __shared__ Stats parts[kMaxCluster];
     __shared__ int sred[2 * kWarps];
+    __shared__ int cnt[24];
+    __shared__ int ncand;
+    if (TOP && threadIdx.x < 24)
+        cnt[threadIdx.x] = 0;
+    if (TOP && threadIdx.x == 0)
+        ncand = 0;
     griddep_wait();
     griddep_launch_dependents();
     const int C = a.cluster;
@@ -676,87 +916,69 @@ logprobs_kernel(const __grid_constant__ LogprobArgs a)
     const TopLayout lay = top_layout((per_max + C - 1) / C, a.top_k, C);
     uint32_t *gkeys = dyn + lay.groups;
 
+    // a warp takes kUnroll groups at a time; their largest elements as floats
+    // first, as keys once all are there
+    float *gmax = reinterpret_cast<float *>(gkeys);
     Stats t = stats_empty();
-    for (int g = g0 + warp * kUnroll; g < g1; g += kWarps * kUnroll) {
-        uint4 v[kUnroll];
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u)
-            v[u] = load_chunk(r, (g + u) * 32 + lane, g1 * 32, total, a.status);
+    auto add = [&](const uint4(&v)[kUnroll], int g) {
         if (TOP) {
 #pragma unroll
             for (int u = 0; u < kUnroll; ++u) {
-                const uint32_t key = __reduce_max_sync(0xFFFFFFFFu, order_key(chunk_max<T>(v[u])));
-                if (lane == 0 && g + u < g1)
-                    gkeys[g + u - g0] = key;
+                const float m = warp_max_of(chunk_max<T>(v[u]));
+                if (lane == u && g + u < g1)
+                    gmax[g + u - g0] = m;
             }
         }
         add_chunks<T, true>(t, v, a.c, a.inv_c);
+    };
+    for (int g = g0 + warp * kUnroll; g < g1; g += kWarps * kUnroll) {
+        uint4 v[kUnroll];
+        const int c = g * 32 + lane;
+        if (g * 32 >= r.w0 && (g + kUnroll) * 32 <= min(g1 * 32, r.w1)) {
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u) {
+                v[u] = neg_inf_chunk(T());
+                if (in_range(r.at - r.off + static_cast<int64_t>(c + 32 * u) * E, E, total, a.status))
+                    v[u] = reinterpret_cast<const uint4 *>(r.base)[c + 32 * u];
+            }
+        } else {
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u)
+                v[u] = load_chunk(r, c + 32 * u, g1 * 32, total, a.status);
+        }
+        add(v, g);
     }
-    if (TOP)
-        __syncthreads();
     const int ec = r.edge(edge_of_thread(), g0 * 32, g1 * 32);
+    float edge_max = F8_NEG_INF;
     if (ec >= 0) {
         float x[E];
         load_edge(r, ec, x, total, a.status);
         add_values<true>(t, x, a.c);
-        if (TOP)
-            atomicMax(&gkeys[ec / 32 - g0], order_key(max_of(x)));
+        edge_max = max_of(x);
     }
-    t = block_join<true, kWarps>(t, a.c, red);
-
-    // the block's own k best: ids and keys into the leader's merge arrays
     if (TOP) {
-        int *list = reinterpret_cast<int *>(dyn + lay.list);
-        uint32_t *keys = dyn + lay.keys;
+        __syncthreads();
+        for (int i = tid; i < g1 - g0; i += kThreads)
+            gkeys[i] = order_key(gmax[i]);
+        __syncthreads();
+        if (ec >= 0)
+            atomicMax(&gkeys[ec / 32 - g0], order_key(edge_max));
+    }
+    t = block_join<true>(t, a.c, red);
+
+    if (TOP) {
         const int k = a.top_k;
         const int v0 = g0 * 32 * E - r.off, v1 = min(g1 * 32 * E - r.off, r.vocab);
         const int have = max(0, min(k, v1 - max(v0, 0)));
-        __syncthreads();
-        block_select(gkeys, g1 - g0, k, list, sred);
-        const int ng = min(k, g1 - g0);
-        for (int i = tid; i < ng * 32; i += kThreads) {
-            const int ch = (g0 + list[i >> 5]) * 32 + (i & 31);
-            uint32_t key = 0;
-            if (ch < r.nch) {
-                float x[E];
-                if (r.whole(ch))
-                    unpack<T>(load_chunk(r, ch, r.nch, total, a.status), x);
-                else
-                    load_edge(r, ch, x, total, a.status);
-                key = order_key(max_of(x));
-            }
-            keys[i] = key;
-        }
-        __syncthreads();
-        // positions among the candidate chunks, then their chunk numbers
-        int *pick = reinterpret_cast<int *>(dyn + lay.pick);
-        block_select(keys, ng * 32, k, pick, sred);
-        const int nc = min(k, ng * 32);
-        for (int i = tid; i < nc; i += kThreads)
-            pick[i] = (g0 + list[pick[i] >> 5]) * 32 + (pick[i] & 31);
-        __syncthreads();
-        for (int i = tid; i < nc * E; i += kThreads) {
-            const int v = pick[i / E] * E + i % E - r.off;
-            keys[i] = v >= 0 && v < r.vocab
-                          ? order_key(as_float(r.base[pick[i / E] * static_cast<int64_t>(E) + i % E]))
-                          : 0u;
-        }
-        __syncthreads();
-        block_select(keys, nc * E, have, list, sred);
-        uint32_t *mk = dyn + lay.merge_key + rank * k, *mi = dyn + lay.merge_id + rank * k;
-        if (C > 1) {
+        block_top<T>(r, g0, g1, k, have, dyn, lay, sred, cnt, &ncand, total, a.status);
+        if (C > 1) {  // into the leader's merge arrays
             cluster_started();
-            mk = peer(mk, 0);
-            mi = peer(mi, 0);
-        }
-        for (int i = tid; i < k; i += kThreads) {
-            uint32_t key = 0, id = 0x7FFFFFFFu;
-            if (i < have) {
-                key = keys[list[i]];
-                id = pick[list[i] / E] * E + list[i] % E - r.off;
+            uint32_t *mk = peer(dyn + lay.merge_key + rank * k, 0);
+            uint32_t *mi = peer(dyn + lay.merge_id + rank * k, 0);
+            for (int i = tid; i < k; i += kThreads) {
+                mk[i] = dyn[lay.best_key + i];
+                mi[i] = dyn[lay.best_id + i];
             }
-            mk[i] = key;
-            mi[i] = id;
         }
     } else if (C > 1) {
         cluster_started();
@@ -804,23 +1026,42 @@ logprobs_kernel(const __grid_constant__ LogprobArgs a)
     }
     if (TOP) {
         const int k = a.top_k;
-        int *list = reinterpret_cast<int *>(dyn + lay.list);
-        const uint32_t *mk = dyn + lay.merge_key;
-        const uint32_t *mi = dyn + lay.merge_id;
-        __syncthreads();
-        block_select(mk, C * k, k, list, sred);
-        // descending order: the rank of each among the k
-        for (int i = tid; i < k; i += kThreads) {
-            const uint32_t key = mk[list[i]];
-            int place = 0;
-            for (int j = 0; j < k; ++j) {
-                const uint32_t o = mk[list[j]];
-                place += (o > key || (o == key && j < i)) ? 1 : 0;
-            }
-            a.top_ids[row * k + place] = static_cast<int32_t>(mi[list[i]]);
+        auto put = [&](int place, uint32_t key, uint32_t id) {
+            a.top_ids[row * k + place] = static_cast<int32_t>(id);
             a.top_logp[row * k + place] =
                 none ? F8_NEG_INF
-                     : (lse != lse ? F8_NAN : fminf((key_value(key) - t.m) * a.inv_t - ls, 0.0f));
+                     : (lse != lse ? F8_NAN
+                                   : fminf((key_value(key) - t.m) * a.inv_t - ls, 0.0f));
+        };
+        if (C == 1) {
+            for (int i = tid; i < k; i += kThreads)
+                put(i, dyn[lay.best_key + i], dyn[lay.best_id + i]);
+            return;
+        }
+        // the blocks' lists are in order, and a later block's ids are larger: an
+        // item's place is its own plus what each other list has before it
+        const uint32_t *mk = dyn + lay.merge_key;
+        const uint32_t *mi = dyn + lay.merge_id;
+        for (int i = tid; i < C * k; i += kThreads) {
+            const uint32_t key = mk[i];
+            const int own = i / k;
+            int place = i % k;
+            for (int l = 0; l < C; ++l) {
+                if (l == own)
+                    continue;
+                int lo = 0, hi = k;  // first of list l that does not come before
+                while (lo < hi) {
+                    const int mid = (lo + hi) / 2;
+                    const uint32_t o = mk[l * k + mid];
+                    if (o > key || (o == key && l < own))
+                        lo = mid + 1;
+                    else
+                        hi = mid;
+                }
+                place += lo;
+            }
+            if (key > 0 && place < k)
+                put(place, key, mi[i]);
         }
     }
 }
@@ -832,69 +1073,106 @@ struct OutArgs {
     unsigned *amax;
 };
 
-// Elements of chunk c that lie in the row, one by one.
+// Where a row of the gradient goes.
 template <typename T>
-__device__ __forceinline__ uint32_t store_elements(const Row<T> &r, T *out, int c,
-                                                   const float (&f)[Chunk<T>::E], int64_t out_at,
-                                                   int64_t out_total, unsigned *status)
+struct OutRow {
+    T *p;
+    int64_t at, total;  // the row's first element in the whole buffer, and its size
+    bool same;          // starts at the logits row's offset from a 16-byte boundary
+
+    __device__ __forceinline__ OutRow(const OutArgs &o, int64_t rows, int64_t row, const Row<T> &r)
+    {
+        at = row * o.ld;
+        p = static_cast<T *>(o.p) + at;
+        total = rows * o.ld;
+        same = static_cast<int>((reinterpret_cast<uintptr_t>(p) & 15u) / sizeof(T)) == r.off;
+    }
+};
+
+// Magnitude bits of two bf16 in each word, folded into a running maximum.
+__device__ __forceinline__ uint32_t abs_max(uint32_t m, uint4 v)
+{
+    return __vmaxu2(__vmaxu2(m, __vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu)),
+                    __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu));
+}
+
+// Elements of chunk c that lie in the row, one by one; m2: running maximum of
+// the stored bf16 values' magnitude bits.
+template <typename T>
+__device__ __forceinline__ void store_elements(const Row<T> &r, const OutRow<T> &o, int c,
+                                               const float (&f)[Chunk<T>::E], uint32_t &m2,
+                                               unsigned *status)
 {
     constexpr int E = Chunk<T>::E;
-    uint32_t m2 = 0;
 #pragma unroll
     for (int e = 0; e < E; ++e) {
         const int i = c * E + e - r.off;
         const T v = static_cast<T>(f[e]);
-        if (i >= 0 && i < r.vocab && in_range(out_at + i, 1, out_total, status)) {
-            out[i] = v;
+        if (i >= 0 && i < r.vocab && in_range(o.at + i, 1, o.total, status)) {
+            o.p[i] = v;
             if (sizeof(T) == 2)
                 m2 = __vmaxu2(m2, (__float_as_uint(as_float(v)) >> 16) & 0x7FFFu);
         }
     }
-    return m2;
 }
 
-// Writes a whole chunk of a row's gradient: one vector where the output row
-// has the input row's offset, else element by element.  Returns the magnitude
-// bits of the stored bf16 values as a maximum over u16 pairs.
-template <typename T>
-__device__ __forceinline__ uint32_t store_chunk(const Row<T> &r, T *out, bool same, int c,
-                                                const float (&f)[Chunk<T>::E], int64_t out_at,
-                                                int64_t out_total, unsigned *status)
+// Writes U whole chunks c + u * N, those below `end`: vectors where the output
+// row has the input row's offset, else element by element.
+template <typename T, int N, int U>
+__device__ __forceinline__ void store_chunks(const Row<T> &r, const OutRow<T> &o, int c, int end,
+                                             const uint4 (&v)[U], bool amax, uint32_t &m2,
+                                             unsigned *status)
 {
     constexpr int E = Chunk<T>::E;
-    if (!same)
-        return store_elements(r, out, c, f, out_at, out_total, status);
-    const uint4 v = pack<T>(f);
-    const int64_t i = static_cast<int64_t>(c) * E - r.off;
-    if (in_range(out_at + i, E, out_total, status))
-        *reinterpret_cast<uint4 *>(out + i) = v;
-    if (sizeof(T) != 2)
-        return 0;
-    return __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu),
-                    __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu));
+    if (!o.same) {
+#pragma unroll 1
+        for (int u = 0; u < U; ++u) {
+            uint4 w = v[0];
+#pragma unroll
+            for (int j = 1; j < U; ++j)
+                w = u == j ? v[j] : w;
+            float f[E];
+            unpack<T>(w, f);
+            if (c + u * N < end)
+                store_elements(r, o, c + u * N, f, m2, status);
+        }
+        return;
+    }
+    uint4 *p = reinterpret_cast<uint4 *>(o.p + (static_cast<int64_t>(c) * E - r.off));
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+        if (c + u * N < end && in_range(o.at + static_cast<int64_t>(c + u * N) * E - r.off, E,
+                                        o.total, status))
+            p[u * N] = v[u];
+    if (amax) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (c + u * N < end)
+                m2 = abs_max(m2, v[u]);
+    }
 }
 
 // Zeros in columns [from, to) of an output row, by n threads of which this is
 // number t: 16-byte pieces, and single elements at the ends.
 template <typename T>
-__device__ __forceinline__ void zero_columns(T *out, int64_t from, int64_t to, int64_t out_at,
-                                             int64_t out_total, unsigned *status, int t, int n)
+__device__ __forceinline__ void zero_columns(const OutRow<T> &o, int64_t from, int64_t to, int t,
+                                             int n, unsigned *status)
 {
     constexpr int64_t E = Chunk<T>::E;
     if (from >= to)
         return;
-    const int64_t lead = (E - static_cast<int64_t>((reinterpret_cast<uintptr_t>(out + from) & 15u) /
+    const int64_t lead = (E - static_cast<int64_t>((reinterpret_cast<uintptr_t>(o.p + from) & 15u) /
                                                    sizeof(T))) % E;
     const int64_t v0 = min(from + lead, to), nv = (to - v0) / E;
     for (int64_t i = from + t; i < v0; i += n)
-        if (in_range(out_at + i, 1, out_total, status))
-            out[i] = T(0.0f);
+        if (in_range(o.at + i, 1, o.total, status))
+            o.p[i] = T(0.0f);
     for (int64_t i = t; i < nv; i += n)
-        if (in_range(out_at + v0 + i * E, E, out_total, status))
-            *reinterpret_cast<uint4 *>(out + v0 + i * E) = make_uint4(0, 0, 0, 0);
+        if (in_range(o.at + v0 + i * E, E, o.total, status))
+            *reinterpret_cast<uint4 *>(o.p + v0 + i * E) = make_uint4(0, 0, 0, 0);
     for (int64_t i = v0 + nv * E + t; i < to; i += n)
-        if (in_range(out_at + i, 1, out_total, status))
-            out[i] = T(0.0f);
+        if (in_range(o.at + i, 1, o.total, status))
+            o.p[i] = T(0.0f);
 }
 
 // One atomicMax per block on the fp32 pattern of a zeroed word (the result
@@ -919,14 +1197,35 @@ __device__ __forceinline__ void block_amax(uint32_t m2, unsigned *amax, unsigned
     }
 }
 
+// p = norm 2^((x a + b) s): the softmax of an element x from the maximum
+// (a 1, b -max, s c, norm 1 / sum) or from lse (a 1 / T, b -lse, s log2 e, norm 1).
+struct Softmax {
+    float a, b, s, norm;
+
+    __device__ __forceinline__ float exponent(float x) const { return fmaf(x, a, b) * s; }
+    __device__ __forceinline__ float2 exponent(float2 x) const
+    {
+        return __fmul2_rn(__ffma2_rn(x, make_float2(a, a), make_float2(b, b)), make_float2(s, s));
+    }
+};
+
+// factor p / norm of a chunk's elements.
 template <typename T>
-__device__ __forceinline__ bool same_offset(const Row<T> &r, const T *out)
+__device__ __forceinline__ uint4 scaled_softmax(uint4 v, const Softmax &k, float factor)
 {
-    return static_cast<int>((reinterpret_cast<uintptr_t>(out) & 15u) / sizeof(T)) == r.off;
+    constexpr int E = Chunk<T>::E;
+    float2 f[E / 2];
+    unpack2<T>(v, f);
+#pragma unroll
+    for (int e = 0; e < E / 2; ++e) {
+        const float2 d = k.exponent(f[e]);
+        f[e] = __fmul2_rn(make_float2(ex2(d.x), ex2(d.y)), make_float2(factor, factor));
+    }
+    return pack2<T>(f);
 }
 
-// Chunks per block of the backward kernels.
-constexpr int kBwdChunks = 8 * kThreads;
+// Blocks of the backward kernels take this many chunks of a row each.
+constexpr int kBwdChunks = 16 * kThreads;
 
 // ------------------------------------------------------------ log probabilities, backward
 struct LogprobBwdArgs {
@@ -935,11 +1234,15 @@ struct LogprobBwdArgs {
     int vocab, blocks_per_row;
     const int64_t *tokens;
     const float *lse, *entropy, *dlogp, *dentropy;
-    float inv_t;
+    float inv_t, t;  // 1 / T, T
     OutArgs out;
     unsigned *status;
 };
 
+// With l = log p, the gradient of a and h is
+//   (a 1[v = token] - p (a + h (l + H))) / T,
+// for most elements p times a linear function of l.  With an entropy gradient
+// the logits are first raised to where p is 0 in fp32 and l still finite.
 template <typename T>
 __global__ void __launch_bounds__(kThreads)
 logprobs_bwd_kernel(const __grid_constant__ LogprobBwdArgs a)
@@ -949,69 +1252,86 @@ logprobs_bwd_kernel(const __grid_constant__ LogprobBwdArgs a)
     griddep_launch_dependents();
     const int64_t row = blockIdx.x / a.blocks_per_row;
     const int part = static_cast<int>(blockIdx.x % a.blocks_per_row);
+    const int tid = threadIdx.x;
     const Row<T> r(static_cast<const T *>(a.logits), row, a.ld, a.vocab);
     const int64_t total = (a.rows - 1) * a.ld + a.vocab;
-    T *out = static_cast<T *>(a.out.p) + row * a.out.ld;
-    const int64_t out_at = row * a.out.ld, out_total = a.rows * a.out.ld;
+    const OutRow<T> o(a.out, a.rows, row, r);
     const int64_t tok = a.tokens != nullptr ? a.tokens[row] : -1;
     const float ga = a.dlogp != nullptr && a.tokens != nullptr ? a.dlogp[row] : 0.0f;
     const float gh = a.dentropy != nullptr ? a.dentropy[row] : 0.0f;
     const float lse = a.lse[row];
     const bool skip = (a.tokens != nullptr && tok < 0) || (ga == 0.0f && gh == 0.0f) ||
                       fabsf(lse) >= kMaxLse;
-    const bool same = same_offset(r, out);
-    const float H = gh != 0.0f ? a.entropy[row] : 0.0f;
-    const float fa = ga * a.inv_t, fh = gh * a.inv_t;
-    uint32_t m2 = 0;
-    if (tok >= r.vocab && threadIdx.x == 0)
+    const bool amax = a.out.amax != nullptr;
+    if (tok >= r.vocab && tid == 0)
         atomicOr(a.status, kStatusIndex);
+    uint32_t m2 = 0;
     const int c0 = part * kBwdChunks, c1 = min(r.nch, c0 + kBwdChunks);
-    // the gradient of one chunk in place of its logits
-    auto gradient = [&](int ch, float (&f)[E]) {
-        const int64_t first = static_cast<int64_t>(ch) * E - r.off;
+    const int wb = max(c0, r.w0), we = min(c1, r.w1);
+    if (skip) {
+        zero_columns(o, max(static_cast<int64_t>(c0) * E - r.off, static_cast<int64_t>(0)),
+                     min(static_cast<int64_t>(c1) * E - r.off, static_cast<int64_t>(r.vocab)), tid,
+                     kThreads, a.status);
+    } else {
+        const float H = gh != 0.0f ? a.entropy[row] : 0.0f;
+        const Softmax k{a.inv_t, -lse, static_cast<float>(kLog2e), 1.0f};
+        const float fa = ga * a.inv_t, fh = gh * a.inv_t;
+        const float f0 = -fmaf(fh, H, fa), f1 = -fh;  // dense part: p (f0 + f1 l)
+        const int tok_chunk = tok >= 0 && tok < r.vocab ? (static_cast<int>(tok) + r.off) / E : -1;
+        auto elements = [&](int ch, float (&f)[E]) {
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-            const float lp = fmaf(f[e], a.inv_t, -lse);
-            const float p = ex2(lp * static_cast<float>(kLog2e));
-            // p (lp + H) is 0 for a masked token, whose lp is -inf
-            const float q = p * (fmaxf(lp, kFloor2) + H);
-            const float g = (tok == first + e ? fa : 0.0f) - fmaf(fa, p, fh * q);
-            f[e] = skip ? 0.0f : g;
-        }
-    };
-    for (int cb = max(c0, r.w0) + static_cast<int>(threadIdx.x); cb < min(c1, r.w1);
-         cb += kUnroll * kThreads) {
-        uint4 v[kUnroll];
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u)
-            v[u] = load_chunk(r, cb + u * kThreads, skip ? 0 : c1, total, a.status);
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            const int ch = cb + u * kThreads;
-            if (ch < min(c1, r.w1)) {
-                float f[E];
-                unpack<T>(v[u], f);
-                gradient(ch, f);
-                m2 = __vmaxu2(m2, store_chunk(r, out, same, ch, f, out_at, out_total, a.status));
+            for (int e = 0; e < E; ++e) {
+                const float l = fmaf(f[e], k.a, k.b);
+                const float p = ex2(l * k.s);
+                const float g = p * fmaf(f1, fmaxf(l, kFloor2), f0);
+                f[e] = ch * E + e - r.off == tok ? fa + g : g;
             }
-        }
-    }
-    const int ec = r.edge(edge_of_thread(), c0, c1);
-    if (ec >= 0) {
-        float f[E];
-        if (skip) {
+        };
+        // the elements' floor: l = -140, where p is 0
+        const float low = (lse - 140.0f) * a.t;
+        const bool dense = gh == 0.0f, ordinary = fabsf(low) < kFastRange;
+        walk_chunks<T, kThreads, kUnroll>(r, wb, we, total, a.status, [&](uint4(&v)[kUnroll], int c) {
+            uint4 g[kUnroll];
+            if (dense) {
 #pragma unroll
-            for (int e = 0; e < E; ++e)
-                f[e] = 0.0f;
-        } else {
+                for (int u = 0; u < kUnroll; ++u)
+                    g[u] = scaled_softmax<T>(v[u], k, f0);
+            } else {
+#pragma unroll
+                for (int u = 0; u < kUnroll; ++u) {
+                    float2 f[E / 2];
+                    unpack2<T>(chunk_floor<T>(v[u], low), f);
+#pragma unroll
+                    for (int e = 0; e < E / 2; ++e) {
+                        const float2 l = __ffma2_rn(f[e], make_float2(k.a, k.a), make_float2(k.b, k.b));
+                        const float2 d = __fmul2_rn(l, make_float2(k.s, k.s));
+                        f[e] = __fmul2_rn(make_float2(ex2(d.x), ex2(d.y)),
+                                          __ffma2_rn(l, make_float2(f1, f1), make_float2(f0, f0)));
+                    }
+                    g[u] = pack2<T>(f);
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u) {
+                if (c + u * kThreads == tok_chunk || !(dense || ordinary)) {
+                    float f[E];
+                    unpack<T>(v[u], f);
+                    elements(c + u * kThreads, f);
+                    g[u] = pack<T>(f);
+                }
+            }
+            store_chunks<T, kThreads>(r, o, c, we, g, amax, m2, a.status);
+        });
+        const int ec = r.edge(edge_of_thread(), c0, c1);
+        if (ec >= 0) {
+            float f[E];
             load_edge(r, ec, f, total, a.status);
+            elements(ec, f);
+            store_elements(r, o, ec, f, m2, a.status);
         }
-        gradient(ec, f);
-        m2 = __vmaxu2(m2, store_elements(r, out, ec, f, out_at, out_total, a.status));
     }
     if (part == a.blocks_per_row - 1)
-        zero_columns(out, r.vocab, a.out.ld, out_at, out_total, a.status,
-                     static_cast<int>(threadIdx.x), static_cast<int>(blockDim.x));
+        zero_columns(o, r.vocab, a.out.ld, tid, kThreads, a.status);
     block_amax(m2, a.out.amax, a.status);
 }
 
@@ -1031,523 +1351,17 @@ struct DistillArgs {
 
 // The row's slots in shared memory.  A table keyed by chunk number finds the
 // slots that name an element of a chunk: head[chunk % kHeads] starts a list
-// of slots.  Slots of equal ids each carry their summed q.
+// of slots.  Slots of equal ids each carry their summed q.  The sums over the
+// slots are all that the loss needs of them:
+//   loss = sum q log q - sum q (z - zref) / T + sum q ((max - zref) / T + ln S)
+// for the row's maximum and S = sum e^((x - max) / T).
 constexpr int kHeads = 2048;
-struct SlotTable {
+struct Slots {
     int head[kHeads];
     int next[F8_MAX_TOP];
-    int id[F8_MAX_TOP];     // -1: empty
-    float q[F8_MAX_TOP];    // the slot's own q
-    float qsum[F8_MAX_TOP]; // of all slots with this id
-};
-struct Slots : SlotTable {
-    float logq[F8_MAX_TOP];
-    float z[F8_MAX_TOP];    // the student's logit at id
-    uint8_t first[F8_MAX_TOP];
-    float red[32];
-  };
-
-struct SlotSums {
-    bool any;     // the row has a slot
-    float total;  // sum q (1 without the tail class)
-    float left;   // q_r
-};
-
-// Reads the row's slots; all threads of the block.
-template <typename T, bool TAIL, int WARPS>
-__device__ __forceinline__ SlotSums load_slots(const DistillArgs &a, const Row<T> &r, int64_t row,
-                                               Slots &s, bool table, bool logits)
-{
-    constexpr int N = WARPS * 32;
-    const int tid = threadIdx.x, k = a.k;
-    if (table) {
-        for (int i = tid; i < kHeads / 4; i += N)
-            reinterpret_cast<uint4 *>(s.head)[i] =
-                make_uint4(0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu);
-    }
-    const bool mine = tid < k;
-    int id = -1;
-    float t = F8_NEG_INF;
-    if (mine) {
-        id = a.ids[row * k + tid];
-        t = a.values[row * k + tid];
-        if (id >= r.vocab) {
-            atomicOr(a.status, kStatusIndex);
-            id = -1;
-        }
-        if (t == F8_NEG_INF)
-            id = -1;
-        if (id < 0)
-            t = F8_NEG_INF;
-        s.id[tid] = id < 0 ? -1 : id;
-    }
-    SlotSums out;
-    out.any = __syncthreads_or(mine && id >= 0) != 0;
-    out.total = 1.0f;
-    out.left = 0.0f;
-    if (!out.any)
-        return out;
-    float q = 0.0f, logq = 0.0f;
-    if (TAIL) {
-        q = id >= 0 ? expf(t) : 0.0f;
-        logq = t;
-        out.total = block_sum<WARPS>(q, s.red);
-        out.left = fmaxf(1.0f - out.total, 0.0f);
-    } else {
-        const float m = block_max<WARPS>(t, s.red);
-        const float d = (t - m) * a.inv_t;
-        const float e = id >= 0 ? expf(d) : 0.0f;
-        const float sum = block_sum<WARPS>(e, s.red);
-        q = e / sum;
-        logq = d - logf(sum);
-    }
-    if (mine) {
-        s.q[tid] = q;
-        s.logq[tid] = logq;
-        if (logits)
-            s.z[tid] = id >= 0 ? as_float(r.base[r.off + id]) : 0.0f;
-    }
-    __syncthreads();
-    bool first = id >= 0;
-    float qs = 0.0f;
-    if (id >= 0) {
-        for (int j = 0; j < k; ++j) {
-            if (s.id[j] == id) {
-                qs += s.q[j];
-                first = first && j >= tid;
-            }
-        }
-    }
-    if (mine) {
-        s.first[tid] = first;
-        s.qsum[tid] = qs;
-    }
-    // a list's order is free: of slots with one id each gives the same values
-    if (table && id >= 0)
-        s.next[tid] = atomicExch(&s.head[((id + r.off) / Chunk<T>::E) % kHeads], tid);
-    __syncthreads();
-    return out;
-}
-
-// -inf in the elements of chunk ch that a slot names.
-template <typename T>
-__device__ __forceinline__ void drop_slots(const SlotTable &s, const Row<T> &r, int ch,
-                                           float (&f)[Chunk<T>::E])
-{
-    constexpr int E = Chunk<T>::E;
-    for (int j = s.head[ch % kHeads]; j >= 0; j = s.next[j]) {
-        const int d = s.id[j] + r.off - ch * E;
-#pragma unroll
-        for (int e = 0; e < E; ++e)
-            if (d == e)
-                f[e] = F8_NEG_INF;
-    }
-}
-
-template <typename T>
-__device__ __forceinline__ uint4 without_slots(const SlotTable &s, const Row<T> &r, int ch, uint4 v)
-{
-    if (s.head[ch % kHeads] >= 0) {
-        float f[Chunk<T>::E];
-        unpack<T>(v, f);
-        drop_slots(s, r, ch, f);
-        v = pack<T>(f);  // exact: the values are the chunk's own
-    }
-    return v;
-}
-
-// The loss of a row from the slots and the student's statistics over the
-// whole vocabulary (TAIL: over the tokens outside the slots' ids); all threads
-// of the block.  Gives lse and the student's mass outside.
-struct RowLoss {
-    float loss, lse, rest;
-    float m, inv_s;  // p = 2^((x - m) c) inv_s
-    bool none;       // every token is masked
-    bool bad;        // NaN or +inf
-};
-
-template <bool TAIL, int WARPS>
-__device__ __forceinline__ RowLoss row_loss(const DistillArgs &a, Slots &s, const SlotSums &q,
-                                            Stats t, bool want)
-{
-    const int tid = threadIdx.x;
-    const bool mine = tid < a.k && s.id[tid] >= 0;
-    const float z = mine ? s.z[tid] : F8_NEG_INF;
-    RowLoss o;
-    o.rest = 0.0f;
-    float outside = t.s, m = t.m;
-    if (TAIL) {
-        m = fmaxf(t.m, block_max<WARPS>(z, s.red));
-        // a NaN is no maximum; it reaches the sum
-        const float mm = m == F8_NEG_INF ? 0.0f : m;
-        outside = t.s * ex2(fmaxf((t.m - m) * a.c, kFloor2));
-        const float in = mine && s.first[tid] ? ex2((z - mm) * a.c) : 0.0f;
-        t.s = outside + block_sum<WARPS>(in, s.red);
-        t.m = m;
-    }
-    o.bad = t.s != t.s || m == F8_POS_INF;
-    o.none = !o.bad && t.s == 0.0f;
-    o.m = m == F8_NEG_INF ? 0.0f : m;
-    o.inv_s = o.none ? 0.0f : 1.0f / t.s;
-    const float ls = logf(t.s);
-    o.lse = o.bad ? F8_NAN : (o.none ? F8_NEG_INF : fmaf(m, a.inv_t, ls));
-    if (TAIL)
-        o.rest = o.bad ? F8_NAN : outside * o.inv_s;
-    o.loss = 0.0f;
-    if (want) {
-        float term = 0.0f;
-        if (mine && s.q[tid] > 0.0f) {
-            // log p from the difference to the maximum; -inf for a masked token
-            const float lp = o.none ? F8_NEG_INF : fmaf(z - o.m, a.inv_t, -ls);
-            term = s.q[tid] * (s.logq[tid] - lp);
-        } else if (mine && s.q[tid] != s.q[tid]) {
-            term = F8_NAN;
-        }
-        o.loss = block_sum<WARPS>(term, s.red);
-        if (TAIL && o.rest > 0.0f && q.left > 0.0f)
-            o.loss += q.left * (logf(q.left) - logf(o.rest));
-        if (o.bad)
-            o.loss = F8_NAN;
-    }
-    return o;
-}
-
-template <typename T, bool TAIL>
-__global__ void __launch_bounds__(kThreads)
-distill_fwd_kernel(const __grid_constant__ DistillArgs a)
-{
-    constexpr int E = Chunk<T>::E;
-    __shared__ __align__(16) Slots slots;
-    __shared__ Stats red[kWarps];
-    __shared__ Stats parts[kMaxCluster];
-    griddep_wait();
-    griddep_launch_dependents();
-    const int C = a.cluster;
-    const int64_t row = blockIdx.x / C;
-    const int rank = static_cast<int>(blockIdx.x % C);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const Row<T> r(static_cast<const T *>(a.logits), row, a.ld, a.vocab);
-    const int64_t total = (a.rows - 1) * a.ld + a.vocab;
-    if (C > 1)
-        cluster_start();
-    const SlotSums q = load_slots<T, TAIL, kWarps>(a, r, row, slots, TAIL, true);
-    if (!q.any) {
-        if (C > 1)
-            cluster_started();
-        if (rank == 0 && tid == 0) {
-            a.loss[row] = 0.0f;
-            a.lse[row] = 0.0f;
-            if (TAIL)
-                a.rest[row] = 0.0f;
-        }
-        return;
-    }
-    const int ngroups = (r.nch + 31) / 32;
-    const int per = (ngroups + C - 1) / C;
-    const int g0 = min(ngroups, rank * per), g1 = min(ngroups, g0 + per);
-    Stats t = stats_empty();
-    for (int g = g0 + warp * kUnroll; g < g1; g += kWarps * kUnroll) {
-        uint4 v[kUnroll];
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u)
-            v[u] = load_chunk(r, (g + u) * 32 + lane, g1 * 32, total, a.status);
-        if (TAIL) {
-#pragma unroll
-            for (int u = 0; u < kUnroll; ++u)
-                v[u] = without_slots(slots, r, (g + u) * 32 + lane, v[u]);
-        }
-        add_chunks<T, false>(t, v, a.c, 0.0f);
-    }
-    const int ec = r.edge(edge_of_thread(), g0 * 32, g1 * 32);
-    if (ec >= 0) {
-        float x[E];
-        load_edge(r, ec, x, total, a.status);
-        if (TAIL)
-            drop_slots(slots, r, ec, x);
-        add_values<false>(t, x, a.c);
-    }
-    t = block_join<false, kWarps>(t, a.c, red);
-    if (C > 1) {
-        cluster_started();
-        if (tid == 0)
-            *peer(&parts[rank], 0) = t;
-        cluster_join();
-        if (rank != 0)
-            return;
-        t = parts[0];
-        for (int i = 1; i < C; ++i)
-            t = join<false>(t, parts[i], a.c);
-    }
-    const RowLoss o = row_loss<TAIL, kWarps>(a, slots, q, t, true);
-    if (tid == 0) {
-        a.loss[row] = o.loss;
-        a.lse[row] = o.lse;
-        if (TAIL)
-            a.rest[row] = o.rest;
-        if (o.bad || o.loss != o.loss)
-            atomicOr(a.status, kStatusNonfinite);
-    }
-}
-
-// dlogits of one chunk: dense * p, and at the slots' ids scale (total p - q).
-template <typename T>
-__device__ __forceinline__ void slot_gradient(const SlotTable &s, const Row<T> &r, int ch,
-                                              const float (&p)[Chunk<T>::E], float scale,
-                                              float total, float (&g)[Chunk<T>::E])
-{
-    constexpr int E = Chunk<T>::E;
-    for (int j = s.head[ch % kHeads]; j >= 0; j = s.next[j]) {
-        const int d = s.id[j] + r.off - ch * E;
-#pragma unroll
-        for (int e = 0; e < E; ++e)
-            if (d == e)
-                g[e] = scale * fmaf(total, p[e], -s.qsum[j]);
-    }
-}
-
-template <typename T, bool TAIL>
-__global__ void __launch_bounds__(kThreads)
-distill_bwd_kernel(const __grid_constant__ DistillArgs a)
-{
-    constexpr int E = Chunk<T>::E;
-    __shared__ __align__(16) Slots slots;
-    griddep_wait();
-    griddep_launch_dependents();
-    const int64_t row = blockIdx.x / a.blocks_per_row;
-    const int part = static_cast<int>(blockIdx.x % a.blocks_per_row);
-    const Row<T> r(static_cast<const T *>(a.logits), row, a.ld, a.vocab);
-    const int64_t total = (a.rows - 1) * a.ld + a.vocab;
-    T *out = static_cast<T *>(a.out.p) + row * a.out.ld;
-    const int64_t out_at = row * a.out.ld, out_total = a.rows * a.out.ld;
-    const bool same = same_offset(r, out);
-    const float scale = a.dloss[row] * a.inv_t;
-    const float lse = a.lse[row];
-    SlotSums q = load_slots<T, TAIL, kWarps>(a, r, row, slots, true, false);
-    const bool skip = !q.any || a.dloss[row] == 0.0f || fabsf(lse) >= kMaxLse;
-    float mass = q.total, dense = q.total;
-    if (TAIL) {
-        const float rest = a.rest[row];
-        if (rest > 0.0f) {
-            mass = q.total + q.left;
-            dense = mass - q.left / rest;
-        }
-    }
-    uint32_t m2 = 0;
-    const int c0 = part * kBwdChunks, c1 = min(r.nch, c0 + kBwdChunks);
-    auto gradient = [&](int ch, float (&f)[E]) {
-        float g[E];
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            f[e] = ex2(fmaf(f[e], a.inv_t, -lse) * static_cast<float>(kLog2e));
-            g[e] = skip ? 0.0f : scale * dense * f[e];
-        }
-        if (!skip)
-            slot_gradient(slots, r, ch, f, scale, mass, g);
-#pragma unroll
-        for (int e = 0; e < E; ++e)
-            f[e] = g[e];
-    };
-    for (int cb = max(c0, r.w0) + static_cast<int>(threadIdx.x); cb < min(c1, r.w1);
-         cb += kUnroll * kThreads) {
-        uint4 v[kUnroll];
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u)
-            v[u] = load_chunk(r, cb + u * kThreads, skip ? 0 : c1, total, a.status);
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            const int ch = cb + u * kThreads;
-            if (ch < min(c1, r.w1)) {
-                float f[E];
-                unpack<T>(v[u], f);
-                gradient(ch, f);
-                m2 = __vmaxu2(m2, store_chunk(r, out, same, ch, f, out_at, out_total, a.status));
-            }
-        }
-    }
-    const int ec = r.edge(edge_of_thread(), c0, c1);
-    if (ec >= 0) {
-        float f[E];
-        if (skip) {
-#pragma unroll
-            for (int e = 0; e < E; ++e)
-                f[e] = 0.0f;
-        } else {
-            load_edge(r, ec, f, total, a.status);
-        }
-        gradient(ec, f);
-        m2 = __vmaxu2(m2, store_elements(r, out, ec, f, out_at, out_total, a.status));
-    }
-    if (part == a.blocks_per_row - 1)
-        zero_columns(out, r.vocab, a.out.ld, out_at, out_total, a.status,
-                     static_cast<int>(threadIdx.x), static_cast<int>(blockDim.x));
-    block_amax(m2, a.out.amax, a.status);
-}
-
-// Loss and gradient together, for short rows and for few.  A block, or a cluster
-// of C blocks, takes a row, each thread holding up to NV of its chunks in
-// registers between the two passes, so a row that fits is read once; a longer
-// one is walked in stretches and read again (from L2).
-constexpr int kNV = 8;
-
-template <typename T, bool TAIL>
-__global__ void __launch_bounds__(kThreads)
-distill_fused_kernel(const __grid_constant__ DistillArgs a)
-{
-    constexpr int E = Chunk<T>::E;
-    constexpr int N = kThreads;
-    __shared__ __align__(16) Slots slots;
-    __shared__ Stats red[kWarps];
-    __shared__ Stats parts[kMaxCluster];
-    griddep_wait();
-    griddep_launch_dependents();
-    const int C = a.cluster;
-    const int64_t row = blockIdx.x / C;
-    const int rank = static_cast<int>(blockIdx.x % C);
-    const int tid = threadIdx.x;
-    const Row<T> r(static_cast<const T *>(a.logits), row, a.ld, a.vocab);
-    const int64_t total = (a.rows - 1) * a.ld + a.vocab;
-    T *out = static_cast<T *>(a.out.p) + row * a.out.ld;
-    const int64_t out_at = row * a.out.ld, out_total = a.rows * a.out.ld;
-    const bool same = same_offset(r, out);
-    if (C > 1)
-        cluster_start();
-    const SlotSums q = load_slots<T, TAIL, kWarps>(a, r, row, slots, true, true);
-    const int per = (r.nch + C - 1) / C;
-    const int c0 = min(r.nch, rank * per), c1 = min(r.nch, c0 + per);
-    const float dl = a.dloss[row];
-    uint32_t m2 = 0;
-    const int ec = r.edge(edge_of_thread(), c0, c1);
-    const int wb = max(c0, r.w0), we = min(c1, r.w1);  // this block's whole chunks
-    if (q.any) {
-        uint4 v[kNV];
-        float edge[E];
-        Stats t = stats_empty();
-        if (ec >= 0) {
-            load_edge(r, ec, edge, total, a.status);
-            float x[E];
-#pragma unroll
-            for (int e = 0; e < E; ++e)
-                x[e] = edge[e];
-            if (TAIL)
-                drop_slots(slots, r, ec, x);
-            add_values<false>(t, x, a.c);
-        }
-        for (int cb = wb; cb < we; cb += kNV * N) {
-#pragma unroll
-            for (int u = 0; u < kNV; ++u)
-                v[u] = load_chunk(r, cb + u * N + tid, we, total, a.status);
-#pragma unroll
-            for (int h = 0; h < kNV; h += kUnroll) {
-                uint4 w[kUnroll];
-#pragma unroll
-                for (int u = 0; u < kUnroll; ++u)
-                    w[u] = TAIL ? without_slots(slots, r, cb + (h + u) * N + tid, v[h + u])
-                                : v[h + u];
-                add_chunks<T, false>(t, w, a.c, 0.0f);
-            }
-        }
-        t = block_join<false, kWarps>(t, a.c, red);
-        if (C > 1) {
-            cluster_started();
-            if (tid < C)
-                *peer(&parts[rank], tid) = t;
-            cluster_join();
-            t = parts[0];
-            for (int i = 1; i < C; ++i)
-                t = join<false>(t, parts[i], a.c);
-        }
-        const RowLoss o = row_loss<TAIL, kWarps>(a, slots, q, t, rank == 0);
-        if (rank == 0 && tid == 0) {
-            a.loss[row] = o.loss;
-            if (o.bad || o.loss != o.loss)
-                atomicOr(a.status, kStatusNonfinite);
-        }
-        float mass = q.total, dense = q.total;
-        if (TAIL && o.rest > 0.0f) {
-            mass = q.total + q.left;
-            dense = mass - q.left / o.rest;
-        }
-        const bool zero = dl == 0.0f || o.none;
-        const float scale = dl * a.inv_t, inv_s = o.bad ? F8_NAN : o.inv_s;
-        auto gradient = [&](int ch, float (&f)[E]) {
-            float g[E];
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-                f[e] = ex2((f[e] - o.m) * a.c) * inv_s;
-                g[e] = zero ? 0.0f : scale * dense * f[e];
-            }
-            if (!zero)
-                slot_gradient(slots, r, ch, f, scale, mass, g);
-#pragma unroll
-            for (int e = 0; e < E; ++e)
-                f[e] = g[e];
-        };
-        for (int cb = wb; cb < we; cb += kNV * N) {
-            if (we - wb > kNV * N) {
-#pragma unroll
-                for (int u = 0; u < kNV; ++u)
-                    v[u] = load_chunk(r, cb + u * N + tid, we, total, a.status);
-            }
-#pragma unroll
-            for (int u = 0; u < kNV; ++u) {
-                const int ch = cb + u * N + tid;
-                if (ch < we) {
-                    float f[E];
-                    unpack<T>(v[u], f);
-                    gradient(ch, f);
-                    m2 = __vmaxu2(m2, store_chunk(r, out, same, ch, f, out_at, out_total, a.status));
-                }
-            }
-        }
-        if (ec >= 0) {
-            gradient(ec, edge);
-            m2 = __vmaxu2(m2, store_elements(r, out, ec, edge, out_at, out_total, a.status));
-        }
-    } else {
-        if (C > 1)
-            cluster_started();
-        if (rank == 0 && tid == 0)
-            a.loss[row] = 0.0f;
-        float g[E];
-#pragma unroll
-        for (int e = 0; e < E; ++e)
-            g[e] = 0.0f;
-        for (int ch = wb + tid; ch < we; ch += N)
-            store_chunk(r, out, same, ch, g, out_at, out_total, a.status);
-        if (ec >= 0)
-            store_elements(r, out, ec, g, out_at, out_total, a.status);
-    }
-    if (rank == C - 1)
-        zero_columns(out, r.vocab, a.out.ld, out_at, out_total, a.status,
-                     static_cast<int>(threadIdx.x), static_cast<int>(blockDim.x));
-    block_amax(m2, a.out.amax, a.status);
-}
-
-// Loss and gradient together, for many long rows.  A row of the logits is
-// needed twice, for its sums and for its gradient, and the blocks of all SMs
-// together hold more than L2 does, so a block keeps what it can: one persistent
-// block per SM takes whole rows through a ring of 16 KB pieces in shared
-// memory that bulk copies fill.
-//   warp 16      reads the next row's slots (two buffers) and sums them up;
-//   warp 17      issues the copies: a row's pieces 0 .. n-1, then again those
-//                that the ring could not keep, then the next row's;
-//   warps 0..15  first pass: running sums over the pieces, releasing all but
-//                the last `keep`; the block's join (one barrier); second pass:
-//                the gradient of the kept pieces, then of those copied again
-//                (from L2, which they have just passed), released one by one.
-// The pieces are released in the order of their copies, so the ring is a queue
-// and the next row's copies run during the second pass.
-constexpr int kRingWarps = 16;
-constexpr int kRingConsumers = kRingWarps * 32;
-constexpr int kRingThreads = kRingConsumers + 64;
-constexpr int kPieceChunks = 1024;
-constexpr int kPieceBytes = kPieceChunks * 16;
-constexpr int kPieces = 12;
-constexpr int kKeep = 9;  // the other three are under way
-constexpr int kPerThread = kPieceChunks / kRingConsumers;
-constexpr uint64_t kDrainLimitNs = 1000000000ull;
-
-struct RingSlots : SlotTable {
+    int id[F8_MAX_TOP];      // -1: empty
+    float q[F8_MAX_TOP];     // the slot's own q
+    float qsum[F8_MAX_TOP];  // of all slots with this id
     int any;        // the row has a slot
     int used;       // some slot has q > 0
     int masked;     // such a slot names a masked token
@@ -1561,8 +1375,6 @@ struct RingSlots : SlotTable {
     float zmax;     // the largest logit of the slots' ids
     float inside;   // sum over these ids of 2^((z - zmax) c)
 };
-
-constexpr size_t kRingSmem = static_cast<size_t>(kPieces) * kPieceBytes + 2 * sizeof(RingSlots);
 
 template <typename V, typename F>
 __device__ __forceinline__ V warp_all(V v, F f)
@@ -1584,9 +1396,11 @@ __device__ __forceinline__ float warp_max(float v)
     return warp_all(v, [](float a, float b) { return fmaxf(a, b); });
 }
 
-// One row's slots, by one warp: slot lane + 32 i in register i.
-template <typename T, bool TAIL>
-__device__ __forceinline__ void ring_slots(const DistillArgs &a, int64_t row, RingSlots &s)
+// One row's slots, by one warp: slot lane + 32 i in register i.  Without LOSS
+// only what the gradient needs, and no logit is read (in a backward pass in
+// place another block may already have written it).
+template <typename T, bool TAIL, bool LOSS>
+__device__ __forceinline__ void warp_slots(const DistillArgs &a, int64_t row, Slots &s)
 {
     constexpr int N = F8_MAX_TOP / 32;
     const int lane = threadIdx.x & 31, k = a.k;
@@ -1602,7 +1416,7 @@ __device__ __forceinline__ void ring_slots(const DistillArgs &a, int64_t row, Ri
         id[i] = -1;
         t[i] = F8_NEG_INF;
         z[i] = F8_NEG_INF;
-        if (j < k) {
+        if (32 * i < k && j < k) {
             id[i] = a.ids[row * k + j];
             t[i] = a.values[row * k + j];
         }
@@ -1620,7 +1434,7 @@ __device__ __forceinline__ void ring_slots(const DistillArgs &a, int64_t row, Ri
         float zm = F8_NEG_INF, tm = F8_NEG_INF;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            if (id[i] >= 0)
+            if (LOSS && id[i] >= 0)
                 z[i] = as_float(r.base[r.off + id[i]]);
             tm = fmaxf(tm, t[i]);
         }
@@ -1630,7 +1444,9 @@ __device__ __forceinline__ void ring_slots(const DistillArgs &a, int64_t row, Ri
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             logq[i] = TAIL ? t[i] : (t[i] - tm) * a.inv_t;
-            q[i] = id[i] >= 0 ? expf(logq[i]) : 0.0f;
+            q[i] = 0.0f;
+            if (32 * i < k)
+                q[i] = id[i] >= 0 ? expf(logq[i]) : 0.0f;
             sum += q[i];
         }
         sum = warp_sum(sum);
@@ -1680,37 +1496,39 @@ __device__ __forceinline__ void ring_slots(const DistillArgs &a, int64_t row, Ri
                 s.qsum[j] = qs;
             }
         }
-        float zref = F8_NEG_INF, plogp = 0.0f;
+        float zref = F8_NEG_INF, plogp = 0.0f, zmean = 0.0f, inside = 0.0f, total = sum;
         bool used = false, masked = false;
+        if (LOSS) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const bool u = q[i] > 0.0f || q[i] != q[i];
-            used |= u;
-            masked |= u && z[i] == F8_NEG_INF;
-            if (u) {
-                plogp = fmaf(q[i], logq[i], plogp);
-                zref = fmaxf(zref, z[i]);
+            for (int i = 0; i < N; ++i) {
+                const bool u = q[i] > 0.0f || q[i] != q[i];
+                used |= u;
+                masked |= u && z[i] == F8_NEG_INF;
+                if (u) {
+                    plogp = fmaf(q[i], logq[i], plogp);
+                    zref = fmaxf(zref, z[i]);
+                }
+                zm = fmaxf(zm, z[i]);
             }
-            zm = fmaxf(zm, z[i]);
-        }
-        zref = warp_max(zref);
-        plogp = warp_sum(plogp);
-        used = __any_sync(0xFFFFFFFFu, used);
-        masked = __any_sync(0xFFFFFFFFu, masked);
-        zm = warp_max(zm);
-        float zmean = 0.0f, inside = 0.0f, total = 0.0f;
+            zref = warp_max(zref);
+            plogp = warp_sum(plogp);
+            used = __any_sync(0xFFFFFFFFu, used);
+            masked = __any_sync(0xFFFFFFFFu, masked);
+            zm = warp_max(zm);
+            total = 0.0f;
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            total += q[i];
-            if (q[i] > 0.0f && z[i] != F8_NEG_INF)
-                zmean = fmaf(q[i], z[i] - zref, zmean);
-            if (TAIL && first[i] && zm != F8_NEG_INF)
-                inside += ex2((z[i] - zm) * a.c);
+            for (int i = 0; i < N; ++i) {
+                total += q[i];
+                if (q[i] > 0.0f && z[i] != F8_NEG_INF)
+                    zmean = fmaf(q[i], z[i] - zref, zmean);
+                if (TAIL && first[i] && zm != F8_NEG_INF)
+                    inside += ex2((z[i] - zm) * a.c);
+            }
+            zmean = warp_sum(zmean);
+            total = TAIL ? sum : warp_sum(total);
+            if (TAIL)
+                inside = warp_sum(inside);
         }
-        zmean = warp_sum(zmean);
-        total = TAIL ? sum : warp_sum(total);
-        if (TAIL)
-            inside = warp_sum(inside);
         if (lane == 0) {
             s.used = used;
             s.masked = masked;
@@ -1726,10 +1544,440 @@ __device__ __forceinline__ void ring_slots(const DistillArgs &a, int64_t row, Ri
     }
     if (lane == 0) {
         s.any = any;
-        s.dloss = a.dloss[row];
+        s.dloss = a.dloss != nullptr ? a.dloss[row] : 0.0f;
     }
     __syncwarp();
 }
+
+// The first slot whose list a chunk has to look through, or -1.
+__device__ __forceinline__ int slot_list(const Slots &s, int ch)
+{
+    return s.head[static_cast<unsigned>(ch) % kHeads];
+}
+
+// -inf in the elements of chunk ch that a slot names.
+template <typename T>
+__device__ __forceinline__ void drop_slots(const Slots &s, const Row<T> &r, int ch,
+                                           float (&f)[Chunk<T>::E])
+{
+    constexpr int E = Chunk<T>::E;
+    for (int j = slot_list(s, ch); j >= 0; j = s.next[j]) {
+        const int d = s.id[j] + r.off - ch * E;
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            if (d == e)
+                f[e] = F8_NEG_INF;
+    }
+}
+
+// The same for U chunks c + u * N.
+template <typename T, int N, int U>
+__device__ __forceinline__ void drop_slots(const Slots &s, const Row<T> &r, int c, uint4 (&v)[U])
+{
+    int l[U], all = -1;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        l[u] = slot_list(s, c + u * N);
+        all &= l[u];
+    }
+    if (all < 0)  // no list: all are -1
+        return;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        if (l[u] >= 0) {
+            float f[Chunk<T>::E];
+            unpack<T>(v[u], f);
+            drop_slots(s, r, c + u * N, f);
+            v[u] = pack<T>(f);  // exact: the values are the chunk's own
+        }
+    }
+}
+
+// What the gradient of a row needs: scale (mass p - q) at the slots' ids,
+// scale dense p elsewhere.
+struct RowGrad {
+    Softmax p;
+    float scale, mass, dense;
+};
+
+template <typename T>
+__device__ __forceinline__ void slot_gradient(const Slots &s, const Row<T> &r, int ch,
+                                              const RowGrad &g, const float (&x)[Chunk<T>::E],
+                                              float (&f)[Chunk<T>::E])
+{
+    constexpr int E = Chunk<T>::E;
+    for (int j = slot_list(s, ch); j >= 0; j = s.next[j]) {
+        const int d = s.id[j] + r.off - ch * E;
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            if (d == e)
+                f[e] = g.scale * fmaf(g.mass, ex2(g.p.exponent(x[e])) * g.p.norm, -s.qsum[j]);
+    }
+}
+
+// The gradient of one chunk's elements, and of U chunks c + u * N.
+template <typename T>
+__device__ __forceinline__ void row_gradient(const Slots &s, const Row<T> &r, int ch,
+                                             const RowGrad &g, float (&x)[Chunk<T>::E])
+{
+    constexpr int E = Chunk<T>::E;
+    float f[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+        f[e] = g.scale * g.dense * (ex2(g.p.exponent(x[e])) * g.p.norm);
+    slot_gradient(s, r, ch, g, x, f);
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+        x[e] = f[e];
+}
+template <typename T, int N, int U>
+__device__ __forceinline__ void row_gradient(const Slots &s, const Row<T> &r, int c,
+                                             const RowGrad &g, const uint4 (&v)[U], uint4 (&out)[U])
+{
+    constexpr int E = Chunk<T>::E;
+    const float factor = g.scale * g.dense * g.p.norm;
+    int l[U], all = -1;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        l[u] = slot_list(s, c + u * N);
+        all &= l[u];
+        out[u] = scaled_softmax<T>(v[u], g.p, factor);
+    }
+    if (all < 0)
+        return;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        if (l[u] >= 0) {
+            float x[E], f[E];
+            unpack<T>(v[u], x);
+            unpack<T>(out[u], f);
+            slot_gradient(s, r, c + u * N, g, x, f);
+            out[u] = pack<T>(f);  // exact for the elements that stay
+        }
+    }
+}
+
+// The row's loss and gradient constants from its slots and its sums (TAIL:
+// over the tokens outside the slots' ids).
+struct RowLoss {
+    float loss, lse, rest;
+    RowGrad grad;
+    bool zero;  // no gradient
+};
+
+template <bool TAIL>
+__device__ __forceinline__ RowLoss row_loss(const DistillArgs &a, const Slots &s, const Stats &t)
+{
+    RowLoss o;
+    float m = t.m, outside = t.s, sum = t.s;
+    if (TAIL) {
+        m = fmaxf(t.m, s.zmax);
+        outside = t.s * ex2(fmaxf((t.m - m) * a.c, kFloor2));
+        sum = outside + s.inside * ex2(fmaxf((s.zmax - m) * a.c, kFloor2));
+    }
+    const bool bad = sum != sum || m == F8_POS_INF;
+    const bool none = !bad && sum == 0.0f;
+    const float inv_s = none ? 0.0f : (bad ? F8_NAN : 1.0f / sum);
+    const float ls = logf(sum);
+    o.lse = bad ? F8_NAN : (none ? F8_NEG_INF : fmaf(m, a.inv_t, ls));
+    o.rest = TAIL ? outside * inv_s : 0.0f;
+    o.loss = 0.0f;
+    if (s.used)
+        o.loss = s.masked || none ? F8_POS_INF
+                                  : s.plogp - s.zmean * a.inv_t +
+                                        s.qall * fmaf(m - s.zref, a.inv_t, ls);
+    if (TAIL && o.rest > 0.0f && s.left > 0.0f)
+        o.loss += s.left * (logf(s.left) - logf(o.rest));
+    if (bad || s.plogp != s.plogp || s.zmean != s.zmean)
+        o.loss = F8_NAN;
+    o.grad.p = Softmax{1.0f, m == F8_NEG_INF ? 0.0f : -m, a.c, inv_s};
+    o.grad.scale = s.dloss * a.inv_t;
+    o.grad.mass = o.grad.dense = s.total;
+    if (TAIL && o.rest > 0.0f) {
+        o.grad.mass = s.total + s.left;
+        o.grad.dense = o.grad.mass - s.left / (TAIL ? o.rest : 1.0f);
+    }
+    o.zero = s.dloss == 0.0f || none;
+    return o;
+}
+
+template <typename T, bool TAIL>
+__global__ void __launch_bounds__(kThreads)
+distill_fwd_kernel(const __grid_constant__ DistillArgs a)
+{
+    constexpr int E = Chunk<T>::E;
+    __shared__ __align__(16) Slots slots;
+    __shared__ Stats red[kWarps];
+    __shared__ Stats parts[kMaxCluster];
+    griddep_wait();
+    griddep_launch_dependents();
+    const int C = a.cluster;
+    const int64_t row = blockIdx.x / C;
+    const int rank = static_cast<int>(blockIdx.x % C);
+    const int tid = threadIdx.x;
+    const Row<T> r(static_cast<const T *>(a.logits), row, a.ld, a.vocab);
+    const int64_t total = (a.rows - 1) * a.ld + a.vocab;
+    if (C > 1)
+        cluster_start();
+    if (tid < 32)
+        warp_slots<T, TAIL, true>(a, row, slots);
+    __syncthreads();
+    if (!slots.any) {
+        if (C > 1)
+            cluster_started();
+        if (rank == 0 && tid == 0) {
+            a.loss[row] = 0.0f;
+            a.lse[row] = 0.0f;
+            if (TAIL)
+                a.rest[row] = 0.0f;
+        }
+        return;
+    }
+    const int per = (r.nch + C - 1) / C;
+    const int c0 = min(r.nch, rank * per), c1 = min(r.nch, c0 + per);
+    Stats t = stats_empty();
+    walk_chunks<T, kThreads, kUnroll>(r, max(c0, r.w0), min(c1, r.w1), total, a.status,
+                                      [&](uint4(&v)[kUnroll], int c) {
+                                          if (TAIL)
+                                              drop_slots<T, kThreads>(slots, r, c, v);
+                                          add_chunks<T, false>(t, v, a.c, 0.0f);
+                                      });
+    const int ec = r.edge(edge_of_thread(), c0, c1);
+    if (ec >= 0) {
+        float x[E];
+        load_edge(r, ec, x, total, a.status);
+        if (TAIL)
+            drop_slots(slots, r, ec, x);
+        add_values<false>(t, x, a.c);
+    }
+    t = block_join<false>(t, a.c, red);
+    if (C > 1) {
+        cluster_started();
+        if (tid == 0)
+            *peer(&parts[rank], 0) = t;
+        cluster_join();
+        if (rank != 0)
+            return;
+        t = parts[0];
+        for (int i = 1; i < C; ++i)
+            t = join<false>(t, parts[i], a.c);
+    }
+    if (tid == 0) {
+        const RowLoss o = row_loss<TAIL>(a, slots, t);
+        a.loss[row] = o.loss;
+        a.lse[row] = o.lse;
+        if (TAIL)
+            a.rest[row] = o.rest;
+        if (o.loss != o.loss)
+            atomicOr(a.status, kStatusNonfinite);
+    }
+}
+
+template <typename T, bool TAIL>
+__global__ void __launch_bounds__(kThreads)
+distill_bwd_kernel(const __grid_constant__ DistillArgs a)
+{
+    constexpr int E = Chunk<T>::E;
+    __shared__ __align__(16) Slots slots;
+    griddep_wait();
+    griddep_launch_dependents();
+    const int64_t row = blockIdx.x / a.blocks_per_row;
+    const int part = static_cast<int>(blockIdx.x % a.blocks_per_row);
+    const int tid = threadIdx.x;
+    const Row<T> r(static_cast<const T *>(a.logits), row, a.ld, a.vocab);
+    const int64_t total = (a.rows - 1) * a.ld + a.vocab;
+    const OutRow<T> o(a.out, a.rows, row, r);
+    if (tid < 32)
+        warp_slots<T, TAIL, false>(a, row, slots);
+    const float lse = a.lse[row];
+    const float rest = TAIL ? a.rest[row] : 0.0f;
+    __syncthreads();
+    RowGrad g{Softmax{a.inv_t, -lse, static_cast<float>(kLog2e), 1.0f}, slots.dloss * a.inv_t,
+              slots.total, slots.total};
+    if (TAIL && rest > 0.0f) {
+        g.mass = slots.total + slots.left;
+        g.dense = g.mass - slots.left / (TAIL ? rest : 1.0f);
+    }
+    uint32_t m2 = 0;
+    const bool amax = a.out.amax != nullptr;
+    const int c0 = part * kBwdChunks, c1 = min(r.nch, c0 + kBwdChunks);
+    const int wb = max(c0, r.w0), we = min(c1, r.w1);
+    if (!slots.any || slots.dloss == 0.0f || fabsf(lse) >= kMaxLse) {
+        zero_columns(o, max(static_cast<int64_t>(c0) * E - r.off, static_cast<int64_t>(0)),
+                     min(static_cast<int64_t>(c1) * E - r.off, static_cast<int64_t>(r.vocab)), tid,
+                     kThreads, a.status);
+    } else {
+        walk_chunks<T, kThreads, kUnroll>(r, wb, we, total, a.status, [&](uint4(&v)[kUnroll], int c) {
+            uint4 f[kUnroll];
+            row_gradient<T, kThreads>(slots, r, c, g, v, f);
+            store_chunks<T, kThreads>(r, o, c, we, f, amax, m2, a.status);
+        });
+        const int ec = r.edge(edge_of_thread(), c0, c1);
+        if (ec >= 0) {
+            float f[E];
+            load_edge(r, ec, f, total, a.status);
+            row_gradient(slots, r, ec, g, f);
+            store_elements(r, o, ec, f, m2, a.status);
+        }
+    }
+    if (part == a.blocks_per_row - 1)
+        zero_columns(o, r.vocab, a.out.ld, tid, kThreads, a.status);
+    block_amax(m2, a.out.amax, a.status);
+}
+
+// Loss and gradient together, for short rows and for few.  A block, or a cluster
+// of C blocks, takes a row, each thread holding up to kNV of its chunks in
+// registers between the two passes, so a row that fits is read once; a longer
+// one is walked in stretches and read again (from L2).
+constexpr int kNV = 8;
+
+template <typename T, bool TAIL>
+__global__ void __launch_bounds__(kThreads)
+distill_fused_kernel(const __grid_constant__ DistillArgs a)
+{
+    constexpr int E = Chunk<T>::E;
+    __shared__ __align__(16) Slots slots;
+    __shared__ Stats red[kWarps];
+    __shared__ Stats parts[kMaxCluster];
+    griddep_wait();
+    griddep_launch_dependents();
+    const int C = a.cluster;
+    const int64_t row = blockIdx.x / C;
+    const int rank = static_cast<int>(blockIdx.x % C);
+    const int tid = threadIdx.x;
+    const Row<T> r(static_cast<const T *>(a.logits), row, a.ld, a.vocab);
+    const int64_t total = (a.rows - 1) * a.ld + a.vocab;
+    const OutRow<T> o(a.out, a.rows, row, r);
+    if (C > 1)
+        cluster_start();
+    if (tid < 32)
+        warp_slots<T, TAIL, true>(a, row, slots);
+    __syncthreads();
+    const int per = (r.nch + C - 1) / C;
+    const int c0 = min(r.nch, rank * per), c1 = min(r.nch, c0 + per);
+    const int wb = max(c0, r.w0), we = min(c1, r.w1);  // this block's whole chunks
+    const int ec = r.edge(edge_of_thread(), c0, c1);
+    const bool amax = a.out.amax != nullptr;
+    uint32_t m2 = 0;
+    bool zero = true;
+    if (slots.any) {
+        uint4 v[kNV / kUnroll][kUnroll];
+        const bool fits = we - wb <= kNV * kThreads;
+        float edge[E];
+        Stats t = stats_empty();
+        if (ec >= 0) {
+            load_edge(r, ec, edge, total, a.status);
+            float x[E];
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                x[e] = edge[e];
+            if (TAIL)
+                drop_slots(slots, r, ec, x);
+            add_values<false>(t, x, a.c);
+        }
+        if (fits) {
+#pragma unroll
+            for (int h = 0; h < kNV / kUnroll; ++h)
+#pragma unroll
+                for (int u = 0; u < kUnroll; ++u)
+                    v[h][u] = load_chunk(r, wb + (h * kUnroll + u) * kThreads + tid, we, total,
+                                         a.status);
+#pragma unroll
+            for (int h = 0; h < kNV / kUnroll; ++h) {
+                const int c = wb + h * kUnroll * kThreads + tid;
+                if (c < we) {
+                    uint4 w[kUnroll];
+#pragma unroll
+                    for (int u = 0; u < kUnroll; ++u)
+                        w[u] = v[h][u];
+                    if (TAIL)
+                        drop_slots<T, kThreads>(slots, r, c, w);
+                    add_chunks<T, false>(t, w, a.c, 0.0f);
+                }
+            }
+        } else {
+            walk_chunks<T, kThreads, kUnroll>(r, wb, we, total, a.status,
+                                              [&](uint4(&w)[kUnroll], int c) {
+                                                  if (TAIL)
+                                                      drop_slots<T, kThreads>(slots, r, c, w);
+                                                  add_chunks<T, false>(t, w, a.c, 0.0f);
+                                              });
+        }
+        t = block_join<false>(t, a.c, red);
+        if (C > 1) {
+            cluster_started();
+            if (tid < C)
+                *peer(&parts[rank], tid) = t;
+            cluster_join();
+            t = parts[0];
+            for (int i = 1; i < C; ++i)
+                t = join<false>(t, parts[i], a.c);
+        }
+        const RowLoss l = row_loss<TAIL>(a, slots, t);
+        zero = l.zero;
+        if (rank == 0 && tid == 0) {
+            a.loss[row] = l.loss;
+            if (l.loss != l.loss)
+                atomicOr(a.status, kStatusNonfinite);
+        }
+        if (!zero) {
+            auto gradient = [&](const uint4(&w)[kUnroll], int c) {
+                uint4 f[kUnroll];
+                row_gradient<T, kThreads>(slots, r, c, l.grad, w, f);
+                store_chunks<T, kThreads>(r, o, c, we, f, amax, m2, a.status);
+            };
+            if (fits) {
+#pragma unroll
+                for (int h = 0; h < kNV / kUnroll; ++h)
+                    if (wb + h * kUnroll * kThreads + tid < we)
+                        gradient(v[h], wb + h * kUnroll * kThreads + tid);
+            } else {
+                walk_chunks<T, kThreads, kUnroll>(r, wb, we, total, a.status, gradient);
+            }
+            if (ec >= 0) {
+                row_gradient(slots, r, ec, l.grad, edge);
+                store_elements(r, o, ec, edge, m2, a.status);
+            }
+        }
+    } else {
+        if (C > 1)
+            cluster_started();
+        if (rank == 0 && tid == 0)
+            a.loss[row] = 0.0f;
+    }
+    if (zero)
+        zero_columns(o, max(static_cast<int64_t>(c0) * E - r.off, static_cast<int64_t>(0)),
+                     min(static_cast<int64_t>(c1) * E - r.off, static_cast<int64_t>(r.vocab)), tid,
+                     kThreads, a.status);
+    if (rank == C - 1)
+        zero_columns(o, r.vocab, a.out.ld, tid, kThreads, a.status);
+    block_amax(m2, a.out.amax, a.status);
+}
+
+// Loss and gradient together, for many long rows.  A row of the logits is
+// needed twice, for its sums and for its gradient, and the blocks of all SMs
+// together hold more than L2 does, so a block keeps what it can: one persistent
+// block per SM takes whole rows through a ring of 32 KB pieces in shared
+// memory that bulk copies fill.
+//   warp 16      reads the next row's slots (two buffers) and sums them up;
+//   warp 17      issues the copies: a row's pieces 0 .. n-1, then again those
+//                that the ring could not keep, then the next row's;
+//   warps 0..15  first pass: running sums over the pieces, releasing all but
+//                the last `keep`; the block's join (one barrier); second pass:
+//                the gradient of the kept pieces, then of those copied again
+//                (from L2, which they have just passed), released one by one.
+// The pieces are released in the order of their copies, so the ring is a queue
+// and the next row's copies run during the second pass.
+constexpr int kRingWarps = 16;
+constexpr int kRingConsumers = kRingWarps * 32;
+constexpr int kRingThreads = kRingConsumers + 64;
+constexpr int kPieceChunks = kUnroll * kRingConsumers;
+constexpr int kPieceBytes = kPieceChunks * 16;
+constexpr int kPieces = 6;
+constexpr int kKeep = 4;  // the other two are under way
+constexpr uint64_t kDrainLimitNs = 1000000000ull;
+
+constexpr size_t kRingSmem = static_cast<size_t>(kPieces) * kPieceBytes + 2 * sizeof(Slots);
 
 // Piece of position `seq` in the queue: its slot, and the parity of its phase.
 __device__ __forceinline__ int ring_slot(uint32_t seq) { return static_cast<int>(seq % kPieces); }
@@ -1748,7 +1996,7 @@ distill_ring_kernel(const __grid_constant__ DistillArgs a, uint64_t limit_ns)
     __shared__ Stats parts[2][kRingWarps];
     __shared__ int abort_word;
     volatile int *abort_flag = &abort_word;
-    RingSlots *slots = reinterpret_cast<RingSlots *>(pieces + static_cast<size_t>(kPieces) * kPieceBytes);
+    Slots *slots = reinterpret_cast<Slots *>(pieces + static_cast<size_t>(kPieces) * kPieceBytes);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
         for (int i = 0; i < kPieces; ++i) {
@@ -1774,6 +2022,7 @@ distill_ring_kernel(const __grid_constant__ DistillArgs a, uint64_t limit_ns)
         return false;
     };
     uint32_t m2 = 0;
+    const bool amax = a.out.amax != nullptr;
 
     if (warp == kRingWarps) {
         // ---------------------------------------------------- the rows' slots
@@ -1783,7 +2032,7 @@ distill_ring_kernel(const __grid_constant__ DistillArgs a, uint64_t limit_ns)
             const bool ok = wait(&sempty[b], ((i >> 1) & 1) ^ 1u);
             if (!__all_sync(0xFFFFFFFFu, ok))
                 break;
-            ring_slots<T, TAIL>(a, row, slots[b]);
+            warp_slots<T, TAIL, true>(a, row, slots[b]);
             if (lane == 0)
                 mbar_arrive(&sfull[b]);
         }
@@ -1836,7 +2085,7 @@ distill_ring_kernel(const __grid_constant__ DistillArgs a, uint64_t limit_ns)
         for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, ++i) {
             const int b = i & 1;
             alive = alive && __all_sync(0xFFFFFFFFu, wait(&sfull[b], (i >> 1) & 1));
-            const RingSlots &s = slots[b];
+            const Slots &s = slots[b];
             const bool any = alive && s.any != 0;
             const Row<T> r(static_cast<const T *>(a.logits), row, a.ld, a.vocab);
             const int n = r.w1 - r.w0;
@@ -1850,29 +2099,26 @@ distill_ring_kernel(const __grid_constant__ DistillArgs a, uint64_t limit_ns)
                 if (lane == 0)
                     mbar_arrive(&empty[ring_slot(q)]);
             };
-            // this thread's chunk u of a piece
-            auto chunk = [&](uint32_t q, int piece, int u) {
-                const int c = u * kRingConsumers + tid;
-                uint4 v = neg_inf_chunk(T());
-                if (piece * kPieceChunks + c < n)
-                    v = reinterpret_cast<const uint4 *>(pieces + ring_slot(q) * kPieceBytes)[c];
-                return v;
+            // this thread's chunks of a piece, -inf past the row's last whole one
+            auto take = [&](uint32_t q, int piece, uint4(&v)[kUnroll]) {
+                const uint4 *p = reinterpret_cast<const uint4 *>(pieces + ring_slot(q) * kPieceBytes);
+                const int left = n - piece * kPieceChunks - tid;
+#pragma unroll
+                for (int u = 0; u < kUnroll; ++u) {
+                    v[u] = neg_inf_chunk(T());
+                    if (u * kRingConsumers < left)
+                        v[u] = p[u * kRingConsumers + tid];
+                }
             };
             Stats t = stats_empty();
             for (int j = 0; j < np; ++j) {
                 arrived(seq + j);
-                uint4 v[kPerThread];
-#pragma unroll
-                for (int u = 0; u < kPerThread; ++u)
-                    v[u] = chunk(seq + j, j, u);
+                uint4 v[kUnroll];
+                take(seq + j, j, v);
                 if (j < again)
                     release(seq + j);
-                if (TAIL) {
-#pragma unroll
-                    for (int u = 0; u < kPerThread; ++u)
-                        v[u] = without_slots(
-                            s, r, r.w0 + j * kPieceChunks + u * kRingConsumers + tid, v[u]);
-                }
+                if (TAIL)
+                    drop_slots<T, kRingConsumers>(s, r, r.w0 + j * kPieceChunks + tid, v);
                 add_chunks<T, false>(t, v, a.c, 0.0f);
             }
             const int ec = any ? r.edge(edge_of_thread(), 0, r.nch) : -1;
@@ -1888,118 +2134,51 @@ distill_ring_kernel(const __grid_constant__ DistillArgs a, uint64_t limit_ns)
                 add_values<false>(t, x, a.c);
             }
             // the block's sums: warps' in shared memory, two sets in turn
-            const float c = a.c;
-            t = warp_stats(t, c);
+            t = warp_stats(t, a.c);
             if (lane == 0)
                 parts[b][warp] = t;
             asm volatile("bar.sync 1, %0;" ::"n"(kRingConsumers) : "memory");
             t = parts[b][lane & (kRingWarps - 1)];
-            t = warp_stats_16(t, c);
+            t = warp_stats_16(t, a.c);
 
-            T *out = static_cast<T *>(a.out.p) + row * a.out.ld;
-            const int64_t out_at = row * a.out.ld, out_total = a.rows * a.out.ld;
-            const bool same = same_offset(r, out);
+            const OutRow<T> o(a.out, a.rows, row, r);
+            bool zero = true;
             if (any) {
-                float m = t.m, outside = t.s, sum = t.s, rest = 0.0f;
-                if (TAIL) {
-                    m = fmaxf(t.m, s.zmax);
-                    outside = t.s * ex2(fmaxf((t.m - m) * c, kFloor2));
-                    sum = outside + s.inside * ex2(fmaxf((s.zmax - m) * c, kFloor2));
-                }
-                const bool bad = sum != sum || m == F8_POS_INF;
-                const bool none = !bad && sum == 0.0f;
-                const float inv_s = none ? 0.0f : (bad ? F8_NAN : 1.0f / sum);
-                if (TAIL)
-                    rest = outside * inv_s;
+                const RowLoss l = row_loss<TAIL>(a, s, t);
+                zero = l.zero;
                 if (tid == 0) {
-                    float loss = 0.0f;
-                    if (s.used) {
-                        loss = s.masked || none
-                                   ? F8_POS_INF
-                                   : s.plogp - s.zmean * a.inv_t +
-                                         s.qall * fmaf(m - s.zref, a.inv_t, logf(sum));
-                    }
-                    if (TAIL && rest > 0.0f && s.left > 0.0f)
-                        loss += s.left * (logf(s.left) - logf(rest));
-                    if (bad || s.plogp != s.plogp || s.zmean != s.zmean)
-                        loss = F8_NAN;
-                    a.loss[row] = loss;
-                    if (loss != loss)
+                    a.loss[row] = l.loss;
+                    if (l.loss != l.loss)
                         atomicOr(a.status, kStatusNonfinite);
                 }
-                float mass = s.total, dense = s.total;
-                if (TAIL && rest > 0.0f) {
-                    mass = s.total + s.left;
-                    dense = mass - s.left / rest;
-                }
-                const bool zero = s.dloss == 0.0f || none;
-                const float scale = zero ? 0.0f : s.dloss * a.inv_t;
-                const float mm = m == F8_NEG_INF ? 0.0f : m;
-                const float2 nm = make_float2(-mm, -mm), c2 = make_float2(c, c);
-                const float fac = zero ? 0.0f : scale * dense * inv_s;
-                const float2 f2 = make_float2(fac, fac);
-                // the gradient of chunk ch in place of its logits
-                auto gradient = [&](int ch, float (&f)[E]) {
-                    if (zero) {
-#pragma unroll
-                        for (int e = 0; e < E; ++e)
-                            f[e] = 0.0f;
-                        return;
-                    }
-                    float p[E];
-#pragma unroll
-                    for (int e = 0; e < E; e += 2) {
-                        const float2 d =
-                            __fmul2_rn(__fadd2_rn(make_float2(f[e], f[e + 1]), nm), c2);
-                        const float2 x = make_float2(ex2(d.x), ex2(d.y));
-                        p[e] = x.x;
-                        p[e + 1] = x.y;
-                        const float2 g = __fmul2_rn(x, f2);
-                        f[e] = g.x;
-                        f[e + 1] = g.y;
-                    }
-                    if (s.head[ch % kHeads] >= 0) {
-#pragma unroll
-                        for (int e = 0; e < E; ++e)
-                            p[e] *= inv_s;
-                        slot_gradient(s, r, ch, p, scale, mass, f);
-                    }
-                };
                 // the kept pieces, then the first ones again
                 for (int j = 0; j < np; ++j) {
                     const int piece = j < keep ? again + j : j - keep;
                     const uint32_t q = seq + again + j;
                     if (j >= keep)
                         arrived(q);
-                    uint4 v[kPerThread];
-#pragma unroll
-                    for (int u = 0; u < kPerThread; ++u)
-                        v[u] = chunk(q, piece, u);
+                    uint4 v[kUnroll], f[kUnroll];
+                    take(q, piece, v);
                     release(q);
-#pragma unroll
-                    for (int u = 0; u < kPerThread; ++u) {
-                        const int k = piece * kPieceChunks + u * kRingConsumers + tid;
-                        if (k < n) {
-                            float f[E];
-                            unpack<T>(v[u], f);
-                            gradient(r.w0 + k, f);
-                            m2 = __vmaxu2(m2, store_chunk(r, out, same, r.w0 + k, f, out_at,
-                                                          out_total, a.status));
-                        }
+                    const int c = r.w0 + piece * kPieceChunks + tid;
+                    if (!zero) {
+                        row_gradient<T, kRingConsumers>(s, r, c, l.grad, v, f);
+                        store_chunks<T, kRingConsumers>(r, o, c, r.w1, f, amax, m2, a.status);
                     }
                 }
-                if (ec >= 0) {
-                    gradient(ec, edge);
-                    m2 = __vmaxu2(m2, store_elements(r, out, ec, edge, out_at, out_total, a.status));
+                if (ec >= 0 && !zero) {
+                    row_gradient(s, r, ec, l.grad, edge);
+                    store_elements(r, o, ec, edge, m2, a.status);
                 }
                 seq += np + again;
-            } else if (alive) {
-                if (tid == 0)
-                    a.loss[row] = 0.0f;
-                zero_columns(out, 0, r.vocab, out_at, out_total, a.status, tid, kRingConsumers);
+            } else if (alive && tid == 0) {
+                a.loss[row] = 0.0f;
             }
-            if (alive)
-                zero_columns(out, r.vocab, a.out.ld, out_at, out_total, a.status, tid, kRingConsumers);
+            if (alive) {
+                if (zero)
+                    zero_columns(o, 0, r.vocab, tid, kRingConsumers, a.status);
+                zero_columns(o, r.vocab, a.out.ld, tid, kRingConsumers, a.status);
+            }
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(&sempty[b]);
@@ -2263,6 +2442,7 @@ f8_status f8_token_logprobs_bwd(const void *logits, f8_dtype type, int64_t rows,
     a.dlogp = dlogp;
     a.dentropy = dentropy;
     a.inv_t = 1.0f / temperature;
+    a.t = temperature;
     a.out = OutArgs{dlogits, ldd, reinterpret_cast<unsigned *>(amax_out)};
     a.status = dev->status;
     return from_cuda(type == F8_BF16 ? logprobs_bwd<__nv_bfloat16>(a, *dev, st)
