@@ -631,24 +631,13 @@ __device__ __forceinline__ void block_select(const uint32_t *keys, int n, int k,
     __syncthreads();
 }
 
-// The k-th largest of n > k keys in shared memory, by seven pivots a round: the
-// largest t with at least k keys >= t, or a lower one with exactly k.  `cnt`:
-// three sets of eight counters, zero at the start and at the end.
-__device__ __forceinline__ uint32_t block_threshold(const uint32_t *keys, int n, int k, int *red,
-                                                    int *cnt)
+// The k-th largest of the block's keys, one per thread (k <= kThreads), by seven
+// pivots a round: the largest t with at least k keys >= t, or a lower one with
+// exactly k.  `cnt`: three sets of eight counters, zero at the start.
+__device__ __forceinline__ uint32_t block_threshold(uint32_t key, int k, int *red, int *cnt)
 {
     const int tid = threadIdx.x, lane = tid & 31;
-    uint32_t lo = 0xFFFFFFFFu, hi = 0;
-    for (int i = tid; i < n; i += kThreads) {
-        lo = min(lo, keys[i]);
-        hi = max(hi, keys[i]);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        lo = min(lo, __shfl_xor_sync(0xFFFFFFFFu, lo, o));
-        hi = max(hi, __shfl_xor_sync(0xFFFFFFFFu, hi, o));
-    }
-    __syncthreads();
+    uint32_t lo = __reduce_min_sync(0xFFFFFFFFu, key), hi = __reduce_max_sync(0xFFFFFFFFu, key);
     if (lane == 0) {
         red[tid >> 5] = static_cast<int>(lo);
         red[kWarps + (tid >> 5)] = static_cast<int>(hi);
@@ -663,49 +652,30 @@ __device__ __forceinline__ uint32_t block_threshold(const uint32_t *keys, int n,
     int set = 0;
     while (lo < hi) {
         const uint32_t step = (hi - lo) / 8 + 1;
-        uint32_t pivot[7];
-#pragma unroll
-        for (int p = 0; p < 7; ++p)  // past hi: nothing to count
-            pivot[p] = (hi - lo) / step >= p + 1u ? lo + (p + 1) * step : 0xFFFFFFFFu;
-        int c[7] = {0, 0, 0, 0, 0, 0, 0};
-        for (int i0 = 0; i0 < n; i0 += kThreads) {
-            const uint32_t key = i0 + tid < n ? keys[i0 + tid] : 0u;
-#pragma unroll
-            for (int p = 0; p < 7; ++p)
-                c[p] += __popc(__ballot_sync(0xFFFFFFFFu, key >= pivot[p]));
-        }
+        const int pivots = static_cast<int>((hi - lo) / step);  // those up to hi, 1 .. 7
         int mine = 0;
 #pragma unroll
-        for (int p = 0; p < 7; ++p)
-            mine = lane == p ? c[p] : mine;
-        if (lane < 7 && mine > 0)
+        for (int p = 0; p < 7; ++p) {
+            const int c = __popc(__ballot_sync(0xFFFFFFFFu, key >= lo + (p + 1) * step));
+            mine = lane == p ? c : mine;
+        }
+        if (lane < pivots && mine > 0)
             atomicAdd(&cnt[8 * set + lane], mine);
         const int next = set == 2 ? 0 : set + 1;
         if (tid < 8)
             cnt[8 * next + tid] = 0;
         __syncthreads();
-        uint32_t nlo = lo, nhi = min(hi, pivot[0] - 1);
-        int at = 0;
-#pragma unroll
-        for (int p = 0; p < 7; ++p) {
-            const bool in = (hi - lo) / step >= p + 1u;
-            const int have = cnt[8 * set + p];
-            if (in && have >= k) {
-                nlo = pivot[p];
-                nhi = p == 6 || (hi - lo) / step < p + 2u ? hi : pivot[p < 6 ? p + 1 : 6] - 1;
-                at = have;
-            }
-        }
-        lo = nlo;
-        hi = nhi;
+        // the last pivot that at least k keys reach
+        const int have = lane < pivots ? cnt[8 * set + lane] : 0;
+        const int above = __popc(__ballot_sync(0xFFFFFFFFu, have >= k));
+        const int at = __shfl_sync(0xFFFFFFFFu, have, above > 0 ? above - 1 : 0);
+        if (above < pivots)
+            hi = lo + (above + 1) * step - 1;
+        lo += above * step;
         set = next;
-        if (at == k)
+        if (above > 0 && at == k)
             break;
     }
-    __syncthreads();
-    if (tid < 24)
-        cnt[tid] = 0;
-    __syncthreads();
     return lo;
 }
 
@@ -734,21 +704,22 @@ __host__ __device__ inline TopLayout top_layout(int ngroups, int k, int cluster)
 }
 
 // The k largest elements of chunks [32 g0, 32 g1) of a row, in order, in
-// best_key / best_id of `lay`; gkeys holds the groups' largest keys.  Every
-// element among the k largest is >= the k-th largest maximum of any k or more
-// disjoint parts of the row.  So: the threshold over the groups' maxima (over
-// the chunks' where there are too few groups), a look at the parts that reach
-// it, and their elements >= it ranked against one another.  Where many values
-// are equal to the threshold or one part holds very many large ones, the
-// candidates may not fit; then parts are chosen exactly (k parts hold all, by
-// maximum and position), groups, chunks, elements in turn.
+// best_key / best_id of `lay`; gkeys holds the groups' largest keys, tkey the
+// key of the largest element that this thread has seen.  The k-th largest of
+// the threads' is no larger than the k-th largest element, so: that threshold,
+// a look at the groups that reach it, and their elements >= it ranked against
+// one another.  Where many values are equal to the threshold, fewer than k
+// threads have seen any, or some have seen very many large ones, the candidates
+// may not fit; then parts are chosen exactly (k parts hold all, by maximum and
+// position), groups, chunks, elements in turn.
 template <typename T>
 __device__ __forceinline__ void block_top(const Row<T> &r, int g0, int g1, int k, int have,
-                                          uint32_t *dyn, const TopLayout &lay, int *red, int *cnt,
-                                          int *ncand, int64_t total, unsigned *status)
+                                          uint32_t tkey, uint32_t *dyn, const TopLayout &lay,
+                                          int *red, int *cnt, int *ncand, int64_t total,
+                                          unsigned *status)
 {
     constexpr int E = Chunk<T>::E;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, lane = tid & 31;
     uint32_t *gkeys = dyn + lay.groups, *keys = dyn + lay.keys;
     uint32_t *ck = dyn + lay.cand_key, *bk = dyn + lay.best_key;
     int *ci = reinterpret_cast<int *>(dyn + lay.cand_id);
@@ -764,7 +735,7 @@ __device__ __forceinline__ void block_top(const Row<T> &r, int g0, int g1, int k
     auto offer = [&](int ch, uint32_t t) {
         float x[E];
         load(ch, x);
-        if (order_key(max_of(x)) < t && t > 1)
+        if (order_key(max_of(x)) < t)
             return;
 #pragma unroll
         for (int e = 0; e < E; ++e) {
@@ -779,9 +750,9 @@ __device__ __forceinline__ void block_top(const Row<T> &r, int g0, int g1, int k
             }
         }
     };
-    auto chunk_keys = [&](const int *groups, int n) {  // of n groups (all from g0 if groups is null)
+    auto chunk_keys = [&](const int *groups, int n) {
         for (int i = tid; i < n * 32; i += kThreads) {
-            const int ch = (g0 + (groups != nullptr ? groups[i >> 5] : i >> 5)) * 32 + (i & 31);
+            const int ch = (g0 + groups[i >> 5]) * 32 + (i & 31);
             uint32_t key = 0;
             if (ch < r.nch) {
                 float x[E];
@@ -792,20 +763,14 @@ __device__ __forceinline__ void block_top(const Row<T> &r, int g0, int g1, int k
         }
         __syncthreads();
     };
-    if (ng > k) {
-        const uint32_t t = block_threshold(gkeys, ng, k, red, cnt);
-        for (int g = warp; g < ng; g += kWarps) {
-            const int ch = (g0 + g) * 32 + lane;
-            if (gkeys[g] >= t && ch < r.nch)
+    const uint32_t t = block_threshold(tkey, k, red, cnt);
+    for (int i = tid - lane; i < ng; i += kThreads) {  // a lane asks for a group, its warp looks at it
+        unsigned reach = __ballot_sync(0xFFFFFFFFu, i + lane < ng && gkeys[i + lane] >= t);
+        for (; reach != 0; reach &= reach - 1) {
+            const int ch = (g0 + i + __ffs(reach) - 1) * 32 + lane;
+            if (ch < r.nch)
                 offer(ch, t);
         }
-    } else {
-        chunk_keys(nullptr, ng);
-        const int nch = min(32 * ng, r.nch - 32 * g0);
-        const uint32_t t = nch > k ? block_threshold(keys, nch, k, red, cnt) : 1u;
-        for (int i = tid; i < nch; i += kThreads)
-            if (keys[i] >= t)
-                offer(g0 * 32 + i, t);
     }
     __syncthreads();
     int n = *ncand;
@@ -964,13 +929,14 @@ logprobs_kernel(const __grid_constant__ LogprobArgs a)
         if (ec >= 0)
             atomicMax(&gkeys[ec / 32 - g0], order_key(edge_max));
     }
+    const uint32_t tkey = order_key(t.m);
     t = block_join<true>(t, a.c, red);
 
     if (TOP) {
         const int k = a.top_k;
         const int v0 = g0 * 32 * E - r.off, v1 = min(g1 * 32 * E - r.off, r.vocab);
         const int have = max(0, min(k, v1 - max(v0, 0)));
-        block_top<T>(r, g0, g1, k, have, dyn, lay, sred, cnt, &ncand, total, a.status);
+        block_top<T>(r, g0, g1, k, have, tkey, dyn, lay, sred, cnt, &ncand, total, a.status);
         if (C > 1) {  // into the leader's merge arrays
             cluster_started();
             uint32_t *mk = peer(dyn + lay.merge_key + rank * k, 0);
@@ -1349,14 +1315,18 @@ struct DistillArgs {
     unsigned *status;
 };
 
-// The row's slots in shared memory.  A table keyed by chunk number finds the
-// slots that name an element of a chunk: head[chunk % kHeads] starts a list
-// of slots.  Slots of equal ids each carry their summed q.  The sums over the
-// slots are all that the loss needs of them:
+// The row's slots in shared memory.  Which chunks a slot names an element of is
+// one bit each in `named` (exact up to 2^19 bf16 tokens, beyond that one bit
+// for several chunks): a warp asks it for every chunk, and a filter with many
+// false hits would send nearly every warp through the lists.  head[chunk %
+// kHeads] then starts the list of slots.  Slots of equal ids each carry their
+// summed q.  The sums over the slots are all that the loss needs of them:
 //   loss = sum q log q - sum q (z - zref) / T + sum q ((max - zref) / T + ln S)
 // for the row's maximum and S = sum e^((x - max) / T).
-constexpr int kHeads = 2048;
-struct Slots {
+constexpr int kHeads = 256;
+constexpr int kNamedWords = 2048;
+struct alignas(16) Slots {
+    uint32_t named[kNamedWords];
     int head[kHeads];
     int next[F8_MAX_TOP];
     int id[F8_MAX_TOP];      // -1: empty
@@ -1365,7 +1335,9 @@ struct Slots {
     int any;        // the row has a slot
     int used;       // some slot has q > 0
     int masked;     // such a slot names a masked token
+    int skip;       // (backward) no gradient, whatever the logits
     float dloss;
+    float lse, rest;  // (backward)
     float total;    // sum q (1 without the tail class)
     float qall;     // sum q as it came out
     float left;     // q_r
@@ -1405,6 +1377,8 @@ __device__ __forceinline__ void warp_slots(const DistillArgs &a, int64_t row, Sl
     constexpr int N = F8_MAX_TOP / 32;
     const int lane = threadIdx.x & 31, k = a.k;
     const Row<T> r(static_cast<const T *>(a.logits), row, a.ld, a.vocab);
+    for (int i = lane; i < kNamedWords / 4; i += 32)
+        reinterpret_cast<uint4 *>(s.named)[i] = make_uint4(0, 0, 0, 0);
     for (int i = lane; i < kHeads / 4; i += 32)
         reinterpret_cast<int4 *>(s.head)[i] = make_int4(-1, -1, -1, -1);
     int id[N];
@@ -1470,9 +1444,11 @@ __device__ __forceinline__ void warp_slots(const DistillArgs &a, int64_t row, Sl
         __syncwarp();
 #pragma unroll
         for (int i = 0; i < N; ++i)
-            if (id[i] >= 0)
-                s.next[lane + 32 * i] =
-                    atomicExch(&s.head[((id[i] + r.off) / Chunk<T>::E) % kHeads], lane + 32 * i);
+            if (id[i] >= 0) {
+                const int ch = (id[i] + r.off) / Chunk<T>::E;
+                s.next[lane + 32 * i] = atomicExch(&s.head[ch % kHeads], lane + 32 * i);
+                atomicOr(&s.named[(ch >> 5) % kNamedWords], 1u << (ch & 31));
+            }
         __syncwarp();
         bool first[N];
 #pragma unroll
@@ -1545,14 +1521,26 @@ __device__ __forceinline__ void warp_slots(const DistillArgs &a, int64_t row, Sl
     if (lane == 0) {
         s.any = any;
         s.dloss = a.dloss != nullptr ? a.dloss[row] : 0.0f;
+        if (!LOSS) {
+            s.lse = a.lse[row];
+            s.rest = TAIL ? a.rest[row] : 0.0f;
+            s.skip = s.dloss == 0.0f || fabsf(s.lse) >= kMaxLse;
+        }
     }
     __syncwarp();
 }
 
-// The first slot whose list a chunk has to look through, or -1.
-__device__ __forceinline__ int slot_list(const Slots &s, int ch)
+// Which of chunks c + u * N a slot names an element of, as bits u; N a multiple
+// of 32.
+template <int N, int U>
+__device__ __forceinline__ uint32_t named_bits(const Slots &s, int c)
 {
-    return s.head[static_cast<unsigned>(ch) % kHeads];
+    uint32_t bits = 0;
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+        bits |= ((s.named[static_cast<unsigned>((c >> 5) + u * (N / 32)) % kNamedWords] >> (c & 31)) & 1u)
+                << u;
+    return bits;
 }
 
 // -inf in the elements of chunk ch that a slot names.
@@ -1561,7 +1549,7 @@ __device__ __forceinline__ void drop_slots(const Slots &s, const Row<T> &r, int 
                                            float (&f)[Chunk<T>::E])
 {
     constexpr int E = Chunk<T>::E;
-    for (int j = slot_list(s, ch); j >= 0; j = s.next[j]) {
+    for (int j = s.head[static_cast<unsigned>(ch) % kHeads]; j >= 0; j = s.next[j]) {
         const int d = s.id[j] + r.off - ch * E;
 #pragma unroll
         for (int e = 0; e < E; ++e)
@@ -1574,17 +1562,12 @@ __device__ __forceinline__ void drop_slots(const Slots &s, const Row<T> &r, int 
 template <typename T, int N, int U>
 __device__ __forceinline__ void drop_slots(const Slots &s, const Row<T> &r, int c, uint4 (&v)[U])
 {
-    int l[U], all = -1;
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-        l[u] = slot_list(s, c + u * N);
-        all &= l[u];
-    }
-    if (all < 0)  // no list: all are -1
+    const uint32_t named = named_bits<N, U>(s, c);
+    if (named == 0)
         return;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        if (l[u] >= 0) {
+        if (named >> u & 1u) {
             float f[Chunk<T>::E];
             unpack<T>(v[u], f);
             drop_slots(s, r, c + u * N, f);
@@ -1606,7 +1589,7 @@ __device__ __forceinline__ void slot_gradient(const Slots &s, const Row<T> &r, i
                                               float (&f)[Chunk<T>::E])
 {
     constexpr int E = Chunk<T>::E;
-    for (int j = slot_list(s, ch); j >= 0; j = s.next[j]) {
+    for (int j = s.head[static_cast<unsigned>(ch) % kHeads]; j >= 0; j = s.next[j]) {
         const int d = s.id[j] + r.off - ch * E;
 #pragma unroll
         for (int e = 0; e < E; ++e)
@@ -1636,18 +1619,15 @@ __device__ __forceinline__ void row_gradient(const Slots &s, const Row<T> &r, in
 {
     constexpr int E = Chunk<T>::E;
     const float factor = g.scale * g.dense * g.p.norm;
-    int l[U], all = -1;
+    const uint32_t named = named_bits<N, U>(s, c);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-        l[u] = slot_list(s, c + u * N);
-        all &= l[u];
+    for (int u = 0; u < U; ++u)
         out[u] = scaled_softmax<T>(v[u], g.p, factor);
-    }
-    if (all < 0)
+    if (named == 0)
         return;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        if (l[u] >= 0) {
+        if (named >> u & 1u) {
             float x[E], f[E];
             unpack<T>(v[u], x);
             unpack<T>(out[u], f);
@@ -1655,6 +1635,19 @@ __device__ __forceinline__ void row_gradient(const Slots &s, const Row<T> &r, in
             out[u] = pack<T>(f);  // exact for the elements that stay
         }
     }
+}
+
+// The constants of the backward pass from the given lse and p_r.
+template <bool TAIL>
+__device__ __forceinline__ RowGrad row_grad(const DistillArgs &a, const Slots &s)
+{
+    RowGrad g{Softmax{a.inv_t, -s.lse, static_cast<float>(kLog2e), 1.0f}, s.dloss * a.inv_t, s.total,
+              s.total};
+    if (TAIL && s.rest > 0.0f) {
+        g.mass = s.total + s.left;
+        g.dense = g.mass - s.left / s.rest;
+    }
+    return g;
 }
 
 // The row's loss and gradient constants from its slots and its sums (TAIL:
@@ -1789,20 +1782,13 @@ distill_bwd_kernel(const __grid_constant__ DistillArgs a)
     const OutRow<T> o(a.out, a.rows, row, r);
     if (tid < 32)
         warp_slots<T, TAIL, false>(a, row, slots);
-    const float lse = a.lse[row];
-    const float rest = TAIL ? a.rest[row] : 0.0f;
     __syncthreads();
-    RowGrad g{Softmax{a.inv_t, -lse, static_cast<float>(kLog2e), 1.0f}, slots.dloss * a.inv_t,
-              slots.total, slots.total};
-    if (TAIL && rest > 0.0f) {
-        g.mass = slots.total + slots.left;
-        g.dense = g.mass - slots.left / (TAIL ? rest : 1.0f);
-    }
+    const RowGrad g = row_grad<TAIL>(a, slots);
     uint32_t m2 = 0;
     const bool amax = a.out.amax != nullptr;
     const int c0 = part * kBwdChunks, c1 = min(r.nch, c0 + kBwdChunks);
     const int wb = max(c0, r.w0), we = min(c1, r.w1);
-    if (!slots.any || slots.dloss == 0.0f || fabsf(lse) >= kMaxLse) {
+    if (!slots.any || slots.skip) {
         zero_columns(o, max(static_cast<int64_t>(c0) * E - r.off, static_cast<int64_t>(0)),
                      min(static_cast<int64_t>(c1) * E - r.off, static_cast<int64_t>(r.vocab)), tid,
                      kThreads, a.status);
@@ -1968,6 +1954,8 @@ distill_fused_kernel(const __grid_constant__ DistillArgs a)
 //                (from L2, which they have just passed), released one by one.
 // The pieces are released in the order of their copies, so the ring is a queue
 // and the next row's copies run during the second pass.
+// BWD is the backward pass alone, with lse (and p_r) given: the second pass
+// only, over every piece once.
 constexpr int kRingWarps = 16;
 constexpr int kRingConsumers = kRingWarps * 32;
 constexpr int kRingThreads = kRingConsumers + 64;
@@ -1983,7 +1971,7 @@ constexpr size_t kRingSmem = static_cast<size_t>(kPieces) * kPieceBytes + 2 * si
 __device__ __forceinline__ int ring_slot(uint32_t seq) { return static_cast<int>(seq % kPieces); }
 __device__ __forceinline__ uint32_t ring_parity(uint32_t seq) { return (seq / kPieces) & 1u; }
 
-template <typename T, bool TAIL>
+template <typename T, bool TAIL, bool BWD>
 __global__ void __launch_bounds__(kRingThreads, 1)
 distill_ring_kernel(const __grid_constant__ DistillArgs a, uint64_t limit_ns)
 {
@@ -2032,7 +2020,7 @@ distill_ring_kernel(const __grid_constant__ DistillArgs a, uint64_t limit_ns)
             const bool ok = wait(&sempty[b], ((i >> 1) & 1) ^ 1u);
             if (!__all_sync(0xFFFFFFFFu, ok))
                 break;
-            warp_slots<T, TAIL, true>(a, row, slots[b]);
+            warp_slots<T, TAIL, !BWD>(a, row, slots[b]);
             if (lane == 0)
                 mbar_arrive(&sfull[b]);
         }
@@ -2048,14 +2036,14 @@ distill_ring_kernel(const __grid_constant__ DistillArgs a, uint64_t limit_ns)
                     stop = true;
                     break;
                 }
-                const bool any = slots[b].any != 0;
+                const bool any = slots[b].any != 0 && !(BWD && slots[b].skip);
                 mbar_arrive(&sempty[b]);
                 if (!any)
                     continue;
                 const Row<T> r(static_cast<const T *>(a.logits), row, a.ld, a.vocab);
                 const int n = r.w1 - r.w0;
                 const int np = (n + kPieceChunks - 1) / kPieceChunks;
-                const int again = np - min(np, kKeep);
+                const int again = BWD ? 0 : np - min(np, kKeep);
                 for (int j = 0; j < np + again; ++j, ++seq) {
                     const int piece = j < np ? j : j - np;
                     const int slot = ring_slot(seq);
@@ -2086,11 +2074,11 @@ distill_ring_kernel(const __grid_constant__ DistillArgs a, uint64_t limit_ns)
             const int b = i & 1;
             alive = alive && __all_sync(0xFFFFFFFFu, wait(&sfull[b], (i >> 1) & 1));
             const Slots &s = slots[b];
-            const bool any = alive && s.any != 0;
+            const bool any = alive && s.any != 0 && !(BWD && s.skip);
             const Row<T> r(static_cast<const T *>(a.logits), row, a.ld, a.vocab);
             const int n = r.w1 - r.w0;
             const int np = any ? (n + kPieceChunks - 1) / kPieceChunks : 0;
-            const int keep = min(np, kKeep), again = np - keep;
+            const int keep = BWD ? 0 : min(np, kKeep), again = BWD ? 0 : np - keep;
             auto arrived = [&](uint32_t q) {
                 alive = alive && __all_sync(0xFFFFFFFFu, wait(&full[ring_slot(q)], ring_parity(q)));
             };
@@ -2102,54 +2090,70 @@ distill_ring_kernel(const __grid_constant__ DistillArgs a, uint64_t limit_ns)
             // this thread's chunks of a piece, -inf past the row's last whole one
             auto take = [&](uint32_t q, int piece, uint4(&v)[kUnroll]) {
                 const uint4 *p = reinterpret_cast<const uint4 *>(pieces + ring_slot(q) * kPieceBytes);
-                const int left = n - piece * kPieceChunks - tid;
+                const int left = n - piece * kPieceChunks;
+                if (left >= kPieceChunks) {
 #pragma unroll
-                for (int u = 0; u < kUnroll; ++u) {
-                    v[u] = neg_inf_chunk(T());
-                    if (u * kRingConsumers < left)
+                    for (int u = 0; u < kUnroll; ++u)
                         v[u] = p[u * kRingConsumers + tid];
+                } else {
+#pragma unroll
+                    for (int u = 0; u < kUnroll; ++u) {
+                        v[u] = neg_inf_chunk(T());
+                        if (u * kRingConsumers + tid < left)
+                            v[u] = p[u * kRingConsumers + tid];
+                    }
                 }
             };
-            Stats t = stats_empty();
-            for (int j = 0; j < np; ++j) {
-                arrived(seq + j);
-                uint4 v[kUnroll];
-                take(seq + j, j, v);
-                if (j < again)
-                    release(seq + j);
-                if (TAIL)
-                    drop_slots<T, kRingConsumers>(s, r, r.w0 + j * kPieceChunks + tid, v);
-                add_chunks<T, false>(t, v, a.c, 0.0f);
-            }
             const int ec = any ? r.edge(edge_of_thread(), 0, r.nch) : -1;
             float edge[E];
-            if (ec >= 0) {
+            if (ec >= 0)
                 load_edge(r, ec, edge, total, a.status);
-                float x[E];
+            Stats t = stats_empty();
+            if (!BWD) {
+                for (int j = 0; j < np; ++j) {
+                    arrived(seq + j);
+                    uint4 v[kUnroll];
+                    take(seq + j, j, v);
+                    if (j < again)
+                        release(seq + j);
+                    if (TAIL)
+                        drop_slots<T, kRingConsumers>(s, r, r.w0 + j * kPieceChunks + tid, v);
+                    add_chunks<T, false>(t, v, a.c, 0.0f);
+                }
+                if (ec >= 0) {
+                    float x[E];
 #pragma unroll
-                for (int e = 0; e < E; ++e)
-                    x[e] = edge[e];
-                if (TAIL)
-                    drop_slots(s, r, ec, x);
-                add_values<false>(t, x, a.c);
+                    for (int e = 0; e < E; ++e)
+                        x[e] = edge[e];
+                    if (TAIL)
+                        drop_slots(s, r, ec, x);
+                    add_values<false>(t, x, a.c);
+                }
+                // the block's sums: warps' in shared memory, two sets in turn
+                t = warp_stats(t, a.c);
+                if (lane == 0)
+                    parts[b][warp] = t;
+                asm volatile("bar.sync 1, %0;" ::"n"(kRingConsumers) : "memory");
+                t = parts[b][lane & (kRingWarps - 1)];
+                t = warp_stats_16(t, a.c);
             }
-            // the block's sums: warps' in shared memory, two sets in turn
-            t = warp_stats(t, a.c);
-            if (lane == 0)
-                parts[b][warp] = t;
-            asm volatile("bar.sync 1, %0;" ::"n"(kRingConsumers) : "memory");
-            t = parts[b][lane & (kRingWarps - 1)];
-            t = warp_stats_16(t, a.c);
 
             const OutRow<T> o(a.out, a.rows, row, r);
             bool zero = true;
             if (any) {
-                const RowLoss l = row_loss<TAIL>(a, s, t);
-                zero = l.zero;
-                if (tid == 0) {
-                    a.loss[row] = l.loss;
-                    if (l.loss != l.loss)
-                        atomicOr(a.status, kStatusNonfinite);
+                RowGrad g;
+                if (BWD) {
+                    g = row_grad<TAIL>(a, s);
+                    zero = false;
+                } else {
+                    const RowLoss l = row_loss<TAIL>(a, s, t);
+                    g = l.grad;
+                    zero = l.zero;
+                    if (tid == 0) {
+                        a.loss[row] = l.loss;
+                        if (l.loss != l.loss)
+                            atomicOr(a.status, kStatusNonfinite);
+                    }
                 }
                 // the kept pieces, then the first ones again
                 for (int j = 0; j < np; ++j) {
@@ -2162,16 +2166,16 @@ distill_ring_kernel(const __grid_constant__ DistillArgs a, uint64_t limit_ns)
                     release(q);
                     const int c = r.w0 + piece * kPieceChunks + tid;
                     if (!zero) {
-                        row_gradient<T, kRingConsumers>(s, r, c, l.grad, v, f);
+                        row_gradient<T, kRingConsumers>(s, r, c, g, v, f);
                         store_chunks<T, kRingConsumers>(r, o, c, r.w1, f, amax, m2, a.status);
                     }
                 }
                 if (ec >= 0 && !zero) {
-                    row_gradient(s, r, ec, l.grad, edge);
+                    row_gradient(s, r, ec, g, edge);
                     store_elements(r, o, ec, edge, m2, a.status);
                 }
                 seq += np + again;
-            } else if (alive && tid == 0) {
+            } else if (!BWD && alive && tid == 0) {
                 a.loss[row] = 0.0f;
             }
             if (alive) {
@@ -2254,9 +2258,38 @@ cudaError_t distill_fwd(DistillArgs a, const DeviceInfo &dev, cudaStream_t st)
                               static_cast<unsigned>(a.cluster), a);
 }
 
-template <typename T, bool TAIL>
-cudaError_t distill_bwd(DistillArgs a, const DeviceInfo &, cudaStream_t st)
+// The ring where a row does not fit one block's registers and there is at least
+// a row for every second SM.
+template <typename T>
+bool ring_takes(const DistillArgs &a, const DeviceInfo &dev)
 {
+    const int64_t chunks = (static_cast<int64_t>(a.vocab) + 2 * Chunk<T>::E - 2) / Chunk<T>::E;
+    return chunks > kNV * kThreads && 2 * a.rows >= dev.sm_count;
+}
+
+template <typename T, bool TAIL, bool BWD>
+cudaError_t distill_ring(const DistillArgs &a, const DeviceInfo &dev, cudaStream_t st)
+{
+    static std::once_flag once[64];
+    static cudaError_t err[64];
+    const int d = dev.ordinal & 63;
+    std::call_once(once[d], [&] {
+        err[d] = cudaFuncSetAttribute(distill_ring_kernel<T, TAIL, BWD>,
+                                      cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                      static_cast<int>(kRingSmem));
+    });
+    if (err[d] != cudaSuccess)
+        return err[d];
+    return launch_pdl(distill_ring_kernel<T, TAIL, BWD>,
+                      dim3(static_cast<unsigned>(std::min<int64_t>(a.rows, dev.sm_count))),
+                      dim3(kRingThreads), kRingSmem, st, a, wait_limit_ns());
+}
+
+template <typename T, bool TAIL>
+cudaError_t distill_bwd(DistillArgs a, const DeviceInfo &dev, cudaStream_t st)
+{
+    if (ring_takes<T>(a, dev))
+        return distill_ring<T, TAIL, true>(a, dev, st);
     a.blocks_per_row = bwd_blocks<T>(a.vocab);
     return launch_pdl(distill_bwd_kernel<T, TAIL>,
                       dim3(static_cast<unsigned>(a.rows * a.blocks_per_row)), dim3(kThreads), 0, st,
@@ -2266,25 +2299,10 @@ cudaError_t distill_bwd(DistillArgs a, const DeviceInfo &, cudaStream_t st)
 template <typename T, bool TAIL>
 cudaError_t distill_fused(DistillArgs a, const DeviceInfo &dev, cudaStream_t st)
 {
-    const int64_t chunks = (static_cast<int64_t>(a.vocab) + 2 * Chunk<T>::E - 2) / Chunk<T>::E;
-    // the ring where a row does not fit one block's registers and there is at
-    // least a row for every second SM
-    if (chunks > kNV * kThreads && 2 * a.rows >= dev.sm_count) {
-        static std::once_flag once[64];
-        static cudaError_t err[64];
-        const int d = dev.ordinal & 63;
-        std::call_once(once[d], [&] {
-            err[d] = cudaFuncSetAttribute(distill_ring_kernel<T, TAIL>,
-                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                          static_cast<int>(kRingSmem));
-        });
-        if (err[d] != cudaSuccess)
-            return err[d];
-        return launch_pdl(distill_ring_kernel<T, TAIL>,
-                          dim3(static_cast<unsigned>(std::min<int64_t>(a.rows, dev.sm_count))),
-                          dim3(kRingThreads), kRingSmem, st, a, wait_limit_ns());
-    }
-    a.cluster = cluster_for(a.rows, chunks, dev);
+    if (ring_takes<T>(a, dev))
+        return distill_ring<T, TAIL, false>(a, dev, st);
+    a.cluster = cluster_for(a.rows, (static_cast<int64_t>(a.vocab) + 2 * Chunk<T>::E - 2) / Chunk<T>::E,
+                            dev);
     return launch_pdl_cluster(distill_fused_kernel<T, TAIL>,
                               dim3(static_cast<unsigned>(a.rows * a.cluster)), dim3(kThreads), 0, st,
                               static_cast<unsigned>(a.cluster), a);
