@@ -55,6 +55,11 @@ __device__ __forceinline__ float ex2(float x)
     return r;
 }
 
+__device__ __forceinline__ void prefetch_l2(const void *p)
+{
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+}
+
 // ------------------------------------------------------------ rows in chunks
 template <typename T>
 struct Chunk {
@@ -282,6 +287,33 @@ __device__ __forceinline__ float max_nan(float a, float b)
     return r;
 }
 
+// Element d of a chunk, and the chunk with it replaced; d is no constant, so the
+// word is found by selects.
+template <typename T>
+__device__ __forceinline__ float get_element(uint4 v, int d)
+{
+    const int i = sizeof(T) == 2 ? d >> 1 : d;
+    const uint32_t w = i < 2 ? (i == 0 ? v.x : v.y) : (i == 2 ? v.z : v.w);
+    if (sizeof(T) == 2)
+        return __uint_as_float(d & 1 ? w & 0xFFFF0000u : w << 16);
+    return __uint_as_float(w);
+}
+template <typename T>
+__device__ __forceinline__ uint4 set_element(uint4 v, int d, float x)
+{
+    uint32_t keep = 0, w = __float_as_uint(x);
+    if (sizeof(T) == 2) {
+        w = static_cast<uint32_t>(__bfloat16_as_ushort(__float2bfloat16_rn(x))) << (16 * (d & 1));
+        keep = d & 1 ? 0x0000FFFFu : 0xFFFF0000u;
+    }
+    const int i = sizeof(T) == 2 ? d >> 1 : d;
+    v.x = i == 0 ? (v.x & keep) | w : v.x;
+    v.y = i == 1 ? (v.y & keep) | w : v.y;
+    v.z = i == 2 ? (v.z & keep) | w : v.z;
+    v.w = i == 3 ? (v.w & keep) | w : v.w;
+    return v;
+}
+
 // The largest element of a chunk (a NaN only if all are).
 template <typename T>
 __device__ __forceinline__ float chunk_max(uint4 v);
@@ -428,30 +460,6 @@ __device__ __forceinline__ void add_chunks(Stats &t, const uint4 (&v)[U], float 
     }
 }
 
-// The block's sums, in every thread.  `red`: one Stats per warp.
-template <bool ENT>
-__device__ __forceinline__ Stats block_join(Stats t, float c, Stats *red)
-{
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        Stats u;
-        u.m = __shfl_xor_sync(0xFFFFFFFFu, t.m, o);
-        u.s = __shfl_xor_sync(0xFFFFFFFFu, t.s, o);
-        u.h = ENT ? __shfl_xor_sync(0xFFFFFFFFu, t.h, o) : 0.0f;
-        // lower lane first on both sides, so that all lanes get equal bits
-        t = (threadIdx.x & o) ? join<ENT>(u, t, c) : join<ENT>(t, u, c);
-    }
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0)
-        red[threadIdx.x >> 5] = t;
-    __syncthreads();
-    t = red[0];
-#pragma unroll 1
-    for (int w = 1; w < kWarps; ++w)
-        t = join<ENT>(t, red[w], c);
-    return t;
-}
-
 // The largest value of a warp's lanes (a NaN only if all are).
 __device__ __forceinline__ float warp_max_of(float v)
 {
@@ -460,31 +468,42 @@ __device__ __forceinline__ float warp_max_of(float v)
     return r;
 }
 
-// The joined sums of the lanes of a warp, in every lane; without the entropy.
+// The joined sums of N lanes (each lane's of its N lanes' group), in every lane:
+// the maximum first, so that each lane rescales once; sums in a fixed order.
+template <bool ENT, int N>
 __device__ __forceinline__ Stats warp_stats(Stats t, float c)
 {
+    float m = t.m;
+    if (N == 32) {
+        m = warp_max_of(m);
+    } else {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        Stats u;
-        u.m = __shfl_xor_sync(0xFFFFFFFFu, t.m, o);
-        u.s = __shfl_xor_sync(0xFFFFFFFFu, t.s, o);
-        u.h = 0.0f;
-        t = (threadIdx.x & o) ? join<false>(u, t, c) : join<false>(t, u, c);
+        for (int o = N / 2; o > 0; o >>= 1)
+            m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+    }
+    const float d = fmaxf((t.m - m) * c, kFloor2), f = ex2(d);
+    t.m = m;
+    if (ENT)
+        t.h = f * fmaf(t.s, d, t.h);
+    t.s *= f;
+#pragma unroll
+    for (int o = N / 2; o > 0; o >>= 1) {
+        t.s += __shfl_xor_sync(0xFFFFFFFFu, t.s, o);
+        if (ENT)
+            t.h += __shfl_xor_sync(0xFFFFFFFFu, t.h, o);
     }
     return t;
 }
-// The same where lanes 16 .. 31 repeat lanes 0 .. 15.
-__device__ __forceinline__ Stats warp_stats_16(Stats t, float c)
+
+// The block's sums, in every thread.  `red`: one Stats per warp.
+template <bool ENT>
+__device__ __forceinline__ Stats block_join(Stats t, float c, Stats *red)
 {
-#pragma unroll
-    for (int o = 8; o > 0; o >>= 1) {
-        Stats u;
-        u.m = __shfl_xor_sync(0xFFFFFFFFu, t.m, o);
-        u.s = __shfl_xor_sync(0xFFFFFFFFu, t.s, o);
-        u.h = 0.0f;
-        t = (threadIdx.x & o) ? join<false>(u, t, c) : join<false>(t, u, c);
-    }
-    return t;
+    t = warp_stats<ENT, 32>(t, c);
+    if ((threadIdx.x & 31) == 0)
+        red[threadIdx.x >> 5] = t;
+    __syncthreads();
+    return warp_stats<ENT, kWarps>(red[threadIdx.x & (kWarps - 1)], c);
 }
 
 // ------------------------------------------------------------ clusters
@@ -1316,7 +1335,7 @@ struct DistillArgs {
 };
 
 // The row's slots in shared memory.  Which chunks a slot names an element of is
-// one bit each in `named` (exact up to 2^19 bf16 tokens, beyond that one bit
+// one bit each in `named` (exact up to 2^18 bf16 tokens, beyond that one bit
 // for several chunks): a warp asks it for every chunk, and a filter with many
 // false hits would send nearly every warp through the lists.  head[chunk %
 // kHeads] then starts the list of slots.  Slots of equal ids each carry their
@@ -1324,7 +1343,7 @@ struct DistillArgs {
 //   loss = sum q log q - sum q (z - zref) / T + sum q ((max - zref) / T + ln S)
 // for the row's maximum and S = sum e^((x - max) / T).
 constexpr int kHeads = 256;
-constexpr int kNamedWords = 2048;
+constexpr int kNamedWords = 1024;
 struct alignas(16) Slots {
     uint32_t named[kNamedWords];
     int head[kHeads];
@@ -1346,54 +1365,64 @@ struct alignas(16) Slots {
     float zmean;    // sum q (z - zref)
     float zmax;     // the largest logit of the slots' ids
     float inside;   // sum over these ids of 2^((z - zmax) c)
+    float edge[2][8];  // (ring) the row's edge chunks
 };
 
-template <typename V, typename F>
-__device__ __forceinline__ V warp_all(V v, F f)
-{
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        const V u = __shfl_xor_sync(0xFFFFFFFFu, v, o);
-        // lower lane first on both sides, so that all lanes get equal bits
-        v = (threadIdx.x & o) ? f(u, v) : f(v, u);
-    }
-    return v;
-}
 __device__ __forceinline__ float warp_sum(float v)
 {
-    return warp_all(v, [](float a, float b) { return a + b; });
-}
-__device__ __forceinline__ float warp_max(float v)
-{
-    return warp_all(v, [](float a, float b) { return fmaxf(a, b); });
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    return v;
 }
 
-// One row's slots, by one warp: slot lane + 32 i in register i.  Without LOSS
-// only what the gradient needs, and no logit is read (in a backward pass in
-// place another block may already have written it).
-template <typename T, bool TAIL, bool LOSS>
-__device__ __forceinline__ void warp_slots(const DistillArgs &a, int64_t row, Slots &s)
+// What one warp reads of a row's slots: slot lane + 32 i in register i.
+struct SlotInput {
+    int id[F8_MAX_TOP / 32];
+    float t[F8_MAX_TOP / 32];
+    float dloss, lse, rest;
+};
+
+template <bool TAIL, bool LOSS>
+__device__ __forceinline__ SlotInput read_slots(const DistillArgs &a, int64_t row)
+{
+    SlotInput in;
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int i = 0; i < F8_MAX_TOP / 32; ++i) {
+        const int j = lane + 32 * i;
+        in.id[i] = -1;
+        in.t[i] = F8_NEG_INF;
+        if (32 * i < a.k && j < a.k) {
+            in.id[i] = a.ids[row * a.k + j];
+            in.t[i] = a.values[row * a.k + j];
+        }
+    }
+    in.dloss = a.dloss != nullptr ? a.dloss[row] : 0.0f;
+    in.lse = LOSS ? 0.0f : a.lse[row];
+    in.rest = !LOSS && TAIL ? a.rest[row] : 0.0f;
+    return in;
+}
+
+// One row's slots, by one warp.  Without LOSS only what the gradient needs, and
+// no logit is read (in a backward pass in place another block may already have
+// written it).
+// `announce` is called as soon as s.any and s.skip are known.
+template <typename T, bool TAIL, bool LOSS, typename F>
+__device__ __forceinline__ void warp_slots(const DistillArgs &a, int64_t row, const SlotInput &in,
+                                           Slots &s, F announce)
 {
     constexpr int N = F8_MAX_TOP / 32;
     const int lane = threadIdx.x & 31, k = a.k;
     const Row<T> r(static_cast<const T *>(a.logits), row, a.ld, a.vocab);
-    for (int i = lane; i < kNamedWords / 4; i += 32)
-        reinterpret_cast<uint4 *>(s.named)[i] = make_uint4(0, 0, 0, 0);
-    for (int i = lane; i < kHeads / 4; i += 32)
-        reinterpret_cast<int4 *>(s.head)[i] = make_int4(-1, -1, -1, -1);
     int id[N];
     float t[N], z[N];
     bool any = false, outside = false;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        const int j = lane + 32 * i;
-        id[i] = -1;
-        t[i] = F8_NEG_INF;
+        id[i] = in.id[i];
+        t[i] = in.t[i];
         z[i] = F8_NEG_INF;
-        if (32 * i < k && j < k) {
-            id[i] = a.ids[row * k + j];
-            t[i] = a.values[row * k + j];
-        }
         outside |= id[i] >= r.vocab;
         if (id[i] >= r.vocab || t[i] == F8_NEG_INF)
             id[i] = -1;
@@ -1404,38 +1433,56 @@ __device__ __forceinline__ void warp_slots(const DistillArgs &a, int64_t row, Sl
     if (outside)
         atomicOr(a.status, kStatusIndex);
     any = __any_sync(0xFFFFFFFFu, any);
+    if (lane == 0) {
+        s.any = any;
+        s.skip = !LOSS && (in.dloss == 0.0f || fabsf(in.lse) >= kMaxLse);
+        announce();
+    }
+    for (int i = lane; i < kNamedWords / 4; i += 32)
+        reinterpret_cast<uint4 *>(s.named)[i] = make_uint4(0, 0, 0, 0);
+    for (int i = lane; i < kHeads / 4; i += 32)
+        reinterpret_cast<int4 *>(s.head)[i] = make_int4(-1, -1, -1, -1);
     if (any) {
-        float zm = F8_NEG_INF, tm = F8_NEG_INF;
+        // slots 32 n and up do not exist; the loops stop there
+        const int n = (k + 31) / 32;
+        float tm = F8_NEG_INF;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
+            if (i >= n)
+                break;
             if (LOSS && id[i] >= 0)
                 z[i] = as_float(r.base[r.off + id[i]]);
             tm = fmaxf(tm, t[i]);
         }
         float q[N], logq[N], sum = 0.0f;
         if (!TAIL)
-            tm = warp_max(tm);
+            tm = warp_max_of(tm);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
+            q[i] = logq[i] = 0.0f;
+            if (i >= n)
+                continue;
             logq[i] = TAIL ? t[i] : (t[i] - tm) * a.inv_t;
-            q[i] = 0.0f;
-            if (32 * i < k)
-                q[i] = id[i] >= 0 ? expf(logq[i]) : 0.0f;
+            q[i] = id[i] >= 0 ? expf(logq[i]) : 0.0f;
             sum += q[i];
         }
         sum = warp_sum(sum);
+        float qall = sum;
         if (!TAIL) {
             const float ls = logf(sum), inv = 1.0f / sum;
+            qall = sum * inv;
 #pragma unroll
             for (int i = 0; i < N; ++i) {
                 q[i] *= inv;
                 logq[i] -= ls;
             }
         }
-        // the table, and each id's summed q
+        // the table
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const int j = lane + 32 * i;
+            if (i >= n)
+                break;
             if (j < k) {
                 s.id[j] = id[i];
                 s.q[j] = q[i];
@@ -1443,20 +1490,26 @@ __device__ __forceinline__ void warp_slots(const DistillArgs &a, int64_t row, Sl
         }
         __syncwarp();
 #pragma unroll
-        for (int i = 0; i < N; ++i)
+        for (int i = 0; i < N; ++i) {
+            if (i >= n)
+                break;
             if (id[i] >= 0) {
                 const int ch = (id[i] + r.off) / Chunk<T>::E;
                 s.next[lane + 32 * i] = atomicExch(&s.head[ch % kHeads], lane + 32 * i);
                 atomicOr(&s.named[(ch >> 5) % kNamedWords], 1u << (ch & 31));
             }
+        }
         __syncwarp();
+        // each id's summed q; the first slot of an id stands for it
         bool first[N];
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const int j = lane + 32 * i;
             first[i] = id[i] >= 0;
-            int same = 0;
+            if (i >= n)
+                continue;
             if (id[i] >= 0) {
+                int same = 0;
                 for (int p = s.head[((id[i] + r.off) / Chunk<T>::E) % kHeads]; p >= 0; p = s.next[p]) {
                     if (s.id[p] == id[i]) {
                         ++same;
@@ -1472,60 +1525,60 @@ __device__ __forceinline__ void warp_slots(const DistillArgs &a, int64_t row, Sl
                 s.qsum[j] = qs;
             }
         }
-        float zref = F8_NEG_INF, plogp = 0.0f, zmean = 0.0f, inside = 0.0f, total = sum;
-        bool used = false, masked = false;
         if (LOSS) {
+            float zref = F8_NEG_INF, zm = F8_NEG_INF;
+            bool used = false, masked = false;
 #pragma unroll
             for (int i = 0; i < N; ++i) {
                 const bool u = q[i] > 0.0f || q[i] != q[i];
                 used |= u;
                 masked |= u && z[i] == F8_NEG_INF;
-                if (u) {
-                    plogp = fmaf(q[i], logq[i], plogp);
-                    zref = fmaxf(zref, z[i]);
-                }
+                zref = u ? fmaxf(zref, z[i]) : zref;
                 zm = fmaxf(zm, z[i]);
             }
-            zref = warp_max(zref);
-            plogp = warp_sum(plogp);
+            zref = warp_max_of(zref);
+            zm = warp_max_of(zm);
             used = __any_sync(0xFFFFFFFFu, used);
             masked = __any_sync(0xFFFFFFFFu, masked);
-            zm = warp_max(zm);
-            total = 0.0f;
+            float plogp = 0.0f, zmean = 0.0f, inside = 0.0f;
 #pragma unroll
             for (int i = 0; i < N; ++i) {
-                total += q[i];
+                if (i >= n)
+                    break;
+                if (q[i] > 0.0f || q[i] != q[i])
+                    plogp = fmaf(q[i], logq[i], plogp);
                 if (q[i] > 0.0f && z[i] != F8_NEG_INF)
                     zmean = fmaf(q[i], z[i] - zref, zmean);
                 if (TAIL && first[i] && zm != F8_NEG_INF)
                     inside += ex2((z[i] - zm) * a.c);
             }
-            zmean = warp_sum(zmean);
-            total = TAIL ? sum : warp_sum(total);
-            if (TAIL)
-                inside = warp_sum(inside);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) {
+                plogp += __shfl_xor_sync(0xFFFFFFFFu, plogp, o);
+                zmean += __shfl_xor_sync(0xFFFFFFFFu, zmean, o);
+                if (TAIL)
+                    inside += __shfl_xor_sync(0xFFFFFFFFu, inside, o);
+            }
+            if (lane == 0) {
+                s.used = used;
+                s.masked = masked;
+                s.plogp = plogp;
+                s.zref = zref;
+                s.zmean = zmean;
+                s.zmax = zm;
+                s.inside = inside;
+            }
         }
         if (lane == 0) {
-            s.used = used;
-            s.masked = masked;
-            s.total = TAIL ? total : 1.0f;
-            s.qall = total;
-            s.left = TAIL ? fmaxf(1.0f - total, 0.0f) : 0.0f;
-            s.plogp = plogp;
-            s.zref = zref;
-            s.zmean = zmean;
-            s.zmax = zm;
-            s.inside = inside;
+            s.total = TAIL ? sum : 1.0f;
+            s.qall = qall;
+            s.left = TAIL ? fmaxf(1.0f - sum, 0.0f) : 0.0f;
         }
     }
     if (lane == 0) {
-        s.any = any;
-        s.dloss = a.dloss != nullptr ? a.dloss[row] : 0.0f;
-        if (!LOSS) {
-            s.lse = a.lse[row];
-            s.rest = TAIL ? a.rest[row] : 0.0f;
-            s.skip = s.dloss == 0.0f || fabsf(s.lse) >= kMaxLse;
-        }
+        s.dloss = in.dloss;
+        s.lse = in.lse;
+        s.rest = in.rest;
     }
     __syncwarp();
 }
@@ -1562,16 +1615,17 @@ __device__ __forceinline__ void drop_slots(const Slots &s, const Row<T> &r, int 
 template <typename T, int N, int U>
 __device__ __forceinline__ void drop_slots(const Slots &s, const Row<T> &r, int c, uint4 (&v)[U])
 {
-    const uint32_t named = named_bits<N, U>(s, c);
-    if (named == 0)
-        return;
+#pragma unroll 1
+    for (uint32_t named = named_bits<N, U>(s, c); named != 0; named &= named - 1) {
+        const int u = __ffs(named) - 1, ch = c + u * N;
+        for (int j = s.head[static_cast<unsigned>(ch) % kHeads]; j >= 0; j = s.next[j]) {
+            const int d = s.id[j] + r.off - ch * Chunk<T>::E;
+            if (d >= 0 && d < Chunk<T>::E) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-        if (named >> u & 1u) {
-            float f[Chunk<T>::E];
-            unpack<T>(v[u], f);
-            drop_slots(s, r, c + u * N, f);
-            v[u] = pack<T>(f);  // exact: the values are the chunk's own
+                for (int i = 0; i < U; ++i)
+                    if (i == u)
+                        v[i] = set_element<T>(v[i], d, F8_NEG_INF);
+            }
         }
     }
 }
@@ -1583,19 +1637,9 @@ struct RowGrad {
     float scale, mass, dense;
 };
 
-template <typename T>
-__device__ __forceinline__ void slot_gradient(const Slots &s, const Row<T> &r, int ch,
-                                              const RowGrad &g, const float (&x)[Chunk<T>::E],
-                                              float (&f)[Chunk<T>::E])
+__device__ __forceinline__ float slot_gradient(const Slots &s, const RowGrad &g, int j, float x)
 {
-    constexpr int E = Chunk<T>::E;
-    for (int j = s.head[static_cast<unsigned>(ch) % kHeads]; j >= 0; j = s.next[j]) {
-        const int d = s.id[j] + r.off - ch * E;
-#pragma unroll
-        for (int e = 0; e < E; ++e)
-            if (d == e)
-                f[e] = g.scale * fmaf(g.mass, ex2(g.p.exponent(x[e])) * g.p.norm, -s.qsum[j]);
-    }
+    return g.scale * fmaf(g.mass, ex2(g.p.exponent(x)) * g.p.norm, -s.qsum[j]);
 }
 
 // The gradient of one chunk's elements, and of U chunks c + u * N.
@@ -1608,7 +1652,13 @@ __device__ __forceinline__ void row_gradient(const Slots &s, const Row<T> &r, in
 #pragma unroll
     for (int e = 0; e < E; ++e)
         f[e] = g.scale * g.dense * (ex2(g.p.exponent(x[e])) * g.p.norm);
-    slot_gradient(s, r, ch, g, x, f);
+    for (int j = s.head[static_cast<unsigned>(ch) % kHeads]; j >= 0; j = s.next[j]) {
+        const int d = s.id[j] + r.off - ch * E;
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            if (d == e)
+                f[e] = slot_gradient(s, g, j, x[e]);
+    }
 #pragma unroll
     for (int e = 0; e < E; ++e)
         x[e] = f[e];
@@ -1619,20 +1669,25 @@ __device__ __forceinline__ void row_gradient(const Slots &s, const Row<T> &r, in
 {
     constexpr int E = Chunk<T>::E;
     const float factor = g.scale * g.dense * g.p.norm;
-    const uint32_t named = named_bits<N, U>(s, c);
 #pragma unroll
     for (int u = 0; u < U; ++u)
         out[u] = scaled_softmax<T>(v[u], g.p, factor);
-    if (named == 0)
-        return;
+#pragma unroll 1
+    for (uint32_t named = named_bits<N, U>(s, c); named != 0; named &= named - 1) {
+        const int u = __ffs(named) - 1, ch = c + u * N;
+        for (int j = s.head[static_cast<unsigned>(ch) % kHeads]; j >= 0; j = s.next[j]) {
+            const int d = s.id[j] + r.off - ch * E;
+            if (d >= 0 && d < E) {
+                uint4 w = v[0];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-        if (named >> u & 1u) {
-            float x[E], f[E];
-            unpack<T>(v[u], x);
-            unpack<T>(out[u], f);
-            slot_gradient(s, r, c + u * N, g, x, f);
-            out[u] = pack<T>(f);  // exact for the elements that stay
+                for (int i = 1; i < U; ++i)
+                    w = i == u ? v[i] : w;
+                const float f = slot_gradient(s, g, j, get_element<T>(w, d));
+#pragma unroll
+                for (int i = 0; i < U; ++i)
+                    if (i == u)
+                        out[i] = set_element<T>(out[i], d, f);
+            }
         }
     }
 }
@@ -1659,7 +1714,8 @@ struct RowLoss {
 };
 
 template <bool TAIL>
-__device__ __forceinline__ RowLoss row_loss(const DistillArgs &a, const Slots &s, const Stats &t)
+__device__ __forceinline__ RowLoss row_loss(const DistillArgs &a, const Slots &s, const Stats &t,
+                                            bool loss)
 {
     RowLoss o;
     float m = t.m, outside = t.s, sum = t.s;
@@ -1671,9 +1727,19 @@ __device__ __forceinline__ RowLoss row_loss(const DistillArgs &a, const Slots &s
     const bool bad = sum != sum || m == F8_POS_INF;
     const bool none = !bad && sum == 0.0f;
     const float inv_s = none ? 0.0f : (bad ? F8_NAN : 1.0f / sum);
+    o.rest = TAIL ? outside * inv_s : 0.0f;
+    o.grad.p = Softmax{1.0f, m == F8_NEG_INF ? 0.0f : -m, a.c, inv_s};
+    o.grad.scale = s.dloss * a.inv_t;
+    o.grad.mass = o.grad.dense = s.total;
+    if (TAIL && o.rest > 0.0f) {
+        o.grad.mass = s.total + s.left;
+        o.grad.dense = o.grad.mass - s.left / (TAIL ? o.rest : 1.0f);
+    }
+    o.zero = s.dloss == 0.0f || none;
+    if (!loss)
+        return o;
     const float ls = logf(sum);
     o.lse = bad ? F8_NAN : (none ? F8_NEG_INF : fmaf(m, a.inv_t, ls));
-    o.rest = TAIL ? outside * inv_s : 0.0f;
     o.loss = 0.0f;
     if (s.used)
         o.loss = s.masked || none ? F8_POS_INF
@@ -1683,14 +1749,6 @@ __device__ __forceinline__ RowLoss row_loss(const DistillArgs &a, const Slots &s
         o.loss += s.left * (logf(s.left) - logf(o.rest));
     if (bad || s.plogp != s.plogp || s.zmean != s.zmean)
         o.loss = F8_NAN;
-    o.grad.p = Softmax{1.0f, m == F8_NEG_INF ? 0.0f : -m, a.c, inv_s};
-    o.grad.scale = s.dloss * a.inv_t;
-    o.grad.mass = o.grad.dense = s.total;
-    if (TAIL && o.rest > 0.0f) {
-        o.grad.mass = s.total + s.left;
-        o.grad.dense = o.grad.mass - s.left / (TAIL ? o.rest : 1.0f);
-    }
-    o.zero = s.dloss == 0.0f || none;
     return o;
 }
 
@@ -1713,7 +1771,7 @@ distill_fwd_kernel(const __grid_constant__ DistillArgs a)
     if (C > 1)
         cluster_start();
     if (tid < 32)
-        warp_slots<T, TAIL, true>(a, row, slots);
+        warp_slots<T, TAIL, true>(a, row, read_slots<TAIL, true>(a, row), slots, [] {});
     __syncthreads();
     if (!slots.any) {
         if (C > 1)
@@ -1756,7 +1814,7 @@ distill_fwd_kernel(const __grid_constant__ DistillArgs a)
             t = join<false>(t, parts[i], a.c);
     }
     if (tid == 0) {
-        const RowLoss o = row_loss<TAIL>(a, slots, t);
+        const RowLoss o = row_loss<TAIL>(a, slots, t, true);
         a.loss[row] = o.loss;
         a.lse[row] = o.lse;
         if (TAIL)
@@ -1781,7 +1839,7 @@ distill_bwd_kernel(const __grid_constant__ DistillArgs a)
     const int64_t total = (a.rows - 1) * a.ld + a.vocab;
     const OutRow<T> o(a.out, a.rows, row, r);
     if (tid < 32)
-        warp_slots<T, TAIL, false>(a, row, slots);
+        warp_slots<T, TAIL, false>(a, row, read_slots<TAIL, false>(a, row), slots, [] {});
     __syncthreads();
     const RowGrad g = row_grad<TAIL>(a, slots);
     uint32_t m2 = 0;
@@ -1837,7 +1895,7 @@ distill_fused_kernel(const __grid_constant__ DistillArgs a)
     if (C > 1)
         cluster_start();
     if (tid < 32)
-        warp_slots<T, TAIL, true>(a, row, slots);
+        warp_slots<T, TAIL, true>(a, row, read_slots<TAIL, true>(a, row), slots, [] {});
     __syncthreads();
     const int per = (r.nch + C - 1) / C;
     const int c0 = min(r.nch, rank * per), c1 = min(r.nch, c0 + per);
@@ -1899,7 +1957,7 @@ distill_fused_kernel(const __grid_constant__ DistillArgs a)
             for (int i = 1; i < C; ++i)
                 t = join<false>(t, parts[i], a.c);
         }
-        const RowLoss l = row_loss<TAIL>(a, slots, t);
+        const RowLoss l = row_loss<TAIL>(a, slots, t, rank == 0 && tid == 0);
         zero = l.zero;
         if (rank == 0 && tid == 0) {
             a.loss[row] = l.loss;
@@ -1945,8 +2003,9 @@ distill_fused_kernel(const __grid_constant__ DistillArgs a)
 // together hold more than L2 does, so a block keeps what it can: one persistent
 // block per SM takes whole rows through a ring of 32 KB pieces in shared
 // memory that bulk copies fill.
-//   warp 16      reads the next row's slots (two buffers) and sums them up;
-//   warp 17      issues the copies: a row's pieces 0 .. n-1, then again those
+//   warps 16..18 each read every third row's slots into a buffer of their own
+//                and sum them up, ahead of the others;
+//   warp 19      issues the copies: a row's pieces 0 .. n-1, then again those
 //                that the ring could not keep, then the next row's;
 //   warps 0..15  first pass: running sums over the pieces, releasing all but
 //                the last `keep`; the block's join (one barrier); second pass:
@@ -1958,14 +2017,16 @@ distill_fused_kernel(const __grid_constant__ DistillArgs a)
 // only, over every piece once.
 constexpr int kRingWarps = 16;
 constexpr int kRingConsumers = kRingWarps * 32;
-constexpr int kRingThreads = kRingConsumers + 64;
+constexpr int kSlotBuffers = 3;
+constexpr int kRingThreads = kRingConsumers + 32 * kSlotBuffers + 32;
 constexpr int kPieceChunks = kUnroll * kRingConsumers;
 constexpr int kPieceBytes = kPieceChunks * 16;
 constexpr int kPieces = 6;
 constexpr int kKeep = 4;  // the other two are under way
 constexpr uint64_t kDrainLimitNs = 1000000000ull;
 
-constexpr size_t kRingSmem = static_cast<size_t>(kPieces) * kPieceBytes + 2 * sizeof(Slots);
+constexpr size_t kRingSmem = static_cast<size_t>(kPieces) * kPieceBytes +
+                             kSlotBuffers * sizeof(Slots);
 
 // Piece of position `seq` in the queue: its slot, and the parity of its phase.
 __device__ __forceinline__ int ring_slot(uint32_t seq) { return static_cast<int>(seq % kPieces); }
@@ -1979,8 +2040,9 @@ distill_ring_kernel(const __grid_constant__ DistillArgs a, uint64_t limit_ns)
     extern __shared__ __align__(128) uint8_t pieces[];
     __shared__ __align__(8) uint64_t full[kPieces];
     __shared__ __align__(8) uint64_t empty[kPieces];
-    __shared__ __align__(8) uint64_t sfull[2];
-    __shared__ __align__(8) uint64_t sempty[2];
+    __shared__ __align__(8) uint64_t sfull[kSlotBuffers];
+    __shared__ __align__(8) uint64_t sempty[kSlotBuffers];
+    __shared__ __align__(8) uint64_t known[kSlotBuffers];
     __shared__ Stats parts[2][kRingWarps];
     __shared__ int abort_word;
     volatile int *abort_flag = &abort_word;
@@ -1991,8 +2053,9 @@ distill_ring_kernel(const __grid_constant__ DistillArgs a, uint64_t limit_ns)
             mbar_init(&full[i], 1);
             mbar_init(&empty[i], kRingWarps);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < kSlotBuffers; ++i) {
             mbar_init(&sfull[i], 1);
+            mbar_init(&known[i], 1);
             mbar_init(&sempty[i], kRingWarps + 1);
         }
         *abort_flag = 0;
@@ -2012,27 +2075,46 @@ distill_ring_kernel(const __grid_constant__ DistillArgs a, uint64_t limit_ns)
     uint32_t m2 = 0;
     const bool amax = a.out.amax != nullptr;
 
-    if (warp == kRingWarps) {
+    if (warp >= kRingWarps && warp < kRingWarps + kSlotBuffers) {
         // ---------------------------------------------------- the rows' slots
-        int i = 0;
-        for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, ++i) {
-            const int b = i & 1;
-            const bool ok = wait(&sempty[b], ((i >> 1) & 1) ^ 1u);
+        const int b = warp - kRingWarps;
+        const int64_t step = static_cast<int64_t>(gridDim.x) * kSlotBuffers;
+        int turn = 0;
+        for (int64_t row = blockIdx.x + static_cast<int64_t>(b) * gridDim.x; row < a.rows;
+             row += step, ++turn) {
+            if (row + step < a.rows && lane * 32 < a.k * 4) {  // the next one's, towards L2
+                const int64_t at = (row + step) * a.k + lane * 8;
+                prefetch_l2(a.ids + at);
+                prefetch_l2(a.values + at);
+            }
+            const bool ok = wait(&sempty[b], (turn & 1) ^ 1u);
             if (!__all_sync(0xFFFFFFFFu, ok))
                 break;
-            warp_slots<T, TAIL, !BWD>(a, row, slots[b]);
+            warp_slots<T, TAIL, !BWD>(a, row, read_slots<TAIL, !BWD>(a, row), slots[b],
+                                      [&] { mbar_arrive(&known[b]); });
+            // the row's edges too, so that no other warp waits for global memory
+            const Row<T> r(static_cast<const T *>(a.logits), row, a.ld, a.vocab);
+            const int ec = slots[b].any ? r.edge(lane, 0, r.nch) : -1;
+            if (ec >= 0) {
+                float f[E];
+                load_edge(r, ec, f, total, a.status);
+#pragma unroll
+                for (int e = 0; e < E; ++e)
+                    slots[b].edge[lane][e] = f[e];
+            }
+            __syncwarp();
             if (lane == 0)
                 mbar_arrive(&sfull[b]);
         }
-    } else if (warp == kRingWarps + 1) {
+    } else if (warp == kRingWarps + kSlotBuffers) {
         // ---------------------------------------------------- copies
         if (lane == 0) {
             uint32_t seq = 0;
             int i = 0;
             bool stop = false;
             for (int64_t row = blockIdx.x; row < a.rows && !stop; row += gridDim.x, ++i) {
-                const int b = i & 1;
-                if (!wait(&sfull[b], (i >> 1) & 1)) {
+                const int b = i % kSlotBuffers;
+                if (!wait(&known[b], (i / kSlotBuffers) & 1)) {
                     stop = true;
                     break;
                 }
@@ -2071,8 +2153,8 @@ distill_ring_kernel(const __grid_constant__ DistillArgs a, uint64_t limit_ns)
         int i = 0;
         bool alive = true;
         for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, ++i) {
-            const int b = i & 1;
-            alive = alive && __all_sync(0xFFFFFFFFu, wait(&sfull[b], (i >> 1) & 1));
+            const int b = i % kSlotBuffers;
+            alive = alive && __all_sync(0xFFFFFFFFu, wait(&sfull[b], (i / kSlotBuffers) & 1));
             const Slots &s = slots[b];
             const bool any = alive && s.any != 0 && !(BWD && s.skip);
             const Row<T> r(static_cast<const T *>(a.logits), row, a.ld, a.vocab);
@@ -2087,55 +2169,55 @@ distill_ring_kernel(const __grid_constant__ DistillArgs a, uint64_t limit_ns)
                 if (lane == 0)
                     mbar_arrive(&empty[ring_slot(q)]);
             };
-            // this thread's chunks of a piece, -inf past the row's last whole one
-            auto take = [&](uint32_t q, int piece, uint4(&v)[kUnroll]) {
-                const uint4 *p = reinterpret_cast<const uint4 *>(pieces + ring_slot(q) * kPieceBytes);
-                const int left = n - piece * kPieceChunks;
-                if (left >= kPieceChunks) {
-#pragma unroll
-                    for (int u = 0; u < kUnroll; ++u)
-                        v[u] = p[u * kRingConsumers + tid];
-                } else {
-#pragma unroll
-                    for (int u = 0; u < kUnroll; ++u) {
-                        v[u] = neg_inf_chunk(T());
-                        if (u * kRingConsumers + tid < left)
-                            v[u] = p[u * kRingConsumers + tid];
-                    }
-                }
+            // this thread's chunk u of a piece; a piece's chunks, and whether it has them all
+            auto chunk = [&](uint32_t q, int u) {
+                return reinterpret_cast<const uint4 *>(pieces + ring_slot(q) * kPieceBytes)
+                    [u * kRingConsumers + tid];
             };
+            auto chunks_of = [&](int piece) { return min(n - piece * kPieceChunks, kPieceChunks); };
             const int ec = any ? r.edge(edge_of_thread(), 0, r.nch) : -1;
-            float edge[E];
-            if (ec >= 0)
-                load_edge(r, ec, edge, total, a.status);
             Stats t = stats_empty();
             if (!BWD) {
                 for (int j = 0; j < np; ++j) {
                     arrived(seq + j);
-                    uint4 v[kUnroll];
-                    take(seq + j, j, v);
-                    if (j < again)
-                        release(seq + j);
-                    if (TAIL)
-                        drop_slots<T, kRingConsumers>(s, r, r.w0 + j * kPieceChunks + tid, v);
-                    add_chunks<T, false>(t, v, a.c, 0.0f);
+                    const int c = r.w0 + j * kPieceChunks + tid, have = chunks_of(j);
+                    if (have == kPieceChunks) {
+                        uint4 v[kUnroll];
+#pragma unroll
+                        for (int u = 0; u < kUnroll; ++u)
+                            v[u] = chunk(seq + j, u);
+                        if (j < again)
+                            release(seq + j);
+                        if (TAIL)
+                            drop_slots<T, kRingConsumers>(s, r, c, v);
+                        add_chunks<T, false>(t, v, a.c, 0.0f);
+                    } else {  // the row's last piece, which is kept: a warp's part of it
+#pragma unroll 1
+                        for (int u = 0; u * kRingConsumers + warp * 32 < have; ++u) {
+                            uint4 v[1] = {neg_inf_chunk(T())};
+                            if (u * kRingConsumers + tid < have)
+                                v[0] = chunk(seq + j, u);
+                            if (TAIL)
+                                drop_slots<T, kRingConsumers>(s, r, c + u * kRingConsumers, v);
+                            add_chunks<T, false>(t, v, a.c, 0.0f);
+                        }
+                    }
                 }
                 if (ec >= 0) {
                     float x[E];
 #pragma unroll
                     for (int e = 0; e < E; ++e)
-                        x[e] = edge[e];
+                        x[e] = s.edge[warp][e];
                     if (TAIL)
                         drop_slots(s, r, ec, x);
                     add_values<false>(t, x, a.c);
                 }
                 // the block's sums: warps' in shared memory, two sets in turn
-                t = warp_stats(t, a.c);
+                t = warp_stats<false, 32>(t, a.c);
                 if (lane == 0)
-                    parts[b][warp] = t;
+                    parts[i & 1][warp] = t;
                 asm volatile("bar.sync 1, %0;" ::"n"(kRingConsumers) : "memory");
-                t = parts[b][lane & (kRingWarps - 1)];
-                t = warp_stats_16(t, a.c);
+                t = warp_stats<false, kRingWarps>(parts[i & 1][lane & (kRingWarps - 1)], a.c);
             }
 
             const OutRow<T> o(a.out, a.rows, row, r);
@@ -2146,7 +2228,7 @@ distill_ring_kernel(const __grid_constant__ DistillArgs a, uint64_t limit_ns)
                     g = row_grad<TAIL>(a, s);
                     zero = false;
                 } else {
-                    const RowLoss l = row_loss<TAIL>(a, s, t);
+                    const RowLoss l = row_loss<TAIL>(a, s, t, tid == 0);
                     g = l.grad;
                     zero = l.zero;
                     if (tid == 0) {
@@ -2161,18 +2243,37 @@ distill_ring_kernel(const __grid_constant__ DistillArgs a, uint64_t limit_ns)
                     const uint32_t q = seq + again + j;
                     if (j >= keep)
                         arrived(q);
-                    uint4 v[kUnroll], f[kUnroll];
-                    take(q, piece, v);
-                    release(q);
-                    const int c = r.w0 + piece * kPieceChunks + tid;
-                    if (!zero) {
+                    const int c = r.w0 + piece * kPieceChunks + tid, have = chunks_of(piece);
+                    if (zero) {
+                        release(q);
+                    } else if (have == kPieceChunks) {
+                        uint4 v[kUnroll], f[kUnroll];
+#pragma unroll
+                        for (int u = 0; u < kUnroll; ++u)
+                            v[u] = chunk(q, u);
+                        release(q);
                         row_gradient<T, kRingConsumers>(s, r, c, g, v, f);
                         store_chunks<T, kRingConsumers>(r, o, c, r.w1, f, amax, m2, a.status);
+                    } else {
+#pragma unroll 1
+                        for (int u = 0; u * kRingConsumers + warp * 32 < have; ++u) {
+                            uint4 v[1] = {neg_inf_chunk(T())}, f[1];
+                            if (u * kRingConsumers + tid < have)
+                                v[0] = chunk(q, u);
+                            row_gradient<T, kRingConsumers>(s, r, c + u * kRingConsumers, g, v, f);
+                            store_chunks<T, kRingConsumers>(r, o, c + u * kRingConsumers, r.w1, f,
+                                                            amax, m2, a.status);
+                        }
+                        release(q);
                     }
                 }
                 if (ec >= 0 && !zero) {
-                    row_gradient(s, r, ec, g, edge);
-                    store_elements(r, o, ec, edge, m2, a.status);
+                    float x[E];
+#pragma unroll
+                    for (int e = 0; e < E; ++e)
+                        x[e] = s.edge[warp][e];
+                    row_gradient(s, r, ec, g, x);
+                    store_elements(r, o, ec, x, m2, a.status);
                 }
                 seq += np + again;
             } else if (!BWD && alive && tid == 0) {
