@@ -1870,13 +1870,11 @@ distill_bwd_kernel(const __grid_constant__ DistillArgs a)
 }
 
 // Loss and gradient together, for short rows and for few.  A block, or a cluster
-// of C blocks, takes a row, each thread holding up to kNV of its chunks in
+// of C blocks, takes a row, each thread holding up to NV of its chunks in
 // registers between the two passes, so a row that fits is read once; a longer
 // one is walked in stretches and read again (from L2).
-constexpr int kNV = 8;
-
-template <typename T, bool TAIL>
-__global__ void __launch_bounds__(kThreads)
+template <typename T, bool TAIL, int NV>
+__global__ void __launch_bounds__(kThreads, NV > 4 ? 2 : 4)
 distill_fused_kernel(const __grid_constant__ DistillArgs a)
 {
     constexpr int E = Chunk<T>::E;
@@ -1905,8 +1903,8 @@ distill_fused_kernel(const __grid_constant__ DistillArgs a)
     uint32_t m2 = 0;
     bool zero = true;
     if (slots.any) {
-        uint4 v[kNV / kUnroll][kUnroll];
-        const bool fits = we - wb <= kNV * kThreads;
+        uint4 v[NV / kUnroll][kUnroll];
+        const bool fits = we - wb <= NV * kThreads;
         float edge[E];
         Stats t = stats_empty();
         if (ec >= 0) {
@@ -1921,13 +1919,13 @@ distill_fused_kernel(const __grid_constant__ DistillArgs a)
         }
         if (fits) {
 #pragma unroll
-            for (int h = 0; h < kNV / kUnroll; ++h)
+            for (int h = 0; h < NV / kUnroll; ++h)
 #pragma unroll
                 for (int u = 0; u < kUnroll; ++u)
                     v[h][u] = load_chunk(r, wb + (h * kUnroll + u) * kThreads + tid, we, total,
                                          a.status);
 #pragma unroll
-            for (int h = 0; h < kNV / kUnroll; ++h) {
+            for (int h = 0; h < NV / kUnroll; ++h) {
                 const int c = wb + h * kUnroll * kThreads + tid;
                 if (c < we) {
                     uint4 w[kUnroll];
@@ -1972,7 +1970,7 @@ distill_fused_kernel(const __grid_constant__ DistillArgs a)
             };
             if (fits) {
 #pragma unroll
-                for (int h = 0; h < kNV / kUnroll; ++h)
+                for (int h = 0; h < NV / kUnroll; ++h)
                     if (wb + h * kUnroll * kThreads + tid < we)
                         gradient(v[h], wb + h * kUnroll * kThreads + tid);
             } else {
@@ -2359,13 +2357,19 @@ cudaError_t distill_fwd(DistillArgs a, const DeviceInfo &dev, cudaStream_t st)
                               static_cast<unsigned>(a.cluster), a);
 }
 
-// The ring where a row does not fit one block's registers and there is at least
-// a row for every second SM.
+// The ring where a row is longer than a block holds in 4 registers a thread and
+// there is at least a row for every second SM.
+constexpr int kShortChunks = 4 * kThreads;
+
+template <typename T>
+int64_t most_chunks(const DistillArgs &a)
+{
+    return (static_cast<int64_t>(a.vocab) + 2 * Chunk<T>::E - 2) / Chunk<T>::E;
+}
 template <typename T>
 bool ring_takes(const DistillArgs &a, const DeviceInfo &dev)
 {
-    const int64_t chunks = (static_cast<int64_t>(a.vocab) + 2 * Chunk<T>::E - 2) / Chunk<T>::E;
-    return chunks > kNV * kThreads && 2 * a.rows >= dev.sm_count;
+    return most_chunks<T>(a) > kShortChunks && 2 * a.rows >= dev.sm_count;
 }
 
 template <typename T, bool TAIL, bool BWD>
@@ -2402,11 +2406,12 @@ cudaError_t distill_fused(DistillArgs a, const DeviceInfo &dev, cudaStream_t st)
 {
     if (ring_takes<T>(a, dev))
         return distill_ring<T, TAIL, false>(a, dev, st);
-    a.cluster = cluster_for(a.rows, (static_cast<int64_t>(a.vocab) + 2 * Chunk<T>::E - 2) / Chunk<T>::E,
-                            dev);
-    return launch_pdl_cluster(distill_fused_kernel<T, TAIL>,
-                              dim3(static_cast<unsigned>(a.rows * a.cluster)), dim3(kThreads), 0, st,
-                              static_cast<unsigned>(a.cluster), a);
+    a.cluster = cluster_for(a.rows, most_chunks<T>(a), dev);
+    const dim3 grid(static_cast<unsigned>(a.rows * a.cluster));
+    const unsigned c = static_cast<unsigned>(a.cluster);
+    if (most_chunks<T>(a) <= kShortChunks)
+        return launch_pdl_cluster(distill_fused_kernel<T, TAIL, 4>, grid, dim3(kThreads), 0, st, c, a);
+    return launch_pdl_cluster(distill_fused_kernel<T, TAIL, 8>, grid, dim3(kThreads), 0, st, c, a);
 }
 
 // What every call of this file asks of its logits.

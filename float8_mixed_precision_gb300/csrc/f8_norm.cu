@@ -257,8 +257,9 @@ __device__ __forceinline__ RowCopy row_copy(int64_t row, int64_t rows, int64_t c
     return c;
 }
 
-// N tensors' rows in one slot, each `pitch` bytes.
-template <typename T, int N>
+// N tensors' rows in one slot, each `pitch` bytes.  WHOLE: every row is whole
+// 16-byte pieces.
+template <typename T, int N, bool WHOLE>
 struct Ring {
     uint8_t *slots;
     uint64_t *full;
@@ -274,6 +275,14 @@ struct Ring {
     }
     __device__ __forceinline__ void fill(int slot, int64_t r) const
     {
+        if (WHOLE) {
+            const uint32_t bytes = static_cast<uint32_t>(cols) * sizeof(T);
+            mbar_arrive_expect_tx(&full[slot], N * bytes);
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                bulk_load(row(slot, i), src[i] + r * cols, bytes, &full[slot]);
+            return;
+        }
         const RowCopy c = row_copy<T>(r, rows, cols);
         mbar_arrive_expect_tx(&full[slot], N * c.bytes);
         if (c.bytes > 0) {
@@ -301,7 +310,7 @@ __device__ __forceinline__ void group_sync(int group)
 // The row's elements past the copied ones (of the tensor's last row only),
 // into the slot by the group's first threads.
 template <typename T, int N, int TPR>
-__device__ __forceinline__ void fill_tail(const Ring<T, N> &ring, int slot, int64_t r, int group,
+__device__ __forceinline__ void fill_tail(const Ring<T, N, false> &ring, int slot, int64_t r, int group,
                                           int t)
 {
     const RowCopy c = row_copy<T>(r, ring.rows, ring.cols);
@@ -424,8 +433,9 @@ __device__ __forceinline__ void pair_vector(const float2 (&f)[NV * VEC / 2], int
 }
 
 // Forward on the ring.  w and b stay in registers as fp32; the arithmetic takes
-// two elements per instruction.
-template <typename T, int VEC, int NV, int TPR>
+// two elements per instruction.  FULL: the row is as wide as the group's
+// registers, so no vector has to be asked for.
+template <typename T, int VEC, int NV, int TPR, bool FULL>
 __global__ void __launch_bounds__(block_threads(TPR), 768 / block_threads(TPR))
 norm_fwd_ring_kernel(const T *x, const void *__restrict__ w, const void *__restrict__ b, int w_type,
                      int rms, int64_t rows, int cols, float eps, T *y, float *__restrict__ mean,
@@ -439,7 +449,7 @@ norm_fwd_ring_kernel(const T *x, const void *__restrict__ w, const void *__restr
     __shared__ __align__(16) float red[4 * block_threads(TPR) / 32];
     __shared__ __align__(8) uint64_t full[kGroups * kMaxStages];
     const int group = threadIdx.x / TPR, t = threadIdx.x % TPR;
-    Ring<T, 1> ring{dyn + static_cast<size_t>(group) * stages * pitch,
+    Ring<T, 1, (VEC > 1)> ring{dyn + static_cast<size_t>(group) * stages * pitch,
                     full + group * kMaxStages, stages, pitch, rows, cols, {x}, true};
     if (t == 0) {
         for (int i = 0; i < stages; ++i)
@@ -458,16 +468,19 @@ norm_fwd_ring_kernel(const T *x, const void *__restrict__ w, const void *__restr
     float2 fw[P], fb[P];
     param_pairs<VEC, NV, TPR>(w, w_type, cols, t, fw, status);
     param_pairs<VEC, NV, TPR>(b, w_type, cols, t, fb, status);
-    const int nvec = cols / VEC;
+    const int nvec = FULL ? NV * TPR : cols / VEC;
     const float inv_c = 1.0f / static_cast<float>(cols);
     const int64_t total = rows * cols;
     uint32_t m2 = 0;
     int buf = 0, slot = 0;
     uint32_t parity = 0;
-    for (int64_t row = row0; row < rows; row += step) {
+    const int64_t ahead = stages * step;
+    R *out = reinterpret_cast<R *>(y + row0 * cols) + t;
+    const int64_t out_step = step * nvec;
+    for (int64_t row = row0; row < rows; row += step, out += out_step) {
         ring.wait(slot, parity, limit_ns, status);
         int shift = 0;
-        if (VEC == 1) {
+        if constexpr (VEC == 1) {
             shift = row_copy<T>(row, rows, cols).shift;
             fill_tail<T, 1, TPR>(ring, slot, row, group, t);
         }
@@ -511,8 +524,8 @@ norm_fwd_ring_kernel(const T *x, const void *__restrict__ w, const void *__restr
             1.0f / sqrtf(ring_sum<TPR, false>(q.x + q.y, 0.0f, red, group, buf).x * inv_c + eps);
         // every thread has taken its part of the row: the slot can be refilled
         if (t == 0) {
-            if (row + stages * step < rows)
-                ring.fill(slot, row + stages * step);
+            if (row + ahead < rows)
+                ring.fill(slot, row + ahead);
             if (mean != nullptr && !rms)
                 mean[row] = mu;
             if (rstd != nullptr)
@@ -522,18 +535,18 @@ norm_fwd_ring_kernel(const T *x, const void *__restrict__ w, const void *__restr
 #pragma unroll
         for (int i = 0; i < P; ++i)
             f[i] = __ffma2_rn(__fmul2_rn(f[i], r2), fw[i], fb[i]);
-        const int64_t at = row * cols;
 #pragma unroll
         for (int u = 0; u < NV; ++u) {
-            const int64_t i = u * TPR + t;
+            const int i = u * TPR + t;
             if (i < nvec) {
                 float o[VEC];
                 pair_vector<VEC, NV>(f, u, o);
                 R p;
                 pack<T>(o, p);
-                m2 = abs_max2(m2, p);
-                if (in_range(at + i * VEC, VEC, total, status))
-                    *reinterpret_cast<R *>(y + at + i * VEC) = p;
+                if (amax_mode != kAmaxNone)
+                    m2 = abs_max2(m2, p);
+                if (in_range(row * cols + i * VEC, VEC, total, status))
+                    out[u * TPR] = p;
             }
         }
         if (++slot == stages) {
@@ -717,7 +730,7 @@ norm_fwd_wide_kernel(const T *x, const void *__restrict__ w, const void *__restr
 // block.  Elements past the row are 0 and add nothing anywhere.
 constexpr int kBwdThreads = 512;
 
-template <typename T, int VEC, int NV, int TPR>
+template <typename T, int VEC, int NV, int TPR, bool FULL>
 __global__ void __launch_bounds__(kBwdThreads, 1)
 norm_bwd_ring_kernel(const T *dy, const T *x, const void *__restrict__ w, int w_type,
                      const float *__restrict__ mean, const float *__restrict__ rstd, int rms,
@@ -731,7 +744,7 @@ norm_bwd_ring_kernel(const T *dy, const T *x, const void *__restrict__ w, int w_
     __shared__ __align__(16) float red[4 * kBwdThreads / 32];
     __shared__ __align__(8) uint64_t full[kGroups * kMaxStages];
     const int group = threadIdx.x / TPR, t = threadIdx.x % TPR;
-    Ring<T, 2> ring{dyn + static_cast<size_t>(group) * stages * 2 * pitch,
+    Ring<T, 2, (VEC > 1)> ring{dyn + static_cast<size_t>(group) * stages * 2 * pitch,
                     full + group * kMaxStages, stages, pitch, rows, cols, {x, dy}, true};
     if (t == 0) {
         for (int i = 0; i < stages; ++i)
@@ -752,7 +765,7 @@ norm_bwd_ring_kernel(const T *dy, const T *x, const void *__restrict__ w, int w_
 #pragma unroll
     for (int i = 0; i < P; ++i)
         aw[i] = ab[i] = make_float2(0.0f, 0.0f);
-    const int nvec = cols / VEC;
+    const int nvec = FULL ? NV * TPR : cols / VEC;
     const float inv_c = 1.0f / static_cast<float>(cols);
     const int64_t total = rows * cols;
     int buf = 0, slot = 0;
@@ -763,7 +776,10 @@ norm_bwd_ring_kernel(const T *dy, const T *x, const void *__restrict__ w, int w_
         mu_next = rms ? 0.0f : mean[row0];
         r_next = rstd[row0];
     }
-    for (int64_t row = row0; row < rows; row += step) {
+    const int64_t ahead = stages * step;
+    R *out = reinterpret_cast<R *>(dx + row0 * cols) + t;
+    const int64_t out_step = step * nvec;
+    for (int64_t row = row0; row < rows; row += step, out += out_step) {
         const float mu = mu_next, r = r_next;
         if (row + step < rows) {
             mu_next = rms ? 0.0f : mean[row + step];
@@ -771,7 +787,7 @@ norm_bwd_ring_kernel(const T *dy, const T *x, const void *__restrict__ w, int w_
         }
         ring.wait(slot, parity, limit_ns, status);
         int shift = 0;
-        if (VEC == 1) {
+        if constexpr (VEC == 1) {
             shift = row_copy<T>(row, rows, cols).shift;
             fill_tail<T, 2, TPR>(ring, slot, row, group, t);
         }
@@ -793,25 +809,24 @@ norm_bwd_ring_kernel(const T *dy, const T *x, const void *__restrict__ w, int w_
             s2 = __fadd2_rn(s2, g[i]);
         }
         const float2 c = ring_sum<TPR, true>(s1.x + s1.y, s2.x + s2.y, red, group, buf);
-        if (t == 0 && row + stages * step < rows)
-            ring.fill(slot, row + stages * step);
+        if (t == 0 && row + ahead < rows)
+            ring.fill(slot, row + ahead);
         if (dx != nullptr) {
             const float k1 = -r * (c.x * inv_c), k2 = rms ? 0.0f : -r * (c.y * inv_c);
             const float2 n1 = make_float2(k1, k1), n2 = make_float2(k2, k2);
-            const int64_t at = row * cols;
 #pragma unroll
             for (int i = 0; i < P; ++i)
                 g[i] = __ffma2_rn(g[i], r2, __ffma2_rn(xh[i], n1, n2));
 #pragma unroll
             for (int u = 0; u < NV; ++u) {
-                const int64_t i = u * TPR + t;
+                const int i = u * TPR + t;
                 if (i < nvec) {
                     float o[VEC];
                     pair_vector<VEC, NV>(g, u, o);
                     R p;
                     pack<T>(o, p);
-                    if (in_range(at + i * VEC, VEC, total, status))
-                        *reinterpret_cast<R *>(dx + at + i * VEC) = p;
+                    if (in_range(row * cols + i * VEC, VEC, total, status))
+                        out[u * TPR] = p;
                 }
             }
         }
@@ -1162,33 +1177,39 @@ RingPlan ring_plan(int64_t rows, int64_t cols, int esize, int groups, int per_sm
 
 constexpr int fwd_blocks(int tpr) { return 768 / block_threads(tpr); }
 
-template <typename T, int VEC, int NV, int TPR>
+template <typename T, int VEC, int NV, int TPR, bool FULL = false>
 cudaError_t fwd_ring(const FwdArgs &a, const DeviceInfo &dev, cudaStream_t st, int *nparts)
 {
+    if constexpr (VEC > 1 && !FULL)
+        if (a.cols == NV * VEC * TPR)
+            return fwd_ring<T, VEC, NV, TPR, true>(a, dev, st, nparts);
     const RingPlan p = ring_plan(a.rows, a.cols, sizeof(T), block_threads(TPR) / TPR,
                                  fwd_blocks(TPR), 1, dev);
-    const cudaError_t e = allow_ring<norm_fwd_ring_kernel<T, VEC, NV, TPR>>(dev);
+    const cudaError_t e = allow_ring<norm_fwd_ring_kernel<T, VEC, NV, TPR, FULL>>(dev);
     if (e != cudaSuccess)
         return e;
     if (nparts != nullptr)
         *nparts = p.grid;
-    return launch_pdl(norm_fwd_ring_kernel<T, VEC, NV, TPR>, dim3(p.grid), dim3(block_threads(TPR)),
+    return launch_pdl(norm_fwd_ring_kernel<T, VEC, NV, TPR, FULL>, dim3(p.grid), dim3(block_threads(TPR)),
                       p.smem, st, static_cast<const T *>(a.x), a.w, a.b, a.w_type, a.rms, a.rows,
                       static_cast<int>(a.cols), a.eps, static_cast<T *>(a.y), a.mean, a.rstd, a.amax,
                       a.amax_mode, p.stages, p.pitch, wait_limit_ns(), dev.status);
 }
 
-template <typename T, int VEC, int NV, int TPR>
+template <typename T, int VEC, int NV, int TPR, bool FULL = false>
 cudaError_t bwd_ring(const BwdArgs &a, const DeviceInfo &dev, cudaStream_t st, int *nparts)
 {
+    if constexpr (VEC > 1 && !FULL)
+        if (a.cols == NV * VEC * TPR)
+            return bwd_ring<T, VEC, NV, TPR, true>(a, dev, st, nparts);
     const RingPlan p = ring_plan(a.rows, a.cols, sizeof(T), kBwdThreads / TPR, 1, 2, dev);
-    const cudaError_t e = allow_ring<norm_bwd_ring_kernel<T, VEC, NV, TPR>>(dev);
+    const cudaError_t e = allow_ring<norm_bwd_ring_kernel<T, VEC, NV, TPR, FULL>>(dev);
     if (e != cudaSuccess)
         return e;
     *nparts = p.grid;
     // the join at the end needs a float2 per thread
     const size_t smem = std::max<size_t>(p.smem, sizeof(float2) * kBwdThreads);
-    return launch_pdl(norm_bwd_ring_kernel<T, VEC, NV, TPR>, dim3(p.grid), dim3(kBwdThreads), smem,
+    return launch_pdl(norm_bwd_ring_kernel<T, VEC, NV, TPR, FULL>, dim3(p.grid), dim3(kBwdThreads), smem,
                       st, static_cast<const T *>(a.dy), static_cast<const T *>(a.x), a.w, a.w_type,
                       a.mean, a.rstd, a.rms, a.rows, static_cast<int>(a.cols),
                       static_cast<T *>(a.dx), a.parts, p.stages, p.pitch, wait_limit_ns(),
