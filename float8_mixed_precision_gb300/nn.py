@@ -16,17 +16,25 @@ modules whose linears have no bias (as in Llama):
   and its amax, and the SwiGLU backward forming d(AB) with its amax.
 - to_float8_linears: swaps eligible nn.Linear modules of a model for
   Float8Linear modules that share their weight Parameter.
+- LayerNorm, RMSNorm: the norm in front of a linear (f8_norm_fwd,
+  f8_norm_bwd).
+- token_logprobs, distill_loss: what a model learns from the logits of a head
+  linear (f8_token_logprobs, f8_distill_fwd and their gradients), for heads
+  padded past the vocabulary too.
 
-Inputs and weights must be bf16 CUDA tensors with every size a multiple of
-16 (the ABI's rule); anything else raises, there is no fallback path.
+Inputs and weights of the linears must be bf16 CUDA tensors with every size a
+multiple of 16 (the ABI's rule); the norms and the logits' functions take bf16
+and fp32 CUDA tensors of any size.  Anything else raises, there is no fallback
+path.
 """
 from __future__ import annotations
 
 from typing import Callable
 
 import torch
+from torch.autograd.function import once_differentiable
 
-from . import binding
+from . import binding, ops
 
 
 class _Float8LinearFn(torch.autograd.Function):
@@ -375,3 +383,188 @@ def to_float8_linears(module: torch.nn.Module,
         raise ValueError("the module itself is a linear: use Float8Linear.from_linear")
     visit(module, "")
     return module
+
+
+class _NormFn(torch.autograd.Function):
+    """f8_norm_fwd over the last dimension; backward from its input and fp32
+    statistics (f8_norm_bwd)."""
+
+    @staticmethod
+    def forward(ctx, x: torch.Tensor, w: torch.Tensor, b: torch.Tensor | None, kind: int,
+                eps: float) -> torch.Tensor:
+        x2 = x.reshape(-1, x.shape[-1]).contiguous()
+        w = w.contiguous()
+        y, mean, rstd = ops.f8_norm_fwd(x2, w, b if b is None else b.contiguous(), kind=kind, eps=eps)
+        ctx.save_for_backward(x2, w, mean, rstd)
+        ctx.kind = kind
+        ctx.x_shape = x.shape
+        return y.reshape(x.shape)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy: torch.Tensor):
+        x2, w, mean, rstd = ctx.saved_tensors
+        want_dx, want_dw, want_db = ctx.needs_input_grad[:3]
+        dx, dw, db = ops.f8_norm_bwd(dy.reshape(x2.shape).contiguous(), x2, w, mean, rstd,
+                                     kind=ctx.kind, want_dx=want_dx, want_dw=want_dw,
+                                     want_db=want_db)
+        return dx.reshape(ctx.x_shape) if want_dx else None, dw, db, None, None
+
+
+class _Norm(torch.nn.Module):
+    def __init__(self, dim: int, eps: float, bias: bool, device, dtype,
+                 weight: torch.nn.Parameter | None, b: torch.nn.Parameter | None):
+        super().__init__()
+        if dim < 1:
+            raise ValueError("a norm needs at least one feature")
+        for name, p in (("weight", weight), ("bias", b)):
+            if p is not None and tuple(p.shape) != (dim,):
+                raise ValueError(f"{name} must be [{dim}]")
+        self.dim, self.eps = dim, float(eps)
+        self.weight = torch.nn.Parameter(torch.ones(dim, device=device, dtype=dtype)) if weight is None else weight
+        if bias and b is None:
+            b = torch.nn.Parameter(torch.zeros_like(self.weight))
+        self.register_parameter("bias", b)
+
+    def forward(self, x: torch.Tensor) -> torch.Tensor:
+        if x.dim() < 1 or x.shape[-1] != self.dim:
+            raise ValueError(f"expected {self.dim} features")
+        return _NormFn.apply(x, self.weight, self.bias, self._kind, self.eps)
+
+    def extra_repr(self) -> str:
+        return f"{self.dim}, eps={self.eps}, bias={self.bias is not None}"
+
+
+class LayerNorm(_Norm):
+    """y = (x - mean) / sqrt(var + eps) * weight + bias over the last
+    dimension, bf16 or fp32, with fp32 statistics; weight and bias of either
+    type."""
+    _kind = binding.F8_LAYER_NORM
+
+    def __init__(self, dim: int, eps: float = 1e-5, bias: bool = True, device=None,
+                 dtype=torch.bfloat16):
+        super().__init__(dim, eps, bias, device, dtype, None, None)
+
+    @classmethod
+    def from_norm(cls, norm: torch.nn.LayerNorm) -> "LayerNorm":
+        """A LayerNorm that shares the Parameters of a torch LayerNorm."""
+        if len(norm.normalized_shape) != 1 or norm.weight is None:
+            raise ValueError("LayerNorm takes one normalised dimension and a weight")
+        self = cls.__new__(cls)
+        _Norm.__init__(self, norm.normalized_shape[0], norm.eps, False, None, None, norm.weight,
+                       norm.bias)
+        return self
+
+
+class RMSNorm(_Norm):
+    """y = x / sqrt(mean(x^2) + eps) * weight over the last dimension, bf16 or
+    fp32, with fp32 statistics; the weight of either type."""
+    _kind = binding.F8_RMS_NORM
+
+    def __init__(self, dim: int, eps: float = 1e-5, device=None, dtype=torch.bfloat16):
+        super().__init__(dim, eps, False, device, dtype, None, None)
+
+    @classmethod
+    def from_norm(cls, norm: torch.nn.RMSNorm) -> "RMSNorm":
+        """An RMSNorm that shares the weight of a torch RMSNorm (with an eps
+        of its own: torch's default follows the input's type)."""
+        if len(norm.normalized_shape) != 1 or norm.weight is None or norm.eps is None:
+            raise ValueError("RMSNorm takes one normalised dimension, a weight and an eps")
+        self = cls.__new__(cls)
+        _Norm.__init__(self, norm.normalized_shape[0], norm.eps, False, None, None, norm.weight, None)
+        return self
+
+
+def _logit_rows(logits: torch.Tensor, vocab: int | None):
+    """Logits [..., width] as dense rows, and the view of their first `vocab`
+    columns: a head linear's rows are padded to a multiple of 16."""
+    if logits.dim() < 1:
+        raise ValueError("logits must have a vocabulary dimension")
+    width = logits.shape[-1]
+    vocab = width if vocab is None else vocab
+    if not 1 <= vocab <= width:
+        raise ValueError("vocab must be between 1 and the logits' last dimension")
+    rows = logits.reshape(-1, width).contiguous()
+    return rows, rows[:, :vocab]
+
+
+def _row_grad(g: torch.Tensor | None) -> torch.Tensor | None:
+    return None if g is None else g.reshape(-1).contiguous()
+
+
+class _TokenLogprobsFn(torch.autograd.Function):
+    """f8_token_logprobs; the gradient is written at the logits' own width,
+    zero past the vocabulary (f8_token_logprobs_bwd)."""
+
+    @staticmethod
+    def forward(ctx, logits: torch.Tensor, tokens: torch.Tensor, temperature: float,
+                vocab: int | None):
+        rows, view = _logit_rows(logits, vocab)
+        flat = tokens.reshape(-1).contiguous()
+        logp, entropy, lse, _, _ = ops.f8_token_logprobs(view, flat, temperature=temperature)
+        ctx.save_for_backward(rows, flat, lse, entropy)
+        ctx.set_materialize_grads(False)
+        ctx.temperature, ctx.vocab, ctx.shape = temperature, view.shape[1], logits.shape
+        lead = logits.shape[:-1]
+        return logp.reshape(lead), entropy.reshape(lead)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dlogp, dentropy):
+        rows, flat, lse, entropy = ctx.saved_tensors
+        if dlogp is None and dentropy is None:
+            return None, None, None, None
+        d = ops.f8_token_logprobs_bwd(rows[:, :ctx.vocab], flat, lse, entropy, _row_grad(dlogp),
+                                      _row_grad(dentropy), temperature=ctx.temperature,
+                                      dlogits=torch.empty_like(rows))
+        return d.reshape(ctx.shape), None, None, None
+
+
+def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, temperature: float = 1.0,
+                   vocab: int | None = None):
+    """(log probability of `tokens`, entropy), both fp32 and differentiable, of
+    the distributions logits / temperature over the first `vocab` columns of
+    logits [..., width]; tokens int64 [...], negative where ignored."""
+    if tuple(tokens.shape) != tuple(logits.shape[:-1]):
+        raise ValueError("tokens must have the logits' leading shape")
+    return _TokenLogprobsFn.apply(logits, tokens, float(temperature), vocab)
+
+
+class _DistillFn(torch.autograd.Function):
+    """f8_distill_fwd; the gradient is written at the logits' own width, zero
+    past the vocabulary (f8_distill_bwd)."""
+
+    @staticmethod
+    def forward(ctx, logits: torch.Tensor, ids: torch.Tensor, values: torch.Tensor,
+                temperature: float, tail: bool, vocab: int | None) -> torch.Tensor:
+        rows, view = _logit_rows(logits, vocab)
+        k = ids.shape[-1]
+        ids2, values2 = ids.reshape(-1, k).contiguous(), values.reshape(-1, k).contiguous()
+        loss, lse, rest = ops.f8_distill_fwd(view, ids2, values2, temperature=temperature, tail=tail)
+        ctx.save_for_backward(rows, ids2, values2, lse, rest)
+        ctx.temperature, ctx.tail, ctx.vocab, ctx.shape = temperature, tail, view.shape[1], logits.shape
+        return loss.reshape(logits.shape[:-1])
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dloss: torch.Tensor):
+        rows, ids, values, lse, rest = ctx.saved_tensors
+        d = ops.f8_distill_bwd(rows[:, :ctx.vocab], ids, values, lse, rest, _row_grad(dloss),
+                               temperature=ctx.temperature, tail=ctx.tail,
+                               dlogits=torch.empty_like(rows))
+        return d.reshape(ctx.shape), None, None, None, None, None
+
+
+def distill_loss(logits: torch.Tensor, ids: torch.Tensor, values: torch.Tensor,
+                 temperature: float = 1.0, tail: bool = False,
+                 vocab: int | None = None) -> torch.Tensor:
+    """The distillation loss [...] (fp32) of logits [..., width] over the first
+    `vocab` columns, against the teacher's top alternatives: ids int32 and log
+    probabilities values fp32, both [..., k], an id below zero for an empty
+    slot.  `tail` counts the rest of the vocabulary as one more class.  A step
+    that knows each row's weight beforehand calls f8_distill_fwd_bwd instead:
+    loss and gradient in one pass over the logits."""
+    lead = tuple(logits.shape[:-1])
+    if ids.dim() < 1 or tuple(ids.shape[:-1]) != lead or ids.shape != values.shape:
+        raise ValueError("ids and values must be [..., k] with the logits' leading shape")
+    return _DistillFn.apply(logits, ids, values, float(temperature), bool(tail), vocab)
