@@ -357,20 +357,6 @@ struct Stats {
 
 __device__ __forceinline__ Stats stats_empty() { return Stats{F8_NEG_INF, 0.0f, 0.0f}; }
 
-template <bool ENT>
-__device__ __forceinline__ Stats join(Stats a, Stats b, float c)
-{
-    const float M = fmaxf(a.m, b.m);
-    // -inf - -inf is NaN here, which fmaxf turns into the floor: factor 0
-    const float da = fmaxf((a.m - M) * c, kFloor2), db = fmaxf((b.m - M) * c, kFloor2);
-    const float fa = ex2(da), fb = ex2(db);
-    Stats r;
-    r.m = M;
-    r.s = a.s * fa + b.s * fb;
-    r.h = ENT ? fa * fmaf(a.s, da, a.h) + fb * fmaf(b.s, db, b.h) : 0.0f;
-    return r;
-}
-
 // The sums' reference grows to bm.
 template <bool ENT>
 __device__ __forceinline__ void raise_max(Stats &t, float bm, float c)
@@ -504,6 +490,14 @@ __device__ __forceinline__ Stats block_join(Stats t, float c, Stats *red)
         red[threadIdx.x >> 5] = t;
     __syncthreads();
     return warp_stats<ENT, kWarps>(red[threadIdx.x & (kWarps - 1)], c);
+}
+
+// The sums of `n` blocks, in every thread.
+template <bool ENT>
+__device__ __forceinline__ Stats cluster_stats(const Stats *parts, int n, float c)
+{
+    const int i = threadIdx.x & (kMaxCluster - 1);
+    return warp_stats<ENT, kMaxCluster>(i < n ? parts[i] : stats_empty(), c);
 }
 
 // ------------------------------------------------------------ clusters
@@ -652,7 +646,7 @@ __device__ __forceinline__ void block_select(const uint32_t *keys, int n, int k,
 
 // The k-th largest of the block's keys, one per thread (k <= kThreads), by seven
 // pivots a round: the largest t with at least k keys >= t, or a lower one with
-// exactly k.  `cnt`: three sets of eight counters, zero at the start.
+// few more than k.  `cnt`: three sets of eight counters, zero at the start.
 __device__ __forceinline__ uint32_t block_threshold(uint32_t key, int k, int *red, int *cnt)
 {
     const int tid = threadIdx.x, lane = tid & 31;
@@ -692,17 +686,29 @@ __device__ __forceinline__ uint32_t block_threshold(uint32_t key, int k, int *re
             hi = lo + (above + 1) * step - 1;
         lo += above * step;
         set = next;
-        if (above > 0 && at == k)
+        if (above > 0 && at <= k + k / 4)
             break;
     }
     return lo;
+}
+
+// A value's key and its position as one number: of two items the larger comes
+// first, by value, then by position.  0 is no item.
+__device__ __forceinline__ uint64_t item_of(uint32_t key, int id)
+{
+    return static_cast<uint64_t>(key) << 32 | ~static_cast<uint32_t>(id);
+}
+__device__ __forceinline__ uint32_t item_key(uint64_t v) { return static_cast<uint32_t>(v >> 32); }
+__device__ __forceinline__ int item_id(uint64_t v)
+{
+    return static_cast<int>(~static_cast<uint32_t>(v));
 }
 
 // Shared memory of the top-k stage, in 4-byte words; every part starts on a
 // 16-byte boundary.
 constexpr int kCandidates = 2048;
 struct TopLayout {
-    int groups, list, keys, pick, cand_key, cand_id, best_key, best_id, merge_key, merge_id, words;
+    int groups, list, keys, pick, cand, best, merge, words;
 };
 __host__ __device__ inline int words4(int n) { return (n + 3) & ~3; }
 __host__ __device__ inline TopLayout top_layout(int ngroups, int k, int cluster)
@@ -710,20 +716,17 @@ __host__ __device__ inline TopLayout top_layout(int ngroups, int k, int cluster)
     TopLayout l;
     l.groups = 0;                         // one key per group of 32 chunks
     l.list = l.groups + words4(ngroups);  // k positions
-    l.keys = l.list + words4(k);          // 32 k chunk keys, then E k element keys
+    l.keys = l.list + words4(k);          // 32 k chunk keys
     l.pick = l.keys + 32 * k;             // k chunks
-    l.cand_key = l.pick + words4(k);
-    l.cand_id = l.cand_key + kCandidates;
-    l.best_key = l.cand_id + kCandidates;  // the block's k best, in order
-    l.best_id = l.best_key + words4(k);
-    l.merge_key = l.best_id + words4(k);
-    l.merge_id = l.merge_key + (cluster > 1 ? words4(cluster * k) : 0);
-    l.words = l.merge_id + (cluster > 1 ? words4(cluster * k) : 0);
+    l.cand = l.pick + words4(k);          // items from here on, two words each
+    l.best = l.cand + 2 * kCandidates;    // the block's k best, in order
+    l.merge = l.best + words4(2 * k);     // every block's, in the cluster's first
+    l.words = l.merge + (cluster > 1 ? words4(2 * cluster * k) : 0);
     return l;
 }
 
-// The k largest elements of chunks [32 g0, 32 g1) of a row, in order, in
-// best_key / best_id of `lay`; gkeys holds the groups' largest keys, tkey the
+// The k largest elements of chunks [32 g0, 32 g1) of a row, in order, in the
+// items `best` of `lay`; gkeys holds the groups' largest keys, tkey the
 // key of the largest element that this thread has seen.  The k-th largest of
 // the threads' is no larger than the k-th largest element, so: that threshold,
 // a look at the groups that reach it, and their elements >= it ranked against
@@ -740,9 +743,8 @@ __device__ __forceinline__ void block_top(const Row<T> &r, int g0, int g1, int k
     constexpr int E = Chunk<T>::E;
     const int tid = threadIdx.x, lane = tid & 31;
     uint32_t *gkeys = dyn + lay.groups, *keys = dyn + lay.keys;
-    uint32_t *ck = dyn + lay.cand_key, *bk = dyn + lay.best_key;
-    int *ci = reinterpret_cast<int *>(dyn + lay.cand_id);
-    int *bi = reinterpret_cast<int *>(dyn + lay.best_id);
+    uint64_t *cand = reinterpret_cast<uint64_t *>(dyn + lay.cand);
+    uint64_t *best = reinterpret_cast<uint64_t *>(dyn + lay.best);
     int *list = reinterpret_cast<int *>(dyn + lay.list);
     const int ng = g1 - g0;
     auto load = [&](int ch, float (&x)[E]) {
@@ -751,9 +753,7 @@ __device__ __forceinline__ void block_top(const Row<T> &r, int g0, int g1, int k
         else
             load_edge(r, ch, x, total, status);
     };
-    auto offer = [&](int ch, uint32_t t) {
-        float x[E];
-        load(ch, x);
+    auto offer = [&](int ch, const float(&x)[E], uint32_t t) {
         if (order_key(max_of(x)) < t)
             return;
 #pragma unroll
@@ -762,10 +762,8 @@ __device__ __forceinline__ void block_top(const Row<T> &r, int g0, int g1, int k
             const uint32_t key = order_key(x[e]);
             if (v >= 0 && v < r.vocab && key >= t) {
                 const int at = atomicAdd(ncand, 1);
-                if (at < kCandidates) {
-                    ck[at] = key;
-                    ci[at] = v;
-                }
+                if (at < kCandidates)
+                    cand[at] = item_of(key, v);
             }
         }
     };
@@ -783,12 +781,31 @@ __device__ __forceinline__ void block_top(const Row<T> &r, int g0, int g1, int k
         __syncthreads();
     };
     const uint32_t t = block_threshold(tkey, k, red, cnt);
-    for (int i = tid - lane; i < ng; i += kThreads) {  // a lane asks for a group, its warp looks at it
-        unsigned reach = __ballot_sync(0xFFFFFFFFu, i + lane < ng && gkeys[i + lane] >= t);
-        for (; reach != 0; reach &= reach - 1) {
-            const int ch = (g0 + i + __ffs(reach) - 1) * 32 + lane;
-            if (ch < r.nch)
-                offer(ch, t);
+    // a lane asks for a group, its warp looks at those that reach t, kLook at a
+    // time; neighbouring groups go to different warps
+    constexpr int kLook = 4;
+    for (int i = tid >> 5; i < ng; i += kThreads) {
+        unsigned reach = __ballot_sync(0xFFFFFFFFu, i + lane * kWarps < ng && gkeys[i + lane * kWarps] >= t);
+        while (reach != 0) {
+            int ch[kLook];
+            uint4 v[kLook];
+#pragma unroll
+            for (int u = 0; u < kLook; ++u) {
+                ch[u] = reach != 0 ? (g0 + i + (__ffs(reach) - 1) * kWarps) * 32 + lane : r.nch;
+                reach &= reach - 1;
+                v[u] = load_chunk(r, ch[u], r.nch, total, status);
+            }
+#pragma unroll
+            for (int u = 0; u < kLook; ++u) {
+                if (ch[u] < r.nch) {
+                    float x[E];
+                    if (r.whole(ch[u]))
+                        unpack<T>(v[u], x);
+                    else
+                        load_edge(r, ch[u], x, total, status);
+                    offer(ch[u], x, t);
+                }
+            }
         }
     }
     __syncthreads();
@@ -806,28 +823,23 @@ __device__ __forceinline__ void block_top(const Row<T> &r, int g0, int g1, int k
         for (int i = tid; i < kc * E; i += kThreads) {
             const int v = pick[i / E] * E + i % E - r.off;
             const bool in = v >= 0 && v < r.vocab;
-            ck[i] = in ? order_key(as_float(r.base[r.off + v])) : 0u;
-            ci[i] = in ? v : 0x7FFFFFFF;
+            cand[i] = in ? item_of(order_key(as_float(r.base[r.off + v])), v) : 0u;
         }
         __syncthreads();
         n = kc * E;
     }
     // each candidate's rank among them
     for (int i = tid; i < n; i += kThreads) {
-        const uint32_t key = ck[i];
-        const int id = ci[i];
+        const uint64_t v = cand[i];
         int place = 0;
+#pragma unroll 8
         for (int j = 0; j < n; ++j)
-            place += ck[j] > key || (ck[j] == key && ci[j] < id) ? 1 : 0;
-        if (place < have) {
-            bk[place] = key;
-            bi[place] = id;
-        }
+            place += cand[j] > v ? 1 : 0;
+        if (place < have)
+            best[place] = v;
     }
-    for (int i = have + tid; i < k; i += kThreads) {
-        bk[i] = 0;
-        bi[i] = 0x7FFFFFFF;
-    }
+    for (int i = have + tid; i < k; i += kThreads)
+        best[i] = 0;
     __syncthreads();
 }
 
@@ -958,12 +970,10 @@ logprobs_kernel(const __grid_constant__ LogprobArgs a)
         block_top<T>(r, g0, g1, k, have, tkey, dyn, lay, sred, cnt, &ncand, total, a.status);
         if (C > 1) {  // into the leader's merge arrays
             cluster_started();
-            uint32_t *mk = peer(dyn + lay.merge_key + rank * k, 0);
-            uint32_t *mi = peer(dyn + lay.merge_id + rank * k, 0);
-            for (int i = tid; i < k; i += kThreads) {
-                mk[i] = dyn[lay.best_key + i];
-                mi[i] = dyn[lay.best_id + i];
-            }
+            const uint64_t *best = reinterpret_cast<const uint64_t *>(dyn + lay.best);
+            uint64_t *m = peer(reinterpret_cast<uint64_t *>(dyn + lay.merge) + rank * k, 0);
+            for (int i = tid; i < k; i += kThreads)
+                m[i] = best[i];
         }
     } else if (C > 1) {
         cluster_started();
@@ -974,9 +984,7 @@ logprobs_kernel(const __grid_constant__ LogprobArgs a)
         cluster_join();
         if (rank != 0)
             return;
-        t = parts[0];
-        for (int i = 1; i < C; ++i)
-            t = join<true>(t, parts[i], a.c);
+        t = cluster_stats<true>(parts, C, a.c);
     } else {
         __syncthreads();
     }
@@ -1011,42 +1019,43 @@ logprobs_kernel(const __grid_constant__ LogprobArgs a)
     }
     if (TOP) {
         const int k = a.top_k;
-        auto put = [&](int place, uint32_t key, uint32_t id) {
-            a.top_ids[row * k + place] = static_cast<int32_t>(id);
+        auto put = [&](int place, uint64_t v) {
+            a.top_ids[row * k + place] = item_id(v);
             a.top_logp[row * k + place] =
                 none ? F8_NEG_INF
                      : (lse != lse ? F8_NAN
-                                   : fminf((key_value(key) - t.m) * a.inv_t - ls, 0.0f));
+                                   : fminf((key_value(item_key(v)) - t.m) * a.inv_t - ls, 0.0f));
         };
         if (C == 1) {
+            const uint64_t *best = reinterpret_cast<const uint64_t *>(dyn + lay.best);
             for (int i = tid; i < k; i += kThreads)
-                put(i, dyn[lay.best_key + i], dyn[lay.best_id + i]);
+                put(i, best[i]);
             return;
         }
-        // the blocks' lists are in order, and a later block's ids are larger: an
-        // item's place is its own plus what each other list has before it
-        const uint32_t *mk = dyn + lay.merge_key;
-        const uint32_t *mi = dyn + lay.merge_id;
+        // the blocks' lists are in order: an item's place is its own plus how many
+        // of each other list come before it; the lists' first items first, so that
+        // whole warps are done once their items have dropped out
+        constexpr int kLists = 4;
+        const uint64_t *m = reinterpret_cast<const uint64_t *>(dyn + lay.merge);
+        const int half = 1 << (31 - __clz(k));  // the largest power of two <= k
         for (int i = tid; i < C * k; i += kThreads) {
-            const uint32_t key = mk[i];
-            const int own = i / k;
-            int place = i % k;
-            for (int l = 0; l < C; ++l) {
-                if (l == own)
-                    continue;
-                int lo = 0, hi = k;  // first of list l that does not come before
-                while (lo < hi) {
-                    const int mid = (lo + hi) / 2;
-                    const uint32_t o = mk[l * k + mid];
-                    if (o > key || (o == key && l < own))
-                        lo = mid + 1;
-                    else
-                        hi = mid;
+            const int own = i % C;
+            int place = i / C;
+            const uint64_t v = m[own * k + place];
+            for (int l = 0; l < C && place < k; l += kLists) {
+                int at[kLists] = {};
+                for (int s = half; s > 0; s >>= 1) {
+#pragma unroll
+                    for (int u = 0; u < kLists; ++u)
+                        if (l + u < C && at[u] + s <= k && m[(l + u) * k + at[u] + s - 1] > v)
+                            at[u] += s;
                 }
-                place += lo;
+#pragma unroll
+                for (int u = 0; u < kLists; ++u)
+                    place += l + u == own ? 0 : at[u];
             }
-            if (key > 0 && place < k)
-                put(place, key, mi[i]);
+            if (v > 0 && place < k)
+                put(place, v);
         }
     }
 }
@@ -1809,9 +1818,7 @@ distill_fwd_kernel(const __grid_constant__ DistillArgs a)
         cluster_join();
         if (rank != 0)
             return;
-        t = parts[0];
-        for (int i = 1; i < C; ++i)
-            t = join<false>(t, parts[i], a.c);
+        t = cluster_stats<false>(parts, C, a.c);
     }
     if (tid == 0) {
         const RowLoss o = row_loss<TAIL>(a, slots, t, true);
@@ -1951,9 +1958,7 @@ distill_fused_kernel(const __grid_constant__ DistillArgs a)
             if (tid < C)
                 *peer(&parts[rank], tid) = t;
             cluster_join();
-            t = parts[0];
-            for (int i = 1; i < C; ++i)
-                t = join<false>(t, parts[i], a.c);
+            t = cluster_stats<false>(parts, C, a.c);
         }
         const RowLoss l = row_loss<TAIL>(a, slots, t, rank == 0 && tid == 0);
         zero = l.zero;

@@ -27,37 +27,44 @@ def _dtype(what: str, t: torch.Tensor) -> int:
 
 def _call(name: str, stream, *args) -> None:
     """The C call `name` with tensors as device pointers, on `stream`."""
-    args = [binding._ptr(a) if isinstance(a, torch.Tensor) else a for a in args]
+    ptr = binding._ptr
+    args = [ptr(a) if isinstance(a, torch.Tensor) else a for a in args]
     binding._check(getattr(binding.lib(), name)(*args, binding._stream(stream)), name)
 
 
-def _like(what: str, name: str, t: torch.Tensor | None, dtype, shape) -> None:
-    """TypeError / ValueError unless `t` (when given) has this type and shape:
-    the C calls write or read it as such."""
+def _like(what: str, name: str, t: torch.Tensor | None, dtype, shape: tuple, dev) -> None:
+    """TypeError / ValueError unless `t` (when given) has this type, shape and
+    device: the C calls write or read it as such."""
     if t is None:
         return
     if t.dtype != dtype:
         raise TypeError(f"{what}: {name} must be {str(dtype).replace('torch.', '')}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{what}: {name} must have shape {tuple(shape)}")
+    if t.device != dev:
+        raise ValueError(f"{what}: tensors on different devices")
 
 
-def _same_device(what: str, dev, *ts) -> None:
-    for t in ts:
-        if t is not None and t.device != dev:
-            raise ValueError(f"{what}: tensors on different devices")
+def _same_device(what: str, dev, t: torch.Tensor | None) -> None:
+    if t is not None and t.device != dev:
+        raise ValueError(f"{what}: tensors on different devices")
 
 
-def _amax(what: str, t: torch.Tensor | None) -> None:
-    if t is not None and (t.dtype != torch.float32 or t.numel() != 1):
+def _amax(what: str, t: torch.Tensor | None, dev) -> None:
+    if t is None:
+        return
+    if t.dtype != torch.float32 or t.numel() != 1:
         raise TypeError(f"{what}: amax_out must be one float32 value")
+    if t.device != dev:
+        raise ValueError(f"{what}: tensors on different devices")
 
 
 def _norm_params(what: str, x, w, b):
     if x.dim() != 2:
         raise TypeError(f"{what} takes a 2-D input")
-    _like(what, "w", w, w.dtype, (x.shape[1],))
-    _like(what, "b", b, w.dtype, (x.shape[1],))
+    cols, dev = (x.shape[1],), x.device
+    _like(what, "w", w, w.dtype, cols, dev)
+    _like(what, "b", b, w.dtype, cols, dev)
     return _dtype(what, x), _dtype(what, w)
 
 
@@ -75,11 +82,10 @@ def f8_norm_fwd(x: torch.Tensor, w: torch.Tensor, b: torch.Tensor | None = None,
     if mean is None and kind == F8_LAYER_NORM:
         mean = torch.empty(rows, dtype=torch.float32, device=dev)
     rstd = torch.empty(rows, dtype=torch.float32, device=dev) if rstd is None else rstd
-    _like("f8_norm_fwd", "y", y, x.dtype, x.shape)
-    _like("f8_norm_fwd", "mean", mean, torch.float32, (rows,))
-    _like("f8_norm_fwd", "rstd", rstd, torch.float32, (rows,))
-    _amax("f8_norm_fwd", amax_out)
-    _same_device("f8_norm_fwd", dev, w, b, y, mean, rstd, amax_out)
+    _like("f8_norm_fwd", "y", y, x.dtype, x.shape, dev)
+    _like("f8_norm_fwd", "mean", mean, torch.float32, (rows,), dev)
+    _like("f8_norm_fwd", "rstd", rstd, torch.float32, (rows,), dev)
+    _amax("f8_norm_fwd", amax_out, dev)
     _call("f8_norm_fwd", stream, x, xt, w, b, wt, int(kind), rows, cols, float(eps), y, mean,
           rstd, amax_out)
     return y, (mean if kind == F8_LAYER_NORM else None), rstd
@@ -99,20 +105,20 @@ def f8_norm_bwd(dy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, mean: torch.
     xt, wt = _norm_params("f8_norm_bwd", x, w, None)
     rows, cols = x.shape
     dev = x.device
-    _like("f8_norm_bwd", "dy", dy, x.dtype, x.shape)
-    _like("f8_norm_bwd", "mean", mean, torch.float32, (rows,))
-    _like("f8_norm_bwd", "rstd", rstd, torch.float32, (rows,))
+    _like("f8_norm_bwd", "dy", dy, x.dtype, x.shape, dev)
+    _like("f8_norm_bwd", "mean", mean, torch.float32, (rows,), dev)
+    _like("f8_norm_bwd", "rstd", rstd, torch.float32, (rows,), dev)
     if want_db is None:
         want_db = kind == F8_LAYER_NORM
     dx = torch.empty_like(x) if dx is None and want_dx else dx
     dw = torch.empty_like(w) if dw is None and want_dw else dw
     db = torch.empty_like(w) if db is None and want_db else db
-    _like("f8_norm_bwd", "dx", dx, x.dtype, x.shape)
-    _like("f8_norm_bwd", "dw", dw, w.dtype, (cols,))
-    _like("f8_norm_bwd", "db", db, w.dtype, (cols,))
+    _like("f8_norm_bwd", "dx", dx, x.dtype, x.shape, dev)
+    _like("f8_norm_bwd", "dw", dw, w.dtype, (cols,), dev)
+    _like("f8_norm_bwd", "db", db, w.dtype, (cols,), dev)
     if ws is None and (dw is not None or db is not None):
         ws = torch.empty(max(f8_norm_bwd_workspace_bytes(rows, cols), 1), dtype=torch.uint8, device=dev)
-    _same_device("f8_norm_bwd", dev, dy, w, mean, rstd, dx, dw, db, ws)
+    _same_device("f8_norm_bwd", dev, ws)
     _call("f8_norm_bwd", stream, dy, x, xt, w, wt, mean, rstd, int(kind), rows, cols, dx, dw,
           db, ws, ws.numel() if ws is not None else 0)
     return dx, dw, db
@@ -139,14 +145,14 @@ def f8_quantize_norm(x: torch.Tensor, w: torch.Tensor, b: torch.Tensor | None = 
     q_t = torch.empty((cols, rows), dtype=torch.uint8, device=dev) if q_t is None else q_t
     if ws is None:
         ws = torch.empty(binding.f8_quantize_workspace_bytes(), dtype=torch.uint8, device=dev)
-    _like("f8_quantize_norm", "y", y, x.dtype, x.shape)
-    _like("f8_quantize_norm", "mean", mean, torch.float32, (rows,))
-    _like("f8_quantize_norm", "rstd", rstd, torch.float32, (rows,))
-    _like("f8_quantize_norm", "q", q, torch.uint8, (rows, cols))
-    _like("f8_quantize_norm", "q_t", q_t, torch.uint8, (cols, rows))
-    _amax("f8_quantize_norm", amax_out)
-    _amax("f8_quantize_norm", scale_out)
-    _same_device("f8_quantize_norm", dev, w, b, y, mean, rstd, amax_out, scale_out, q, q_t, ws)
+    _like("f8_quantize_norm", "y", y, x.dtype, x.shape, dev)
+    _like("f8_quantize_norm", "mean", mean, torch.float32, (rows,), dev)
+    _like("f8_quantize_norm", "rstd", rstd, torch.float32, (rows,), dev)
+    _like("f8_quantize_norm", "q", q, torch.uint8, (rows, cols), dev)
+    _like("f8_quantize_norm", "q_t", q_t, torch.uint8, (cols, rows), dev)
+    _amax("f8_quantize_norm", amax_out, dev)
+    _amax("f8_quantize_norm", scale_out, dev)
+    _same_device("f8_quantize_norm", dev, ws)
     _call("f8_quantize_norm", stream, x, w, b, wt, int(kind), rows, cols, float(eps), y, mean,
           rstd, amax_out, scale_out, q, q_t, ws, ws.numel())
     return q, q_t, scale_out, amax_out, y, (mean if kind == F8_LAYER_NORM else None), rstd
@@ -179,6 +185,8 @@ def _dlogits(what: str, logits: torch.Tensor, dlogits: torch.Tensor | None):
     rows, vocab = logits.shape
     if dlogits is None:
         dlogits = torch.empty((rows, vocab), dtype=logits.dtype, device=logits.device)
+    if dlogits.device != logits.device:
+        raise ValueError(f"{what}: tensors on different devices")
     if dlogits.dtype != logits.dtype:
         raise TypeError(f"{what}: dlogits must have the type of logits")
     if dlogits.dim() != 2 or dlogits.shape[0] != rows or dlogits.shape[1] < vocab:
@@ -198,7 +206,8 @@ def f8_token_logprobs(logits: torch.Tensor, tokens: torch.Tensor | None = None, 
     what = "f8_token_logprobs"
     p, ld = _rows(what, "logits", logits)
     rows, vocab = logits.shape
-    f32 = dict(dtype=torch.float32, device=logits.device)
+    dev = logits.device
+    f32 = dict(dtype=torch.float32, device=dev)
     if tokens is not None and logp is None:
         logp = torch.empty(rows, **f32)
     entropy = torch.empty(rows, **f32) if entropy is None else entropy
@@ -207,12 +216,11 @@ def f8_token_logprobs(logits: torch.Tensor, tokens: torch.Tensor | None = None, 
         top_ids = torch.empty((rows, top_k), dtype=torch.int32, device=logits.device)
     if top_k and top_logp is None:
         top_logp = torch.empty((rows, top_k), **f32)
-    _like(what, "tokens", tokens, torch.int64, (rows,))
+    _like(what, "tokens", tokens, torch.int64, (rows,), dev)
     for n, t in (("logp", logp), ("entropy", entropy), ("lse", lse)):
-        _like(what, n, t, torch.float32, (rows,))
-    _like(what, "top_ids", top_ids, torch.int32, (rows, top_k))
-    _like(what, "top_logp", top_logp, torch.float32, (rows, top_k))
-    _same_device(what, logits.device, tokens, logp, entropy, lse, top_ids, top_logp)
+        _like(what, n, t, torch.float32, (rows,), dev)
+    _like(what, "top_ids", top_ids, torch.int32, (rows, top_k), dev)
+    _like(what, "top_logp", top_logp, torch.float32, (rows, top_k), dev)
     _call("f8_token_logprobs", stream, p, _dtype(what, logits), rows, vocab, ld, tokens,
           float(temperature), int(top_k), logp, entropy, lse, top_ids, top_logp)
     return logp, entropy, lse, top_ids, top_logp
@@ -228,12 +236,12 @@ def f8_token_logprobs_bwd(logits: torch.Tensor, tokens: torch.Tensor | None, lse
     what = "f8_token_logprobs_bwd"
     p, ld = _rows(what, "logits", logits)
     rows, vocab = logits.shape
+    dev = logits.device
     dlogits, dp, ldd = _dlogits(what, logits, dlogits)
-    _like(what, "tokens", tokens, torch.int64, (rows,))
+    _like(what, "tokens", tokens, torch.int64, (rows,), dev)
     for n, t in (("lse", lse), ("entropy", entropy), ("dlogp", dlogp), ("dentropy", dentropy)):
-        _like(what, n, t, torch.float32, (rows,))
-    _same_device(what, logits.device, tokens, lse, entropy, dlogp, dentropy, dlogits, amax_out)
-    _amax(what, amax_out)
+        _like(what, n, t, torch.float32, (rows,), dev)
+    _amax(what, amax_out, dev)
     _call("f8_token_logprobs_bwd", stream, p, _dtype(what, logits), rows, vocab, ld, tokens,
           lse, entropy, dlogp, dentropy, float(temperature), dp, ldd, amax_out)
     return dlogits
@@ -242,9 +250,9 @@ def f8_token_logprobs_bwd(logits: torch.Tensor, tokens: torch.Tensor | None, lse
 def _slots(what: str, logits: torch.Tensor, ids: torch.Tensor, values: torch.Tensor) -> int:
     if ids.dim() != 2:
         raise TypeError(f"{what}: ids must be 2-D")
-    k = ids.shape[1]
-    _like(what, "ids", ids, torch.int32, (logits.shape[0], k))
-    _like(what, "values", values, torch.float32, (logits.shape[0], k))
+    k, dev = ids.shape[1], logits.device
+    _like(what, "ids", ids, torch.int32, (logits.shape[0], k), dev)
+    _like(what, "values", values, torch.float32, (logits.shape[0], k), dev)
     return k
 
 
@@ -257,6 +265,7 @@ def f8_distill_fwd(logits: torch.Tensor, ids: torch.Tensor, values: torch.Tensor
     what = "f8_distill_fwd"
     p, ld = _rows(what, "logits", logits)
     rows, vocab = logits.shape
+    dev = logits.device
     k = _slots(what, logits, ids, values)
     f32 = dict(dtype=torch.float32, device=logits.device)
     loss = torch.empty(rows, **f32) if loss is None else loss
@@ -264,8 +273,7 @@ def f8_distill_fwd(logits: torch.Tensor, ids: torch.Tensor, values: torch.Tensor
     if tail and rest is None:
         rest = torch.empty(rows, **f32)
     for n, t in (("loss", loss), ("lse", lse), ("rest", rest)):
-        _like(what, n, t, torch.float32, (rows,))
-    _same_device(what, logits.device, ids, values, loss, lse, rest)
+        _like(what, n, t, torch.float32, (rows,), dev)
     _call("f8_distill_fwd", stream, p, _dtype(what, logits), rows, vocab, ld, ids, values, k,
           float(temperature), int(bool(tail)), loss, lse, rest)
     return loss, lse, (rest if tail else None)
@@ -279,12 +287,12 @@ def f8_distill_bwd(logits: torch.Tensor, ids: torch.Tensor, values: torch.Tensor
     what = "f8_distill_bwd"
     p, ld = _rows(what, "logits", logits)
     rows, vocab = logits.shape
+    dev = logits.device
     k = _slots(what, logits, ids, values)
     dlogits, dp, ldd = _dlogits(what, logits, dlogits)
     for n, t in (("lse", lse), ("rest", rest), ("dloss", dloss)):
-        _like(what, n, t, torch.float32, (rows,))
-    _same_device(what, logits.device, ids, values, lse, rest, dloss, dlogits, amax_out)
-    _amax(what, amax_out)
+        _like(what, n, t, torch.float32, (rows,), dev)
+    _amax(what, amax_out, dev)
     _call("f8_distill_bwd", stream, p, _dtype(what, logits), rows, vocab, ld, ids, values, k,
           float(temperature), int(bool(tail)), lse, rest, dloss, dp, ldd, amax_out)
     return dlogits
@@ -299,13 +307,13 @@ def f8_distill_fwd_bwd(logits: torch.Tensor, ids: torch.Tensor, values: torch.Te
     what = "f8_distill_fwd_bwd"
     p, ld = _rows(what, "logits", logits)
     rows, vocab = logits.shape
+    dev = logits.device
     k = _slots(what, logits, ids, values)
     dlogits, dp, ldd = _dlogits(what, logits, dlogits)
     loss = torch.empty(rows, dtype=torch.float32, device=logits.device) if loss is None else loss
     for n, t in (("loss", loss), ("dloss", dloss)):
-        _like(what, n, t, torch.float32, (rows,))
-    _same_device(what, logits.device, ids, values, dloss, loss, dlogits, amax_out)
-    _amax(what, amax_out)
+        _like(what, n, t, torch.float32, (rows,), dev)
+    _amax(what, amax_out, dev)
     _call("f8_distill_fwd_bwd", stream, p, _dtype(what, logits), rows, vocab, ld, ids, values,
           k, float(temperature), int(bool(tail)), dloss, loss, dp, ldd, amax_out)
     return loss, dlogits
