@@ -1045,14 +1045,17 @@ logprobs_kernel(const __grid_constant__ LogprobArgs a)
             for (int l = 0; l < C && place < k; l += kLists) {
                 int at[kLists] = {};
                 for (int s = half; s > 0; s >>= 1) {
+                    uint64_t o[kLists];  // loads without branches between them
 #pragma unroll
                     for (int u = 0; u < kLists; ++u)
-                        if (l + u < C && at[u] + s <= k && m[(l + u) * k + at[u] + s - 1] > v)
-                            at[u] += s;
+                        o[u] = m[min(l + u, C - 1) * k + min(at[u] + s, k) - 1];
+#pragma unroll
+                    for (int u = 0; u < kLists; ++u)
+                        at[u] += at[u] + s <= k && o[u] > v ? s : 0;
                 }
 #pragma unroll
                 for (int u = 0; u < kLists; ++u)
-                    place += l + u == own ? 0 : at[u];
+                    place += l + u == own || l + u >= C ? 0 : at[u];
             }
             if (v > 0 && place < k)
                 put(place, v);
