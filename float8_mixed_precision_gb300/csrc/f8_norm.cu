@@ -397,28 +397,46 @@ __device__ __forceinline__ void to_pairs(const typename Raw<T, VEC>::type (&v)[N
     }
 }
 
+// The thread's parameters into L2 ahead of the rows' copies, behind which their
+// loads would otherwise wait for as long as the slots take to fill.
+template <int VEC, int NV, int TPR>
+__device__ __forceinline__ void prefetch_params(const void *p, int type, int cols, int t)
+{
+    if (p == nullptr)
+        return;
+    const int bytes = type == kBf16 ? 2 : 4;
+#pragma unroll
+    for (int u = 0; u < NV; ++u) {
+        const int i = u * TPR + t;
+        if (i < cols / VEC)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const char *>(p) + i * VEC * bytes));
+    }
+}
+
+template <int VEC, int NV, int TPR, int TYPE>
+__device__ __forceinline__ void param_values(const void *p, int cols, int t, float (&x)[NV * VEC],
+                                             unsigned *status)
+{
+#pragma unroll
+    for (int u = 0; u < NV; ++u)
+        if (u * TPR + t < cols / VEC)
+            load_param<VEC>(p, TYPE, (u * TPR + t) * VEC, cols, &x[u * VEC], status);
+}
+
 template <int VEC, int NV, int TPR>
 __device__ __forceinline__ void param_pairs(const void *p, int type, int cols, int t,
                                             float2 (&f)[NV * VEC / 2], unsigned *status)
 {
-#pragma unroll
-    for (int u = 0; u < NV; ++u) {
-        float x[VEC];
-        const int i = u * TPR + t;
-#pragma unroll
-        for (int e = 0; e < VEC; ++e)
-            x[e] = 0.0f;
-        if (p != nullptr && i < cols / VEC)
-            load_param<VEC>(p, type, i * VEC, cols, x, status);
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            const int k = u * VEC + e;
-            if (k & 1)
-                f[k / 2].y = x[e];
-            else
-                f[k / 2].x = x[e];
-        }
+    float x[NV * VEC] = {};
+    if (p != nullptr) {
+        if (type == kBf16)
+            param_values<VEC, NV, TPR, kBf16>(p, cols, t, x, status);
+        else
+            param_values<VEC, NV, TPR, kBf16 + 1>(p, cols, t, x, status);
     }
+#pragma unroll
+    for (int i = 0; i < NV * VEC / 2; ++i)
+        f[i] = make_float2(x[2 * i], x[2 * i + 1]);
 }
 
 // The pairs of vector u as an array of VEC floats.
@@ -458,6 +476,8 @@ norm_fwd_ring_kernel(const T *x, const void *__restrict__ w, const void *__restr
     }
     griddep_wait();
     griddep_launch_dependents();
+    prefetch_params<VEC, NV, TPR>(w, w_type, cols, t);
+    prefetch_params<VEC, NV, TPR>(b, w_type, cols, t);
     const int64_t step = static_cast<int64_t>(gridDim.x) * kGroups;
     const int64_t row0 = static_cast<int64_t>(blockIdx.x) * kGroups + group;
     __syncthreads();
@@ -753,6 +773,7 @@ norm_bwd_ring_kernel(const T *dy, const T *x, const void *__restrict__ w, int w_
     }
     griddep_wait();
     griddep_launch_dependents();
+    prefetch_params<VEC, NV, TPR>(w, w_type, cols, t);
     const int64_t step = static_cast<int64_t>(gridDim.x) * kGroups;
     const int64_t row0 = static_cast<int64_t>(blockIdx.x) * kGroups + group;
     __syncthreads();
@@ -840,50 +861,55 @@ norm_bwd_ring_kernel(const T *dy, const T *x, const void *__restrict__ w, int w_
             mbar_wait(&ring.full[i], parity ^ (i < slot ? 1u : 0u), nullptr, limit_ns);
     if (parts == nullptr)
         return;
-    // the groups' sums joined in group order, two floats per thread at a time
+    // the groups' sums joined in group order, through the slots' memory
     if (kGroups > 1) {
-        float2 *ex = reinterpret_cast<float2 *>(dyn);
-#pragma unroll 1
-        for (int i = 0; i < 2 * P; ++i) {
-            float2 v = make_float2(0.0f, 0.0f);
+        float4 *ex = reinterpret_cast<float4 *>(dyn);
+        __syncthreads();
+        if (group > 0) {
+            float4 *mine = ex + (group - 1) * P * TPR + t;
 #pragma unroll
-            for (int k = 0; k < P; ++k) {
-                v = i == k ? aw[k] : v;
-                v = i == P + k ? ab[k] : v;
+            for (int i = 0; i < P; i += 2) {
+                mine[i * TPR] = make_float4(aw[i].x, aw[i].y, aw[i + 1].x, aw[i + 1].y);
+                mine[(i + 1) * TPR] = make_float4(ab[i].x, ab[i].y, ab[i + 1].x, ab[i + 1].y);
             }
-            __syncthreads();
-            ex[threadIdx.x] = v;
-            __syncthreads();
-            if (group == 0) {
+        }
+        __syncthreads();
+        if (group > 0)
+            return;
 #pragma unroll
-                for (int j = 1; j < kGroups; ++j)
-                    v = __fadd2_rn(v, ex[j * TPR + t]);
+        for (int j = 0; j < kGroups - 1; ++j) {
+            const float4 *o = ex + j * P * TPR + t;
 #pragma unroll
-                for (int k = 0; k < P; ++k) {
-                    aw[k] = i == k ? v : aw[k];
-                    ab[k] = i == P + k ? v : ab[k];
-                }
+            for (int i = 0; i < P; i += 2) {
+                const float4 u = o[i * TPR], v = o[(i + 1) * TPR];
+                aw[i] = __fadd2_rn(aw[i], make_float2(u.x, u.y));
+                aw[i + 1] = __fadd2_rn(aw[i + 1], make_float2(u.z, u.w));
+                ab[i] = __fadd2_rn(ab[i], make_float2(v.x, v.y));
+                ab[i + 1] = __fadd2_rn(ab[i + 1], make_float2(v.z, v.w));
             }
         }
     }
-    if (group == 0) {
-        float *p = parts + static_cast<int64_t>(blockIdx.x) * 2 * cols;
+    float *p = parts + static_cast<int64_t>(blockIdx.x) * 2 * cols;
+    auto put = [&](float *to, const float2(&f)[P]) {
 #pragma unroll
         for (int u = 0; u < NV; ++u) {
             const int i = u * TPR + t;
             if (i < nvec) {
                 float o[VEC];
-                pair_vector<VEC, NV>(aw, u, o);
+                pair_vector<VEC, NV>(f, u, o);
+                if constexpr (VEC == 1) {
+                    to[i] = o[0];
+                } else {
 #pragma unroll
-                for (int e = 0; e < VEC; ++e)
-                    p[i * VEC + e] = o[e];
-                pair_vector<VEC, NV>(ab, u, o);
-#pragma unroll
-                for (int e = 0; e < VEC; ++e)
-                    p[cols + i * VEC + e] = o[e];
+                    for (int e = 0; e < VEC; e += 4)
+                        *reinterpret_cast<float4 *>(to + i * VEC + e) =
+                            make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                }
             }
         }
-    }
+    };
+    put(p, aw);
+    put(p + cols, ab);
 }
 
 // ------------------------------------------------------------ backward
@@ -1207,8 +1233,8 @@ cudaError_t bwd_ring(const BwdArgs &a, const DeviceInfo &dev, cudaStream_t st, i
     if (e != cudaSuccess)
         return e;
     *nparts = p.grid;
-    // the join at the end needs a float2 per thread
-    const size_t smem = std::max<size_t>(p.smem, sizeof(float2) * kBwdThreads);
+    // the join at the end needs what the other groups' threads have added up
+    const size_t smem = std::max<size_t>(p.smem, sizeof(float) * 2 * NV * VEC * (kBwdThreads - TPR));
     return launch_pdl(norm_bwd_ring_kernel<T, VEC, NV, TPR, FULL>, dim3(p.grid), dim3(kBwdThreads), smem,
                       st, static_cast<const T *>(a.dy), static_cast<const T *>(a.x), a.w, a.w_type,
                       a.mean, a.rstd, a.rms, a.rows, static_cast<int>(a.cols),
