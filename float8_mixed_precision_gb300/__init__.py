@@ -1,8 +1,9 @@
 """GB300-native Float8 training linear with dynamic tensorwise scaling.
 
 The compute path is libf8 (hand-written sm_103a CUDA behind the C ABI of
-include/f8.h); ``binding`` marshals torch tensors into it.  ``workloads``
-draws the seeded synthetic inputs.
+include/f8.h); ``binding`` marshals torch tensors into it, ``ops`` the norm and
+the calls on a head linear's logits.  ``workloads`` draws the seeded synthetic
+inputs.
 """
 from .binding import (EXPORTS, F8_E4M3, F8_E5M2, F8Error, LinearSaved, f8_amax, f8_cast_transpose, f8_gemm,  # noqa: F401
                       f8_gemm_grouped, f8_last_device_status, f8_linear_bwd, f8_linear_fwd,

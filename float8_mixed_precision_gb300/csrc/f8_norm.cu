@@ -14,13 +14,23 @@
 // the differences to the mean (two reductions over registers), not from the
 // sum of squares.
 //
+// Rows of more than 512 columns come through a ring of shared-memory slots that
+// bulk copies fill some rows ahead: the registers that hold a row, its
+// parameters and its column sums leave too few threads to have enough loads in
+// flight of their own.  With plain loads 8192 x 4096 took 34 us forward and
+// 85 us backward, through the ring at once 27 and 51 us.
+//
 // The backward's sums over rows stay in registers too: a group walks its rows
 // with a stride of the grid, each thread adding dy xh and dy of the columns it
-// owns, and writes one row of partial sums at the end; a second kernel adds
-// the partial rows in order.  No atomics, so equal inputs give equal bits.
+// owns; a block's groups are joined at the end and leave one row of partial
+// sums; a second kernel adds the partial rows in order.  No atomics, so equal
+// inputs give equal bits.
 //
-// Rows wider than the register path's 16384 columns take kernels that walk the
-// row once per reduction, with the column sums in a kernel of their own.
+// Rows wider than the 16384 columns that registers hold take kernels that walk
+// the row once per reduction, with the column sums in a kernel of their own.
+//
+// Measured, bf16, layer norm: forward 8192 x 4096 25.0 us, 5.4 TB/s; backward
+// with both parameters' gradients 39.8 us, 5.1 TB/s; a plain copy runs at 6.8.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -234,6 +244,10 @@ __host__ __device__ constexpr int block_threads(int tpr) { return tpr < 256 ? 25
 // once the group has taken the row into registers.  A copy covers the row's
 // 16-byte pieces, so a row may start inside one (widths that are no multiple
 // of 8); the piece that would reach past the last row's end is read directly.
+// Such rows are taken from their slot and stored element by element, since an
+// element's place in its 16 bytes differs from row to row while a thread's
+// columns, parameters and sums do not: 1999 x 5003 bf16 backward 32 us, where
+// 2000 x 5000 takes 25.
 constexpr int kMaxStages = 8;
 
 struct RowCopy {
@@ -748,6 +762,10 @@ norm_fwd_wide_kernel(const T *x, const void *__restrict__ w, const void *__restr
 // 512 threads in as many groups as its rows' width leaves; their column sums
 // are joined in shared memory at the end, so there is one partial row per
 // block.  Elements past the row are 0 and add nothing anywhere.
+// 512 threads of 128 registers (the row, dy and the two sums of 16 columns, and
+// w) fill an SM; what bounds it is a row's chain of shared-memory reads,
+// reduction and stores with two rows in work: about 2000 cycles a row of 4096,
+// of which the wait for its copy is 150.
 constexpr int kBwdThreads = 512;
 
 template <typename T, int VEC, int NV, int TPR, bool FULL>

@@ -26,46 +26,54 @@ def _dtype(what: str, t: torch.Tensor) -> int:
 
 
 def _call(name: str, stream, *args) -> None:
-    """The C call `name` with tensors as device pointers, on `stream`."""
-    ptr = binding._ptr
-    args = [ptr(a) if isinstance(a, torch.Tensor) else a for a in args]
+    """The C call `name` on `stream`."""
     binding._check(getattr(binding.lib(), name)(*args, binding._stream(stream)), name)
 
 
-def _like(what: str, name: str, t: torch.Tensor | None, dtype, shape: tuple, dev) -> None:
-    """TypeError / ValueError unless `t` (when given) has this type, shape and
-    device: the C calls write or read it as such."""
+def _ptr(what: str, name: str, t: torch.Tensor | None, dtype, shape: tuple, dev):
+    """The pointer of `t` (None if not given): TypeError / ValueError unless it
+    has this type, shape and device and is contiguous, as the C calls read or
+    write it.  `dev` is the device of a tensor that binding._ptr or _rows
+    takes, so it is the GPU's."""
     if t is None:
-        return
+        return None
     if t.dtype != dtype:
         raise TypeError(f"{what}: {name} must be {str(dtype).replace('torch.', '')}")
     if t.shape != shape:
         raise ValueError(f"{what}: {name} must have shape {tuple(shape)}")
     if t.device != dev:
         raise ValueError(f"{what}: tensors on different devices")
+    if not t.is_contiguous():
+        raise ValueError("libf8 takes contiguous (row-major) tensors only")
+    return t.data_ptr()
 
 
-def _same_device(what: str, dev, t: torch.Tensor | None) -> None:
-    if t is not None and t.device != dev:
-        raise ValueError(f"{what}: tensors on different devices")
+def _bytes(what: str, ws: torch.Tensor | None, dev):
+    """The pointer and the size of a workspace, a tensor of bytes."""
+    if ws is None:
+        return None, 0
+    return _ptr(what, "ws", ws, torch.uint8, (ws.numel(),), dev), ws.numel()
 
 
-def _amax(what: str, t: torch.Tensor | None, dev) -> None:
+def _scalar(what: str, t: torch.Tensor | None, dev):
+    """The pointer of one fp32 value (None if not given)."""
     if t is None:
-        return
+        return None
     if t.dtype != torch.float32 or t.numel() != 1:
         raise TypeError(f"{what}: amax_out must be one float32 value")
     if t.device != dev:
         raise ValueError(f"{what}: tensors on different devices")
+    return t.data_ptr()
 
 
 def _norm_params(what: str, x, w, b):
+    """Types and pointers of x, w and b."""
     if x.dim() != 2:
         raise TypeError(f"{what} takes a 2-D input")
     cols, dev = (x.shape[1],), x.device
-    _like(what, "w", w, w.dtype, cols, dev)
-    _like(what, "b", b, w.dtype, cols, dev)
-    return _dtype(what, x), _dtype(what, w)
+    wt = _dtype(what, w)
+    wp, bp = _ptr(what, "w", w, w.dtype, cols, dev), _ptr(what, "b", b, w.dtype, cols, dev)
+    return _dtype(what, x), wt, binding._ptr(x), wp, bp
 
 
 def f8_norm_fwd(x: torch.Tensor, w: torch.Tensor, b: torch.Tensor | None = None,
@@ -75,19 +83,18 @@ def f8_norm_fwd(x: torch.Tensor, w: torch.Tensor, b: torch.Tensor | None = None,
     """Layer norm or RMS norm of the rows of a 2-D bf16 or fp32 tensor;
     returns (y, mean, rstd), mean None for F8_RMS_NORM.  `amax_out` (fp32
     scalar, bf16 inputs) receives max |y|, ready for f8_cast_transpose."""
-    xt, wt = _norm_params("f8_norm_fwd", x, w, b)
-    rows, cols = x.shape
+    what = "f8_norm_fwd"
+    xt, wt, xp, wp, bp = _norm_params(what, x, w, b)
+    rows, cols = shape = x.shape
     dev = x.device
     y = torch.empty_like(x) if y is None else y
     if mean is None and kind == F8_LAYER_NORM:
         mean = torch.empty(rows, dtype=torch.float32, device=dev)
     rstd = torch.empty(rows, dtype=torch.float32, device=dev) if rstd is None else rstd
-    _like("f8_norm_fwd", "y", y, x.dtype, x.shape, dev)
-    _like("f8_norm_fwd", "mean", mean, torch.float32, (rows,), dev)
-    _like("f8_norm_fwd", "rstd", rstd, torch.float32, (rows,), dev)
-    _amax("f8_norm_fwd", amax_out, dev)
-    _call("f8_norm_fwd", stream, x, xt, w, b, wt, int(kind), rows, cols, float(eps), y, mean,
-          rstd, amax_out)
+    _call(what, stream, xp, xt, wp, bp, wt, int(kind), rows, cols, float(eps),
+          _ptr(what, "y", y, x.dtype, shape, dev),
+          _ptr(what, "mean", mean, torch.float32, (rows,), dev),
+          _ptr(what, "rstd", rstd, torch.float32, (rows,), dev), _scalar(what, amax_out, dev))
     return y, (mean if kind == F8_LAYER_NORM else None), rstd
 
 
@@ -102,25 +109,23 @@ def f8_norm_bwd(dy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, mean: torch.
                 want_db: bool | None = None, stream=None):
     """(dx, dw, db) of f8_norm_fwd for the gradient dy of y; db is formed by
     default for F8_LAYER_NORM (`want_db`)."""
-    xt, wt = _norm_params("f8_norm_bwd", x, w, None)
-    rows, cols = x.shape
+    what = "f8_norm_bwd"
+    xt, wt, xp, wp, _ = _norm_params(what, x, w, None)
+    rows, cols = shape = x.shape
     dev = x.device
-    _like("f8_norm_bwd", "dy", dy, x.dtype, x.shape, dev)
-    _like("f8_norm_bwd", "mean", mean, torch.float32, (rows,), dev)
-    _like("f8_norm_bwd", "rstd", rstd, torch.float32, (rows,), dev)
     if want_db is None:
         want_db = kind == F8_LAYER_NORM
     dx = torch.empty_like(x) if dx is None and want_dx else dx
     dw = torch.empty_like(w) if dw is None and want_dw else dw
     db = torch.empty_like(w) if db is None and want_db else db
-    _like("f8_norm_bwd", "dx", dx, x.dtype, x.shape, dev)
-    _like("f8_norm_bwd", "dw", dw, w.dtype, (cols,), dev)
-    _like("f8_norm_bwd", "db", db, w.dtype, (cols,), dev)
+    args = (_ptr(what, "dy", dy, x.dtype, shape, dev), xp, xt, wp, wt,
+            _ptr(what, "mean", mean, torch.float32, (rows,), dev),
+            _ptr(what, "rstd", rstd, torch.float32, (rows,), dev), int(kind), rows, cols,
+            _ptr(what, "dx", dx, x.dtype, shape, dev), _ptr(what, "dw", dw, w.dtype, (cols,), dev),
+            _ptr(what, "db", db, w.dtype, (cols,), dev))
     if ws is None and (dw is not None or db is not None):
         ws = torch.empty(max(f8_norm_bwd_workspace_bytes(rows, cols), 1), dtype=torch.uint8, device=dev)
-    _same_device("f8_norm_bwd", dev, ws)
-    _call("f8_norm_bwd", stream, dy, x, xt, w, wt, mean, rstd, int(kind), rows, cols, dx, dw,
-          db, ws, ws.numel() if ws is not None else 0)
+    _call(what, stream, *args, *_bytes(what, ws, dev))
     return dx, dw, db
 
 
@@ -130,10 +135,11 @@ def f8_quantize_norm(x: torch.Tensor, w: torch.Tensor, b: torch.Tensor | None = 
                      amax_out=None, scale_out=None, q=None, q_t=None, ws=None, stream=None):
     """The norm of a 2-D bf16 tensor with its amax from the producing pass,
     then its E4M3 cast: returns (q, q_t, scale, amax, y, mean, rstd)."""
+    what = "f8_quantize_norm"
     if x.dtype != torch.bfloat16:
-        raise TypeError("f8_quantize_norm takes a bf16 input")
-    _, wt = _norm_params("f8_quantize_norm", x, w, b)
-    rows, cols = x.shape
+        raise TypeError(f"{what} takes a bf16 input")
+    _, wt, xp, wp, bp = _norm_params(what, x, w, b)
+    rows, cols = shape = x.shape
     dev = x.device
     y = torch.empty_like(x) if y is None else y
     if mean is None and kind == F8_LAYER_NORM:
@@ -145,16 +151,12 @@ def f8_quantize_norm(x: torch.Tensor, w: torch.Tensor, b: torch.Tensor | None = 
     q_t = torch.empty((cols, rows), dtype=torch.uint8, device=dev) if q_t is None else q_t
     if ws is None:
         ws = torch.empty(binding.f8_quantize_workspace_bytes(), dtype=torch.uint8, device=dev)
-    _like("f8_quantize_norm", "y", y, x.dtype, x.shape, dev)
-    _like("f8_quantize_norm", "mean", mean, torch.float32, (rows,), dev)
-    _like("f8_quantize_norm", "rstd", rstd, torch.float32, (rows,), dev)
-    _like("f8_quantize_norm", "q", q, torch.uint8, (rows, cols), dev)
-    _like("f8_quantize_norm", "q_t", q_t, torch.uint8, (cols, rows), dev)
-    _amax("f8_quantize_norm", amax_out, dev)
-    _amax("f8_quantize_norm", scale_out, dev)
-    _same_device("f8_quantize_norm", dev, ws)
-    _call("f8_quantize_norm", stream, x, w, b, wt, int(kind), rows, cols, float(eps), y, mean,
-          rstd, amax_out, scale_out, q, q_t, ws, ws.numel())
+    _call(what, stream, xp, wp, bp, wt, int(kind), rows, cols, float(eps),
+          _ptr(what, "y", y, x.dtype, shape, dev),
+          _ptr(what, "mean", mean, torch.float32, (rows,), dev),
+          _ptr(what, "rstd", rstd, torch.float32, (rows,), dev), _scalar(what, amax_out, dev),
+          _scalar(what, scale_out, dev), _ptr(what, "q", q, torch.uint8, (rows, cols), dev),
+          _ptr(what, "q_t", q_t, torch.uint8, (cols, rows), dev), *_bytes(what, ws, dev))
     return q, q_t, scale_out, amax_out, y, (mean if kind == F8_LAYER_NORM else None), rstd
 
 
@@ -216,13 +218,13 @@ def f8_token_logprobs(logits: torch.Tensor, tokens: torch.Tensor | None = None, 
         top_ids = torch.empty((rows, top_k), dtype=torch.int32, device=logits.device)
     if top_k and top_logp is None:
         top_logp = torch.empty((rows, top_k), **f32)
-    _like(what, "tokens", tokens, torch.int64, (rows,), dev)
-    for n, t in (("logp", logp), ("entropy", entropy), ("lse", lse)):
-        _like(what, n, t, torch.float32, (rows,), dev)
-    _like(what, "top_ids", top_ids, torch.int32, (rows, top_k), dev)
-    _like(what, "top_logp", top_logp, torch.float32, (rows, top_k), dev)
-    _call("f8_token_logprobs", stream, p, _dtype(what, logits), rows, vocab, ld, tokens,
-          float(temperature), int(top_k), logp, entropy, lse, top_ids, top_logp)
+    _call(what, stream, p, _dtype(what, logits), rows, vocab, ld,
+          _ptr(what, "tokens", tokens, torch.int64, (rows,), dev), float(temperature), int(top_k),
+          _ptr(what, "logp", logp, torch.float32, (rows,), dev),
+          _ptr(what, "entropy", entropy, torch.float32, (rows,), dev),
+          _ptr(what, "lse", lse, torch.float32, (rows,), dev),
+          _ptr(what, "top_ids", top_ids, torch.int32, (rows, top_k), dev),
+          _ptr(what, "top_logp", top_logp, torch.float32, (rows, top_k), dev))
     return logp, entropy, lse, top_ids, top_logp
 
 
@@ -238,22 +240,23 @@ def f8_token_logprobs_bwd(logits: torch.Tensor, tokens: torch.Tensor | None, lse
     rows, vocab = logits.shape
     dev = logits.device
     dlogits, dp, ldd = _dlogits(what, logits, dlogits)
-    _like(what, "tokens", tokens, torch.int64, (rows,), dev)
-    for n, t in (("lse", lse), ("entropy", entropy), ("dlogp", dlogp), ("dentropy", dentropy)):
-        _like(what, n, t, torch.float32, (rows,), dev)
-    _amax(what, amax_out, dev)
-    _call("f8_token_logprobs_bwd", stream, p, _dtype(what, logits), rows, vocab, ld, tokens,
-          lse, entropy, dlogp, dentropy, float(temperature), dp, ldd, amax_out)
+    _call(what, stream, p, _dtype(what, logits), rows, vocab, ld,
+          _ptr(what, "tokens", tokens, torch.int64, (rows,), dev),
+          _ptr(what, "lse", lse, torch.float32, (rows,), dev),
+          _ptr(what, "entropy", entropy, torch.float32, (rows,), dev),
+          _ptr(what, "dlogp", dlogp, torch.float32, (rows,), dev),
+          _ptr(what, "dentropy", dentropy, torch.float32, (rows,), dev), float(temperature), dp,
+          ldd, _scalar(what, amax_out, dev))
     return dlogits
 
 
-def _slots(what: str, logits: torch.Tensor, ids: torch.Tensor, values: torch.Tensor) -> int:
+def _slots(what: str, logits: torch.Tensor, ids: torch.Tensor, values: torch.Tensor):
+    """The pointers of the slots' ids and values, and their number."""
     if ids.dim() != 2:
         raise TypeError(f"{what}: ids must be 2-D")
-    k, dev = ids.shape[1], logits.device
-    _like(what, "ids", ids, torch.int32, (logits.shape[0], k), dev)
-    _like(what, "values", values, torch.float32, (logits.shape[0], k), dev)
-    return k
+    shape, dev = (logits.shape[0], ids.shape[1]), logits.device
+    return (_ptr(what, "ids", ids, torch.int32, shape, dev),
+            _ptr(what, "values", values, torch.float32, shape, dev), shape[1])
 
 
 def f8_distill_fwd(logits: torch.Tensor, ids: torch.Tensor, values: torch.Tensor,
@@ -266,16 +269,16 @@ def f8_distill_fwd(logits: torch.Tensor, ids: torch.Tensor, values: torch.Tensor
     p, ld = _rows(what, "logits", logits)
     rows, vocab = logits.shape
     dev = logits.device
-    k = _slots(what, logits, ids, values)
+    slots = _slots(what, logits, ids, values)
     f32 = dict(dtype=torch.float32, device=logits.device)
     loss = torch.empty(rows, **f32) if loss is None else loss
     lse = torch.empty(rows, **f32) if lse is None else lse
     if tail and rest is None:
         rest = torch.empty(rows, **f32)
-    for n, t in (("loss", loss), ("lse", lse), ("rest", rest)):
-        _like(what, n, t, torch.float32, (rows,), dev)
-    _call("f8_distill_fwd", stream, p, _dtype(what, logits), rows, vocab, ld, ids, values, k,
-          float(temperature), int(bool(tail)), loss, lse, rest)
+    _call(what, stream, p, _dtype(what, logits), rows, vocab, ld, *slots, float(temperature),
+          int(bool(tail)), _ptr(what, "loss", loss, torch.float32, (rows,), dev),
+          _ptr(what, "lse", lse, torch.float32, (rows,), dev),
+          _ptr(what, "rest", rest, torch.float32, (rows,), dev))
     return loss, lse, (rest if tail else None)
 
 
@@ -288,13 +291,13 @@ def f8_distill_bwd(logits: torch.Tensor, ids: torch.Tensor, values: torch.Tensor
     p, ld = _rows(what, "logits", logits)
     rows, vocab = logits.shape
     dev = logits.device
-    k = _slots(what, logits, ids, values)
+    slots = _slots(what, logits, ids, values)
     dlogits, dp, ldd = _dlogits(what, logits, dlogits)
-    for n, t in (("lse", lse), ("rest", rest), ("dloss", dloss)):
-        _like(what, n, t, torch.float32, (rows,), dev)
-    _amax(what, amax_out, dev)
-    _call("f8_distill_bwd", stream, p, _dtype(what, logits), rows, vocab, ld, ids, values, k,
-          float(temperature), int(bool(tail)), lse, rest, dloss, dp, ldd, amax_out)
+    _call(what, stream, p, _dtype(what, logits), rows, vocab, ld, *slots, float(temperature),
+          int(bool(tail)), _ptr(what, "lse", lse, torch.float32, (rows,), dev),
+          _ptr(what, "rest", rest, torch.float32, (rows,), dev),
+          _ptr(what, "dloss", dloss, torch.float32, (rows,), dev), dp, ldd,
+          _scalar(what, amax_out, dev))
     return dlogits
 
 
@@ -308,12 +311,11 @@ def f8_distill_fwd_bwd(logits: torch.Tensor, ids: torch.Tensor, values: torch.Te
     p, ld = _rows(what, "logits", logits)
     rows, vocab = logits.shape
     dev = logits.device
-    k = _slots(what, logits, ids, values)
+    slots = _slots(what, logits, ids, values)
     dlogits, dp, ldd = _dlogits(what, logits, dlogits)
     loss = torch.empty(rows, dtype=torch.float32, device=logits.device) if loss is None else loss
-    for n, t in (("loss", loss), ("dloss", dloss)):
-        _like(what, n, t, torch.float32, (rows,), dev)
-    _amax(what, amax_out, dev)
-    _call("f8_distill_fwd_bwd", stream, p, _dtype(what, logits), rows, vocab, ld, ids, values,
-          k, float(temperature), int(bool(tail)), dloss, loss, dp, ldd, amax_out)
+    _call(what, stream, p, _dtype(what, logits), rows, vocab, ld, *slots, float(temperature),
+          int(bool(tail)), _ptr(what, "dloss", dloss, torch.float32, (rows,), dev),
+          _ptr(what, "loss", loss, torch.float32, (rows,), dev), dp, ldd,
+          _scalar(what, amax_out, dev))
     return loss, dlogits
