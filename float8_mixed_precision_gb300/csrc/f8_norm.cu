@@ -247,7 +247,7 @@ __host__ __device__ constexpr int block_threads(int tpr) { return tpr < 256 ? 25
 // Such rows are taken from their slot and stored element by element, since an
 // element's place in its 16 bytes differs from row to row while a thread's
 // columns, parameters and sums do not: 1999 x 5003 bf16 backward 32 us, where
-// 2000 x 5000 takes 25.
+// 2000 x 5000 takes 23.
 constexpr int kMaxStages = 8;
 
 struct RowCopy {
@@ -931,7 +931,8 @@ norm_bwd_ring_kernel(const T *dy, const T *x, const void *__restrict__ w, int w_
 }
 
 // ------------------------------------------------------------ backward
-// parts: [gridDim.x * groups][2][cols] fp32 partial sums of dw and db.
+// Rows of up to 512 columns by a warp each, and those of more than 8192 by 1024
+// threads.  parts: [gridDim.x][2][cols] fp32 partial sums of dw and db.
 template <typename T, int VEC, int NV, int TPR>
 __global__ void __launch_bounds__(block_threads(TPR))
 norm_bwd_kernel(const T *dy, const T *x, const void *__restrict__ w, int w_type,
@@ -1011,16 +1012,46 @@ norm_bwd_kernel(const T *dy, const T *x, const void *__restrict__ w, int w_type,
             }
         }
     }
-    if (parts != nullptr) {
-        float *p = parts + unit * 2 * cols;
+    if (parts == nullptr)
+        return;
+    if constexpr (kGroups > 1) {  // joined in group order, as on the ring
+        constexpr int Q = NV * VEC / 4;
+        __shared__ float4 ex[(kGroups - 1) * 2 * Q * TPR];
+        auto at = [&](int g, int i) -> float4 & { return ex[((g - 1) * 2 * Q + i) * TPR + t]; };
+        if (group > 0) {
 #pragma unroll
-        for (int u = 0; u < NV; ++u) {
-            const int i = u * TPR + t;
-            if (i < nvec) {
+            for (int i = 0; i < Q; ++i) {
+                at(group, i) = make_float4(aw[4 * i], aw[4 * i + 1], aw[4 * i + 2], aw[4 * i + 3]);
+                at(group, Q + i) = make_float4(ab[4 * i], ab[4 * i + 1], ab[4 * i + 2], ab[4 * i + 3]);
+            }
+        }
+        __syncthreads();
+        if (group > 0)
+            return;
+        for (int g = 1; g < kGroups; ++g) {
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    p[i * VEC + e] = aw[u * VEC + e];
-                    p[cols + i * VEC + e] = ab[u * VEC + e];
+            for (int i = 0; i < Q; ++i) {
+                const float4 a = at(g, i), b = at(g, Q + i);
+                aw[4 * i] += a.x, aw[4 * i + 1] += a.y, aw[4 * i + 2] += a.z, aw[4 * i + 3] += a.w;
+                ab[4 * i] += b.x, ab[4 * i + 1] += b.y, ab[4 * i + 2] += b.z, ab[4 * i + 3] += b.w;
+            }
+        }
+    }
+    float *p = parts + static_cast<int64_t>(blockIdx.x) * 2 * cols;
+#pragma unroll
+    for (int u = 0; u < NV; ++u) {
+        const int i = u * TPR + t;
+        if (i < nvec) {
+            if constexpr (VEC == 1) {
+                p[i] = aw[u];
+                p[cols + i] = ab[u];
+            } else {
+#pragma unroll
+                for (int e = u * VEC; e < (u + 1) * VEC; e += 4) {
+                    const int c = i * VEC + e - u * VEC;
+                    *reinterpret_cast<float4 *>(p + c) = make_float4(aw[e], aw[e + 1], aw[e + 2], aw[e + 3]);
+                    *reinterpret_cast<float4 *>(p + cols + c) =
+                        make_float4(ab[e], ab[e + 1], ab[e + 2], ab[e + 3]);
                 }
             }
         }
@@ -1268,7 +1299,7 @@ cudaError_t bwd_launch(const BwdArgs &a, const DeviceInfo &dev, cudaStream_t st,
 {
     const int per_sm = std::max(1, std::min(kMaxBwdBlocksPerSm, 1024 / block_threads(TPR)));
     const int64_t grid = grid_for(a.rows, TPR, dev, per_sm);
-    *nparts = static_cast<int>(grid) * (block_threads(TPR) / TPR);
+    *nparts = static_cast<int>(grid);
     return launch_pdl(norm_bwd_kernel<T, VEC, NV, TPR>, dim3(static_cast<unsigned>(grid)),
                       dim3(block_threads(TPR)), 0, st, static_cast<const T *>(a.dy),
                       static_cast<const T *>(a.x), a.w, a.w_type, a.mean, a.rstd, a.rms, a.rows,
@@ -1276,7 +1307,11 @@ cudaError_t bwd_launch(const BwdArgs &a, const DeviceInfo &dev, cudaStream_t st,
 }
 
 // Threads per row by its width: the smallest group that holds the row at 16
-// elements a thread (32 in the forward's widest).
+// elements a thread (32 in the forward's widest).  Up to 512 columns a warp has
+// the row and needs no barrier, and many warps have loads in flight: 65536 x
+// 512 bf16 29 us forward and 55 us backward, on the ring 88 and 101; 65537 x
+// 511 57 and 104, on the ring 159 and 157.  Above, the ring (measured at the
+// head of this file) up to what its registers hold.
 template <typename T, int VEC>
 cudaError_t fwd_pick(const FwdArgs &a, const DeviceInfo &dev, cudaStream_t st, int *nparts)
 {
@@ -1452,10 +1487,10 @@ size_t f8_norm_bwd_workspace_bytes(int64_t rows, int64_t cols)
         return 0;
     const DeviceInfo *dev = device_info();
     const int64_t sms = dev != nullptr ? dev->sm_count : 152;
-    // at most one partial row per warp of the resident blocks, or kMaxWideParts
-    const int64_t groups = cols <= kRegCols ? sms * kMaxBwdBlocksPerSm * 8 : kMaxWideParts;
-    return static_cast<size_t>(std::min<int64_t>(((rows + 7) / 8) * 8, groups)) * 2 *
-           static_cast<size_t>(cols) * sizeof(float);
+    // at most one partial row per resident block, or kMaxWideParts
+    const int64_t parts = cols <= kRegCols ? sms * kMaxBwdBlocksPerSm : kMaxWideParts;
+    return static_cast<size_t>(std::min<int64_t>(rows, parts)) * 2 * static_cast<size_t>(cols) *
+           sizeof(float);
 }
 
 f8_status f8_norm_bwd(const void *dy, const void *x, f8_dtype x_type, const void *w,
