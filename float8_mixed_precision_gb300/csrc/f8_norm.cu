@@ -1307,17 +1307,27 @@ cudaError_t bwd_launch(const BwdArgs &a, const DeviceInfo &dev, cudaStream_t st,
 }
 
 // Threads per row by its width: the smallest group that holds the row at 16
-// elements a thread (32 in the forward's widest).  Up to 512 columns a warp has
+// elements a thread (32 in the forward's widest).  Up to 512 columns, forward in
+// whole vectors up to 1024, a warp has
 // the row and needs no barrier, and many warps have loads in flight: 65536 x
 // 512 bf16 29 us forward and 55 us backward, on the ring 88 and 101; 65537 x
-// 511 57 and 104, on the ring 159 and 157.  Above, the ring (measured at the
-// head of this file) up to what its registers hold.
+// 511 57 and 104, on the ring 159 and 157; 32768 x 1024 forward 27, on the ring
+// 51.  Above, the ring (measured at the head of this file) up to what its
+// registers hold; up to 1024 columns 8 elements a thread, since half the threads
+// would have none of 16: 32768 x 1024 backward 47 us against 57, x 1023 forward
+// 64 against 91 and backward 61 against 87.
 template <typename T, int VEC>
 cudaError_t fwd_pick(const FwdArgs &a, const DeviceInfo &dev, cudaStream_t st, int *nparts)
 {
     constexpr int NV = 16 / VEC;
     if (a.cols <= 512)
         return fwd_launch<T, VEC, NV, 32>(a, dev, st, nparts);
+    if (a.cols <= 1024) {
+        if constexpr (VEC > 1)
+            return fwd_launch<T, VEC, 2 * NV, 32>(a, dev, st, nparts);
+        else
+            return fwd_ring<T, VEC, NV / 2, 128>(a, dev, st, nparts);
+    }
     if (a.cols <= 2048)
         return fwd_ring<T, VEC, NV, 128>(a, dev, st, nparts);
     if (a.cols <= 4096)
@@ -1333,6 +1343,8 @@ cudaError_t bwd_pick(const BwdArgs &a, const DeviceInfo &dev, cudaStream_t st, i
     constexpr int NV = 16 / VEC;
     if (a.cols <= 512)
         return bwd_launch<T, VEC, NV, 32>(a, dev, st, nparts);
+    if (a.cols <= 1024)
+        return bwd_ring<T, VEC, NV / 2, 128>(a, dev, st, nparts);
     if (a.cols <= 2048)
         return bwd_ring<T, VEC, NV, 128>(a, dev, st, nparts);
     if (a.cols <= 4096)
