@@ -14,7 +14,7 @@
 // the differences to the mean (two reductions over registers), not from the
 // sum of squares.
 //
-// Rows of more than 512 columns come through a ring of shared-memory slots that
+// Rows wider than a warp holds come through a ring of shared-memory slots that
 // bulk copies fill some rows ahead: the registers that hold a row, its
 // parameters and its column sums leave too few threads to have enough loads in
 // flight of their own.  With plain loads 8192 x 4096 took 34 us forward and
