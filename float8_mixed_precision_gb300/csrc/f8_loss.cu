@@ -1289,9 +1289,12 @@ logprobs_bwd_kernel(const __grid_constant__ LogprobBwdArgs a)
                 f[e] = ch * E + e - r.off == tok ? fa + g : g;
             }
         };
-        // the elements' floor: l = -140, where p is 0
+        // the elements' floor: l = -140, where p is 0.  chunk_floor rounds it to
+        // the logits' type, which moves l by up to 2^-9 |lse - 140| for bf16: 8 in
+        // the range where it is used.
         const float low = (lse - 140.0f) * a.t;
-        const bool dense = gh == 0.0f, ordinary = fabsf(low) < kFastRange;
+        const bool dense = gh == 0.0f;
+        const bool ordinary = fabsf(low) < kFastRange && fabsf(lse - 140.0f) < kFastRange;
         walk_chunks<T, kThreads, kUnroll>(r, wb, we, total, a.status, [&](uint4(&v)[kUnroll], int c) {
             uint4 g[kUnroll];
             if (dense) {
