@@ -44,6 +44,11 @@ constexpr double kLog2e = 1.44269504088896340736;
 constexpr float kFloor2 = -1.0e4f;
 // past this an fp32 log-sum-exp no longer tells a row's tokens apart
 constexpr float kMaxLse = 16777216.0f;
+// The mass p_r outside a row's slots: below kSmallRest its logarithm stands for
+// it (sums of exponentials that far below the row's maximum leave fp32), and
+// below 2^kNoRest, where 64 bits hold no normal number, there is none.
+constexpr float kSmallRest = 7.888609052210118e-31f;  // 2^-100
+constexpr float kNoRest = -1022.0f;
 #define F8_NEG_INF __int_as_float(0xff800000)
 #define F8_POS_INF __int_as_float(0x7f800000)
 #define F8_NAN __int_as_float(0x7fffffff)
@@ -1650,11 +1655,16 @@ __device__ __forceinline__ void drop_slots(const Slots &s, const Row<T> &r, int 
     }
 }
 
-// What the gradient of a row needs: scale (mass p - q) at the slots' ids,
-// scale dense p elsewhere.
+// What the gradient of a row needs: scale (mass p - q) at the slots' ids.
+// Elsewhere it is scale (mass p_r - q_r) times the token's share of p_r, a
+// softmax over the tokens outside the slots with a maximum of its own (shift),
+// so it does not depend on how small p_r is: factor 2^((x a + shift) s).
+// Without the tail class that is scale mass p.
 struct RowGrad {
     Softmax p;
-    float scale, mass, dense;
+    float scale, mass, factor, shift;
+
+    __device__ __forceinline__ Softmax outside() const { return Softmax{p.a, shift, p.s, 1.0f}; }
 };
 
 __device__ __forceinline__ float slot_gradient(const Slots &s, const RowGrad &g, int j, float x)
@@ -1671,7 +1681,7 @@ __device__ __forceinline__ void row_gradient(const Slots &s, const Row<T> &r, in
     float f[E];
 #pragma unroll
     for (int e = 0; e < E; ++e)
-        f[e] = g.scale * g.dense * (ex2(g.p.exponent(x[e])) * g.p.norm);
+        f[e] = g.factor * ex2(g.outside().exponent(x[e]));
     for (int j = s.head[static_cast<unsigned>(ch) % kHeads]; j >= 0; j = s.next[j]) {
         const int d = s.id[j] + r.off - ch * E;
 #pragma unroll
@@ -1688,10 +1698,9 @@ __device__ __forceinline__ void row_gradient(const Slots &s, const Row<T> &r, in
                                              const RowGrad &g, const uint4 (&v)[U], uint4 (&out)[U])
 {
     constexpr int E = Chunk<T>::E;
-    const float factor = g.scale * g.dense * g.p.norm;
 #pragma unroll
     for (int u = 0; u < U; ++u)
-        out[u] = scaled_softmax<T>(v[u], g.p, factor);
+        out[u] = scaled_softmax<T>(v[u], g.outside(), g.factor);
 #pragma unroll 1
     for (uint32_t named = named_bits<N, U>(s, c); named != 0; named &= named - 1) {
         const int u = __ffs(named) - 1, ch = c + u * N;
@@ -1716,11 +1725,13 @@ __device__ __forceinline__ void row_gradient(const Slots &s, const Row<T> &r, in
 template <bool TAIL>
 __device__ __forceinline__ RowGrad row_grad(const DistillArgs &a, const Slots &s)
 {
-    RowGrad g{Softmax{a.inv_t, -s.lse, static_cast<float>(kLog2e), 1.0f}, s.dloss * a.inv_t, s.total,
-              s.total};
-    if (TAIL && s.rest > 0.0f) {
+    const float scale = s.dloss * a.inv_t;
+    RowGrad g{Softmax{a.inv_t, -s.lse, static_cast<float>(kLog2e), 1.0f}, scale, s.total,
+              scale * s.total, -s.lse};
+    if (TAIL && s.rest != 0.0f) {
         g.mass = s.total + s.left;
-        g.dense = g.mass - s.left / s.rest;
+        g.factor = scale * (g.mass * fmaxf(s.rest, 0.0f) - s.left);
+        g.shift = -(s.lse + (s.rest > 0.0f ? logf(s.rest) : s.rest));
     }
     return g;
 }
@@ -1747,26 +1758,31 @@ __device__ __forceinline__ RowLoss row_loss(const DistillArgs &a, const Slots &s
     const bool bad = sum != sum || m == F8_POS_INF;
     const bool none = !bad && sum == 0.0f;
     const float inv_s = none ? 0.0f : (bad ? F8_NAN : 1.0f / sum);
+    const float ls = logf(sum);
     o.rest = TAIL ? outside * inv_s : 0.0f;
-    o.grad.p = Softmax{1.0f, m == F8_NEG_INF ? 0.0f : -m, a.c, inv_s};
-    o.grad.scale = s.dloss * a.inv_t;
-    o.grad.mass = o.grad.dense = s.total;
-    if (TAIL && o.rest > 0.0f) {
+    if (TAIL && o.rest < kSmallRest && t.s > 0.0f)
+        o.rest = fmaf(t.m - m, a.c, log2f(t.s / sum)) >= kNoRest
+                     ? fmaf(t.m - m, a.inv_t, logf(t.s) - ls)
+                     : 0.0f;
+    const float scale = s.dloss * a.inv_t;
+    const float shift = m == F8_NEG_INF ? 0.0f : -m;
+    o.grad = RowGrad{Softmax{1.0f, shift, a.c, inv_s}, scale, s.total, scale * s.total * inv_s, shift};
+    if (TAIL && o.rest != 0.0f) {
         o.grad.mass = s.total + s.left;
-        o.grad.dense = o.grad.mass - s.left / (TAIL ? o.rest : 1.0f);
+        o.grad.factor = scale * (o.grad.mass * fmaxf(o.rest, 0.0f) - s.left) / t.s;
+        o.grad.shift = -t.m;
     }
     o.zero = s.dloss == 0.0f || none;
     if (!loss)
         return o;
-    const float ls = logf(sum);
     o.lse = bad ? F8_NAN : (none ? F8_NEG_INF : fmaf(m, a.inv_t, ls));
     o.loss = 0.0f;
     if (s.used)
         o.loss = s.masked || none ? F8_POS_INF
                                   : s.plogp - s.zmean * a.inv_t +
                                         s.qall * fmaf(m - s.zref, a.inv_t, ls);
-    if (TAIL && o.rest > 0.0f && s.left > 0.0f)
-        o.loss += s.left * (logf(s.left) - logf(o.rest));
+    if (TAIL && o.rest != 0.0f && s.left > 0.0f)
+        o.loss += s.left * (logf(s.left) - (o.rest > 0.0f ? logf(o.rest) : o.rest));
     if (bad || s.plogp != s.plogp || s.zmean != s.zmean)
         o.loss = F8_NAN;
     return o;

@@ -708,7 +708,8 @@ f8_status f8_token_logprobs_bwd(const void *logits, f8_dtype type, int64_t rows,
  *             is the mass of one more class, "any other token", of which the
  *             student holds p_r = the sum of p outside the slots' ids;
  *             loss = sum_j q_j (log q_j - log p_id_j) + q_r (log q_r - log p_r),
- *             the last term dropped where p_r = 0.
+ *             the last term (and the gradient's) dropped where p_r < 2^-1022: the
+ *             tokens outside the ids are masked, or there are none.
  *   dlogits_v = dloss / temperature *
  *               (m p_v - sum_{j: id_j = v} q_j - [tail, v outside] p_v q_r / p_r),
  *               m = sum q + q_r
@@ -719,8 +720,9 @@ f8_status f8_token_logprobs_bwd(const void *logits, f8_dtype type, int64_t rows,
  *   values: device fp32 [rows, k].
  *   loss:   device fp32 [rows].  +inf where a slot with q > 0 names a masked
  *           token; a row of masked tokens only gets zero gradient.
- *   lse:    device fp32 [rows];  rest: device fp32 [rows] receiving p_r, needed
- *           with tail = 1 and NULL otherwise.
+ *   lse:    device fp32 [rows];  rest: device fp32 [rows] receiving p_r, or
+ *           log p_r (below 0) where p_r < 2^-100 and its term is not dropped;
+ *           needed with tail = 1 and NULL otherwise.
  *   dloss:  device fp32 [rows].  Rows with dloss = 0 get zero gradient (and
  *           are not read by f8_distill_bwd, nor are rows of |lse| >= 2^24, which
  *           it gives zeros as f8_token_logprobs_bwd does).
