@@ -222,6 +222,29 @@ def _stream(stream) -> int:
     return int(stream)
 
 
+def _empty(shape, dtype, device, stream=None) -> torch.Tensor:
+    """A new tensor for a call on `stream`.  torch's allocator orders the uses of
+    a block by the stream that was current when it was allocated: under any
+    other, the call could write where that stream still works, or have the block
+    taken from it.  So it is allocated under the call's stream, and marked as
+    used by the current one, where the caller may read it once the streams are
+    ordered."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    here = torch.cuda.current_stream(device)
+    handle = _stream(stream)
+    if handle == here.cuda_stream:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        # 0 and 1 name the default stream
+        stream = (torch.cuda.default_stream(device) if handle in (0, 1) else
+                  torch.cuda.ExternalStream(handle, device=device))
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(here)
+    return t
+
+
 def _need(what: str, dtype, *ts) -> None:
     """TypeError unless every given tensor is 2-D of `dtype`: the C calls
     read the bytes as that type and take the shape from the tensor."""

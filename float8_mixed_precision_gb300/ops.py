@@ -5,14 +5,15 @@ the distillation loss against a teacher's top logits.
 As in ``binding``, every function has the name of the C entry point of
 include/f8.h that it calls and only checks and marshals its arguments: types,
 shapes, devices and strides here, everything else in the C call.  Outputs and
-workspaces that are not passed are allocated with torch.  There is no fallback.
+workspaces that are not passed are allocated with torch, for the stream that
+the call runs on.  There is no fallback.
 """
 from __future__ import annotations
 
 import torch
 
 from . import binding
-from .binding import F8_LAYER_NORM
+from .binding import F8_LAYER_NORM, _empty
 
 
 # ---------------------------------------------------------------- norm
@@ -87,10 +88,10 @@ def f8_norm_fwd(x: torch.Tensor, w: torch.Tensor, b: torch.Tensor | None = None,
     xt, wt, xp, wp, bp = _norm_params(what, x, w, b)
     rows, cols = shape = x.shape
     dev = x.device
-    y = torch.empty_like(x) if y is None else y
+    y = _empty(shape, x.dtype, dev, stream) if y is None else y
     if mean is None and kind == F8_LAYER_NORM:
-        mean = torch.empty(rows, dtype=torch.float32, device=dev)
-    rstd = torch.empty(rows, dtype=torch.float32, device=dev) if rstd is None else rstd
+        mean = _empty(rows, torch.float32, dev, stream)
+    rstd = _empty(rows, torch.float32, dev, stream) if rstd is None else rstd
     _call(what, stream, xp, xt, wp, bp, wt, int(kind), rows, cols, float(eps),
           _ptr(what, "y", y, x.dtype, shape, dev),
           _ptr(what, "mean", mean, torch.float32, (rows,), dev),
@@ -115,16 +116,16 @@ def f8_norm_bwd(dy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, mean: torch.
     dev = x.device
     if want_db is None:
         want_db = kind == F8_LAYER_NORM
-    dx = torch.empty_like(x) if dx is None and want_dx else dx
-    dw = torch.empty_like(w) if dw is None and want_dw else dw
-    db = torch.empty_like(w) if db is None and want_db else db
+    dx = _empty(shape, x.dtype, dev, stream) if dx is None and want_dx else dx
+    dw = _empty(cols, w.dtype, dev, stream) if dw is None and want_dw else dw
+    db = _empty(cols, w.dtype, dev, stream) if db is None and want_db else db
     args = (_ptr(what, "dy", dy, x.dtype, shape, dev), xp, xt, wp, wt,
             _ptr(what, "mean", mean, torch.float32, (rows,), dev),
             _ptr(what, "rstd", rstd, torch.float32, (rows,), dev), int(kind), rows, cols,
             _ptr(what, "dx", dx, x.dtype, shape, dev), _ptr(what, "dw", dw, w.dtype, (cols,), dev),
             _ptr(what, "db", db, w.dtype, (cols,), dev))
     if ws is None and (dw is not None or db is not None):
-        ws = torch.empty(max(f8_norm_bwd_workspace_bytes(rows, cols), 1), dtype=torch.uint8, device=dev)
+        ws = _empty(max(f8_norm_bwd_workspace_bytes(rows, cols), 1), torch.uint8, dev, stream)
     _call(what, stream, *args, *_bytes(what, ws, dev))
     return dx, dw, db
 
@@ -141,16 +142,16 @@ def f8_quantize_norm(x: torch.Tensor, w: torch.Tensor, b: torch.Tensor | None = 
     _, wt, xp, wp, bp = _norm_params(what, x, w, b)
     rows, cols = shape = x.shape
     dev = x.device
-    y = torch.empty_like(x) if y is None else y
+    y = _empty(shape, x.dtype, dev, stream) if y is None else y
     if mean is None and kind == F8_LAYER_NORM:
-        mean = torch.empty(rows, dtype=torch.float32, device=dev)
-    rstd = torch.empty(rows, dtype=torch.float32, device=dev) if rstd is None else rstd
-    amax_out = torch.empty((), dtype=torch.float32, device=dev) if amax_out is None else amax_out
-    scale_out = torch.empty((), dtype=torch.float32, device=dev) if scale_out is None else scale_out
-    q = torch.empty((rows, cols), dtype=torch.uint8, device=dev) if q is None else q
-    q_t = torch.empty((cols, rows), dtype=torch.uint8, device=dev) if q_t is None else q_t
+        mean = _empty(rows, torch.float32, dev, stream)
+    rstd = _empty(rows, torch.float32, dev, stream) if rstd is None else rstd
+    amax_out = _empty((), torch.float32, dev, stream) if amax_out is None else amax_out
+    scale_out = _empty((), torch.float32, dev, stream) if scale_out is None else scale_out
+    q = _empty((rows, cols), torch.uint8, dev, stream) if q is None else q
+    q_t = _empty((cols, rows), torch.uint8, dev, stream) if q_t is None else q_t
     if ws is None:
-        ws = torch.empty(binding.f8_quantize_workspace_bytes(), dtype=torch.uint8, device=dev)
+        ws = _empty(binding.f8_quantize_workspace_bytes(), torch.uint8, dev, stream)
     _call(what, stream, xp, wp, bp, wt, int(kind), rows, cols, float(eps),
           _ptr(what, "y", y, x.dtype, shape, dev),
           _ptr(what, "mean", mean, torch.float32, (rows,), dev),
@@ -181,12 +182,12 @@ def _rows(what: str, name: str, t: torch.Tensor):
     return t.data_ptr(), ld
 
 
-def _dlogits(what: str, logits: torch.Tensor, dlogits: torch.Tensor | None):
+def _dlogits(what: str, logits: torch.Tensor, dlogits: torch.Tensor | None, stream):
     """The gradient buffer (one row per row of logits, its columns past the
     vocabulary set to zero by the call) and its pointer and row stride."""
     rows, vocab = logits.shape
     if dlogits is None:
-        dlogits = torch.empty((rows, vocab), dtype=logits.dtype, device=logits.device)
+        dlogits = _empty((rows, vocab), logits.dtype, logits.device, stream)
     if dlogits.device != logits.device:
         raise ValueError(f"{what}: tensors on different devices")
     if dlogits.dtype != logits.dtype:
@@ -209,15 +210,15 @@ def f8_token_logprobs(logits: torch.Tensor, tokens: torch.Tensor | None = None, 
     p, ld = _rows(what, "logits", logits)
     rows, vocab = logits.shape
     dev = logits.device
-    f32 = dict(dtype=torch.float32, device=dev)
+    f32 = (torch.float32, dev, stream)
     if tokens is not None and logp is None:
-        logp = torch.empty(rows, **f32)
-    entropy = torch.empty(rows, **f32) if entropy is None else entropy
-    lse = torch.empty(rows, **f32) if lse is None else lse
+        logp = _empty(rows, *f32)
+    entropy = _empty(rows, *f32) if entropy is None else entropy
+    lse = _empty(rows, *f32) if lse is None else lse
     if top_k and top_ids is None:
-        top_ids = torch.empty((rows, top_k), dtype=torch.int32, device=logits.device)
+        top_ids = _empty((rows, top_k), torch.int32, dev, stream)
     if top_k and top_logp is None:
-        top_logp = torch.empty((rows, top_k), **f32)
+        top_logp = _empty((rows, top_k), *f32)
     _call(what, stream, p, _dtype(what, logits), rows, vocab, ld,
           _ptr(what, "tokens", tokens, torch.int64, (rows,), dev), float(temperature), int(top_k),
           _ptr(what, "logp", logp, torch.float32, (rows,), dev),
@@ -239,7 +240,7 @@ def f8_token_logprobs_bwd(logits: torch.Tensor, tokens: torch.Tensor | None, lse
     p, ld = _rows(what, "logits", logits)
     rows, vocab = logits.shape
     dev = logits.device
-    dlogits, dp, ldd = _dlogits(what, logits, dlogits)
+    dlogits, dp, ldd = _dlogits(what, logits, dlogits, stream)
     _call(what, stream, p, _dtype(what, logits), rows, vocab, ld,
           _ptr(what, "tokens", tokens, torch.int64, (rows,), dev),
           _ptr(what, "lse", lse, torch.float32, (rows,), dev),
@@ -270,11 +271,11 @@ def f8_distill_fwd(logits: torch.Tensor, ids: torch.Tensor, values: torch.Tensor
     rows, vocab = logits.shape
     dev = logits.device
     slots = _slots(what, logits, ids, values)
-    f32 = dict(dtype=torch.float32, device=logits.device)
-    loss = torch.empty(rows, **f32) if loss is None else loss
-    lse = torch.empty(rows, **f32) if lse is None else lse
+    f32 = (torch.float32, dev, stream)
+    loss = _empty(rows, *f32) if loss is None else loss
+    lse = _empty(rows, *f32) if lse is None else lse
     if tail and rest is None:
-        rest = torch.empty(rows, **f32)
+        rest = _empty(rows, *f32)
     _call(what, stream, p, _dtype(what, logits), rows, vocab, ld, *slots, float(temperature),
           int(bool(tail)), _ptr(what, "loss", loss, torch.float32, (rows,), dev),
           _ptr(what, "lse", lse, torch.float32, (rows,), dev),
@@ -292,7 +293,7 @@ def f8_distill_bwd(logits: torch.Tensor, ids: torch.Tensor, values: torch.Tensor
     rows, vocab = logits.shape
     dev = logits.device
     slots = _slots(what, logits, ids, values)
-    dlogits, dp, ldd = _dlogits(what, logits, dlogits)
+    dlogits, dp, ldd = _dlogits(what, logits, dlogits, stream)
     _call(what, stream, p, _dtype(what, logits), rows, vocab, ld, *slots, float(temperature),
           int(bool(tail)), _ptr(what, "lse", lse, torch.float32, (rows,), dev),
           _ptr(what, "rest", rest, torch.float32, (rows,), dev),
@@ -312,8 +313,8 @@ def f8_distill_fwd_bwd(logits: torch.Tensor, ids: torch.Tensor, values: torch.Te
     rows, vocab = logits.shape
     dev = logits.device
     slots = _slots(what, logits, ids, values)
-    dlogits, dp, ldd = _dlogits(what, logits, dlogits)
-    loss = torch.empty(rows, dtype=torch.float32, device=logits.device) if loss is None else loss
+    dlogits, dp, ldd = _dlogits(what, logits, dlogits, stream)
+    loss = _empty(rows, torch.float32, dev, stream) if loss is None else loss
     _call(what, stream, p, _dtype(what, logits), rows, vocab, ld, *slots, float(temperature),
           int(bool(tail)), _ptr(what, "dloss", dloss, torch.float32, (rows,), dev),
           _ptr(what, "loss", loss, torch.float32, (rows,), dev), dp, ldd,
