@@ -301,7 +301,7 @@ def f8_amax(x: torch.Tensor, out: torch.Tensor | None = None, stream=None) -> to
     if x.dtype != torch.bfloat16:
         raise TypeError("f8_amax takes a bf16 tensor")
     if out is None:
-        out = torch.empty((), dtype=torch.float32, device=x.device)
+        out = _empty((), torch.float32, x.device, stream)
     _check(lib().f8_amax(_ptr(x), x.numel(), _ptr(out), _stream(stream)), "f8_amax")
     return out
 
@@ -315,11 +315,11 @@ def f8_cast_transpose(x: torch.Tensor, amax: torch.Tensor, scale_out: torch.Tens
     rows, cols = x.shape
     dev = x.device
     if scale_out is None:
-        scale_out = torch.empty((), dtype=torch.float32, device=dev)
+        scale_out = _empty((), torch.float32, dev, stream)
     if q is None and want_q:
-        q = torch.empty((rows, cols), dtype=torch.uint8, device=dev)
+        q = _empty((rows, cols), torch.uint8, dev, stream)
     if q_t is None and want_t:
-        q_t = torch.empty((cols, rows), dtype=torch.uint8, device=dev)
+        q_t = _empty((cols, rows), torch.uint8, dev, stream)
     _check(lib().f8_cast_transpose(_ptr(x), rows, cols, _ptr(amax), _ptr(scale_out), _ptr(q),
                                    _ptr(q_t), _stream(stream)), "f8_cast_transpose")
     return q, q_t, scale_out
@@ -341,15 +341,15 @@ def f8_quantize(x: torch.Tensor, amax_out: torch.Tensor | None = None,
     rows, cols = x.shape
     dev = x.device
     if amax_out is None:
-        amax_out = torch.empty((), dtype=torch.float32, device=dev)
+        amax_out = _empty((), torch.float32, dev, stream)
     if scale_out is None:
-        scale_out = torch.empty((), dtype=torch.float32, device=dev)
+        scale_out = _empty((), torch.float32, dev, stream)
     if q is None and want_q:
-        q = torch.empty((rows, cols), dtype=torch.uint8, device=dev)
+        q = _empty((rows, cols), torch.uint8, dev, stream)
     if q_t is None and want_t:
-        q_t = torch.empty((cols, rows), dtype=torch.uint8, device=dev)
+        q_t = _empty((cols, rows), torch.uint8, dev, stream)
     if ws is None:
-        ws = torch.empty(f8_quantize_workspace_bytes(), dtype=torch.uint8, device=dev)
+        ws = _empty(f8_quantize_workspace_bytes(), torch.uint8, dev, stream)
     if fmt == F8_E4M3:
         _check(lib().f8_quantize(_ptr(x), rows, cols, _ptr(amax_out), _ptr(scale_out), _ptr(q),
                                  _ptr(q_t), _ptr(ws), ws.numel(), _stream(stream)), "f8_quantize")
@@ -371,7 +371,7 @@ def f8_gemm(a: torch.Tensor, b: torch.Tensor, scale_a: torch.Tensor, scale_b: to
     if K != K2:
         raise ValueError("contraction sizes differ")
     if out is None:
-        out = torch.empty((M, N), dtype=torch.bfloat16, device=a.device)
+        out = _empty((M, N), torch.bfloat16, a.device, stream)
     if fmt_a == F8_E4M3 and fmt_b == F8_E4M3:
         _check(lib().f8_gemm(_ptr(a), _ptr(b), M, N, K, _ptr(scale_a), _ptr(scale_b), _ptr(out),
                              _stream(stream)), "f8_gemm")
@@ -400,7 +400,7 @@ def f8_gemm_grouped(problems, stream=None) -> list:
         if K != K2:
             raise ValueError("contraction sizes differ")
         if out is None:
-            out = torch.empty((M, N), dtype=torch.bfloat16, device=a.device)
+            out = _empty((M, N), torch.bfloat16, a.device, stream)
         arr[i] = _GemmProblem(_ptr(a), _ptr(b), M, N, K, _ptr(sa), _ptr(sb), _ptr(out), int(fa),
                               int(fb))
         outs.append(out)
@@ -423,10 +423,10 @@ class LinearSaved:
     x_scalars: torch.Tensor | None = None  # [2] fp32 amax_x, scale_x shared by a group
 
     @classmethod
-    def empty(cls, M: int, N: int, K: int, device) -> "LinearSaved":
-        return cls(torch.empty((K, M), dtype=torch.uint8, device=device),
-                   torch.empty((K, N), dtype=torch.uint8, device=device),
-                   torch.empty(4, dtype=torch.float32, device=device))
+    def empty(cls, M: int, N: int, K: int, device, stream=None) -> "LinearSaved":
+        return cls(_empty((K, M), torch.uint8, device, stream),
+                   _empty((K, N), torch.uint8, device, stream),
+                   _empty(4, torch.float32, device, stream))
 
     def c_struct(self) -> _Saved:
         p = self.scalars.data_ptr()
@@ -448,8 +448,8 @@ class LinearSaved:
     def scale_w(self): return self.scalars[3]
 
 
-def workspace(M: int, N: int, K: int, device) -> torch.Tensor:
-    return torch.empty(max(f8_linear_workspace_bytes(M, N, K), 1), dtype=torch.uint8, device=device)
+def workspace(M: int, N: int, K: int, device, stream=None) -> torch.Tensor:
+    return _empty(max(f8_linear_workspace_bytes(M, N, K), 1), torch.uint8, device, stream)
 
 
 def f8_quantize_multi_workspace_bytes() -> int:
@@ -472,14 +472,14 @@ def f8_quantize_multi(xs, fmt: int = F8_E4M3, outs=None, ws: torch.Tensor | None
         if outs is not None:
             q, q_t, sc, am = outs[i]
         else:
-            q = torch.empty((rows, cols), dtype=torch.uint8, device=dev) if want_q else None
-            q_t = torch.empty((cols, rows), dtype=torch.uint8, device=dev) if want_t else None
-            sc = torch.empty((), dtype=torch.float32, device=dev)
-            am = torch.empty((), dtype=torch.float32, device=dev)
+            q = _empty((rows, cols), torch.uint8, dev, stream) if want_q else None
+            q_t = _empty((cols, rows), torch.uint8, dev, stream) if want_t else None
+            sc = _empty((), torch.float32, dev, stream)
+            am = _empty((), torch.float32, dev, stream)
         arr[i] = _QuantTensor(_ptr(x), rows, cols, _ptr(am), _ptr(sc), _ptr(q), _ptr(q_t))
         res.append((q, q_t, sc, am))
     if ws is None:
-        ws = torch.empty(f8_quantize_multi_workspace_bytes(), dtype=torch.uint8, device=xs[0].device)
+        ws = _empty(f8_quantize_multi_workspace_bytes(), torch.uint8, xs[0].device, stream)
     _check(lib().f8_quantize_multi(arr, n, int(fmt), _ptr(ws), ws.numel(), _stream(stream)),
            "f8_quantize_multi")
     return res
@@ -490,18 +490,17 @@ def f8_linear_group_workspace_bytes(M: int, K: int, Ns) -> int:
     return int(lib().f8_linear_group_workspace_bytes(M, K, arr, len(Ns)))
 
 
-def group_workspace(M: int, K: int, Ns, device) -> torch.Tensor:
-    return torch.empty(max(f8_linear_group_workspace_bytes(M, K, Ns), 1), dtype=torch.uint8,
-                       device=device)
+def group_workspace(M: int, K: int, Ns, device, stream=None) -> torch.Tensor:
+    return _empty(max(f8_linear_group_workspace_bytes(M, K, Ns), 1), torch.uint8, device, stream)
 
 
-def group_saved(M: int, K: int, Ns, device) -> list:
+def group_saved(M: int, K: int, Ns, device, stream=None) -> list:
     """Saved buffers of a group of linears sharing X [M, K]: one q(X)^T and
     one (amax_x, scale_x) shared, q(W_i)^T and (amax_w, scale_w) per member."""
-    x_t = torch.empty((K, M), dtype=torch.uint8, device=device)
-    xs = torch.empty(2, dtype=torch.float32, device=device)
-    return [LinearSaved(x_t, torch.empty((K, N), dtype=torch.uint8, device=device),
-                        torch.empty(4, dtype=torch.float32, device=device), xs) for N in Ns]
+    x_t = _empty((K, M), torch.uint8, device, stream)
+    xs = _empty(2, torch.float32, device, stream)
+    return [LinearSaved(x_t, _empty((K, N), torch.uint8, device, stream),
+                        _empty(4, torch.float32, device, stream), xs) for N in Ns]
 
 
 def _group_array(saved, Ns, w=None, y=None, dy=None, dx=None, dw=None):
@@ -526,11 +525,11 @@ def f8_linear_fwd_group(x: torch.Tensor, ws_: list, ys: list | None = None, save
             raise ValueError("in-feature sizes differ")
     dev = x.device
     if ys is None:
-        ys = [torch.empty((M, N), dtype=torch.bfloat16, device=dev) for N in Ns]
+        ys = [_empty((M, N), torch.bfloat16, dev, stream) for N in Ns]
     if saved is None:
-        saved = group_saved(M, K, Ns, dev)
+        saved = group_saved(M, K, Ns, dev, stream)
     if ws is None:
-        ws = group_workspace(M, K, Ns, dev)
+        ws = group_workspace(M, K, Ns, dev, stream)
     arr = _group_array(saved, Ns, w=ws_, y=ys)
     _check(lib().f8_linear_fwd_group(_ptr(x), M, K, arr, len(Ns), _ptr(ws), ws.numel(),
                                      _stream(stream)), "f8_linear_fwd_group")
@@ -547,11 +546,11 @@ def f8_linear_bwd_group(dys: list, saved: list, K: int, dxs: list | None = None,
     Ns = [dy.shape[1] for dy in dys]
     dev = dys[0].device
     if want_dx and dxs is None:
-        dxs = [torch.empty((M, K), dtype=torch.bfloat16, device=dev) for _ in Ns]
+        dxs = [_empty((M, K), torch.bfloat16, dev, stream) for _ in Ns]
     if want_dw and dws is None:
-        dws = [torch.empty((N, K), dtype=torch.bfloat16, device=dev) for N in Ns]
+        dws = [_empty((N, K), torch.bfloat16, dev, stream) for N in Ns]
     if ws is None:
-        ws = group_workspace(M, K, Ns, dev)
+        ws = group_workspace(M, K, Ns, dev, stream)
     arr = _group_array(saved, Ns, dy=dys, dx=dxs if want_dx else None, dw=dws if want_dw else None)
     _check(lib().f8_linear_bwd_group(arr, len(Ns), M, K, int(fmt), _ptr(ws), ws.numel(),
                                      _stream(stream)), "f8_linear_bwd_group")
@@ -568,11 +567,11 @@ def f8_linear_fwd(x: torch.Tensor, w: torch.Tensor, y: torch.Tensor | None = Non
         raise ValueError("in-feature sizes differ")
     dev = x.device
     if y is None:
-        y = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
+        y = _empty((M, N), torch.bfloat16, dev, stream)
     if saved is None:
-        saved = LinearSaved.empty(M, N, K, dev)
+        saved = LinearSaved.empty(M, N, K, dev, stream)
     if ws is None:
-        ws = workspace(M, N, K, dev)
+        ws = workspace(M, N, K, dev, stream)
     s = saved.c_struct()
     _check(lib().f8_linear_fwd(_ptr(x), _ptr(w), M, N, K, _ptr(y), ctypes.byref(s), _ptr(ws),
                                ws.numel(), _stream(stream)), "f8_linear_fwd")
@@ -590,9 +589,9 @@ def f8_linear_fwd_noalloc(x: torch.Tensor, w: torch.Tensor, y: torch.Tensor | No
         raise ValueError("in-feature sizes differ")
     dev = x.device
     if y is None:
-        y = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
+        y = _empty((M, N), torch.bfloat16, dev, stream)
     if saved is None:
-        saved = LinearSaved.empty(M, N, K, dev)
+        saved = LinearSaved.empty(M, N, K, dev, stream)
     s = saved.c_struct()
     _check(lib().f8_linear_fwd_noalloc(_ptr(x), _ptr(w), M, N, K, _ptr(y), ctypes.byref(s),
                                        _stream(stream)), "f8_linear_fwd_noalloc")
@@ -607,13 +606,13 @@ def f8_quantize_swiglu(a: torch.Tensor, b: torch.Tensor, h: torch.Tensor | None 
         raise TypeError("f8_quantize_swiglu takes two 2-D bf16 tensors of one shape")
     rows, cols = a.shape
     dev = a.device
-    amax_out = torch.empty((), dtype=torch.float32, device=dev) if amax_out is None else amax_out
-    scale_out = torch.empty((), dtype=torch.float32, device=dev) if scale_out is None else scale_out
-    q = torch.empty((rows, cols), dtype=torch.uint8, device=dev) if q is None else q
-    q_t = torch.empty((cols, rows), dtype=torch.uint8, device=dev) if q_t is None else q_t
+    amax_out = _empty((), torch.float32, dev, stream) if amax_out is None else amax_out
+    scale_out = _empty((), torch.float32, dev, stream) if scale_out is None else scale_out
+    q = _empty((rows, cols), torch.uint8, dev, stream) if q is None else q
+    q_t = _empty((cols, rows), torch.uint8, dev, stream) if q_t is None else q_t
     if ws is None:
-        ws = torch.empty(f8_quantize_workspace_bytes(), dtype=torch.uint8, device=dev)
-    h = torch.empty_like(a) if h is None else h
+        ws = _empty(f8_quantize_workspace_bytes(), torch.uint8, dev, stream)
+    h = _empty(a.shape, a.dtype, a.device, stream) if h is None else h
     _check(lib().f8_quantize_swiglu(_ptr(a), _ptr(b), _ptr(h), rows, cols, _ptr(amax_out),
                                     _ptr(scale_out), _ptr(q), _ptr(q_t), _ptr(ws), ws.numel(),
                                     _stream(stream)), "f8_quantize_swiglu")
@@ -631,12 +630,12 @@ def f8_linear_fwd_swiglu(a: torch.Tensor, b: torch.Tensor, w: torch.Tensor,
         raise ValueError("shapes do not match")
     dev = a.device
     if y is None:
-        y = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
+        y = _empty((M, N), torch.bfloat16, dev, stream)
     if saved is None:
-        saved = LinearSaved.empty(M, N, K, dev)
+        saved = LinearSaved.empty(M, N, K, dev, stream)
     if ws is None:
-        ws = workspace(M, N, K, dev)
-    h = torch.empty_like(a) if h is None else h
+        ws = workspace(M, N, K, dev, stream)
+    h = _empty(a.shape, a.dtype, a.device, stream) if h is None else h
     s = saved.c_struct()
     _check(lib().f8_linear_fwd_swiglu(_ptr(a), _ptr(b), _ptr(h), _ptr(w), M, N, K, _ptr(y),
                                       ctypes.byref(s), _ptr(ws), ws.numel(), _stream(stream)),
@@ -676,14 +675,14 @@ def f8_linear_fwd_w13_swiglu(x: torch.Tensor, w13: torch.Tensor, ab: torch.Tenso
         raise ValueError("w13 must be [2F, K] with F % 128 == 0")
     F = N // 2
     dev = x.device
-    ab = torch.empty((M, N), dtype=torch.bfloat16, device=dev) if ab is None else ab
-    h = torch.empty((M, F), dtype=torch.bfloat16, device=dev) if h is None else h
-    saved = LinearSaved.empty(M, N, K, dev) if saved is None else saved
-    amax_h = torch.empty(1, dtype=torch.float32, device=dev) if amax_h is None else amax_h
-    scale_h = torch.empty(1, dtype=torch.float32, device=dev) if scale_h is None else scale_h
-    h_q = torch.empty((M, F), dtype=torch.uint8, device=dev) if h_q is None else h_q
-    h_t = torch.empty((F, M), dtype=torch.uint8, device=dev) if h_t is None else h_t
-    ws = workspace(M, N, K, dev) if ws is None else ws
+    ab = _empty((M, N), torch.bfloat16, dev, stream) if ab is None else ab
+    h = _empty((M, F), torch.bfloat16, dev, stream) if h is None else h
+    saved = LinearSaved.empty(M, N, K, dev, stream) if saved is None else saved
+    amax_h = _empty(1, torch.float32, dev, stream) if amax_h is None else amax_h
+    scale_h = _empty(1, torch.float32, dev, stream) if scale_h is None else scale_h
+    h_q = _empty((M, F), torch.uint8, dev, stream) if h_q is None else h_q
+    h_t = _empty((F, M), torch.uint8, dev, stream) if h_t is None else h_t
+    ws = workspace(M, N, K, dev, stream) if ws is None else ws
     s = saved.c_struct()
     _check(lib().f8_linear_fwd_w13_swiglu(_ptr(x), _ptr(w13), M, F, K, _ptr(ab), _ptr(h),
                                           ctypes.byref(s), _ptr(amax_h), _ptr(scale_h), _ptr(h_q),
@@ -705,12 +704,12 @@ def f8_linear_bwd_w13_swiglu(dh: torch.Tensor, ab: torch.Tensor, saved: LinearSa
     if ab.shape != (M, 2 * F):
         raise ValueError("ab must be [M, 2F] for dh [M, F]")
     dev = dh.device
-    dab = torch.empty_like(ab) if dab is None else dab
+    dab = _empty(ab.shape, ab.dtype, ab.device, stream) if dab is None else dab
     if dx is None and want_dx:
-        dx = torch.empty((M, K), dtype=torch.bfloat16, device=dev)
+        dx = _empty((M, K), torch.bfloat16, dev, stream)
     if dw is None and want_dw:
-        dw = torch.empty((2 * F, K), dtype=torch.bfloat16, device=dev)
-    ws = workspace(M, 2 * F, K, dev) if ws is None else ws
+        dw = _empty((2 * F, K), torch.bfloat16, dev, stream)
+    ws = workspace(M, 2 * F, K, dev, stream) if ws is None else ws
     s = saved.c_struct()
     _check(lib().f8_linear_bwd_w13_swiglu(_ptr(dh), _ptr(ab), ctypes.byref(s), M, F, K, _ptr(dab),
                                           int(dy_fmt), _ptr(dx), _ptr(dw), _ptr(ws), ws.numel(),
@@ -728,13 +727,13 @@ def f8_quantize_swiglu_bwd(dh: torch.Tensor, ab: torch.Tensor, dab: torch.Tensor
     if ab.shape != (M, 2 * F):
         raise ValueError("ab must be [M, 2F] for dh [M, F]")
     dev = dh.device
-    dab = torch.empty_like(ab) if dab is None else dab
-    amax_out = torch.empty((), dtype=torch.float32, device=dev) if amax_out is None else amax_out
-    scale_out = torch.empty((), dtype=torch.float32, device=dev) if scale_out is None else scale_out
-    q = torch.empty((M, 2 * F), dtype=torch.uint8, device=dev) if q is None else q
-    q_t = torch.empty((2 * F, M), dtype=torch.uint8, device=dev) if q_t is None else q_t
+    dab = _empty(ab.shape, ab.dtype, ab.device, stream) if dab is None else dab
+    amax_out = _empty((), torch.float32, dev, stream) if amax_out is None else amax_out
+    scale_out = _empty((), torch.float32, dev, stream) if scale_out is None else scale_out
+    q = _empty((M, 2 * F), torch.uint8, dev, stream) if q is None else q
+    q_t = _empty((2 * F, M), torch.uint8, dev, stream) if q_t is None else q_t
     if ws is None:
-        ws = torch.empty(f8_quantize_workspace_bytes(), dtype=torch.uint8, device=dev)
+        ws = _empty(f8_quantize_workspace_bytes(), torch.uint8, dev, stream)
     _check(lib().f8_quantize_swiglu_bwd(_ptr(dh), _ptr(ab), M, F, _ptr(dab), int(fmt),
                                         _ptr(amax_out), _ptr(scale_out), _ptr(q), _ptr(q_t),
                                         _ptr(ws), ws.numel(), _stream(stream)),
@@ -754,9 +753,9 @@ def f8_gemm_w13_swiglu(x_q: torch.Tensor, w13_q: torch.Tensor, scale_x: torch.Te
     if K != K2 or N % 256:
         raise ValueError("w13_q must be [2F, K] with F % 128 == 0")
     dev = x_q.device
-    ab = torch.empty((M, N), dtype=torch.bfloat16, device=dev) if ab is None else ab
-    h = torch.empty((M, N // 2), dtype=torch.bfloat16, device=dev) if h is None else h
-    amax_h = torch.empty(1, dtype=torch.float32, device=dev) if amax_h is None else amax_h
+    ab = _empty((M, N), torch.bfloat16, dev, stream) if ab is None else ab
+    h = _empty((M, N // 2), torch.bfloat16, dev, stream) if h is None else h
+    amax_h = _empty(1, torch.float32, dev, stream) if amax_h is None else amax_h
     _check(lib().f8_gemm_w13_swiglu(_ptr(x_q), _ptr(w13_q), M, N // 2, K, _ptr(scale_x),
                                     _ptr(scale_w13), _ptr(ab), _ptr(h), _ptr(amax_h),
                                     _stream(stream)), "f8_gemm_w13_swiglu")
@@ -774,11 +773,11 @@ def f8_linear_bwd(dy: torch.Tensor, saved: LinearSaved, K: int | None = None,
     K = saved.x_t.shape[0]
     dev = dy.device
     if dx is None and want_dx:
-        dx = torch.empty((M, K), dtype=torch.bfloat16, device=dev)
+        dx = _empty((M, K), torch.bfloat16, dev, stream)
     if dw is None and want_dw:
-        dw = torch.empty((N, K), dtype=torch.bfloat16, device=dev)
+        dw = _empty((N, K), torch.bfloat16, dev, stream)
     if ws is None:
-        ws = workspace(M, N, K, dev)
+        ws = workspace(M, N, K, dev, stream)
     s = saved.c_struct()
     if dy_fmt == F8_E4M3:
         _check(lib().f8_linear_bwd(_ptr(dy), ctypes.byref(s), M, N, K, _ptr(dx), _ptr(dw), _ptr(ws),
@@ -796,7 +795,7 @@ def f8_transpose_u8(x: torch.Tensor, out: torch.Tensor | None = None, stream=Non
         raise TypeError("f8_transpose_u8 takes a 2-D uint8 tensor")
     rows, cols = x.shape
     if out is None:
-        out = torch.empty((cols, rows), dtype=torch.uint8, device=x.device)
+        out = _empty((cols, rows), torch.uint8, x.device, stream)
     _check(lib().f8_transpose_u8(_ptr(x), rows, cols, _ptr(out), _stream(stream)), "f8_transpose_u8")
     return out
 
@@ -817,10 +816,9 @@ def f8_linear_fwd_qw(x: torch.Tensor, w_q: torch.Tensor, saved: LinearSaved,
     if K != K2:
         raise ValueError("in-feature sizes differ")
     if y is None:
-        y = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
+        y = _empty((M, N), torch.bfloat16, x.device, stream)
     if ws is None:
-        ws = torch.empty(max(f8_linear_fwd_qw_workspace_bytes(M, K), 1), dtype=torch.uint8,
-                         device=x.device)
+        ws = _empty(max(f8_linear_fwd_qw_workspace_bytes(M, K), 1), torch.uint8, x.device, stream)
     s = saved.c_struct()
     _check(lib().f8_linear_fwd_qw(_ptr(x), _ptr(w_q), M, N, K, _ptr(y), ctypes.byref(s), _ptr(ws),
                                   ws.numel(), _stream(stream)), "f8_linear_fwd_qw")
