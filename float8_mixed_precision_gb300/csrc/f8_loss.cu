@@ -2343,13 +2343,28 @@ int cluster_for(int64_t rows, int64_t chunks, const DeviceInfo &dev)
     return c;
 }
 
-template <typename F>
-cudaError_t allow_smem(F *kernel, size_t bytes)
+// Lets Kernel be launched with up to `bytes` of dynamic shared memory: once per
+// device, at the most that any call needs, since the limit belongs to the kernel
+// and calls from other threads launch under it too.
+template <auto Kernel>
+cudaError_t allow_smem(size_t bytes, const DeviceInfo &dev)
 {
-    if (bytes <= 48 * 1024)
-        return cudaSuccess;
-    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                static_cast<int>(bytes));
+    static std::once_flag once[64];
+    static cudaError_t err[64];
+    const int d = dev.ordinal & 63;
+    std::call_once(once[d], [&] {
+        err[d] = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                      static_cast<int>(bytes));
+    });
+    return err[d];
+}
+
+// Groups of 32 chunks that a row of `vocab` tokens touches at any offset.
+template <typename T>
+int most_groups(int64_t vocab)
+{
+    constexpr int E = Chunk<T>::E;
+    return static_cast<int>(((vocab + E - 1 + E) / E + 31) / 32);
 }
 
 template <typename T>
@@ -2358,13 +2373,15 @@ cudaError_t logprobs(LogprobArgs a, const DeviceInfo &dev, cudaStream_t st)
     constexpr int E = Chunk<T>::E;
     const int64_t chunks = (static_cast<int64_t>(a.vocab) + E - 1 + E) / E;
     a.cluster = cluster_for(a.rows, chunks, dev);
-    const int ngroups = static_cast<int>((chunks + 31) / 32);
-    size_t smem = 0;
-    if (a.top_k > 0)
-        smem = 4u * top_layout((ngroups + a.cluster - 1) / a.cluster, a.top_k, a.cluster).words;
     const dim3 grid(static_cast<unsigned>(a.rows * a.cluster));
     if (a.top_k > 0) {
-        const cudaError_t e = allow_smem(logprobs_kernel<T, true>, smem);
+        const int ngroups = most_groups<T>(a.vocab);
+        const size_t smem =
+            4u * top_layout((ngroups + a.cluster - 1) / a.cluster, a.top_k, a.cluster).words;
+        // one block a row of the largest vocabulary: 116 KB for bf16, 180 KB for
+        // fp32; a cluster's merge arrays take less than the groups that it shares
+        const cudaError_t e = allow_smem<logprobs_kernel<T, true>>(
+            4u * top_layout(most_groups<T>(F8_MAX_VOCAB), F8_MAX_TOP, 1).words, dev);
         if (e != cudaSuccess)
             return e;
         return launch_pdl_cluster(logprobs_kernel<T, true>, grid, dim3(kThreads), smem, st,
@@ -2423,16 +2440,9 @@ bool ring_takes(const DistillArgs &a, const DeviceInfo &dev)
 template <typename T, bool TAIL, bool BWD>
 cudaError_t distill_ring(const DistillArgs &a, const DeviceInfo &dev, cudaStream_t st)
 {
-    static std::once_flag once[64];
-    static cudaError_t err[64];
-    const int d = dev.ordinal & 63;
-    std::call_once(once[d], [&] {
-        err[d] = cudaFuncSetAttribute(distill_ring_kernel<T, TAIL, BWD>,
-                                      cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                      static_cast<int>(kRingSmem));
-    });
-    if (err[d] != cudaSuccess)
-        return err[d];
+    const cudaError_t e = allow_smem<distill_ring_kernel<T, TAIL, BWD>>(kRingSmem, dev);
+    if (e != cudaSuccess)
+        return e;
     return launch_pdl(distill_ring_kernel<T, TAIL, BWD>,
                       dim3(static_cast<unsigned>(std::min<int64_t>(a.rows, dev.sm_count))),
                       dim3(kRingThreads), kRingSmem, st, a, wait_limit_ns());
