@@ -40,6 +40,7 @@
 
 #include "f8_internal.h"
 #include "f8_ptx.cuh"
+#include "f8_ring.h"
 
 namespace f8 {
 namespace {
@@ -281,14 +282,16 @@ struct Ring {
     uint32_t pitch;
     int64_t rows, cols;
     const T *src[N];
-    bool ok;  // no wait has run out
+    int issued;  // copies, by the thread that issues them
+    bool ok;     // no wait has run out
 
     __device__ __forceinline__ T *row(int slot, int which) const
     {
         return reinterpret_cast<T *>(slots + (slot * N + which) * pitch);
     }
-    __device__ __forceinline__ void fill(int slot, int64_t r) const
+    __device__ __forceinline__ void fill(int slot, int64_t r)
     {
+        ++issued;
         if (WHOLE) {
             const uint32_t bytes = static_cast<uint32_t>(cols) * sizeof(T);
             mbar_arrive_expect_tx(&full[slot], N * bytes);
@@ -305,13 +308,25 @@ struct Ring {
                 bulk_load(row(slot, i), src[i] + c.first, c.bytes, &full[slot]);
         }
     }
+    // A wait that runs out sets the status.  The thread then goes on without
+    // waiting, so that all keep to the barriers (what it stores is of no use); the
+    // one that issues the copies issues no more, since the slot's phase is not over.
     __device__ __forceinline__ void wait(int slot, uint32_t parity, uint64_t limit_ns,
                                          unsigned *status)
     {
         if (ok && !mbar_wait(&full[slot], parity, nullptr, limit_ns)) {
-            ok = false;  // go on without waiting: every thread keeps to the barriers
+            ok = false;
             atomicOr(status, kStatusTimeout);
         }
+    }
+    // The issuing thread's copies land before the block leaves, or takes the slots'
+    // memory for something else.
+    __device__ __forceinline__ void drain() const
+    {
+        if (!ok)
+            ring_drain(issued, stages, [&](int slot, uint32_t parity) {
+                mbar_wait(&full[slot], parity, nullptr, kDrainLimitNs);
+            });
     }
 };
 
@@ -482,7 +497,7 @@ norm_fwd_ring_kernel(const T *x, const void *__restrict__ w, const void *__restr
     __shared__ __align__(8) uint64_t full[kGroups * kMaxStages];
     const int group = threadIdx.x / TPR, t = threadIdx.x % TPR;
     Ring<T, 1, (VEC > 1)> ring{dyn + static_cast<size_t>(group) * stages * pitch,
-                    full + group * kMaxStages, stages, pitch, rows, cols, {x}, true};
+                    full + group * kMaxStages, stages, pitch, rows, cols, {x}, 0, true};
     if (t == 0) {
         for (int i = 0; i < stages; ++i)
             mbar_init(&ring.full[i], 1);
@@ -558,7 +573,7 @@ norm_fwd_ring_kernel(const T *x, const void *__restrict__ w, const void *__restr
             1.0f / sqrtf(ring_sum<TPR, false>(q.x + q.y, 0.0f, red, group, buf).x * inv_c + eps);
         // every thread has taken its part of the row: the slot can be refilled
         if (t == 0) {
-            if (row + ahead < rows)
+            if (ring.ok && row + ahead < rows)
                 ring.fill(slot, row + ahead);
             if (mean != nullptr && !rms)
                 mean[row] = mu;
@@ -588,10 +603,8 @@ norm_fwd_ring_kernel(const T *x, const void *__restrict__ w, const void *__restr
             parity ^= 1u;
         }
     }
-    // copies that a wait gave up on land before the block leaves
-    if (!ring.ok && t == 0)
-        for (int i = 0; i < stages; ++i)
-            mbar_wait(&ring.full[i], parity ^ (i < slot ? 1u : 0u), nullptr, limit_ns);
+    if (t == 0)
+        ring.drain();
     if (amax_mode != kAmaxNone)
         block_amax(m2, amax_mode, amax, status);
 }
@@ -783,7 +796,7 @@ norm_bwd_ring_kernel(const T *dy, const T *x, const void *__restrict__ w, int w_
     __shared__ __align__(8) uint64_t full[kGroups * kMaxStages];
     const int group = threadIdx.x / TPR, t = threadIdx.x % TPR;
     Ring<T, 2, (VEC > 1)> ring{dyn + static_cast<size_t>(group) * stages * 2 * pitch,
-                    full + group * kMaxStages, stages, pitch, rows, cols, {x, dy}, true};
+                    full + group * kMaxStages, stages, pitch, rows, cols, {x, dy}, 0, true};
     if (t == 0) {
         for (int i = 0; i < stages; ++i)
             mbar_init(&ring.full[i], 1);
@@ -848,7 +861,7 @@ norm_bwd_ring_kernel(const T *dy, const T *x, const void *__restrict__ w, int w_
             s2 = __fadd2_rn(s2, g[i]);
         }
         const float2 c = ring_sum<TPR, true>(s1.x + s1.y, s2.x + s2.y, red, group, buf);
-        if (t == 0 && row + ahead < rows)
+        if (t == 0 && ring.ok && row + ahead < rows)
             ring.fill(slot, row + ahead);
         if (dx != nullptr) {
             const float k1 = -r * (c.x * inv_c), k2 = rms ? 0.0f : -r * (c.y * inv_c);
@@ -874,9 +887,8 @@ norm_bwd_ring_kernel(const T *dy, const T *x, const void *__restrict__ w, int w_
             parity ^= 1u;
         }
     }
-    if (!ring.ok && t == 0)
-        for (int i = 0; i < stages; ++i)
-            mbar_wait(&ring.full[i], parity ^ (i < slot ? 1u : 0u), nullptr, limit_ns);
+    if (t == 0)
+        ring.drain();
     if (parts == nullptr)
         return;
     // the groups' sums joined in group order, through the slots' memory
