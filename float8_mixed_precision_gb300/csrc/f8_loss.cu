@@ -31,6 +31,7 @@
 
 #include "f8_internal.h"
 #include "f8_ptx.cuh"
+#include "f8_ring.h"
 
 namespace f8 {
 namespace {
@@ -2059,14 +2060,16 @@ constexpr int kPieceChunks = kUnroll * kRingConsumers;
 constexpr int kPieceBytes = kPieceChunks * 16;
 constexpr int kPieces = 6;
 constexpr int kKeep = 4;  // the other two are under way
-constexpr uint64_t kDrainLimitNs = 1000000000ull;
 
 constexpr size_t kRingSmem = static_cast<size_t>(kPieces) * kPieceBytes +
                              kSlotBuffers * sizeof(Slots);
 
 // Piece of position `seq` in the queue: its slot, and the parity of its phase.
-__device__ __forceinline__ int ring_slot(uint32_t seq) { return static_cast<int>(seq % kPieces); }
-__device__ __forceinline__ uint32_t ring_parity(uint32_t seq) { return (seq / kPieces) & 1u; }
+__device__ __forceinline__ int ring_slot(uint32_t seq) { return f8::ring_slot(seq, kPieces); }
+__device__ __forceinline__ uint32_t ring_parity(uint32_t seq)
+{
+    return f8::ring_parity(seq, kPieces);
+}
 
 template <typename T, bool TAIL, bool BWD>
 __global__ void __launch_bounds__(kRingThreads, 1)
@@ -2176,11 +2179,11 @@ distill_ring_kernel(const __grid_constant__ DistillArgs a, uint64_t limit_ns)
                               r.base + static_cast<int64_t>(r.w0 + c0) * E, bytes, &full[slot]);
                 }
             }
-            if (*abort_flag) {  // copies still under way land before the block leaves
-                const uint32_t first = seq > kPieces ? seq - kPieces : 0;
-                for (uint32_t p = first; p < seq; ++p)
-                    mbar_wait(&full[ring_slot(p)], ring_parity(p), nullptr, kDrainLimitNs);
-            }
+            // the copies land before the block leaves, also where another warp gives up
+            // on one after this
+            ring_drain(seq, kPieces, [&](int slot, uint32_t parity) {
+                mbar_wait(&full[slot], parity, nullptr, kDrainLimitNs);
+            });
         }
         __syncwarp();
     } else {

@@ -3,7 +3,8 @@
 // wait for a parity returns once the phase of that parity is over, and a second
 // copy into a slot whose phase is not over is an error.  A thread fills the
 // slots ahead of its items and refills them as the items arrive, up to a wait
-// that gives up, with any of the copies then under way landed or not.
+// that gives up, with any of the copies then under way landed or not; or one
+// thread issues all copies and is done before another's wait for one gives up.
 // Afterwards every copy must have landed, and no wait may name a phase that is
 // not the slot's own (it would return at once, or never).
 // Usage: ring_check [cases]; prints "<n> cases, <m> mismatches".
@@ -94,6 +95,27 @@ static int64_t taking(int slots, int64_t count, int64_t at)
     return m.bad + m.left();
 }
 
+// The thread that issues the copies is not the one that takes them: it has issued
+// the last of `count` while the taker has yet to give up, so it waits for them
+// whether or not anyone has.
+static int64_t apart(int slots, int64_t count)
+{
+    Model m(slots);
+    uint32_t issued = 0;
+    int64_t taken = 0;
+    while (issued < count) {
+        if (issued < taken + slots && (rnd() & 1))
+            m.issue(issued++);
+        else if (taken < issued)
+            m.wait(f8::ring_slot(taken, slots), f8::ring_parity(taken, slots)), ++taken;
+    }
+    for (int i = 0; i < slots; ++i)
+        if (rnd() & 1)
+            m.land(i);
+    f8::ring_drain(issued, slots, [&](int slot, uint32_t parity) { m.wait(slot, parity); });
+    return m.bad + m.left();
+}
+
 int main(int argc, char **argv)
 {
     const long cases = argc > 1 ? atol(argv[1]) : 2000;
@@ -105,6 +127,7 @@ int main(int argc, char **argv)
     for (long i = 0; i < cases; ++i, ++n) {
         const int64_t count = 1 + rnd() % 2000;
         bad += taking(1 + rnd() % 8, count, rnd() % (count + 1)) != 0;
+        bad += apart(1 + rnd() % 8, count) != 0;
     }
     printf("%ld cases, %ld mismatches\n", n, bad);
     return bad != 0;
