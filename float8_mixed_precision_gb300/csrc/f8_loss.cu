@@ -2498,7 +2498,8 @@ f8_status check_out(const void *dlogits, f8_dtype type, int64_t rows, int64_t vo
 {
     if (ldd < vocab || (rows > 0 && dlogits == nullptr))
         return F8_ERR_INVALID;
-    if (dlogits != nullptr && dlogits == logits && ldd != ld)
+    // in place the rows have to lie alike; a single one has no stride
+    if (dlogits != nullptr && dlogits == logits && ldd != ld && rows > 1)
         return F8_ERR_INVALID;
     if (amax_out != nullptr && type != F8_BF16)
         return F8_ERR_INVALID;

@@ -682,7 +682,8 @@ f8_status f8_token_logprobs(const void *logits, f8_dtype type, int64_t rows, int
  *   entropy: needed with dentropy only.
  *   dlogits: device [rows, ldd] of type `type`, row r at dlogits + r * ldd;
  *           columns vocab .. ldd are set to zero (the padding of a head whose
- *           width is rounded up).  May be the logits buffer itself if ldd = ld.
+ *           width is rounded up).  May be the logits buffer itself if ldd = ld or
+ *           there is one row.
  *   amax_out: device fp32 receiving max |dlogits| as stored, ready for
  *           f8_cast_transpose, or NULL; needs type F8_BF16.
  * Ignored rows (negative token), rows whose upstream gradients are both 0, and
