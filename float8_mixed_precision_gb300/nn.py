@@ -385,6 +385,13 @@ def to_float8_linears(module: torch.nn.Module,
     return module
 
 
+def _dense(t: torch.Tensor) -> torch.Tensor:
+    """`t` as libf8 takes it, contiguous from a 16-byte boundary; a piece of a
+    larger buffer may start elsewhere and is copied."""
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
 class _NormFn(torch.autograd.Function):
     """f8_norm_fwd over the last dimension; backward from its input and fp32
     statistics (f8_norm_bwd)."""
@@ -392,9 +399,9 @@ class _NormFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x: torch.Tensor, w: torch.Tensor, b: torch.Tensor | None, kind: int,
                 eps: float) -> torch.Tensor:
-        x2 = x.reshape(-1, x.shape[-1]).contiguous()
-        w = w.contiguous()
-        y, mean, rstd = ops.f8_norm_fwd(x2, w, b if b is None else b.contiguous(), kind=kind, eps=eps)
+        x2 = _dense(x.reshape(-1, x.shape[-1]))
+        w = _dense(w)
+        y, mean, rstd = ops.f8_norm_fwd(x2, w, b if b is None else _dense(b), kind=kind, eps=eps)
         ctx.save_for_backward(x2, w, mean, rstd)
         ctx.kind = kind
         ctx.x_shape = x.shape
@@ -405,7 +412,7 @@ class _NormFn(torch.autograd.Function):
     def backward(ctx, dy: torch.Tensor):
         x2, w, mean, rstd = ctx.saved_tensors
         want_dx, want_dw, want_db = ctx.needs_input_grad[:3]
-        dx, dw, db = ops.f8_norm_bwd(dy.reshape(x2.shape).contiguous(), x2, w, mean, rstd,
+        dx, dw, db = ops.f8_norm_bwd(_dense(dy.reshape(x2.shape)), x2, w, mean, rstd,
                                      kind=ctx.kind, want_dx=want_dx, want_dw=want_dw,
                                      want_db=want_db)
         return dx.reshape(ctx.x_shape) if want_dx else None, dw, db, None, None
@@ -484,7 +491,7 @@ def _logit_rows(logits: torch.Tensor, vocab: int | None):
     vocab = width if vocab is None else vocab
     if not 1 <= vocab <= width:
         raise ValueError("vocab must be between 1 and the logits' last dimension")
-    rows = logits.reshape(-1, width).contiguous()
+    rows = _dense(logits.reshape(-1, width))
     return rows, rows[:, :vocab]
 
 
