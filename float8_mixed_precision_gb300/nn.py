@@ -568,10 +568,13 @@ def distill_loss(logits: torch.Tensor, ids: torch.Tensor, values: torch.Tensor,
     """The distillation loss [...] (fp32) of logits [..., width] over the first
     `vocab` columns, against the teacher's top alternatives: ids int32 and log
     probabilities values fp32, both [..., k], an id below zero for an empty
-    slot.  `tail` counts the rest of the vocabulary as one more class.  A step
+    slot.  `tail` counts the rest of the vocabulary as one more class.  The loss
+    has a gradient to the logits only, so values may not require one.  A step
     that knows each row's weight beforehand calls f8_distill_fwd_bwd instead:
     loss and gradient in one pass over the logits."""
     lead = tuple(logits.shape[:-1])
     if ids.dim() < 1 or tuple(ids.shape[:-1]) != lead or ids.shape != values.shape:
         raise ValueError("ids and values must be [..., k] with the logits' leading shape")
+    if values.requires_grad and torch.is_grad_enabled():
+        raise ValueError("distill_loss forms no gradient of values: pass values.detach()")
     return _DistillFn.apply(logits, ids, values, float(temperature), bool(tail), vocab)
