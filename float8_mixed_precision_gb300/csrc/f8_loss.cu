@@ -2475,13 +2475,20 @@ cudaError_t distill_fused(DistillArgs a, const DeviceInfo &dev, cudaStream_t st)
     return launch_pdl_cluster(distill_fused_kernel<T, TAIL, 8>, grid, dim3(kThreads), 0, st, c, a);
 }
 
+// log2(e) / T.
+float exponent_scale(float temperature)
+{
+    return static_cast<float>(kLog2e / static_cast<double>(temperature));
+}
+
 // What every call of this file asks of its logits.
 f8_status check_logits(const void *logits, f8_dtype type, int64_t rows, int64_t vocab, int64_t ld,
                        float temperature)
 {
     if ((type != F8_BF16 && type != F8_F32) || rows < 0 || vocab < 0 || ld < vocab)
         return F8_ERR_INVALID;
-    if (!(temperature > 0.0f) || !std::isfinite(temperature) || !std::isfinite(1.0f / temperature))
+    // the kernels work with log2(e) / T, which leaves fp32's range before 1 / T does
+    if (!(temperature > 0.0f) || !std::isfinite(temperature) || !std::isfinite(exponent_scale(temperature)))
         return F8_ERR_INVALID;
     if (rows > 0 && (vocab == 0 || logits == nullptr))
         return F8_ERR_INVALID;
@@ -2535,7 +2542,7 @@ DistillArgs distill_args(const void *logits, int64_t rows, int64_t vocab, int64_
     a.ids = ids;
     a.values = values;
     a.inv_t = 1.0f / temperature;
-    a.c = static_cast<float>(kLog2e / static_cast<double>(temperature));
+    a.c = exponent_scale(temperature);
     a.loss = loss;
     a.lse = lse;
     a.rest = rest;
@@ -2583,7 +2590,7 @@ f8_status f8_token_logprobs(const void *logits, f8_dtype type, int64_t rows, int
     a.top_k = top_k;
     a.tokens = tokens;
     a.inv_t = 1.0f / temperature;
-    a.c = static_cast<float>(kLog2e / static_cast<double>(temperature));
+    a.c = exponent_scale(temperature);
     a.inv_c = static_cast<float>(static_cast<double>(temperature) / kLog2e);
     a.logp = logp;
     a.entropy = entropy;

@@ -667,7 +667,8 @@ f8_status f8_quantize_norm(const void *x, const void *w, const void *b, f8_dtype
  * logp and top_logp -inf and entropy 0.  A NaN or +inf logit makes its row's
  * results NaN (top_ids then are distinct ids, not otherwise specified) and
  * sets F8_ERR_NONFINITE.
- * temperature > 0; 0 <= top_k <= min(vocab, F8_MAX_TOP); vocab <= F8_MAX_VOCAB.
+ * temperature > 0, with log2(e) / temperature in fp32's range (from 4.3e-39);
+ * 0 <= top_k <= min(vocab, F8_MAX_TOP); vocab <= F8_MAX_VOCAB.
  */
 f8_status f8_token_logprobs(const void *logits, f8_dtype type, int64_t rows, int64_t vocab,
                             int64_t ld, const int64_t *tokens, float temperature, int top_k,
@@ -732,7 +733,7 @@ f8_status f8_token_logprobs_bwd(const void *logits, f8_dtype type, int64_t rows,
  * sets F8_ERR_NONFINITE.
  * f8_distill_fwd_bwd is both passes for callers that know dloss beforehand
  * (e.g. 1 / tokens): the logits are read once.
- * 1 <= k <= F8_MAX_TOP; temperature > 0; vocab <= F8_MAX_VOCAB.
+ * 1 <= k <= F8_MAX_TOP; temperature and vocab as for f8_token_logprobs.
  */
 f8_status f8_distill_fwd(const void *logits, f8_dtype type, int64_t rows, int64_t vocab, int64_t ld,
                          const int32_t *ids, const float *values, int k, float temperature,
