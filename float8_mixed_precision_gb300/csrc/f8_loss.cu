@@ -1383,7 +1383,7 @@ struct alignas(16) Slots {
     int skip;       // (backward) no gradient, whatever the logits
     float dloss;
     float lse, rest;  // (backward)
-    float total;    // sum q (1 without the tail class)
+    float total;    // sum q (1 without the tail class); NaN if a value is NaN or +inf
     float qall;     // sum q as it came out
     float left;     // q_r
     float plogp;    // sum q log q
@@ -1493,6 +1493,8 @@ __device__ __forceinline__ void warp_slots(const DistillArgs &a, int64_t row, co
             sum += q[i];
         }
         sum = warp_sum(sum);
+        if (!(fabsf(sum) < F8_POS_INF))  // a NaN or +inf among the values
+            sum = F8_NAN;
         float qall = sum;
         if (!TAIL) {
             const float ls = logf(sum), inv = 1.0f / sum;
@@ -1596,7 +1598,7 @@ __device__ __forceinline__ void warp_slots(const DistillArgs &a, int64_t row, co
             }
         }
         if (lane == 0) {
-            s.total = TAIL ? sum : 1.0f;
+            s.total = TAIL || sum != sum ? sum : 1.0f;
             s.qall = qall;
             s.left = TAIL ? fmaxf(1.0f - sum, 0.0f) : 0.0f;
         }
@@ -1784,7 +1786,7 @@ __device__ __forceinline__ RowLoss row_loss(const DistillArgs &a, const Slots &s
                                         s.qall * fmaf(m - s.zref, a.inv_t, ls);
     if (TAIL && o.rest != 0.0f && s.left > 0.0f)
         o.loss += s.left * (logf(s.left) - (o.rest > 0.0f ? logf(o.rest) : o.rest));
-    if (bad || s.plogp != s.plogp || s.zmean != s.zmean)
+    if (bad || s.total != s.total || s.zmean != s.zmean)
         o.loss = F8_NAN;
     return o;
 }
