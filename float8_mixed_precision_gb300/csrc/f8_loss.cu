@@ -2428,7 +2428,8 @@ cudaError_t distill_fwd(DistillArgs a, const DeviceInfo &dev, cudaStream_t st)
 // 131072 17 against 25; but 32 x 131072 17 against 14, and 4096 x 8000 83 against
 // 52.  The backward pass alone is near even: with the tail class 777 x 50003 31
 // against 35 and 2048 x 65536 90 against 95, without it 300 x 131072 28 against
-// 29, 1024 x 131072 88 against 84.
+// 29, but 1024 x 131072 88 against 84 and 4096 x 131072 338 against 327: there the
+// ring costs 3 to 5 %, and one rule for the calls is kept.
 constexpr int kShortChunks = 4 * kThreads;
 
 template <typename T>

@@ -29,8 +29,13 @@
 // Rows wider than the 16384 columns that registers hold take kernels that walk
 // the row once per reduction, with the column sums in a kernel of their own.
 //
-// Measured, bf16, layer norm: forward 8192 x 4096 25.0 us, 5.4 TB/s; backward
-// with both parameters' gradients 39.8 us, 5.1 TB/s; a plain copy runs at 6.8.
+// Measured, bf16, layer norm: forward 8192 x 4096 25.1 us, 5.3 TB/s; backward
+// with both parameters' gradients 39.9 us, 5.1 TB/s; a plain copy runs at 6.8.
+// RMS norm 21.1 and 39.8: its backward does layer norm's work, sums that only the
+// bias needs included.  Farther from the copy rate: widths between the groups'
+// (8192 x 2560 24.0 and 36.5 us, of 12.4 and 18.6 for the bytes), odd ones
+// (1999 x 5003 26 and 31, of 5.9 and 8.9), narrow ones (65536 x 128 21 and 37, of
+// 4.9 and 7.4) and the backward above 8192 columns (4096 x 16384 115 of 59).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -1201,7 +1206,10 @@ struct BwdArgs {
     float *parts;
 };
 
-// Resident blocks: 2048 threads an SM by the register use of these kernels.
+// At most `per_sm` blocks an SM.  The kernels without a ring ask for more than
+// their registers let run at once (forward 58 to 64, 108 for fp32 rows of up to 1024
+// columns: four or two blocks of 256 threads, of eight asked for; backward 80 to
+// 128: three or two, of four), so their blocks run in two waves or more.
 int64_t grid_for(int64_t rows, int tpr, const DeviceInfo &dev, int per_sm)
 {
     const int groups = block_threads(tpr) / tpr;

@@ -605,8 +605,10 @@ typedef enum { F8_LAYER_NORM = 0, F8_RMS_NORM = 1 } f8_norm;
  *           it first.  A non-finite y then sets F8_ERR_NONFINITE.
  * rows, cols >= 0 (nothing is done for 0; amax_out is then 0); eps >= 0.
  * x, y, w, b 16-byte aligned, mean, rstd, amax_out 4-byte aligned.  Any cols is
- * taken; rows of whole 16-byte vectors (cols a multiple of 8 for bf16, of 4
- * for fp32) and cols <= 16384 take the fastest path.
+ * taken up to 2^30 - 1, and rows * cols < 2^60.  Rows of whole 16-byte vectors
+ * (cols a multiple of 8 for bf16, of 4 for fp32) move in vectors, others element
+ * by element, as do all rows past 16384 columns.  Of the whole ones the powers of
+ * two from 2048 are the fastest; the backward pass is slower above 8192 columns.
  */
 f8_status f8_norm_fwd(const void *x, f8_dtype x_type, const void *w, const void *b,
                       f8_dtype w_type, f8_norm kind, int64_t rows, int64_t cols, float eps,
@@ -655,8 +657,8 @@ f8_status f8_quantize_norm(const void *x, const void *w, const void *b, f8_dtype
  * and the top_k largest logits in descending order (equal ones by ascending
  * id) with their log probabilities.
  *   logits: device [rows, vocab] of type `type`, row r at logits + r * ld
- *           elements (ld >= vocab; columns vocab .. ld are not read), 16-byte
- *           aligned.  Rows that start off a 16-byte boundary are taken.
+ *           elements (ld >= vocab; columns vocab .. ld are not read).  The first
+ *           row starts on a 16-byte boundary; others may start off one.
  *   tokens: device int64 [rows] or NULL (then logp must be NULL).  A negative
  *           token marks a row that is ignored: its logits are not read, logp,
  *           entropy and lse are 0, top_ids -1 and top_logp -inf.  A token >=
@@ -668,7 +670,8 @@ f8_status f8_quantize_norm(const void *x, const void *w, const void *b, f8_dtype
  * results NaN (top_ids then are distinct ids, not otherwise specified) and
  * sets F8_ERR_NONFINITE.
  * temperature > 0, with log2(e) / temperature in fp32's range (from 4.3e-39);
- * 0 <= top_k <= min(vocab, F8_MAX_TOP); vocab <= F8_MAX_VOCAB.
+ * 0 <= top_k <= min(vocab, F8_MAX_TOP); vocab <= F8_MAX_VOCAB; rows < 2^21;
+ * ld < 2^31 (and ldd in the calls below): F8_ERR_SHAPE past these.
  */
 f8_status f8_token_logprobs(const void *logits, f8_dtype type, int64_t rows, int64_t vocab,
                             int64_t ld, const int64_t *tokens, float temperature, int top_k,
@@ -690,7 +693,8 @@ f8_status f8_token_logprobs(const void *logits, f8_dtype type, int64_t rows, int
  * Ignored rows (negative token), rows whose upstream gradients are both 0, and
  * rows of |lse| >= 2^24 (every token masked by -inf or by the type's lowest
  * value: an fp32 lse no longer holds the row's sum) are not read and get zeros.
- * Without tokens (NULL) only the entropy has a gradient.
+ * Without tokens (NULL) only the entropy has a gradient.  p = exp(z - lse) has the
+ * relative error of lse's rounding, up to 2^-24 |lse|.
  */
 f8_status f8_token_logprobs_bwd(const void *logits, f8_dtype type, int64_t rows, int64_t vocab,
                                 int64_t ld, const int64_t *tokens, const float *lse,
