@@ -43,7 +43,9 @@ EXPORTS = ("f8_amax", "f8_cast_transpose", "f8_gemm", "f8_linear_workspace_bytes
            "f8_transpose_u8", "f8_linear_fwd_qw", "f8_linear_fwd_qw_workspace_bytes",
            "f8_norm_fwd", "f8_norm_bwd", "f8_norm_bwd_workspace_bytes", "f8_quantize_norm",
            "f8_token_logprobs", "f8_token_logprobs_bwd", "f8_distill_fwd", "f8_distill_bwd",
-           "f8_distill_fwd_bwd")
+           "f8_distill_fwd_bwd", "f8_gemm_act", "f8_act_bwd", "f8_act_bwd_workspace_bytes",
+           "f8_rope", "f8_rope_frequencies", "f8_residual_norm_fwd", "f8_residual_norm_bwd",
+           "f8_residual_norm_bwd_workspace_bytes")
 
 F8_MAX_GROUPED_GEMMS = 8
 F8_MAX_MULTI_TENSORS = 8
@@ -58,6 +60,18 @@ F8_LAYER_NORM = 0
 F8_RMS_NORM = 1
 F8_MAX_TOP = 256
 F8_MAX_VOCAB = 1 << 22
+F8_ACT_NONE = 0
+F8_ACT_RELU = 1
+F8_ACT_RELU2 = 2
+F8_ACT_SILU = 3
+F8_ACT_GELU = 4
+F8_ACT_GELU_TANH = 5
+F8_ROPE_HALF = 0
+F8_ROPE_INTERLEAVED = 1
+F8_ROPE_PLAIN = 0
+F8_ROPE_LINEAR = 1
+F8_ROPE_BASE = 2
+F8_ROPE_BY_PARTS = 3
 
 
 class F8Error(RuntimeError):
@@ -89,6 +103,25 @@ class _GroupLinear(ctypes.Structure):
     _fields_ = [("N", ctypes.c_int64), ("w", ctypes.c_void_p), ("y", ctypes.c_void_p),
                 ("dy", ctypes.c_void_p), ("dx", ctypes.c_void_p), ("dw", ctypes.c_void_p),
                 ("saved", _Saved)]
+
+
+class _RopeTensor(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("out", ctypes.c_void_p), ("heads", ctypes.c_int64),
+                ("x_batch", ctypes.c_int64), ("x_seq", ctypes.c_int64), ("x_head", ctypes.c_int64),
+                ("out_batch", ctypes.c_int64), ("out_seq", ctypes.c_int64), ("out_head", ctypes.c_int64)]
+
+
+class _ResidualNorm(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int), ("x_type", ctypes.c_int), ("r_type", ctypes.c_int),
+                ("w_type", ctypes.c_int), ("gate_type", ctypes.c_int), ("rows", ctypes.c_int64),
+                ("cols", ctypes.c_int64), ("gate_rows", ctypes.c_int64), ("eps", ctypes.c_float),
+                ("scale", ctypes.c_float), ("w_pre", ctypes.c_void_p), ("b_pre", ctypes.c_void_p),
+                ("w_post", ctypes.c_void_p), ("b_post", ctypes.c_void_p), ("gate", ctypes.c_void_p)]
+
+
+class _ResidualNormGrads(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("da", "dr", "dw_pre", "db_pre", "dw_post", "db_post",
+                                               "dgate")]
 
 
 _lock = threading.Lock()
@@ -208,6 +241,25 @@ def lib() -> ctypes.CDLL:
         L.f8_distill_fwd_bwd.argtypes = [vp, ci, i64, i64, i64, vp, vp, ci, f32, ci, vp, vp, vp, i64,
                                          vp, vp]
         L.f8_distill_fwd_bwd.restype = st
+        L.f8_gemm_act.argtypes = [vp, ci, vp, ci, i64, i64, i64, vp, vp, vp, ci, ci, vp, vp, vp, vp, vp]
+        L.f8_gemm_act.restype = st
+        L.f8_act_bwd_workspace_bytes.argtypes = [i64, i64]
+        L.f8_act_bwd_workspace_bytes.restype = sz
+        L.f8_act_bwd.argtypes = [vp, vp, ci, i64, i64, vp, vp, ci, vp, vp, sz, vp]
+        L.f8_act_bwd.restype = st
+        L.f8_rope.argtypes = [ctypes.POINTER(_RopeTensor), ci, ci, i64, i64, i64, i64, ci, vp, i64, i64,
+                              vp, f32, ci, vp]
+        L.f8_rope.restype = st
+        f64 = ctypes.c_double
+        L.f8_rope_frequencies.argtypes = [i64, f64, ci, f64, f64, f64, f64, ctypes.POINTER(f64)]
+        L.f8_rope_frequencies.restype = st
+        L.f8_residual_norm_fwd.argtypes = [ctypes.POINTER(_ResidualNorm), vp, vp, vp, vp, vp, vp, vp]
+        L.f8_residual_norm_fwd.restype = st
+        L.f8_residual_norm_bwd_workspace_bytes.argtypes = [i64, i64]
+        L.f8_residual_norm_bwd_workspace_bytes.restype = sz
+        L.f8_residual_norm_bwd.argtypes = [ctypes.POINTER(_ResidualNorm), vp, vp, vp, vp, vp,
+                                           ctypes.POINTER(_ResidualNormGrads), vp, sz, vp]
+        L.f8_residual_norm_bwd.restype = st
         _lib = L
         return L
 

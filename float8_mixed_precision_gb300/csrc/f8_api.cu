@@ -428,6 +428,33 @@ f8_status f8_gemm_fmt(const uint8_t *a, f8_format fmt_a, const uint8_t *b, f8_fo
     return gemm_impl(a, fmt_a, b, fmt_b, M, N, K, scale_a, scale_b, c, stream);
 }
 
+f8_status f8_gemm_act(const uint8_t *a, f8_format fmt_a, const uint8_t *b, f8_format fmt_b,
+                      int64_t M, int64_t N, int64_t K, const float *scale_a, const float *scale_b,
+                      const void *bias, f8_dtype bias_type, f8_act act, const void *residual,
+                      void *y, void *z, float *amax_out, void *stream)
+{
+    if ((fmt_a != F8_E4M3 && fmt_a != F8_E5M2) || (fmt_b != F8_E4M3 && fmt_b != F8_E5M2) ||
+        (bias_type != F8_BF16 && bias_type != F8_F32) || act < F8_ACT_NONE || act > F8_ACT_GELU_TANH)
+        return F8_ERR_INVALID;
+    F8_TRY(check_gemm_args(a, b, M, N, K, scale_a, scale_b, y));
+    if (z != nullptr && (z == y || z == residual))
+        return F8_ERR_INVALID;
+    if (!aligned(bias, 16) || !aligned(residual, 16) || !aligned(z, 16) || !aligned(amax_out, 4))
+        return F8_ERR_ALIGN;
+    if (M > 0 && N > 0 && K == 0)
+        return F8_ERR_SHAPE;
+    const DeviceInfo *dev;
+    F8_TRY(get_device(&dev));
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (amax_out != nullptr)
+        F8_TRY_CUDA(cudaMemsetAsync(amax_out, 0, sizeof(float), st));
+    if (M == 0 || N == 0)
+        return F8_OK;
+    const GemmDesc g{a, b, M, N, K, scale_a, scale_b, y, fmt_a, fmt_b};
+    const ActEpilogue e{bias, bias_type == F8_F32, act, residual, z, reinterpret_cast<unsigned *>(amax_out)};
+    return from_cuda(launch_gemm_act(g, e, *dev, st));
+}
+
 f8_status f8_gemm_grouped(const f8_gemm_problem *problems, int count, void *stream)
 {
     if (problems == nullptr || count < 1 || count > F8_MAX_GROUPED_GEMMS)

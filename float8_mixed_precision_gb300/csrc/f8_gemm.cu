@@ -15,13 +15,18 @@
 //               memory and write it with one TMA tensor store; the
 //               accumulator is released (tempty[a]) as soon as it has been
 //               read, so the MMAs of tile i+1 overlap the epilogue of tile i.
-// GLU = true is the W13 GEMM of a SwiGLU FFN: B holds W1 and W3 interleaved
+// EPI = kEpiGlu is the W13 GEMM of a SwiGLU FFN: B holds W1 and W3 interleaved
 // by 128 rows, so the 256 columns of a tile are 128 columns of a = X W1^T and
 // the matching 128 of b = X W3^T.  The epilogue stores a and b (bf16) and
 // h = bf16(silu(a) b), formed from those bf16 values, into a second [M, N/2]
 // output, all by TMA stores, and keeps the largest |h|: one partial maximum
 // per CTA is written at the end for the cast of h (or, with hatomic, one
 // atomicMax per CTA into a zeroed fp32 amax).
+// kEpiAct is the linear with its bias, activation and residual: per step of 64
+// columns the epilogue forms z = acc / (sa sb) + bias and y = act(z) + residual in
+// fp32 and writes y, and z where it is kept, each rounded once.  The residual's box
+// comes by TMA into the buffer that y leaves from, one step ahead; the first one of
+// a tile is fetched while the tile's products are still being formed.
 // Two shapes of the same kernel:
 //   PAIR = false  one CTA computes a 128 x BN tile (tcgen05 cta_group::1);
 //   PAIR = true   a cluster of two CTAs on neighbouring SMs computes a
@@ -54,6 +59,7 @@
 #include <mutex>
 #include <vector>
 
+#include "f8_act.cuh"
 #include "f8_internal.h"
 #include "f8_ptx.cuh"
 #include "f8_sched.h"
@@ -71,8 +77,14 @@ constexpr int kEpiCols = 64;                       // columns per epilogue step
 constexpr int kEpiBufBytes = 32 * kEpiCols * 2;    // 32 rows x 128 bytes
 constexpr uint64_t kDrainLimitNs = 1000000000ull;
 
-template <int BN, int STAGES, bool PAIR, bool GLU = false>
+// What the epilogue does with an accumulator.
+constexpr int kEpiPlain = 0;
+constexpr int kEpiGlu = 1;
+constexpr int kEpiAct = 2;
+
+template <int BN, int STAGES, bool PAIR, int EPI = kEpiPlain>
 struct Cfg {
+    static constexpr bool GLU = EPI == kEpiGlu;
     static constexpr int kTileM = PAIR ? 2 * kBM : kBM;
     static constexpr int kBRows = PAIR ? BN / 2 : BN;  // rows of B each CTA loads
     static constexpr int kABytes = kBM * kBK;
@@ -81,10 +93,13 @@ struct Cfg {
     static constexpr int kTmemCols = (2 * BN <= 256) ? 256 : 512;
     static constexpr int kThreads = 64 + 32 * kEpiWarps;  // producer, MMA, epilogue
     // per epilogue warp: plain, two 32 x 128-byte swizzled store buffers;
-    // GLU, one set of three 32 x 64-byte boxes (a, b, h)
-    static constexpr int kWarpStaging = GLU ? 3 * kGluBoxBytes : 2 * kEpiBufBytes;
+    // GLU, one set of three 32 x 64-byte boxes (a, b, h); Act, two buffers of y and
+    // one of z
+    static constexpr int kWarpStaging = GLU ? 3 * kGluBoxBytes
+                                            : (EPI == kEpiAct ? 3 : 2) * kEpiBufBytes;
     static constexpr int kStagingBytes = kEpiWarps * kWarpStaging;
-    static constexpr int kBarBytes = 8 * (2 * STAGES + 5) + 16;
+    static constexpr int kResBars = EPI == kEpiAct ? 2 * kEpiWarps : 0;  // residual boxes
+    static constexpr int kBarBytes = 8 * (2 * STAGES + 5 + kResBars) + 16;
     static constexpr int kSmemBytes = STAGES * kStageBytes + kStagingBytes + kBarBytes + 1024;
     static_assert(kSmemBytes <= 232448, "shared memory budget");
     static_assert(BN % kEpiCols == 0, "epilogue steps");
@@ -261,6 +276,225 @@ __device__ __forceinline__ void epilogue_rows_glu(uint32_t taddr, int row0, int 
     }
 }
 
+// What an epilogue takes besides the accumulator.
+template <int EPI>
+struct EpiParams {};
+template <>
+struct EpiParams<kEpiGlu> {
+    CUtensorMap h;
+    unsigned *hparts;
+    int hatomic;
+};
+template <>
+struct EpiParams<kEpiAct> {
+    CUtensorMap res, z;  // with TMA stores only
+    const void *bias;
+    const __nv_bfloat16 *residual;
+    __nv_bfloat16 *zout;
+    unsigned *amax;
+    int bias_f32, act;
+};
+
+// Eight biases from column `col`; 0 past the last one.
+__device__ __forceinline__ void load_bias8(const void *bias, int f32, int col, int N, float (&f)[8],
+                                           unsigned *status)
+{
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        f[e] = 0.0f;
+    if (bias == nullptr || col >= N || !in_range(col, min(8, N - col), N, status))
+        return;
+    if (col + 8 <= N) {  // col is a multiple of 8
+        if (f32) {
+            const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(bias) + col);
+            const float4 u = __ldg(p), v = __ldg(p + 1);
+            f[0] = u.x, f[1] = u.y, f[2] = u.z, f[3] = u.w;
+            f[4] = v.x, f[5] = v.y, f[6] = v.z, f[7] = v.w;
+        } else {
+            const uint4 u =
+                __ldg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(bias) + col));
+            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                f[e] = __uint_as_float((e & 1) ? w[e / 2] & 0xFFFF0000u : w[e / 2] << 16);
+        }
+        return;
+    }
+    for (int e = 0; e < 8; ++e)
+        if (col + e < N)
+            f[e] = f32 ? static_cast<const float *>(bias)[col + e]
+                       : __bfloat162float(static_cast<const __nv_bfloat16 *>(bias)[col + e]);
+}
+
+// z and y of one row's 64 columns: z = r inv + bias to `zb` (if not NULL), y =
+// act(z) + what `b` holds (with `res`) to `b`; both rows of the 128-byte swizzle.
+template <int ACT>
+__device__ __forceinline__ void act_row(const uint32_t (&r)[kEpiCols], float inv,
+                                        const EpiParams<kEpiAct> &ep, int col0, int N, uint8_t *b,
+                                        uint8_t *zb, bool res, bool live, int lane, uint32_t &max2,
+                                        unsigned *status)
+{
+    const float2 inv2 = make_float2(inv, inv);
+#pragma unroll
+    for (int q = 0; q < kEpiCols / 8; ++q) {
+        float bias[8];
+        load_bias8(ep.bias, ep.bias_f32, col0 + 8 * q, N, bias, status);
+        const int off = lane * 128 + ((q ^ (lane & 7)) << 4);
+        uint32_t old[4] = {0u, 0u, 0u, 0u};
+        if (res) {
+            const uint4 v = *reinterpret_cast<const uint4 *>(b + off);
+            old[0] = v.x, old[1] = v.y, old[2] = v.z, old[3] = v.w;
+        }
+        uint32_t z2[4], y2[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int e = 8 * q + 2 * i;
+            const float2 z = __ffma2_rn(make_float2(__uint_as_float(r[e]), __uint_as_float(r[e + 1])),
+                                        inv2, make_float2(bias[2 * i], bias[2 * i + 1]));
+            float2 y = act::value<ACT>(z);
+            if (res)
+                y = __fadd2_rn(y, make_float2(__uint_as_float(old[i] << 16),
+                                              __uint_as_float(old[i] & 0xFFFF0000u)));
+            z2[i] = pack_bf16x2(z.x, z.y);
+            y2[i] = pack_bf16x2(y.x, y.y);
+            if (live)
+                max2 = swiglu::max_abs2(max2, y2[i]);
+        }
+        *reinterpret_cast<uint4 *>(b + off) = make_uint4(y2[0], y2[1], y2[2], y2[3]);
+        if (zb != nullptr)
+            *reinterpret_cast<uint4 *>(zb + off) = make_uint4(z2[0], z2[1], z2[2], z2[3]);
+    }
+}
+
+// A box of 32 rows x 64 columns between a staging buffer and a row-major tensor
+// whose rows no TMA store takes: a row at a time, two columns a lane.
+template <bool STORE>
+__device__ __forceinline__ void box_rows(uint8_t *b, __nv_bfloat16 *t, int row0, int col0, int M, int N,
+                                         int lane, unsigned *status)
+{
+    const int64_t mn = static_cast<int64_t>(M) * N;
+    const int c = col0 + 2 * lane;
+    for (int i = 0; i < 32 && row0 + i < M; ++i) {
+        uint32_t *w = reinterpret_cast<uint32_t *>(b + i * 128 + (((lane >> 2) ^ (i & 7)) << 4) +
+                                                   ((lane & 3) << 2));
+        uint16_t *p = reinterpret_cast<uint16_t *>(t);
+        const int64_t o = static_cast<int64_t>(row0 + i) * N + c;
+        if (STORE) {
+            if (c < N && in_range(o, 1, mn, status))
+                p[o] = static_cast<uint16_t>(*w);
+            if (c + 1 < N && in_range(o + 1, 1, mn, status))
+                p[o + 1] = static_cast<uint16_t>(*w >> 16);
+        } else {
+            uint32_t v = 0u;
+            if (c < N && in_range(o, 1, mn, status))
+                v = p[o];
+            if (c + 1 < N && in_range(o + 1, 1, mn, status))
+                v |= static_cast<uint32_t>(p[o + 1]) << 16;
+            *w = v;
+        }
+    }
+}
+
+// The residual's box of step `col0` into buffer `buf`, by one lane.
+__device__ __forceinline__ void fetch_residual(const EpiParams<kEpiAct> &ep, uint8_t *stage,
+                                               uint64_t *bars, uint32_t buf, int col0, int row0)
+{
+    mbar_arrive_expect_tx(&bars[buf], kEpiBufBytes);
+    tma_load_2d(stage + buf * kEpiBufBytes, &ep.res, &bars[buf], col0, row0);
+}
+
+// The Act epilogue of one warp over the columns of a tile.  With a residual by TMA
+// the caller has fetched the first step's box into buffer `buf`; phases holds the
+// parity of each buffer's next box.  False if a wait gave up.
+template <int BN>
+__device__ __forceinline__ bool epilogue_rows_act(uint32_t taddr, int row0, int col_base, int M, int N,
+                                                  float inv, const EpiParams<kEpiAct> &ep,
+                                                  __nv_bfloat16 *c,
+                                                  const CUtensorMap *tma_c, bool tma, uint8_t *stage,
+                                                  uint64_t *bars, uint32_t &buf, uint32_t &phases,
+                                                  uint32_t &max2, int lane, unsigned *status,
+                                                  volatile int *abort_flag, uint64_t limit_ns)
+{
+    uint8_t *zb = ep.zout != nullptr ? stage + 2 * kEpiBufBytes : nullptr;
+    const bool res = ep.residual != nullptr;
+#pragma unroll 1
+    for (int j = 0; j < BN / kEpiCols; ++j) {
+        const int col0 = col_base + j * kEpiCols;
+        if (row0 >= M || col0 >= N)  // nothing of this box lies in C (warp-uniform)
+            break;
+        uint32_t r[kEpiCols];
+        tc_ld_32x32b_x32(taddr + j * kEpiCols, *reinterpret_cast<uint32_t(*)[32]>(&r[0]));
+        tc_ld_32x32b_x32(taddr + j * kEpiCols + 32, *reinterpret_cast<uint32_t(*)[32]>(&r[32]));
+        uint8_t *b = stage + buf * kEpiBufBytes;
+        if (tma) {
+            if (lane == 0) {
+                bulk_wait_group_read<0>();  // the stores so far have read their buffers
+                if (res && j + 1 < BN / kEpiCols && col0 + kEpiCols < N)
+                    fetch_residual(ep, stage, bars, buf ^ 1u, col0 + kEpiCols, row0);
+            }
+            if (res) {
+                const bool ok = mbar_wait(&bars[buf], (phases >> buf) & 1u, abort_flag, limit_ns);
+                phases ^= 1u << buf;
+                if (!__all_sync(0xFFFFFFFFu, ok)) {
+                    tc_wait_ld();
+                    if (lane == 0) {
+                        note_timeout(abort_flag, status);
+                        // the boxes under way land before the buffers are given up
+                        mbar_wait(&bars[buf], ((phases >> buf) & 1u) ^ 1u, nullptr, kDrainLimitNs);
+                        if (j + 1 < BN / kEpiCols && col0 + kEpiCols < N)
+                            mbar_wait(&bars[buf ^ 1u], (phases >> (buf ^ 1u)) & 1u, nullptr, kDrainLimitNs);
+                    }
+                    __syncwarp();
+                    return false;
+                }
+            }
+        } else if (res) {
+            box_rows<false>(b, const_cast<__nv_bfloat16 *>(ep.residual), row0, col0, M, N, lane, status);
+        }
+        __syncwarp();
+        tc_wait_ld();
+        const bool live = row0 + lane < M;
+        switch (ep.act) {
+        case F8_ACT_RELU:
+            act_row<F8_ACT_RELU>(r, inv, ep, col0, N, b, zb, res, live, lane, max2, status);
+            break;
+        case F8_ACT_RELU2:
+            act_row<F8_ACT_RELU2>(r, inv, ep, col0, N, b, zb, res, live, lane, max2, status);
+            break;
+        case F8_ACT_SILU:
+            act_row<F8_ACT_SILU>(r, inv, ep, col0, N, b, zb, res, live, lane, max2, status);
+            break;
+        case F8_ACT_GELU:
+            act_row<F8_ACT_GELU>(r, inv, ep, col0, N, b, zb, res, live, lane, max2, status);
+            break;
+        case F8_ACT_GELU_TANH:
+            act_row<F8_ACT_GELU_TANH>(r, inv, ep, col0, N, b, zb, res, live, lane, max2, status);
+            break;
+        default:
+            act_row<F8_ACT_NONE>(r, inv, ep, col0, N, b, zb, res, live, lane, max2, status);
+            break;
+        }
+        if (tma) {
+            fence_proxy_async_shared();
+            __syncwarp();
+            if (lane == 0) {
+                tma_store_2d(tma_c, b, col0, row0);
+                if (zb != nullptr)
+                    tma_store_2d(&ep.z, zb, col0, row0);
+                bulk_commit_group();
+            }
+            buf ^= 1u;
+        } else {
+            __syncwarp();
+            box_rows<true>(b, c, row0, col0, M, N, lane, status);
+            if (zb != nullptr)
+                box_rows<true>(zb, ep.zout, row0, col0, M, N, lane, status);
+            __syncwarp();
+        }
+    }
+    return true;
+}
+
 // One GEMM problem of a launch.
 struct GemmProb {
     __nv_bfloat16 *c;
@@ -319,14 +553,13 @@ __device__ __forceinline__ float pick(const float (&v)[NP], int slot)
     return r;
 }
 
-template <int BN, int STAGES, bool PAIR, bool GLU, int NP>
-__global__ void __launch_bounds__(Cfg<BN, STAGES, PAIR, GLU>::kThreads, 1)
-gemm_kernel(const __grid_constant__ GemmSet<NP> set, const __grid_constant__ CUtensorMap tma_h,
-            unsigned *__restrict__ status, uint64_t limit_ns, int group_m,
-            unsigned *__restrict__ hparts, int hatomic)
+template <int BN, int STAGES, bool PAIR, int EPI, int NP>
+__global__ void __launch_bounds__(Cfg<BN, STAGES, PAIR, EPI>::kThreads, 1)
+gemm_kernel(const __grid_constant__ GemmSet<NP> set, const __grid_constant__ EpiParams<EPI> ep,
+            unsigned *__restrict__ status, uint64_t limit_ns, int group_m)
 {
-    using C = Cfg<BN, STAGES, PAIR, GLU>;
-    static_assert(!GLU || NP == 1, "the SwiGLU epilogue runs single-problem launches");
+    using C = Cfg<BN, STAGES, PAIR, EPI>;
+    static_assert(EPI == kEpiPlain || NP == 1, "the fused epilogues run single-problem launches");
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                 ~static_cast<uintptr_t>(1023));
@@ -340,7 +573,8 @@ gemm_kernel(const __grid_constant__ GemmSet<NP> set, const __grid_constant__ CUt
     uint64_t *drain = tempty + 2;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-    unsigned *hmax_cta = reinterpret_cast<unsigned *>(tmem_slot + 2);  // GLU: largest |h| bits
+    unsigned *hmax_cta = reinterpret_cast<unsigned *>(tmem_slot + 2);  // largest |h| or |y| bits
+    uint64_t *res_bars = reinterpret_cast<uint64_t *>(tmem_slot + 4);  // Act: two a warp
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
@@ -358,6 +592,8 @@ gemm_kernel(const __grid_constant__ GemmSet<NP> set, const __grid_constant__ CUt
             mbar_init(&tempty[a], PAIR ? 2 * kEpiWarps : kEpiWarps);
         }
         mbar_init(drain, 1);
+        for (int i = 0; i < C::kResBars; ++i)
+            mbar_init(&res_bars[i], 1);
         *abort_flag = 0;
         *hmax_cta = 0u;
         fence_mbar_init();
@@ -372,8 +608,16 @@ gemm_kernel(const __grid_constant__ GemmSet<NP> set, const __grid_constant__ CUt
                     tma_prefetch_desc(&set.c[j]);
             }
         }
-        if (GLU)
-            tma_prefetch_desc(&tma_h);
+        if constexpr (EPI == kEpiGlu)
+            tma_prefetch_desc(&ep.h);
+        if constexpr (EPI == kEpiAct) {
+            if (set.p[0].tma_store) {
+                if (ep.residual != nullptr)
+                    tma_prefetch_desc(&ep.res);
+                if (ep.zout != nullptr)
+                    tma_prefetch_desc(&ep.z);
+            }
+        }
     }
     if (warp == 1) {
         if (PAIR) {
@@ -548,6 +792,7 @@ gemm_kernel(const __grid_constant__ GemmSet<NP> set, const __grid_constant__ CUt
         uint32_t hmax2 = 0;
         const uint32_t tempty_leader = PAIR ? cluster_map(smem_addr(&tempty[0]), 0) : 0u;
         uint32_t buf = 0;
+        [[maybe_unused]] uint32_t phases = 0;
         for (int local = 0;; ++local) {
             const int g = unit_tile<NP>(set, unit, local);
             if (g < 0)
@@ -557,26 +802,44 @@ gemm_kernel(const __grid_constant__ GemmSet<NP> set, const __grid_constant__ CUt
             const GemmProb &pr = set.p[slot];
             const uint32_t acc = local & 1;
             const uint32_t aph = (local >> 1) & 1;
-            bool ok = mbar_wait(&tfull[acc], aph, abort_flag, limit_ns);
-            ok = __all_sync(0xFFFFFFFFu, ok);
-            if (!ok) {
-                if (lane == 0)
-                    note_timeout(abort_flag, status);
-                break;
-            }
-            tc_fence_after_sync();
             int mb, nb;
             tile_coords(tile, pr.num_m, pr.num_n, group_m, mb, nb);
             const int row0 = mb * C::kTileM + static_cast<int>(rank) * kBM + quad * 32;
+            [[maybe_unused]] uint64_t *my_bars = res_bars + 2 * (warp - 2);
+            [[maybe_unused]] bool fetched = false;
+            if constexpr (EPI == kEpiAct) {
+                fetched = ep.residual != nullptr && pr.tma_store != 0 && row0 < pr.M;
+                if (fetched && lane == 0) {
+                    bulk_wait_group_read<0>();
+                    fetch_residual(ep, my_stage, my_bars, buf, nb * BN, row0);
+                }
+            }
+            bool ok = mbar_wait(&tfull[acc], aph, abort_flag, limit_ns);
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            if (!ok) {
+                if (lane == 0) {
+                    note_timeout(abort_flag, status);
+                    if (fetched)
+                        mbar_wait(&my_bars[buf], (phases >> buf) & 1u, nullptr, kDrainLimitNs);
+                }
+                break;
+            }
+            tc_fence_after_sync();
             const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + acc * BN;
-            if (GLU)
-                epilogue_rows_glu(taddr, row0, nb * BN, pr.M, inv[0], &set.c[0], &tma_h, my_stage,
+            if constexpr (EPI == kEpiGlu)
+                epilogue_rows_glu(taddr, row0, nb * BN, pr.M, inv[0], &set.c[0], &ep.h, my_stage,
                                   hmax2, lane);
+            else if constexpr (EPI == kEpiAct)
+                ok = epilogue_rows_act<BN>(taddr, row0, nb * BN, pr.M, pr.N, inv[0], ep, pr.c,
+                                           &set.c[0], pr.tma_store != 0, my_stage, my_bars, buf,
+                                           phases, hmax2, lane, status, abort_flag, limit_ns);
             else
                 epilogue_rows<BN>(taddr, row0, nb * BN, pr.M, pr.N, pick<NP>(inv, slot), pr.c,
                                   &set.c[slot], pr.tma_store != 0, my_stage, buf, lane, status);
             tc_fence_before_sync();
             __syncwarp();
+            if (EPI == kEpiAct && !ok)
+                break;
             if (lane == 0) {
                 if (!PAIR || leader)
                     mbar_arrive(&tempty[acc]);
@@ -587,7 +850,7 @@ gemm_kernel(const __grid_constant__ GemmSet<NP> set, const __grid_constant__ CUt
         if (lane == 0)
             bulk_wait_group_all();
         __syncwarp();
-        if (GLU) {
+        if (EPI != kEpiPlain) {
             const unsigned m = __reduce_max_sync(0xFFFFFFFFu, max(hmax2 & 0xFFFFu, hmax2 >> 16));
             if (lane == 0)
                 atomicMax(hmax_cta, m);
@@ -599,14 +862,24 @@ gemm_kernel(const __grid_constant__ GemmSet<NP> set, const __grid_constant__ CUt
         cluster_sync();
     else
         __syncthreads();
-    if (GLU && threadIdx.x == 0) {
-        const unsigned m = *hmax_cta;
-        if (m >= 0x7F80u)
-            atomicOr(status, kStatusNonfinite);
-        if (hatomic)
-            atomicMax(hparts, m << 16);  // fp32 bits of the bf16 |h|: integer order = numeric
-        else
-            hparts[blockIdx.x] = m << 16;
+    if constexpr (EPI == kEpiGlu) {
+        if (threadIdx.x == 0) {
+            const unsigned m = *hmax_cta;
+            if (m >= 0x7F80u)
+                atomicOr(status, kStatusNonfinite);
+            if (ep.hatomic)
+                atomicMax(ep.hparts, m << 16);  // fp32 bits of the bf16 |h|: integer order = numeric
+            else
+                ep.hparts[blockIdx.x] = m << 16;
+        }
+    }
+    if constexpr (EPI == kEpiAct) {
+        if (threadIdx.x == 0 && ep.amax != nullptr) {
+            const unsigned m = *hmax_cta;
+            if (m >= 0x7F80u)
+                atomicOr(status, kStatusNonfinite);
+            atomicMax(ep.amax, m << 16);
+        }
     }
     if (warp == 1) {
         tc_fence_after_sync();
@@ -672,16 +945,15 @@ static_assert(kBK == kSchedBlockK, "the schedule's tile costs count the kernel's
 
 // One launch of gemm_kernel over the problems probs[plan.order[0 .. n)]
 // (n = 1 for NP = 1), in the plan's slot order.
-template <int BN, int STAGES, bool PAIR, bool GLU = false, int NP = 1>
+template <int BN, int STAGES, bool PAIR, int EPI = kEpiPlain, int NP = 1>
 cudaError_t run_gemm(const GemmDesc *probs, const LaunchPlan &plan, const DeviceInfo &dev,
-                     cudaStream_t stream, void *h = nullptr, unsigned *hparts = nullptr,
-                     int *nparts = nullptr, int hatomic = 0)
+                     cudaStream_t stream, EpiParams<EPI> ep = {}, void *h = nullptr,
+                     int *nparts = nullptr)
 {
-    using C = Cfg<BN, STAGES, PAIR, GLU>;
+    using C = Cfg<BN, STAGES, PAIR, EPI>;
     if (!plan.ok || plan.nprob < 1 || plan.nprob > NP)
         return cudaErrorInvalidValue;
     GemmSet<NP> set;
-    CUtensorMap mh;
     for (int i = 0; i < plan.nprob; ++i) {
         const GemmDesc &p = probs[plan.order[i]];
         if (!make_map(&set.a[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, p.a, p.M, p.K, kBK, kBM) ||
@@ -689,18 +961,27 @@ cudaError_t run_gemm(const GemmDesc *probs, const LaunchPlan &plan, const Device
             return cudaErrorNotSupported;
         // TMA stores need every C row to start on a 16-byte boundary
         int tma_store;
-        if (GLU) {
+        if constexpr (EPI == kEpiGlu) {
             // AB and h through 32-row x 32-column boxes in the 64-byte swizzle
             tma_store = 1;
             if (p.N % 256 != 0 ||
                 !make_tensor_map_2d(&set.c[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p.c, p.M, p.N,
                                     kGluCols, 32, CU_TENSOR_MAP_SWIZZLE_64B) ||
-                !make_tensor_map_2d(&mh, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, h, p.M, p.N / 2,
+                !make_tensor_map_2d(&ep.h, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, h, p.M, p.N / 2,
                                     kGluCols, 32, CU_TENSOR_MAP_SWIZZLE_64B))
                 return cudaErrorNotSupported;
         } else {
             tma_store = (p.N % 8 == 0) && make_map(&set.c[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
                                                    p.c, p.M, p.N, kEpiCols, 32);
+            if constexpr (EPI == kEpiAct) {
+                const CUtensorMapDataType bf = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+                if (tma_store && ep.residual != nullptr &&
+                    !make_map(&ep.res, bf, 2, ep.residual, p.M, p.N, kEpiCols, 32))
+                    return cudaErrorNotSupported;
+                if (tma_store && ep.zout != nullptr &&
+                    !make_map(&ep.z, bf, 2, ep.zout, p.M, p.N, kEpiCols, 32))
+                    return cudaErrorNotSupported;
+            }
             if (!tma_store)
                 set.c[i] = set.a[i];  // not used by the kernel
         }
@@ -722,13 +1003,11 @@ cudaError_t run_gemm(const GemmDesc *probs, const LaunchPlan &plan, const Device
         set.first_tile[i] = i <= plan.nprob ? plan.first_tile[i] : plan.first_tile[plan.nprob];
     set.nprob = plan.nprob;
     set.sched = plan.s;
-    if (!GLU)
-        mh = set.a[0];  // not used by the kernel
     static std::once_flag attr_once[64];
     static cudaError_t attr_err[64];
     const int dv = dev.ordinal & 63;
     std::call_once(attr_once[dv], [&] {
-        attr_err[dv] = cudaFuncSetAttribute(gemm_kernel<BN, STAGES, PAIR, GLU, NP>,
+        attr_err[dv] = cudaFuncSetAttribute(gemm_kernel<BN, STAGES, PAIR, EPI, NP>,
                                             cudaFuncAttributeMaxDynamicSharedMemorySize,
                                             C::kSmemBytes);
     });
@@ -738,9 +1017,9 @@ cudaError_t run_gemm(const GemmDesc *probs, const LaunchPlan &plan, const Device
     const int group_m = PAIR ? 8 : 16;
     if (nparts != nullptr)
         *nparts = (PAIR ? 2 : 1) * units;
-    return launch_pdl_cluster(gemm_kernel<BN, STAGES, PAIR, GLU, NP>, dim3((PAIR ? 2 : 1) * units),
-                              dim3(C::kThreads), C::kSmemBytes, stream, PAIR ? 2u : 1u, set, mh,
-                              dev.status, wait_limit_ns(), group_m, hparts, hatomic);
+    return launch_pdl_cluster(gemm_kernel<BN, STAGES, PAIR, EPI, NP>, dim3((PAIR ? 2 : 1) * units),
+                              dim3(C::kThreads), C::kSmemBytes, stream, PAIR ? 2u : 1u, set, ep,
+                              dev.status, wait_limit_ns(), group_m);
 }
 
 constexpr int kVariantSingle = 1;
@@ -839,8 +1118,8 @@ cudaError_t launch_set(const GemmDesc *probs, const int *idx, int n, int v, cons
     if (n == 1)
         return v == kVariantPair ? run_gemm<256, 6, true>(g, plan, dev, stream)
                                  : run_gemm<256, 4, false>(g, plan, dev, stream);
-    return v == kVariantPair ? run_gemm<256, 6, true, false, kMaxLaunchProblems>(g, plan, dev, stream)
-                             : run_gemm<256, 4, false, false, kMaxLaunchProblems>(g, plan, dev, stream);
+    return v == kVariantPair ? run_gemm<256, 6, true, kEpiPlain, kMaxLaunchProblems>(g, plan, dev, stream)
+                             : run_gemm<256, 4, false, kEpiPlain, kMaxLaunchProblems>(g, plan, dev, stream);
 }
 
 } // namespace
@@ -914,10 +1193,30 @@ cudaError_t launch_gemm_w13_swiglu(const uint8_t *x_q, const uint8_t *w13_q, int
     const int v = gemm_variant(M, dev);
     const SchedProblem sp = sched_problem(g);
     const LaunchPlan plan = sched_plan(&sp, 1, variant_tile_m(v), 256, variant_units(v, dev));
+    EpiParams<kEpiGlu> ep = {};
+    ep.hparts = hparts;
+    ep.hatomic = hatomic ? 1 : 0;
     if (v == kVariantPair)
-        return run_gemm<256, 6, true, true>(&g, plan, dev, stream, h, hparts, nparts,
-                                            hatomic ? 1 : 0);
-    return run_gemm<256, 4, false, true>(&g, plan, dev, stream, h, hparts, nparts, hatomic ? 1 : 0);
+        return run_gemm<256, 6, true, kEpiGlu>(&g, plan, dev, stream, ep, h, nparts);
+    return run_gemm<256, 4, false, kEpiGlu>(&g, plan, dev, stream, ep, h, nparts);
+}
+
+cudaError_t launch_gemm_act(const GemmDesc &g, const ActEpilogue &e, const DeviceInfo &dev,
+                            cudaStream_t stream)
+{
+    EpiParams<kEpiAct> ep = {};
+    ep.bias = e.bias;
+    ep.bias_f32 = e.bias_f32;
+    ep.act = e.act;
+    ep.residual = static_cast<const __nv_bfloat16 *>(e.residual);
+    ep.zout = static_cast<__nv_bfloat16 *>(e.z);
+    ep.amax = e.amax;
+    const int v = gemm_variant(g.M, dev);
+    const SchedProblem sp = sched_problem(g);
+    const LaunchPlan plan = sched_plan(&sp, 1, variant_tile_m(v), 256, variant_units(v, dev));
+    if (v == kVariantPair)
+        return run_gemm<256, 5, true, kEpiAct>(&g, plan, dev, stream, ep);
+    return run_gemm<256, 3, false, kEpiAct>(&g, plan, dev, stream, ep);
 }
 
 cudaError_t launch_wait_selftest(uint64_t limit_ns, const DeviceInfo &dev, cudaStream_t stream)

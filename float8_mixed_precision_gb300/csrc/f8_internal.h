@@ -276,6 +276,19 @@ cudaError_t launch_gemm_w13_swiglu(const uint8_t *x_q, const uint8_t *w13_q, int
                                    unsigned *hparts, int *nparts, const DeviceInfo &dev,
                                    cudaStream_t stream, bool hatomic = false);
 
+// What launch_gemm_act's epilogue adds to a GEMM: y = act(acc / (sa sb) + bias) +
+// residual to g.c, the activation's input to z, and one atomicMax of |y| per CTA
+// into the zeroed amax; bias, residual, z and amax may be null.
+struct ActEpilogue {
+    const void *bias;
+    int bias_f32, act;
+    const void *residual;
+    void *z;
+    unsigned *amax;
+};
+cudaError_t launch_gemm_act(const GemmDesc &g, const ActEpilogue &e, const DeviceInfo &dev,
+                            cudaStream_t stream);
+
 // d(AB) [M, 2F] (AB's column order) of the w1+w3 group from the gradient dh
 // [M, F] of h = silu(a) b and the forward's AB, with one |d(AB)| partial
 // maximum per CTA in partials (*nparts receives their count).  F % 128 == 0.

@@ -1,0 +1,605 @@
+// The residual stream between two blocks: a block's output normed, gated and added
+// to the scaled stream, and the norm in front of the next block; with its backward
+// pass and every parameter's gradient.
+//
+//   forward   u = norm_post(a), r' = scale r + g u, y = norm_pre(r')
+//   backward  D = dr' + s2 (dy w2 - mean(dy w2) - e2 mean(dy w2 e2)), dr = scale D,
+//             du = g D, da = s1 (du w1 - mean(du w1) - e1 mean(du w1 e1)),
+//             dw2 = sum dy e2, db2 = sum dy, dw1 = sum du e1, db1 = sum du,
+//             dg = sum over the gate's rows of D u
+//
+// Everything between the loads and the stores is fp32.  Sums over rows: rows are cut
+// into chunks; a chunk leaves one partial row of each parameter's gradient, writes
+// the gate gradients whose rows it has whole, and leaves partial rows for the gates
+// of its first and last rows where those reach into other chunks.  Partial rows are
+// added in order by kernels of their own.  No atomics: equal inputs give equal bits.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "f8_internal.h"
+#include "f8_ptx.cuh"
+
+namespace f8 {
+namespace {
+
+constexpr int kWalkThreads = 512;
+
+__device__ __forceinline__ float elem(const __nv_bfloat16 *p) { return __bfloat162float(*p); }
+__device__ __forceinline__ float elem(const float *p) { return *p; }
+__device__ __forceinline__ void put(__nv_bfloat16 *p, float f) { *p = __float2bfloat16_rn(f); }
+__device__ __forceinline__ void put(float *p, float f) { *p = f; }
+
+// One parameter value, bf16 or fp32.
+__device__ __forceinline__ float param(const void *p, int f32, int64_t i)
+{
+    return f32 ? static_cast<const float *>(p)[i]
+               : __bfloat162float(static_cast<const __nv_bfloat16 *>(p)[i]);
+}
+
+__device__ __forceinline__ void put_param(void *p, int f32, int64_t i, float v)
+{
+    if (f32)
+        static_cast<float *>(p)[i] = v;
+    else
+        static_cast<__nv_bfloat16 *>(p)[i] = __float2bfloat16_rn(v);
+}
+
+// What both passes know of the call.
+struct Call {
+    int layer;           // layer norm (else RMS norm)
+    int w_f32, g_f32;
+    int64_t rows, cols, gate_rows;
+    float eps, scale;
+    const void *w_pre, *b_pre, *w_post, *b_post, *gate;
+    float *stats;        // [4][rows]: mean and 1/deviation of a, then of r'
+};
+
+// Sum over the block, in a fixed order; every thread gets it.  `red` has two halves
+// used in turn, so one barrier a sum.
+template <int THREADS>
+struct BlockSum {
+    float *red;  // [2][THREADS / 32]
+    int half;
+
+    __device__ __forceinline__ float operator()(float v)
+    {
+        constexpr int W = THREADS / 32;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+            v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+        float *r = red + half * W;
+        half ^= 1;
+        if ((threadIdx.x & 31) == 0)
+            r[threadIdx.x >> 5] = v;
+        __syncthreads();
+        v = 0.0f;
+#pragma unroll
+        for (int w = 0; w < W; ++w)
+            v += r[w];
+        return v;
+    }
+};
+
+// ------------------------------------------------------------ any width
+// One block a row, which is walked once per reduction and once for the outputs.
+template <typename TA, typename TR>
+__global__ void __launch_bounds__(kWalkThreads)
+fwd_walk_kernel(const Call c, const TA *a, const TR *r, TR *r_out, TA *y, unsigned *amax,
+                unsigned *status)
+{
+    __shared__ float red[2 * kWalkThreads / 32];
+    __shared__ unsigned blk;
+    if (threadIdx.x == 0)
+        blk = 0u;
+    griddep_wait();
+    griddep_launch_dependents();
+    BlockSum<kWalkThreads> sum{red, 0};
+    const float inv_c = 1.0f / static_cast<float>(c.cols);
+    const int64_t total = c.rows * c.cols;
+    unsigned m = 0u;
+    for (int64_t row = blockIdx.x; row < c.rows; row += gridDim.x) {
+        const int64_t at = row * c.cols;
+        const int64_t gat = c.gate != nullptr ? row / c.gate_rows * c.cols : 0;
+        float mu1 = 0.0f, s1 = 1.0f;
+        if (c.w_post != nullptr) {
+            float t = 0.0f;
+            if (c.layer) {
+                for (int64_t i = threadIdx.x; i < c.cols; i += kWalkThreads)
+                    if (in_range(at + i, 1, total, status))
+                        t += elem(a + at + i);
+                mu1 = sum(t) * inv_c;
+            }
+            t = 0.0f;
+            for (int64_t i = threadIdx.x; i < c.cols; i += kWalkThreads)
+                if (in_range(at + i, 1, total, status)) {
+                    const float d = elem(a + at + i) - mu1;
+                    t = fmaf(d, d, t);
+                }
+            s1 = 1.0f / sqrtf(sum(t) * inv_c + c.eps);
+        }
+        auto stream = [&](int64_t i) {
+            if (!in_range(at + i, 1, total, status))
+                return 0.0f;
+            float u = elem(a + at + i);
+            if (c.w_post != nullptr) {
+                u = (u - mu1) * s1 * param(c.w_post, c.w_f32, i);
+                if (c.b_post != nullptr)
+                    u += param(c.b_post, c.w_f32, i);
+            }
+            if (c.gate != nullptr)
+                u *= param(c.gate, c.g_f32, gat + i);
+            return fmaf(c.scale, elem(r + at + i), u);
+        };
+        float mu2 = 0.0f, t = 0.0f;
+        if (c.layer) {
+            for (int64_t i = threadIdx.x; i < c.cols; i += kWalkThreads)
+                t += stream(i);
+            mu2 = sum(t) * inv_c;
+        }
+        t = 0.0f;
+        for (int64_t i = threadIdx.x; i < c.cols; i += kWalkThreads) {
+            const float d = stream(i) - mu2;
+            t = fmaf(d, d, t);
+        }
+        const float s2 = 1.0f / sqrtf(sum(t) * inv_c + c.eps);
+        // a thread reads its own columns only, so r_out may be r and y may be a
+        for (int64_t i = threadIdx.x; i < c.cols; i += kWalkThreads) {
+            const float v = stream(i);
+            float o = (v - mu2) * s2 * param(c.w_pre, c.w_f32, i);
+            if (c.b_pre != nullptr)
+                o += param(c.b_pre, c.w_f32, i);
+            if (!in_range(at + i, 1, total, status))
+                continue;
+            put(r_out + at + i, v);
+            put(y + at + i, o);
+            if constexpr (sizeof(TA) == 2)
+                m = max(m, static_cast<unsigned>(__bfloat16_as_ushort(y[at + i])) & 0x7FFFu);
+        }
+        if (threadIdx.x == 0) {
+            if (c.w_post != nullptr) {
+                if (c.layer)
+                    c.stats[row] = mu1;
+                c.stats[c.rows + row] = s1;
+            }
+            if (c.layer)
+                c.stats[2 * c.rows + row] = mu2;
+            c.stats[3 * c.rows + row] = s2;
+        }
+    }
+    if (amax != nullptr) {
+        __syncthreads();
+        m = __reduce_max_sync(0xFFFFFFFFu, m);
+        if ((threadIdx.x & 31) == 0)
+            atomicMax(&blk, m);
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            if (blk >= 0x7F80u)
+                atomicOr(status, kStatusNonfinite);
+            atomicMax(amax, blk << 16);  // the maximum does not depend on the order
+        }
+    }
+}
+
+// D = dr' + s2 g - s2 mean(g) - e2 s2 mean(g e2) of one element, g = dy w2, from the
+// row's k1 = -s2 mean(g e2) and k2 = -s2 mean(g).
+__device__ __forceinline__ float stream_grad(float dr, float g, float e2, float s2, float k1, float k2)
+{
+    return dr + fmaf(g, s2, fmaf(e2, k1, k2));
+}
+
+template <typename TA, typename TR>
+__global__ void __launch_bounds__(kWalkThreads)
+bwd_walk_kernel(const Call c, const TA *__restrict__ dy, const TR *__restrict__ dr_out,
+                const TA *__restrict__ a, const TR *__restrict__ r_out, TA *__restrict__ da,
+                TR *__restrict__ dr, float *__restrict__ consts, unsigned *status)
+{
+    __shared__ float red[2 * kWalkThreads / 32];
+    griddep_wait();
+    griddep_launch_dependents();
+    BlockSum<kWalkThreads> sum{red, 0};
+    const float inv_c = 1.0f / static_cast<float>(c.cols);
+    const int64_t total = c.rows * c.cols;
+    const bool post = c.w_post != nullptr;
+    for (int64_t row = blockIdx.x; row < c.rows; row += gridDim.x) {
+        const int64_t at = row * c.cols;
+        const int64_t gat = c.gate != nullptr ? row / c.gate_rows * c.cols : 0;
+        const float mu1 = post && c.layer ? c.stats[row] : 0.0f;
+        const float s1 = post ? c.stats[c.rows + row] : 1.0f;
+        const float mu2 = c.layer ? c.stats[2 * c.rows + row] : 0.0f;
+        const float s2 = c.stats[3 * c.rows + row];
+        float t1 = 0.0f, t2 = 0.0f;
+        for (int64_t i = threadIdx.x; i < c.cols; i += kWalkThreads)
+            if (in_range(at + i, 1, total, status)) {
+                const float g = elem(dy + at + i) * param(c.w_pre, c.w_f32, i);
+                t1 = fmaf(g, (elem(r_out + at + i) - mu2) * s2, t1);
+                t2 += g;
+            }
+        const float k1 = -s2 * (sum(t1) * inv_c);
+        const float k2 = c.layer ? -s2 * (sum(t2) * inv_c) : 0.0f;
+        auto grad = [&](int64_t i) {
+            return stream_grad(dr_out != nullptr ? elem(dr_out + at + i) : 0.0f,
+                               elem(dy + at + i) * param(c.w_pre, c.w_f32, i),
+                               (elem(r_out + at + i) - mu2) * s2, s2, k1, k2);
+        };
+        float d1 = 0.0f, d2 = 0.0f;
+        if (post) {
+            t1 = t2 = 0.0f;
+            for (int64_t i = threadIdx.x; i < c.cols; i += kWalkThreads)
+                if (in_range(at + i, 1, total, status)) {
+                    float h = grad(i) * param(c.w_post, c.w_f32, i);
+                    if (c.gate != nullptr)
+                        h *= param(c.gate, c.g_f32, gat + i);
+                    t1 = fmaf(h, (elem(a + at + i) - mu1) * s1, t1);
+                    t2 += h;
+                }
+            d1 = sum(t1) * inv_c;
+            d2 = c.layer ? sum(t2) * inv_c : 0.0f;
+        }
+        for (int64_t i = threadIdx.x; i < c.cols; i += kWalkThreads) {
+            if (!in_range(at + i, 1, total, status))
+                continue;
+            const float d = grad(i);
+            if (dr != nullptr)
+                put(dr + at + i, c.scale * d);
+            if (da == nullptr)
+                continue;
+            float h = c.gate != nullptr ? d * param(c.gate, c.g_f32, gat + i) : d;
+            if (post) {
+                const float e1 = (elem(a + at + i) - mu1) * s1;
+                h = s1 * (fmaf(-e1, d1, h * param(c.w_post, c.w_f32, i)) - d2);
+            }
+            put(da + at + i, h);
+        }
+        if (threadIdx.x == 0 && consts != nullptr) {
+            consts[row] = k1;
+            consts[c.rows + row] = k2;
+        }
+    }
+}
+
+// ------------------------------------------------------------ sums over rows
+// The gates of a chunk of rows [first, stop): a gate's rows may reach into other
+// chunks only at the chunk's ends.
+struct Chunks {
+    int64_t rows, gate_rows, chunk;
+    __host__ __device__ int64_t first(int64_t i) const { return i * chunk; }
+    __host__ __device__ int64_t stop(int64_t i) const
+    {
+        const int64_t e = (i + 1) * chunk;
+        return e < rows ? e : rows;
+    }
+    __host__ __device__ int64_t gate(int64_t row) const { return row / gate_rows; }
+    __host__ __device__ int64_t gate_first(int64_t g) const { return g * gate_rows; }
+    __host__ __device__ int64_t gate_stop(int64_t g) const
+    {
+        return gate_rows >= rows - g * gate_rows ? rows : (g + 1) * gate_rows;
+    }
+    // whether gate g's rows all lie in chunk i, and which of the chunk's two partial
+    // rows takes them where they do not
+    __host__ __device__ bool whole(int64_t g, int64_t i) const
+    {
+        return gate_first(g) >= first(i) && gate_stop(g) <= stop(i);
+    }
+    __host__ __device__ int slot(int64_t g, int64_t i) const { return gate(first(i)) == g ? 0 : 1; }
+};
+
+// Block (x, y): 256 columns, chunk y.  parts: [chunks][4][cols] of dw_pre, db_pre,
+// dw_post, db_post; ends: [chunks][2][cols] of dgate.
+template <typename TA, typename TR>
+__global__ void __launch_bounds__(256)
+cols_walk_kernel(const Call c, const Chunks ch, const TA *__restrict__ dy, const TR *__restrict__ dr_out,
+                 const TA *__restrict__ a, const TR *__restrict__ r_out,
+                 const float *__restrict__ consts, float *__restrict__ parts, float *__restrict__ ends,
+                 void *__restrict__ dgate, unsigned *status)
+{
+    griddep_wait();
+    griddep_launch_dependents();
+    const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    if (i >= c.cols)
+        return;
+    const int64_t chunk = blockIdx.y, first = ch.first(chunk), stop = ch.stop(chunk);
+    const int64_t total = c.rows * c.cols;
+    const bool post = c.w_post != nullptr, gated = c.gate != nullptr;
+    const float w2 = param(c.w_pre, c.w_f32, i);
+    const float w1 = post ? param(c.w_post, c.w_f32, i) : 1.0f;
+    const float b1 = c.b_post != nullptr ? param(c.b_post, c.w_f32, i) : 0.0f;
+    float dw2 = 0.0f, db2 = 0.0f, dw1 = 0.0f, db1 = 0.0f;
+    for (int64_t row = first; row < stop;) {
+        // rows of one gate: S = sum D e1, T = sum D
+        const int64_t g = gated ? ch.gate(row) : 0;
+        const int64_t end = gated ? min(stop, ch.gate_stop(g)) : stop;
+        float S = 0.0f, T = 0.0f;
+        for (; row < end; ++row) {
+            const int64_t at = row * c.cols + i;
+            if (!in_range(at, 1, total, status))
+                continue;
+            const float mu1 = post && c.layer ? c.stats[row] : 0.0f;
+            const float s1 = post ? c.stats[c.rows + row] : 1.0f;
+            const float mu2 = c.layer ? c.stats[2 * c.rows + row] : 0.0f;
+            const float s2 = c.stats[3 * c.rows + row];
+            const float v = elem(dy + at), e2 = (elem(r_out + at) - mu2) * s2;
+            const float d = stream_grad(dr_out != nullptr ? elem(dr_out + at) : 0.0f, v * w2, e2, s2,
+                                        consts[row], consts[c.rows + row]);
+            const float e1 = (elem(a + at) - mu1) * s1;
+            dw2 = fmaf(v, e2, dw2);
+            db2 += v;
+            S = fmaf(d, e1, S);
+            T += d;
+        }
+        const float gate = gated ? param(c.gate, c.g_f32, g * c.cols + i) : 1.0f;
+        dw1 = fmaf(gate, S, dw1);
+        db1 = fmaf(gate, T, db1);
+        if (dgate != nullptr) {
+            const float dg = fmaf(S, w1, T * b1);
+            if (ch.whole(g, chunk))
+                put_param(dgate, c.g_f32, g * c.cols + i, dg);
+            else
+                ends[(chunk * 2 + ch.slot(g, chunk)) * c.cols + i] = dg;
+        }
+    }
+    float *p = parts + chunk * 4 * c.cols + i;
+    p[0] = dw2;
+    p[c.cols] = db2;
+    p[2 * c.cols] = dw1;
+    p[3 * c.cols] = db1;
+}
+
+// The parameters' gradients from the partial rows, in a fixed order: 32 columns a
+// block, 32 threads a column, each every 32nd row; blockIdx.y names the gradient.
+struct Sums {
+    void *out[4];
+};
+
+__global__ void __launch_bounds__(1024)
+reduce_kernel(const float *__restrict__ parts, int nparts, int64_t cols, int f32, const Sums sums,
+              unsigned *status)
+{
+    __shared__ float acc[32][33];
+    griddep_wait();
+    griddep_launch_dependents();
+    void *out = sums.out[blockIdx.y];
+    if (out == nullptr)
+        return;
+    const int lane = threadIdx.x & 31, k = threadIdx.x >> 5;
+    const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + lane;
+    float s = 0.0f;
+    if (c < cols) {
+        const float *p = parts + static_cast<int64_t>(blockIdx.y) * cols + c;
+#pragma unroll 8
+        for (int i = k; i < nparts; i += 32)
+            s += p[static_cast<int64_t>(i) * 4 * cols];
+    }
+    acc[k][lane] = s;
+    __syncthreads();
+    s = acc[lane][k];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+    const int64_t col = static_cast<int64_t>(blockIdx.x) * 32 + k;
+    if (lane == 0 && col < cols && in_range(col, 1, cols, status))
+        put_param(out, f32, col, s);
+}
+
+// dgate of the gates whose rows lie in several chunks.  Block (x, y) looks at the
+// border after chunk y and sums the gate that reaches over it, if its rows begin in
+// that chunk, over all its chunks.
+__global__ void __launch_bounds__(256)
+gate_reduce_kernel(const float *__restrict__ ends, const Chunks ch, int64_t nchunks, int64_t cols,
+                   int f32, void *__restrict__ dgate, unsigned *status)
+{
+    griddep_wait();
+    griddep_launch_dependents();
+    const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    const int64_t first = blockIdx.y;
+    const int64_t g = ch.gate(ch.stop(first) - 1);
+    if (i >= cols || ch.gate_stop(g) <= ch.stop(first) || ch.gate_first(g) < ch.first(first))
+        return;
+    float s = 0.0f;
+#pragma unroll 8
+    for (int64_t k = first; k < nchunks; ++k) {
+        if (k > first && ch.first(k) >= ch.gate_stop(g))
+            break;
+        s += ends[(k * 2 + ch.slot(g, k)) * cols + i];
+    }
+    if (in_range(g * cols + i, 1, ((ch.rows - 1) / ch.gate_rows + 1) * cols, status))
+        put_param(dgate, f32, g * cols + i, s);
+}
+
+// ------------------------------------------------------------ launches
+constexpr int kMaxChunks = 1024;
+
+int64_t walk_chunks(int64_t rows, int64_t cols, int sms)
+{
+    const int64_t strips = (cols + 255) / 256;
+    return std::max<int64_t>(1, std::min<int64_t>({(8ll * sms + strips - 1) / strips, (rows + 7) / 8,
+                                                   kMaxChunks}));
+}
+
+size_t round256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
+
+// The backward pass's workspace: row constants, partial rows of the parameters'
+// gradients, and of the gates at the chunks' ends.
+struct Workspace {
+    size_t consts, parts, ends, bytes;
+};
+
+Workspace workspace_of(int64_t rows, int64_t cols, int sms)
+{
+    const size_t n = static_cast<size_t>(walk_chunks(rows, cols, sms));
+    const size_t row = static_cast<size_t>(cols) * sizeof(float);
+    Workspace w;
+    w.consts = 0;
+    w.parts = round256(2 * static_cast<size_t>(rows) * sizeof(float));
+    w.ends = w.parts + round256(4 * n * row);
+    w.bytes = w.ends + round256(2 * n * row);
+    return w;
+}
+
+Call call_of(const f8_residual_norm &n, float *stats)
+{
+    return Call{n.kind == F8_LAYER_NORM, n.w_type == F8_F32, n.gate_type == F8_F32, n.rows, n.cols,
+                n.gate_rows, n.eps, n.scale, n.w_pre, n.b_pre, n.w_post, n.b_post, n.gate, stats};
+}
+
+template <typename TA, typename TR>
+cudaError_t fwd(const Call &c, const void *a, const void *r, void *r_out, void *y, unsigned *amax,
+                const DeviceInfo &dev, cudaStream_t st)
+{
+    const int64_t grid = std::min<int64_t>(c.rows, 4 * dev.sm_count);
+    return launch_pdl(fwd_walk_kernel<TA, TR>, dim3(static_cast<unsigned>(grid)), dim3(kWalkThreads), 0,
+                      st, c, static_cast<const TA *>(a), static_cast<const TR *>(r),
+                      static_cast<TR *>(r_out), static_cast<TA *>(y), amax, dev.status);
+}
+
+template <typename TA, typename TR>
+cudaError_t bwd(const Call &c, const void *dy, const void *dr_out, const void *a, const void *r_out,
+                const f8_residual_norm_grads &g, uint8_t *ws, const DeviceInfo &dev, cudaStream_t st)
+{
+    const bool sums = g.dw_pre != nullptr || g.db_pre != nullptr || g.dw_post != nullptr ||
+                      g.db_post != nullptr || g.dgate != nullptr;
+    const Workspace w = workspace_of(c.rows, c.cols, dev.sm_count);
+    float *consts = reinterpret_cast<float *>(ws + w.consts);
+    float *parts = reinterpret_cast<float *>(ws + w.parts);
+    float *ends = reinterpret_cast<float *>(ws + w.ends);
+    const auto *dy_ = static_cast<const TA *>(dy), *a_ = static_cast<const TA *>(a);
+    const auto *dr_ = static_cast<const TR *>(dr_out), *r_ = static_cast<const TR *>(r_out);
+    const int64_t grid = std::min<int64_t>(c.rows, 4 * dev.sm_count);
+    cudaError_t e = launch_pdl(bwd_walk_kernel<TA, TR>, dim3(static_cast<unsigned>(grid)),
+                               dim3(kWalkThreads), 0, st, c, dy_, dr_, a_, r_, static_cast<TA *>(g.da),
+                               static_cast<TR *>(g.dr), consts, dev.status);
+    if (e != cudaSuccess || !sums)
+        return e;
+    const int64_t want = walk_chunks(c.rows, c.cols, dev.sm_count);
+    const Chunks ch{c.rows, c.gate != nullptr ? c.gate_rows : c.rows, (c.rows + want - 1) / want};
+    const int64_t n = (c.rows + ch.chunk - 1) / ch.chunk;
+    const unsigned strips = static_cast<unsigned>((c.cols + 255) / 256);
+    e = launch_pdl(cols_walk_kernel<TA, TR>, dim3(strips, static_cast<unsigned>(n)), dim3(256), 0, st, c,
+                   ch, dy_, dr_, a_, r_, static_cast<const float *>(consts), parts, ends, g.dgate,
+                   dev.status);
+    if (e != cudaSuccess)
+        return e;
+    const Sums out{{g.dw_pre, g.db_pre, g.dw_post, g.db_post}};
+    e = launch_pdl(reduce_kernel, dim3(static_cast<unsigned>((c.cols + 31) / 32), 4), dim3(1024), 0, st,
+                   static_cast<const float *>(parts), static_cast<int>(n), c.cols, c.w_f32, out,
+                   dev.status);
+    if (e != cudaSuccess || g.dgate == nullptr || n == 1)
+        return e;
+    return launch_pdl(gate_reduce_kernel, dim3(strips, static_cast<unsigned>(n - 1)), dim3(256), 0, st,
+                      static_cast<const float *>(ends), ch, n, c.cols, c.g_f32, g.dgate, dev.status);
+}
+
+bool type_ok(f8_dtype t) { return t == F8_BF16 || t == F8_F32; }
+
+f8_status check_call(const f8_residual_norm *n)
+{
+    if (n == nullptr || (n->kind != F8_LAYER_NORM && n->kind != F8_RMS_NORM) || !type_ok(n->x_type) ||
+        !type_ok(n->r_type) || !type_ok(n->w_type) || !type_ok(n->gate_type) || n->rows < 0 ||
+        n->cols < 0 || !(n->eps >= 0.0f) || !std::isfinite(n->scale))
+        return F8_ERR_INVALID;
+    if (n->r_type != n->x_type && n->r_type != F8_F32)
+        return F8_ERR_INVALID;
+    if ((n->gate != nullptr && n->gate_rows < 1) || (n->b_post != nullptr && n->w_post == nullptr))
+        return F8_ERR_INVALID;
+    if (n->cols > INT32_MAX / 2 || (n->cols > 0 && n->rows > INT64_MAX / 8 / n->cols))
+        return F8_ERR_SHAPE;
+    if (n->rows > 0 && n->cols > 0 && n->w_pre == nullptr)
+        return F8_ERR_INVALID;
+    if (!aligned(n->w_pre, 16) || !aligned(n->b_pre, 16) || !aligned(n->w_post, 16) ||
+        !aligned(n->b_post, 16) || !aligned(n->gate, 16))
+        return F8_ERR_ALIGN;
+    return F8_OK;
+}
+
+} // namespace
+} // namespace f8
+
+using namespace f8;
+
+extern "C" {
+
+f8_status f8_residual_norm_fwd(const f8_residual_norm *n, const void *a, const void *r, void *r_out,
+                               void *y, float *stats, float *amax_out, void *stream)
+{
+    F8_TRY(check_call(n));
+    const bool some = n->rows > 0 && n->cols > 0;
+    if (amax_out != nullptr && n->x_type != F8_BF16)
+        return F8_ERR_INVALID;
+    if (some && (a == nullptr || r == nullptr || r_out == nullptr || y == nullptr || stats == nullptr ||
+                 r_out == y || r_out == a || y == r))
+        return F8_ERR_INVALID;
+    if (!aligned(a, 16) || !aligned(r, 16) || !aligned(r_out, 16) || !aligned(y, 16) ||
+        !aligned(stats, 4) || !aligned(amax_out, 4))
+        return F8_ERR_ALIGN;
+    const DeviceInfo *dev;
+    F8_TRY(get_device(&dev));
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (amax_out != nullptr)
+        F8_TRY_CUDA(cudaMemsetAsync(amax_out, 0, sizeof(float), st));
+    if (!some)
+        return F8_OK;
+    const Call c = call_of(*n, stats);
+    unsigned *amax = reinterpret_cast<unsigned *>(amax_out);
+    if (n->x_type == F8_F32)
+        return from_cuda(fwd<float, float>(c, a, r, r_out, y, amax, *dev, st));
+    if (n->r_type == F8_F32)
+        return from_cuda(fwd<__nv_bfloat16, float>(c, a, r, r_out, y, amax, *dev, st));
+    return from_cuda(fwd<__nv_bfloat16, __nv_bfloat16>(c, a, r, r_out, y, amax, *dev, st));
+}
+
+size_t f8_residual_norm_bwd_workspace_bytes(int64_t rows, int64_t cols)
+{
+    if (rows <= 0 || cols <= 0)
+        return 0;
+    const DeviceInfo *dev = device_info();
+    return workspace_of(rows, cols, dev != nullptr ? dev->sm_count : 152).bytes;
+}
+
+f8_status f8_residual_norm_bwd(const f8_residual_norm *n, const void *dy, const void *dr_out,
+                               const void *a, const void *r_out, const float *stats,
+                               const f8_residual_norm_grads *grads, void *workspace,
+                               size_t workspace_bytes, void *stream)
+{
+    F8_TRY(check_call(n));
+    if (grads == nullptr)
+        return F8_ERR_INVALID;
+    const f8_residual_norm_grads &g = *grads;
+    const bool some = n->rows > 0 && n->cols > 0;
+    if (((g.dw_post != nullptr || g.db_post != nullptr) && n->w_post == nullptr) ||
+        (g.dgate != nullptr && n->gate == nullptr))
+        return F8_ERR_INVALID;
+    if (some && (dy == nullptr || a == nullptr || r_out == nullptr || stats == nullptr ||
+                 workspace == nullptr ||
+                 workspace_bytes < f8_residual_norm_bwd_workspace_bytes(n->rows, n->cols)))
+        return F8_ERR_INVALID;
+    for (const void *in : {dy, dr_out, a, r_out})
+        if (some && in != nullptr && (in == g.da || in == g.dr))
+            return F8_ERR_INVALID;
+    if (!aligned(dy, 16) || !aligned(dr_out, 16) || !aligned(a, 16) || !aligned(r_out, 16) ||
+        !aligned(stats, 4) || !aligned(g.da, 16) || !aligned(g.dr, 16) || !aligned(g.dw_pre, 16) ||
+        !aligned(g.db_pre, 16) || !aligned(g.dw_post, 16) || !aligned(g.db_post, 16) ||
+        !aligned(g.dgate, 16) || !aligned(workspace, 16))
+        return F8_ERR_ALIGN;
+    const DeviceInfo *dev;
+    F8_TRY(get_device(&dev));
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (!some) {  // sums over no rows
+        const size_t bytes = static_cast<size_t>(n->cols) * (n->w_type == F8_BF16 ? 2 : 4);
+        for (void *p : {g.dw_pre, g.db_pre, g.dw_post, g.db_post})
+            if (p != nullptr && bytes > 0)
+                F8_TRY_CUDA(cudaMemsetAsync(p, 0, bytes, st));
+        return F8_OK;
+    }
+    const Call c = call_of(*n, const_cast<float *>(stats));
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    if (n->x_type == F8_F32)
+        return from_cuda(bwd<float, float>(c, dy, dr_out, a, r_out, g, ws, *dev, st));
+    if (n->r_type == F8_F32)
+        return from_cuda(bwd<__nv_bfloat16, float>(c, dy, dr_out, a, r_out, g, ws, *dev, st));
+    return from_cuda(bwd<__nv_bfloat16, __nv_bfloat16>(c, dy, dr_out, a, r_out, g, ws, *dev, st));
+}
+
+} // extern "C"

@@ -1,0 +1,348 @@
+// Rotary positions: pairs of columns of each head turned by position * frequency.
+//
+// Bound by HBM: each element is read and written once, with three operations on it.
+// A block takes a few rows (tokens) and forms their cosines and sines once in shared
+// memory, for all heads of queries and keys; then its threads walk the rows' heads,
+// each moving two vectors of VEC elements that hold VEC whole pairs.
+//
+// The angle: a frequency becomes a fraction of a turn in 64-bit fixed point, so
+// position * fraction mod 2^64 is the angle's fraction of a turn, exactly; its upper
+// 32 bits as a signed number lie in half a turn either way, and sincospi takes them
+// without any further reduction.  A far position thus costs no precision and no
+// 64-bit floating point.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "f8_internal.h"
+#include "f8_ptx.cuh"
+
+namespace f8 {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kMaxDim = 1024;
+constexpr int kMaxRows = 8;  // of a block
+
+// x / d for 0 <= x < 2^16 and 1 <= d < 2^16, by the rounded-up reciprocal.
+struct Div {
+    uint32_t mul, d;
+    explicit Div(uint32_t v) : mul(v > 1 ? (0xFFFFFFFFu / v + 1u) : 0u), d(v) {}
+    Div() = default;
+    __device__ __forceinline__ uint32_t operator()(uint32_t x) const
+    {
+        return d > 1 ? __umulhi(x, mul) : x;
+    }
+};
+
+struct Tensor {
+    const void *x;
+    void *out;
+    int64_t x_batch, x_seq, x_head, out_batch, out_seq, out_head;
+};
+
+struct Args {
+    Tensor t[2];
+    int heads0;          // heads of the first tensor
+    int heads;           // of both
+    int half;            // pairs of a head
+    int turned;          // units of a head that turn
+    int units;           // units of a head
+    int dim;
+    int rows_per_block;
+    int64_t rows, seq;
+    const int64_t *pos;
+    int64_t pos_batch, pos_seq;
+    const double *freqs;
+    float scale;
+    int inverse;
+    Div by_units, by_head_units;
+};
+
+template <typename T, int VEC>
+struct Vec;
+template <>
+struct Vec<__nv_bfloat16, 8> {
+    using type = uint4;
+};
+template <>
+struct Vec<__nv_bfloat16, 4> {
+    using type = uint2;
+};
+template <>
+struct Vec<__nv_bfloat16, 2> {
+    using type = uint32_t;
+};
+template <>
+struct Vec<__nv_bfloat16, 1> {
+    using type = uint16_t;
+};
+template <>
+struct Vec<float, 4> {
+    using type = uint4;
+};
+template <>
+struct Vec<float, 2> {
+    using type = uint2;
+};
+template <>
+struct Vec<float, 1> {
+    using type = uint32_t;
+};
+
+template <typename T, int VEC>
+union Bits {
+    typename Vec<T, VEC>::type v;
+    T e[VEC];
+    __device__ Bits() {}
+};
+
+__device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float to_f(float v) { return v; }
+__device__ __forceinline__ void from_f(float f, __nv_bfloat16 &v) { v = __float2bfloat16_rn(f); }
+__device__ __forceinline__ void from_f(float f, float &v) { v = f; }
+
+// A unit is VEC pairs: columns [VEC u, VEC u + VEC) and the same rot / 2 further on
+// (half), or [2 VEC u, 2 VEC u + 2 VEC) (interleaved).  Units from `turned` on are
+// two vectors of the columns that are copied, the last unit's second one perhaps
+// past the head's end.
+template <typename T, int VEC, bool HALF>
+__global__ void __launch_bounds__(kThreads)
+rope_kernel(const __grid_constant__ Args a)
+{
+    using V = typename Vec<T, VEC>::type;
+    extern __shared__ float2 turn[];  // [rows_per_block][half] cosine and sine, scaled
+    __shared__ int64_t at[kMaxRows];  // the rows' positions
+    griddep_wait();
+    griddep_launch_dependents();
+    const int64_t row0 = static_cast<int64_t>(blockIdx.x) * a.rows_per_block;
+    const int nrows = static_cast<int>(min(static_cast<int64_t>(a.rows_per_block), a.rows - row0));
+    if (threadIdx.x < nrows) {
+        const int64_t row = row0 + threadIdx.x, b = row / a.seq, s = row - b * a.seq;
+        at[threadIdx.x] = a.pos[b * a.pos_batch + s * a.pos_seq];
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < a.half * nrows; i += kThreads) {
+        const int j = i / a.half, p = i - j * a.half;
+        double f = a.freqs[p] * 0.15915494309189535;  // turns a position; whole ones do not count
+        f -= floor(f);
+        const uint64_t frac = __double2ull_rz(f * 18446744073709551616.0);
+        const uint64_t angle = frac * static_cast<uint64_t>(at[j]);
+        const float t = static_cast<float>(static_cast<int32_t>(angle >> 32)) * 0x1p-31f;  // half turns
+        float sn, cs;
+        sincospif(t, &sn, &cs);
+        turn[i] = make_float2(cs * a.scale, (a.inverse ? -sn : sn) * a.scale);
+    }
+    __syncthreads();
+    const int per_row = a.heads * a.units;
+    for (int i = threadIdx.x; i < nrows * per_row; i += kThreads) {
+        const int j = static_cast<int>(a.by_head_units(i));
+        const int hu = i - j * per_row;
+        int h = static_cast<int>(a.by_units(hu));
+        const int u = hu - h * a.units;
+        const Tensor &t = a.t[h < a.heads0 ? 0 : 1];
+        if (h >= a.heads0)
+            h -= a.heads0;
+        const int64_t row = row0 + j, b = row / a.seq, s = row - b * a.seq;
+        const T *x = static_cast<const T *>(t.x) + b * t.x_batch + s * t.x_seq + h * t.x_head;
+        T *o = static_cast<T *>(t.out) + b * t.out_batch + s * t.out_seq + h * t.out_head;
+        const bool turned = u < a.turned;
+        const int c0 = turned ? (HALF ? VEC * u : 2 * VEC * u) : 2 * a.half + 2 * VEC * (u - a.turned);
+        const int c1 = turned && HALF ? c0 + a.half : c0 + VEC;
+        Bits<T, VEC> v0, v1;
+        v0.v = *reinterpret_cast<const V *>(x + c0);
+        if (c1 < a.dim)
+            v1.v = *reinterpret_cast<const V *>(x + c1);
+        if (turned && at[j] >= 0) {
+            const float2 *cs = turn + j * a.half + VEC * u;
+            if (HALF) {
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    const float p = to_f(v0.e[e]), q = to_f(v1.e[e]);
+                    from_f(p * cs[e].x - q * cs[e].y, v0.e[e]);
+                    from_f(q * cs[e].x + p * cs[e].y, v1.e[e]);
+                }
+            } else if (VEC > 1) {
+#pragma unroll
+                for (int e = 0; e < VEC; e += 2) {
+                    const float2 k0 = cs[e / 2], k1 = cs[VEC / 2 + e / 2];
+                    float p = to_f(v0.e[e]), q = to_f(v0.e[e + 1]);
+                    from_f(p * k0.x - q * k0.y, v0.e[e]);
+                    from_f(q * k0.x + p * k0.y, v0.e[e + 1]);
+                    p = to_f(v1.e[e]), q = to_f(v1.e[e + 1]);
+                    from_f(p * k1.x - q * k1.y, v1.e[e]);
+                    from_f(q * k1.x + p * k1.y, v1.e[e + 1]);
+                }
+            } else {
+                const float p = to_f(v0.e[0]), q = to_f(v1.e[0]);
+                from_f(p * cs[0].x - q * cs[0].y, v0.e[0]);
+                from_f(q * cs[0].x + p * cs[0].y, v1.e[0]);
+            }
+        }
+        *reinterpret_cast<V *>(o + c0) = v0.v;
+        if (c1 < a.dim)
+            *reinterpret_cast<V *>(o + c1) = v1.v;
+    }
+}
+
+template <typename T, int VEC, bool HALF>
+cudaError_t run(Args &a, const DeviceInfo &dev, cudaStream_t st)
+{
+    a.turned = a.half / VEC;
+    a.units = a.turned + (a.dim - 2 * a.half + 2 * VEC - 1) / (2 * VEC);
+    const int per_row = a.heads * a.units;
+    // rows of a block: some 1024 units, while all SMs have blocks, within 32 KB of
+    // cosines and sines and the index's range
+    int64_t r = std::min<int64_t>(kMaxRows, std::max(1, 1024 / per_row));
+    r = std::min<int64_t>(r, std::max<int64_t>(1, a.rows / (4 * dev.sm_count)));
+    r = std::min<int64_t>(r, std::max(1, 4096 / a.half));
+    a.rows_per_block = static_cast<int>(r);
+    a.by_units = Div(static_cast<uint32_t>(a.units));
+    a.by_head_units = Div(static_cast<uint32_t>(per_row));
+    const int64_t blocks = (a.rows + r - 1) / r;
+    return launch_pdl(rope_kernel<T, VEC, HALF>, dim3(static_cast<unsigned>(blocks)), dim3(kThreads),
+                      static_cast<size_t>(r) * a.half * sizeof(float2), st, a);
+}
+
+template <typename T, bool HALF>
+cudaError_t pick(Args &a, int vec, const DeviceInfo &dev, cudaStream_t st)
+{
+    if constexpr (sizeof(T) == 2)
+        if (vec == 8)
+            return run<T, 8, HALF>(a, dev, st);
+    switch (vec) {
+    case 4: return run<T, 4, HALF>(a, dev, st);
+    case 2: return run<T, 2, HALF>(a, dev, st);
+    default: return run<T, 1, HALF>(a, dev, st);
+    }
+}
+
+// The widest vector (elements) whose units the columns, strides and addresses allow.
+int vector_of(const f8_rope_tensor *t, int count, int esize, int64_t batch, int64_t seq, int64_t dim,
+              int64_t rot)
+{
+    for (int v = 16 / esize; v > 1; v /= 2) {
+        bool ok = (rot / 2) % v == 0 && dim % v == 0;
+        for (int i = 0; i < count && ok; ++i) {
+            const int64_t strides[6] = {batch > 1 ? t[i].x_batch : 0,   seq > 1 ? t[i].x_seq : 0,
+                                        t[i].heads > 1 ? t[i].x_head : 0, batch > 1 ? t[i].out_batch : 0,
+                                        seq > 1 ? t[i].out_seq : 0,     t[i].heads > 1 ? t[i].out_head : 0};
+            for (int64_t s : strides)
+                ok = ok && s % v == 0;
+            ok = ok && aligned(t[i].x, static_cast<uintptr_t>(v) * esize) &&
+                 aligned(t[i].out, static_cast<uintptr_t>(v) * esize);
+        }
+        if (ok)
+            return v;
+    }
+    return 1;
+}
+
+} // namespace
+} // namespace f8
+
+using namespace f8;
+
+extern "C" {
+
+f8_status f8_rope(const f8_rope_tensor *tensors, int count, f8_dtype type, int64_t batch,
+                  int64_t seq, int64_t dim, int64_t rot, f8_rope_layout layout,
+                  const int64_t *positions, int64_t pos_batch, int64_t pos_seq, const double *freqs,
+                  float scale, int inverse, void *stream)
+{
+    if (tensors == nullptr || count < 1 || count > 2 || (type != F8_BF16 && type != F8_F32) ||
+        (layout != F8_ROPE_HALF && layout != F8_ROPE_INTERLEAVED) || batch < 0 || seq < 0 || dim < 0 ||
+        !std::isfinite(scale))
+        return F8_ERR_INVALID;
+    if (rot < 2 || rot % 2 != 0 || rot > dim || dim > kMaxDim)
+        return F8_ERR_SHAPE;
+    const int esize = type == F8_BF16 ? 2 : 4;
+    int64_t heads = 0;
+    const bool some = batch > 0 && seq > 0;
+    for (int i = 0; i < count; ++i) {
+        const f8_rope_tensor &t = tensors[i];
+        if (t.heads < 0)
+            return F8_ERR_INVALID;
+        if (t.heads > 1 << 12)
+            return F8_ERR_SHAPE;
+        heads += t.heads;
+        if (some && t.heads > 0 && (t.x == nullptr || t.out == nullptr))
+            return F8_ERR_INVALID;
+        // in place means in place: another order of the rows would read what it wrote
+        if (t.x == t.out && (t.x_batch != t.out_batch || t.x_seq != t.out_seq || t.x_head != t.out_head))
+            return F8_ERR_INVALID;
+        if (!aligned(t.x, esize) || !aligned(t.out, esize))
+            return F8_ERR_ALIGN;
+    }
+    if (some && heads > 0 && (positions == nullptr || freqs == nullptr))
+        return F8_ERR_INVALID;
+    if (!aligned(positions, 8) || !aligned(freqs, 8))
+        return F8_ERR_ALIGN;
+    if (batch > 0 && seq > INT32_MAX / batch)
+        return F8_ERR_SHAPE;
+    const DeviceInfo *dev;
+    F8_TRY(get_device(&dev));
+    if (!some || heads == 0)
+        return F8_OK;
+    const int vec = vector_of(tensors, count, esize, batch, seq, dim, rot);
+    if (heads * (dim / vec) > 65535)  // units of a row, within the index's range
+        return F8_ERR_SHAPE;
+    Args a = {};
+    for (int i = 0; i < count; ++i) {
+        const f8_rope_tensor &t = tensors[i];
+        a.t[i] = Tensor{t.x, t.out, t.x_batch, t.x_seq, t.x_head, t.out_batch, t.out_seq, t.out_head};
+    }
+    a.heads0 = static_cast<int>(tensors[0].heads);
+    a.heads = static_cast<int>(heads);
+    a.half = static_cast<int>(rot / 2);
+    a.dim = static_cast<int>(dim);
+    a.rows = batch * seq;
+    a.seq = seq;
+    a.pos = positions;
+    a.pos_batch = pos_batch;
+    a.pos_seq = pos_seq;
+    a.freqs = freqs;
+    a.scale = scale;
+    a.inverse = inverse != 0;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const bool half = layout == F8_ROPE_HALF;
+    if (type == F8_BF16)
+        return from_cuda(half ? pick<__nv_bfloat16, true>(a, vec, *dev, st)
+                              : pick<__nv_bfloat16, false>(a, vec, *dev, st));
+    return from_cuda(half ? pick<float, true>(a, vec, *dev, st) : pick<float, false>(a, vec, *dev, st));
+}
+
+f8_status f8_rope_frequencies(int64_t rot, double base, f8_rope_scaling scaling, double factor,
+                              double original, double slow, double fast, double *freqs)
+{
+    if (freqs == nullptr || !(base > 0.0) || !std::isfinite(base) || scaling < F8_ROPE_PLAIN ||
+        scaling > F8_ROPE_BY_PARTS)
+        return F8_ERR_INVALID;
+    if (rot < 2 || rot % 2 != 0 || rot > kMaxDim || (scaling == F8_ROPE_BASE && rot == 2))
+        return F8_ERR_SHAPE;
+    if (scaling != F8_ROPE_PLAIN && !(factor > 0.0 && std::isfinite(factor)))
+        return F8_ERR_INVALID;
+    if (scaling == F8_ROPE_BY_PARTS && !(original > 0.0 && std::isfinite(original) && slow >= 0.0 && slow < fast &&
+                                         std::isfinite(fast)))
+        return F8_ERR_INVALID;
+    const double n = static_cast<double>(rot);
+    if (scaling == F8_ROPE_BASE)
+        base *= std::pow(factor, n / (n - 2.0));
+    for (int64_t i = 0; i < rot / 2; ++i) {
+        double f = std::pow(base, -2.0 * static_cast<double>(i) / n);
+        if (scaling == F8_ROPE_LINEAR) {
+            f /= factor;
+        } else if (scaling == F8_ROPE_BY_PARTS) {
+            const double turns = original * f / 6.283185307179586;
+            const double keep = std::min(1.0, std::max(0.0, (turns - slow) / (fast - slow)));
+            f = f * keep + f / factor * (1.0 - keep);
+        }
+        freqs[i] = f;
+    }
+    return F8_OK;
+}
+
+} // extern "C"

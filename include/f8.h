@@ -752,6 +752,194 @@ f8_status f8_distill_fwd_bwd(const void *logits, f8_dtype type, int64_t rows, in
                              void *dlogits, int64_t ldd, float *amax_out, void *stream);
 
 /*
+ * What stands between the Float8 linears of a block.  The torchtitan pages name
+ * neither an interface nor a kernel for these either; the formulas below are the
+ * definitions, evaluated in fp32 with one rounding to the output's type.
+ *
+ * Activations:
+ *   F8_ACT_NONE       z
+ *   F8_ACT_RELU       max(z, 0);           slope 1 above 0, 0 at and below it
+ *   F8_ACT_RELU2      max(z, 0)^2;         slope 2 max(z, 0)
+ *   F8_ACT_SILU       z / (1 + exp -z)
+ *   F8_ACT_GELU       z Phi(z), Phi the normal distribution's function
+ *   F8_ACT_GELU_TANH  z / (1 + exp(-2 u)), u = sqrt(2 / pi) (z + 0.044715 z^3)
+ * A NaN gives NaN; -inf gives NaN where the formula is a product with 0.  Values
+ * below 2^-119 may come out as 0.
+ */
+typedef enum {
+    F8_ACT_NONE = 0,
+    F8_ACT_RELU = 1,
+    F8_ACT_RELU2 = 2,
+    F8_ACT_SILU = 3,
+    F8_ACT_GELU = 4,
+    F8_ACT_GELU_TANH = 5
+} f8_act;
+
+/*
+ * f8_gemm_fmt with the linear's bias, activation and residual in its epilogue:
+ *   z = A B^T / (scale_a scale_b) + bias,   y = act(z) + residual
+ * with the residual added to the fp32 activation, so y is rounded once.
+ *   a, b, scale_a, scale_b, M, N, K: as for f8_gemm_fmt (K % 16 == 0; any M, N).
+ *   bias:     device [N] of type bias_type, or NULL.
+ *   residual: device bf16 [M, N], or NULL; may be y.
+ *   y:        device bf16 [M, N].
+ *   z:        device bf16 [M, N] receiving the activation's input for the
+ *             backward pass, or NULL.  y comes from the unrounded z.
+ *   amax_out: device fp32 receiving max |y| of the values as stored, ready for
+ *             f8_cast_transpose (the next linear's input), or NULL.  The call
+ *             zeroes it first.  A non-finite y then sets F8_ERR_NONFINITE.
+ * bf16 tensors, bias and codes 16-byte aligned, scales and amax_out 4-byte.
+ * M, N >= 0 (nothing is done for 0; amax_out is then 0), K >= 16.
+ */
+f8_status f8_gemm_act(const uint8_t *a, f8_format fmt_a, const uint8_t *b, f8_format fmt_b,
+                      int64_t M, int64_t N, int64_t K, const float *scale_a, const float *scale_b,
+                      const void *bias, f8_dtype bias_type, f8_act act, const void *residual,
+                      void *y, void *z, float *amax_out, void *stream);
+
+/*
+ * Backward of the activation and the bias, for the gradient dy of y and the z
+ * that f8_gemm_act kept (the residual's gradient is dy itself):
+ *   dz = dy act'(z),   dbias = sum over rows of dz (before its rounding)
+ *   dy, z, dz: device bf16 [rows, cols]; dz may be dy or z.  z may be NULL for
+ *             F8_ACT_NONE; dz may be NULL.
+ *   dbias:    device [cols] of type bias_type, or NULL.
+ *   amax_out: device fp32 receiving max |dz| as stored (needs dz), or NULL; zeroed
+ *             by the call.
+ *   workspace: f8_act_bwd_workspace_bytes(rows, cols) bytes, 16-byte aligned;
+ *             may be NULL if dbias is.
+ * The sums over rows are formed in a fixed order: equal inputs give equal bits.
+ * rows, cols >= 0; cols < 2^30 and rows * cols < 2^60.
+ */
+size_t f8_act_bwd_workspace_bytes(int64_t rows, int64_t cols);
+f8_status f8_act_bwd(const void *dy, const void *z, f8_act act, int64_t rows, int64_t cols, void *dz,
+                     void *dbias, f8_dtype bias_type, float *amax_out, void *workspace,
+                     size_t workspace_bytes, void *stream);
+
+/*
+ * Rotary positions.  Column pair i of a head (0 <= i < rot / 2) turns by the angle
+ * t_i = position * freqs[i]:
+ *   (x1, x2) -> scale * (x1 cos t - x2 sin t,  x2 cos t + x1 sin t)
+ * F8_ROPE_HALF pairs the columns i and i + rot / 2, F8_ROPE_INTERLEAVED 2i and
+ * 2i + 1.  Columns rot .. dim are copied.  `inverse` turns by -t: with the same
+ * scale it is the gradient of the call.
+ */
+typedef enum { F8_ROPE_HALF = 0, F8_ROPE_INTERLEAVED = 1 } f8_rope_layout;
+
+/*
+ * One tensor of f8_rope, [batch, seq, heads, dim] with its columns dense and any
+ * strides (in elements) of the batch, the sequence and the heads; `out` has strides
+ * of its own.  out may be x with x's strides; it may not overlap x otherwise.
+ */
+typedef struct {
+    const void *x;
+    void *out;
+    int64_t heads;
+    int64_t x_batch, x_seq, x_head;
+    int64_t out_batch, out_seq, out_head;
+} f8_rope_tensor;
+
+/*
+ * Rotates `count` (1 or 2) tensors, usually queries and keys, in one launch.
+ *   type:      element type of all tensors.
+ *   positions: device int64, that of row (b, s) at positions[b * pos_batch + s *
+ *              pos_seq] (pos_batch 0: one list for the batch).  A row of a negative
+ *              position is padding and is copied as it is.
+ *   freqs:     device fp64 [rot / 2], radians a position.  Angles are formed as
+ *              64-bit fractions of a turn, so a far position loses nothing beyond
+ *              freqs' own rounding.
+ *   rot:       even, 2 <= rot <= dim;  dim <= 1024;  scale finite.
+ * x, out aligned to their elements, freqs and positions to 8 bytes.  Rows of whole
+ * 16-byte vectors on 16-byte boundaries (with rot / 2 a multiple of a vector's
+ * elements) move in vectors, others in smaller pieces.
+ */
+f8_status f8_rope(const f8_rope_tensor *tensors, int count, f8_dtype type, int64_t batch,
+                  int64_t seq, int64_t dim, int64_t rot, f8_rope_layout layout,
+                  const int64_t *positions, int64_t pos_batch, int64_t pos_seq, const double *freqs,
+                  float scale, int inverse, void *stream);
+
+/*
+ * The frequencies of f8_rope for a head of `rot` rotated columns, on the HOST:
+ * f_i = base^(-2 i / rot), for contexts of `factor` times the `original` length
+ * that a model was trained at:
+ *   F8_ROPE_PLAIN    f_i
+ *   F8_ROPE_LINEAR   f_i / factor
+ *   F8_ROPE_BASE     the base raised so that the slowest pair is slowed down by
+ *                    factor: base factor^(rot / (rot - 2))  (rot > 2)
+ *   F8_ROPE_BY_PARTS pairs of at least `fast` turns in `original` positions keep f_i,
+ *                    those of at most `slow` get f_i / factor, with a ramp linear in
+ *                    the turns between
+ *   freqs: host fp64 [rot / 2].  `original`, `slow` and `fast` (0 <= slow < fast) are
+ *   used by F8_ROPE_BY_PARTS only.
+ */
+typedef enum {
+    F8_ROPE_PLAIN = 0,
+    F8_ROPE_LINEAR = 1,
+    F8_ROPE_BASE = 2,
+    F8_ROPE_BY_PARTS = 3
+} f8_rope_scaling;
+f8_status f8_rope_frequencies(int64_t rot, double base, f8_rope_scaling scaling, double factor,
+                              double original, double slow, double fast, double *freqs);
+
+/*
+ * The residual stream between two blocks: a block's output a, normed, gated and
+ * added, and the norm in front of the next block, in one pass:
+ *   u  = norm(a; w_post, b_post)       (u = a without w_post)
+ *   r' = scale r + gate[row / gate_rows] u     (no gate: scale r + u)
+ *   y  = norm(r'; w_pre, b_pre)        of r' before its rounding
+ * with the norms of f8_norm, both of one kind.
+ *   a, y:   device [rows, cols] of type x_type;  r, r_out: of type r_type, which is
+ *           x_type or F8_F32.  r_out may be r, and y may be a.
+ *   w_pre, b_pre, w_post, b_post: device [cols] of type w_type; w_post and the
+ *           biases may be NULL (b_post needs w_post).
+ *   gate:   device [ceil(rows / gate_rows), cols] of type gate_type, or NULL: one
+ *           row for each gate_rows >= 1 consecutive rows (gate_rows >= rows: one
+ *           gate for all).
+ *   stats:  device fp32 [4, rows] receiving what the backward pass needs: mean and
+ *           1/deviation of a, mean and 1/deviation of r' (rows of a norm that is not
+ *           there, and means of F8_RMS_NORM, are left as they were).
+ *   amax_out: device fp32 receiving max |y| as stored, ready for f8_cast_transpose,
+ *           or NULL; needs x_type F8_BF16; zeroed by the call.  A non-finite y then
+ *           sets F8_ERR_NONFINITE.
+ * rows, cols >= 0; cols < 2^30, rows * cols < 2^60; eps >= 0; scale finite.  All
+ * tensors 16-byte aligned, stats and amax_out 4-byte.
+ */
+typedef struct {
+    f8_norm kind;
+    f8_dtype x_type, r_type, w_type, gate_type;
+    int64_t rows, cols, gate_rows;
+    float eps, scale;
+    const void *w_pre, *b_pre, *w_post, *b_post, *gate;
+} f8_residual_norm;
+
+f8_status f8_residual_norm_fwd(const f8_residual_norm *n, const void *a, const void *r, void *r_out,
+                               void *y, float *stats, float *amax_out, void *stream);
+
+/*
+ * Backward, for the gradients dy of y and dr_out of r_out (NULL: zero), from the
+ * forward's a, r_out and stats.  With e2 = (r' - mu2) s2, e1 = (a - mu1) s1:
+ *   D   = dr_out + s2 (dy w_pre - mean(dy w_pre) - e2 mean(dy w_pre e2))
+ *   dr  = scale D;   dgate = sum over the gate's rows of D u;   du = gate D
+ *   da  = s1 (du w_post - mean(du w_post) - e1 mean(du w_post e1))   (du without w_post)
+ *   dw_pre = sum dy e2, db_pre = sum dy, dw_post = sum du e1, db_post = sum du
+ * (means over the row, without mean(dy w_pre) and mean(du w_post) for F8_RMS_NORM).
+ *   dy, a, da: of x_type;  dr_out, r_out, dr: of r_type;  dw_*, db_*: [cols] of
+ *   w_type;  dgate: as gate.  Every output may be NULL (dw_post, db_post only
+ *   without w_post, dgate only without gate).  No output may be an input.
+ *   workspace: f8_residual_norm_bwd_workspace_bytes(rows, cols) bytes, 16-byte
+ *   aligned.
+ * Sums over rows are formed in a fixed order: equal inputs give equal bits.
+ */
+typedef struct {
+    void *da, *dr, *dw_pre, *db_pre, *dw_post, *db_post, *dgate;
+} f8_residual_norm_grads;
+
+size_t f8_residual_norm_bwd_workspace_bytes(int64_t rows, int64_t cols);
+f8_status f8_residual_norm_bwd(const f8_residual_norm *n, const void *dy, const void *dr_out,
+                               const void *a, const void *r_out, const float *stats,
+                               const f8_residual_norm_grads *grads, void *workspace,
+                               size_t workspace_bytes, void *stream);
+
+/*
  * Number of kernels this library has launched (enqueued) in this process so
  * far, over all devices and streams; host-side, no synchronisation.  The
  * difference across a sequence of calls is the number of GPU kernels those
