@@ -131,6 +131,8 @@ _lib = None
 def lib() -> ctypes.CDLL:
     """The loaded libf8 (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib

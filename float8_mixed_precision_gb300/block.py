@@ -13,17 +13,51 @@ import torch
 
 from . import binding, ops
 from .binding import F8_LAYER_NORM, F8_RMS_NORM, _empty
-from .ops import _bytes, _call, _dtype, _ptr, _scalar
+from .ops import _DTYPES, _call, _dtype
+
+_BF16, _F32, _U8 = torch.bfloat16, torch.float32, torch.uint8
+
+
+def _arg(what: str, name: str, t: torch.Tensor | None, dtype, shape: tuple, index: int):
+    """ops._ptr for a call whose first tensor is on device `index`.  These calls take
+    up to ten tensors while a decoding step's kernel runs for a few microseconds, so
+    what holds is found in one expression and what does not by ops._ptr."""
+    if t is None:
+        return None
+    if t.dtype is dtype and t.shape == shape and t.get_device() == index and t.is_contiguous():
+        return t.data_ptr()
+    return ops._ptr(what, name, t, dtype, shape, torch.device("cuda", index) if index >= 0 else torch.device("cpu"))
+
+
+def _one(what: str, name: str, t: torch.Tensor | None, index: int):
+    """The pointer of one fp32 value (None if not given)."""
+    if t is None:
+        return None
+    if t.dtype is not _F32 or t.numel() != 1:
+        raise TypeError(f"{what}: {name} must be one float32 value")
+    if t.get_device() != index:
+        raise ValueError(f"{what}: tensors on different devices")
+    return t.data_ptr()
+
+
+def _typed(what: str, name: str, t: torch.Tensor | None, shape: tuple, index: int):
+    """The pointer and type of a bf16 or fp32 tensor (None and bf16 if not given)."""
+    if t is None:
+        return None, binding.F8_BF16
+    return _arg(what, name, t, t.dtype, shape, index), _dtype(what, t)
+
+
+def _ws(what: str, ws: torch.Tensor | None, nbytes: int, like: torch.Tensor, stream):
+    """The pointer and size of the workspace, which is allocated if none is given."""
+    if ws is None:
+        if nbytes == 0:
+            return None, None, 0
+        ws = _empty(nbytes, _U8, like.device, stream)
+    n = ws.numel()
+    return ws, _arg(what, "ws", ws, _U8, (n,), like.get_device()), n
 
 
 # ---------------------------------------------------------------- epilogues
-def _bias(what: str, bias: torch.Tensor | None, cols: int, dev):
-    """The pointer and type of a bias [cols], bf16 or fp32."""
-    if bias is None:
-        return None, binding.F8_BF16
-    return _ptr(what, "bias", bias, bias.dtype, (cols,), dev), _dtype(what, bias)
-
-
 def f8_gemm_act(a: torch.Tensor, b: torch.Tensor, scale_a: torch.Tensor, scale_b: torch.Tensor,
                 bias: torch.Tensor | None = None, act: int = binding.F8_ACT_NONE,
                 residual: torch.Tensor | None = None, y: torch.Tensor | None = None,
@@ -34,20 +68,19 @@ def f8_gemm_act(a: torch.Tensor, b: torch.Tensor, scale_a: torch.Tensor, scale_b
     scale_b) + bias, y = act(z) + residual, both bf16 [M, N]; z None unless given
     or wanted.  A [M, K] and B [N, K] are uint8 codes, the bias bf16 or fp32."""
     what = "f8_gemm_act"
-    binding._need(what, torch.uint8, a, b)
-    M, K = a.shape
-    N, dev = b.shape[0], a.device
-    if b.shape[1] != K:
+    binding._need(what, _U8, a, b)
+    (M, K), (N, K2), at = a.shape, b.shape, a.get_device()
+    if K2 != K:
         raise ValueError(f"{what}: a and b must have the same K")
-    y = _empty((M, N), torch.bfloat16, dev, stream) if y is None else y
+    shape = (M, N)
+    y = _empty(shape, _BF16, a.device, stream) if y is None else y
     if z is None and want_z:
-        z = _empty((M, N), torch.bfloat16, dev, stream)
-    bf = torch.bfloat16
-    _call(what, stream, binding._ptr(a), int(fmt_a), _ptr(what, "b", b, torch.uint8, (N, K), dev),
-          int(fmt_b), M, N, K, _scalar(what, scale_a, dev, "scale_a"),
-          _scalar(what, scale_b, dev, "scale_b"), *_bias(what, bias, N, dev), int(act),
-          _ptr(what, "residual", residual, bf, (M, N), dev), _ptr(what, "y", y, bf, (M, N), dev),
-          _ptr(what, "z", z, bf, (M, N), dev), _scalar(what, amax_out, dev))
+        z = _empty(shape, _BF16, a.device, stream)
+    bias_p, bias_t = _typed(what, "bias", bias, (N,), at)
+    _call(what, stream, binding._ptr(a), fmt_a, _arg(what, "b", b, _U8, (N, K), at), fmt_b, M, N, K,
+          _one(what, "scale_a", scale_a, at), _one(what, "scale_b", scale_b, at), bias_p, bias_t, act,
+          _arg(what, "residual", residual, _BF16, shape, at), _arg(what, "y", y, _BF16, shape, at),
+          _arg(what, "z", z, _BF16, shape, at), _one(what, "amax_out", amax_out, at))
     return y, z
 
 
@@ -62,51 +95,43 @@ def f8_act_bwd(dy: torch.Tensor, z: torch.Tensor | None, act: int, dz: torch.Ten
     """(dz, dbias) of f8_gemm_act's epilogue for the gradient dy [rows, cols] of y
     and the z it kept: dz = dy act'(z), dbias its column sums, of `bias_dtype`."""
     what = "f8_act_bwd"
-    binding._need(what, torch.bfloat16, dy)
+    binding._need(what, _BF16, dy)
     rows, cols = shape = dy.shape
-    dev = dy.device
-    dz = _empty(shape, torch.bfloat16, dev, stream) if dz is None and want_dz else dz
-    dbias = _empty(cols, bias_dtype, dev, stream) if dbias is None and want_dbias else dbias
-    bf = torch.bfloat16
-    args = (binding._ptr(dy), _ptr(what, "z", z, bf, shape, dev), int(act), rows, cols,
-            _ptr(what, "dz", dz, bf, shape, dev), *_bias(what, dbias, cols, dev),
-            _scalar(what, amax_out, dev))
-    if ws is None and dbias is not None:
-        ws = _empty(max(f8_act_bwd_workspace_bytes(rows, cols), 1), torch.uint8, dev, stream)
-    _call(what, stream, *args, *_bytes(what, ws, dev))
+    at = dy.get_device()
+    dz = _empty(shape, _BF16, dy.device, stream) if dz is None and want_dz else dz
+    dbias = _empty(cols, bias_dtype, dy.device, stream) if dbias is None and want_dbias else dbias
+    dbias_p, dbias_t = _typed(what, "dbias", dbias, (cols,), at)
+    args = (binding._ptr(dy), _arg(what, "z", z, _BF16, shape, at), act, rows, cols,
+            _arg(what, "dz", dz, _BF16, shape, at), dbias_p, dbias_t, _one(what, "amax_out", amax_out, at))
+    need = f8_act_bwd_workspace_bytes(rows, cols) if ws is None and dbias is not None else 0
+    ws, *space = _ws(what, ws, need, dy, stream)
+    _call(what, stream, *args, *space)
     return dz, dbias
 
 
 # ---------------------------------------------------------------- rotary positions
-def _heads(what: str, name: str, t: torch.Tensor, like: torch.Tensor | None = None) -> tuple:
-    """(batch, seq, heads, dim) and the strides of the first three, of a tensor
-    [tokens, heads, dim] or [batch, seq, heads, dim] with dense columns."""
-    if like is not None:
-        if t.dtype != like.dtype:
-            raise TypeError(f"{what}: {name} must be {str(like.dtype).replace('torch.', '')}")
-        if t.device != like.device:
-            raise ValueError(f"{what}: tensors on different devices")
-        if t.dim() != like.dim():
-            raise ValueError(f"{what}: {name} must have as many dimensions as q")
+_ONE, _TWO = binding._RopeTensor * 1, binding._RopeTensor * 2
+
+
+def _heads(what: str, name: str, t: torch.Tensor, lead: tuple | None, dtype, index: int):
+    """(pointer, shape, strides) of a tensor [tokens, heads, dim] or [batch, seq,
+    heads, dim] with dense columns, as four of each; `lead` is what q has in front of
+    the heads."""
     shape, stride = t.shape, t.stride()
-    if len(shape) == 3:
-        shape, stride = (1, *shape), (0, *stride)
-    elif len(shape) != 4:
-        raise ValueError(f"{what}: {name} must be [tokens, heads, dim] or [batch, seq, heads, dim]")
-    if shape[3] > 1 and stride[3] != 1:
+    if t.dtype is not dtype:
+        raise TypeError(f"{what}: {name} must be {str(dtype).replace('torch.', '')}")
+    if t.get_device() != index:
+        raise ValueError(f"{what}: tensors on different devices")
+    n = len(shape)
+    if n != 3 and n != 4 or lead is not None and n != len(lead) + 2:
+        raise ValueError(f"{what}: {name} must be [tokens, heads, dim] or [batch, seq, heads, dim], as q is")
+    if lead is not None and shape[:-2] != lead:
+        raise ValueError(f"{what}: q, k and the outputs must agree in all but the heads")
+    if stride[-1] != 1 and shape[-1] > 1:
         raise ValueError(f"{what}: the columns of {name} must be contiguous")
-    return shape, stride
-
-
-def _rope_tensor(what: str, name: str, x: torch.Tensor, out: torch.Tensor | None, like, stream):
-    """The C struct of a tensor and its output, the output, and the shape."""
-    shape, sx = _heads(what, name, x, like)
-    if out is None:
-        out = _empty(x.shape, x.dtype, x.device, stream)
-    elif out.shape != x.shape:
-        raise ValueError(f"{what}: {name}_out must have the shape of {name}")
-    _, so = _heads(what, name + "_out", out, x)
-    return (x.data_ptr(), out.data_ptr(), shape[2], sx[0], sx[1], sx[2], so[0], so[1], so[2]), out, shape
+    if n == 3:
+        return t.data_ptr(), (1, *shape), (0, *stride)
+    return t.data_ptr(), shape, stride
 
 
 def f8_rope(q: torch.Tensor, positions: torch.Tensor, freqs: torch.Tensor,
@@ -120,33 +145,43 @@ def f8_rope(q: torch.Tensor, positions: torch.Tensor, freqs: torch.Tensor,
     (f8_rope_frequencies).  q_out may be q, and k_out k.  `inverse` turns back: the
     gradient of the call."""
     what = "f8_rope"
-    kind = _dtype(what, q)
+    kind, dtype, at = _dtype(what, q), q.dtype, q.get_device()
     if not ops._on_device(q):
         raise ValueError("libf8 takes device tensors only")
-    dev = q.device
-    first, q_out, (batch, seq, _, dim) = _rope_tensor(what, "q", q, q_out, None, stream)
-    if k is None:
-        tensors = (binding._RopeTensor * 1)(first)
-    else:
-        second, k_out, (b2, s2, _, d2) = _rope_tensor(what, "k", k, k_out, q, stream)
-        if b2 != batch or s2 != seq or d2 != dim:
-            raise ValueError(f"{what}: q and k must agree in all but the heads")
-        tensors = (binding._RopeTensor * 2)(first, second)
-    if positions.dtype != torch.int64:
-        raise TypeError(f"{what}: positions must be int64")
     lead = q.shape[:-2]
+    q_out = _empty(q.shape, dtype, q.device, stream) if q_out is None else q_out
+    qp, (batch, seq, heads, dim), sq = _heads(what, "q", q, None, dtype, at)
+    if q_out.shape != q.shape:
+        raise ValueError(f"{what}: q_out must have the shape of q")
+    op, _, so = _heads(what, "q_out", q_out, lead, dtype, at)
+    first = (qp, op, heads, sq[0], sq[1], sq[2], so[0], so[1], so[2])
+    if k is None:
+        k_out = None
+        tensors = _ONE(first)
+    else:
+        kp, (_, _, heads, dim_k), sk = _heads(what, "k", k, lead, dtype, at)
+        if dim_k != dim:
+            raise ValueError(f"{what}: q and k must agree in all but the heads")
+        k_out = _empty(k.shape, dtype, k.device, stream) if k_out is None else k_out
+        if k_out.shape != k.shape:
+            raise ValueError(f"{what}: k_out must have the shape of k")
+        op, _, so = _heads(what, "k_out", k_out, lead, dtype, at)
+        tensors = _TWO(first, (kp, op, heads, sk[0], sk[1], sk[2], so[0], so[1], so[2]))
+    if positions.dtype is not torch.int64:
+        raise TypeError(f"{what}: positions must be int64")
     if positions.shape == lead:
-        pb, ps = (0, positions.stride(0)) if len(lead) == 1 else positions.stride()
+        steps = positions.stride()
+        pb, ps = steps if len(steps) == 2 else (0, steps[0])
     elif positions.dim() == 1 and positions.shape[0] == seq:
         pb, ps = 0, positions.stride(0)
     else:
         raise ValueError(f"{what}: positions must have q's leading shape, or be [seq]")
-    if positions.device != dev or freqs.device != dev:
+    if positions.get_device() != at or freqs.get_device() != at:
         raise ValueError(f"{what}: tensors on different devices")
-    if freqs.dtype != torch.float64 or freqs.dim() != 1 or not freqs.is_contiguous():
+    if freqs.dtype is not torch.float64 or freqs.dim() != 1 or not freqs.is_contiguous():
         raise TypeError(f"{what}: freqs must be a contiguous 1-D float64 tensor")
-    _call(what, stream, tensors, len(tensors), kind, batch, seq, dim, 2 * freqs.shape[0], int(layout),
-          positions.data_ptr(), pb, ps, freqs.data_ptr(), float(scale), int(bool(inverse)))
+    _call(what, stream, tensors, len(tensors), kind, batch, seq, dim, 2 * freqs.shape[0], layout,
+          positions.data_ptr(), pb, ps, freqs.data_ptr(), scale, 1 if inverse else 0)
     return q_out, k_out
 
 
@@ -164,29 +199,27 @@ def f8_rope_frequencies(rot: int, base: float = 10000.0, scaling: int = binding.
 
 # ---------------------------------------------------------------- residual stream
 def _residual_norm(what: str, a, r, w_pre, b_pre, w_post, b_post, gate, gate_rows, scale, kind, eps):
-    """The C struct of the call; a and r are checked here, b's and w's types too."""
+    """The C struct of the call; a's and r's shapes are the caller's to check."""
     if a.dim() != 2:
         raise TypeError(f"{what} takes 2-D tensors")
     rows, cols = a.shape
-    dev, shape = a.device, (cols,)
-    xt, rt, wt = _dtype(what, a), _dtype(what, r), _dtype(what, w_pre)
+    at, shape, wt = a.get_device(), (cols,), w_pre.dtype
     gt, gp = binding.F8_BF16, None
     if gate is not None:
-        gate_rows = rows if gate_rows is None else int(gate_rows)
-        if gate_rows < 1 and rows > 0:
+        gate_rows = max(rows, 1) if gate_rows is None else int(gate_rows)
+        if gate_rows < 1:
             raise ValueError(f"{what}: gate_rows must be at least 1")
-        groups = -(-rows // max(gate_rows, 1))
-        gt = _dtype(what, gate)
-        if gate.dim() == 1 and groups <= 1:  # one gate for all rows
-            gp = _ptr(what, "gate", gate, gate.dtype, shape, dev)
-        else:
-            gp = _ptr(what, "gate", gate, gate.dtype, (groups, cols), dev)
-    return binding._ResidualNorm(
-        int(kind), xt, rt, wt, gt, rows, cols, max(int(gate_rows or 1), 1), float(eps), float(scale),
-        _ptr(what, "w_pre", w_pre, w_pre.dtype, shape, dev),
-        _ptr(what, "b_pre", b_pre, w_pre.dtype, shape, dev),
-        _ptr(what, "w_post", w_post, w_pre.dtype, shape, dev),
-        _ptr(what, "b_post", b_post, w_pre.dtype, shape, dev), gp)
+        whole = gate.dim() == 1 and rows <= gate_rows  # one gate for all rows
+        gp, gt = _typed(what, "gate", gate, shape if whole else (-(-rows // gate_rows), cols), at)
+    try:
+        types = _DTYPES[a.dtype], _DTYPES[r.dtype], _DTYPES[wt]
+    except KeyError:
+        raise TypeError(f"{what} takes bfloat16 or float32 tensors") from None
+    return binding._ResidualNorm(kind, *types, gt, rows, cols, gate_rows or 1, eps, scale,
+                                 _arg(what, "w_pre", w_pre, wt, shape, at),
+                                 _arg(what, "b_pre", b_pre, wt, shape, at),
+                                 _arg(what, "w_post", w_post, wt, shape, at),
+                                 _arg(what, "b_post", b_post, wt, shape, at), gp)
 
 
 def f8_residual_norm_fwd(a: torch.Tensor, r: torch.Tensor, w_pre: torch.Tensor,
@@ -203,14 +236,20 @@ def f8_residual_norm_fwd(a: torch.Tensor, r: torch.Tensor, w_pre: torch.Tensor,
     all).  r may be fp32 beside a bf16 a.  stats fp32 [4, rows] is the backward's."""
     what = "f8_residual_norm_fwd"
     n = _residual_norm(what, a, r, w_pre, b_pre, w_post, b_post, gate, gate_rows, scale, kind, eps)
-    shape, dev = a.shape, a.device
-    r_out = _empty(shape, r.dtype, dev, stream) if r_out is None else r_out
-    y = _empty(shape, a.dtype, dev, stream) if y is None else y
-    stats = _empty((4, shape[0]), torch.float32, dev, stream) if stats is None else stats
-    _call(what, stream, ctypes.byref(n), binding._ptr(a), _ptr(what, "r", r, r.dtype, shape, dev),
-          _ptr(what, "r_out", r_out, r.dtype, shape, dev), _ptr(what, "y", y, a.dtype, shape, dev),
-          _ptr(what, "stats", stats, torch.float32, (4, shape[0]), dev), _scalar(what, amax_out, dev))
+    shape, at, xt, rt = a.shape, a.get_device(), a.dtype, r.dtype
+    r_out = _empty(shape, rt, a.device, stream) if r_out is None else r_out
+    y = _empty(shape, xt, a.device, stream) if y is None else y
+    stats = _empty((4, shape[0]), _F32, a.device, stream) if stats is None else stats
+    _call(what, stream, ctypes.byref(n), binding._ptr(a), _arg(what, "r", r, rt, shape, at),
+          _arg(what, "r_out", r_out, rt, shape, at), _arg(what, "y", y, xt, shape, at),
+          _arg(what, "stats", stats, _F32, (4, shape[0]), at), _one(what, "amax_out", amax_out, at))
     return r_out, y, stats
+
+
+# the gradients formed by default: (layer norm, w_post given, gate given)
+_WANT = {(layer, post, gated): frozenset(
+    ["da", "dr", "dw_pre"] + ["db_pre"] * layer + ["dw_post"] * post + ["db_post"] * (layer and post) + ["dgate"] * gated)
+    for layer in (False, True) for post in (False, True) for gated in (False, True)}
 
 
 def f8_residual_norm_bwd_workspace_bytes(rows: int, cols: int) -> int:
@@ -233,33 +272,22 @@ def f8_residual_norm_bwd(dy: torch.Tensor, dr_out: torch.Tensor | None, a: torch
     F8_LAYER_NORM); the others are None."""
     what = "f8_residual_norm_bwd"
     n = _residual_norm(what, a, r_out, w_pre, None, w_post, b_post, gate, gate_rows, scale, kind, 0.0)
-    shape, dev = a.shape, a.device
-    cols = (shape[1],)
-    like = {"da": (da, shape, a.dtype), "dr": (dr, shape, r_out.dtype),
-            "dw_pre": (dw_pre, cols, w_pre.dtype), "db_pre": (db_pre, cols, w_pre.dtype),
-            "dw_post": (dw_post, cols, w_pre.dtype), "db_post": (db_post, cols, w_pre.dtype),
-            "dgate": (dgate, gate.shape if gate is not None else cols,
-                      gate.dtype if gate is not None else w_pre.dtype)}
+    shape, at, xt, rt, wt = a.shape, a.get_device(), a.dtype, r_out.dtype, w_pre.dtype
+    cols = shape[1:]
     if want is None:
-        want = {"da", "dr", "dw_pre"}
-        if kind == F8_LAYER_NORM:
-            want.add("db_pre")
-        if w_post is not None:
-            want |= {"dw_post", "db_post"} if kind == F8_LAYER_NORM else {"dw_post"}
-        if gate is not None:
-            want.add("dgate")
+        want = _WANT[kind == F8_LAYER_NORM, w_post is not None, gate is not None]
     out, ptrs = [], []
-    for name, (t, size, dtype) in like.items():
+    for name, t, size, dtype in (("da", da, shape, xt), ("dr", dr, shape, rt), ("dw_pre", dw_pre, cols, wt),
+                                 ("db_pre", db_pre, cols, wt), ("dw_post", dw_post, cols, wt),
+                                 ("db_post", db_post, cols, wt),
+                                 ("dgate", dgate, *((cols, wt) if gate is None else (gate.shape, gate.dtype)))):
         if t is None and name in want:
-            t = _empty(size, dtype, dev, stream)
+            t = _empty(size, dtype, a.device, stream)
         out.append(t)
-        ptrs.append(_ptr(what, name, t, dtype, size, dev))
-    grads = binding._ResidualNormGrads(*ptrs)
-    if ws is None:
-        ws = _empty(max(f8_residual_norm_bwd_workspace_bytes(*shape), 1), torch.uint8, dev, stream)
-    _call(what, stream, ctypes.byref(n), _ptr(what, "dy", dy, a.dtype, shape, dev),
-          _ptr(what, "dr_out", dr_out, r_out.dtype, shape, dev), binding._ptr(a),
-          _ptr(what, "r_out", r_out, r_out.dtype, shape, dev),
-          _ptr(what, "stats", stats, torch.float32, (4, shape[0]), dev), ctypes.byref(grads),
-          *_bytes(what, ws, dev))
+        ptrs.append(_arg(what, name, t, dtype, size, at))
+    ws, *space = _ws(what, ws, f8_residual_norm_bwd_workspace_bytes(*shape) if ws is None else 0, a, stream)
+    _call(what, stream, ctypes.byref(n), _arg(what, "dy", dy, xt, shape, at),
+          _arg(what, "dr_out", dr_out, rt, shape, at), binding._ptr(a), _arg(what, "r_out", r_out, rt, shape, at),
+          _arg(what, "stats", stats, _F32, (4, shape[0]), at), ctypes.byref(binding._ResidualNormGrads(*ptrs)),
+          *space)
     return tuple(out)

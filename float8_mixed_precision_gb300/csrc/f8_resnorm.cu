@@ -19,9 +19,11 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <mutex>
 
 #include "f8_internal.h"
 #include "f8_ptx.cuh"
+#include "f8_resnorm_rows.cuh"
 
 namespace f8 {
 namespace {
@@ -261,6 +263,169 @@ bwd_walk_kernel(const Call c, const TA *__restrict__ dy, const TR *__restrict__ 
     }
 }
 
+// ------------------------------------------------------------ rows in registers
+// A block keeps its row, or its slice of a row that a cluster shares, in registers,
+// and rows come some ahead through shared memory.
+using rows::kE;
+constexpr int kP = kE / 2;
+
+__device__ __forceinline__ float2 splat(float v) { return make_float2(v, v); }
+
+__device__ __forceinline__ rows::Slice slice_of(int64_t cols, uint32_t rank, uint32_t ranks)
+{
+    // slices of whole 16-byte vectors, the last one perhaps shorter
+    const int per = static_cast<int>((cols + kE * ranks - 1) / (kE * ranks)) * kE;
+    rows::Slice s;
+    s.first = per * static_cast<int>(rank);
+    s.n = max(0, min(per, static_cast<int>(cols) - s.first));
+    return s;
+}
+
+// (sum, sum of squared differences to their mean) / cols, over the row, of the
+// columns that there are: mean (0 without `layer`) and 1/deviation.
+template <bool VEC>
+__device__ __forceinline__ void row_stats(float2 (&x)[kP], int n, bool layer, float inv_c, float eps,
+                                          rows::ClusterSum &sum, float &mu, float &rstd)
+{
+    mu = 0.0f;
+    if (layer) {
+        const float2 s = __fadd2_rn(__fadd2_rn(x[0], x[1]), __fadd2_rn(x[2], x[3]));
+        mu = sum(s.x + s.y, 0.0f).x * inv_c;
+    }
+    float2 q = splat(0.0f);
+#pragma unroll
+    for (int i = 0; i < kP; ++i) {
+        x[i] = __fadd2_rn(x[i], splat(-mu));
+        if (VEC) {
+            if (kE * static_cast<int>(threadIdx.x) < n)
+                q = __ffma2_rn(x[i], x[i], q);
+        } else {
+            const int c = threadIdx.x + 2 * i * blockDim.x;
+            if (c < n)
+                q.x = fmaf(x[i].x, x[i].x, q.x);
+            if (c + static_cast<int>(blockDim.x) < n)
+                q.y = fmaf(x[i].y, x[i].y, q.y);
+        }
+    }
+    rstd = 1.0f / sqrtf(sum(q.x + q.y, 0.0f).x * inv_c + eps);
+}
+
+template <typename TA, typename TR, bool VEC>
+__global__ void __launch_bounds__(1024, 1)
+fwd_kernel(const Call c, const TA *a, const TR *r, TR *r_out, TA *y, unsigned *amax, int ranks, int stages,
+           uint64_t limit_ns, unsigned *status)
+{
+    extern __shared__ __align__(16) uint8_t dyn[];
+    __shared__ float2 red[2 * rows::kMaxCluster * 32];
+    __shared__ __align__(8) uint64_t full[rows::kMaxStages];
+    __shared__ unsigned blk;
+    const uint32_t rank = ranks > 1 ? cluster_ctarank() : 0u;
+    const int64_t unit = blockIdx.x / ranks, units = gridDim.x / ranks;
+    const rows::Slice sl = slice_of(c.cols, rank, ranks);
+    const int64_t total = c.rows * c.cols;
+    rows::Slots<TA, 1, TR, 1> slots{dyn, full, stages, c.cols, total, sl, {a}, {r}, 0u, true};
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < stages; ++i)
+            mbar_init(&full[i], 1);
+        fence_mbar_init();
+        blk = 0u;
+    }
+    griddep_wait();
+    griddep_launch_dependents();
+    if (ranks > 1)
+        cluster_sync();  // a peer's part of a sum may come from here on
+    else
+        __syncthreads();
+    if (threadIdx.x == 0)
+        for (int i = 0; i < stages && unit + i * units < c.rows; ++i)
+            slots.fill(unit + i * units);
+    rows::ClusterSum sum{red, 0, rank, static_cast<uint32_t>(ranks)};
+    const float inv_c = 1.0f / static_cast<float>(c.cols);
+    uint32_t m2 = 0u, seq = 0u;
+    for (int64_t row = unit; row < c.rows; row += units, ++seq) {
+        slots.wait(seq, limit_ns, status);
+        int sa = 0, sr = 0;
+        if constexpr (!VEC) {
+            sa = rows::Window<TA>(slots.begin(row), sl.n, total).shift;
+            sr = rows::Window<TR>(slots.begin(row), sl.n, total).shift;
+            slots.tails(seq, row);
+        }
+        float2 x[kP], v[kP], p[kP];
+        const int slot = ring_slot(seq, stages);
+        rows::take<VEC, TA>(slots.at_a(slot, 0), sa, sl.n, x);
+        rows::take<VEC, TR>(slots.at_r(slot, 0), sr, sl.n, v);
+        float mu1 = 0.0f, s1 = 1.0f;
+        if (c.w_post != nullptr) {
+            row_stats<VEC>(x, sl.n, c.layer, inv_c, c.eps, sum, mu1, s1);
+            rows::take_param<VEC>(c.w_post, c.w_f32, sl.first, sl.n, 1.0f, p);
+#pragma unroll
+            for (int i = 0; i < kP; ++i)
+                x[i] = __fmul2_rn(__fmul2_rn(x[i], splat(s1)), p[i]);
+            if (c.b_post != nullptr) {
+                rows::take_param<VEC>(c.b_post, c.w_f32, sl.first, sl.n, 0.0f, p);
+#pragma unroll
+                for (int i = 0; i < kP; ++i)
+                    x[i] = __fadd2_rn(x[i], p[i]);
+            }
+        }
+        if (c.gate != nullptr) {
+            rows::take_param<VEC>(c.gate, c.g_f32, row / c.gate_rows * c.cols + sl.first, sl.n, 1.0f, p);
+#pragma unroll
+            for (int i = 0; i < kP; ++i)
+                x[i] = __fmul2_rn(x[i], p[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < kP; ++i) {
+            x[i] = __ffma2_rn(v[i], splat(c.scale), x[i]);
+            v[i] = x[i];
+        }
+        float mu2, s2;
+        row_stats<VEC>(x, sl.n, c.layer, inv_c, c.eps, sum, mu2, s2);
+        // every thread has taken its columns: the slot may be filled again
+        if (threadIdx.x == 0 && slots.ok && row + stages * units < c.rows)
+            slots.fill(row + stages * units);
+        const int64_t at = slots.begin(row);
+        const bool inside = in_range(at, sl.n, total, status);
+        rows::give<VEC>(r_out + at, sl.n, v, nullptr, inside);
+        rows::take_param<VEC>(c.w_pre, c.w_f32, sl.first, sl.n, 1.0f, p);
+#pragma unroll
+        for (int i = 0; i < kP; ++i)
+            x[i] = __fmul2_rn(__fmul2_rn(x[i], splat(s2)), p[i]);
+        if (c.b_pre != nullptr) {
+            rows::take_param<VEC>(c.b_pre, c.w_f32, sl.first, sl.n, 0.0f, p);
+#pragma unroll
+            for (int i = 0; i < kP; ++i)
+                x[i] = __fadd2_rn(x[i], p[i]);
+        }
+        rows::give<VEC>(y + at, sl.n, x, amax != nullptr ? &m2 : nullptr, inside);
+        if (threadIdx.x == 0 && rank == 0) {
+            if (c.w_post != nullptr) {
+                if (c.layer)
+                    c.stats[row] = mu1;
+                c.stats[c.rows + row] = s1;
+            }
+            if (c.layer)
+                c.stats[2 * c.rows + row] = mu2;
+            c.stats[3 * c.rows + row] = s2;
+        }
+    }
+    if (threadIdx.x == 0)
+        slots.drain();
+    if (amax != nullptr) {
+        const unsigned m = __reduce_max_sync(0xFFFFFFFFu, max(m2 & 0xFFFFu, m2 >> 16));
+        if ((threadIdx.x & 31) == 0)
+            atomicMax(&blk, m);
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            if (blk >= 0x7F80u)
+                atomicOr(status, kStatusNonfinite);
+            atomicMax(amax, blk << 16);  // the maximum does not depend on the order
+        }
+    }
+    if (ranks > 1)
+        cluster_sync();  // a peer may still write its part of a sum here
+}
+
 // ------------------------------------------------------------ sums over rows
 // The gates of a chunk of rows [first, stop): a gate's rows may reach into other
 // chunks only at the chunk's ends.
@@ -348,6 +513,186 @@ cols_walk_kernel(const Call c, const Chunks ch, const TA *__restrict__ dy, const
     p[3 * c.cols] = db1;
 }
 
+// The backward pass in one: a unit (a block, or a cluster by column slices) walks the
+// chunk `unit` of rows, with the column sums of all gradients in registers.  FULL:
+// with means or biases; without, the sums that only those need are left out.
+template <typename TA, typename TR, bool VEC, bool FULL>
+__global__ void __launch_bounds__(512, 1)
+bwd_kernel(const Call c, const Chunks ch, const TA *__restrict__ dy, const TR *__restrict__ dr_out,
+           const TA *__restrict__ a, const TR *__restrict__ r_out, TA *__restrict__ da,
+           TR *__restrict__ dr, float *__restrict__ parts, float *__restrict__ ends,
+           void *__restrict__ dgate, int ranks, int stages, uint64_t limit_ns, unsigned *status)
+{
+    extern __shared__ __align__(16) uint8_t dyn[];
+    __shared__ float2 red[2 * rows::kMaxCluster * 32];
+    __shared__ __align__(8) uint64_t full[rows::kMaxStages];
+    const uint32_t rank = ranks > 1 ? cluster_ctarank() : 0u;
+    const int64_t unit = blockIdx.x / ranks;
+    const rows::Slice sl = slice_of(c.cols, rank, ranks);
+    const int64_t total = c.rows * c.cols, first = ch.first(unit), stop = ch.stop(unit);
+    rows::Slots<TA, 2, TR, 2> slots{dyn, full, stages, c.cols, total, sl, {dy, a}, {dr_out, r_out}, 0u, true};
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < stages; ++i)
+            mbar_init(&full[i], 1);
+        fence_mbar_init();
+    }
+    griddep_wait();
+    griddep_launch_dependents();
+    if (ranks > 1)
+        cluster_sync();
+    else
+        __syncthreads();
+    if (threadIdx.x == 0)
+        for (int64_t i = 0; i < stages && first + i < stop; ++i)
+            slots.fill(first + i);
+    rows::ClusterSum sum{red, 0, rank, static_cast<uint32_t>(ranks)};
+    const float inv_c = 1.0f / static_cast<float>(c.cols);
+    const bool post = c.w_post != nullptr, gated = c.gate != nullptr, layer = FULL && c.layer;
+    float2 w2[kP], w1[kP], b1[kP], g[kP];
+    rows::take_param<VEC>(c.w_pre, c.w_f32, sl.first, sl.n, 1.0f, w2);
+    rows::take_param<VEC>(c.w_post, c.w_f32, sl.first, sl.n, 1.0f, w1);
+    if (FULL)
+        rows::take_param<VEC>(c.b_post, c.w_f32, sl.first, sl.n, 0.0f, b1);
+    float2 dw2[kP], db2[kP], dw1[kP], db1[kP], dg[kP];
+#pragma unroll
+    for (int i = 0; i < kP; ++i)
+        dw2[i] = db2[i] = dw1[i] = db1[i] = dg[i] = g[i] = splat(0.0f);
+    int64_t gate = 0, gate_end = gated ? first : stop;
+    if (!gated) {
+#pragma unroll
+        for (int i = 0; i < kP; ++i)
+            g[i] = splat(1.0f);
+    }
+    // what a gate's rows of this chunk have given, into place
+    auto flush = [&]() {
+        if (dgate == nullptr)
+            return;
+        if (ch.whole(gate, unit))
+            rows::give_param<VEC>(dgate, c.g_f32, gate * c.cols + sl.first, sl.n, dg);
+        else
+            rows::give<VEC>(ends + (unit * 2 + ch.slot(gate, unit)) * c.cols + sl.first, sl.n, dg, nullptr, true);
+#pragma unroll
+        for (int i = 0; i < kP; ++i)
+            dg[i] = splat(0.0f);
+    };
+    // the next row's statistics are on their way while a row is worked on
+    float n_mu1 = 0.0f, n_s1 = 1.0f, n_mu2 = 0.0f, n_s2 = 0.0f;
+    auto next_stats = [&](int64_t row) {
+        if (post) {
+            n_s1 = c.stats[c.rows + row];
+            if (layer)
+                n_mu1 = c.stats[row];
+        }
+        n_s2 = c.stats[3 * c.rows + row];
+        if (layer)
+            n_mu2 = c.stats[2 * c.rows + row];
+    };
+    if (first < stop)
+        next_stats(first);
+    uint32_t seq = 0u;
+    for (int64_t row = first; row < stop; ++row, ++seq) {
+        if (row == gate_end) {
+            if (row > first)
+                flush();
+            gate = ch.gate(row);
+            gate_end = min(stop, ch.gate_stop(gate));
+            rows::take_param<VEC>(c.gate, c.g_f32, gate * c.cols + sl.first, sl.n, 1.0f, g);
+        }
+        const float mu1 = n_mu1, s1 = n_s1, mu2 = n_mu2, s2 = n_s2;
+        if (row + 1 < stop)
+            next_stats(row + 1);
+        slots.wait(seq, limit_ns, status);
+        const int slot = ring_slot(seq, stages);
+        int sa = 0, sr = 0;
+        if constexpr (!VEC) {
+            sa = rows::Window<TA>(slots.begin(row), sl.n, total).shift;
+            sr = rows::Window<TR>(slots.begin(row), sl.n, total).shift;
+            slots.tails(seq, row);
+        }
+        float2 h[kP], e[kP];
+        rows::take<VEC, TA>(slots.at_a(slot, 0), sa, sl.n, h);
+        rows::take<VEC, TR>(slots.at_r(slot, 1), sr, sl.n, e);
+        float2 t1 = splat(0.0f), t2 = splat(0.0f);
+#pragma unroll
+        for (int i = 0; i < kP; ++i) {
+            e[i] = __fmul2_rn(__fadd2_rn(e[i], splat(-mu2)), splat(s2));
+            dw2[i] = __ffma2_rn(h[i], e[i], dw2[i]);
+            if (FULL)
+                db2[i] = __fadd2_rn(db2[i], h[i]);
+            h[i] = __fmul2_rn(h[i], w2[i]);
+            t1 = __ffma2_rn(h[i], e[i], t1);
+            if (FULL)
+                t2 = __fadd2_rn(t2, h[i]);
+        }
+        float2 k = sum(t1.x + t1.y, t2.x + t2.y);
+        // every thread is done with the row before: its slot may be filled again
+        if (threadIdx.x == 0 && slots.ok && seq > 0 && row - 1 + stages < stop)
+            slots.fill(row - 1 + stages);
+        const float k1 = -s2 * (k.x * inv_c), k2 = layer ? -s2 * (k.y * inv_c) : 0.0f;
+        // h becomes D
+        float2 o[kP];
+        if (dr_out != nullptr) {
+            rows::take<VEC, TR>(slots.at_r(slot, 0), sr, sl.n, o);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kP; ++i)
+                o[i] = splat(0.0f);
+        }
+#pragma unroll
+        for (int i = 0; i < kP; ++i)
+            h[i] = __fadd2_rn(o[i], __ffma2_rn(h[i], splat(s2), __ffma2_rn(e[i], splat(k1), splat(k2))));
+        rows::take<VEC, TA>(slots.at_a(slot, 1), sa, sl.n, e);
+        const int64_t at = slots.begin(row);
+        const bool inside = in_range(at, sl.n, total, status);
+        if (dr != nullptr) {
+#pragma unroll
+            for (int i = 0; i < kP; ++i)
+                o[i] = __fmul2_rn(h[i], splat(c.scale));
+            rows::give<VEC>(dr + at, sl.n, o, nullptr, inside);
+        }
+        // e becomes e1 (a without the norm), h du
+        t1 = t2 = splat(0.0f);
+#pragma unroll
+        for (int i = 0; i < kP; ++i) {
+            e[i] = __fmul2_rn(__fadd2_rn(e[i], splat(-mu1)), splat(s1));
+            float2 u = __fmul2_rn(e[i], w1[i]);
+            if (FULL)
+                u = __fadd2_rn(u, b1[i]);
+            dg[i] = __ffma2_rn(h[i], u, dg[i]);
+            h[i] = __fmul2_rn(h[i], g[i]);
+            dw1[i] = __ffma2_rn(h[i], e[i], dw1[i]);
+            if (FULL)
+                db1[i] = __fadd2_rn(db1[i], h[i]);
+            h[i] = __fmul2_rn(h[i], w1[i]);
+            t1 = __ffma2_rn(h[i], e[i], t1);
+            if (FULL)
+                t2 = __fadd2_rn(t2, h[i]);
+        }
+        if (post) {
+            k = sum(t1.x + t1.y, t2.x + t2.y);
+            const float d1 = -s1 * (k.x * inv_c), d2 = layer ? -s1 * (k.y * inv_c) : 0.0f;
+#pragma unroll
+            for (int i = 0; i < kP; ++i)
+                h[i] = __ffma2_rn(h[i], splat(s1), __ffma2_rn(e[i], splat(d1), splat(d2)));
+        }
+        if (da != nullptr)
+            rows::give<VEC>(da + at, sl.n, h, nullptr, inside);
+    }
+    if (gated && first < stop)
+        flush();
+    float *p = parts + unit * 4 * c.cols + sl.first;
+    rows::give<VEC>(p, sl.n, dw2, nullptr, true);
+    rows::give<VEC>(p + 2 * c.cols, sl.n, dw1, nullptr, true);
+    if (FULL) {
+        rows::give<VEC>(p + c.cols, sl.n, db2, nullptr, true);
+        rows::give<VEC>(p + 3 * c.cols, sl.n, db1, nullptr, true);
+    }
+    if (threadIdx.x == 0)
+        slots.drain();
+    if (ranks > 1)
+        cluster_sync();
+}
+
 // The parameters' gradients from the partial rows, in a fixed order: 32 columns a
 // block, 32 threads a column, each every 32nd row; blockIdx.y names the gradient.
 struct Sums {
@@ -411,6 +756,8 @@ gate_reduce_kernel(const float *__restrict__ ends, const Chunks ch, int64_t nchu
 
 // ------------------------------------------------------------ launches
 constexpr int kMaxChunks = 1024;
+constexpr int64_t kRegCols = 16384;  // a cluster's registers hold no more
+constexpr int kRingBytes = 200 * 1024;
 
 int64_t walk_chunks(int64_t rows, int64_t cols, int sms)
 {
@@ -419,21 +766,53 @@ int64_t walk_chunks(int64_t rows, int64_t cols, int sms)
                                                    kMaxChunks}));
 }
 
+// How rows are laid over the GPU: `ranks` blocks of `threads` to a row, `per_sm`
+// blocks an SM.
+struct Plan {
+    int ranks, threads, per_sm, slice;
+};
+
+Plan plan_of(int64_t cols, int max_threads, int sm_threads)
+{
+    Plan p;
+    p.ranks = 1;
+    while (p.ranks * max_threads * kE < cols)
+        p.ranks *= 2;
+    p.slice = static_cast<int>((cols + kE * p.ranks - 1) / (kE * p.ranks)) * kE;
+    p.threads = (p.slice / kE + 31) / 32 * 32;
+    p.per_sm = std::max(1, std::min(8, sm_threads / p.threads));
+    return p;
+}
+
+constexpr int kFwdThreads = 1024, kFwdSmThreads = 1024;
+constexpr int kBwdThreads = 512, kBwdSmThreads = 512;
+
+Plan fwd_plan(int64_t cols) { return plan_of(cols, kFwdThreads, kFwdSmThreads); }
+Plan bwd_plan(int64_t cols) { return plan_of(cols, kBwdThreads, kBwdSmThreads); }
+
+// Most units (blocks, or clusters) of the backward pass.
+int64_t bwd_units(int64_t rows, int64_t cols, int sms)
+{
+    const Plan p = bwd_plan(cols);
+    return std::max<int64_t>(1, std::min<int64_t>(rows, static_cast<int64_t>(sms) * p.per_sm / p.ranks));
+}
+
 size_t round256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
 
-// The backward pass's workspace: row constants, partial rows of the parameters'
-// gradients, and of the gates at the chunks' ends.
+// The backward pass's workspace: row constants (past kRegCols), partial rows of the
+// parameters' gradients, and of the gates at the chunks' ends.
 struct Workspace {
     size_t consts, parts, ends, bytes;
 };
 
 Workspace workspace_of(int64_t rows, int64_t cols, int sms)
 {
-    const size_t n = static_cast<size_t>(walk_chunks(rows, cols, sms));
+    const bool walk = cols > kRegCols;
+    const size_t n = static_cast<size_t>(walk ? walk_chunks(rows, cols, sms) : bwd_units(rows, cols, sms));
     const size_t row = static_cast<size_t>(cols) * sizeof(float);
     Workspace w;
     w.consts = 0;
-    w.parts = round256(2 * static_cast<size_t>(rows) * sizeof(float));
+    w.parts = walk ? round256(2 * static_cast<size_t>(rows) * sizeof(float)) : 0;
     w.ends = w.parts + round256(4 * n * row);
     w.bytes = w.ends + round256(2 * n * row);
     return w;
@@ -445,14 +824,106 @@ Call call_of(const f8_residual_norm &n, float *stats)
                 n.gate_rows, n.eps, n.scale, n.w_pre, n.b_pre, n.w_post, n.b_post, n.gate, stats};
 }
 
+// Units that run at once, and the slots of each: a launch of more would walk its
+// last chunks alone.
+struct Shape {
+    int units, stages;
+    size_t smem;
+};
+
+template <auto Kernel>
+cudaError_t shape_of(const Plan &p, int64_t rows, uint32_t slot_bytes, const DeviceInfo &dev, Shape *out)
+{
+    static std::once_flag once[64];
+    static cudaError_t err[64];
+    const int d = dev.ordinal & 63;
+    std::call_once(once[d], [&] {
+        err[d] = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
+    });
+    if (err[d] != cudaSuccess)
+        return err[d];
+    const int fit = kRingBytes / p.per_sm / static_cast<int>(slot_bytes);
+    out->stages = std::max(2, std::min(fit, rows::kMaxStages));
+    out->smem = static_cast<size_t>(out->stages) * slot_bytes;
+    int64_t units = static_cast<int64_t>(dev.sm_count) * p.per_sm / p.ranks;
+    if (p.ranks > 2) {
+        // clusters of more than a pair may leave SMs of a group over
+        static std::mutex mutex;
+        static int known[64][rows::kMaxCluster + 1];
+        std::lock_guard<std::mutex> lock(mutex);
+        int &n = known[d][p.ranks];
+        if (n == 0) {
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3(static_cast<unsigned>(units * p.ranks));
+            cfg.blockDim = dim3(static_cast<unsigned>(p.threads));
+            cfg.dynamicSmemBytes = out->smem;
+            cudaLaunchAttribute attr;
+            attr.id = cudaLaunchAttributeClusterDimension;
+            attr.val.clusterDim.x = static_cast<unsigned>(p.ranks);
+            attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+            cfg.attrs = &attr;
+            cfg.numAttrs = 1;
+            const cudaError_t e = cudaOccupancyMaxActiveClusters(&n, Kernel, &cfg);
+            if (e != cudaSuccess)
+                return e;
+            n = std::max(n, 1);
+        }
+        units = std::min<int64_t>(units, n);
+    }
+    out->units = static_cast<int>(std::max<int64_t>(1, std::min(units, rows)));
+    return cudaSuccess;
+}
+
+template <typename TA, typename TR, bool VEC>
+cudaError_t fwd_rows(const Call &c, const void *a, const void *r, void *r_out, void *y, unsigned *amax,
+                     const DeviceInfo &dev, cudaStream_t st)
+{
+    const Plan p = fwd_plan(c.cols);
+    Shape s;
+    const cudaError_t e = shape_of<fwd_kernel<TA, TR, VEC>>(
+        p, c.rows, rows::slice_pitch<TA>(p.slice) + rows::slice_pitch<TR>(p.slice), dev, &s);
+    if (e != cudaSuccess)
+        return e;
+    return launch_pdl_cluster(fwd_kernel<TA, TR, VEC>, dim3(static_cast<unsigned>(s.units * p.ranks)),
+                              dim3(static_cast<unsigned>(p.threads)), s.smem, st,
+                              static_cast<unsigned>(p.ranks), c, static_cast<const TA *>(a),
+                              static_cast<const TR *>(r), static_cast<TR *>(r_out), static_cast<TA *>(y),
+                              amax, p.ranks, s.stages, wait_limit_ns(), dev.status);
+}
+
 template <typename TA, typename TR>
 cudaError_t fwd(const Call &c, const void *a, const void *r, void *r_out, void *y, unsigned *amax,
                 const DeviceInfo &dev, cudaStream_t st)
 {
+    if (c.cols <= kRegCols)
+        return c.cols % kE == 0 ? fwd_rows<TA, TR, true>(c, a, r, r_out, y, amax, dev, st)
+                                : fwd_rows<TA, TR, false>(c, a, r, r_out, y, amax, dev, st);
     const int64_t grid = std::min<int64_t>(c.rows, 4 * dev.sm_count);
     return launch_pdl(fwd_walk_kernel<TA, TR>, dim3(static_cast<unsigned>(grid)), dim3(kWalkThreads), 0,
                       st, c, static_cast<const TA *>(a), static_cast<const TR *>(r),
                       static_cast<TR *>(r_out), static_cast<TA *>(y), amax, dev.status);
+}
+
+template <typename TA, typename TR, bool VEC, bool FULL>
+cudaError_t bwd_rows(const Call &c, Chunks &ch, const void *dy, const void *dr_out, const void *a,
+                     const void *r_out, const f8_residual_norm_grads &g, float *parts, float *ends,
+                     const DeviceInfo &dev, cudaStream_t st)
+{
+    const Plan p = bwd_plan(c.cols);
+    Shape s;
+    const cudaError_t e = shape_of<bwd_kernel<TA, TR, VEC, FULL>>(
+        p, c.rows, 2 * (rows::slice_pitch<TA>(p.slice) + rows::slice_pitch<TR>(p.slice)), dev, &s);
+    if (e != cudaSuccess)
+        return e;
+    ch.chunk = (c.rows + s.units - 1) / s.units;
+    const int64_t units = (c.rows + ch.chunk - 1) / ch.chunk;
+    return launch_pdl_cluster(bwd_kernel<TA, TR, VEC, FULL>, dim3(static_cast<unsigned>(units * p.ranks)),
+                              dim3(static_cast<unsigned>(p.threads)), s.smem, st,
+                              static_cast<unsigned>(p.ranks), c, ch, static_cast<const TA *>(dy),
+                              static_cast<const TR *>(dr_out), static_cast<const TA *>(a),
+                              static_cast<const TR *>(r_out), static_cast<TA *>(g.da),
+                              static_cast<TR *>(g.dr), parts, ends, g.dgate, p.ranks, s.stages,
+                              wait_limit_ns(), dev.status);
 }
 
 template <typename TA, typename TR>
@@ -462,26 +933,39 @@ cudaError_t bwd(const Call &c, const void *dy, const void *dr_out, const void *a
     const bool sums = g.dw_pre != nullptr || g.db_pre != nullptr || g.dw_post != nullptr ||
                       g.db_post != nullptr || g.dgate != nullptr;
     const Workspace w = workspace_of(c.rows, c.cols, dev.sm_count);
-    float *consts = reinterpret_cast<float *>(ws + w.consts);
     float *parts = reinterpret_cast<float *>(ws + w.parts);
     float *ends = reinterpret_cast<float *>(ws + w.ends);
-    const auto *dy_ = static_cast<const TA *>(dy), *a_ = static_cast<const TA *>(a);
-    const auto *dr_ = static_cast<const TR *>(dr_out), *r_ = static_cast<const TR *>(r_out);
-    const int64_t grid = std::min<int64_t>(c.rows, 4 * dev.sm_count);
-    cudaError_t e = launch_pdl(bwd_walk_kernel<TA, TR>, dim3(static_cast<unsigned>(grid)),
-                               dim3(kWalkThreads), 0, st, c, dy_, dr_, a_, r_, static_cast<TA *>(g.da),
-                               static_cast<TR *>(g.dr), consts, dev.status);
+    const unsigned strips = static_cast<unsigned>((c.cols + 255) / 256);
+    Chunks ch{c.rows, c.gate != nullptr ? c.gate_rows : c.rows, 0};
+    cudaError_t e;
+    if (c.cols <= kRegCols) {
+        const bool full = c.layer || c.b_post != nullptr || g.db_pre != nullptr || g.db_post != nullptr;
+        if (c.cols % kE == 0)
+            e = full ? bwd_rows<TA, TR, true, true>(c, ch, dy, dr_out, a, r_out, g, parts, ends, dev, st)
+                     : bwd_rows<TA, TR, true, false>(c, ch, dy, dr_out, a, r_out, g, parts, ends, dev, st);
+        else
+            e = full ? bwd_rows<TA, TR, false, true>(c, ch, dy, dr_out, a, r_out, g, parts, ends, dev, st)
+                     : bwd_rows<TA, TR, false, false>(c, ch, dy, dr_out, a, r_out, g, parts, ends, dev, st);
+    } else {
+        float *consts = reinterpret_cast<float *>(ws + w.consts);
+        const auto *dy_ = static_cast<const TA *>(dy), *a_ = static_cast<const TA *>(a);
+        const auto *dr_ = static_cast<const TR *>(dr_out), *r_ = static_cast<const TR *>(r_out);
+        const int64_t grid = std::min<int64_t>(c.rows, 4 * dev.sm_count);
+        e = launch_pdl(bwd_walk_kernel<TA, TR>, dim3(static_cast<unsigned>(grid)), dim3(kWalkThreads), 0,
+                       st, c, dy_, dr_, a_, r_, static_cast<TA *>(g.da), static_cast<TR *>(g.dr), consts,
+                       dev.status);
+        if (e != cudaSuccess || !sums)
+            return e;
+        const int64_t want = walk_chunks(c.rows, c.cols, dev.sm_count);
+        ch.chunk = (c.rows + want - 1) / want;
+        e = launch_pdl(cols_walk_kernel<TA, TR>,
+                       dim3(strips, static_cast<unsigned>((c.rows + ch.chunk - 1) / ch.chunk)), dim3(256), 0,
+                       st, c, ch, dy_, dr_, a_, r_, static_cast<const float *>(consts), parts, ends,
+                       g.dgate, dev.status);
+    }
     if (e != cudaSuccess || !sums)
         return e;
-    const int64_t want = walk_chunks(c.rows, c.cols, dev.sm_count);
-    const Chunks ch{c.rows, c.gate != nullptr ? c.gate_rows : c.rows, (c.rows + want - 1) / want};
     const int64_t n = (c.rows + ch.chunk - 1) / ch.chunk;
-    const unsigned strips = static_cast<unsigned>((c.cols + 255) / 256);
-    e = launch_pdl(cols_walk_kernel<TA, TR>, dim3(strips, static_cast<unsigned>(n)), dim3(256), 0, st, c,
-                   ch, dy_, dr_, a_, r_, static_cast<const float *>(consts), parts, ends, g.dgate,
-                   dev.status);
-    if (e != cudaSuccess)
-        return e;
     const Sums out{{g.dw_pre, g.db_pre, g.dw_post, g.db_post}};
     e = launch_pdl(reduce_kernel, dim3(static_cast<unsigned>((c.cols + 31) / 32), 4), dim3(1024), 0, st,
                    static_cast<const float *>(parts), static_cast<int>(n), c.cols, c.w_f32, out,

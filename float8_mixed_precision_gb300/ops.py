@@ -56,12 +56,12 @@ def _bytes(what: str, ws: torch.Tensor | None, dev):
     return _ptr(what, "ws", ws, torch.uint8, (ws.numel(),), dev), ws.numel()
 
 
-def _scalar(what: str, t: torch.Tensor | None, dev, name: str = "amax_out"):
+def _scalar(what: str, t: torch.Tensor | None, dev):
     """The pointer of one fp32 value (None if not given)."""
     if t is None:
         return None
     if t.dtype != torch.float32 or t.numel() != 1:
-        raise TypeError(f"{what}: {name} must be one float32 value")
+        raise TypeError(f"{what}: amax_out must be one float32 value")
     if t.device != dev:
         raise ValueError(f"{what}: tensors on different devices")
     return t.data_ptr()
