@@ -367,30 +367,54 @@ __device__ __forceinline__ void act_row(const uint32_t (&r)[kEpiCols], float inv
 }
 
 // A box of 32 rows x 64 columns between a staging buffer and a row-major tensor
-// whose rows no TMA store takes: a row at a time, two columns a lane.
-template <bool STORE>
-__device__ __forceinline__ void box_rows(uint8_t *b, __nv_bfloat16 *t, int row0, int col0, int M, int N,
-                                         int lane, unsigned *status)
+// whose rows no TMA store takes: a row at a time, two columns a lane, the loads of
+// 16 rows under way together.
+__device__ __forceinline__ uint32_t *box_word(uint8_t *b, int row, int lane)
 {
+    return reinterpret_cast<uint32_t *>(b + row * 128 + (((lane >> 2) ^ (row & 7)) << 4) + ((lane & 3) << 2));
+}
+
+__device__ __forceinline__ void load_box(uint8_t *b, const __nv_bfloat16 *t, int row0, int col0, int M,
+                                         int N, int lane, unsigned *status)
+{
+    const uint16_t *p = reinterpret_cast<const uint16_t *>(t);
     const int64_t mn = static_cast<int64_t>(M) * N;
     const int c = col0 + 2 * lane;
-    for (int i = 0; i < 32 && row0 + i < M; ++i) {
-        uint32_t *w = reinterpret_cast<uint32_t *>(b + i * 128 + (((lane >> 2) ^ (i & 7)) << 4) +
-                                                   ((lane & 3) << 2));
-        uint16_t *p = reinterpret_cast<uint16_t *>(t);
+#pragma unroll 1
+    for (int h = 0; h < 32; h += 16) {
+        uint32_t v[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const int64_t o = static_cast<int64_t>(row0 + h + i) * N + c;
+            v[i] = 0u;
+            if (row0 + h + i < M) {
+                if (c < N && in_range(o, 1, mn, status))
+                    v[i] = p[o];
+                if (c + 1 < N && in_range(o + 1, 1, mn, status))
+                    v[i] |= static_cast<uint32_t>(p[o + 1]) << 16;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            *box_word(b, h + i, lane) = v[i];
+    }
+}
+
+__device__ __forceinline__ void store_box(uint8_t *b, __nv_bfloat16 *t, int row0, int col0, int M, int N,
+                                          int lane, unsigned *status)
+{
+    uint16_t *p = reinterpret_cast<uint16_t *>(t);
+    const int64_t mn = static_cast<int64_t>(M) * N;
+    const int c = col0 + 2 * lane;
+#pragma unroll 8
+    for (int i = 0; i < 32; ++i) {
+        const uint32_t w = *box_word(b, i, lane);
         const int64_t o = static_cast<int64_t>(row0 + i) * N + c;
-        if (STORE) {
+        if (row0 + i < M) {
             if (c < N && in_range(o, 1, mn, status))
-                p[o] = static_cast<uint16_t>(*w);
+                p[o] = static_cast<uint16_t>(w);
             if (c + 1 < N && in_range(o + 1, 1, mn, status))
-                p[o + 1] = static_cast<uint16_t>(*w >> 16);
-        } else {
-            uint32_t v = 0u;
-            if (c < N && in_range(o, 1, mn, status))
-                v = p[o];
-            if (c + 1 < N && in_range(o + 1, 1, mn, status))
-                v |= static_cast<uint32_t>(p[o + 1]) << 16;
-            *w = v;
+                p[o + 1] = static_cast<uint16_t>(w >> 16);
         }
     }
 }
@@ -449,7 +473,7 @@ __device__ __forceinline__ bool epilogue_rows_act(uint32_t taddr, int row0, int 
                 }
             }
         } else if (res) {
-            box_rows<false>(b, const_cast<__nv_bfloat16 *>(ep.residual), row0, col0, M, N, lane, status);
+            load_box(b, ep.residual, row0, col0, M, N, lane, status);
         }
         __syncwarp();
         tc_wait_ld();
@@ -486,9 +510,9 @@ __device__ __forceinline__ bool epilogue_rows_act(uint32_t taddr, int row0, int 
             buf ^= 1u;
         } else {
             __syncwarp();
-            box_rows<true>(b, c, row0, col0, M, N, lane, status);
+            store_box(b, c, row0, col0, M, N, lane, status);
             if (zb != nullptr)
-                box_rows<true>(zb, ep.zout, row0, col0, M, N, lane, status);
+                store_box(zb, ep.zout, row0, col0, M, N, lane, status);
             __syncwarp();
         }
     }

@@ -20,6 +20,7 @@
 #include <cmath>
 #include <cstdint>
 #include <mutex>
+#include <type_traits>
 
 #include "f8_internal.h"
 #include "f8_ptx.cuh"
@@ -266,64 +267,84 @@ bwd_walk_kernel(const Call c, const TA *__restrict__ dy, const TR *__restrict__ 
 // ------------------------------------------------------------ rows in registers
 // A block keeps its row, or its slice of a row that a cluster shares, in registers,
 // and rows come some ahead through shared memory.
-using rows::kE;
-constexpr int kP = kE / 2;
+using rows::Param;
+constexpr int kFwdE = 16, kBwdE = 8;  // columns of a thread
 
 __device__ __forceinline__ float2 splat(float v) { return make_float2(v, v); }
 
-__device__ __forceinline__ rows::Slice slice_of(int64_t cols, uint32_t rank, uint32_t ranks)
+__device__ __forceinline__ rows::Slice slice_of(int64_t cols, int per, uint32_t rank)
 {
-    // slices of whole 16-byte vectors, the last one perhaps shorter
-    const int per = static_cast<int>((cols + kE * ranks - 1) / (kE * ranks)) * kE;
     rows::Slice s;
     s.first = per * static_cast<int>(rank);
     s.n = max(0, min(per, static_cast<int>(cols) - s.first));
     return s;
 }
 
-// (sum, sum of squared differences to their mean) / cols, over the row, of the
-// columns that there are: mean (0 without `layer`) and 1/deviation.
-template <bool VEC>
-__device__ __forceinline__ void row_stats(float2 (&x)[kP], int n, bool layer, float inv_c, float eps,
+// Mean (0 without `layer`) and 1/deviation of the row; x becomes x - mean.
+template <bool VEC, int E>
+__device__ __forceinline__ void row_stats(float2 (&x)[E / 2], int n, bool layer, float inv_c, float eps,
                                           rows::ClusterSum &sum, float &mu, float &rstd)
 {
     mu = 0.0f;
     if (layer) {
-        const float2 s = __fadd2_rn(__fadd2_rn(x[0], x[1]), __fadd2_rn(x[2], x[3]));
-        mu = sum(s.x + s.y, 0.0f).x * inv_c;
+        float2 s = x[0];
+#pragma unroll
+        for (int i = 1; i < E / 2; ++i)
+            s = __fadd2_rn(s, x[i]);
+        mu = sum(s.x + s.y) * inv_c;
+#pragma unroll
+        for (int i = 0; i < E / 2; ++i)
+            x[i] = __fadd2_rn(x[i], splat(-mu));
     }
     float2 q = splat(0.0f);
+    // columns past the slice are -mean and do not count
+    if constexpr (VEC) {
 #pragma unroll
-    for (int i = 0; i < kP; ++i) {
-        x[i] = __fadd2_rn(x[i], splat(-mu));
-        if (VEC) {
-            if (kE * static_cast<int>(threadIdx.x) < n)
-                q = __ffma2_rn(x[i], x[i], q);
-        } else {
-            const int c = threadIdx.x + 2 * i * blockDim.x;
-            if (c < n)
+        for (int u = 0; u < E / 8; ++u)
+            if (rows::vec_col<VEC>(u) < n) {
+#pragma unroll
+                for (int i = 4 * u; i < 4 * u + 4; ++i)
+                    q = __ffma2_rn(x[i], x[i], q);
+            }
+    } else {
+#pragma unroll
+        for (int i = 0; i < E / 2; ++i) {
+            if (rows::elem_col(2 * i) < n)
                 q.x = fmaf(x[i].x, x[i].x, q.x);
-            if (c + static_cast<int>(blockDim.x) < n)
+            if (rows::elem_col(2 * i + 1) < n)
                 q.y = fmaf(x[i].y, x[i].y, q.y);
         }
     }
-    rstd = 1.0f / sqrtf(sum(q.x + q.y, 0.0f).x * inv_c + eps);
+    rstd = rsqrtf(sum(q.x + q.y) * inv_c + eps);
 }
 
-template <typename TA, typename TR, bool VEC>
-__global__ void __launch_bounds__(1024, 1)
-fwd_kernel(const Call c, const TA *a, const TR *r, TR *r_out, TA *y, unsigned *amax, int ranks, int stages,
-           uint64_t limit_ns, unsigned *status)
+__device__ __forceinline__ void zero_sums(float *red)
 {
+    for (int i = threadIdx.x; i < 4 * rows::kMaxParts; i += blockDim.x)
+        red[i] = 0.0f;
+}
+
+// A unit (a block, or a cluster by column slices) walks the rows [unit chunk, (unit +
+// 1) chunk).  BF: all parameters are bf16 and stay in registers over the rows; fp32
+// ones are read again for each row, from L1.
+template <typename TA, typename TR, bool VEC, bool BF>
+__global__ void __launch_bounds__(512, 1)
+fwd_kernel(const Call c, const TA *a, const TR *r, TR *r_out, TA *y, unsigned *amax, int64_t chunk,
+           int ranks, int slice, int stages, uint64_t limit_ns, unsigned *status)
+{
+    constexpr int E = kFwdE, P = E / 2;
     extern __shared__ __align__(16) uint8_t dyn[];
-    __shared__ float2 red[2 * rows::kMaxCluster * 32];
+    __shared__ __align__(16) float red[4 * rows::kMaxParts];
     __shared__ __align__(8) uint64_t full[rows::kMaxStages];
     __shared__ unsigned blk;
     const uint32_t rank = ranks > 1 ? cluster_ctarank() : 0u;
-    const int64_t unit = blockIdx.x / ranks, units = gridDim.x / ranks;
-    const rows::Slice sl = slice_of(c.cols, rank, ranks);
-    const int64_t total = c.rows * c.cols;
-    rows::Slots<TA, 1, TR, 1> slots{dyn, full, stages, c.cols, total, sl, {a}, {r}, 0u, true};
+    const int64_t unit = blockIdx.x / ranks, first = unit * chunk, stop = min(first + chunk, c.rows);
+    const rows::Slice sl = slice_of(c.cols, slice, rank);
+    rows::Slots<TA, 1, TR, 1, VEC> slots;
+    slots.start(dyn, full, stages, c.cols, c.rows, sl);
+    slots.a[0] = a;
+    slots.r[0] = r;
+    zero_sums(red);
     if (threadIdx.x == 0) {
         for (int i = 0; i < stages; ++i)
             mbar_init(&full[i], 1);
@@ -337,77 +358,88 @@ fwd_kernel(const Call c, const TA *a, const TR *r, TR *r_out, TA *y, unsigned *a
     else
         __syncthreads();
     if (threadIdx.x == 0)
-        for (int i = 0; i < stages && unit + i * units < c.rows; ++i)
-            slots.fill(unit + i * units);
+        for (int i = 0; i < stages && first + i < stop; ++i)
+            slots.fill(first + i);
     rows::ClusterSum sum{red, 0, rank, static_cast<uint32_t>(ranks)};
     const float inv_c = 1.0f / static_cast<float>(c.cols);
-    uint32_t m2 = 0u, seq = 0u;
-    for (int64_t row = unit; row < c.rows; row += units, ++seq) {
-        slots.wait(seq, limit_ns, status);
+    const bool post = c.w_post != nullptr, gated = c.gate != nullptr, layer = c.layer != 0;
+    Param<E, BF> w1, b1, g, w2, b2;
+    if (BF) {
+        rows::take_param<VEC>(c.w_post, 0, sl.first, sl.n, 1.0f, w1);
+        rows::take_param<VEC>(c.b_post, 0, sl.first, sl.n, 0.0f, b1);
+        rows::take_param<VEC>(c.w_pre, 0, sl.first, sl.n, 1.0f, w2);
+        rows::take_param<VEC>(c.b_pre, 0, sl.first, sl.n, 0.0f, b2);
+    }
+    int64_t gate = gated ? first / c.gate_rows : 0;
+    int64_t gate_end = gated ? first : stop, gate_at = 0;
+    uint32_t m2 = 0u;
+    int64_t at = slots.begin(first);
+    for (int64_t row = first; row < stop; ++row, at += c.cols) {
+        if (gated && row == gate_end) {
+            if (BF)
+                rows::take_param<VEC>(c.gate, 0, gate * c.cols + sl.first, sl.n, 1.0f, g);
+            gate_at = gate * c.cols + sl.first;
+            ++gate;
+            gate_end = min(stop, gate * c.gate_rows);  // within rows + gate_rows
+        }
+        slots.wait(limit_ns, status);
         int sa = 0, sr = 0;
-        if constexpr (!VEC) {
-            sa = rows::Window<TA>(slots.begin(row), sl.n, total).shift;
-            sr = rows::Window<TR>(slots.begin(row), sl.n, total).shift;
-            slots.tails(seq, row);
-        }
-        float2 x[kP], v[kP], p[kP];
-        const int slot = ring_slot(seq, stages);
-        rows::take<VEC, TA>(slots.at_a(slot, 0), sa, sl.n, x);
-        rows::take<VEC, TR>(slots.at_r(slot, 0), sr, sl.n, v);
+        if constexpr (!VEC)
+            slots.ragged(row, sa, sr);
+        float2 x[P], v[P];
+        rows::take<VEC, E, TA>(slots.at_a(0), sa, sl.n, x);
+        rows::take<VEC, E, TR>(slots.at_r(0), sr, sl.n, v);
         float mu1 = 0.0f, s1 = 1.0f;
-        if (c.w_post != nullptr) {
-            row_stats<VEC>(x, sl.n, c.layer, inv_c, c.eps, sum, mu1, s1);
-            rows::take_param<VEC>(c.w_post, c.w_f32, sl.first, sl.n, 1.0f, p);
+        if (post) {
+            row_stats<VEC, E>(x, sl.n, layer, inv_c, c.eps, sum, mu1, s1);
+            if (!BF)
+                rows::take_param<VEC>(c.w_post, c.w_f32, sl.first, sl.n, 1.0f, w1);
+            if (!BF)
+                rows::take_param<VEC>(c.b_post, c.w_f32, sl.first, sl.n, 0.0f, b1);
 #pragma unroll
-            for (int i = 0; i < kP; ++i)
-                x[i] = __fmul2_rn(__fmul2_rn(x[i], splat(s1)), p[i]);
-            if (c.b_post != nullptr) {
-                rows::take_param<VEC>(c.b_post, c.w_f32, sl.first, sl.n, 0.0f, p);
-#pragma unroll
-                for (int i = 0; i < kP; ++i)
-                    x[i] = __fadd2_rn(x[i], p[i]);
-            }
+            for (int i = 0; i < P; ++i)
+                x[i] = __ffma2_rn(__fmul2_rn(x[i], splat(s1)), w1.pair(i), b1.pair(i));
         }
-        if (c.gate != nullptr) {
-            rows::take_param<VEC>(c.gate, c.g_f32, row / c.gate_rows * c.cols + sl.first, sl.n, 1.0f, p);
+        if (gated) {
+            if (!BF)
+                rows::take_param<VEC>(c.gate, c.g_f32, gate_at, sl.n, 1.0f, g);
 #pragma unroll
-            for (int i = 0; i < kP; ++i)
-                x[i] = __fmul2_rn(x[i], p[i]);
+            for (int i = 0; i < P; ++i)
+                x[i] = __fmul2_rn(x[i], g.pair(i));
         }
 #pragma unroll
-        for (int i = 0; i < kP; ++i) {
+        for (int i = 0; i < P; ++i)
             x[i] = __ffma2_rn(v[i], splat(c.scale), x[i]);
-            v[i] = x[i];
-        }
+        const bool inside = in_range(at, sl.n, c.rows * c.cols, status);
+        if (inside)
+            rows::give<VEC, E>(r_out + at, sl.n, x);
         float mu2, s2;
-        row_stats<VEC>(x, sl.n, c.layer, inv_c, c.eps, sum, mu2, s2);
+        row_stats<VEC, E>(x, sl.n, layer, inv_c, c.eps, sum, mu2, s2);
         // every thread has taken its columns: the slot may be filled again
-        if (threadIdx.x == 0 && slots.ok && row + stages * units < c.rows)
-            slots.fill(row + stages * units);
-        const int64_t at = slots.begin(row);
-        const bool inside = in_range(at, sl.n, total, status);
-        rows::give<VEC>(r_out + at, sl.n, v, nullptr, inside);
-        rows::take_param<VEC>(c.w_pre, c.w_f32, sl.first, sl.n, 1.0f, p);
-#pragma unroll
-        for (int i = 0; i < kP; ++i)
-            x[i] = __fmul2_rn(__fmul2_rn(x[i], splat(s2)), p[i]);
-        if (c.b_pre != nullptr) {
-            rows::take_param<VEC>(c.b_pre, c.w_f32, sl.first, sl.n, 0.0f, p);
-#pragma unroll
-            for (int i = 0; i < kP; ++i)
-                x[i] = __fadd2_rn(x[i], p[i]);
-        }
-        rows::give<VEC>(y + at, sl.n, x, amax != nullptr ? &m2 : nullptr, inside);
-        if (threadIdx.x == 0 && rank == 0) {
-            if (c.w_post != nullptr) {
-                if (c.layer)
-                    c.stats[row] = mu1;
-                c.stats[c.rows + row] = s1;
+        if (threadIdx.x == 0) {
+            if (slots.ok && row + stages < stop)
+                slots.fill(row + stages);
+            if (rank == 0) {
+                if (post) {
+                    if (layer)
+                        c.stats[row] = mu1;
+                    c.stats[c.rows + row] = s1;
+                }
+                if (layer)
+                    c.stats[2 * c.rows + row] = mu2;
+                c.stats[3 * c.rows + row] = s2;
             }
-            if (c.layer)
-                c.stats[2 * c.rows + row] = mu2;
-            c.stats[3 * c.rows + row] = s2;
         }
+        if (!BF)
+            rows::take_param<VEC>(c.w_pre, c.w_f32, sl.first, sl.n, 1.0f, w2);
+        if (!BF)
+            rows::take_param<VEC>(c.b_pre, c.w_f32, sl.first, sl.n, 0.0f, b2);
+#pragma unroll
+        for (int i = 0; i < P; ++i)
+            x[i] = __ffma2_rn(__fmul2_rn(x[i], splat(s2)), w2.pair(i), b2.pair(i));
+        if (inside)
+            rows::give<VEC, E>(y + at, sl.n, x, amax != nullptr ? &m2 : nullptr);
+        slots.step();
     }
     if (threadIdx.x == 0)
         slots.drain();
@@ -516,21 +548,28 @@ cols_walk_kernel(const Call c, const Chunks ch, const TA *__restrict__ dy, const
 // The backward pass in one: a unit (a block, or a cluster by column slices) walks the
 // chunk `unit` of rows, with the column sums of all gradients in registers.  FULL:
 // with means or biases; without, the sums that only those need are left out.
-template <typename TA, typename TR, bool VEC, bool FULL>
+template <typename TA, typename TR, bool VEC, bool FULL, bool BF>
 __global__ void __launch_bounds__(512, 1)
 bwd_kernel(const Call c, const Chunks ch, const TA *__restrict__ dy, const TR *__restrict__ dr_out,
            const TA *__restrict__ a, const TR *__restrict__ r_out, TA *__restrict__ da,
            TR *__restrict__ dr, float *__restrict__ parts, float *__restrict__ ends,
-           void *__restrict__ dgate, int ranks, int stages, uint64_t limit_ns, unsigned *status)
+           void *__restrict__ dgate, int ranks, int slice, int stages, uint64_t limit_ns, unsigned *status)
 {
+    constexpr int E = kBwdE, P = E / 2;
     extern __shared__ __align__(16) uint8_t dyn[];
-    __shared__ float2 red[2 * rows::kMaxCluster * 32];
+    __shared__ __align__(16) float red[4 * rows::kMaxParts];
     __shared__ __align__(8) uint64_t full[rows::kMaxStages];
     const uint32_t rank = ranks > 1 ? cluster_ctarank() : 0u;
     const int64_t unit = blockIdx.x / ranks;
-    const rows::Slice sl = slice_of(c.cols, rank, ranks);
-    const int64_t total = c.rows * c.cols, first = ch.first(unit), stop = ch.stop(unit);
-    rows::Slots<TA, 2, TR, 2> slots{dyn, full, stages, c.cols, total, sl, {dy, a}, {dr_out, r_out}, 0u, true};
+    const rows::Slice sl = slice_of(c.cols, slice, rank);
+    const int64_t first = ch.first(unit), stop = ch.stop(unit);
+    rows::Slots<TA, 2, TR, 2, VEC> slots;
+    slots.start(dyn, full, stages, c.cols, c.rows, sl);
+    slots.a[0] = dy;
+    slots.a[1] = a;
+    slots.r[0] = dr_out;
+    slots.r[1] = r_out;
+    zero_sums(red);
     if (threadIdx.x == 0) {
         for (int i = 0; i < stages; ++i)
             mbar_init(&full[i], 1);
@@ -548,31 +587,27 @@ bwd_kernel(const Call c, const Chunks ch, const TA *__restrict__ dy, const TR *_
     rows::ClusterSum sum{red, 0, rank, static_cast<uint32_t>(ranks)};
     const float inv_c = 1.0f / static_cast<float>(c.cols);
     const bool post = c.w_post != nullptr, gated = c.gate != nullptr, layer = FULL && c.layer;
-    float2 w2[kP], w1[kP], b1[kP], g[kP];
+    Param<E, BF> w2, w1, b1, g;
     rows::take_param<VEC>(c.w_pre, c.w_f32, sl.first, sl.n, 1.0f, w2);
     rows::take_param<VEC>(c.w_post, c.w_f32, sl.first, sl.n, 1.0f, w1);
     if (FULL)
         rows::take_param<VEC>(c.b_post, c.w_f32, sl.first, sl.n, 0.0f, b1);
-    float2 dw2[kP], db2[kP], dw1[kP], db1[kP], dg[kP];
+    float2 dw2[P], db2[P], dw1[P], db1[P], dg[P];
 #pragma unroll
-    for (int i = 0; i < kP; ++i)
-        dw2[i] = db2[i] = dw1[i] = db1[i] = dg[i] = g[i] = splat(0.0f);
+    for (int i = 0; i < P; ++i)
+        dw2[i] = db2[i] = dw1[i] = db1[i] = dg[i] = splat(0.0f);
     int64_t gate = 0, gate_end = gated ? first : stop;
-    if (!gated) {
-#pragma unroll
-        for (int i = 0; i < kP; ++i)
-            g[i] = splat(1.0f);
-    }
+    rows::take_param<VEC>(nullptr, 0, 0, sl.n, 1.0f, g);
     // what a gate's rows of this chunk have given, into place
     auto flush = [&]() {
         if (dgate == nullptr)
             return;
         if (ch.whole(gate, unit))
-            rows::give_param<VEC>(dgate, c.g_f32, gate * c.cols + sl.first, sl.n, dg);
+            rows::give_param<VEC, E>(dgate, c.g_f32, gate * c.cols + sl.first, sl.n, dg);
         else
-            rows::give<VEC>(ends + (unit * 2 + ch.slot(gate, unit)) * c.cols + sl.first, sl.n, dg, nullptr, true);
+            rows::give<VEC, E>(ends + (unit * 2 + ch.slot(gate, unit)) * c.cols + sl.first, sl.n, dg);
 #pragma unroll
-        for (int i = 0; i < kP; ++i)
+        for (int i = 0; i < P; ++i)
             dg[i] = splat(0.0f);
     };
     // the next row's statistics are on their way while a row is worked on
@@ -589,8 +624,8 @@ bwd_kernel(const Call c, const Chunks ch, const TA *__restrict__ dy, const TR *_
     };
     if (first < stop)
         next_stats(first);
-    uint32_t seq = 0u;
-    for (int64_t row = first; row < stop; ++row, ++seq) {
+    int64_t at = slots.begin(first);
+    for (int64_t row = first; row < stop; ++row, at += c.cols) {
         if (row == gate_end) {
             if (row > first)
                 flush();
@@ -601,69 +636,64 @@ bwd_kernel(const Call c, const Chunks ch, const TA *__restrict__ dy, const TR *_
         const float mu1 = n_mu1, s1 = n_s1, mu2 = n_mu2, s2 = n_s2;
         if (row + 1 < stop)
             next_stats(row + 1);
-        slots.wait(seq, limit_ns, status);
-        const int slot = ring_slot(seq, stages);
+        slots.wait(limit_ns, status);
         int sa = 0, sr = 0;
-        if constexpr (!VEC) {
-            sa = rows::Window<TA>(slots.begin(row), sl.n, total).shift;
-            sr = rows::Window<TR>(slots.begin(row), sl.n, total).shift;
-            slots.tails(seq, row);
-        }
-        float2 h[kP], e[kP];
-        rows::take<VEC, TA>(slots.at_a(slot, 0), sa, sl.n, h);
-        rows::take<VEC, TR>(slots.at_r(slot, 1), sr, sl.n, e);
+        if constexpr (!VEC)
+            slots.ragged(row, sa, sr);
+        float2 h[P], e[P];
+        rows::take<VEC, E, TA>(slots.at_a(0), sa, sl.n, h);
+        rows::take<VEC, E, TR>(slots.at_r(1), sr, sl.n, e);
         float2 t1 = splat(0.0f), t2 = splat(0.0f);
 #pragma unroll
-        for (int i = 0; i < kP; ++i) {
+        for (int i = 0; i < P; ++i) {
             e[i] = __fmul2_rn(__fadd2_rn(e[i], splat(-mu2)), splat(s2));
             dw2[i] = __ffma2_rn(h[i], e[i], dw2[i]);
             if (FULL)
                 db2[i] = __fadd2_rn(db2[i], h[i]);
-            h[i] = __fmul2_rn(h[i], w2[i]);
+            h[i] = __fmul2_rn(h[i], w2.pair(i));
             t1 = __ffma2_rn(h[i], e[i], t1);
             if (FULL)
                 t2 = __fadd2_rn(t2, h[i]);
         }
         float2 k = sum(t1.x + t1.y, t2.x + t2.y);
         // every thread is done with the row before: its slot may be filled again
-        if (threadIdx.x == 0 && slots.ok && seq > 0 && row - 1 + stages < stop)
+        if (threadIdx.x == 0 && slots.ok && row > first && row - 1 + stages < stop)
             slots.fill(row - 1 + stages);
         const float k1 = -s2 * (k.x * inv_c), k2 = layer ? -s2 * (k.y * inv_c) : 0.0f;
         // h becomes D
-        float2 o[kP];
+        float2 o[P];
         if (dr_out != nullptr) {
-            rows::take<VEC, TR>(slots.at_r(slot, 0), sr, sl.n, o);
+            rows::take<VEC, E, TR>(slots.at_r(0), sr, sl.n, o);
         } else {
 #pragma unroll
-            for (int i = 0; i < kP; ++i)
+            for (int i = 0; i < P; ++i)
                 o[i] = splat(0.0f);
         }
 #pragma unroll
-        for (int i = 0; i < kP; ++i)
+        for (int i = 0; i < P; ++i)
             h[i] = __fadd2_rn(o[i], __ffma2_rn(h[i], splat(s2), __ffma2_rn(e[i], splat(k1), splat(k2))));
-        rows::take<VEC, TA>(slots.at_a(slot, 1), sa, sl.n, e);
-        const int64_t at = slots.begin(row);
-        const bool inside = in_range(at, sl.n, total, status);
-        if (dr != nullptr) {
+        rows::take<VEC, E, TA>(slots.at_a(1), sa, sl.n, e);
+        const bool inside = in_range(at, sl.n, c.rows * c.cols, status);
+        if (dr != nullptr && inside) {
 #pragma unroll
-            for (int i = 0; i < kP; ++i)
+            for (int i = 0; i < P; ++i)
                 o[i] = __fmul2_rn(h[i], splat(c.scale));
-            rows::give<VEC>(dr + at, sl.n, o, nullptr, inside);
+            rows::give<VEC, E>(dr + at, sl.n, o);
         }
         // e becomes e1 (a without the norm), h du
         t1 = t2 = splat(0.0f);
 #pragma unroll
-        for (int i = 0; i < kP; ++i) {
+        for (int i = 0; i < P; ++i) {
             e[i] = __fmul2_rn(__fadd2_rn(e[i], splat(-mu1)), splat(s1));
-            float2 u = __fmul2_rn(e[i], w1[i]);
+            float2 u = __fmul2_rn(e[i], w1.pair(i));
             if (FULL)
-                u = __fadd2_rn(u, b1[i]);
+                u = __fadd2_rn(u, b1.pair(i));
             dg[i] = __ffma2_rn(h[i], u, dg[i]);
-            h[i] = __fmul2_rn(h[i], g[i]);
+            h[i] = __fmul2_rn(h[i], g.pair(i));
             dw1[i] = __ffma2_rn(h[i], e[i], dw1[i]);
             if (FULL)
                 db1[i] = __fadd2_rn(db1[i], h[i]);
-            h[i] = __fmul2_rn(h[i], w1[i]);
+            h[i] = __fmul2_rn(h[i], w1.pair(i));
             t1 = __ffma2_rn(h[i], e[i], t1);
             if (FULL)
                 t2 = __fadd2_rn(t2, h[i]);
@@ -672,20 +702,21 @@ bwd_kernel(const Call c, const Chunks ch, const TA *__restrict__ dy, const TR *_
             k = sum(t1.x + t1.y, t2.x + t2.y);
             const float d1 = -s1 * (k.x * inv_c), d2 = layer ? -s1 * (k.y * inv_c) : 0.0f;
 #pragma unroll
-            for (int i = 0; i < kP; ++i)
+            for (int i = 0; i < P; ++i)
                 h[i] = __ffma2_rn(h[i], splat(s1), __ffma2_rn(e[i], splat(d1), splat(d2)));
         }
-        if (da != nullptr)
-            rows::give<VEC>(da + at, sl.n, h, nullptr, inside);
+        if (da != nullptr && inside)
+            rows::give<VEC, E>(da + at, sl.n, h);
+        slots.step();
     }
     if (gated && first < stop)
         flush();
     float *p = parts + unit * 4 * c.cols + sl.first;
-    rows::give<VEC>(p, sl.n, dw2, nullptr, true);
-    rows::give<VEC>(p + 2 * c.cols, sl.n, dw1, nullptr, true);
+    rows::give<VEC, E>(p, sl.n, dw2);
+    rows::give<VEC, E>(p + 2 * c.cols, sl.n, dw1);
     if (FULL) {
-        rows::give<VEC>(p + c.cols, sl.n, db2, nullptr, true);
-        rows::give<VEC>(p + 3 * c.cols, sl.n, db1, nullptr, true);
+        rows::give<VEC, E>(p + c.cols, sl.n, db2);
+        rows::give<VEC, E>(p + 3 * c.cols, sl.n, db1);
     }
     if (threadIdx.x == 0)
         slots.drain();
@@ -693,30 +724,57 @@ bwd_kernel(const Call c, const Chunks ch, const TA *__restrict__ dy, const TR *_
         cluster_sync();
 }
 
-// The parameters' gradients from the partial rows, in a fixed order: 32 columns a
-// block, 32 threads a column, each every 32nd row; blockIdx.y names the gradient.
+// The gradients from the partial rows, in a fixed order: 32 columns a block, 32
+// threads a column, each every 32nd row.  blockIdx.y names a parameter's gradient, or
+// from 4 on a gate whose rows may lie in several chunks: gate y - 4 itself where
+// there are no more gates than borders between chunks, else the one that reaches over
+// the border after chunk y - 4.  What a chunk has whole it has written.
 struct Sums {
     void *out[4];
+    void *dgate;
+    const float *parts, *ends;
+    int nparts, w_f32, g_f32, by_border;
+    int64_t cols;
 };
 
 __global__ void __launch_bounds__(1024)
-reduce_kernel(const float *__restrict__ parts, int nparts, int64_t cols, int f32, const Sums sums,
-              unsigned *status)
+reduce_kernel(const __grid_constant__ Sums a, const Chunks ch, unsigned *status)
 {
     __shared__ float acc[32][33];
     griddep_wait();
     griddep_launch_dependents();
-    void *out = sums.out[blockIdx.y];
-    if (out == nullptr)
-        return;
     const int lane = threadIdx.x & 31, k = threadIdx.x >> 5;
-    const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + lane;
+    const int64_t cols = a.cols, c = static_cast<int64_t>(blockIdx.x) * 32 + lane;
+    void *out;
+    int64_t at = 0;
+    int f32 = a.w_f32;
     float s = 0.0f;
-    if (c < cols) {
-        const float *p = parts + static_cast<int64_t>(blockIdx.y) * cols + c;
+    if (blockIdx.y < 4) {
+        out = a.out[blockIdx.y];
+        if (out == nullptr)
+            return;
+        if (c < cols) {
+            const float *p = a.parts + static_cast<int64_t>(blockIdx.y) * cols + c;
 #pragma unroll 8
-        for (int i = k; i < nparts; i += 32)
-            s += p[static_cast<int64_t>(i) * 4 * cols];
+            for (int i = k; i < a.nparts; i += 32)
+                s += p[static_cast<int64_t>(i) * 4 * cols];
+        }
+    } else {
+        const int64_t y = blockIdx.y - 4, g = a.by_border ? ch.gate(ch.stop(y) - 1) : y;
+        const int64_t first = ch.gate_first(g) / ch.chunk, last = (ch.gate_stop(g) - 1) / ch.chunk;
+        if (first == last || (a.by_border && first != y))
+            return;
+        out = a.dgate;
+        at = g * cols;
+        f32 = a.g_f32;
+        // the gate comes first in every chunk but the one that it begins in
+        if (c < cols) {
+            if (k == 0)
+                s = a.ends[(first * 2 + ch.slot(g, first)) * cols + c];
+#pragma unroll 8
+            for (int64_t i = first + 1 + k; i <= last; i += 32)
+                s += a.ends[i * 2 * cols + c];
+        }
     }
     acc[k][lane] = s;
     __syncthreads();
@@ -726,32 +784,7 @@ reduce_kernel(const float *__restrict__ parts, int nparts, int64_t cols, int f32
         s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
     const int64_t col = static_cast<int64_t>(blockIdx.x) * 32 + k;
     if (lane == 0 && col < cols && in_range(col, 1, cols, status))
-        put_param(out, f32, col, s);
-}
-
-// dgate of the gates whose rows lie in several chunks.  Block (x, y) looks at the
-// border after chunk y and sums the gate that reaches over it, if its rows begin in
-// that chunk, over all its chunks.
-__global__ void __launch_bounds__(256)
-gate_reduce_kernel(const float *__restrict__ ends, const Chunks ch, int64_t nchunks, int64_t cols,
-                   int f32, void *__restrict__ dgate, unsigned *status)
-{
-    griddep_wait();
-    griddep_launch_dependents();
-    const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-    const int64_t first = blockIdx.y;
-    const int64_t g = ch.gate(ch.stop(first) - 1);
-    if (i >= cols || ch.gate_stop(g) <= ch.stop(first) || ch.gate_first(g) < ch.first(first))
-        return;
-    float s = 0.0f;
-#pragma unroll 8
-    for (int64_t k = first; k < nchunks; ++k) {
-        if (k > first && ch.first(k) >= ch.gate_stop(g))
-            break;
-        s += ends[(k * 2 + ch.slot(g, k)) * cols + i];
-    }
-    if (in_range(g * cols + i, 1, ((ch.rows - 1) / ch.gate_rows + 1) * cols, status))
-        put_param(dgate, f32, g * cols + i, s);
+        put_param(out, f32, at + col, s);
 }
 
 // ------------------------------------------------------------ launches
@@ -772,23 +805,23 @@ struct Plan {
     int ranks, threads, per_sm, slice;
 };
 
-Plan plan_of(int64_t cols, int max_threads, int sm_threads)
+// 512 threads of 128 registers an SM, of `e` columns each, in blocks that hold a row's
+// slice; slices of whole vectors, the last one perhaps shorter.
+Plan plan_of(int64_t cols, int e)
 {
+    constexpr int kThreads = 512;
     Plan p;
     p.ranks = 1;
-    while (p.ranks * max_threads * kE < cols)
+    while (p.ranks * kThreads * e < cols)
         p.ranks *= 2;
-    p.slice = static_cast<int>((cols + kE * p.ranks - 1) / (kE * p.ranks)) * kE;
-    p.threads = (p.slice / kE + 31) / 32 * 32;
-    p.per_sm = std::max(1, std::min(8, sm_threads / p.threads));
+    p.slice = static_cast<int>((cols + 8 * p.ranks - 1) / (8 * p.ranks)) * 8;
+    p.threads = (p.slice + 32 * e - 1) / (32 * e) * 32;
+    p.per_sm = std::max(1, std::min(8, kThreads / p.threads));
     return p;
 }
 
-constexpr int kFwdThreads = 1024, kFwdSmThreads = 1024;
-constexpr int kBwdThreads = 512, kBwdSmThreads = 512;
-
-Plan fwd_plan(int64_t cols) { return plan_of(cols, kFwdThreads, kFwdSmThreads); }
-Plan bwd_plan(int64_t cols) { return plan_of(cols, kBwdThreads, kBwdSmThreads); }
+Plan fwd_plan(int64_t cols) { return plan_of(cols, kFwdE); }
+Plan bwd_plan(int64_t cols) { return plan_of(cols, kBwdE); }
 
 // Most units (blocks, or clusters) of the backward pass.
 int64_t bwd_units(int64_t rows, int64_t cols, int sms)
@@ -823,6 +856,8 @@ Call call_of(const f8_residual_norm &n, float *stats)
     return Call{n.kind == F8_LAYER_NORM, n.w_type == F8_F32, n.gate_type == F8_F32, n.rows, n.cols,
                 n.gate_rows, n.eps, n.scale, n.w_pre, n.b_pre, n.w_post, n.b_post, n.gate, stats};
 }
+
+bool params_bf16(const Call &c) { return !c.w_f32 && (c.gate == nullptr || !c.g_f32); }
 
 // Units that run at once, and the slots of each: a launch of more would walk its
 // last chunks alone.
@@ -874,55 +909,60 @@ cudaError_t shape_of(const Plan &p, int64_t rows, uint32_t slot_bytes, const Dev
     return cudaSuccess;
 }
 
-template <typename TA, typename TR, bool VEC>
+template <typename TA, typename TR, bool VEC, bool BF>
 cudaError_t fwd_rows(const Call &c, const void *a, const void *r, void *r_out, void *y, unsigned *amax,
                      const DeviceInfo &dev, cudaStream_t st)
 {
     const Plan p = fwd_plan(c.cols);
     Shape s;
-    const cudaError_t e = shape_of<fwd_kernel<TA, TR, VEC>>(
+    const cudaError_t e = shape_of<fwd_kernel<TA, TR, VEC, BF>>(
         p, c.rows, rows::slice_pitch<TA>(p.slice) + rows::slice_pitch<TR>(p.slice), dev, &s);
     if (e != cudaSuccess)
         return e;
-    return launch_pdl_cluster(fwd_kernel<TA, TR, VEC>, dim3(static_cast<unsigned>(s.units * p.ranks)),
+    const int64_t chunk = (c.rows + s.units - 1) / s.units, units = (c.rows + chunk - 1) / chunk;
+    return launch_pdl_cluster(fwd_kernel<TA, TR, VEC, BF>, dim3(static_cast<unsigned>(units * p.ranks)),
                               dim3(static_cast<unsigned>(p.threads)), s.smem, st,
                               static_cast<unsigned>(p.ranks), c, static_cast<const TA *>(a),
                               static_cast<const TR *>(r), static_cast<TR *>(r_out), static_cast<TA *>(y),
-                              amax, p.ranks, s.stages, wait_limit_ns(), dev.status);
+                              amax, chunk, p.ranks, p.slice, s.stages, wait_limit_ns(), dev.status);
 }
 
 template <typename TA, typename TR>
 cudaError_t fwd(const Call &c, const void *a, const void *r, void *r_out, void *y, unsigned *amax,
                 const DeviceInfo &dev, cudaStream_t st)
 {
-    if (c.cols <= kRegCols)
-        return c.cols % kE == 0 ? fwd_rows<TA, TR, true>(c, a, r, r_out, y, amax, dev, st)
-                                : fwd_rows<TA, TR, false>(c, a, r, r_out, y, amax, dev, st);
+    if (c.cols <= kRegCols) {
+        if (params_bf16(c))
+            return c.cols % 8 == 0 ? fwd_rows<TA, TR, true, true>(c, a, r, r_out, y, amax, dev, st)
+                                   : fwd_rows<TA, TR, false, true>(c, a, r, r_out, y, amax, dev, st);
+        return c.cols % 8 == 0 ? fwd_rows<TA, TR, true, false>(c, a, r, r_out, y, amax, dev, st)
+                               : fwd_rows<TA, TR, false, false>(c, a, r, r_out, y, amax, dev, st);
+    }
     const int64_t grid = std::min<int64_t>(c.rows, 4 * dev.sm_count);
     return launch_pdl(fwd_walk_kernel<TA, TR>, dim3(static_cast<unsigned>(grid)), dim3(kWalkThreads), 0,
                       st, c, static_cast<const TA *>(a), static_cast<const TR *>(r),
                       static_cast<TR *>(r_out), static_cast<TA *>(y), amax, dev.status);
 }
 
-template <typename TA, typename TR, bool VEC, bool FULL>
+template <typename TA, typename TR, bool VEC, bool FULL, bool BF>
 cudaError_t bwd_rows(const Call &c, Chunks &ch, const void *dy, const void *dr_out, const void *a,
                      const void *r_out, const f8_residual_norm_grads &g, float *parts, float *ends,
                      const DeviceInfo &dev, cudaStream_t st)
 {
     const Plan p = bwd_plan(c.cols);
     Shape s;
-    const cudaError_t e = shape_of<bwd_kernel<TA, TR, VEC, FULL>>(
+    const cudaError_t e = shape_of<bwd_kernel<TA, TR, VEC, FULL, BF>>(
         p, c.rows, 2 * (rows::slice_pitch<TA>(p.slice) + rows::slice_pitch<TR>(p.slice)), dev, &s);
     if (e != cudaSuccess)
         return e;
     ch.chunk = (c.rows + s.units - 1) / s.units;
     const int64_t units = (c.rows + ch.chunk - 1) / ch.chunk;
-    return launch_pdl_cluster(bwd_kernel<TA, TR, VEC, FULL>, dim3(static_cast<unsigned>(units * p.ranks)),
+    return launch_pdl_cluster(bwd_kernel<TA, TR, VEC, FULL, BF>, dim3(static_cast<unsigned>(units * p.ranks)),
                               dim3(static_cast<unsigned>(p.threads)), s.smem, st,
                               static_cast<unsigned>(p.ranks), c, ch, static_cast<const TA *>(dy),
                               static_cast<const TR *>(dr_out), static_cast<const TA *>(a),
                               static_cast<const TR *>(r_out), static_cast<TA *>(g.da),
-                              static_cast<TR *>(g.dr), parts, ends, g.dgate, p.ranks, s.stages,
+                              static_cast<TR *>(g.dr), parts, ends, g.dgate, p.ranks, p.slice, s.stages,
                               wait_limit_ns(), dev.status);
 }
 
@@ -940,12 +980,17 @@ cudaError_t bwd(const Call &c, const void *dy, const void *dr_out, const void *a
     cudaError_t e;
     if (c.cols <= kRegCols) {
         const bool full = c.layer || c.b_post != nullptr || g.db_pre != nullptr || g.db_post != nullptr;
-        if (c.cols % kE == 0)
-            e = full ? bwd_rows<TA, TR, true, true>(c, ch, dy, dr_out, a, r_out, g, parts, ends, dev, st)
-                     : bwd_rows<TA, TR, true, false>(c, ch, dy, dr_out, a, r_out, g, parts, ends, dev, st);
+        auto run = [&](auto vec, auto all, auto bf) {
+            return bwd_rows<TA, TR, vec.value, all.value, bf.value>(c, ch, dy, dr_out, a, r_out, g, parts, ends,
+                                                                    dev, st);
+        };
+        constexpr std::true_type yes;
+        constexpr std::false_type no;
+        const bool vec = c.cols % 8 == 0, bf = params_bf16(c);
+        if (bf)
+            e = vec ? (full ? run(yes, yes, yes) : run(yes, no, yes)) : (full ? run(no, yes, yes) : run(no, no, yes));
         else
-            e = full ? bwd_rows<TA, TR, false, true>(c, ch, dy, dr_out, a, r_out, g, parts, ends, dev, st)
-                     : bwd_rows<TA, TR, false, false>(c, ch, dy, dr_out, a, r_out, g, parts, ends, dev, st);
+            e = vec ? (full ? run(yes, yes, no) : run(yes, no, no)) : (full ? run(no, yes, no) : run(no, no, no));
     } else {
         float *consts = reinterpret_cast<float *>(ws + w.consts);
         const auto *dy_ = static_cast<const TA *>(dy), *a_ = static_cast<const TA *>(a);
@@ -966,14 +1011,14 @@ cudaError_t bwd(const Call &c, const void *dy, const void *dr_out, const void *a
     if (e != cudaSuccess || !sums)
         return e;
     const int64_t n = (c.rows + ch.chunk - 1) / ch.chunk;
-    const Sums out{{g.dw_pre, g.db_pre, g.dw_post, g.db_post}};
-    e = launch_pdl(reduce_kernel, dim3(static_cast<unsigned>((c.cols + 31) / 32), 4), dim3(1024), 0, st,
-                   static_cast<const float *>(parts), static_cast<int>(n), c.cols, c.w_f32, out,
-                   dev.status);
-    if (e != cudaSuccess || g.dgate == nullptr || n == 1)
-        return e;
-    return launch_pdl(gate_reduce_kernel, dim3(strips, static_cast<unsigned>(n - 1)), dim3(256), 0, st,
-                      static_cast<const float *>(ends), ch, n, c.cols, c.g_f32, g.dgate, dev.status);
+    const int64_t gates = (c.rows - 1) / ch.gate_rows + 1;
+    const Sums out{{g.dw_pre, g.db_pre, g.dw_post, g.db_post}, g.dgate,          parts,  ends,
+                   static_cast<int>(n),                        c.w_f32,          c.g_f32, gates > n - 1,
+                   c.cols};
+    const int64_t across = g.dgate != nullptr ? std::min(gates, n - 1) : 0;
+    return launch_pdl(reduce_kernel,
+                      dim3(static_cast<unsigned>((c.cols + 31) / 32), static_cast<unsigned>(4 + across)),
+                      dim3(1024), 0, st, out, ch, dev.status);
 }
 
 bool type_ok(f8_dtype t) { return t == F8_BF16 || t == F8_F32; }
