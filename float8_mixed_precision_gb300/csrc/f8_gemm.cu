@@ -25,8 +25,8 @@
 // kEpiAct is the linear with its bias, activation and residual: per step of 64
 // columns the epilogue forms z = acc / (sa sb) + bias and y = act(z) + residual in
 // fp32 and writes y, and z where it is kept, each rounded once.  The residual's box
-// comes by TMA into the buffer that y leaves from, one step ahead; the first one of
-// a tile is fetched while the tile's products are still being formed.
+// comes by TMA into the buffer that y leaves from while the activation is formed.
+// Eight epilogue warps: one a scheduler does not keep up with the products.
 // Two shapes of the same kernel:
 //   PAIR = false  one CTA computes a 128 x BN tile (tcgen05 cta_group::1);
 //   PAIR = true   a cluster of two CTAs on neighbouring SMs computes a
@@ -71,6 +71,7 @@ namespace {
 constexpr int kBM = 128;   // accumulator rows per CTA (TMEM lanes)
 constexpr int kBK = 128;   // bytes of K per stage = one 128-byte swizzle row
 constexpr int kEpiWarps = 4;       // one per TMEM lane quarter
+constexpr int kActWarps = 8;       // two per quarter, each half of the columns
 constexpr int kGluCols = 32;       // GLU: h columns per epilogue step
 constexpr int kGluBoxBytes = 32 * kGluCols * 2;  // one 32 x 64-byte box, 64-byte swizzle
 constexpr int kEpiCols = 64;                       // columns per epilogue step
@@ -91,14 +92,13 @@ struct Cfg {
     static constexpr int kBBytes = kBRows * kBK;
     static constexpr int kStageBytes = kABytes + kBBytes;
     static constexpr int kTmemCols = (2 * BN <= 256) ? 256 : 512;
-    static constexpr int kThreads = 64 + 32 * kEpiWarps;  // producer, MMA, epilogue
-    // per epilogue warp: plain, two 32 x 128-byte swizzled store buffers;
-    // GLU, one set of three 32 x 64-byte boxes (a, b, h); Act, two buffers of y and
-    // one of z
-    static constexpr int kWarpStaging = GLU ? 3 * kGluBoxBytes
-                                            : (EPI == kEpiAct ? 3 : 2) * kEpiBufBytes;
-    static constexpr int kStagingBytes = kEpiWarps * kWarpStaging;
-    static constexpr int kResBars = EPI == kEpiAct ? 2 * kEpiWarps : 0;  // residual boxes
+    static constexpr int kWarps = EPI == kEpiAct ? kActWarps : kEpiWarps;
+    static constexpr int kThreads = 64 + 32 * kWarps;  // producer, MMA, epilogue
+    // per epilogue warp: plain and Act, two 32 x 128-byte swizzled store buffers;
+    // GLU, one set of three 32 x 64-byte boxes (a, b, h)
+    static constexpr int kWarpStaging = GLU ? 3 * kGluBoxBytes : 2 * kEpiBufBytes;
+    static constexpr int kStagingBytes = kWarps * kWarpStaging;
+    static constexpr int kResBars = EPI == kEpiAct ? kActWarps : 0;  // a residual box each
     static constexpr int kBarBytes = 8 * (2 * STAGES + 5 + kResBars) + 16;
     static constexpr int kSmemBytes = STAGES * kStageBytes + kStagingBytes + kBarBytes + 1024;
     static_assert(kSmemBytes <= 232448, "shared memory budget");
@@ -295,74 +295,76 @@ struct EpiParams<kEpiAct> {
     int bias_f32, act;
 };
 
-// Eight biases from column `col`; 0 past the last one.
-__device__ __forceinline__ void load_bias8(const void *bias, int f32, int col, int N, float (&f)[8],
+// The bias of a lane's four columns from `col`; 0 past the last one.
+__device__ __forceinline__ void load_bias4(const void *bias, int f32, int col, int N, float (&f)[4],
                                            unsigned *status)
 {
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-        f[e] = 0.0f;
-    if (bias == nullptr || col >= N || !in_range(col, min(8, N - col), N, status))
-        return;
-    if (col + 8 <= N) {  // col is a multiple of 8
-        if (f32) {
-            const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(bias) + col);
-            const float4 u = __ldg(p), v = __ldg(p + 1);
-            f[0] = u.x, f[1] = u.y, f[2] = u.z, f[3] = u.w;
-            f[4] = v.x, f[5] = v.y, f[6] = v.z, f[7] = v.w;
-        } else {
-            const uint4 u =
-                __ldg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(bias) + col));
-            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                f[e] = __uint_as_float((e & 1) ? w[e / 2] & 0xFFFF0000u : w[e / 2] << 16);
-        }
-        return;
-    }
-    for (int e = 0; e < 8; ++e)
-        if (col + e < N)
-            f[e] = f32 ? static_cast<const float *>(bias)[col + e]
+    for (int e = 0; e < 4; ++e)
+        if (bias != nullptr && col + e < N && in_range(col + e, 1, N, status))
+            f[e] = f32 ? __ldg(static_cast<const float *>(bias) + col + e)
                        : __bfloat162float(static_cast<const __nv_bfloat16 *>(bias)[col + e]);
+        else
+            f[e] = 0.0f;
 }
 
-// z and y of one row's 64 columns: z = r inv + bias to `zb` (if not NULL), y =
-// act(z) + what `b` holds (with `res`) to `b`; both rows of the 128-byte swizzle.
+// z = r inv + bias of one row's 64 columns, as a row of the 128-byte swizzle to `zb`
+// (if not NULL), and r <- act(z).  bias: lane l's are those of columns 4l .. 4l + 3 of
+// the warp's 128, of which this step's are the 64 from lane `from` on.
 template <int ACT>
-__device__ __forceinline__ void act_row(const uint32_t (&r)[kEpiCols], float inv,
-                                        const EpiParams<kEpiAct> &ep, int col0, int N, uint8_t *b,
-                                        uint8_t *zb, bool res, bool live, int lane, uint32_t &max2,
-                                        unsigned *status)
+__device__ __forceinline__ void act_row(uint32_t (&r)[kEpiCols], float inv, const float (&bias)[4],
+                                        bool biased, int from, uint8_t *zb, int lane)
 {
     const float2 inv2 = make_float2(inv, inv);
 #pragma unroll
     for (int q = 0; q < kEpiCols / 8; ++q) {
-        float bias[8];
-        load_bias8(ep.bias, ep.bias_f32, col0 + 8 * q, N, bias, status);
-        const int off = lane * 128 + ((q ^ (lane & 7)) << 4);
-        uint32_t old[4] = {0u, 0u, 0u, 0u};
-        if (res) {
-            const uint4 v = *reinterpret_cast<const uint4 *>(b + off);
-            old[0] = v.x, old[1] = v.y, old[2] = v.z, old[3] = v.w;
-        }
-        uint32_t z2[4], y2[4];
+        uint32_t z2[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int e = 8 * q + 2 * i;
-            const float2 z = __ffma2_rn(make_float2(__uint_as_float(r[e]), __uint_as_float(r[e + 1])),
-                                        inv2, make_float2(bias[2 * i], bias[2 * i + 1]));
-            float2 y = act::value<ACT>(z);
+            float2 z = make_float2(__uint_as_float(r[e]), __uint_as_float(r[e + 1]));
+            if (biased) {
+                const int src = from + e / 4;
+                z = __ffma2_rn(z, inv2, make_float2(__shfl_sync(0xFFFFFFFFu, bias[e & 3], src),
+                                                    __shfl_sync(0xFFFFFFFFu, bias[(e & 3) + 1], src)));
+            } else {
+                z = __fmul2_rn(z, inv2);
+            }
+            z2[i] = pack_bf16x2(z.x, z.y);
+            const float2 y = act::value<ACT>(z);
+            r[e] = __float_as_uint(y.x);
+            r[e + 1] = __float_as_uint(y.y);
+        }
+        if (zb != nullptr)
+            *reinterpret_cast<uint4 *>(zb + lane * 128 + ((q ^ (lane & 7)) << 4)) =
+                make_uint4(z2[0], z2[1], z2[2], z2[3]);
+    }
+}
+
+// y = r + what the row of `b` holds (with `res`), to `b`.
+__device__ __forceinline__ void out_row(const uint32_t (&r)[kEpiCols], uint8_t *b, bool res, bool live,
+                                        int lane, uint32_t &max2)
+{
+#pragma unroll
+    for (int q = 0; q < kEpiCols / 8; ++q) {
+        uint4 *p = reinterpret_cast<uint4 *>(b + lane * 128 + ((q ^ (lane & 7)) << 4));
+        uint32_t old[4] = {0u, 0u, 0u, 0u}, y2[4];
+        if (res) {
+            const uint4 v = *p;
+            old[0] = v.x, old[1] = v.y, old[2] = v.z, old[3] = v.w;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int e = 8 * q + 2 * i;
+            float2 y = make_float2(__uint_as_float(r[e]), __uint_as_float(r[e + 1]));
             if (res)
                 y = __fadd2_rn(y, make_float2(__uint_as_float(old[i] << 16),
                                               __uint_as_float(old[i] & 0xFFFF0000u)));
-            z2[i] = pack_bf16x2(z.x, z.y);
             y2[i] = pack_bf16x2(y.x, y.y);
             if (live)
                 max2 = swiglu::max_abs2(max2, y2[i]);
         }
-        *reinterpret_cast<uint4 *>(b + off) = make_uint4(y2[0], y2[1], y2[2], y2[3]);
-        if (zb != nullptr)
-            *reinterpret_cast<uint4 *>(zb + off) = make_uint4(z2[0], z2[1], z2[2], z2[3]);
+        *p = make_uint4(y2[0], y2[1], y2[2], y2[3]);
     }
 }
 
@@ -380,23 +382,21 @@ __device__ __forceinline__ void load_box(uint8_t *b, const __nv_bfloat16 *t, int
     const uint16_t *p = reinterpret_cast<const uint16_t *>(t);
     const int64_t mn = static_cast<int64_t>(M) * N;
     const int c = col0 + 2 * lane;
+    // places outside the tensor read its last row or column instead: no branch keeps
+    // the loads from being issued together
+    const int c0 = min(c, N - 1), c1 = min(c + 1, N - 1);
 #pragma unroll 1
     for (int h = 0; h < 32; h += 16) {
-        uint32_t v[16];
+        uint32_t lo[16], hi[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-            const int64_t o = static_cast<int64_t>(row0 + h + i) * N + c;
-            v[i] = 0u;
-            if (row0 + h + i < M) {
-                if (c < N && in_range(o, 1, mn, status))
-                    v[i] = p[o];
-                if (c + 1 < N && in_range(o + 1, 1, mn, status))
-                    v[i] |= static_cast<uint32_t>(p[o + 1]) << 16;
-            }
+            const int64_t o = static_cast<int64_t>(min(row0 + h + i, M - 1)) * N;
+            lo[i] = in_range(o + c0, 1, mn, status) ? p[o + c0] : 0u;
+            hi[i] = in_range(o + c1, 1, mn, status) ? p[o + c1] : 0u;
         }
 #pragma unroll
         for (int i = 0; i < 16; ++i)
-            *box_word(b, h + i, lane) = v[i];
+            *box_word(b, h + i, lane) = (c < N ? lo[i] : 0u) | (c + 1 < N ? hi[i] << 16 : 0u);
     }
 }
 
@@ -419,30 +419,33 @@ __device__ __forceinline__ void store_box(uint8_t *b, __nv_bfloat16 *t, int row0
     }
 }
 
-// The residual's box of step `col0` into buffer `buf`, by one lane.
-__device__ __forceinline__ void fetch_residual(const EpiParams<kEpiAct> &ep, uint8_t *stage,
-                                               uint64_t *bars, uint32_t buf, int col0, int row0)
+// The residual's box at (col0, row0) into `b`, by one lane.
+__device__ __forceinline__ void fetch_residual(const EpiParams<kEpiAct> &ep, uint8_t *b, uint64_t *bar,
+                                               int col0, int row0)
 {
-    mbar_arrive_expect_tx(&bars[buf], kEpiBufBytes);
-    tma_load_2d(stage + buf * kEpiBufBytes, &ep.res, &bars[buf], col0, row0);
+    mbar_arrive_expect_tx(bar, kEpiBufBytes);
+    tma_load_2d(b, &ep.res, bar, col0, row0);
 }
 
-// The Act epilogue of one warp over the columns of a tile.  With a residual by TMA
-// the caller has fetched the first step's box into buffer `buf`; phases holds the
-// parity of each buffer's next box.  False if a wait gave up.
-template <int BN>
+// The Act epilogue of one warp over COLS columns from col_base.  With stores by TMA the
+// two buffers are y's in turn, or y's and z's where z is kept.  A residual comes by TMA
+// into y's buffer while z and the activation are formed; `fetched` says that the
+// caller has asked for the first step's box, `phase` is the parity of the next one.
+// False if a wait gave up.
+template <int COLS>
 __device__ __forceinline__ bool epilogue_rows_act(uint32_t taddr, int row0, int col_base, int M, int N,
-                                                  float inv, const EpiParams<kEpiAct> &ep,
-                                                  __nv_bfloat16 *c,
+                                                  float inv, const float (&bias)[4],
+                                                  const EpiParams<kEpiAct> &ep, __nv_bfloat16 *c,
                                                   const CUtensorMap *tma_c, bool tma, uint8_t *stage,
-                                                  uint64_t *bars, uint32_t &buf, uint32_t &phases,
-                                                  uint32_t &max2, int lane, unsigned *status,
-                                                  volatile int *abort_flag, uint64_t limit_ns)
+                                                  uint64_t *bar, bool fetched, uint32_t &buf,
+                                                  uint32_t &phase, uint32_t &max2, int lane,
+                                                  unsigned *status, volatile int *abort_flag,
+                                                  uint64_t limit_ns)
 {
-    uint8_t *zb = ep.zout != nullptr ? stage + 2 * kEpiBufBytes : nullptr;
-    const bool res = ep.residual != nullptr;
+    uint8_t *zb = ep.zout != nullptr ? stage + kEpiBufBytes : nullptr;
+    const bool res = ep.residual != nullptr, biased = ep.bias != nullptr;
 #pragma unroll 1
-    for (int j = 0; j < BN / kEpiCols; ++j) {
+    for (int j = 0; j < COLS / kEpiCols; ++j) {
         const int col0 = col_base + j * kEpiCols;
         if (row0 >= M || col0 >= N)  // nothing of this box lies in C (warp-uniform)
             break;
@@ -452,52 +455,40 @@ __device__ __forceinline__ bool epilogue_rows_act(uint32_t taddr, int row0, int 
         uint8_t *b = stage + buf * kEpiBufBytes;
         if (tma) {
             if (lane == 0) {
-                bulk_wait_group_read<0>();  // the stores so far have read their buffers
-                if (res && j + 1 < BN / kEpiCols && col0 + kEpiCols < N)
-                    fetch_residual(ep, stage, bars, buf ^ 1u, col0 + kEpiCols, row0);
-            }
-            if (res) {
-                const bool ok = mbar_wait(&bars[buf], (phases >> buf) & 1u, abort_flag, limit_ns);
-                phases ^= 1u << buf;
-                if (!__all_sync(0xFFFFFFFFu, ok)) {
-                    tc_wait_ld();
-                    if (lane == 0) {
-                        note_timeout(abort_flag, status);
-                        // the boxes under way land before the buffers are given up
-                        mbar_wait(&bars[buf], ((phases >> buf) & 1u) ^ 1u, nullptr, kDrainLimitNs);
-                        if (j + 1 < BN / kEpiCols && col0 + kEpiCols < N)
-                            mbar_wait(&bars[buf ^ 1u], (phases >> (buf ^ 1u)) & 1u, nullptr, kDrainLimitNs);
-                    }
-                    __syncwarp();
-                    return false;
-                }
+                // the store that last left from these buffers has read them
+                if (zb != nullptr)
+                    bulk_wait_group_read<0>();
+                else
+                    bulk_wait_group_read<1>();
+                if (res && !(fetched && j == 0))
+                    fetch_residual(ep, b, bar, col0, row0);
             }
         } else if (res) {
             load_box(b, ep.residual, row0, col0, M, N, lane, status);
         }
         __syncwarp();
         tc_wait_ld();
-        const bool live = row0 + lane < M;
         switch (ep.act) {
-        case F8_ACT_RELU:
-            act_row<F8_ACT_RELU>(r, inv, ep, col0, N, b, zb, res, live, lane, max2, status);
-            break;
-        case F8_ACT_RELU2:
-            act_row<F8_ACT_RELU2>(r, inv, ep, col0, N, b, zb, res, live, lane, max2, status);
-            break;
-        case F8_ACT_SILU:
-            act_row<F8_ACT_SILU>(r, inv, ep, col0, N, b, zb, res, live, lane, max2, status);
-            break;
-        case F8_ACT_GELU:
-            act_row<F8_ACT_GELU>(r, inv, ep, col0, N, b, zb, res, live, lane, max2, status);
-            break;
-        case F8_ACT_GELU_TANH:
-            act_row<F8_ACT_GELU_TANH>(r, inv, ep, col0, N, b, zb, res, live, lane, max2, status);
-            break;
-        default:
-            act_row<F8_ACT_NONE>(r, inv, ep, col0, N, b, zb, res, live, lane, max2, status);
-            break;
+        case F8_ACT_RELU: act_row<F8_ACT_RELU>(r, inv, bias, biased, 16 * j, zb, lane); break;
+        case F8_ACT_RELU2: act_row<F8_ACT_RELU2>(r, inv, bias, biased, 16 * j, zb, lane); break;
+        case F8_ACT_SILU: act_row<F8_ACT_SILU>(r, inv, bias, biased, 16 * j, zb, lane); break;
+        case F8_ACT_GELU: act_row<F8_ACT_GELU>(r, inv, bias, biased, 16 * j, zb, lane); break;
+        case F8_ACT_GELU_TANH: act_row<F8_ACT_GELU_TANH>(r, inv, bias, biased, 16 * j, zb, lane); break;
+        default: act_row<F8_ACT_NONE>(r, inv, bias, biased, 16 * j, zb, lane); break;
         }
+        if (tma && res) {
+            const bool ok = mbar_wait(bar, phase, abort_flag, limit_ns);
+            if (!__all_sync(0xFFFFFFFFu, ok)) {
+                if (lane == 0) {
+                    note_timeout(abort_flag, status);
+                    mbar_wait(bar, phase, nullptr, kDrainLimitNs);  // the box lands before the CTA leaves
+                }
+                __syncwarp();
+                return false;
+            }
+            phase ^= 1u;
+        }
+        out_row(r, b, res, row0 + lane < M, lane, max2);
         if (tma) {
             fence_proxy_async_shared();
             __syncwarp();
@@ -507,7 +498,8 @@ __device__ __forceinline__ bool epilogue_rows_act(uint32_t taddr, int row0, int 
                     tma_store_2d(&ep.z, zb, col0, row0);
                 bulk_commit_group();
             }
-            buf ^= 1u;
+            if (zb == nullptr)
+                buf ^= 1u;
         } else {
             __syncwarp();
             store_box(b, c, row0, col0, M, N, lane, status);
@@ -598,7 +590,7 @@ gemm_kernel(const __grid_constant__ GemmSet<NP> set, const __grid_constant__ Epi
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     unsigned *hmax_cta = reinterpret_cast<unsigned *>(tmem_slot + 2);  // largest |h| or |y| bits
-    uint64_t *res_bars = reinterpret_cast<uint64_t *>(tmem_slot + 4);  // Act: two a warp
+    uint64_t *res_bars = reinterpret_cast<uint64_t *>(tmem_slot + 4);  // Act: one a warp
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
@@ -613,7 +605,7 @@ gemm_kernel(const __grid_constant__ GemmSet<NP> set, const __grid_constant__ Epi
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(&tfull[a], 1);
-            mbar_init(&tempty[a], PAIR ? 2 * kEpiWarps : kEpiWarps);
+            mbar_init(&tempty[a], PAIR ? 2 * C::kWarps : C::kWarps);
         }
         mbar_init(drain, 1);
         for (int i = 0; i < C::kResBars; ++i)
@@ -816,7 +808,7 @@ gemm_kernel(const __grid_constant__ GemmSet<NP> set, const __grid_constant__ Epi
         uint32_t hmax2 = 0;
         const uint32_t tempty_leader = PAIR ? cluster_map(smem_addr(&tempty[0]), 0) : 0u;
         uint32_t buf = 0;
-        [[maybe_unused]] uint32_t phases = 0;
+        [[maybe_unused]] uint32_t phase = 0;
         for (int local = 0;; ++local) {
             const int g = unit_tile<NP>(set, unit, local);
             if (g < 0)
@@ -829,13 +821,21 @@ gemm_kernel(const __grid_constant__ GemmSet<NP> set, const __grid_constant__ Epi
             int mb, nb;
             tile_coords(tile, pr.num_m, pr.num_n, group_m, mb, nb);
             const int row0 = mb * C::kTileM + static_cast<int>(rank) * kBM + quad * 32;
-            [[maybe_unused]] uint64_t *my_bars = res_bars + 2 * (warp - 2);
+            constexpr int kCols = BN * kEpiWarps / C::kWarps;  // columns of a warp
+            const int col_base = nb * BN + (warp - 2) / kEpiWarps * kCols;
+            [[maybe_unused]] uint64_t *my_bar = res_bars + (warp - 2);
             [[maybe_unused]] bool fetched = false;
+            [[maybe_unused]] float bias[4];
             if constexpr (EPI == kEpiAct) {
-                fetched = ep.residual != nullptr && pr.tma_store != 0 && row0 < pr.M;
+                static_assert(kCols == 128, "a lane's four biases cover the warp's columns");
+                load_bias4(ep.bias, ep.bias_f32, col_base + 4 * lane, pr.N, bias, status);
+                fetched = ep.residual != nullptr && pr.tma_store != 0 && row0 < pr.M && col_base < pr.N;
                 if (fetched && lane == 0) {
-                    bulk_wait_group_read<0>();
-                    fetch_residual(ep, my_stage, my_bars, buf, nb * BN, row0);
+                    if (ep.zout != nullptr)
+                        bulk_wait_group_read<0>();
+                    else
+                        bulk_wait_group_read<1>();
+                    fetch_residual(ep, my_stage + buf * kEpiBufBytes, my_bar, col_base, row0);
                 }
             }
             bool ok = mbar_wait(&tfull[acc], aph, abort_flag, limit_ns);
@@ -844,7 +844,7 @@ gemm_kernel(const __grid_constant__ GemmSet<NP> set, const __grid_constant__ Epi
                 if (lane == 0) {
                     note_timeout(abort_flag, status);
                     if (fetched)
-                        mbar_wait(&my_bars[buf], (phases >> buf) & 1u, nullptr, kDrainLimitNs);
+                        mbar_wait(my_bar, phase, nullptr, kDrainLimitNs);
                 }
                 break;
             }
@@ -854,9 +854,10 @@ gemm_kernel(const __grid_constant__ GemmSet<NP> set, const __grid_constant__ Epi
                 epilogue_rows_glu(taddr, row0, nb * BN, pr.M, inv[0], &set.c[0], &ep.h, my_stage,
                                   hmax2, lane);
             else if constexpr (EPI == kEpiAct)
-                ok = epilogue_rows_act<BN>(taddr, row0, nb * BN, pr.M, pr.N, inv[0], ep, pr.c,
-                                           &set.c[0], pr.tma_store != 0, my_stage, my_bars, buf,
-                                           phases, hmax2, lane, status, abort_flag, limit_ns);
+                ok = epilogue_rows_act<kCols>(taddr + (col_base - nb * BN), row0, col_base, pr.M, pr.N,
+                                              inv[0], bias, ep, pr.c, &set.c[0], pr.tma_store != 0,
+                                              my_stage, my_bar, fetched, buf, phase, hmax2, lane, status,
+                                              abort_flag, limit_ns);
             else
                 epilogue_rows<BN>(taddr, row0, nb * BN, pr.M, pr.N, pick<NP>(inv, slot), pr.c,
                                   &set.c[slot], pr.tma_store != 0, my_stage, buf, lane, status);
@@ -1225,6 +1226,21 @@ cudaError_t launch_gemm_w13_swiglu(const uint8_t *x_q, const uint8_t *w13_q, int
     return run_gemm<256, 4, false, kEpiGlu>(&g, plan, dev, stream, ep, h, nparts);
 }
 
+// Whether the kernel for few rows takes the GEMM: up to 128 rows, and up to 255 where
+// its tiles leave SMs over that splitting K fills.  B [N, K] at M rows, bias and SiLU,
+// this kernel against that one: 4096 x 4096 at 8 rows 25 and 14 us, at 128 26 and 18, at
+// 256 23 and 23; 4096 x 14336 at 8 rows 61 and 23, at 192 61 and 31; 14336 x 4096 (no
+// split) at 64 rows 29 and 25, at 192 31 and 29, with a residual 31 and 35; 16384 x 1024
+// at 192 rows 16 and 18, with a residual 18 and 25.  F8_GEMM_FEW=0|1 forces one (for
+// measurement).
+bool few_rows(const GemmDesc &g, const DeviceInfo &dev)
+{
+    const char *e = std::getenv("F8_GEMM_FEW");
+    if (e != nullptr)
+        return e[0] == '1';
+    return g.M <= kBM || (g.M < 2 * kBM && gemm_few_plan(g.M, g.N, g.K, dev.sm_count).splits >= 4);
+}
+
 cudaError_t launch_gemm_act(const GemmDesc &g, const ActEpilogue &e, const DeviceInfo &dev,
                             cudaStream_t stream)
 {
@@ -1235,6 +1251,8 @@ cudaError_t launch_gemm_act(const GemmDesc &g, const ActEpilogue &e, const Devic
     ep.residual = static_cast<const __nv_bfloat16 *>(e.residual);
     ep.zout = static_cast<__nv_bfloat16 *>(e.z);
     ep.amax = e.amax;
+    if (few_rows(g, dev))
+        return launch_gemm_few(g, e, dev, stream);
     const int v = gemm_variant(g.M, dev);
     const SchedProblem sp = sched_problem(g);
     const LaunchPlan plan = sched_plan(&sp, 1, variant_tile_m(v), 256, variant_units(v, dev));

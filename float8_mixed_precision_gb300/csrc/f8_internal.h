@@ -289,6 +289,16 @@ struct ActEpilogue {
 cudaError_t launch_gemm_act(const GemmDesc &g, const ActEpilogue &e, const DeviceInfo &dev,
                             cudaStream_t stream);
 
+// The same for few rows of A: how its rows and K blocks are laid over the GPU (tiles of
+// 128 columns and nt rows, each the work of a cluster of `splits` CTAs), and the launch.
+struct FewPlan {
+    int64_t tiles;
+    int nt, splits;
+};
+FewPlan gemm_few_plan(int64_t M, int64_t N, int64_t K, int sms);
+cudaError_t launch_gemm_few(const GemmDesc &g, const ActEpilogue &e, const DeviceInfo &dev,
+                            cudaStream_t stream);
+
 // d(AB) [M, 2F] (AB's column order) of the w1+w3 group from the gradient dh
 // [M, F] of h = silu(a) b and the forward's AB, with one |d(AB)| partial
 // maximum per CTA in partials (*nparts receives their count).  F % 128 == 0.
