@@ -249,18 +249,18 @@ def lib() -> ctypes.CDLL:
         L.f8_act_bwd_workspace_bytes.restype = sz
         L.f8_act_bwd.argtypes = [vp, vp, ci, i64, i64, vp, vp, ci, vp, vp, sz, vp]
         L.f8_act_bwd.restype = st
-        L.f8_rope.argtypes = [ctypes.POINTER(_RopeTensor), ci, ci, i64, i64, i64, i64, ci, vp, i64, i64,
+        # structs of these calls come as bytes (block.py) or as the classes above
+        L.f8_rope.argtypes = [vp, ci, ci, i64, i64, i64, i64, ci, vp, i64, i64,
                               vp, f32, ci, vp]
         L.f8_rope.restype = st
         f64 = ctypes.c_double
         L.f8_rope_frequencies.argtypes = [i64, f64, ci, f64, f64, f64, f64, ctypes.POINTER(f64)]
         L.f8_rope_frequencies.restype = st
-        L.f8_residual_norm_fwd.argtypes = [ctypes.POINTER(_ResidualNorm), vp, vp, vp, vp, vp, vp, vp]
+        L.f8_residual_norm_fwd.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp]
         L.f8_residual_norm_fwd.restype = st
         L.f8_residual_norm_bwd_workspace_bytes.argtypes = [i64, i64]
         L.f8_residual_norm_bwd_workspace_bytes.restype = sz
-        L.f8_residual_norm_bwd.argtypes = [ctypes.POINTER(_ResidualNorm), vp, vp, vp, vp, vp,
-                                           ctypes.POINTER(_ResidualNormGrads), vp, sz, vp]
+        L.f8_residual_norm_bwd.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
         L.f8_residual_norm_bwd.restype = st
         _lib = L
         return L

@@ -8,6 +8,7 @@ that it calls and only checks and marshals its arguments.
 from __future__ import annotations
 
 import ctypes
+import struct
 
 import torch
 
@@ -23,7 +24,7 @@ def _arg(what: str, name: str, t: torch.Tensor | None, dtype, shape: tuple, inde
     up to ten tensors while a decoding step's kernel runs for a few microseconds, so
     what holds is found in one expression and what does not by ops._ptr."""
     if t is None:
-        return None
+        return 0
     if t.dtype is dtype and t.shape == shape and t.get_device() == index and t.is_contiguous():
         return t.data_ptr()
     return ops._ptr(what, name, t, dtype, shape, torch.device("cuda", index) if index >= 0 else torch.device("cpu"))
@@ -43,7 +44,7 @@ def _one(what: str, name: str, t: torch.Tensor | None, index: int):
 def _typed(what: str, name: str, t: torch.Tensor | None, shape: tuple, index: int):
     """The pointer and type of a bf16 or fp32 tensor (None and bf16 if not given)."""
     if t is None:
-        return None, binding.F8_BF16
+        return 0, binding.F8_BF16
     return _arg(what, name, t, t.dtype, shape, index), _dtype(what, t)
 
 
@@ -110,28 +111,31 @@ def f8_act_bwd(dy: torch.Tensor, z: torch.Tensor | None, act: int, dz: torch.Ten
 
 
 # ---------------------------------------------------------------- rotary positions
-_ONE, _TWO = binding._RopeTensor * 1, binding._RopeTensor * 2
+# the C structs as bytes: built in one step each
+_ROPE_ONE, _ROPE_TWO = struct.Struct("=2Q7q"), struct.Struct("=2Q7q2Q7q")
+_NORM = struct.Struct("=5i4x3q2f5Q")
+_GRADS = struct.Struct("=7Q")
 
 
-def _heads(what: str, name: str, t: torch.Tensor, lead: tuple | None, dtype, index: int):
-    """(pointer, shape, strides) of a tensor [tokens, heads, dim] or [batch, seq,
-    heads, dim] with dense columns, as four of each; `lead` is what q has in front of
-    the heads."""
-    shape, stride = t.shape, t.stride()
-    if t.dtype is not dtype:
-        raise TypeError(f"{what}: {name} must be {str(dtype).replace('torch.', '')}")
-    if t.get_device() != index:
-        raise ValueError(f"{what}: tensors on different devices")
-    n = len(shape)
-    if n != 3 and n != 4 or lead is not None and n != len(lead) + 2:
-        raise ValueError(f"{what}: {name} must be [tokens, heads, dim] or [batch, seq, heads, dim], as q is")
-    if lead is not None and shape[:-2] != lead:
-        raise ValueError(f"{what}: q, k and the outputs must agree in all but the heads")
-    if stride[-1] != 1 and shape[-1] > 1:
-        raise ValueError(f"{what}: the columns of {name} must be contiguous")
-    if n == 3:
-        return t.data_ptr(), (1, *shape), (0, *stride)
-    return t.data_ptr(), shape, stride
+def _heads(what: str, name: str, t: torch.Tensor, out: torch.Tensor, lead: tuple, dim: int, dtype, index: int):
+    """The C struct's values of a tensor [*lead, heads, dim] and its output; what does
+    not hold is found by name."""
+    shape, x, o = t.shape, t.stride(), out.stride()
+    if (shape == out.shape and shape[:-2] == lead and shape[-1] == dim and (x[-1] == o[-1] == 1 or dim <= 1)
+            and t.dtype is dtype and out.dtype is dtype and t.get_device() == index and out.get_device() == index):
+        if len(x) == 4:
+            return t.data_ptr(), out.data_ptr(), shape[2], *x[:3], *o[:3]
+        return t.data_ptr(), out.data_ptr(), shape[1], 0, *x[:2], 0, *o[:2]
+    for n, v in ((name, t), (name + "_out", out)):
+        if v.dtype is not dtype:
+            raise TypeError(f"{what}: {n} must be {str(dtype).replace('torch.', '')}")
+        if v.get_device() != index:
+            raise ValueError(f"{what}: tensors on different devices")
+        if v.shape[:-2] != lead or v.shape[-1:] != (dim,) or v.dim() != len(lead) + 2:
+            raise ValueError(f"{what}: q, k and the outputs must agree in all but the heads")
+        if v.stride(-1) != 1 and dim > 1:
+            raise ValueError(f"{what}: the columns of {n} must be contiguous")
+    raise ValueError(f"{what}: {name}_out must have the shape of {name}")
 
 
 def f8_rope(q: torch.Tensor, positions: torch.Tensor, freqs: torch.Tensor,
@@ -145,42 +149,34 @@ def f8_rope(q: torch.Tensor, positions: torch.Tensor, freqs: torch.Tensor,
     (f8_rope_frequencies).  q_out may be q, and k_out k.  `inverse` turns back: the
     gradient of the call."""
     what = "f8_rope"
-    kind, dtype, at = _dtype(what, q), q.dtype, q.get_device()
+    kind, dtype, at, shape = _dtype(what, q), q.dtype, q.get_device(), q.shape
     if not ops._on_device(q):
         raise ValueError("libf8 takes device tensors only")
-    lead = q.shape[:-2]
-    q_out = _empty(q.shape, dtype, q.device, stream) if q_out is None else q_out
-    qp, (batch, seq, heads, dim), sq = _heads(what, "q", q, None, dtype, at)
-    if q_out.shape != q.shape:
-        raise ValueError(f"{what}: q_out must have the shape of q")
-    op, _, so = _heads(what, "q_out", q_out, lead, dtype, at)
-    first = (qp, op, heads, sq[0], sq[1], sq[2], so[0], so[1], so[2])
+    lead, n = shape[:-2], len(shape)
+    if n != 4 and n != 3:
+        raise ValueError(f"{what}: q must be [tokens, heads, dim] or [batch, seq, heads, dim]")
+    batch, seq, dim = lead[0] if n == 4 else 1, lead[-1], shape[-1]
+    q_out = _empty(shape, dtype, q.device, stream) if q_out is None else q_out
+    first = _heads(what, "q", q, q_out, lead, dim, dtype, at)
     if k is None:
-        k_out = None
-        tensors = _ONE(first)
+        count, k_out, tensors = 1, None, _ROPE_ONE.pack(*first)
     else:
-        kp, (_, _, heads, dim_k), sk = _heads(what, "k", k, lead, dtype, at)
-        if dim_k != dim:
-            raise ValueError(f"{what}: q and k must agree in all but the heads")
         k_out = _empty(k.shape, dtype, k.device, stream) if k_out is None else k_out
-        if k_out.shape != k.shape:
-            raise ValueError(f"{what}: k_out must have the shape of k")
-        op, _, so = _heads(what, "k_out", k_out, lead, dtype, at)
-        tensors = _TWO(first, (kp, op, heads, sk[0], sk[1], sk[2], so[0], so[1], so[2]))
-    if positions.dtype is not torch.int64:
-        raise TypeError(f"{what}: positions must be int64")
-    if positions.shape == lead:
-        steps = positions.stride()
-        pb, ps = steps if len(steps) == 2 else (0, steps[0])
-    elif positions.dim() == 1 and positions.shape[0] == seq:
-        pb, ps = 0, positions.stride(0)
+        count, tensors = 2, _ROPE_TWO.pack(*first, *_heads(what, "k", k, k_out, lead, dim, dtype, at))
+    place, steps = positions.shape, positions.stride()
+    if place == lead:
+        pb, ps = steps if n == 4 else (0, steps[0])
+    elif len(place) == 1 and place[0] == seq:
+        pb, ps = 0, steps[0]
     else:
         raise ValueError(f"{what}: positions must have q's leading shape, or be [seq]")
-    if positions.get_device() != at or freqs.get_device() != at:
-        raise ValueError(f"{what}: tensors on different devices")
+    if positions.dtype is not torch.int64:
+        raise TypeError(f"{what}: positions must be int64")
     if freqs.dtype is not torch.float64 or freqs.dim() != 1 or not freqs.is_contiguous():
         raise TypeError(f"{what}: freqs must be a contiguous 1-D float64 tensor")
-    _call(what, stream, tensors, len(tensors), kind, batch, seq, dim, 2 * freqs.shape[0], layout,
+    if positions.get_device() != at or freqs.get_device() != at:
+        raise ValueError(f"{what}: tensors on different devices")
+    _call(what, stream, tensors, count, kind, batch, seq, dim, 2 * freqs.shape[0], layout,
           positions.data_ptr(), pb, ps, freqs.data_ptr(), scale, 1 if inverse else 0)
     return q_out, k_out
 
@@ -199,12 +195,12 @@ def f8_rope_frequencies(rot: int, base: float = 10000.0, scaling: int = binding.
 
 # ---------------------------------------------------------------- residual stream
 def _residual_norm(what: str, a, r, w_pre, b_pre, w_post, b_post, gate, gate_rows, scale, kind, eps):
-    """The C struct of the call; a's and r's shapes are the caller's to check."""
+    """The C struct of the call, as bytes; a's and r's shapes are the caller's to check."""
     if a.dim() != 2:
         raise TypeError(f"{what} takes 2-D tensors")
     rows, cols = a.shape
     at, shape, wt = a.get_device(), (cols,), w_pre.dtype
-    gt, gp = binding.F8_BF16, None
+    gt, gp = binding.F8_BF16, 0
     if gate is not None:
         gate_rows = max(rows, 1) if gate_rows is None else int(gate_rows)
         if gate_rows < 1:
@@ -215,11 +211,9 @@ def _residual_norm(what: str, a, r, w_pre, b_pre, w_post, b_post, gate, gate_row
         types = _DTYPES[a.dtype], _DTYPES[r.dtype], _DTYPES[wt]
     except KeyError:
         raise TypeError(f"{what} takes bfloat16 or float32 tensors") from None
-    return binding._ResidualNorm(kind, *types, gt, rows, cols, gate_rows or 1, eps, scale,
-                                 _arg(what, "w_pre", w_pre, wt, shape, at),
-                                 _arg(what, "b_pre", b_pre, wt, shape, at),
-                                 _arg(what, "w_post", w_post, wt, shape, at),
-                                 _arg(what, "b_post", b_post, wt, shape, at), gp)
+    return _NORM.pack(kind, *types, gt, rows, cols, gate_rows or 1, eps, scale,
+                      _arg(what, "w_pre", w_pre, wt, shape, at), _arg(what, "b_pre", b_pre, wt, shape, at),
+                      _arg(what, "w_post", w_post, wt, shape, at), _arg(what, "b_post", b_post, wt, shape, at), gp)
 
 
 def f8_residual_norm_fwd(a: torch.Tensor, r: torch.Tensor, w_pre: torch.Tensor,
@@ -240,7 +234,7 @@ def f8_residual_norm_fwd(a: torch.Tensor, r: torch.Tensor, w_pre: torch.Tensor,
     r_out = _empty(shape, rt, a.device, stream) if r_out is None else r_out
     y = _empty(shape, xt, a.device, stream) if y is None else y
     stats = _empty((4, shape[0]), _F32, a.device, stream) if stats is None else stats
-    _call(what, stream, ctypes.byref(n), binding._ptr(a), _arg(what, "r", r, rt, shape, at),
+    _call(what, stream, n, binding._ptr(a), _arg(what, "r", r, rt, shape, at),
           _arg(what, "r_out", r_out, rt, shape, at), _arg(what, "y", y, xt, shape, at),
           _arg(what, "stats", stats, _F32, (4, shape[0]), at), _one(what, "amax_out", amax_out, at))
     return r_out, y, stats
@@ -286,8 +280,7 @@ def f8_residual_norm_bwd(dy: torch.Tensor, dr_out: torch.Tensor | None, a: torch
         out.append(t)
         ptrs.append(_arg(what, name, t, dtype, size, at))
     ws, *space = _ws(what, ws, f8_residual_norm_bwd_workspace_bytes(*shape) if ws is None else 0, a, stream)
-    _call(what, stream, ctypes.byref(n), _arg(what, "dy", dy, xt, shape, at),
+    _call(what, stream, n, _arg(what, "dy", dy, xt, shape, at),
           _arg(what, "dr_out", dr_out, rt, shape, at), binding._ptr(a), _arg(what, "r_out", r_out, rt, shape, at),
-          _arg(what, "stats", stats, _F32, (4, shape[0]), at), ctypes.byref(binding._ResidualNormGrads(*ptrs)),
-          *space)
+          _arg(what, "stats", stats, _F32, (4, shape[0]), at), _GRADS.pack(*ptrs), *space)
     return tuple(out)

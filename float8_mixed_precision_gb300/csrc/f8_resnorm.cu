@@ -281,11 +281,17 @@ __device__ __forceinline__ rows::Slice slice_of(int64_t cols, int per, uint32_t 
 }
 
 // Mean (0 without `layer`) and 1/deviation of the row; x becomes x - mean.
-template <bool VEC, int E>
+template <int MODE, int E>
 __device__ __forceinline__ void row_stats(float2 (&x)[E / 2], int n, bool layer, float inv_c, float eps,
-                                          rows::ClusterSum &sum, float &mu, float &rstd)
+                                          rows::Sum<MODE> &sum, float &mu, float &rstd)
 {
     mu = 0.0f;
+    if (MODE == rows::kFull && layer) {
+        const float2 m = sum.template moments<E>(x);
+        mu = m.x;
+        rstd = rsqrtf(m.y * inv_c + eps);
+        return;
+    }
     if (layer) {
         float2 s = x[0];
 #pragma unroll
@@ -298,10 +304,10 @@ __device__ __forceinline__ void row_stats(float2 (&x)[E / 2], int n, bool layer,
     }
     float2 q = splat(0.0f);
     // columns past the slice are -mean and do not count
-    if constexpr (VEC) {
+    if constexpr (MODE != rows::kRagged) {
 #pragma unroll
         for (int u = 0; u < E / 8; ++u)
-            if (rows::vec_col<VEC>(u) < n) {
+            if (rows::vec_in<MODE>(rows::vec_col(u), n)) {
 #pragma unroll
                 for (int i = 4 * u; i < 4 * u + 4; ++i)
                     q = __ffma2_rn(x[i], x[i], q);
@@ -327,7 +333,7 @@ __device__ __forceinline__ void zero_sums(float *red)
 // A unit (a block, or a cluster by column slices) walks the rows [unit chunk, (unit +
 // 1) chunk).  BF: all parameters are bf16 and stay in registers over the rows; fp32
 // ones are read again for each row, from L1.
-template <typename TA, typename TR, bool VEC, bool BF>
+template <typename TA, typename TR, int MODE, bool BF>
 __global__ void __launch_bounds__(512, 1)
 fwd_kernel(const Call c, const TA *a, const TR *r, TR *r_out, TA *y, unsigned *amax, int64_t chunk,
            int ranks, int slice, int stages, uint64_t limit_ns, unsigned *status)
@@ -337,10 +343,10 @@ fwd_kernel(const Call c, const TA *a, const TR *r, TR *r_out, TA *y, unsigned *a
     __shared__ __align__(16) float red[4 * rows::kMaxParts];
     __shared__ __align__(8) uint64_t full[rows::kMaxStages];
     __shared__ unsigned blk;
-    const uint32_t rank = ranks > 1 ? cluster_ctarank() : 0u;
+    const uint32_t rank = MODE != rows::kFull && ranks > 1 ? cluster_ctarank() : 0u;
     const int64_t unit = blockIdx.x / ranks, first = unit * chunk, stop = min(first + chunk, c.rows);
     const rows::Slice sl = slice_of(c.cols, slice, rank);
-    rows::Slots<TA, 1, TR, 1, VEC> slots;
+    rows::Slots<TA, 1, TR, 1, MODE> slots;
     slots.start(dyn, full, stages, c.cols, c.rows, sl);
     slots.a[0] = a;
     slots.r[0] = r;
@@ -353,22 +359,22 @@ fwd_kernel(const Call c, const TA *a, const TR *r, TR *r_out, TA *y, unsigned *a
     }
     griddep_wait();
     griddep_launch_dependents();
-    if (ranks > 1)
+    if (MODE != rows::kFull && ranks > 1)
         cluster_sync();  // a peer's part of a sum may come from here on
     else
         __syncthreads();
     if (threadIdx.x == 0)
         for (int i = 0; i < stages && first + i < stop; ++i)
             slots.fill(first + i);
-    rows::ClusterSum sum{red, 0, rank, static_cast<uint32_t>(ranks)};
+    rows::Sum<MODE> sum{red, 0, rank, static_cast<uint32_t>(ranks)};
     const float inv_c = 1.0f / static_cast<float>(c.cols);
     const bool post = c.w_post != nullptr, gated = c.gate != nullptr, layer = c.layer != 0;
     Param<E, BF> w1, b1, g, w2, b2;
     if (BF) {
-        rows::take_param<VEC>(c.w_post, 0, sl.first, sl.n, 1.0f, w1);
-        rows::take_param<VEC>(c.b_post, 0, sl.first, sl.n, 0.0f, b1);
-        rows::take_param<VEC>(c.w_pre, 0, sl.first, sl.n, 1.0f, w2);
-        rows::take_param<VEC>(c.b_pre, 0, sl.first, sl.n, 0.0f, b2);
+        rows::take_param<MODE>(c.w_post, 0, sl.first, sl.n, 1.0f, w1);
+        rows::take_param<MODE>(c.b_post, 0, sl.first, sl.n, 0.0f, b1);
+        rows::take_param<MODE>(c.w_pre, 0, sl.first, sl.n, 1.0f, w2);
+        rows::take_param<MODE>(c.b_pre, 0, sl.first, sl.n, 0.0f, b2);
     }
     int64_t gate = gated ? first / c.gate_rows : 0;
     int64_t gate_end = gated ? first : stop, gate_at = 0;
@@ -377,32 +383,32 @@ fwd_kernel(const Call c, const TA *a, const TR *r, TR *r_out, TA *y, unsigned *a
     for (int64_t row = first; row < stop; ++row, at += c.cols) {
         if (gated && row == gate_end) {
             if (BF)
-                rows::take_param<VEC>(c.gate, 0, gate * c.cols + sl.first, sl.n, 1.0f, g);
+                rows::take_param<MODE>(c.gate, 0, gate * c.cols + sl.first, sl.n, 1.0f, g);
             gate_at = gate * c.cols + sl.first;
             ++gate;
             gate_end = min(stop, gate * c.gate_rows);  // within rows + gate_rows
         }
         slots.wait(limit_ns, status);
         int sa = 0, sr = 0;
-        if constexpr (!VEC)
+        if constexpr (MODE == rows::kRagged)
             slots.ragged(row, sa, sr);
         float2 x[P], v[P];
-        rows::take<VEC, E, TA>(slots.at_a(0), sa, sl.n, x);
-        rows::take<VEC, E, TR>(slots.at_r(0), sr, sl.n, v);
+        rows::take<MODE, E, TA>(slots.at_a(0), sa, sl.n, x);
+        rows::take<MODE, E, TR>(slots.at_r(0), sr, sl.n, v);
         float mu1 = 0.0f, s1 = 1.0f;
         if (post) {
-            row_stats<VEC, E>(x, sl.n, layer, inv_c, c.eps, sum, mu1, s1);
+            row_stats<MODE, E>(x, sl.n, layer, inv_c, c.eps, sum, mu1, s1);
             if (!BF)
-                rows::take_param<VEC>(c.w_post, c.w_f32, sl.first, sl.n, 1.0f, w1);
+                rows::take_param<MODE>(c.w_post, c.w_f32, sl.first, sl.n, 1.0f, w1);
             if (!BF)
-                rows::take_param<VEC>(c.b_post, c.w_f32, sl.first, sl.n, 0.0f, b1);
+                rows::take_param<MODE>(c.b_post, c.w_f32, sl.first, sl.n, 0.0f, b1);
 #pragma unroll
             for (int i = 0; i < P; ++i)
                 x[i] = __ffma2_rn(__fmul2_rn(x[i], splat(s1)), w1.pair(i), b1.pair(i));
         }
         if (gated) {
             if (!BF)
-                rows::take_param<VEC>(c.gate, c.g_f32, gate_at, sl.n, 1.0f, g);
+                rows::take_param<MODE>(c.gate, c.g_f32, gate_at, sl.n, 1.0f, g);
 #pragma unroll
             for (int i = 0; i < P; ++i)
                 x[i] = __fmul2_rn(x[i], g.pair(i));
@@ -412,9 +418,9 @@ fwd_kernel(const Call c, const TA *a, const TR *r, TR *r_out, TA *y, unsigned *a
             x[i] = __ffma2_rn(v[i], splat(c.scale), x[i]);
         const bool inside = in_range(at, sl.n, c.rows * c.cols, status);
         if (inside)
-            rows::give<VEC, E>(r_out + at, sl.n, x);
+            rows::give<MODE, E>(r_out + at, sl.n, x);
         float mu2, s2;
-        row_stats<VEC, E>(x, sl.n, layer, inv_c, c.eps, sum, mu2, s2);
+        row_stats<MODE, E>(x, sl.n, layer, inv_c, c.eps, sum, mu2, s2);
         // every thread has taken its columns: the slot may be filled again
         if (threadIdx.x == 0) {
             if (slots.ok && row + stages < stop)
@@ -431,14 +437,14 @@ fwd_kernel(const Call c, const TA *a, const TR *r, TR *r_out, TA *y, unsigned *a
             }
         }
         if (!BF)
-            rows::take_param<VEC>(c.w_pre, c.w_f32, sl.first, sl.n, 1.0f, w2);
+            rows::take_param<MODE>(c.w_pre, c.w_f32, sl.first, sl.n, 1.0f, w2);
         if (!BF)
-            rows::take_param<VEC>(c.b_pre, c.w_f32, sl.first, sl.n, 0.0f, b2);
+            rows::take_param<MODE>(c.b_pre, c.w_f32, sl.first, sl.n, 0.0f, b2);
 #pragma unroll
         for (int i = 0; i < P; ++i)
             x[i] = __ffma2_rn(__fmul2_rn(x[i], splat(s2)), w2.pair(i), b2.pair(i));
         if (inside)
-            rows::give<VEC, E>(y + at, sl.n, x, amax != nullptr ? &m2 : nullptr);
+            rows::give<MODE, E>(y + at, sl.n, x, amax != nullptr ? &m2 : nullptr);
         slots.step();
     }
     if (threadIdx.x == 0)
@@ -454,7 +460,7 @@ fwd_kernel(const Call c, const TA *a, const TR *r, TR *r_out, TA *y, unsigned *a
             atomicMax(amax, blk << 16);  // the maximum does not depend on the order
         }
     }
-    if (ranks > 1)
+    if (MODE != rows::kFull && ranks > 1)
         cluster_sync();  // a peer may still write its part of a sum here
 }
 
@@ -548,7 +554,7 @@ cols_walk_kernel(const Call c, const Chunks ch, const TA *__restrict__ dy, const
 // The backward pass in one: a unit (a block, or a cluster by column slices) walks the
 // chunk `unit` of rows, with the column sums of all gradients in registers.  FULL:
 // with means or biases; without, the sums that only those need are left out.
-template <typename TA, typename TR, bool VEC, bool FULL, bool BF>
+template <typename TA, typename TR, int MODE, bool FULL, bool BF>
 __global__ void __launch_bounds__(512, 1)
 bwd_kernel(const Call c, const Chunks ch, const TA *__restrict__ dy, const TR *__restrict__ dr_out,
            const TA *__restrict__ a, const TR *__restrict__ r_out, TA *__restrict__ da,
@@ -559,11 +565,11 @@ bwd_kernel(const Call c, const Chunks ch, const TA *__restrict__ dy, const TR *_
     extern __shared__ __align__(16) uint8_t dyn[];
     __shared__ __align__(16) float red[4 * rows::kMaxParts];
     __shared__ __align__(8) uint64_t full[rows::kMaxStages];
-    const uint32_t rank = ranks > 1 ? cluster_ctarank() : 0u;
+    const uint32_t rank = MODE != rows::kFull && ranks > 1 ? cluster_ctarank() : 0u;
     const int64_t unit = blockIdx.x / ranks;
     const rows::Slice sl = slice_of(c.cols, slice, rank);
     const int64_t first = ch.first(unit), stop = ch.stop(unit);
-    rows::Slots<TA, 2, TR, 2, VEC> slots;
+    rows::Slots<TA, 2, TR, 2, MODE> slots;
     slots.start(dyn, full, stages, c.cols, c.rows, sl);
     slots.a[0] = dy;
     slots.a[1] = a;
@@ -577,35 +583,35 @@ bwd_kernel(const Call c, const Chunks ch, const TA *__restrict__ dy, const TR *_
     }
     griddep_wait();
     griddep_launch_dependents();
-    if (ranks > 1)
+    if (MODE != rows::kFull && ranks > 1)
         cluster_sync();
     else
         __syncthreads();
     if (threadIdx.x == 0)
         for (int64_t i = 0; i < stages && first + i < stop; ++i)
             slots.fill(first + i);
-    rows::ClusterSum sum{red, 0, rank, static_cast<uint32_t>(ranks)};
+    rows::Sum<MODE> sum{red, 0, rank, static_cast<uint32_t>(ranks)};
     const float inv_c = 1.0f / static_cast<float>(c.cols);
     const bool post = c.w_post != nullptr, gated = c.gate != nullptr, layer = FULL && c.layer;
     Param<E, BF> w2, w1, b1, g;
-    rows::take_param<VEC>(c.w_pre, c.w_f32, sl.first, sl.n, 1.0f, w2);
-    rows::take_param<VEC>(c.w_post, c.w_f32, sl.first, sl.n, 1.0f, w1);
+    rows::take_param<MODE>(c.w_pre, c.w_f32, sl.first, sl.n, 1.0f, w2);
+    rows::take_param<MODE>(c.w_post, c.w_f32, sl.first, sl.n, 1.0f, w1);
     if (FULL)
-        rows::take_param<VEC>(c.b_post, c.w_f32, sl.first, sl.n, 0.0f, b1);
+        rows::take_param<MODE>(c.b_post, c.w_f32, sl.first, sl.n, 0.0f, b1);
     float2 dw2[P], db2[P], dw1[P], db1[P], dg[P];
 #pragma unroll
     for (int i = 0; i < P; ++i)
         dw2[i] = db2[i] = dw1[i] = db1[i] = dg[i] = splat(0.0f);
     int64_t gate = 0, gate_end = gated ? first : stop;
-    rows::take_param<VEC>(nullptr, 0, 0, sl.n, 1.0f, g);
+    rows::take_param<MODE>(nullptr, 0, 0, sl.n, 1.0f, g);
     // what a gate's rows of this chunk have given, into place
     auto flush = [&]() {
         if (dgate == nullptr)
             return;
         if (ch.whole(gate, unit))
-            rows::give_param<VEC, E>(dgate, c.g_f32, gate * c.cols + sl.first, sl.n, dg);
+            rows::give_param<MODE, E>(dgate, c.g_f32, gate * c.cols + sl.first, sl.n, dg);
         else
-            rows::give<VEC, E>(ends + (unit * 2 + ch.slot(gate, unit)) * c.cols + sl.first, sl.n, dg);
+            rows::give<MODE, E>(ends + (unit * 2 + ch.slot(gate, unit)) * c.cols + sl.first, sl.n, dg);
 #pragma unroll
         for (int i = 0; i < P; ++i)
             dg[i] = splat(0.0f);
@@ -631,18 +637,18 @@ bwd_kernel(const Call c, const Chunks ch, const TA *__restrict__ dy, const TR *_
                 flush();
             gate = ch.gate(row);
             gate_end = min(stop, ch.gate_stop(gate));
-            rows::take_param<VEC>(c.gate, c.g_f32, gate * c.cols + sl.first, sl.n, 1.0f, g);
+            rows::take_param<MODE>(c.gate, c.g_f32, gate * c.cols + sl.first, sl.n, 1.0f, g);
         }
         const float mu1 = n_mu1, s1 = n_s1, mu2 = n_mu2, s2 = n_s2;
         if (row + 1 < stop)
             next_stats(row + 1);
         slots.wait(limit_ns, status);
         int sa = 0, sr = 0;
-        if constexpr (!VEC)
+        if constexpr (MODE == rows::kRagged)
             slots.ragged(row, sa, sr);
         float2 h[P], e[P];
-        rows::take<VEC, E, TA>(slots.at_a(0), sa, sl.n, h);
-        rows::take<VEC, E, TR>(slots.at_r(1), sr, sl.n, e);
+        rows::take<MODE, E, TA>(slots.at_a(0), sa, sl.n, h);
+        rows::take<MODE, E, TR>(slots.at_r(1), sr, sl.n, e);
         float2 t1 = splat(0.0f), t2 = splat(0.0f);
 #pragma unroll
         for (int i = 0; i < P; ++i) {
@@ -663,7 +669,7 @@ bwd_kernel(const Call c, const Chunks ch, const TA *__restrict__ dy, const TR *_
         // h becomes D
         float2 o[P];
         if (dr_out != nullptr) {
-            rows::take<VEC, E, TR>(slots.at_r(0), sr, sl.n, o);
+            rows::take<MODE, E, TR>(slots.at_r(0), sr, sl.n, o);
         } else {
 #pragma unroll
             for (int i = 0; i < P; ++i)
@@ -672,13 +678,13 @@ bwd_kernel(const Call c, const Chunks ch, const TA *__restrict__ dy, const TR *_
 #pragma unroll
         for (int i = 0; i < P; ++i)
             h[i] = __fadd2_rn(o[i], __ffma2_rn(h[i], splat(s2), __ffma2_rn(e[i], splat(k1), splat(k2))));
-        rows::take<VEC, E, TA>(slots.at_a(1), sa, sl.n, e);
+        rows::take<MODE, E, TA>(slots.at_a(1), sa, sl.n, e);
         const bool inside = in_range(at, sl.n, c.rows * c.cols, status);
         if (dr != nullptr && inside) {
 #pragma unroll
             for (int i = 0; i < P; ++i)
                 o[i] = __fmul2_rn(h[i], splat(c.scale));
-            rows::give<VEC, E>(dr + at, sl.n, o);
+            rows::give<MODE, E>(dr + at, sl.n, o);
         }
         // e becomes e1 (a without the norm), h du
         t1 = t2 = splat(0.0f);
@@ -706,21 +712,21 @@ bwd_kernel(const Call c, const Chunks ch, const TA *__restrict__ dy, const TR *_
                 h[i] = __ffma2_rn(h[i], splat(s1), __ffma2_rn(e[i], splat(d1), splat(d2)));
         }
         if (da != nullptr && inside)
-            rows::give<VEC, E>(da + at, sl.n, h);
+            rows::give<MODE, E>(da + at, sl.n, h);
         slots.step();
     }
     if (gated && first < stop)
         flush();
     float *p = parts + unit * 4 * c.cols + sl.first;
-    rows::give<VEC, E>(p, sl.n, dw2);
-    rows::give<VEC, E>(p + 2 * c.cols, sl.n, dw1);
+    rows::give<MODE, E>(p, sl.n, dw2);
+    rows::give<MODE, E>(p + 2 * c.cols, sl.n, dw1);
     if (FULL) {
-        rows::give<VEC, E>(p + c.cols, sl.n, db2);
-        rows::give<VEC, E>(p + 3 * c.cols, sl.n, db1);
+        rows::give<MODE, E>(p + c.cols, sl.n, db2);
+        rows::give<MODE, E>(p + 3 * c.cols, sl.n, db1);
     }
     if (threadIdx.x == 0)
         slots.drain();
-    if (ranks > 1)
+    if (MODE != rows::kFull && ranks > 1)
         cluster_sync();
 }
 
@@ -857,6 +863,20 @@ Call call_of(const f8_residual_norm &n, float *stats)
                 n.gate_rows, n.eps, n.scale, n.w_pre, n.b_pre, n.w_post, n.b_post, n.gate, stats};
 }
 
+constexpr std::true_type yes;
+constexpr std::false_type no;
+
+// f(mode) for the rows' width.
+template <typename F>
+cudaError_t by_mode(int64_t cols, const Plan &p, int e, F f)
+{
+    if (cols % 8 != 0)
+        return f(std::integral_constant<int, rows::kRagged>());
+    if (p.ranks == 1 && cols == static_cast<int64_t>(p.threads) * e)
+        return f(std::integral_constant<int, rows::kFull>());
+    return f(std::integral_constant<int, rows::kVec>());
+}
+
 bool params_bf16(const Call &c) { return !c.w_f32 && (c.gate == nullptr || !c.g_f32); }
 
 // Units that run at once, and the slots of each: a launch of more would walk its
@@ -909,18 +929,18 @@ cudaError_t shape_of(const Plan &p, int64_t rows, uint32_t slot_bytes, const Dev
     return cudaSuccess;
 }
 
-template <typename TA, typename TR, bool VEC, bool BF>
+template <typename TA, typename TR, int MODE, bool BF>
 cudaError_t fwd_rows(const Call &c, const void *a, const void *r, void *r_out, void *y, unsigned *amax,
                      const DeviceInfo &dev, cudaStream_t st)
 {
     const Plan p = fwd_plan(c.cols);
     Shape s;
-    const cudaError_t e = shape_of<fwd_kernel<TA, TR, VEC, BF>>(
+    const cudaError_t e = shape_of<fwd_kernel<TA, TR, MODE, BF>>(
         p, c.rows, rows::slice_pitch<TA>(p.slice) + rows::slice_pitch<TR>(p.slice), dev, &s);
     if (e != cudaSuccess)
         return e;
     const int64_t chunk = (c.rows + s.units - 1) / s.units, units = (c.rows + chunk - 1) / chunk;
-    return launch_pdl_cluster(fwd_kernel<TA, TR, VEC, BF>, dim3(static_cast<unsigned>(units * p.ranks)),
+    return launch_pdl_cluster(fwd_kernel<TA, TR, MODE, BF>, dim3(static_cast<unsigned>(units * p.ranks)),
                               dim3(static_cast<unsigned>(p.threads)), s.smem, st,
                               static_cast<unsigned>(p.ranks), c, static_cast<const TA *>(a),
                               static_cast<const TR *>(r), static_cast<TR *>(r_out), static_cast<TA *>(y),
@@ -932,11 +952,11 @@ cudaError_t fwd(const Call &c, const void *a, const void *r, void *r_out, void *
                 const DeviceInfo &dev, cudaStream_t st)
 {
     if (c.cols <= kRegCols) {
-        if (params_bf16(c))
-            return c.cols % 8 == 0 ? fwd_rows<TA, TR, true, true>(c, a, r, r_out, y, amax, dev, st)
-                                   : fwd_rows<TA, TR, false, true>(c, a, r, r_out, y, amax, dev, st);
-        return c.cols % 8 == 0 ? fwd_rows<TA, TR, true, false>(c, a, r, r_out, y, amax, dev, st)
-                               : fwd_rows<TA, TR, false, false>(c, a, r, r_out, y, amax, dev, st);
+        auto run = [&](auto mode, auto bf) {
+            return fwd_rows<TA, TR, mode.value, bf.value>(c, a, r, r_out, y, amax, dev, st);
+        };
+        return params_bf16(c) ? by_mode(c.cols, fwd_plan(c.cols), kFwdE, [&](auto m) { return run(m, yes); })
+                              : by_mode(c.cols, fwd_plan(c.cols), kFwdE, [&](auto m) { return run(m, no); });
     }
     const int64_t grid = std::min<int64_t>(c.rows, 4 * dev.sm_count);
     return launch_pdl(fwd_walk_kernel<TA, TR>, dim3(static_cast<unsigned>(grid)), dim3(kWalkThreads), 0,
@@ -944,20 +964,20 @@ cudaError_t fwd(const Call &c, const void *a, const void *r, void *r_out, void *
                       static_cast<TR *>(r_out), static_cast<TA *>(y), amax, dev.status);
 }
 
-template <typename TA, typename TR, bool VEC, bool FULL, bool BF>
+template <typename TA, typename TR, int MODE, bool FULL, bool BF>
 cudaError_t bwd_rows(const Call &c, Chunks &ch, const void *dy, const void *dr_out, const void *a,
                      const void *r_out, const f8_residual_norm_grads &g, float *parts, float *ends,
                      const DeviceInfo &dev, cudaStream_t st)
 {
     const Plan p = bwd_plan(c.cols);
     Shape s;
-    const cudaError_t e = shape_of<bwd_kernel<TA, TR, VEC, FULL, BF>>(
+    const cudaError_t e = shape_of<bwd_kernel<TA, TR, MODE, FULL, BF>>(
         p, c.rows, 2 * (rows::slice_pitch<TA>(p.slice) + rows::slice_pitch<TR>(p.slice)), dev, &s);
     if (e != cudaSuccess)
         return e;
     ch.chunk = (c.rows + s.units - 1) / s.units;
     const int64_t units = (c.rows + ch.chunk - 1) / ch.chunk;
-    return launch_pdl_cluster(bwd_kernel<TA, TR, VEC, FULL, BF>, dim3(static_cast<unsigned>(units * p.ranks)),
+    return launch_pdl_cluster(bwd_kernel<TA, TR, MODE, FULL, BF>, dim3(static_cast<unsigned>(units * p.ranks)),
                               dim3(static_cast<unsigned>(p.threads)), s.smem, st,
                               static_cast<unsigned>(p.ranks), c, ch, static_cast<const TA *>(dy),
                               static_cast<const TR *>(dr_out), static_cast<const TA *>(a),
@@ -980,17 +1000,17 @@ cudaError_t bwd(const Call &c, const void *dy, const void *dr_out, const void *a
     cudaError_t e;
     if (c.cols <= kRegCols) {
         const bool full = c.layer || c.b_post != nullptr || g.db_pre != nullptr || g.db_post != nullptr;
-        auto run = [&](auto vec, auto all, auto bf) {
-            return bwd_rows<TA, TR, vec.value, all.value, bf.value>(c, ch, dy, dr_out, a, r_out, g, parts, ends,
-                                                                    dev, st);
+        auto run = [&](auto mode, auto all, auto bf) {
+            return bwd_rows<TA, TR, mode.value, all.value, bf.value>(c, ch, dy, dr_out, a, r_out, g, parts,
+                                                                     ends, dev, st);
         };
-        constexpr std::true_type yes;
-        constexpr std::false_type no;
-        const bool vec = c.cols % 8 == 0, bf = params_bf16(c);
-        if (bf)
-            e = vec ? (full ? run(yes, yes, yes) : run(yes, no, yes)) : (full ? run(no, yes, yes) : run(no, no, yes));
+        const Plan p = bwd_plan(c.cols);
+        if (params_bf16(c))
+            e = full ? by_mode(c.cols, p, kBwdE, [&](auto m) { return run(m, yes, yes); })
+                     : by_mode(c.cols, p, kBwdE, [&](auto m) { return run(m, no, yes); });
         else
-            e = vec ? (full ? run(yes, yes, no) : run(yes, no, no)) : (full ? run(no, yes, no) : run(no, no, no));
+            e = full ? by_mode(c.cols, p, kBwdE, [&](auto m) { return run(m, yes, no); })
+                     : by_mode(c.cols, p, kBwdE, [&](auto m) { return run(m, no, no); });
     } else {
         float *consts = reinterpret_cast<float *>(ws + w.consts);
         const auto *dy_ = static_cast<const TA *>(dy), *a_ = static_cast<const TA *>(a);

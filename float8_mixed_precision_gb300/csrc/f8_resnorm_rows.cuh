@@ -18,6 +18,11 @@ constexpr int kMaxStages = 8;
 constexpr int kMaxCluster = 4;
 constexpr int kMaxParts = 64;  // warps of a cluster
 
+// How a block's threads lie over its columns.
+constexpr int kFull = 0;    // E / 8 vectors of eight each, all within the row, one block a row
+constexpr int kVec = 1;     // the same for any whole vectors, of a cluster's slice
+constexpr int kRagged = 2;  // element by element
+
 // The elements [begin, begin + n) of a tensor of `total` as the 16-byte pieces that
 // hold them; the piece that would reach past the tensor's end is not copied.
 template <typename T>
@@ -52,8 +57,8 @@ struct Slice {
 };
 
 // NA tensors of TA and NR of TR; a slot holds a slice of each.  Of the pointers, NULL
-// ones are left out.  VEC: every slice is whole 16-byte pieces.
-template <typename TA, int NA, typename TR, int NR, bool VEC>
+// ones are left out.
+template <typename TA, int NA, typename TR, int NR, int MODE>
 struct Slots {
     uint8_t *mem;
     uint64_t *full;
@@ -103,7 +108,7 @@ struct Slots {
         const int64_t b = begin(row);
         int64_t fa = b, fr = b;
         uint32_t ba = slice.n * sizeof(TA), br = slice.n * sizeof(TR);
-        if constexpr (!VEC) {
+        if constexpr (MODE == kRagged) {
             const Window<TA> wa(b, slice.n, total);
             const Window<TR> wr(b, slice.n, total);
             fa = wa.first, fr = wr.first, ba = wa.bytes, br = wr.bytes;
@@ -196,10 +201,9 @@ __device__ __forceinline__ uint32_t pack2(float2 f)
     return *reinterpret_cast<uint32_t *>(&h);
 }
 
-// A thread's E columns as pairs.  VEC: E / 8 vectors of eight, vector u at column
-// 8 (u T + t); else columns t + j T, pair i being j = 2i and 2i + 1.  T is the block's
-// size.  Columns past the slice are 0 and are not stored.
-template <bool VEC>
+// A thread's E columns as pairs.  In vectors: vector u at column 8 (u T + t); ragged:
+// columns t + j T, pair i being j = 2i and 2i + 1.  T is the block's size.  Columns past
+// the slice are 0 and are not stored.
 __device__ __forceinline__ int vec_col(int u)
 {
     return 8 * (u * static_cast<int>(blockDim.x) + static_cast<int>(threadIdx.x));
@@ -208,16 +212,21 @@ __device__ __forceinline__ int elem_col(int j)
 {
     return static_cast<int>(threadIdx.x) + j * static_cast<int>(blockDim.x);
 }
+template <int MODE>
+__device__ __forceinline__ bool vec_in(int c, int n)
+{
+    return MODE == kFull || c < n;
+}
 
-template <bool VEC, int E, typename T>
+template <int MODE, int E, typename T>
 __device__ __forceinline__ void take(const uint8_t *slot, int shift, int n, float2 (&f)[E / 2])
 {
-    if constexpr (VEC) {
+    if constexpr (MODE != kRagged) {
 #pragma unroll
         for (int u = 0; u < E / 8; ++u) {
-            const int c = vec_col<VEC>(u);
+            const int c = vec_col(u);
             uint4 v = make_uint4(0u, 0u, 0u, 0u), w = v;
-            if (c < n) {
+            if (vec_in<MODE>(c, n)) {
                 const uint4 *p = reinterpret_cast<const uint4 *>(slot + static_cast<size_t>(c) * sizeof(T));
                 v = p[0];
                 if (sizeof(T) == 4)
@@ -266,7 +275,7 @@ struct Param<E, true> {
 
 // A row of parameters in global memory, from element `at`, bf16 or fp32 (BF: bf16); 0
 // past the slice, `none` throughout where there is no parameter.
-template <bool VEC, int E, bool BF>
+template <int MODE, int E, bool BF>
 __device__ __forceinline__ void take_param(const void *p, int f32, int64_t at, int n, float none,
                                            Param<E, BF> &out)
 {
@@ -275,11 +284,11 @@ __device__ __forceinline__ void take_param(const void *p, int f32, int64_t at, i
         out.set(i, p == nullptr ? make_float2(none, none) : make_float2(0.0f, 0.0f));
     if (p == nullptr)
         return;
-    if constexpr (VEC) {
+    if constexpr (MODE != kRagged) {
 #pragma unroll
         for (int u = 0; u < E / 8; ++u) {
-            const int c = vec_col<VEC>(u);
-            if (c >= n)
+            const int c = vec_col(u);
+            if (!vec_in<MODE>(c, n))
                 continue;
             if (!BF && f32) {
                 const float4 *q = reinterpret_cast<const float4 *>(static_cast<const float *>(p) + at + c);
@@ -316,14 +325,14 @@ __device__ __forceinline__ void take_param(const void *p, int f32, int64_t at, i
 
 // The thread's columns to `p` (the slice's first element), rounded to T.  `seen`
 // gathers the largest magnitude of the stored bf16 values.
-template <bool VEC, int E, typename T>
+template <int MODE, int E, typename T>
 __device__ __forceinline__ void give(T *p, int n, const float2 (&f)[E / 2], uint32_t *seen = nullptr)
 {
-    if constexpr (VEC) {
+    if constexpr (MODE != kRagged) {
 #pragma unroll
         for (int u = 0; u < E / 8; ++u) {
-            const int c = vec_col<VEC>(u);
-            if (c >= n)
+            const int c = vec_col(u);
+            if (!vec_in<MODE>(c, n))
                 continue;
             uint4 *q = reinterpret_cast<uint4 *>(p + c);
             const float2 *g = f + 4 * u;
@@ -362,31 +371,34 @@ __device__ __forceinline__ void give(T *p, int n, const float2 (&f)[E / 2], uint
 }
 
 // The thread's columns of one row of a gradient in type `f32` (else bf16).
-template <bool VEC, int E>
+template <int MODE, int E>
 __device__ __forceinline__ void give_param(void *p, int f32, int64_t at, int n, const float2 (&f)[E / 2])
 {
     if (f32)
-        give<VEC, E>(static_cast<float *>(p) + at, n, f);
+        give<MODE, E>(static_cast<float *>(p) + at, n, f);
     else
-        give<VEC, E>(static_cast<__nv_bfloat16 *>(p) + at, n, f);
+        give<MODE, E>(static_cast<__nv_bfloat16 *>(p) + at, n, f);
 }
 
-// Sums over the cluster's blocks in a fixed order; every thread gets them.  Each warp
-// leaves its parts in every block of the cluster, so one barrier a sum; the two halves
-// of `red` [2][2][kMaxParts] are used in turn.  `red` starts as zeros: the parts are
-// read four at a time.
-struct ClusterSum {
+// Sums over the block, or over the cluster's blocks, in a fixed order; every thread
+// gets them.  Each warp leaves its parts (in every block of a cluster), so there is one
+// barrier a sum; the two halves of `red` [2][2][kMaxParts] are used in turn.  `red`
+// starts as zeros: parts are read four at a time.
+template <int MODE>
+struct Sum {
     float *red;
     int half;
     uint32_t rank, ranks;
 
+    __device__ __forceinline__ bool single() const { return MODE == kFull || ranks == 1; }
     __device__ __forceinline__ void leave(float *to, float v, bool mine)
     {
-        const uint32_t part = rank * (blockDim.x >> 5) + (threadIdx.x >> 5);
-        if (ranks == 1) {
+        const uint32_t w = threadIdx.x >> 5;
+        if (single()) {
             if (mine)
-                to[part] = v;
+                to[w] = v;
         } else if (mine) {
+            const uint32_t part = rank * (blockDim.x >> 5) + w;
             for (uint32_t k = 0; k < ranks; ++k)
                 asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(cluster_map(smem_addr(to + part), k)), "f"(v)
                              : "memory");
@@ -394,29 +406,47 @@ struct ClusterSum {
     }
     __device__ __forceinline__ void meet() const
     {
-        if (ranks == 1)
+        if (single())
             __syncthreads();
         else
             cluster_sync();
     }
     __device__ __forceinline__ float total(const float *from) const
     {
-        const int parts = static_cast<int>(ranks * (blockDim.x >> 5));
         float2 s = make_float2(0.0f, 0.0f);
-        for (int i = 0; i < parts; i += 4) {
-            const float4 v = *reinterpret_cast<const float4 *>(from + i);
-            s = __fadd2_rn(s, __fadd2_rn(make_float2(v.x, v.y), make_float2(v.z, v.w)));
+        if (single()) {  // at most 16 warps
+#pragma unroll
+            for (int i = 0; i < 16; i += 4) {
+                const float4 v = *reinterpret_cast<const float4 *>(from + i);
+                s = __fadd2_rn(s, __fadd2_rn(make_float2(v.x, v.y), make_float2(v.z, v.w)));
+            }
+        } else {
+            const int parts = static_cast<int>(ranks * (blockDim.x >> 5));
+            for (int i = 0; i < parts; i += 4) {
+                const float4 v = *reinterpret_cast<const float4 *>(from + i);
+                s = __fadd2_rn(s, __fadd2_rn(make_float2(v.x, v.y), make_float2(v.z, v.w)));
+            }
         }
         return s.x + s.y;
     }
-
-    __device__ __forceinline__ float operator()(float a)
+    __device__ __forceinline__ float *next()
+    {
+        float *r = red + half * 2 * kMaxParts;
+        half ^= 1;
+        return r;
+    }
+    static __device__ __forceinline__ float warp(float a)
     {
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1)
             a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
-        float *r = red + half * 2 * kMaxParts;
-        half ^= 1;
+        return a;
+    }
+
+    __device__ __forceinline__ float operator()(float a)
+    {
+        a = warp(a);
+        float *r = next();
         leave(r, a, (threadIdx.x & 31) == 0);
         meet();
         return total(r);
@@ -430,11 +460,57 @@ struct ClusterSum {
 #pragma unroll
         for (int o = 8; o > 0; o >>= 1)
             v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-        float *r = red + half * 2 * kMaxParts;
-        half ^= 1;
+        float *r = next();
         leave(r + (upper ? kMaxParts : 0), v, (threadIdx.x & 15) == 0);
         meet();
         return make_float2(total(r), total(r + kMaxParts));
+    }
+    // Mean of the row and sum of the squared differences to it, from a full block's
+    // warps of 32 E values each: a warp takes its own mean and its values' differences
+    // to that, and the warps are joined by their means' differences to the row's.  As
+    // exact as two passes, with one barrier.  x becomes x - mean.
+    template <int E>
+    __device__ __forceinline__ float2 moments(float2 (&x)[E / 2])
+    {
+        constexpr float kCount = 32.0f * E;
+        float2 s = x[0];
+#pragma unroll
+        for (int i = 1; i < E / 2; ++i)
+            s = __fadd2_rn(s, x[i]);
+        const float mean = warp(s.x + s.y) * (1.0f / kCount);
+        float2 q = make_float2(0.0f, 0.0f);
+        const float2 nm = make_float2(-mean, -mean);
+#pragma unroll
+        for (int i = 0; i < E / 2; ++i) {
+            const float2 d = __fadd2_rn(x[i], nm);
+            q = __ffma2_rn(d, d, q);
+        }
+        const float m2 = warp(q.x + q.y);
+        float *r = next();
+        leave(r, mean, (threadIdx.x & 31) == 0);
+        leave(r + kMaxParts, m2, (threadIdx.x & 31) == 0);
+        meet();
+        const int w = static_cast<int>(blockDim.x >> 5);
+        const float mu = total(r) / static_cast<float>(w);
+        float2 between = make_float2(0.0f, 0.0f);
+        const float2 nu = make_float2(-mu, -mu);
+#pragma unroll
+        for (int i = 0; i < 16; i += 4) {
+            const float4 v = *reinterpret_cast<const float4 *>(r + i);
+            const float2 a = __fadd2_rn(make_float2(v.x, v.y), nu), b = __fadd2_rn(make_float2(v.z, v.w), nu);
+            if (i < w)
+                between.x = fmaf(a.x, a.x, between.x);
+            if (i + 1 < w)
+                between.y = fmaf(a.y, a.y, between.y);
+            if (i + 2 < w)
+                between.x = fmaf(b.x, b.x, between.x);
+            if (i + 3 < w)
+                between.y = fmaf(b.y, b.y, between.y);
+        }
+#pragma unroll
+        for (int i = 0; i < E / 2; ++i)
+            x[i] = __fadd2_rn(x[i], nu);
+        return make_float2(mu, fmaf(between.x + between.y, kCount, total(r + kMaxParts)));
     }
 };
 

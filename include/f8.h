@@ -806,7 +806,7 @@ f8_status f8_gemm_act(const uint8_t *a, f8_format fmt_a, const uint8_t *b, f8_fo
  *   amax_out: device fp32 receiving max |dz| as stored (needs dz), or NULL; zeroed
  *             by the call.
  *   workspace: f8_act_bwd_workspace_bytes(rows, cols) bytes, 16-byte aligned;
- *             may be NULL if dbias is.
+ *             may be NULL if dbias is or no bytes are needed.
  * The sums over rows are formed in a fixed order: equal inputs give equal bits.
  * rows, cols >= 0; cols < 2^30 and rows * cols < 2^60.
  */

@@ -43,14 +43,15 @@ def test_gemm_act_refusals(L):
 
 def test_act_bwd_refusals(L):
     #      dy z act rows cols dz dbias type amax ws bytes stream
-    ok = (P, P, 3, 8, 64, P, P, 0, P, P, 1 << 20, None)
+    ok = (P, P, 3, 640, 64, P, P, 0, P, P, 1 << 20, None)
     _refuse(L.f8_act_bwd, ok, [
         (0, None, INVALID), (1, None, INVALID), (2, 6, INVALID), (3, -1, INVALID), (4, -1, INVALID),
         (5, None, INVALID),                                  # an amax needs dz
         (7, 3, INVALID), (9, None, INVALID), (10, 16, INVALID), (4, 1 << 30, SHAPE), (3, 1 << 60, SHAPE),
         (0, P8, ALIGN), (1, P8, ALIGN), (5, P8, ALIGN), (6, P8, ALIGN), (9, P8, ALIGN), (8, P2, ALIGN)])
     assert L.f8_act_bwd_workspace_bytes(0, 64) == 0
-    assert L.f8_act_bwd_workspace_bytes(8, 64) >= 64 * 4
+    assert L.f8_act_bwd_workspace_bytes(8, 64) == 0          # one chunk of rows: the sums are the result
+    assert L.f8_act_bwd_workspace_bytes(8, 65) >= 65 * 4 and L.f8_act_bwd_workspace_bytes(640, 64) >= 20 * 64 * 4
 
 
 def _rope_args(**kw):
