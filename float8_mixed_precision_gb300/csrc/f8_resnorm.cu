@@ -280,9 +280,31 @@ __device__ __forceinline__ rows::Slice slice_of(int64_t cols, int per, uint32_t 
     return s;
 }
 
+// The rows of a unit: every one of a chunk's, or (kShift) every eighth, eight units
+// sharing a chunk of a multiple of eight rows.
+template <int MODE>
+struct Walk {
+    static constexpr int kStep = MODE == rows::kShift ? 8 : 1;
+    int64_t chunk;  // number
+    int64_t first, stop;
+    int shift;
+    __device__ __forceinline__ Walk(int64_t unit, int64_t rows_of_chunk, int64_t rows, int64_t cols)
+    {
+        chunk = unit / kStep;
+        first = chunk * rows_of_chunk + unit % kStep;
+        stop = min((chunk + 1) * rows_of_chunk, rows);
+        shift = MODE == rows::kShift ? static_cast<int>((first * cols) & 7) : 0;
+    }
+    // columns, or the positions that hold them in whole vectors
+    __device__ __forceinline__ int64_t width(int64_t cols) const
+    {
+        return MODE == rows::kShift ? (shift + cols + 7) & ~int64_t{7} : cols;
+    }
+};
+
 // Mean (0 without `layer`) and 1/deviation of the row; x becomes x - mean.
 template <int MODE, int E>
-__device__ __forceinline__ void row_stats(float2 (&x)[E / 2], int n, bool layer, float inv_c, float eps,
+__device__ __forceinline__ void row_stats(float2 (&x)[E / 2], const rows::Place<MODE, E> &pl, bool layer, float inv_c, float eps,
                                           rows::Sum<MODE> &sum, float &mu, float &rstd)
 {
     mu = 0.0f;
@@ -303,8 +325,15 @@ __device__ __forceinline__ void row_stats(float2 (&x)[E / 2], int n, bool layer,
             x[i] = __fadd2_rn(x[i], splat(-mu));
     }
     float2 q = splat(0.0f);
-    // columns past the slice are -mean and do not count
-    if constexpr (MODE != rows::kRagged) {
+    // places past the slice are -mean and do not count
+    [[maybe_unused]] const int n = pl.n;
+    if constexpr (MODE == rows::kShift) {
+        if (layer)
+            rows::mask<E>(pl, x);
+#pragma unroll
+        for (int i = 0; i < E / 2; ++i)
+            q = __ffma2_rn(x[i], x[i], q);
+    } else if constexpr (MODE != rows::kRagged) {
 #pragma unroll
         for (int u = 0; u < E / 8; ++u)
             if (rows::vec_in<MODE>(rows::vec_col(u), n)) {
@@ -324,6 +353,14 @@ __device__ __forceinline__ void row_stats(float2 (&x)[E / 2], int n, bool layer,
     rstd = rsqrtf(sum(q.x + q.y) * inv_c + eps);
 }
 
+// The checked build's test of a row's slice: of kShift's, whose first and last vectors
+// are shared with other rows, the part that is the tensor's.
+template <int MODE>
+__device__ __forceinline__ bool inside_of(int64_t at, int n, int64_t total, unsigned *status)
+{
+    return in_range(at, MODE == rows::kShift ? min(static_cast<int64_t>(n), total - at) : n, total, status);
+}
+
 __device__ __forceinline__ void zero_sums(float *red)
 {
     for (int i = threadIdx.x; i < 4 * rows::kMaxParts; i += blockDim.x)
@@ -341,19 +378,25 @@ fwd_kernel(const Call c, const TA *a, const TR *r, TR *r_out, TA *y, unsigned *a
     constexpr int E = kFwdE, P = E / 2;
     extern __shared__ __align__(16) uint8_t dyn[];
     __shared__ __align__(16) float red[4 * rows::kMaxParts];
-    __shared__ __align__(8) uint64_t full[rows::kMaxStages];
+    __shared__ __align__(8) uint64_t full[rows::kMaxStages], meets[2];
     __shared__ unsigned blk;
     const uint32_t rank = MODE != rows::kFull && ranks > 1 ? cluster_ctarank() : 0u;
-    const int64_t unit = blockIdx.x / ranks, first = unit * chunk, stop = min(first + chunk, c.rows);
-    const rows::Slice sl = slice_of(c.cols, slice, rank);
+    const Walk<MODE> walk(blockIdx.x / ranks, chunk, c.rows, c.cols);
+    constexpr int kStep = Walk<MODE>::kStep;
+    const int64_t first = walk.first, stop = walk.stop;
+    const rows::Slice sl = slice_of(walk.width(c.cols), slice, rank);
+    rows::Place<MODE, E> pl;
+    pl.set(sl.first, sl.n, walk.shift, static_cast<int>(c.cols));
     rows::Slots<TA, 1, TR, 1, MODE> slots;
-    slots.start(dyn, full, stages, c.cols, c.rows, sl);
+    slots.start(dyn, full, stages, c.cols, c.rows, sl, walk.shift);
     slots.a[0] = a;
     slots.r[0] = r;
     zero_sums(red);
     if (threadIdx.x == 0) {
         for (int i = 0; i < stages; ++i)
             mbar_init(&full[i], 1);
+        mbar_init(&meets[0], 1);
+        mbar_init(&meets[1], 1);
         fence_mbar_init();
         blk = 0u;
     }
@@ -364,27 +407,29 @@ fwd_kernel(const Call c, const TA *a, const TR *r, TR *r_out, TA *y, unsigned *a
     else
         __syncthreads();
     if (threadIdx.x == 0)
-        for (int i = 0; i < stages && first + i < stop; ++i)
-            slots.fill(first + i);
-    rows::Sum<MODE> sum{red, 0, rank, static_cast<uint32_t>(ranks)};
+        for (int i = 0; i < stages && first + i * kStep < stop; ++i)
+            slots.fill(first + i * kStep);
+    rows::Sum<MODE> sum;
+    sum.start(red, meets, rank, static_cast<uint32_t>(ranks), limit_ns, status);
     const float inv_c = 1.0f / static_cast<float>(c.cols);
     const bool post = c.w_post != nullptr, gated = c.gate != nullptr, layer = c.layer != 0;
     Param<E, BF> w1, b1, g, w2, b2;
     if (BF) {
-        rows::take_param<MODE>(c.w_post, 0, sl.first, sl.n, 1.0f, w1);
-        rows::take_param<MODE>(c.b_post, 0, sl.first, sl.n, 0.0f, b1);
-        rows::take_param<MODE>(c.w_pre, 0, sl.first, sl.n, 1.0f, w2);
-        rows::take_param<MODE>(c.b_pre, 0, sl.first, sl.n, 0.0f, b2);
+        rows::take_param<MODE>(c.w_post, 0, 0, pl, 1.0f, w1);
+        rows::take_param<MODE>(c.b_post, 0, 0, pl, 0.0f, b1);
+        rows::take_param<MODE>(c.w_pre, 0, 0, pl, 1.0f, w2);
+        rows::take_param<MODE>(c.b_pre, 0, 0, pl, 0.0f, b2);
     }
     int64_t gate = gated ? first / c.gate_rows : 0;
     int64_t gate_end = gated ? first : stop, gate_at = 0;
     uint32_t m2 = 0u;
     int64_t at = slots.begin(first);
-    for (int64_t row = first; row < stop; ++row, at += c.cols) {
-        if (gated && row == gate_end) {
+    for (int64_t row = first; row < stop; row += kStep, at += kStep * c.cols) {
+        if (gated && row >= gate_end) {
+            gate = MODE == rows::kShift ? row / c.gate_rows : gate;
             if (BF)
-                rows::take_param<MODE>(c.gate, 0, gate * c.cols + sl.first, sl.n, 1.0f, g);
-            gate_at = gate * c.cols + sl.first;
+                rows::take_param<MODE>(c.gate, 0, gate * c.cols, pl, 1.0f, g);
+            gate_at = gate * c.cols;
             ++gate;
             gate_end = min(stop, gate * c.gate_rows);  // within rows + gate_rows
         }
@@ -392,23 +437,25 @@ fwd_kernel(const Call c, const TA *a, const TR *r, TR *r_out, TA *y, unsigned *a
         int sa = 0, sr = 0;
         if constexpr (MODE == rows::kRagged)
             slots.ragged(row, sa, sr);
+        if constexpr (MODE == rows::kShift)
+            slots.tail(row);
         float2 x[P], v[P];
-        rows::take<MODE, E, TA>(slots.at_a(0), sa, sl.n, x);
-        rows::take<MODE, E, TR>(slots.at_r(0), sr, sl.n, v);
+        rows::take<MODE, E, TA>(slots.at_a(0), sa, pl, x);
+        rows::take<MODE, E, TR>(slots.at_r(0), sr, pl, v);
         float mu1 = 0.0f, s1 = 1.0f;
         if (post) {
-            row_stats<MODE, E>(x, sl.n, layer, inv_c, c.eps, sum, mu1, s1);
+            row_stats<MODE, E>(x, pl, layer, inv_c, c.eps, sum, mu1, s1);
             if (!BF)
-                rows::take_param<MODE>(c.w_post, c.w_f32, sl.first, sl.n, 1.0f, w1);
+                rows::take_param<MODE>(c.w_post, c.w_f32, 0, pl, 1.0f, w1);
             if (!BF)
-                rows::take_param<MODE>(c.b_post, c.w_f32, sl.first, sl.n, 0.0f, b1);
+                rows::take_param<MODE>(c.b_post, c.w_f32, 0, pl, 0.0f, b1);
 #pragma unroll
             for (int i = 0; i < P; ++i)
                 x[i] = __ffma2_rn(__fmul2_rn(x[i], splat(s1)), w1.pair(i), b1.pair(i));
         }
         if (gated) {
             if (!BF)
-                rows::take_param<MODE>(c.gate, c.g_f32, gate_at, sl.n, 1.0f, g);
+                rows::take_param<MODE>(c.gate, c.g_f32, gate_at, pl, 1.0f, g);
 #pragma unroll
             for (int i = 0; i < P; ++i)
                 x[i] = __fmul2_rn(x[i], g.pair(i));
@@ -416,15 +463,15 @@ fwd_kernel(const Call c, const TA *a, const TR *r, TR *r_out, TA *y, unsigned *a
 #pragma unroll
         for (int i = 0; i < P; ++i)
             x[i] = __ffma2_rn(v[i], splat(c.scale), x[i]);
-        const bool inside = in_range(at, sl.n, c.rows * c.cols, status);
+        const bool inside = inside_of<MODE>(at, sl.n, c.rows * c.cols, status);
         if (inside)
-            rows::give<MODE, E>(r_out + at, sl.n, x);
+            rows::give<MODE, E>(r_out + at, pl, x);
         float mu2, s2;
-        row_stats<MODE, E>(x, sl.n, layer, inv_c, c.eps, sum, mu2, s2);
+        row_stats<MODE, E>(x, pl, layer, inv_c, c.eps, sum, mu2, s2);
         // every thread has taken its columns: the slot may be filled again
         if (threadIdx.x == 0) {
-            if (slots.ok && row + stages < stop)
-                slots.fill(row + stages);
+            if (slots.ok && row + stages * kStep < stop)
+                slots.fill(row + stages * kStep);
             if (rank == 0) {
                 if (post) {
                     if (layer)
@@ -437,14 +484,14 @@ fwd_kernel(const Call c, const TA *a, const TR *r, TR *r_out, TA *y, unsigned *a
             }
         }
         if (!BF)
-            rows::take_param<MODE>(c.w_pre, c.w_f32, sl.first, sl.n, 1.0f, w2);
+            rows::take_param<MODE>(c.w_pre, c.w_f32, 0, pl, 1.0f, w2);
         if (!BF)
-            rows::take_param<MODE>(c.b_pre, c.w_f32, sl.first, sl.n, 0.0f, b2);
+            rows::take_param<MODE>(c.b_pre, c.w_f32, 0, pl, 0.0f, b2);
 #pragma unroll
         for (int i = 0; i < P; ++i)
             x[i] = __ffma2_rn(__fmul2_rn(x[i], splat(s2)), w2.pair(i), b2.pair(i));
         if (inside)
-            rows::give<MODE, E>(y + at, sl.n, x, amax != nullptr ? &m2 : nullptr);
+            rows::give<MODE, E>(y + at, pl, x, amax != nullptr ? &m2 : nullptr);
         slots.step();
     }
     if (threadIdx.x == 0)
@@ -564,13 +611,17 @@ bwd_kernel(const Call c, const Chunks ch, const TA *__restrict__ dy, const TR *_
     constexpr int E = kBwdE, P = E / 2;
     extern __shared__ __align__(16) uint8_t dyn[];
     __shared__ __align__(16) float red[4 * rows::kMaxParts];
-    __shared__ __align__(8) uint64_t full[rows::kMaxStages];
+    __shared__ __align__(8) uint64_t full[rows::kMaxStages], meets[2];
     const uint32_t rank = MODE != rows::kFull && ranks > 1 ? cluster_ctarank() : 0u;
     const int64_t unit = blockIdx.x / ranks;
-    const rows::Slice sl = slice_of(c.cols, slice, rank);
-    const int64_t first = ch.first(unit), stop = ch.stop(unit);
+    const Walk<MODE> walk(unit, ch.chunk, c.rows, c.cols);
+    constexpr int kStep = Walk<MODE>::kStep;
+    const int64_t first = walk.first, stop = walk.stop;
+    const rows::Slice sl = slice_of(walk.width(c.cols), slice, rank);
+    rows::Place<MODE, E> pl;
+    pl.set(sl.first, sl.n, walk.shift, static_cast<int>(c.cols));
     rows::Slots<TA, 2, TR, 2, MODE> slots;
-    slots.start(dyn, full, stages, c.cols, c.rows, sl);
+    slots.start(dyn, full, stages, c.cols, c.rows, sl, walk.shift);
     slots.a[0] = dy;
     slots.a[1] = a;
     slots.r[0] = dr_out;
@@ -579,6 +630,8 @@ bwd_kernel(const Call c, const Chunks ch, const TA *__restrict__ dy, const TR *_
     if (threadIdx.x == 0) {
         for (int i = 0; i < stages; ++i)
             mbar_init(&full[i], 1);
+        mbar_init(&meets[0], 1);
+        mbar_init(&meets[1], 1);
         fence_mbar_init();
     }
     griddep_wait();
@@ -588,30 +641,36 @@ bwd_kernel(const Call c, const Chunks ch, const TA *__restrict__ dy, const TR *_
     else
         __syncthreads();
     if (threadIdx.x == 0)
-        for (int64_t i = 0; i < stages && first + i < stop; ++i)
-            slots.fill(first + i);
-    rows::Sum<MODE> sum{red, 0, rank, static_cast<uint32_t>(ranks)};
+        for (int64_t i = 0; i < stages && first + i * kStep < stop; ++i)
+            slots.fill(first + i * kStep);
+    rows::Sum<MODE> sum;
+    sum.start(red, meets, rank, static_cast<uint32_t>(ranks), limit_ns, status);
     const float inv_c = 1.0f / static_cast<float>(c.cols);
     const bool post = c.w_post != nullptr, gated = c.gate != nullptr, layer = FULL && c.layer;
     Param<E, BF> w2, w1, b1, g;
-    rows::take_param<MODE>(c.w_pre, c.w_f32, sl.first, sl.n, 1.0f, w2);
-    rows::take_param<MODE>(c.w_post, c.w_f32, sl.first, sl.n, 1.0f, w1);
+    rows::take_param<MODE>(c.w_pre, c.w_f32, 0, pl, 1.0f, w2);
+    rows::take_param<MODE>(c.w_post, c.w_f32, 0, pl, 1.0f, w1);
     if (FULL)
-        rows::take_param<MODE>(c.b_post, c.w_f32, sl.first, sl.n, 0.0f, b1);
+        rows::take_param<MODE>(c.b_post, c.w_f32, 0, pl, 0.0f, b1);
     float2 dw2[P], db2[P], dw1[P], db1[P], dg[P];
 #pragma unroll
     for (int i = 0; i < P; ++i)
         dw2[i] = db2[i] = dw1[i] = db1[i] = dg[i] = splat(0.0f);
     int64_t gate = 0, gate_end = gated ? first : stop;
-    rows::take_param<MODE>(nullptr, 0, 0, sl.n, 1.0f, g);
-    // what a gate's rows of this chunk have given, into place
+    rows::take_param<MODE>(nullptr, 0, 0, pl, 1.0f, g);
+    // What a gate's rows of this unit have given, into place.  Units of kShift share
+    // their chunk's gates, of which there are at most two.
+    int left = 0;  // which of the unit's two partial rows are written
     auto flush = [&]() {
         if (dgate == nullptr)
             return;
-        if (ch.whole(gate, unit))
-            rows::give_param<MODE, E>(dgate, c.g_f32, gate * c.cols + sl.first, sl.n, dg);
-        else
-            rows::give<MODE, E>(ends + (unit * 2 + ch.slot(gate, unit)) * c.cols + sl.first, sl.n, dg);
+        if (MODE != rows::kShift && ch.whole(gate, walk.chunk)) {
+            rows::give_param<MODE, E>(dgate, c.g_f32, gate * c.cols, pl, dg);
+        } else {
+            const int to = ch.slot(gate, walk.chunk);
+            left |= 1 << to;
+            rows::give_sums<MODE, E>(ends + (unit * 2 + to) * c.cols, pl, dg);
+        }
 #pragma unroll
         for (int i = 0; i < P; ++i)
             dg[i] = splat(0.0f);
@@ -631,24 +690,26 @@ bwd_kernel(const Call c, const Chunks ch, const TA *__restrict__ dy, const TR *_
     if (first < stop)
         next_stats(first);
     int64_t at = slots.begin(first);
-    for (int64_t row = first; row < stop; ++row, at += c.cols) {
-        if (row == gate_end) {
+    for (int64_t row = first; row < stop; row += kStep, at += kStep * c.cols) {
+        if (row >= gate_end) {
             if (row > first)
                 flush();
             gate = ch.gate(row);
             gate_end = min(stop, ch.gate_stop(gate));
-            rows::take_param<MODE>(c.gate, c.g_f32, gate * c.cols + sl.first, sl.n, 1.0f, g);
+            rows::take_param<MODE>(c.gate, c.g_f32, gate * c.cols, pl, 1.0f, g);
         }
         const float mu1 = n_mu1, s1 = n_s1, mu2 = n_mu2, s2 = n_s2;
-        if (row + 1 < stop)
-            next_stats(row + 1);
+        if (row + kStep < stop)
+            next_stats(row + kStep);
         slots.wait(limit_ns, status);
         int sa = 0, sr = 0;
         if constexpr (MODE == rows::kRagged)
             slots.ragged(row, sa, sr);
+        if constexpr (MODE == rows::kShift)
+            slots.tail(row);
         float2 h[P], e[P];
-        rows::take<MODE, E, TA>(slots.at_a(0), sa, sl.n, h);
-        rows::take<MODE, E, TR>(slots.at_r(1), sr, sl.n, e);
+        rows::take<MODE, E, TA>(slots.at_a(0), sa, pl, h);
+        rows::take<MODE, E, TR>(slots.at_r(1), sr, pl, e);
         float2 t1 = splat(0.0f), t2 = splat(0.0f);
 #pragma unroll
         for (int i = 0; i < P; ++i) {
@@ -663,13 +724,13 @@ bwd_kernel(const Call c, const Chunks ch, const TA *__restrict__ dy, const TR *_
         }
         float2 k = sum(t1.x + t1.y, t2.x + t2.y);
         // every thread is done with the row before: its slot may be filled again
-        if (threadIdx.x == 0 && slots.ok && row > first && row - 1 + stages < stop)
-            slots.fill(row - 1 + stages);
+        if (threadIdx.x == 0 && slots.ok && row > first && row + (stages - 1) * kStep < stop)
+            slots.fill(row + (stages - 1) * kStep);
         const float k1 = -s2 * (k.x * inv_c), k2 = layer ? -s2 * (k.y * inv_c) : 0.0f;
         // h becomes D
         float2 o[P];
         if (dr_out != nullptr) {
-            rows::take<MODE, E, TR>(slots.at_r(0), sr, sl.n, o);
+            rows::take<MODE, E, TR>(slots.at_r(0), sr, pl, o);
         } else {
 #pragma unroll
             for (int i = 0; i < P; ++i)
@@ -678,13 +739,13 @@ bwd_kernel(const Call c, const Chunks ch, const TA *__restrict__ dy, const TR *_
 #pragma unroll
         for (int i = 0; i < P; ++i)
             h[i] = __fadd2_rn(o[i], __ffma2_rn(h[i], splat(s2), __ffma2_rn(e[i], splat(k1), splat(k2))));
-        rows::take<MODE, E, TA>(slots.at_a(1), sa, sl.n, e);
-        const bool inside = in_range(at, sl.n, c.rows * c.cols, status);
+        rows::take<MODE, E, TA>(slots.at_a(1), sa, pl, e);
+        const bool inside = inside_of<MODE>(at, sl.n, c.rows * c.cols, status);
         if (dr != nullptr && inside) {
 #pragma unroll
             for (int i = 0; i < P; ++i)
                 o[i] = __fmul2_rn(h[i], splat(c.scale));
-            rows::give<MODE, E>(dr + at, sl.n, o);
+            rows::give<MODE, E>(dr + at, pl, o);
         }
         // e becomes e1 (a without the norm), h du
         t1 = t2 = splat(0.0f);
@@ -712,17 +773,23 @@ bwd_kernel(const Call c, const Chunks ch, const TA *__restrict__ dy, const TR *_
                 h[i] = __ffma2_rn(h[i], splat(s1), __ffma2_rn(e[i], splat(d1), splat(d2)));
         }
         if (da != nullptr && inside)
-            rows::give<MODE, E>(da + at, sl.n, h);
+            rows::give<MODE, E>(da + at, pl, h);
         slots.step();
     }
     if (gated && first < stop)
         flush();
-    float *p = parts + unit * 4 * c.cols + sl.first;
-    rows::give<MODE, E>(p, sl.n, dw2);
-    rows::give<MODE, E>(p + 2 * c.cols, sl.n, dw1);
+    if (MODE == rows::kShift && gated && dgate != nullptr) {
+        // a unit without rows of one of them: flush left zeros
+        for (int to = 0; to < 2; ++to)
+            if ((left & (1 << to)) == 0)
+                rows::give_sums<MODE, E>(ends + (unit * 2 + to) * c.cols, pl, dg);
+    }
+    float *p = parts + unit * 4 * c.cols;
+    rows::give_sums<MODE, E>(p, pl, dw2);
+    rows::give_sums<MODE, E>(p + 2 * c.cols, pl, dw1);
     if (FULL) {
-        rows::give<MODE, E>(p + c.cols, sl.n, db2);
-        rows::give<MODE, E>(p + 3 * c.cols, sl.n, db1);
+        rows::give_sums<MODE, E>(p + c.cols, pl, db2);
+        rows::give_sums<MODE, E>(p + 3 * c.cols, pl, db1);
     }
     if (threadIdx.x == 0)
         slots.drain();
@@ -732,14 +799,15 @@ bwd_kernel(const Call c, const Chunks ch, const TA *__restrict__ dy, const TR *_
 
 // The gradients from the partial rows, in a fixed order: 32 columns a block, 32
 // threads a column, each every 32nd row.  blockIdx.y names a parameter's gradient, or
-// from 4 on a gate whose rows may lie in several chunks: gate y - 4 itself where
-// there are no more gates than borders between chunks, else the one that reaches over
-// the border after chunk y - 4.  What a chunk has whole it has written.
+// from 4 on gates whose rows may lie in several chunks: gate y - 4 where there are no
+// more gates than borders between chunks, else those that reach over the borders after
+// the 32 chunks from 32 (y - 4) on.  What a chunk has whole it has written, unless its
+// rows are shared by `units` (kShift), which all leave partial rows.
 struct Sums {
     void *out[4];
     void *dgate;
     const float *parts, *ends;
-    int nparts, w_f32, g_f32, by_border;
+    int nparts, w_f32, g_f32, by_border, units;
     int64_t cols;
 };
 
@@ -766,19 +834,35 @@ reduce_kernel(const __grid_constant__ Sums a, const Chunks ch, unsigned *status)
                 s += p[static_cast<int64_t>(i) * 4 * cols];
         }
     } else {
-        const int64_t y = blockIdx.y - 4, g = a.by_border ? ch.gate(ch.stop(y) - 1) : y;
+        if (a.by_border) {
+            // a thread for each border: its gate reaches into few chunks
+            const int64_t y = (blockIdx.y - 4) * int64_t{32} + k;
+            if (y + 1 >= a.nparts || c >= cols)
+                return;
+            const int64_t g = ch.gate(ch.stop(y) - 1), last = (ch.gate_stop(g) - 1) / ch.chunk;
+            if (last == y || ch.gate_first(g) / ch.chunk != y)
+                return;
+            s = a.ends[(y * 2 + ch.slot(g, y)) * cols + c];
+            for (int64_t i = y + 1; i <= last; ++i)
+                s += a.ends[i * 2 * cols + c];
+            if (in_range(g * cols + c, 1, ((ch.rows - 1) / ch.gate_rows + 1) * cols, status))
+                put_param(a.dgate, a.g_f32, g * cols + c, s);
+            return;
+        }
+        const int64_t g = blockIdx.y - 4;
         const int64_t first = ch.gate_first(g) / ch.chunk, last = (ch.gate_stop(g) - 1) / ch.chunk;
-        if (first == last || (a.by_border && first != y))
+        if (a.units == 1 && first == last)
             return;
         out = a.dgate;
         at = g * cols;
         f32 = a.g_f32;
         // the gate comes first in every chunk but the one that it begins in
         if (c < cols) {
-            if (k == 0)
-                s = a.ends[(first * 2 + ch.slot(g, first)) * cols + c];
+            const int n = a.units;
+            if (k < n)
+                s = a.ends[((first * n + k) * 2 + ch.slot(g, first)) * cols + c];
 #pragma unroll 8
-            for (int64_t i = first + 1 + k; i <= last; i += 32)
+            for (int64_t i = (first + 1) * n + k; i < (last + 1) * n; i += 32)
                 s += a.ends[i * 2 * cols + c];
         }
     }
@@ -796,6 +880,11 @@ reduce_kernel(const __grid_constant__ Sums a, const Chunks ch, unsigned *status)
 // ------------------------------------------------------------ launches
 constexpr int kMaxChunks = 1024;
 constexpr int64_t kRegCols = 16384;  // a cluster's registers hold no more
+
+// Columns, or the positions that an odd width's rows reach into, a vector more than
+// they fill.
+int64_t width_of(int64_t cols) { return cols % 8 == 0 ? cols : cols + 7; }
+bool in_registers(int64_t cols) { return width_of(cols) <= kRegCols; }
 constexpr int kRingBytes = 200 * 1024;
 
 int64_t walk_chunks(int64_t rows, int64_t cols, int sms)
@@ -818,11 +907,12 @@ Plan plan_of(int64_t cols, int e)
     constexpr int kThreads = 512;
     Plan p;
     p.ranks = 1;
-    while (p.ranks * kThreads * e < cols)
+    while (p.ranks * kThreads * e < width_of(cols))
         p.ranks *= 2;
-    p.slice = static_cast<int>((cols + 8 * p.ranks - 1) / (8 * p.ranks)) * 8;
+    const int64_t width = width_of(cols);
+    p.slice = static_cast<int>((width + 8 * p.ranks - 1) / (8 * p.ranks)) * 8;
     p.threads = (p.slice + 32 * e - 1) / (32 * e) * 32;
-    p.per_sm = std::max(1, std::min(8, kThreads / p.threads));
+    p.per_sm = std::max(1, std::min(16, kThreads / p.threads));
     return p;
 }
 
@@ -833,7 +923,7 @@ Plan bwd_plan(int64_t cols) { return plan_of(cols, kBwdE); }
 int64_t bwd_units(int64_t rows, int64_t cols, int sms)
 {
     const Plan p = bwd_plan(cols);
-    return std::max<int64_t>(1, std::min<int64_t>(rows, static_cast<int64_t>(sms) * p.per_sm / p.ranks));
+    return std::max<int64_t>(8, std::min<int64_t>((rows + 7) / 8 * 8, static_cast<int64_t>(sms) * p.per_sm / p.ranks));
 }
 
 size_t round256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
@@ -846,7 +936,7 @@ struct Workspace {
 
 Workspace workspace_of(int64_t rows, int64_t cols, int sms)
 {
-    const bool walk = cols > kRegCols;
+    const bool walk = !in_registers(cols);
     const size_t n = static_cast<size_t>(walk ? walk_chunks(rows, cols, sms) : bwd_units(rows, cols, sms));
     const size_t row = static_cast<size_t>(cols) * sizeof(float);
     Workspace w;
@@ -868,8 +958,10 @@ constexpr std::false_type no;
 
 // f(mode) for the rows' width.
 template <typename F>
-cudaError_t by_mode(int64_t cols, const Plan &p, int e, F f)
+cudaError_t by_mode(int64_t cols, const Plan &p, int e, bool shift, F f)
 {
+    if (cols % 8 != 0 && shift)
+        return f(std::integral_constant<int, rows::kShift>());
     if (cols % 8 != 0)
         return f(std::integral_constant<int, rows::kRagged>());
     if (p.ranks == 1 && cols == static_cast<int64_t>(p.threads) * e)
@@ -882,12 +974,13 @@ bool params_bf16(const Call &c) { return !c.w_f32 && (c.gate == nullptr || !c.g_
 // Units that run at once, and the slots of each: a launch of more would walk its
 // last chunks alone.
 struct Shape {
-    int units, stages;
+    int64_t most;
+    int stages;
     size_t smem;
 };
 
 template <auto Kernel>
-cudaError_t shape_of(const Plan &p, int64_t rows, uint32_t slot_bytes, const DeviceInfo &dev, Shape *out)
+cudaError_t shape_of(const Plan &p, uint32_t slot_bytes, const DeviceInfo &dev, Shape *out)
 {
     static std::once_flag once[64];
     static cudaError_t err[64];
@@ -925,8 +1018,22 @@ cudaError_t shape_of(const Plan &p, int64_t rows, uint32_t slot_bytes, const Dev
         }
         units = std::min<int64_t>(units, n);
     }
-    out->units = static_cast<int>(std::max<int64_t>(1, std::min(units, rows)));
+    out->most = std::max<int64_t>(1, units);
     return cudaSuccess;
+}
+
+// Rows of a chunk and the units that walk them, for at most `most` units at once (but
+// eight, kShift's for one chunk).
+template <int MODE>
+int64_t chunk_rows(int64_t rows, int64_t most, int64_t *chunk)
+{
+    if (MODE != rows::kShift) {
+        *chunk = (rows + std::min(most, rows) - 1) / std::min(most, rows);
+        return (rows + *chunk - 1) / *chunk;
+    }
+    const int64_t n = std::max<int64_t>(1, std::min(most / 8, (rows + 7) / 8));
+    *chunk = (rows + 8 * n - 1) / (8 * n) * 8;
+    return (rows + *chunk - 1) / *chunk * 8;
 }
 
 template <typename TA, typename TR, int MODE, bool BF>
@@ -936,10 +1043,11 @@ cudaError_t fwd_rows(const Call &c, const void *a, const void *r, void *r_out, v
     const Plan p = fwd_plan(c.cols);
     Shape s;
     const cudaError_t e = shape_of<fwd_kernel<TA, TR, MODE, BF>>(
-        p, c.rows, rows::slice_pitch<TA>(p.slice) + rows::slice_pitch<TR>(p.slice), dev, &s);
+        p, rows::slice_pitch<TA>(p.slice) + rows::slice_pitch<TR>(p.slice), dev, &s);
     if (e != cudaSuccess)
         return e;
-    const int64_t chunk = (c.rows + s.units - 1) / s.units, units = (c.rows + chunk - 1) / chunk;
+    int64_t chunk;
+    const int64_t units = chunk_rows<MODE>(c.rows, s.most, &chunk);
     return launch_pdl_cluster(fwd_kernel<TA, TR, MODE, BF>, dim3(static_cast<unsigned>(units * p.ranks)),
                               dim3(static_cast<unsigned>(p.threads)), s.smem, st,
                               static_cast<unsigned>(p.ranks), c, static_cast<const TA *>(a),
@@ -951,12 +1059,12 @@ template <typename TA, typename TR>
 cudaError_t fwd(const Call &c, const void *a, const void *r, void *r_out, void *y, unsigned *amax,
                 const DeviceInfo &dev, cudaStream_t st)
 {
-    if (c.cols <= kRegCols) {
+    if (in_registers(c.cols)) {
         auto run = [&](auto mode, auto bf) {
             return fwd_rows<TA, TR, mode.value, bf.value>(c, a, r, r_out, y, amax, dev, st);
         };
-        return params_bf16(c) ? by_mode(c.cols, fwd_plan(c.cols), kFwdE, [&](auto m) { return run(m, yes); })
-                              : by_mode(c.cols, fwd_plan(c.cols), kFwdE, [&](auto m) { return run(m, no); });
+        return params_bf16(c) ? by_mode(c.cols, fwd_plan(c.cols), kFwdE, params_bf16(c), [&](auto m) { return run(m, yes); })
+                              : by_mode(c.cols, fwd_plan(c.cols), kFwdE, params_bf16(c), [&](auto m) { return run(m, no); });
     }
     const int64_t grid = std::min<int64_t>(c.rows, 4 * dev.sm_count);
     return launch_pdl(fwd_walk_kernel<TA, TR>, dim3(static_cast<unsigned>(grid)), dim3(kWalkThreads), 0,
@@ -965,18 +1073,23 @@ cudaError_t fwd(const Call &c, const void *a, const void *r, void *r_out, void *
 }
 
 template <typename TA, typename TR, int MODE, bool FULL, bool BF>
-cudaError_t bwd_rows(const Call &c, Chunks &ch, const void *dy, const void *dr_out, const void *a,
+cudaError_t bwd_rows(const Call &c, Chunks &ch, int *shared, const void *dy, const void *dr_out, const void *a,
                      const void *r_out, const f8_residual_norm_grads &g, float *parts, float *ends,
                      const DeviceInfo &dev, cudaStream_t st)
 {
     const Plan p = bwd_plan(c.cols);
     Shape s;
     const cudaError_t e = shape_of<bwd_kernel<TA, TR, MODE, FULL, BF>>(
-        p, c.rows, 2 * (rows::slice_pitch<TA>(p.slice) + rows::slice_pitch<TR>(p.slice)), dev, &s);
+        p, 2 * (rows::slice_pitch<TA>(p.slice) + rows::slice_pitch<TR>(p.slice)), dev, &s);
     if (e != cudaSuccess)
         return e;
-    ch.chunk = (c.rows + s.units - 1) / s.units;
-    const int64_t units = (c.rows + ch.chunk - 1) / ch.chunk;
+    const int64_t units = chunk_rows<MODE>(c.rows, s.most, &ch.chunk);
+    *shared = MODE == rows::kShift ? 8 : 1;
+    // kShift's units have room for two gates of their chunk
+    if constexpr (MODE == rows::kShift)
+        if (c.gate != nullptr && c.gate_rows < ch.chunk)
+            return bwd_rows<TA, TR, rows::kRagged, FULL, BF>(c, ch, shared, dy, dr_out, a, r_out, g, parts, ends,
+                                                             dev, st);
     return launch_pdl_cluster(bwd_kernel<TA, TR, MODE, FULL, BF>, dim3(static_cast<unsigned>(units * p.ranks)),
                               dim3(static_cast<unsigned>(p.threads)), s.smem, st,
                               static_cast<unsigned>(p.ranks), c, ch, static_cast<const TA *>(dy),
@@ -997,20 +1110,21 @@ cudaError_t bwd(const Call &c, const void *dy, const void *dr_out, const void *a
     float *ends = reinterpret_cast<float *>(ws + w.ends);
     const unsigned strips = static_cast<unsigned>((c.cols + 255) / 256);
     Chunks ch{c.rows, c.gate != nullptr ? c.gate_rows : c.rows, 0};
+    int shared = 1;  // units that share a chunk
     cudaError_t e;
-    if (c.cols <= kRegCols) {
+    if (in_registers(c.cols)) {
         const bool full = c.layer || c.b_post != nullptr || g.db_pre != nullptr || g.db_post != nullptr;
         auto run = [&](auto mode, auto all, auto bf) {
-            return bwd_rows<TA, TR, mode.value, all.value, bf.value>(c, ch, dy, dr_out, a, r_out, g, parts,
+            return bwd_rows<TA, TR, mode.value, all.value, bf.value>(c, ch, &shared, dy, dr_out, a, r_out, g, parts,
                                                                      ends, dev, st);
         };
         const Plan p = bwd_plan(c.cols);
         if (params_bf16(c))
-            e = full ? by_mode(c.cols, p, kBwdE, [&](auto m) { return run(m, yes, yes); })
-                     : by_mode(c.cols, p, kBwdE, [&](auto m) { return run(m, no, yes); });
+            e = full ? by_mode(c.cols, p, kBwdE, true, [&](auto m) { return run(m, yes, yes); })
+                     : by_mode(c.cols, p, kBwdE, true, [&](auto m) { return run(m, no, yes); });
         else
-            e = full ? by_mode(c.cols, p, kBwdE, [&](auto m) { return run(m, yes, no); })
-                     : by_mode(c.cols, p, kBwdE, [&](auto m) { return run(m, no, no); });
+            e = full ? by_mode(c.cols, p, kBwdE, true, [&](auto m) { return run(m, yes, no); })
+                     : by_mode(c.cols, p, kBwdE, true, [&](auto m) { return run(m, no, no); });
     } else {
         float *consts = reinterpret_cast<float *>(ws + w.consts);
         const auto *dy_ = static_cast<const TA *>(dy), *a_ = static_cast<const TA *>(a);
@@ -1032,10 +1146,21 @@ cudaError_t bwd(const Call &c, const void *dy, const void *dr_out, const void *a
         return e;
     const int64_t n = (c.rows + ch.chunk - 1) / ch.chunk;
     const int64_t gates = (c.rows - 1) / ch.gate_rows + 1;
-    const Sums out{{g.dw_pre, g.db_pre, g.dw_post, g.db_post}, g.dgate,          parts,  ends,
-                   static_cast<int>(n),                        c.w_f32,          c.g_f32, gates > n - 1,
-                   c.cols};
-    const int64_t across = g.dgate != nullptr ? std::min(gates, n - 1) : 0;
+    Sums out = {};
+    out.out[0] = g.dw_pre;
+    out.out[1] = g.db_pre;
+    out.out[2] = g.dw_post;
+    out.out[3] = g.db_post;
+    out.dgate = g.dgate;
+    out.parts = parts;
+    out.ends = ends;
+    out.nparts = static_cast<int>(n * shared);
+    out.w_f32 = c.w_f32;
+    out.g_f32 = c.g_f32;
+    out.units = shared;
+    out.by_border = shared == 1 && gates > n - 1;
+    out.cols = c.cols;
+    const int64_t across = g.dgate == nullptr ? 0 : out.by_border ? (n + 30) / 32 : gates;
     return launch_pdl(reduce_kernel,
                       dim3(static_cast<unsigned>((c.cols + 31) / 32), static_cast<unsigned>(4 + across)),
                       dim3(1024), 0, st, out, ch, dev.status);

@@ -22,6 +22,59 @@ constexpr int kMaxParts = 64;  // warps of a cluster
 constexpr int kFull = 0;    // E / 8 vectors of eight each, all within the row, one block a row
 constexpr int kVec = 1;     // the same for any whole vectors, of a cluster's slice
 constexpr int kRagged = 2;  // element by element
+constexpr int kShift = 3;   // vectors on the tensors' own 16-byte boundaries, whatever the width
+
+// Where a thread's vectors of kShift lie.  A row starts s = (row cols) mod 8 elements
+// into a vector of the tensor (bf16 and fp32 alike: 16 and 32 bytes), and rows eight
+// apart have the same s, so a unit that walks every eighth row keeps its threads on
+// their columns.  Position p of such a row is its column p - s; vector u of the thread
+// has the positions from slice.first + 8 (u T + t), of which [lo, hi) are columns.  A
+// block's slice is in positions too.
+template <int MODE, int E>
+struct Place {
+    int n;      // columns (positions) of the slice
+    int first;  // and their first
+    __device__ __forceinline__ void set(int slice_first, int slice_n, int, int)
+    {
+        first = slice_first;
+        n = slice_n;
+    }
+};
+template <int E>
+struct Place<kShift, E> {
+    int n, first, s;
+    int lo[E / 8], hi[E / 8];
+    __device__ __forceinline__ void set(int slice_first, int slice_n, int shift, int cols)
+    {
+        n = slice_n;
+        first = slice_first;
+        s = shift;
+#pragma unroll
+        for (int u = 0; u < E / 8; ++u) {
+            const int c = 8 * (u * static_cast<int>(blockDim.x) + static_cast<int>(threadIdx.x));
+            lo[u] = min(8, max(0, s - (first + c)));
+            hi[u] = c < n ? max(0, min(8, s + cols - (first + c))) : 0;
+        }
+    }
+    __device__ __forceinline__ bool whole(int u) const { return lo[u] == 0 && hi[u] == 8; }
+    __device__ __forceinline__ bool has(int u, int e) const { return e >= lo[u] && e < hi[u]; }
+};
+
+// Zeros where a thread's vectors are not columns.
+template <int E>
+__device__ __forceinline__ void mask(const Place<kShift, E> &pl, float2 (&f)[E / 2])
+{
+#pragma unroll
+    for (int u = 0; u < E / 8; ++u) {
+        if (pl.whole(u))
+            continue;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f[4 * u + i].x = pl.has(u, 2 * i) ? f[4 * u + i].x : 0.0f;
+            f[4 * u + i].y = pl.has(u, 2 * i + 1) ? f[4 * u + i].y : 0.0f;
+        }
+    }
+}
 
 // The elements [begin, begin + n) of a tensor of `total` as the 16-byte pieces that
 // hold them; the piece that would reach past the tensor's end is not copied.
@@ -65,6 +118,7 @@ struct Slots {
     int stages;
     int64_t cols, total;
     Slice slice;
+    int shift;  // of kShift
     const TA *a[NA];
     const TR *r[NR];
     uint32_t pitch_a, pitch_r;
@@ -78,8 +132,9 @@ struct Slots {
     bool ok;  // no wait has run out
 
     __device__ __forceinline__ void start(uint8_t *memory, uint64_t *bars, int n, int64_t columns, int64_t rows,
-                                          const Slice &s)
+                                          const Slice &s, int s0)
     {
+        shift = s0;
         mem = at = memory;
         full = bars;
         stages = n;
@@ -95,7 +150,17 @@ struct Slots {
     __device__ __forceinline__ uint32_t slot_bytes() const { return NA * pitch_a + NR * pitch_r; }
     __device__ __forceinline__ uint8_t *at_a(int i) const { return at + i * pitch_a; }
     __device__ __forceinline__ uint8_t *at_r(int i) const { return at + NA * pitch_a + i * pitch_r; }
-    __device__ __forceinline__ int64_t begin(int64_t row) const { return row * cols + slice.first; }
+    __device__ __forceinline__ int64_t begin(int64_t row) const
+    {
+        return row * cols + slice.first - (MODE == kShift ? shift : 0);
+    }
+    // Elements of a slice from b that lie in whole 16-byte pieces of the tensor.
+    template <typename T>
+    __device__ __forceinline__ int whole(int64_t b) const
+    {
+        constexpr int64_t P = 16 / sizeof(T);
+        return static_cast<int>(max(min(static_cast<int64_t>(slice.n), (total & ~(P - 1)) - b), int64_t{0}));
+    }
 
     // by one thread, once every thread is done with the slot
     __device__ __forceinline__ void fill(int64_t row)
@@ -112,6 +177,10 @@ struct Slots {
             const Window<TA> wa(b, slice.n, total);
             const Window<TR> wr(b, slice.n, total);
             fa = wa.first, fr = wr.first, ba = wa.bytes, br = wr.bytes;
+        }
+        if constexpr (MODE == kShift) {
+            ba = whole<TA>(b) * sizeof(TA);
+            br = whole<TR>(b) * sizeof(TR);
         }
         uint32_t bytes = 0;
 #pragma unroll
@@ -181,6 +250,29 @@ struct Slots {
         __syncthreads();
     }
 
+    // The same for kShift, whose slices start at their vectors.
+    __device__ __forceinline__ void tail(int64_t row)
+    {
+        const int64_t b = begin(row);
+        const int wa = whole<TA>(b), wr = whole<TR>(b), end = static_cast<int>(min(static_cast<int64_t>(slice.n), total - b));
+        if (wa >= end && wr >= end)
+            return;
+        const int t = threadIdx.x;
+        if (wa + t < end) {
+#pragma unroll
+            for (int i = 0; i < NA; ++i)
+                if (a[i] != nullptr)
+                    reinterpret_cast<TA *>(at_a(i))[wa + t] = a[i][b + wa + t];
+        }
+        if (wr + t < end) {
+#pragma unroll
+            for (int i = 0; i < NR; ++i)
+                if (r[i] != nullptr)
+                    reinterpret_cast<TR *>(at_r(i))[wr + t] = r[i][b + wr + t];
+        }
+        __syncthreads();
+    }
+
     // Thread 0's copies land before the block leaves.
     __device__ __forceinline__ void drain() const
     {
@@ -219,8 +311,10 @@ __device__ __forceinline__ bool vec_in(int c, int n)
 }
 
 template <int MODE, int E, typename T>
-__device__ __forceinline__ void take(const uint8_t *slot, int shift, int n, float2 (&f)[E / 2])
+__device__ __forceinline__ void take(const uint8_t *slot, int shift, const Place<MODE, E> &pl,
+                                     float2 (&f)[E / 2])
 {
+    const int n = pl.n;
     if constexpr (MODE != kRagged) {
 #pragma unroll
         for (int u = 0; u < E / 8; ++u) {
@@ -242,6 +336,9 @@ __device__ __forceinline__ void take(const uint8_t *slot, int shift, int n, floa
                 f[4 * u + 3] = make_float2(__uint_as_float(w.z), __uint_as_float(w.w));
             }
         }
+        // beside a row's first and last columns lie its neighbours'
+        if constexpr (MODE == kShift)
+            mask<E>(pl, f);
     } else {
         const T *p = reinterpret_cast<const T *>(slot) + shift;
 #pragma unroll
@@ -273,18 +370,37 @@ struct Param<E, true> {
     __device__ __forceinline__ void set(int i, float2 v) { w[i] = pack2(v); }
 };
 
-// A row of parameters in global memory, from element `at`, bf16 or fp32 (BF: bf16); 0
-// past the slice, `none` throughout where there is no parameter.
+// The slice of a row of parameters in global memory that begins at element `row`, bf16
+// or fp32 (BF: bf16); 0 past the slice, `none` throughout where there is no parameter.
 template <int MODE, int E, bool BF>
-__device__ __forceinline__ void take_param(const void *p, int f32, int64_t at, int n, float none,
-                                           Param<E, BF> &out)
+__device__ __forceinline__ void take_param(const void *p, int f32, int64_t row, const Place<MODE, E> &pl,
+                                           float none, Param<E, BF> &out)
 {
+    const int n = pl.n;
+    const int64_t at = row + pl.first;
 #pragma unroll
     for (int i = 0; i < E / 2; ++i)
         out.set(i, p == nullptr ? make_float2(none, none) : make_float2(0.0f, 0.0f));
     if (p == nullptr)
         return;
-    if constexpr (MODE != kRagged) {
+    if constexpr (MODE == kShift) {
+#pragma unroll
+        for (int u = 0; u < E / 8; ++u) {
+            const int64_t c = at + vec_col(u) - pl.s;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float v[2] = {0.0f, 0.0f};
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const int e = 2 * i + k;
+                    if (pl.has(u, e))
+                        v[k] = !BF && f32 ? __ldg(static_cast<const float *>(p) + c + e)
+                                          : __bfloat162float(static_cast<const __nv_bfloat16 *>(p)[c + e]);
+                }
+                out.set(4 * u + i, make_float2(v[0], v[1]));
+            }
+        }
+    } else if constexpr (MODE != kRagged) {
 #pragma unroll
         for (int u = 0; u < E / 8; ++u) {
             const int c = vec_col(u);
@@ -323,17 +439,43 @@ __device__ __forceinline__ void take_param(const void *p, int f32, int64_t at, i
     }
 }
 
-// The thread's columns to `p` (the slice's first element), rounded to T.  `seen`
-// gathers the largest magnitude of the stored bf16 values.
-template <int MODE, int E, typename T>
-__device__ __forceinline__ void give(T *p, int n, const float2 (&f)[E / 2], uint32_t *seen = nullptr)
+// One value to `p`, rounded to T.
+template <typename T>
+__device__ __forceinline__ void give_one(T *p, float v, uint32_t *seen)
 {
+    if constexpr (sizeof(T) == 2) {
+        const __nv_bfloat16 h = __float2bfloat16_rn(v);
+        if (seen != nullptr)
+            *seen = __vmaxu2(*seen, static_cast<uint32_t>(__bfloat16_as_ushort(h)) & 0x7FFFu);
+        *p = h;
+    } else {
+        *p = v;
+    }
+}
+
+// The thread's columns to `p` (the slice's first element), rounded to T.  `seen`
+// gathers the largest magnitude of the stored bf16 values.  ALIGNED: p lies as the
+// tensors' rows do (else kShift's vectors go element by element).
+template <int MODE, int E, bool ALIGNED = true, typename T>
+__device__ __forceinline__ void give(T *p, const Place<MODE, E> &pl, const float2 (&f)[E / 2],
+                                     uint32_t *seen = nullptr)
+{
+    const int n = pl.n;
     if constexpr (MODE != kRagged) {
 #pragma unroll
         for (int u = 0; u < E / 8; ++u) {
             const int c = vec_col(u);
             if (!vec_in<MODE>(c, n))
                 continue;
+            if constexpr (MODE == kShift) {
+                if (!ALIGNED || !pl.whole(u)) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        if (pl.has(u, e))
+                            give_one(p + c + e, (e & 1) ? f[4 * u + e / 2].y : f[4 * u + e / 2].x, seen);
+                    continue;
+                }
+            }
             uint4 *q = reinterpret_cast<uint4 *>(p + c);
             const float2 *g = f + 4 * u;
             if constexpr (sizeof(T) == 2) {
@@ -357,59 +499,99 @@ __device__ __forceinline__ void give(T *p, int n, const float2 (&f)[E / 2], uint
             const int c = elem_col(j);
             if (c >= n)
                 continue;
-            const float v = (j & 1) ? f[j / 2].y : f[j / 2].x;
-            if constexpr (sizeof(T) == 2) {
-                const __nv_bfloat16 h = __float2bfloat16_rn(v);
-                if (seen != nullptr)
-                    *seen = __vmaxu2(*seen, static_cast<uint32_t>(__bfloat16_as_ushort(h)) & 0x7FFFu);
-                p[c] = h;
-            } else {
-                p[c] = v;
-            }
+            give_one(p + c, (j & 1) ? f[j / 2].y : f[j / 2].x, seen);
         }
     }
 }
 
-// The thread's columns of one row of a gradient in type `f32` (else bf16).
+// The thread's columns of a row of sums that begins at `row`, or of one of a gradient of
+// type `f32` (else bf16).
 template <int MODE, int E>
-__device__ __forceinline__ void give_param(void *p, int f32, int64_t at, int n, const float2 (&f)[E / 2])
+__device__ __forceinline__ void give_sums(float *row, const Place<MODE, E> &pl, const float2 (&f)[E / 2])
 {
-    if (f32)
-        give<MODE, E>(static_cast<float *>(p) + at, n, f);
+    if constexpr (MODE == kShift)
+        give<MODE, E, false>(row + pl.first - pl.s, pl, f);
     else
-        give<MODE, E>(static_cast<__nv_bfloat16 *>(p) + at, n, f);
+        give<MODE, E>(row + pl.first, pl, f);
+}
+template <int MODE, int E>
+__device__ __forceinline__ void give_param(void *p, int f32, int64_t row, const Place<MODE, E> &pl,
+                                           const float2 (&f)[E / 2])
+{
+    if (f32) {
+        give_sums<MODE, E>(static_cast<float *>(p) + row, pl, f);
+    } else if constexpr (MODE == kShift) {
+        give<MODE, E, false>(static_cast<__nv_bfloat16 *>(p) + row + pl.first - pl.s, pl, f);
+    } else {
+        give<MODE, E>(static_cast<__nv_bfloat16 *>(p) + row + pl.first, pl, f);
+    }
 }
 
 // Sums over the block, or over the cluster's blocks, in a fixed order; every thread
-// gets them.  Each warp leaves its parts (in every block of a cluster), so there is one
-// barrier a sum; the two halves of `red` [2][2][kMaxParts] are used in turn.  `red`
-// starts as zeros: parts are read four at a time.
+// gets them.  Each warp leaves its parts, in a cluster by a store to every block that
+// counts on that block's mbarrier: a cluster barrier's release would wait for the
+// rows' stores to global memory each time (8192 columns over two blocks, backward: 3.0 us
+// a row).  The two halves of `red` [2][2][kMaxParts] and of `bars` are used in turn; a
+// half is written again only once every warp has left its part of the sum between,
+// which it does after reading this one.  `red` starts as zeros: parts are read four at
+// a time.
 template <int MODE>
 struct Sum {
     float *red;
+    uint64_t *bars;
     int half;
-    uint32_t rank, ranks;
+    uint32_t rank, ranks, phases;
+    bool ok;  // no wait has run out
+    uint64_t limit_ns;
+    unsigned *status;
 
+    __device__ __forceinline__ void start(float *memory, uint64_t *barriers, uint32_t r, uint32_t n,
+                                          uint64_t limit, unsigned *word)
+    {
+        red = memory;
+        bars = barriers;
+        half = 0;
+        rank = r;
+        ranks = n;
+        phases = 0u;
+        ok = true;
+        limit_ns = limit;
+        status = word;
+    }
     __device__ __forceinline__ bool single() const { return MODE == kFull || ranks == 1; }
-    __device__ __forceinline__ void leave(float *to, float v, bool mine)
+    // The part of this warp, by the lanes of `mine`, into `to` of half h.
+    __device__ __forceinline__ void leave(float *to, float v, bool mine, int h)
     {
         const uint32_t w = threadIdx.x >> 5;
         if (single()) {
             if (mine)
                 to[w] = v;
         } else if (mine) {
-            const uint32_t part = rank * (blockDim.x >> 5) + w;
+            const uint32_t part = smem_addr(to + rank * (blockDim.x >> 5) + w), bar = smem_addr(&bars[h]);
             for (uint32_t k = 0; k < ranks; ++k)
-                asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(cluster_map(smem_addr(to + part), k)), "f"(v)
-                             : "memory");
+                asm volatile(
+                    "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(
+                        cluster_map(part, k)),
+                    "r"(__float_as_uint(v)), "r"(cluster_map(bar, k))
+                    : "memory");
         }
     }
-    __device__ __forceinline__ void meet() const
+    // All parts of half h are there; `count` a warp.  A wait that runs out sets the
+    // status; the thread then goes on without waiting (what it forms is of no use).
+    __device__ __forceinline__ void meet(int h, uint32_t count)
     {
-        if (single())
+        if (single()) {
             __syncthreads();
-        else
-            cluster_sync();
+            return;
+        }
+        if (threadIdx.x == 0)
+            mbar_arrive_expect_tx(&bars[h], count * ranks * (blockDim.x >> 5) * 4u);
+        if (ok && !mbar_wait(&bars[h], (phases >> h) & 1u, nullptr, limit_ns)) {
+            ok = false;
+            atomicOr(status, kStatusTimeout);
+        }
+        phases ^= 1u << h;
+        __syncwarp();
     }
     __device__ __forceinline__ float total(const float *from) const
     {
@@ -429,11 +611,11 @@ struct Sum {
         }
         return s.x + s.y;
     }
-    __device__ __forceinline__ float *next()
+    __device__ __forceinline__ float *next(int &h)
     {
-        float *r = red + half * 2 * kMaxParts;
+        h = half;
         half ^= 1;
-        return r;
+        return red + h * 2 * kMaxParts;
     }
     static __device__ __forceinline__ float warp(float a)
     {
@@ -446,9 +628,10 @@ struct Sum {
     __device__ __forceinline__ float operator()(float a)
     {
         a = warp(a);
-        float *r = next();
-        leave(r, a, (threadIdx.x & 31) == 0);
-        meet();
+        int h;
+        float *r = next(h);
+        leave(r, a, (threadIdx.x & 31) == 0, h);
+        meet(h, 1);
         return total(r);
     }
     // of a and b: the lower lanes gather a, the upper ones b
@@ -460,9 +643,10 @@ struct Sum {
 #pragma unroll
         for (int o = 8; o > 0; o >>= 1)
             v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-        float *r = next();
-        leave(r + (upper ? kMaxParts : 0), v, (threadIdx.x & 15) == 0);
-        meet();
+        int h;
+        float *r = next(h);
+        leave(r + (upper ? kMaxParts : 0), v, (threadIdx.x & 15) == 0, h);
+        meet(h, 2);
         return make_float2(total(r), total(r + kMaxParts));
     }
     // Mean of the row and sum of the squared differences to it, from a full block's
@@ -486,10 +670,11 @@ struct Sum {
             q = __ffma2_rn(d, d, q);
         }
         const float m2 = warp(q.x + q.y);
-        float *r = next();
-        leave(r, mean, (threadIdx.x & 31) == 0);
-        leave(r + kMaxParts, m2, (threadIdx.x & 31) == 0);
-        meet();
+        int h;
+        float *r = next(h);
+        leave(r, mean, (threadIdx.x & 31) == 0, h);
+        leave(r + kMaxParts, m2, (threadIdx.x & 31) == 0, h);
+        meet(h, 2);
         const int w = static_cast<int>(blockDim.x >> 5);
         const float mu = total(r) / static_cast<float>(w);
         float2 between = make_float2(0.0f, 0.0f);

@@ -8,8 +8,8 @@
 // The angle: a frequency becomes a fraction of a turn in 64-bit fixed point, so
 // position * fraction mod 2^64 is the angle's fraction of a turn, exactly; its upper
 // 32 bits as a signed number lie in half a turn either way, and sincospi takes them
-// without any further reduction.  A far position thus costs no precision and no
-// 64-bit floating point.
+// without any further reduction.  A far position thus costs no precision, and one
+// 64-bit floating point multiplication is all there is of those.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -59,7 +59,7 @@ struct Args {
     const double *freqs;
     float scale;
     int inverse;
-    Div by_units, by_head_units;
+    Div by_units, by_head_units, by_half;
 };
 
 template <typename T, int VEC>
@@ -98,6 +98,12 @@ union Bits {
     typename Vec<T, VEC>::type v;
     T e[VEC];
     __device__ Bits() {}
+    __device__ Bits(const Bits &o) : v(o.v) {}
+    __device__ Bits &operator=(const Bits &o)
+    {
+        v = o.v;
+        return *this;
+    }
 };
 
 __device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
@@ -105,15 +111,90 @@ __device__ __forceinline__ float to_f(float v) { return v; }
 __device__ __forceinline__ void from_f(float f, __nv_bfloat16 &v) { v = __float2bfloat16_rn(f); }
 __device__ __forceinline__ void from_f(float f, float &v) { v = f; }
 
+// A frequency (radians a position) as a fraction of a turn in 64 bits; whole turns do
+// not count.  The double's 53 bits are moved to their place by shifts.
+__device__ __forceinline__ uint64_t turn_fraction(double f)
+{
+    const int64_t bits = __double_as_longlong(f * 0.15915494309189535);
+    const int e = static_cast<int>((bits >> 52) & 0x7FF) - 1023;  // 2^e times [1, 2)
+    const uint64_t m = (static_cast<uint64_t>(bits) & 0xFFFFFFFFFFFFFull) | 0x10000000000000ull;
+    const int left = e + 12;  // of the 52 bits behind the point
+    const uint64_t v = left >= 64 || left <= -64 ? 0ull : (left >= 0 ? m << left : m >> -left);
+    return bits < 0 ? 0ull - v : v;
+}
+
 // A unit is VEC pairs: columns [VEC u, VEC u + VEC) and the same rot / 2 further on
 // (half), or [2 VEC u, 2 VEC u + 2 VEC) (interleaved).  Units from `turned` on are
 // two vectors of the columns that are copied, the last unit's second one perhaps
 // past the head's end.
 template <typename T, int VEC, bool HALF>
+struct Unit {
+    using V = typename Vec<T, VEC>::type;
+    Bits<T, VEC> v0, v1;
+    T *out;
+    int c0, c1, row, u;
+
+    __device__ __forceinline__ void load(const Args &a, int i, int64_t row0)
+    {
+        row = static_cast<int>(a.by_head_units(i));
+        const int hu = i - row * a.heads * a.units;
+        int h = static_cast<int>(a.by_units(hu));
+        u = hu - h * a.units;
+        const bool second = h >= a.heads0;
+        const Tensor &t = a.t[second ? 1 : 0];
+        if (second)
+            h -= a.heads0;
+        // positions of a block's rows in the batch: 32-bit division
+        const uint32_t r = static_cast<uint32_t>(row0) + row, b = r / static_cast<uint32_t>(a.seq);
+        const int64_t s = r - b * static_cast<uint32_t>(a.seq);
+        const T *x = static_cast<const T *>(t.x) + b * t.x_batch + s * t.x_seq + h * t.x_head;
+        out = static_cast<T *>(t.out) + b * t.out_batch + s * t.out_seq + h * t.out_head;
+        const bool turned = u < a.turned;
+        c0 = turned ? (HALF ? VEC * u : 2 * VEC * u) : 2 * a.half + 2 * VEC * (u - a.turned);
+        c1 = turned && HALF ? c0 + a.half : c0 + VEC;
+        v0.v = *reinterpret_cast<const V *>(x + c0);
+        if (c1 < a.dim)
+            v1.v = *reinterpret_cast<const V *>(x + c1);
+    }
+
+    __device__ __forceinline__ void rotate(const Args &a, const int64_t *at, const float2 *turn)
+    {
+        if (u >= a.turned || at[row] < 0)
+            return;
+        const float2 *cs = turn + row * a.half + VEC * u;
+        if (HALF || VEC == 1) {
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                const float p = to_f(v0.e[e]), q = to_f(v1.e[e]);
+                from_f(p * cs[e].x - q * cs[e].y, v0.e[e]);
+                from_f(q * cs[e].x + p * cs[e].y, v1.e[e]);
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e + 1 < VEC; e += 2) {
+                const float2 k0 = cs[e / 2], k1 = cs[VEC / 2 + e / 2];
+                float p = to_f(v0.e[e]), q = to_f(v0.e[e + 1]);
+                from_f(p * k0.x - q * k0.y, v0.e[e]);
+                from_f(q * k0.x + p * k0.y, v0.e[e + 1]);
+                p = to_f(v1.e[e]), q = to_f(v1.e[e + 1]);
+                from_f(p * k1.x - q * k1.y, v1.e[e]);
+                from_f(q * k1.x + p * k1.y, v1.e[e + 1]);
+            }
+        }
+    }
+
+    __device__ __forceinline__ void store(const Args &a) const
+    {
+        *reinterpret_cast<V *>(out + c0) = v0.v;
+        if (c1 < a.dim)
+            *reinterpret_cast<V *>(out + c1) = v1.v;
+    }
+};
+
+template <typename T, int VEC, bool HALF>
 __global__ void __launch_bounds__(kThreads)
 rope_kernel(const __grid_constant__ Args a)
 {
-    using V = typename Vec<T, VEC>::type;
     extern __shared__ float2 turn[];  // [rows_per_block][half] cosine and sine, scaled
     __shared__ int64_t at[kMaxRows];  // the rows' positions
     griddep_wait();
@@ -121,70 +202,34 @@ rope_kernel(const __grid_constant__ Args a)
     const int64_t row0 = static_cast<int64_t>(blockIdx.x) * a.rows_per_block;
     const int nrows = static_cast<int>(min(static_cast<int64_t>(a.rows_per_block), a.rows - row0));
     if (threadIdx.x < nrows) {
-        const int64_t row = row0 + threadIdx.x, b = row / a.seq, s = row - b * a.seq;
+        const uint32_t row = static_cast<uint32_t>(row0) + threadIdx.x, b = row / static_cast<uint32_t>(a.seq);
+        const int64_t s = row - b * static_cast<uint32_t>(a.seq);
         at[threadIdx.x] = a.pos[b * a.pos_batch + s * a.pos_seq];
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < a.half * nrows; i += kThreads) {
-        const int j = i / a.half, p = i - j * a.half;
-        double f = a.freqs[p] * 0.15915494309189535;  // turns a position; whole ones do not count
-        f -= floor(f);
-        const uint64_t frac = __double2ull_rz(f * 18446744073709551616.0);
-        const uint64_t angle = frac * static_cast<uint64_t>(at[j]);
+    // the first unit's loads are under way while the angles are formed
+    Unit<T, VEC, HALF> unit;
+    int i = threadIdx.x;
+    const int units = nrows * a.heads * a.units;
+    if (i < units)
+        unit.load(a, i, row0);
+    for (int p = threadIdx.x; p < a.half * nrows; p += kThreads) {
+        const int j = static_cast<int>(a.by_half(p));
+        const uint64_t angle = turn_fraction(a.freqs[p - j * a.half]) * static_cast<uint64_t>(at[j]);
         const float t = static_cast<float>(static_cast<int32_t>(angle >> 32)) * 0x1p-31f;  // half turns
         float sn, cs;
         sincospif(t, &sn, &cs);
-        turn[i] = make_float2(cs * a.scale, (a.inverse ? -sn : sn) * a.scale);
+        turn[p] = make_float2(cs * a.scale, (a.inverse ? -sn : sn) * a.scale);
     }
     __syncthreads();
-    const int per_row = a.heads * a.units;
-    for (int i = threadIdx.x; i < nrows * per_row; i += kThreads) {
-        const int j = static_cast<int>(a.by_head_units(i));
-        const int hu = i - j * per_row;
-        int h = static_cast<int>(a.by_units(hu));
-        const int u = hu - h * a.units;
-        const Tensor &t = a.t[h < a.heads0 ? 0 : 1];
-        if (h >= a.heads0)
-            h -= a.heads0;
-        const int64_t row = row0 + j, b = row / a.seq, s = row - b * a.seq;
-        const T *x = static_cast<const T *>(t.x) + b * t.x_batch + s * t.x_seq + h * t.x_head;
-        T *o = static_cast<T *>(t.out) + b * t.out_batch + s * t.out_seq + h * t.out_head;
-        const bool turned = u < a.turned;
-        const int c0 = turned ? (HALF ? VEC * u : 2 * VEC * u) : 2 * a.half + 2 * VEC * (u - a.turned);
-        const int c1 = turned && HALF ? c0 + a.half : c0 + VEC;
-        Bits<T, VEC> v0, v1;
-        v0.v = *reinterpret_cast<const V *>(x + c0);
-        if (c1 < a.dim)
-            v1.v = *reinterpret_cast<const V *>(x + c1);
-        if (turned && at[j] >= 0) {
-            const float2 *cs = turn + j * a.half + VEC * u;
-            if (HALF) {
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    const float p = to_f(v0.e[e]), q = to_f(v1.e[e]);
-                    from_f(p * cs[e].x - q * cs[e].y, v0.e[e]);
-                    from_f(q * cs[e].x + p * cs[e].y, v1.e[e]);
-                }
-            } else if (VEC > 1) {
-#pragma unroll
-                for (int e = 0; e < VEC; e += 2) {
-                    const float2 k0 = cs[e / 2], k1 = cs[VEC / 2 + e / 2];
-                    float p = to_f(v0.e[e]), q = to_f(v0.e[e + 1]);
-                    from_f(p * k0.x - q * k0.y, v0.e[e]);
-                    from_f(q * k0.x + p * k0.y, v0.e[e + 1]);
-                    p = to_f(v1.e[e]), q = to_f(v1.e[e + 1]);
-                    from_f(p * k1.x - q * k1.y, v1.e[e]);
-                    from_f(q * k1.x + p * k1.y, v1.e[e + 1]);
-                }
-            } else {
-                const float p = to_f(v0.e[0]), q = to_f(v1.e[0]);
-                from_f(p * cs[0].x - q * cs[0].y, v0.e[0]);
-                from_f(q * cs[0].x + p * cs[0].y, v1.e[0]);
-            }
-        }
-        *reinterpret_cast<V *>(o + c0) = v0.v;
-        if (c1 < a.dim)
-            *reinterpret_cast<V *>(o + c1) = v1.v;
+    while (i < units) {
+        Unit<T, VEC, HALF> next;
+        i += kThreads;
+        if (i < units)
+            next.load(a, i, row0);
+        unit.rotate(a, at, turn);
+        unit.store(a);
+        unit = next;
     }
 }
 
@@ -202,6 +247,7 @@ cudaError_t run(Args &a, const DeviceInfo &dev, cudaStream_t st)
     a.rows_per_block = static_cast<int>(r);
     a.by_units = Div(static_cast<uint32_t>(a.units));
     a.by_head_units = Div(static_cast<uint32_t>(per_row));
+    a.by_half = Div(static_cast<uint32_t>(a.half));
     const int64_t blocks = (a.rows + r - 1) / r;
     return launch_pdl(rope_kernel<T, VEC, HALF>, dim3(static_cast<unsigned>(blocks)), dim3(kThreads),
                       static_cast<size_t>(r) * a.half * sizeof(float2), st, a);
