@@ -43,7 +43,8 @@ struct Place {
 template <int E>
 struct Place<kShift, E> {
     int n, first, s;
-    int lo[E / 8], hi[E / 8];
+    uint32_t m[E / 2];  // of each pair's elements, 16 set bits where it is a column
+    bool all[E / 8];    // the vector is columns only
     __device__ __forceinline__ void set(int slice_first, int slice_n, int shift, int cols)
     {
         n = slice_n;
@@ -52,12 +53,16 @@ struct Place<kShift, E> {
 #pragma unroll
         for (int u = 0; u < E / 8; ++u) {
             const int c = 8 * (u * static_cast<int>(blockDim.x) + static_cast<int>(threadIdx.x));
-            lo[u] = min(8, max(0, s - (first + c)));
-            hi[u] = c < n ? max(0, min(8, s + cols - (first + c))) : 0;
+            const int lo = s - (first + c), hi = c < n ? s + cols - (first + c) : 0;
+            all[u] = lo <= 0 && hi >= 8;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                m[4 * u + i] = (2 * i >= lo && 2 * i < hi ? 0xFFFFu : 0u) |
+                               (2 * i + 1 >= lo && 2 * i + 1 < hi ? 0xFFFF0000u : 0u);
         }
     }
-    __device__ __forceinline__ bool whole(int u) const { return lo[u] == 0 && hi[u] == 8; }
-    __device__ __forceinline__ bool has(int u, int e) const { return e >= lo[u] && e < hi[u]; }
+    __device__ __forceinline__ bool whole(int u) const { return all[u]; }
+    __device__ __forceinline__ bool has(int u, int e) const { return ((m[4 * u + e / 2] >> (16 * (e & 1))) & 1u) != 0u; }
 };
 
 // Zeros where a thread's vectors are not columns.
@@ -69,9 +74,9 @@ __device__ __forceinline__ void mask(const Place<kShift, E> &pl, float2 (&f)[E /
         if (pl.whole(u))
             continue;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            f[4 * u + i].x = pl.has(u, 2 * i) ? f[4 * u + i].x : 0.0f;
-            f[4 * u + i].y = pl.has(u, 2 * i + 1) ? f[4 * u + i].y : 0.0f;
+        for (int i = 4 * u; i < 4 * u + 4; ++i) {
+            f[i].x = __int_as_float(__float_as_int(f[i].x) & (static_cast<int>(pl.m[i] << 16) >> 16));
+            f[i].y = __int_as_float(__float_as_int(f[i].y) & (static_cast<int>(pl.m[i]) >> 16));
         }
     }
 }
@@ -108,6 +113,17 @@ __host__ __device__ constexpr uint32_t slice_pitch(int n)
 struct Slice {
     int first, n;  // column and count
 };
+
+// mbar_wait for what is due within a microsecond or two: it reads the global timer
+// only after some tries, which would cost more than the wait.
+__device__ __forceinline__ bool wait_soon(uint64_t *bar, uint32_t parity, uint64_t limit_ns)
+{
+#pragma unroll 1
+    for (int i = 0; i < 64; ++i)
+        if (mbar_try_wait(bar, parity))
+            return true;
+    return mbar_wait(bar, parity, nullptr, limit_ns);
+}
 
 // NA tensors of TA and NR of TR; a slot holds a slice of each.  Of the pointers, NULL
 // ones are left out.
@@ -205,7 +221,7 @@ struct Slots {
     // of no use), and issues no more copies.
     __device__ __forceinline__ void wait(uint64_t limit_ns, unsigned *status)
     {
-        if (ok && !mbar_wait(&full[slot], parity, nullptr, limit_ns)) {
+        if (ok && !wait_soon(&full[slot], parity, limit_ns)) {
             ok = false;
             atomicOr(status, kStatusTimeout);
         }
@@ -326,6 +342,9 @@ __device__ __forceinline__ void take(const uint8_t *slot, int shift, const Place
                 if (sizeof(T) == 4)
                     w = p[1];
             }
+            // beside a row's first and last columns lie its neighbours'
+            if constexpr (MODE == kShift && sizeof(T) == 2)
+                v = make_uint4(v.x & pl.m[4 * u], v.y & pl.m[4 * u + 1], v.z & pl.m[4 * u + 2], v.w & pl.m[4 * u + 3]);
             if constexpr (sizeof(T) == 2) {
                 f[4 * u] = bf2(v.x), f[4 * u + 1] = bf2(v.y);
                 f[4 * u + 2] = bf2(v.z), f[4 * u + 3] = bf2(v.w);
@@ -336,8 +355,7 @@ __device__ __forceinline__ void take(const uint8_t *slot, int shift, const Place
                 f[4 * u + 3] = make_float2(__uint_as_float(w.z), __uint_as_float(w.w));
             }
         }
-        // beside a row's first and last columns lie its neighbours'
-        if constexpr (MODE == kShift)
+        if constexpr (MODE == kShift && sizeof(T) == 4)
             mask<E>(pl, f);
     } else {
         const T *p = reinterpret_cast<const T *>(slot) + shift;
@@ -586,7 +604,7 @@ struct Sum {
         }
         if (threadIdx.x == 0)
             mbar_arrive_expect_tx(&bars[h], count * ranks * (blockDim.x >> 5) * 4u);
-        if (ok && !mbar_wait(&bars[h], (phases >> h) & 1u, nullptr, limit_ns)) {
+        if (ok && !wait_soon(&bars[h], (phases >> h) & 1u, limit_ns)) {
             ok = false;
             atomicOr(status, kStatusTimeout);
         }
@@ -604,6 +622,7 @@ struct Sum {
             }
         } else {
             const int parts = static_cast<int>(ranks * (blockDim.x >> 5));
+#pragma unroll 4
             for (int i = 0; i < parts; i += 4) {
                 const float4 v = *reinterpret_cast<const float4 *>(from + i);
                 s = __fadd2_rn(s, __fadd2_rn(make_float2(v.x, v.y), make_float2(v.z, v.w)));
