@@ -8,6 +8,7 @@ that it calls and only checks and marshals its arguments.
 from __future__ import annotations
 
 import ctypes
+import functools
 import struct
 
 import torch
@@ -48,6 +49,12 @@ def _typed(what: str, name: str, t: torch.Tensor | None, shape: tuple, index: in
     return _arg(what, name, t, t.dtype, shape, index), _dtype(what, t)
 
 
+@functools.lru_cache(maxsize=1024)
+def _ws_bytes(lib, name: str, rows: int, cols: int) -> int:
+    """A workspace's bytes, which a training step asks for with the same few sizes."""
+    return int(getattr(lib, name)(rows, cols))
+
+
 def _ws(what: str, ws: torch.Tensor | None, nbytes: int, like: torch.Tensor, stream):
     """The pointer and size of the workspace, which is allocated if none is given."""
     if ws is None:
@@ -86,7 +93,7 @@ def f8_gemm_act(a: torch.Tensor, b: torch.Tensor, scale_a: torch.Tensor, scale_b
 
 
 def f8_act_bwd_workspace_bytes(rows: int, cols: int) -> int:
-    return int(binding.lib().f8_act_bwd_workspace_bytes(rows, cols))
+    return _ws_bytes(binding.lib(), "f8_act_bwd_workspace_bytes", rows, cols)
 
 
 def f8_act_bwd(dy: torch.Tensor, z: torch.Tensor | None, act: int, dz: torch.Tensor | None = None,
@@ -247,7 +254,7 @@ _WANT = {(layer, post, gated): frozenset(
 
 
 def f8_residual_norm_bwd_workspace_bytes(rows: int, cols: int) -> int:
-    return int(binding.lib().f8_residual_norm_bwd_workspace_bytes(rows, cols))
+    return _ws_bytes(binding.lib(), "f8_residual_norm_bwd_workspace_bytes", rows, cols)
 
 
 def f8_residual_norm_bwd(dy: torch.Tensor, dr_out: torch.Tensor | None, a: torch.Tensor,
@@ -270,17 +277,24 @@ def f8_residual_norm_bwd(dy: torch.Tensor, dr_out: torch.Tensor | None, a: torch
     cols = shape[1:]
     if want is None:
         want = _WANT[kind == F8_LAYER_NORM, w_post is not None, gate is not None]
-    out, ptrs = [], []
-    for name, t, size, dtype in (("da", da, shape, xt), ("dr", dr, shape, rt), ("dw_pre", dw_pre, cols, wt),
-                                 ("db_pre", db_pre, cols, wt), ("dw_post", dw_post, cols, wt),
-                                 ("db_post", db_post, cols, wt),
-                                 ("dgate", dgate, *((cols, wt) if gate is None else (gate.shape, gate.dtype)))):
-        if t is None and name in want:
-            t = _empty(size, dtype, a.device, stream)
-        out.append(t)
-        ptrs.append(_arg(what, name, t, dtype, size, at))
+    if want:
+        gd, gs = (wt, cols) if gate is None else (gate.dtype, gate.shape)
+        new = lambda size, dtype: _empty(size, dtype, a.device, stream)  # noqa: E731
+        da = new(shape, xt) if da is None and "da" in want else da
+        dr = new(shape, rt) if dr is None and "dr" in want else dr
+        dw_pre = new(cols, wt) if dw_pre is None and "dw_pre" in want else dw_pre
+        db_pre = new(cols, wt) if db_pre is None and "db_pre" in want else db_pre
+        dw_post = new(cols, wt) if dw_post is None and "dw_post" in want else dw_post
+        db_post = new(cols, wt) if db_post is None and "db_post" in want else db_post
+        dgate = new(gs, gd) if dgate is None and "dgate" in want else dgate
+    grads = _GRADS.pack(
+        _arg(what, "da", da, xt, shape, at), _arg(what, "dr", dr, rt, shape, at),
+        _arg(what, "dw_pre", dw_pre, wt, cols, at), _arg(what, "db_pre", db_pre, wt, cols, at),
+        _arg(what, "dw_post", dw_post, wt, cols, at), _arg(what, "db_post", db_post, wt, cols, at),
+        0 if dgate is None else _arg(what, "dgate", dgate, wt if gate is None else gate.dtype,
+                                     cols if gate is None else gate.shape, at))
     ws, *space = _ws(what, ws, f8_residual_norm_bwd_workspace_bytes(*shape) if ws is None else 0, a, stream)
     _call(what, stream, n, _arg(what, "dy", dy, xt, shape, at),
           _arg(what, "dr_out", dr_out, rt, shape, at), binding._ptr(a), _arg(what, "r_out", r_out, rt, shape, at),
-          _arg(what, "stats", stats, _F32, (4, shape[0]), at), _GRADS.pack(*ptrs), *space)
-    return tuple(out)
+          _arg(what, "stats", stats, _F32, (4, shape[0]), at), grads, *space)
+    return da, dr, dw_pre, db_pre, dw_post, db_post, dgate

@@ -3,7 +3,7 @@
 The atlas.scime.ai summary of the TorchTitan paper (Approach) treats Float8
 as a per-linear transformation composed onto a model, and its ablation
 table measures it on Llama 3.1 8B.  This module is that transformation for
-modules whose linears have no bias (as in Llama):
+modules whose linears have no bias (as in Llama), and for linears with one:
 
 - Float8Linear: Y = X W^T with the forward and backward of a Float8 linear
   (f8_linear_fwd, f8_linear_bwd): dynamic tensorwise E4M3 scaling of X, W
@@ -21,6 +21,12 @@ modules whose linears have no bias (as in Llama):
 - token_logprobs, distill_loss: what a model learns from the logits of a head
   linear (f8_token_logprobs, f8_distill_fwd and their gradients), for heads
   padded past the vocabulary too.
+- Float8LinearAct: a Float8 linear with a bias, an activation and a residual in
+  the GEMM's epilogue (f8_gemm_act, f8_act_bwd); to_float8_linears swaps linears
+  that have a bias for it where asked to.
+- ResidualNorm: the residual stream's update by a block's output and the next
+  block's norm (f8_residual_norm_fwd, f8_residual_norm_bwd).
+- RotaryPositions: queries and keys turned by their positions (f8_rope).
 
 Inputs and weights of the linears must be bf16 CUDA tensors with every size a
 multiple of 16 (the ABI's rule); the norms and the logits' functions take bf16
@@ -34,7 +40,7 @@ from typing import Callable
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import binding, ops
+from . import binding, block, ops
 
 
 class _Float8LinearFn(torch.autograd.Function):
@@ -364,23 +370,38 @@ def eligible(linear: torch.nn.Module) -> bool:
             and linear.in_features % 16 == 0 and linear.out_features % 16 == 0)
 
 
+def eligible_with_bias(linear: torch.nn.Module) -> bool:
+    """An nn.Linear Float8LinearAct can stand in for: as `eligible`, with a bf16 or
+    fp32 bias."""
+    return (isinstance(linear, torch.nn.Linear) and linear.bias is not None
+            and linear.weight.dtype == torch.bfloat16 and linear.bias.dtype in (torch.bfloat16, torch.float32)
+            and linear.in_features % 16 == 0 and linear.out_features % 16 == 0)
+
+
 def to_float8_linears(module: torch.nn.Module,
                       keep: Callable[[str, torch.nn.Module], bool] | None = None,
-                      grad_format: str = "e4m3", cache_weights: bool = False) -> torch.nn.Module:
+                      grad_format: str = "e4m3", cache_weights: bool = False,
+                      biases: bool = False) -> torch.nn.Module:
     """Replaces, in place, every eligible nn.Linear below `module` for which
     `keep(qualified_name, linear)` is true (all of them when `keep` is None)
     with a Float8Linear sharing its weight Parameter (dY in `grad_format`;
-    `cache_weights` as Float8Linear's cache_weight); returns `module`."""
+    `cache_weights` as Float8Linear's cache_weight); returns `module`.  With
+    `biases`, linears that have a bf16 or fp32 bias become Float8LinearAct
+    modules that share it too (their weights are quantised in every forward)."""
     def visit(parent: torch.nn.Module, prefix: str) -> None:
         for name, child in list(parent.named_children()):
             qual = f"{prefix}.{name}" if prefix else name
             if eligible(child) and (keep is None or keep(qual, child)):
                 setattr(parent, name, Float8Linear.from_linear(child, grad_format, cache_weights))
+            elif biases and eligible_with_bias(child) and (keep is None or keep(qual, child)):
+                setattr(parent, name, Float8LinearAct.from_linear(child, grad_format=grad_format))
             else:
                 visit(child, qual)
 
     if eligible(module) and (keep is None or keep("", module)):
         raise ValueError("the module itself is a linear: use Float8Linear.from_linear")
+    if biases and eligible_with_bias(module) and (keep is None or keep("", module)):
+        raise ValueError("the module itself is a linear: use Float8LinearAct.from_linear")
     visit(module, "")
     return module
 
@@ -578,3 +599,254 @@ def distill_loss(logits: torch.Tensor, ids: torch.Tensor, values: torch.Tensor,
     if values.requires_grad and torch.is_grad_enabled():
         raise ValueError("distill_loss forms no gradient of values: pass values.detach()")
     return _DistillFn.apply(logits, ids, values, float(temperature), bool(tail), vocab)
+
+
+# what stands between a block's linears
+_ACTIVATIONS = {None: binding.F8_ACT_NONE, "none": binding.F8_ACT_NONE, "relu": binding.F8_ACT_RELU,
+                "relu2": binding.F8_ACT_RELU2, "silu": binding.F8_ACT_SILU, "gelu": binding.F8_ACT_GELU,
+                "gelu_tanh": binding.F8_ACT_GELU_TANH}
+
+
+class _Float8LinearActFn(torch.autograd.Function):
+    """X and W quantised (f8_quantize_multi), then the GEMM with its epilogue
+    (f8_gemm_act); backward f8_act_bwd to dz and dbias, then f8_linear_bwd.  The
+    residual's gradient is dy."""
+
+    @staticmethod
+    def forward(ctx, x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None,
+                residual: torch.Tensor | None, act: int, dy_fmt: int) -> torch.Tensor:
+        lead, (N, K) = x.shape[:-1], weight.shape
+        x2 = _dense(x.reshape(-1, K))
+        M, dev = x2.shape[0], x.device
+        saved = binding.LinearSaved.empty(M, N, K, dev)
+        xq, wq = (torch.empty(shape, dtype=torch.uint8, device=dev) for shape in ((M, K), (N, K)))
+        sc = saved.scalars
+        binding.f8_quantize_multi([x2, _dense(weight)], outs=[(xq, saved.x_t, sc[1:2], sc[0:1]),
+                                                              (wq, saved.w_t, sc[3:4], sc[2:3])])
+        res = None if residual is None else _dense(residual.reshape(-1, N))
+        keep = act != binding.F8_ACT_NONE and any(ctx.needs_input_grad[:3])
+        y, z = block.f8_gemm_act(xq, wq, sc[1:2], sc[3:4], bias=None if bias is None else _dense(bias), act=act,
+                                 residual=res, want_z=keep)
+        ctx.f8_saved, ctx.z, ctx.act, ctx.dy_fmt, ctx.x_shape = saved, z, act, dy_fmt, x.shape
+        ctx.bias_dtype = None if bias is None else bias.dtype
+        return y.reshape(*lead, N)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy: torch.Tensor):
+        want_dx, want_dw, want_db, want_dres = ctx.needs_input_grad[:4]
+        dx = dw = db = None
+        if want_dx or want_dw or want_db:
+            dz = _dense(dy.reshape(-1, dy.shape[-1]))
+            if ctx.act != binding.F8_ACT_NONE or want_db:
+                dz2, db = block.f8_act_bwd(dz, ctx.z, ctx.act, want_dz=ctx.act != binding.F8_ACT_NONE,
+                                           want_dbias=want_db, bias_dtype=ctx.bias_dtype)
+                dz = dz if dz2 is None else dz2
+            if want_dx or want_dw:
+                dx, dw = binding.f8_linear_bwd(dz, ctx.f8_saved, want_dx=want_dx, want_dw=want_dw,
+                                               dy_fmt=ctx.dy_fmt)
+        return (dx.reshape(ctx.x_shape) if want_dx else None, dw if want_dw else None, db,
+                dy if want_dres else None, None, None)
+
+
+class Float8LinearAct(torch.nn.Module):
+    """y = act(x W^T + bias) + residual, computed by the Float8 path with the sum,
+    the activation and the residual in the GEMM's epilogue (one rounding to
+    bf16).  `weight` is [out_features, in_features] bf16, `bias` bf16 or fp32 or
+    None; activation "none", "relu", "relu2", "silu", "gelu" (by erf) or
+    "gelu_tanh".  The input's leading dimensions flatten into a token count that is
+    a multiple of 16."""
+
+    def __init__(self, in_features: int, out_features: int, bias: bool = True, activation: str | None = None,
+                 device=None, weight: torch.nn.Parameter | None = None, b: torch.nn.Parameter | None = None,
+                 grad_format: str = "e4m3"):
+        super().__init__()
+        _check_sizes(in_features, out_features)
+        if activation not in _ACTIVATIONS:
+            raise ValueError(f"activation is one of {', '.join(repr(a) for a in _ACTIVATIONS if a)}")
+        self.in_features, self.out_features = in_features, out_features
+        self.activation, self.act = activation or "none", _ACTIVATIONS[activation]
+        self.grad_format = _grad_format(grad_format)
+        if weight is None:
+            weight = torch.nn.Parameter(torch.empty((out_features, in_features), dtype=torch.bfloat16,
+                                                    device=device))
+            torch.nn.init.normal_(weight, std=0.02)
+        if bias and b is None:
+            b = torch.nn.Parameter(torch.zeros(out_features, dtype=torch.bfloat16, device=weight.device))
+        if tuple(weight.shape) != (out_features, in_features) or weight.dtype != torch.bfloat16:
+            raise TypeError("Float8LinearAct's weight is a bf16 [out_features, in_features] tensor")
+        if b is not None and (tuple(b.shape) != (out_features,) or b.dtype not in (torch.bfloat16, torch.float32)):
+            raise TypeError("Float8LinearAct's bias is a bf16 or fp32 [out_features] tensor")
+        self.weight = weight
+        self.register_parameter("bias", b)
+
+    @classmethod
+    def from_linear(cls, linear: torch.nn.Linear, activation: str | None = None,
+                    grad_format: str = "e4m3") -> "Float8LinearAct":
+        """The counterpart of `linear`, sharing its weight and bias Parameters."""
+        return cls(linear.in_features, linear.out_features, bias=False, activation=activation,
+                   weight=linear.weight, b=linear.bias, grad_format=grad_format)
+
+    def forward(self, x: torch.Tensor, residual: torch.Tensor | None = None) -> torch.Tensor:
+        if x.dtype != torch.bfloat16 or (residual is not None and residual.dtype != torch.bfloat16):
+            raise TypeError("Float8LinearAct takes bf16 inputs")
+        if x.shape[-1] != self.in_features:
+            raise ValueError("the input's last dimension is not in_features")
+        if (x.numel() // self.in_features) % 16 or x.numel() == 0:
+            raise ValueError("Float8LinearAct needs a token count that is a multiple of 16")
+        if residual is not None and tuple(residual.shape) != (*x.shape[:-1], self.out_features):
+            raise ValueError("the residual must have the output's shape")
+        return _Float8LinearActFn.apply(x, self.weight, self.bias, residual, self.act, self.grad_format)
+
+    def extra_repr(self) -> str:
+        return (f"in_features={self.in_features}, out_features={self.out_features}, "
+                f"bias={self.bias is not None}, activation={self.activation}, float8=e4m3")
+
+
+class _ResidualNormFn(torch.autograd.Function):
+    """f8_residual_norm_fwd over the last dimension; backward from its inputs'
+    a, r_out and fp32 statistics (f8_residual_norm_bwd)."""
+
+    @staticmethod
+    def forward(ctx, a, r, gate, w_pre, b_pre, w_post, b_post, gate_rows, scale, kind, eps):
+        cols = a.shape[-1]
+        dense = [None if t is None else _dense(t) for t in (w_pre, b_pre, w_post, b_post)]
+        a2, r2 = _dense(a.reshape(-1, cols)), _dense(r.reshape(-1, cols))
+        g = None if gate is None else _dense(gate.reshape(-1, cols))
+        r_out, y, stats = block.f8_residual_norm_fwd(a2, r2, dense[0], dense[1], dense[2], dense[3], gate=g,
+                                                     gate_rows=gate_rows, scale=scale, kind=kind, eps=eps)
+        ctx.save_for_backward(a2, r_out, stats, dense[0], dense[2], dense[3], g)
+        ctx.set_materialize_grads(False)
+        ctx.args = dict(gate_rows=gate_rows, scale=scale, kind=kind)
+        ctx.shapes = a.shape, None if gate is None else gate.shape
+        return r_out.reshape(r.shape), y.reshape(a.shape)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dr_out, dy):
+        a, r_out, stats, w_pre, w_post, b_post, g = ctx.saved_tensors
+        if dr_out is None and dy is None:
+            return (None,) * 11
+        dy = torch.zeros_like(a) if dy is None else _dense(dy.reshape(a.shape))
+        dr_out = None if dr_out is None else _dense(dr_out.reshape(a.shape))
+        names = ("da", "dr", "dgate", "dw_pre", "db_pre", "dw_post", "db_post")
+        want = {n for n, need in zip(names, ctx.needs_input_grad) if need}
+        da, dr, dw_pre, db_pre, dw_post, db_post, dgate = block.f8_residual_norm_bwd(
+            dy, dr_out, a, r_out, w_pre, stats, w_post=w_post, b_post=b_post, gate=g, want=want, **ctx.args)
+        shape, gate_shape = ctx.shapes
+        return (None if da is None else da.reshape(shape), None if dr is None else dr.reshape(shape),
+                None if dgate is None else dgate.reshape(gate_shape), dw_pre, db_pre, dw_post, db_post,
+                None, None, None, None)
+
+
+class ResidualNorm(torch.nn.Module):
+    """The residual stream between two blocks: (r', y) of the stream r and a block's
+    output a [..., dim], with r' = scale r + gate * norm(a) and y = norm(r'), the
+    next block's input, in one pass.  kind "rms" or "layer" for both norms;
+    `post` False leaves a as it is; layer norms have biases.  The gate is given
+    with each call: [dim], or [groups, dim] where each gate is that of as many
+    consecutive rows (a [batch, seq, dim] with a gate [batch, dim]).  r may be fp32
+    beside a bf16 a."""
+
+    def __init__(self, dim: int, kind: str = "rms", post: bool = True, scale: float = 1.0, eps: float = 1e-5,
+                 device=None, dtype=torch.bfloat16):
+        super().__init__()
+        if dim < 1:
+            raise ValueError("a norm needs at least one feature")
+        if kind not in ("rms", "layer"):
+            raise ValueError("kind is 'rms' or 'layer'")
+        self.dim, self.scale, self.eps = dim, float(scale), float(eps)
+        self.kind = binding.F8_LAYER_NORM if kind == "layer" else binding.F8_RMS_NORM
+
+        def param(on: bool, value: float):
+            return torch.nn.Parameter(torch.full((dim,), value, device=device, dtype=dtype)) if on else None
+        layer = kind == "layer"
+        self.weight = param(True, 1.0)
+        self.register_parameter("bias", param(layer, 0.0))
+        self.register_parameter("post_weight", param(post, 1.0))
+        self.register_parameter("post_bias", param(post and layer, 0.0))
+
+    def forward(self, a: torch.Tensor, r: torch.Tensor, gate: torch.Tensor | None = None):
+        if a.dim() < 1 or a.shape[-1] != self.dim or r.shape != a.shape:
+            raise ValueError(f"a and r must have one shape, of {self.dim} features")
+        rows, gate_rows = a.numel() // self.dim, None
+        if gate is not None:
+            if gate.dim() < 1 or gate.shape[-1] != self.dim:
+                raise ValueError(f"the gate must have {self.dim} features")
+            groups = gate.numel() // self.dim
+            if groups < 1 or rows % groups:
+                raise ValueError("the rows must be a multiple of the gates")
+            gate_rows = max(rows // groups, 1)
+        return _ResidualNormFn.apply(a, r, gate, self.weight, self.bias, self.post_weight, self.post_bias,
+                                     gate_rows, self.scale, self.kind, self.eps)
+
+    def extra_repr(self) -> str:
+        kind = "layer" if self.kind == binding.F8_LAYER_NORM else "rms"
+        return f"{self.dim}, kind={kind}, post={self.post_weight is not None}, scale={self.scale}, eps={self.eps}"
+
+
+def _heads_dense(t: torch.Tensor) -> torch.Tensor:
+    return t if t.shape[-1] <= 1 or t.stride(-1) == 1 else t.contiguous()
+
+
+class _RopeFn(torch.autograd.Function):
+    """f8_rope; the gradient is the inverse turn."""
+
+    @staticmethod
+    def forward(ctx, q, k, positions, freqs, layout, scale):
+        ctx.save_for_backward(positions, freqs)
+        ctx.layout, ctx.scale = layout, scale
+        ctx.set_materialize_grads(False)
+        q_out, k_out = block.f8_rope(_heads_dense(q), positions, freqs, k=None if k is None else _heads_dense(k),
+                                     layout=layout, scale=scale)
+        return q_out if k is None else (q_out, k_out)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dq, dk=None):
+        positions, freqs = ctx.saved_tensors
+        given = [_heads_dense(t) for t in (dq, dk) if t is not None]
+        if not given:
+            return (None,) * 6
+        first, second = block.f8_rope(given[0], positions, freqs, k=given[1] if len(given) > 1 else None,
+                                      layout=ctx.layout, scale=ctx.scale, inverse=True)
+        return (None, first, None, None, None, None) if dq is None else (first, second, None, None, None, None)
+
+
+_SCALINGS = {"plain": binding.F8_ROPE_PLAIN, "linear": binding.F8_ROPE_LINEAR, "base": binding.F8_ROPE_BASE,
+             "by_parts": binding.F8_ROPE_BY_PARTS}
+
+
+class RotaryPositions(torch.nn.Module):
+    """Rotary positions for heads whose first `rot` columns turn: forward(q,
+    positions, k) gives the turned tensors, [tokens, heads, dim] or [batch, seq,
+    heads, dim] of any strides with dense columns, bf16 or fp32; positions int64,
+    negative where a row is padding (and is left as it is).  layout "half" or
+    "interleaved"; scaling "plain", "linear", "base" or "by_parts" with its
+    arguments as f8_rope_frequencies takes them; `scale` multiplies cosine and
+    sine."""
+
+    def __init__(self, rot: int, base: float = 10000.0, layout: str = "half", scaling: str = "plain",
+                 scale: float = 1.0, **more):
+        super().__init__()
+        if layout not in ("half", "interleaved"):
+            raise ValueError("layout is 'half' or 'interleaved'")
+        if scaling not in _SCALINGS:
+            raise ValueError(f"scaling is one of {', '.join(map(repr, _SCALINGS))}")
+        self.rot, self.scale = rot, float(scale)
+        self.layout = binding.F8_ROPE_HALF if layout == "half" else binding.F8_ROPE_INTERLEAVED
+        # fp64 and not a buffer: a cast of the module's type must not reach it
+        self._freqs = {None: block.f8_rope_frequencies(rot, base, _SCALINGS[scaling], **more)}
+
+    def frequencies(self, device) -> torch.Tensor:
+        device = torch.device(device)
+        if device not in self._freqs:
+            self._freqs[device] = self._freqs[None].to(device)
+        return self._freqs[device]
+
+    def forward(self, q: torch.Tensor, positions: torch.Tensor, k: torch.Tensor | None = None):
+        return _RopeFn.apply(q, k, positions, self.frequencies(q.device), self.layout, self.scale)
+
+    def extra_repr(self) -> str:
+        layout = "half" if self.layout == binding.F8_ROPE_HALF else "interleaved"
+        return f"rot={self.rot}, layout={layout}, scale={self.scale}"
