@@ -827,7 +827,7 @@ gemm_kernel(const __grid_constant__ GemmSet<NP> set, const __grid_constant__ Epi
             [[maybe_unused]] bool fetched = false;
             [[maybe_unused]] float bias[4];
             if constexpr (EPI == kEpiAct) {
-                static_assert(kCols == 128, "a lane's four biases cover the warp's columns");
+                static_assert(kCols <= 128, "a lane's four biases cover the warp's columns");
                 load_bias4(ep.bias, ep.bias_f32, col_base + 4 * lane, pr.N, bias, status);
                 fetched = ep.residual != nullptr && pr.tma_store != 0 && row0 < pr.M && col_base < pr.N;
                 if (fetched && lane == 0) {
@@ -1241,6 +1241,26 @@ bool few_rows(const GemmDesc &g, const DeviceInfo &dev)
     return g.M <= kBM || (g.M < 2 * kBM && gemm_few_plan(g.M, g.N, g.K, dev.sm_count).splits >= 4);
 }
 
+// Whether a CTA pair takes tiles of 256 x 128 instead of 256 x 256.  What it loads for a
+// tile is three quarters of the wider one's, and the tile's time nearly that, so they
+// pay where they take no more rounds of the pairs: 300 x 4096 x 4096 with bias and SiLU
+// 15.5 us against 17.3, with a residual and z kept too 17.3 against 21.2; 1000 x 4096 x
+// 4096 (two rounds against one) 25 against 18.  Where rows are stored element by
+// element, the epilogue's share makes up for half a round: 1000 x 5003 x 2064 with all
+// of it 35 against 39 (three against two).  F8_GEMM_TILE=128|256 forces one (for
+// measurement).
+bool narrow_tiles(const GemmDesc &g, const DeviceInfo &dev)
+{
+    const char *e = std::getenv("F8_GEMM_TILE");
+    if (e != nullptr)
+        return std::atoi(e) == 128;
+    const int64_t units = variant_units(kVariantPair, dev);
+    const SchedProblem p = sched_problem(g);
+    const int64_t wide = (sched_tiles(p, 2 * kBM, 256) + units - 1) / units;
+    const int64_t narrow = (sched_tiles(p, 2 * kBM, 128) + units - 1) / units;
+    return g.N % 8 == 0 ? narrow <= wide : narrow * 2 <= wide * 3;
+}
+
 cudaError_t launch_gemm_act(const GemmDesc &g, const ActEpilogue &e, const DeviceInfo &dev,
                             cudaStream_t stream)
 {
@@ -1255,7 +1275,10 @@ cudaError_t launch_gemm_act(const GemmDesc &g, const ActEpilogue &e, const Devic
         return launch_gemm_few(g, e, dev, stream);
     const int v = gemm_variant(g.M, dev);
     const SchedProblem sp = sched_problem(g);
-    const LaunchPlan plan = sched_plan(&sp, 1, variant_tile_m(v), 256, variant_units(v, dev));
+    const int bn = v == kVariantPair && narrow_tiles(g, dev) ? 128 : 256;
+    const LaunchPlan plan = sched_plan(&sp, 1, variant_tile_m(v), bn, variant_units(v, dev));
+    if (bn == 128)
+        return run_gemm<128, 6, true, kEpiAct>(&g, plan, dev, stream, ep);
     if (v == kVariantPair)
         return run_gemm<256, 5, true, kEpiAct>(&g, plan, dev, stream, ep);
     return run_gemm<256, 3, false, kEpiAct>(&g, plan, dev, stream, ep);

@@ -59,7 +59,7 @@ struct Args {
     const double *freqs;
     float scale;
     int inverse;
-    Div by_units, by_head_units, by_half;
+    Div by_units, by_heads, by_half;  // by_units of min(units, threads)
 };
 
 template <typename T, int VEC>
@@ -93,23 +93,79 @@ struct Vec<float, 1> {
     using type = uint32_t;
 };
 
-template <typename T, int VEC>
-union Bits {
-    typename Vec<T, VEC>::type v;
-    T e[VEC];
-    __device__ Bits() {}
-    __device__ Bits(const Bits &o) : v(o.v) {}
-    __device__ Bits &operator=(const Bits &o)
-    {
-        v = o.v;
-        return *this;
-    }
-};
+__device__ __forceinline__ float2 to_pair(uint32_t w)
+{
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+__device__ __forceinline__ uint32_t from_pair(float2 f)
+{
+    __nv_bfloat162 h = __float22bfloat162_rn(f);
+    return *reinterpret_cast<uint32_t *>(&h);
+}
 
-__device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
-__device__ __forceinline__ float to_f(float v) { return v; }
-__device__ __forceinline__ void from_f(float f, __nv_bfloat16 &v) { v = __float2bfloat16_rn(f); }
-__device__ __forceinline__ void from_f(float f, float &v) { v = f; }
+// A vector's elements as floats, and back.
+template <typename T, int VEC>
+__device__ __forceinline__ void unpack(const typename Vec<T, VEC>::type &v, float (&f)[VEC])
+{
+    if constexpr (sizeof(T) == 4) {
+        const float *p = reinterpret_cast<const float *>(&v);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+            f[e] = p[e];
+    } else if constexpr (VEC == 1) {
+        f[0] = __uint_as_float(static_cast<uint32_t>(v) << 16);
+    } else {
+        const uint32_t *p = reinterpret_cast<const uint32_t *>(&v);
+#pragma unroll
+        for (int i = 0; i < VEC / 2; ++i) {
+            const float2 g = to_pair(p[i]);
+            f[2 * i] = g.x, f[2 * i + 1] = g.y;
+        }
+    }
+}
+
+template <typename T, int VEC>
+__device__ __forceinline__ void pack(const float (&f)[VEC], typename Vec<T, VEC>::type &v)
+{
+    if constexpr (sizeof(T) == 4) {
+        float *p = reinterpret_cast<float *>(&v);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+            p[e] = f[e];
+    } else if constexpr (VEC == 1) {
+        v = __bfloat16_as_ushort(__float2bfloat16_rn(f[0]));
+    } else {
+        uint32_t *p = reinterpret_cast<uint32_t *>(&v);
+#pragma unroll
+        for (int i = 0; i < VEC / 2; ++i)
+            p[i] = from_pair(make_float2(f[2 * i], f[2 * i + 1]));
+    }
+}
+
+// One pair; the same roundings whatever the vector's width.
+__device__ __forceinline__ void turn_pair(float &x1, float &x2, float c, float s)
+{
+    const float y = fmaf(x1, c, -__fmul_rn(x2, s));
+    x2 = fmaf(x2, c, __fmul_rn(x1, s));
+    x1 = y;
+}
+
+// VEC cosines or sines from shared memory.
+template <int VEC>
+__device__ __forceinline__ void angles(const float *p, float (&f)[VEC])
+{
+    if constexpr (VEC >= 4) {
+#pragma unroll
+        for (int e = 0; e < VEC; e += 4) {
+            const float4 v = *reinterpret_cast<const float4 *>(p + e);
+            f[e] = v.x, f[e + 1] = v.y, f[e + 2] = v.z, f[e + 3] = v.w;
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+            f[e] = p[e];
+    }
+}
 
 // A frequency (radians a position) as a fraction of a turn in 64 bits; whole turns do
 // not count.  The double's 53 bits are moved to their place by shifts.
@@ -126,110 +182,85 @@ __device__ __forceinline__ uint64_t turn_fraction(double f)
 // A unit is VEC pairs: columns [VEC u, VEC u + VEC) and the same rot / 2 further on
 // (half), or [2 VEC u, 2 VEC u + 2 VEC) (interleaved).  Units from `turned` on are
 // two vectors of the columns that are copied, the last unit's second one perhaps
-// past the head's end.
-template <typename T, int VEC, bool HALF>
-struct Unit {
-    using V = typename Vec<T, VEC>::type;
-    Bits<T, VEC> v0, v1;
-    T *out;
-    int c0, c1, row, u;
-
-    __device__ __forceinline__ void load(const Args &a, int i, int64_t row0)
-    {
-        row = static_cast<int>(a.by_head_units(i));
-        const int hu = i - row * a.heads * a.units;
-        int h = static_cast<int>(a.by_units(hu));
-        u = hu - h * a.units;
-        const bool second = h >= a.heads0;
-        const Tensor &t = a.t[second ? 1 : 0];
-        if (second)
-            h -= a.heads0;
-        // positions of a block's rows in the batch: 32-bit division
-        const uint32_t r = static_cast<uint32_t>(row0) + row, b = r / static_cast<uint32_t>(a.seq);
-        const int64_t s = r - b * static_cast<uint32_t>(a.seq);
-        const T *x = static_cast<const T *>(t.x) + b * t.x_batch + s * t.x_seq + h * t.x_head;
-        out = static_cast<T *>(t.out) + b * t.out_batch + s * t.out_seq + h * t.out_head;
-        const bool turned = u < a.turned;
-        c0 = turned ? (HALF ? VEC * u : 2 * VEC * u) : 2 * a.half + 2 * VEC * (u - a.turned);
-        c1 = turned && HALF ? c0 + a.half : c0 + VEC;
-        v0.v = *reinterpret_cast<const V *>(x + c0);
-        if (c1 < a.dim)
-            v1.v = *reinterpret_cast<const V *>(x + c1);
-    }
-
-    __device__ __forceinline__ void rotate(const Args &a, const int64_t *at, const float2 *turn)
-    {
-        if (u >= a.turned || at[row] < 0)
-            return;
-        const float2 *cs = turn + row * a.half + VEC * u;
-        if (HALF || VEC == 1) {
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                const float p = to_f(v0.e[e]), q = to_f(v1.e[e]);
-                from_f(p * cs[e].x - q * cs[e].y, v0.e[e]);
-                from_f(q * cs[e].x + p * cs[e].y, v1.e[e]);
-            }
-        } else {
-#pragma unroll
-            for (int e = 0; e + 1 < VEC; e += 2) {
-                const float2 k0 = cs[e / 2], k1 = cs[VEC / 2 + e / 2];
-                float p = to_f(v0.e[e]), q = to_f(v0.e[e + 1]);
-                from_f(p * k0.x - q * k0.y, v0.e[e]);
-                from_f(q * k0.x + p * k0.y, v0.e[e + 1]);
-                p = to_f(v1.e[e]), q = to_f(v1.e[e + 1]);
-                from_f(p * k1.x - q * k1.y, v1.e[e]);
-                from_f(q * k1.x + p * k1.y, v1.e[e + 1]);
-            }
-        }
-    }
-
-    __device__ __forceinline__ void store(const Args &a) const
-    {
-        *reinterpret_cast<V *>(out + c0) = v0.v;
-        if (c1 < a.dim)
-            *reinterpret_cast<V *>(out + c1) = v1.v;
-    }
-};
-
+// past the head's end.  A thread keeps its unit and walks the rows' heads.
 template <typename T, int VEC, bool HALF>
 __global__ void __launch_bounds__(kThreads)
 rope_kernel(const __grid_constant__ Args a)
 {
-    extern __shared__ float2 turn[];  // [rows_per_block][half] cosine and sine, scaled
-    __shared__ int64_t at[kMaxRows];  // the rows' positions
+    using V = typename Vec<T, VEC>::type;
+    extern __shared__ __align__(16) float turn[];  // [2][rows_per_block][half] cosines, then sines, scaled
+    __shared__ int64_t at[kMaxRows], base[kMaxRows][4];  // the rows' positions, and where they start
     griddep_wait();
     griddep_launch_dependents();
     const int64_t row0 = static_cast<int64_t>(blockIdx.x) * a.rows_per_block;
     const int nrows = static_cast<int>(min(static_cast<int64_t>(a.rows_per_block), a.rows - row0));
     if (threadIdx.x < nrows) {
-        const uint32_t row = static_cast<uint32_t>(row0) + threadIdx.x, b = row / static_cast<uint32_t>(a.seq);
-        const int64_t s = row - b * static_cast<uint32_t>(a.seq);
+        const int64_t row = row0 + threadIdx.x, b = row / a.seq, s = row - b * a.seq;
         at[threadIdx.x] = a.pos[b * a.pos_batch + s * a.pos_seq];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            base[threadIdx.x][2 * k] = b * a.t[k].x_batch + s * a.t[k].x_seq;
+            base[threadIdx.x][2 * k + 1] = b * a.t[k].out_batch + s * a.t[k].out_seq;
+        }
     }
     __syncthreads();
-    // the first unit's loads are under way while the angles are formed
-    Unit<T, VEC, HALF> unit;
-    int i = threadIdx.x;
-    const int units = nrows * a.heads * a.units;
-    if (i < units)
-        unit.load(a, i, row0);
+    float *const cosines = turn, *const sines = turn + a.rows_per_block * a.half;
     for (int p = threadIdx.x; p < a.half * nrows; p += kThreads) {
         const int j = static_cast<int>(a.by_half(p));
         const uint64_t angle = turn_fraction(a.freqs[p - j * a.half]) * static_cast<uint64_t>(at[j]);
         const float t = static_cast<float>(static_cast<int32_t>(angle >> 32)) * 0x1p-31f;  // half turns
         float sn, cs;
         sincospif(t, &sn, &cs);
-        turn[p] = make_float2(cs * a.scale, (a.inverse ? -sn : sn) * a.scale);
+        cosines[p] = cs * a.scale;
+        sines[p] = (a.inverse ? -sn : sn) * a.scale;
     }
     __syncthreads();
-    while (i < units) {
-        Unit<T, VEC, HALF> next;
-        i += kThreads;
-        if (i < units)
-            next.load(a, i, row0);
-        unit.rotate(a, at, turn);
-        unit.store(a);
-        unit = next;
+    // thread = (slot of heads, unit)
+    const int wide = min(a.units, kThreads), slots = kThreads / wide;
+    const int slot = static_cast<int>(a.by_units(threadIdx.x)), heads = nrows * a.heads;
+    if (slot >= slots)
+        return;
+    for (int u = threadIdx.x - slot * wide; u < a.units; u += wide) {
+        const bool turned = u < a.turned;
+        const int c0 = turned ? (HALF ? VEC * u : 2 * VEC * u) : 2 * a.half + 2 * VEC * (u - a.turned);
+        const int c1 = turned && HALF ? c0 + a.half : c0 + VEC;
+        const bool second = c1 < a.dim;
+        for (int i = slot; i < heads; i += slots) {
+            const int j = static_cast<int>(a.by_heads(i));
+            int h = i - j * a.heads;
+            const int k = h >= a.heads0 ? 1 : 0;
+            h -= k ? a.heads0 : 0;
+            const Tensor &t = a.t[k];
+            const T *x = static_cast<const T *>(t.x) + base[j][2 * k] + h * t.x_head;
+            T *o = static_cast<T *>(t.out) + base[j][2 * k + 1] + h * t.out_head;
+            V v0 = *reinterpret_cast<const V *>(x + c0), v1 = v0;
+            if (second)
+                v1 = *reinterpret_cast<const V *>(x + c1);
+            if (turned && at[j] >= 0) {
+                float p[VEC], q[VEC], cs[VEC], sn[VEC];
+                unpack<T, VEC>(v0, p);
+                unpack<T, VEC>(v1, q);
+                const int from = j * a.half + VEC * u;
+                angles<VEC>(cosines + from, cs);
+                angles<VEC>(sines + from, sn);
+                if constexpr (HALF || VEC == 1) {
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e)
+                        turn_pair(p[e], q[e], cs[e], sn[e]);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < VEC; e += 2) {
+                        turn_pair(p[e], p[e + 1], cs[e / 2], sn[e / 2]);
+                        turn_pair(q[e], q[e + 1], cs[VEC / 2 + e / 2], sn[VEC / 2 + e / 2]);
+                    }
+                }
+                pack<T, VEC>(p, v0);
+                pack<T, VEC>(q, v1);
+            }
+            *reinterpret_cast<V *>(o + c0) = v0;
+            if (second)
+                *reinterpret_cast<V *>(o + c1) = v1;
+        }
     }
 }
 
@@ -240,17 +271,17 @@ cudaError_t run(Args &a, const DeviceInfo &dev, cudaStream_t st)
     a.units = a.turned + (a.dim - 2 * a.half + 2 * VEC - 1) / (2 * VEC);
     const int per_row = a.heads * a.units;
     // rows of a block: some 1024 units, while all SMs have blocks, within 32 KB of
-    // cosines and sines and the index's range
+    // cosines and sines
     int64_t r = std::min<int64_t>(kMaxRows, std::max(1, 1024 / per_row));
     r = std::min<int64_t>(r, std::max<int64_t>(1, a.rows / (4 * dev.sm_count)));
     r = std::min<int64_t>(r, std::max(1, 4096 / a.half));
     a.rows_per_block = static_cast<int>(r);
-    a.by_units = Div(static_cast<uint32_t>(a.units));
-    a.by_head_units = Div(static_cast<uint32_t>(per_row));
+    a.by_units = Div(static_cast<uint32_t>(std::min(a.units, kThreads)));
+    a.by_heads = Div(static_cast<uint32_t>(a.heads));
     a.by_half = Div(static_cast<uint32_t>(a.half));
     const int64_t blocks = (a.rows + r - 1) / r;
     return launch_pdl(rope_kernel<T, VEC, HALF>, dim3(static_cast<unsigned>(blocks)), dim3(kThreads),
-                      static_cast<size_t>(r) * a.half * sizeof(float2), st, a);
+                      2 * static_cast<size_t>(r) * a.half * sizeof(float), st, a);
 }
 
 template <typename T, bool HALF>
@@ -334,8 +365,6 @@ f8_status f8_rope(const f8_rope_tensor *tensors, int count, f8_dtype type, int64
     if (!some || heads == 0)
         return F8_OK;
     const int vec = vector_of(tensors, count, esize, batch, seq, dim, rot);
-    if (heads * (dim / vec) > 65535)  // units of a row, within the index's range
-        return F8_ERR_SHAPE;
     Args a = {};
     for (int i = 0; i < count; ++i) {
         const f8_rope_tensor &t = tensors[i];
