@@ -17,6 +17,8 @@ namespace rows {
 constexpr int kMaxStages = 8;
 constexpr int kMaxCluster = 4;
 constexpr int kMaxParts = 64;  // warps of a cluster
+constexpr int kPartsPitch = kMaxParts + 16;  // half the banks further on
+constexpr int kSumFloats = 2 * 4 * kPartsPitch;
 
 // How a block's threads lie over its columns.
 constexpr int kFull = 0;    // E / 8 vectors of eight each, all within the row, one block a row
@@ -125,6 +127,13 @@ __device__ __forceinline__ bool wait_soon(uint64_t *bar, uint32_t parity, uint64
     return mbar_wait(bar, parity, nullptr, limit_ns);
 }
 
+// A row's slot, the phase of its copies, and its memory.
+struct Cursor {
+    int slot;
+    uint32_t parity;
+    uint8_t *at;
+};
+
 // NA tensors of TA and NR of TR; a slot holds a slice of each.  Of the pointers, NULL
 // ones are left out.
 template <typename TA, int NA, typename TR, int NR, int MODE>
@@ -138,10 +147,6 @@ struct Slots {
     const TA *a[NA];
     const TR *r[NR];
     uint32_t pitch_a, pitch_r;
-    // the row being read: its slot, the slot's phase, its memory
-    int slot;
-    uint32_t parity;
-    uint8_t *at;
     // thread 0's copies
     uint32_t issued;
     int next;
@@ -151,7 +156,7 @@ struct Slots {
                                           const Slice &s, int s0)
     {
         shift = s0;
-        mem = at = memory;
+        mem = memory;
         full = bars;
         stages = n;
         cols = columns;
@@ -159,13 +164,16 @@ struct Slots {
         slice = s;
         pitch_a = slice_pitch<TA>(s.n);
         pitch_r = slice_pitch<TR>(s.n);
-        slot = next = 0;
-        parity = issued = 0u;
+        next = 0;
+        issued = 0u;
         ok = true;
     }
     __device__ __forceinline__ uint32_t slot_bytes() const { return NA * pitch_a + NR * pitch_r; }
-    __device__ __forceinline__ uint8_t *at_a(int i) const { return at + i * pitch_a; }
-    __device__ __forceinline__ uint8_t *at_r(int i) const { return at + NA * pitch_a + i * pitch_r; }
+    __device__ __forceinline__ uint8_t *at_a(const Cursor &c, int i) const { return c.at + i * pitch_a; }
+    __device__ __forceinline__ uint8_t *at_r(const Cursor &c, int i) const
+    {
+        return c.at + NA * pitch_a + i * pitch_r;
+    }
     __device__ __forceinline__ int64_t begin(int64_t row) const
     {
         return row * cols + slice.first - (MODE == kShift ? shift : 0);
@@ -216,30 +224,31 @@ struct Slots {
                 bulk_load(to + NA * pitch_a + i * pitch_r, r[i] + fr, br, bar);
     }
 
-    // Waits for the row at `slot`.  A wait that runs out sets the status; the thread
+    // Waits for the row at `c`.  A wait that runs out sets the status; the thread
     // then goes on without waiting, so that all keep to the barriers (what it stores is
     // of no use), and issues no more copies.
-    __device__ __forceinline__ void wait(uint64_t limit_ns, unsigned *status)
+    __device__ __forceinline__ void wait(const Cursor &c, uint64_t limit_ns, unsigned *status)
     {
-        if (ok && !wait_soon(&full[slot], parity, limit_ns)) {
+        if (ok && !wait_soon(&full[c.slot], c.parity, limit_ns)) {
             ok = false;
             atomicOr(status, kStatusTimeout);
         }
     }
-    __device__ __forceinline__ void step()
+    __device__ __forceinline__ Cursor first() const { return Cursor{0, 0u, mem}; }
+    __device__ __forceinline__ void step(Cursor &c) const
     {
-        at += slot_bytes();
-        if (++slot == stages) {
-            slot = 0;
-            at = mem;
-            parity ^= 1u;
+        c.at += slot_bytes();
+        if (++c.slot == stages) {
+            c.slot = 0;
+            c.at = mem;
+            c.parity ^= 1u;
         }
     }
 
     // Where a row's slice starts in its window, and the elements past the copied ones
     // (of the tensors' last row only) into the slot; all threads, with a barrier where
     // there are any.
-    __device__ __forceinline__ void ragged(int64_t row, int &shift_a, int &shift_r)
+    __device__ __forceinline__ void ragged(const Cursor &c, int64_t row, int &shift_a, int &shift_r)
     {
         const int64_t b = begin(row), end = b + slice.n;
         const Window<TA> wa(b, slice.n, total);
@@ -254,20 +263,20 @@ struct Slots {
 #pragma unroll
             for (int i = 0; i < NA; ++i)
                 if (a[i] != nullptr)
-                    reinterpret_cast<TA *>(at_a(i))[e - wa.first] = a[i][e];
+                    reinterpret_cast<TA *>(at_a(c, i))[e - wa.first] = a[i][e];
         }
         if (t < wr.tail) {
             const int64_t e = end - wr.tail + t;
 #pragma unroll
             for (int i = 0; i < NR; ++i)
                 if (r[i] != nullptr)
-                    reinterpret_cast<TR *>(at_r(i))[e - wr.first] = r[i][e];
+                    reinterpret_cast<TR *>(at_r(c, i))[e - wr.first] = r[i][e];
         }
         __syncthreads();
     }
 
     // The same for kShift, whose slices start at their vectors.
-    __device__ __forceinline__ void tail(int64_t row)
+    __device__ __forceinline__ void tail(const Cursor &c, int64_t row)
     {
         const int64_t b = begin(row);
         const int wa = whole<TA>(b), wr = whole<TR>(b), end = static_cast<int>(min(static_cast<int64_t>(slice.n), total - b));
@@ -278,13 +287,13 @@ struct Slots {
 #pragma unroll
             for (int i = 0; i < NA; ++i)
                 if (a[i] != nullptr)
-                    reinterpret_cast<TA *>(at_a(i))[wa + t] = a[i][b + wa + t];
+                    reinterpret_cast<TA *>(at_a(c, i))[wa + t] = a[i][b + wa + t];
         }
         if (wr + t < end) {
 #pragma unroll
             for (int i = 0; i < NR; ++i)
                 if (r[i] != nullptr)
-                    reinterpret_cast<TR *>(at_r(i))[wr + t] = r[i][b + wr + t];
+                    reinterpret_cast<TR *>(at_r(c, i))[wr + t] = r[i][b + wr + t];
         }
         __syncthreads();
     }
@@ -549,7 +558,7 @@ __device__ __forceinline__ void give_param(void *p, int f32, int64_t row, const 
 // gets them.  Each warp leaves its parts, in a cluster by a store to every block that
 // counts on that block's mbarrier: a cluster barrier's release would wait for the
 // rows' stores to global memory each time (8192 columns over two blocks, backward: 3.0 us
-// a row).  The two halves of `red` [2][2][kMaxParts] and of `bars` are used in turn; a
+// a row).  The two halves of `red` [2][4][kPartsPitch] and of `bars` are used in turn; a
 // half is written again only once every warp has left its part of the sum between,
 // which it does after reading this one.  `red` starts as zeros: parts are read four at
 // a time.
@@ -634,7 +643,7 @@ struct Sum {
     {
         h = half;
         half ^= 1;
-        return red + h * 2 * kMaxParts;
+        return red + h * 4 * kPartsPitch;
     }
     static __device__ __forceinline__ float warp(float a)
     {
@@ -664,16 +673,46 @@ struct Sum {
             v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
         int h;
         float *r = next(h);
-        leave(r + (upper ? kMaxParts : 0), v, (threadIdx.x & 15) == 0, h);
+        leave(r + (upper ? kPartsPitch : 0), v, (threadIdx.x & 15) == 0, h);
         meet(h, 2);
-        return make_float2(total(r), total(r + kMaxParts));
+        return make_float2(total(r), total(r + kPartsPitch));
+    }
+    // Of four values: a group of eight lanes gathers one each, on the way to the other
+    // warps and back.
+    __device__ __forceinline__ float4 operator()(float a, float b, float c, float d)
+    {
+        const int group = (threadIdx.x & 31) >> 3;
+        const bool up2 = (group & 2) != 0, up1 = (group & 1) != 0;
+        float u = up2 ? c : a, v = up2 ? d : b;
+        u += __shfl_xor_sync(0xFFFFFFFFu, up2 ? a : c, 16);
+        v += __shfl_xor_sync(0xFFFFFFFFu, up2 ? b : d, 16);
+        float s = up1 ? v : u;
+        s += __shfl_xor_sync(0xFFFFFFFFu, up1 ? u : v, 8);
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1)
+            s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+        int h;
+        float *r = next(h) + group * kPartsPitch;
+        leave(r, s, (threadIdx.x & 7) == 0, h);
+        meet(h, 4);
+        const int parts = static_cast<int>(ranks * (blockDim.x >> 5));
+        s = 0.0f;
+        for (int i = 2 * (threadIdx.x & 7); i < parts; i += 16) {
+            const float2 w = *reinterpret_cast<const float2 *>(r + i);
+            s += w.x + w.y;
+        }
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1)
+            s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+        return make_float4(__shfl_sync(0xFFFFFFFFu, s, 0), __shfl_sync(0xFFFFFFFFu, s, 8),
+                           __shfl_sync(0xFFFFFFFFu, s, 16), __shfl_sync(0xFFFFFFFFu, s, 24));
     }
     // Mean of the row and sum of the squared differences to it, from a full block's
     // warps of 32 E values each: a warp takes its own mean and its values' differences
     // to that, and the warps are joined by their means' differences to the row's.  As
     // exact as two passes, with one barrier.  x becomes x - mean.
     template <int E>
-    __device__ __forceinline__ float2 moments(float2 (&x)[E / 2])
+    __device__ __forceinline__ float2 moments(float2 (&x)[E / 2], float inv_w)
     {
         constexpr float kCount = 32.0f * E;
         float2 s = x[0];
@@ -692,29 +731,29 @@ struct Sum {
         int h;
         float *r = next(h);
         leave(r, mean, (threadIdx.x & 31) == 0, h);
-        leave(r + kMaxParts, m2, (threadIdx.x & 31) == 0, h);
+        leave(r + kPartsPitch, m2, (threadIdx.x & 31) == 0, h);
         meet(h, 2);
         const int w = static_cast<int>(blockDim.x >> 5);
-        const float mu = total(r) / static_cast<float>(w);
-        float2 between = make_float2(0.0f, 0.0f);
-        const float2 nu = make_float2(-mu, -mu);
-#pragma unroll
-        for (int i = 0; i < 16; i += 4) {
+        const float mu = total(r) * inv_w;
+        float2 all = make_float2(0.0f, 0.0f);
+        const float2 nu = make_float2(-mu, -mu), count = make_float2(kCount, kCount);
+        for (int i = 0; i < w; i += 4) {
             const float4 v = *reinterpret_cast<const float4 *>(r + i);
-            const float2 a = __fadd2_rn(make_float2(v.x, v.y), nu), b = __fadd2_rn(make_float2(v.z, v.w), nu);
-            if (i < w)
-                between.x = fmaf(a.x, a.x, between.x);
-            if (i + 1 < w)
-                between.y = fmaf(a.y, a.y, between.y);
-            if (i + 2 < w)
-                between.x = fmaf(b.x, b.x, between.x);
-            if (i + 3 < w)
-                between.y = fmaf(b.y, b.y, between.y);
+            const float4 q4 = *reinterpret_cast<const float4 *>(r + kPartsPitch + i);
+            float2 p = __fadd2_rn(make_float2(v.x, v.y), nu), o = __fadd2_rn(make_float2(v.z, v.w), nu);
+            if (i + 4 > w) {  // places past the last warp hold no mean
+                p.y = i + 1 < w ? p.y : 0.0f;
+                o.x = i + 2 < w ? o.x : 0.0f;
+                o.y = 0.0f;
+            }
+            all = __fadd2_rn(all, __fadd2_rn(make_float2(q4.x, q4.y), make_float2(q4.z, q4.w)));
+            all = __ffma2_rn(__fmul2_rn(p, p), count, all);
+            all = __ffma2_rn(__fmul2_rn(o, o), count, all);
         }
 #pragma unroll
         for (int i = 0; i < E / 2; ++i)
             x[i] = __fadd2_rn(x[i], nu);
-        return make_float2(mu, fmaf(between.x + between.y, kCount, total(r + kMaxParts)));
+        return make_float2(mu, all.x + all.y);
     }
 };
 
