@@ -50,8 +50,9 @@ def _typed(what: str, name: str, t: torch.Tensor | None, shape: tuple, index: in
 
 
 @functools.lru_cache(maxsize=1024)
-def _ws_bytes(lib, name: str, rows: int, cols: int) -> int:
-    """A workspace's bytes, which a training step asks for with the same few sizes."""
+def _ws_bytes(lib, name: str, rows: int, cols: int, index: int) -> int:
+    """The workspace's bytes of a call on device `index`: a training step asks for the
+    same few sizes again and again."""
     return int(getattr(lib, name)(rows, cols))
 
 
@@ -93,7 +94,7 @@ def f8_gemm_act(a: torch.Tensor, b: torch.Tensor, scale_a: torch.Tensor, scale_b
 
 
 def f8_act_bwd_workspace_bytes(rows: int, cols: int) -> int:
-    return _ws_bytes(binding.lib(), "f8_act_bwd_workspace_bytes", rows, cols)
+    return int(binding.lib().f8_act_bwd_workspace_bytes(rows, cols))
 
 
 def f8_act_bwd(dy: torch.Tensor, z: torch.Tensor | None, act: int, dz: torch.Tensor | None = None,
@@ -111,7 +112,9 @@ def f8_act_bwd(dy: torch.Tensor, z: torch.Tensor | None, act: int, dz: torch.Ten
     dbias_p, dbias_t = _typed(what, "dbias", dbias, (cols,), at)
     args = (binding._ptr(dy), _arg(what, "z", z, _BF16, shape, at), act, rows, cols,
             _arg(what, "dz", dz, _BF16, shape, at), dbias_p, dbias_t, _one(what, "amax_out", amax_out, at))
-    need = f8_act_bwd_workspace_bytes(rows, cols) if ws is None and dbias is not None else 0
+    need = 0
+    if ws is None and dbias is not None:
+        need = _ws_bytes(binding.lib(), "f8_act_bwd_workspace_bytes", rows, cols, at)
     ws, *space = _ws(what, ws, need, dy, stream)
     _call(what, stream, *args, *space)
     return dz, dbias
@@ -209,7 +212,7 @@ def _residual_norm(what: str, a, r, w_pre, b_pre, w_post, b_post, gate, gate_row
     at, shape, wt = a.get_device(), (cols,), w_pre.dtype
     gt, gp = binding.F8_BF16, 0
     if gate is not None:
-        gate_rows = max(rows, 1) if gate_rows is None else int(gate_rows)
+        gate_rows = max(rows, 1) if gate_rows is None else min(int(gate_rows), 1 << 62)
         if gate_rows < 1:
             raise ValueError(f"{what}: gate_rows must be at least 1")
         whole = gate.dim() == 1 and rows <= gate_rows  # one gate for all rows
@@ -254,7 +257,7 @@ _WANT = {(layer, post, gated): frozenset(
 
 
 def f8_residual_norm_bwd_workspace_bytes(rows: int, cols: int) -> int:
-    return _ws_bytes(binding.lib(), "f8_residual_norm_bwd_workspace_bytes", rows, cols)
+    return int(binding.lib().f8_residual_norm_bwd_workspace_bytes(rows, cols))
 
 
 def f8_residual_norm_bwd(dy: torch.Tensor, dr_out: torch.Tensor | None, a: torch.Tensor,
@@ -293,7 +296,8 @@ def f8_residual_norm_bwd(dy: torch.Tensor, dr_out: torch.Tensor | None, a: torch
         _arg(what, "dw_post", dw_post, wt, cols, at), _arg(what, "db_post", db_post, wt, cols, at),
         0 if dgate is None else _arg(what, "dgate", dgate, wt if gate is None else gate.dtype,
                                      cols if gate is None else gate.shape, at))
-    ws, *space = _ws(what, ws, f8_residual_norm_bwd_workspace_bytes(*shape) if ws is None else 0, a, stream)
+    need = 0 if ws is not None else _ws_bytes(binding.lib(), "f8_residual_norm_bwd_workspace_bytes", *shape, at)
+    ws, *space = _ws(what, ws, need, a, stream)
     _call(what, stream, n, _arg(what, "dy", dy, xt, shape, at),
           _arg(what, "dr_out", dr_out, rt, shape, at), binding._ptr(a), _arg(what, "r_out", r_out, rt, shape, at),
           _arg(what, "stats", stats, _F32, (4, shape[0]), at), grads, *space)

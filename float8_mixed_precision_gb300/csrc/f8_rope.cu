@@ -351,6 +351,9 @@ f8_status f8_rope(const f8_rope_tensor *tensors, int count, f8_dtype type, int64
         // in place means in place: another order of the rows would read what it wrote
         if (t.x == t.out && (t.x_batch != t.out_batch || t.x_seq != t.out_seq || t.x_head != t.out_head))
             return F8_ERR_INVALID;
+        // rows of the output lie apart
+        if ((batch > 1 && t.out_batch == 0) || (seq > 1 && t.out_seq == 0) || (t.heads > 1 && t.out_head == 0))
+            return F8_ERR_INVALID;
         if (!aligned(t.x, esize) || !aligned(t.out, esize))
             return F8_ERR_ALIGN;
     }

@@ -828,7 +828,8 @@ typedef enum { F8_ROPE_HALF = 0, F8_ROPE_INTERLEAVED = 1 } f8_rope_layout;
 /*
  * One tensor of f8_rope, [batch, seq, heads, dim] with its columns dense and any
  * strides (in elements) of the batch, the sequence and the heads; `out` has strides
- * of its own.  out may be x with x's strides; it may not overlap x otherwise.
+ * of its own, none 0 of more than one batch, row or head.  out may be x with x's
+ * strides; it may not overlap x otherwise.
  */
 typedef struct {
     const void *x;

@@ -71,7 +71,9 @@ def test_rope_refusals(L):
         (4, 1 << 40, SHAPE), (8, P + 4, ALIGN), (11, P + 4, ALIGN), (0, _rope_args(x=P + 1), ALIGN),
         (0, _rope_args(out=P + 1), ALIGN), (0, _rope_args(x=None), INVALID), (0, _rope_args(out=None), INVALID),
         (0, _rope_args(heads=-1), INVALID), (0, _rope_args(heads=1 << 13), SHAPE),
-        (0, _rope_args(out=P, out_seq=1024), INVALID)])     # in place, but elsewhere
+        (0, _rope_args(out=P, out_seq=1024), INVALID),      # in place, but elsewhere
+        (0, _rope_args(out_head=0), INVALID), (0, _rope_args(out_seq=0), INVALID),
+        (0, _rope_args(out_batch=0), INVALID)])             # outputs on one another
 
 
 def _norm_args(**kw):

@@ -257,6 +257,20 @@ def test_nan_passes(f8, act):
     assert torch.isnan(y[:, 5]).all() and torch.isnan(y).sum() == 2
 
 
+@pytest.mark.parametrize("shape", [(40, 9), (40, 131), (300, 1001), (70, 5003)])
+def test_bwd_neighbours_of_odd_rows(f8, shape):
+    """NaN and infinities at a row's ends reach their own columns' sums only, and no other row."""
+    gen = torch.Generator(device=DEV).manual_seed(53)
+    z, dy = (torch.randn(shape, generator=gen, device=DEV).to(BF) for _ in range(2))
+    dz, db = f8.f8_act_bwd(dy, z, f8.F8_ACT_SILU)
+    dirty = dy.clone()
+    dirty[3, -1], dirty[11, 0], dirty[26, -1] = float("nan"), float("inf"), float("-inf")
+    got, gb = f8.f8_act_bwd(dirty, z, f8.F8_ACT_SILU)
+    same = torch.isfinite(dirty)
+    assert torch.equal(got[same], dz[same]) and not torch.isfinite(got[~same]).any()
+    assert torch.equal(gb[1:-1], db[1:-1]) and not torch.isfinite(gb[[0, -1]]).any()
+
+
 @pytest.mark.parametrize("act", ref.ACTS[1:])
 def test_bwd_against_differences(f8, act):
     """The slope against differences of the forward call's own values, whose inputs a bias in 32 bits brings; at points

@@ -179,6 +179,33 @@ def test_nan_stays_in_its_row(f8, cols):
     assert torch.isnan(got[1][17]).all() and torch.isnan(got[1][29]).any()
 
 
+@pytest.mark.parametrize("cols", [9, 131, 1001, 4095, 5003])
+@pytest.mark.parametrize("kind", ["layer", "rms"])
+@pytest.mark.parametrize("rt", [BF, F32], ids=["bf16", "f32"])
+def test_neighbours_of_odd_rows(f8, cols, kind, rt):
+    """Rows that share their first and last 16 bytes with others: NaN and infinities at a row's ends stay there, forward
+    and backward, and rows behind it are as without them."""
+    layer = kind == "layer"
+    s = _inputs(40, cols, BF, rt, gate_rows=40)
+    kw = _kw(f8, s, layer, 1.0)
+    want = f8.f8_residual_norm_fwd(s["a"], s["r"], s["w_pre"], b_pre=s["b_pre"], eps=EPS, **kw)
+    names = ("da", "dr")
+    grads = f8.f8_residual_norm_bwd(s["dy"], s["dr_out"], s["a"], want[0], s["w_pre"], want[2], want=names, **kw)[:2]
+    bad = [3, 11, 26]
+    dirty = dict(s, a=s["a"].clone(), r=s["r"].clone(), dy=s["dy"].clone(), dr_out=s["dr_out"].clone())
+    for name in ("a", "r", "dy", "dr_out"):
+        dirty[name][3, -1], dirty[name][11, 0], dirty[name][26, -1] = float("nan"), float("inf"), float("-inf")
+    got = f8.f8_residual_norm_fwd(dirty["a"], dirty["r"], s["w_pre"], b_pre=s["b_pre"], eps=EPS, **kw)
+    clean = torch.ones(40, dtype=torch.bool, device=DEV)
+    clean[bad] = False
+    for u, v in zip(got[:2], want[:2]):
+        assert torch.equal(u[clean], v[clean])
+    back = f8.f8_residual_norm_bwd(dirty["dy"], dirty["dr_out"], dirty["a"], got[0], s["w_pre"], got[2], want=names, **kw)[:2]
+    for u, v in zip(back, grads):
+        assert torch.equal(u[clean], v[clean])
+    f8.f8_last_device_status()
+
+
 def test_differences(f8):
     """The gradients against differences of the forward call along random directions, in fp32."""
     s = _inputs(24, 200, F32, F32, F32, gt=F32, gate_rows=5, seed=3)
