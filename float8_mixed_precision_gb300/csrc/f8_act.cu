@@ -12,6 +12,10 @@
 // no multiple of eight, a row starts inside a vector, at an element that depends on the
 // row's number modulo eight alone.  A warp's rows are eight apart, so its lanes keep
 // their columns all the same; only a row's first and last vector go element by element.
+//
+// Measured, with the bias's gradient: tanh-GELU 8192 x 14336 112 us, 6.3 TB/s of the 6.8
+// of a plain copy (at eight rows a warp in flight and two blocks an SM 126 us); GELU 1999
+// x 5003 23 us of 8.8 for the bytes, in rows element by element 38.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -218,7 +222,7 @@ act_reduce_kernel(const float *__restrict__ parts, const float *__restrict__ car
 // once, of at least 32 rows (four of each warp).  Even widths: one round for chunks of
 // up to 64 rows and up to four for more; 1999 x 5000 in one round 12 us, in two 14.  Odd
 // ones, whose rows' first and last vectors keep their warps longer, two: 1999 x 5003 in
-// one round 23 us, in two 21.5, in four 24.
+// one round 23 us, in two 22, in four 24.
 struct Plan {
     int64_t strips, chunks, chunk;
     bool even, direct;  // direct: the one chunk's sums are the result

@@ -26,7 +26,10 @@
 // columns the epilogue forms z = acc / (sa sb) + bias and y = act(z) + residual in
 // fp32 and writes y, and z where it is kept, each rounded once.  The residual's box
 // comes by TMA into the buffer that y leaves from while the activation is formed.
-// Eight epilogue warps: one a scheduler does not keep up with the products.
+// Eight epilogue warps: one a scheduler does not keep up with the products.  8192 x
+// 14336 x 4096, each alone: f8_gemm 272 us, with a bias 285, tanh-GELU 293, z kept as
+// well 320; with four epilogue warps 312 and 341 on codes that took f8_gemm 255.  Back to
+// back, at the power limit, the last takes 355: 2.7 PFLOP/s.
 // Two shapes of the same kernel:
 //   PAIR = false  one CTA computes a 128 x BN tile (tcgen05 cta_group::1);
 //   PAIR = true   a cluster of two CTAs on neighbouring SMs computes a

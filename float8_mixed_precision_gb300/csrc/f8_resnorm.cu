@@ -12,7 +12,19 @@
 // into chunks; a chunk leaves one partial row of each parameter's gradient, writes
 // the gate gradients whose rows it has whole, and leaves partial rows for the gates
 // of its first and last rows where those reach into other chunks.  Partial rows are
-// added in order by kernels of their own.  No atomics: equal inputs give equal bits.
+// added in order by a kernel of its own.  No atomics: equal inputs give equal bits.
+//
+// Both are bound by HBM: four values moved per element forward, six backward.  A row's
+// values stay in registers between the loads and the stores, 16 a thread forward and 8
+// backward (beside the column sums of five gradients), and rows come some ahead through
+// shared memory by bulk copies (f8_resnorm_rows.cuh); with the rows read again for each
+// reduction 8192 x 4096 took 327 us forward and 482 backward.  What is left is the
+// arithmetic, some 600 instructions a warp and row forward, with two rows in work an SM.
+//
+// Measured, bf16, gates of 1024 rows: 8192 x 4096 layer norm forward 58 us, 4.6 TB/s;
+// RMS norm backward with every gradient 82 us, 4.9 TB/s; a plain copy runs at 6.8.  1999 x
+// 5003 with an fp32 stream and layer norms, backward, 97 us of 26.5 for the bytes: a row
+// takes a cluster, with one row in work and an exchange of 1 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -269,6 +281,7 @@ bwd_walk_kernel(const Call c, const TA *__restrict__ dy, const TR *__restrict__ 
 // and rows come some ahead through shared memory.
 using rows::Param;
 constexpr int kFwdE = 16, kBwdE = 8;  // columns of a thread
+constexpr int kThreads = 512;         // of a block at most, but for wide_block()'s
 
 __device__ __forceinline__ float2 splat(float v) { return make_float2(v, v); }
 
@@ -602,8 +615,8 @@ cols_walk_kernel(const Call c, const Chunks ch, const TA *__restrict__ dy, const
 // The backward pass in one: a unit (a block, or a cluster by column slices) walks the
 // chunk `unit` of rows, with the column sums of all gradients in registers.  FULL:
 // with means or biases; without, the sums that only those need are left out.
-template <typename TA, typename TR, int MODE, bool FULL, bool BF>
-__global__ void __launch_bounds__(512, 1)
+template <typename TA, typename TR, int MODE, bool FULL, bool BF, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1)
 bwd_kernel(const Call c, const Chunks ch, const TA *__restrict__ dy, const TR *__restrict__ dr_out,
            const TA *__restrict__ a, const TR *__restrict__ r_out, TA *__restrict__ da,
            TR *__restrict__ dr, float *__restrict__ parts, float *__restrict__ ends,
@@ -704,7 +717,7 @@ bwd_kernel(const Call c, const Chunks ch, const TA *__restrict__ dy, const TR *_
     // next, and phase two forms phase one's values again from the slot: 8192 columns,
     // layer norm, 1999 rows 80 us against 95, where 8192 x 4096 in one block takes 84
     // us so, and 80 with two barriers.
-    constexpr bool kTwo = MODE == rows::kFull;
+    constexpr bool kTwo = MODE == rows::kFull || THREADS > kThreads;
     [[maybe_unused]] float2 kept_h[P], kept_e[P];
     // Phase one of a row: the sums that D needs, and the gradients of w2 and b2.
     auto one = [&](int64_t row, const Stats &v) {
@@ -962,12 +975,11 @@ struct Plan {
 
 // 512 threads of 128 registers an SM, of `e` columns each, in blocks that hold a row's
 // slice; slices of whole vectors, the last one perhaps shorter.
-Plan plan_of(int64_t cols, int e)
+Plan plan_of(int64_t cols, int e, int most = kThreads)
 {
-    constexpr int kThreads = 512;
     Plan p;
     p.ranks = 1;
-    while (p.ranks * kThreads * e < width_of(cols))
+    while (p.ranks * most * e < width_of(cols))
         p.ranks *= 2;
     const int64_t width = width_of(cols);
     p.slice = static_cast<int>((width + 8 * p.ranks - 1) / (8 * p.ranks)) * 8;
@@ -977,12 +989,27 @@ Plan plan_of(int64_t cols, int e)
 }
 
 Plan fwd_plan(int64_t cols) { return plan_of(cols, kFwdE); }
-Plan bwd_plan(int64_t cols) { return plan_of(cols, kBwdE); }
+
+// Backward, a block of 640 threads (96 registers each) takes rows of up to 5120 columns
+// with bf16 parameters, where a cluster of two would have one row in work on two SMs: 8192
+// x 5120 RMS norm 103 us against 179, layer norm 144 against 213.  Not those of odd widths
+// with the sums of means and biases, which do not fit the registers: 1999 x 5003 layer
+// norm with an fp32 stream 101 us against 93, RMS norm 68 against 76.
+constexpr int kWideThreads = 640;
+bool wide_width(int64_t cols)
+{
+    return width_of(cols) > kThreads * kBwdE && width_of(cols) <= kWideThreads * kBwdE;
+}
+bool wide_block(int64_t cols, bool full, bool bf)
+{
+    return bf && wide_width(cols) && (cols % 8 == 0 || !full);
+}
+Plan bwd_plan(int64_t cols, bool wide) { return plan_of(cols, kBwdE, wide ? kWideThreads : kThreads); }
 
 // Most units (blocks, or clusters) of the backward pass.
 int64_t bwd_units(int64_t rows, int64_t cols, int sms)
 {
-    const Plan p = bwd_plan(cols);
+    const Plan p = bwd_plan(cols, wide_width(cols));
     return std::max<int64_t>(8, std::min<int64_t>((rows + 7) / 8 * 8, static_cast<int64_t>(sms) * p.per_sm / p.ranks));
 }
 
@@ -1132,14 +1159,14 @@ cudaError_t fwd(const Call &c, const void *a, const void *r, void *r_out, void *
                       static_cast<TR *>(r_out), static_cast<TA *>(y), amax, dev.status);
 }
 
-template <typename TA, typename TR, int MODE, bool FULL, bool BF>
+template <typename TA, typename TR, int MODE, bool FULL, bool BF, int THREADS>
 cudaError_t bwd_rows(const Call &c, Chunks &ch, int *shared, const void *dy, const void *dr_out, const void *a,
                      const void *r_out, const f8_residual_norm_grads &g, float *parts, float *ends,
                      const DeviceInfo &dev, cudaStream_t st)
 {
-    const Plan p = bwd_plan(c.cols);
+    const Plan p = bwd_plan(c.cols, THREADS == kWideThreads);
     Shape s;
-    const cudaError_t e = shape_of<bwd_kernel<TA, TR, MODE, FULL, BF>>(
+    const cudaError_t e = shape_of<bwd_kernel<TA, TR, MODE, FULL, BF, THREADS>>(
         p, 2 * (rows::slice_pitch<TA>(p.slice) + rows::slice_pitch<TR>(p.slice)), dev, &s);
     if (e != cudaSuccess)
         return e;
@@ -1148,9 +1175,9 @@ cudaError_t bwd_rows(const Call &c, Chunks &ch, int *shared, const void *dy, con
     // kShift's units have room for two gates of their chunk
     if constexpr (MODE == rows::kShift)
         if (c.gate != nullptr && c.gate_rows < ch.chunk)
-            return bwd_rows<TA, TR, rows::kRagged, FULL, BF>(c, ch, shared, dy, dr_out, a, r_out, g, parts, ends,
+            return bwd_rows<TA, TR, rows::kRagged, FULL, BF, THREADS>(c, ch, shared, dy, dr_out, a, r_out, g, parts, ends,
                                                              dev, st);
-    return launch_pdl_cluster(bwd_kernel<TA, TR, MODE, FULL, BF>, dim3(static_cast<unsigned>(units * p.ranks)),
+    return launch_pdl_cluster(bwd_kernel<TA, TR, MODE, FULL, BF, THREADS>, dim3(static_cast<unsigned>(units * p.ranks)),
                               dim3(static_cast<unsigned>(p.threads)), s.smem, st,
                               static_cast<unsigned>(p.ranks), c, ch, static_cast<const TA *>(dy),
                               static_cast<const TR *>(dr_out), static_cast<const TA *>(a),
@@ -1174,17 +1201,23 @@ cudaError_t bwd(const Call &c, const void *dy, const void *dr_out, const void *a
     cudaError_t e;
     if (in_registers(c.cols)) {
         const bool full = c.layer || c.b_post != nullptr || g.db_pre != nullptr || g.db_post != nullptr;
-        auto run = [&](auto mode, auto all, auto bf) {
-            return bwd_rows<TA, TR, mode.value, all.value, bf.value>(c, ch, &shared, dy, dr_out, a, r_out, g, parts,
-                                                                     ends, dev, st);
+        auto run = [&](auto mode, auto all, auto bf, auto threads) {
+            return bwd_rows<TA, TR, mode.value, all.value, bf.value, threads.value>(c, ch, &shared, dy, dr_out, a,
+                                                                                   r_out, g, parts, ends, dev, st);
         };
-        const Plan p = bwd_plan(c.cols);
-        if (params_bf16(c))
-            e = full ? by_mode(c.cols, p, kBwdE, true, [&](auto m) { return run(m, yes, yes); })
-                     : by_mode(c.cols, p, kBwdE, true, [&](auto m) { return run(m, no, yes); });
+        constexpr std::integral_constant<int, kThreads> usual;
+        constexpr std::integral_constant<int, kWideThreads> more;
+        const bool bf = params_bf16(c), wide = wide_block(c.cols, full, bf);
+        const Plan p = bwd_plan(c.cols, wide);
+        auto modes = [&](auto all, auto bf16, auto threads) {
+            return by_mode(c.cols, p, kBwdE, true, [&](auto m) { return run(m, all, bf16, threads); });
+        };
+        if (wide)
+            e = full ? modes(yes, yes, more) : modes(no, yes, more);
+        else if (bf)
+            e = full ? modes(yes, yes, usual) : modes(no, yes, usual);
         else
-            e = full ? by_mode(c.cols, p, kBwdE, true, [&](auto m) { return run(m, yes, no); })
-                     : by_mode(c.cols, p, kBwdE, true, [&](auto m) { return run(m, no, no); });
+            e = full ? modes(yes, no, usual) : modes(no, no, usual);
     } else {
         float *consts = reinterpret_cast<float *>(ws + w.consts);
         const auto *dy_ = static_cast<const TA *>(dy), *a_ = static_cast<const TA *>(a);

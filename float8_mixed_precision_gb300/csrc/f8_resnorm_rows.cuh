@@ -16,6 +16,7 @@ namespace rows {
 
 constexpr int kMaxStages = 8;
 constexpr int kMaxCluster = 4;
+constexpr int kMaxWarps = 20;  // of a block
 constexpr int kMaxParts = 64;  // warps of a cluster
 constexpr int kPartsPitch = kMaxParts + 16;  // half the banks further on
 constexpr int kSumFloats = 2 * 4 * kPartsPitch;
@@ -623,9 +624,9 @@ struct Sum {
     __device__ __forceinline__ float total(const float *from) const
     {
         float2 s = make_float2(0.0f, 0.0f);
-        if (single()) {  // at most 16 warps
+        if (single()) {
 #pragma unroll
-            for (int i = 0; i < 16; i += 4) {
+            for (int i = 0; i < kMaxWarps; i += 4) {
                 const float4 v = *reinterpret_cast<const float4 *>(from + i);
                 s = __fadd2_rn(s, __fadd2_rn(make_float2(v.x, v.y), make_float2(v.z, v.w)));
             }

@@ -2,8 +2,11 @@
 //
 // Bound by HBM: each element is read and written once, with three operations on it.
 // A block takes a few rows (tokens) and forms their cosines and sines once in shared
-// memory, for all heads of queries and keys; then its threads walk the rows' heads,
-// each moving two vectors of VEC elements that hold VEC whole pairs.
+// memory, for all heads of queries and keys; then a thread keeps its place in the head
+// and walks the rows' heads, moving two vectors of VEC elements that hold VEC whole
+// pairs.  Addresses are the larger part of its instructions: with a place and a head
+// worked out per unit, and the rows' starts by division, 8192 rows of 32 + 8 heads of 128
+// (96 turned, out of a packed projection) took 34.6 us; so 30.0, 5.6 TB/s.
 //
 // The angle: a frequency becomes a fraction of a turn in 64-bit fixed point, so
 // position * fraction mod 2^64 is the angle's fraction of a turn, exactly; its upper

@@ -126,6 +126,15 @@ def test_gates(f8, rows, gate_rows):
         _check(f8, s, True, 1.0, f"{rows} rows by {gate_rows}")
 
 
+@pytest.mark.parametrize("layer, bias", [(True, True), (False, False)], ids=["layer", "rms"])
+@pytest.mark.parametrize("cols", [4098, 4104, 4608, 4999, 5113, 5114, 5120, 5128])
+def test_wide_blocks(f8, cols, layer, bias):
+    """Widths just above a block's usual columns."""
+    for i, (rt, rows, gate_rows) in enumerate([(BF, 21, 1), (F32, 200, 67), (BF, 333, 333), (F32, 3, 2)]):
+        s = _inputs(rows, cols, BF, rt, gate_rows=gate_rows, bias=bias, seed=i)
+        _check(f8, s, layer, 0.75, f"{rows}x{cols} by {gate_rows} {rt}")
+
+
 def test_one_gate_for_all(f8):
     s = _inputs(40, 256, gate_rows=40)
     want = _check(f8, s, False, 1.0, "rows")
