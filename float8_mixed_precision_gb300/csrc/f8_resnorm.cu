@@ -615,7 +615,11 @@ cols_walk_kernel(const Call c, const Chunks ch, const TA *__restrict__ dy, const
 // The backward pass in one: a unit (a block, or a cluster by column slices) walks the
 // chunk `unit` of rows, with the column sums of all gradients in registers.  FULL:
 // with means or biases; without, the sums that only those need are left out.
-template <typename TA, typename TR, int MODE, bool FULL, bool BF, int THREADS>
+// Of a gate's rows only S = sum D e1 and T = sum D are kept: they give dgate = w1 S + b1 T,
+// and g S and g T for dw1 and db1, whose sums over several gates lie in shared memory.
+// With u formed for each row and its three sums, five parameters' columns and five sums
+// a thread, 8192 x 4096 RMS norm took OLDSUM us and 1999 x 5003 layer norm 97.
+template <typename TA, typename TR, int MODE, bool FULL, int THREADS>
 __global__ void __launch_bounds__(THREADS, 1)
 bwd_kernel(const Call c, const Chunks ch, const TA *__restrict__ dy, const TR *__restrict__ dr_out,
            const TA *__restrict__ a, const TR *__restrict__ r_out, TA *__restrict__ da,
@@ -660,34 +664,59 @@ bwd_kernel(const Call c, const Chunks ch, const TA *__restrict__ dy, const TR *_
     rows::Sum<MODE> sum;
     sum.start(red, meets, rank, static_cast<uint32_t>(ranks), limit_ns, status);
     const float inv_c = 1.0f / static_cast<float>(c.cols);
-    const bool post = c.w_post != nullptr, gated = c.gate != nullptr, layer = FULL && c.layer;
-    Param<E, BF> w2, w1, b1, g;
+    const bool post = c.w_post != nullptr, layer = FULL && c.layer;
+    float2 *acc = reinterpret_cast<float2 *>(dyn + stages * slots.slot_bytes()) + threadIdx.x;
+    auto acc_at = [&](int i) -> float2 & { return acc[i * blockDim.x]; };
+    float *p = parts + unit * 4 * c.cols;
+    Param<E, false> w2, gw;  // gw: gate w1
     rows::take_param<MODE>(c.w_pre, c.w_f32, 0, pl, 1.0f, w2);
-    rows::take_param<MODE>(c.w_post, c.w_f32, 0, pl, 1.0f, w1);
-    if (FULL)
-        rows::take_param<MODE>(c.b_post, c.w_f32, 0, pl, 0.0f, b1);
-    float2 dw2[P], db2[P], dw1[P], db1[P], dg[P];
+    float2 dw2[P], db2[P], S[P], T[P];
 #pragma unroll
     for (int i = 0; i < P; ++i)
-        dw2[i] = db2[i] = dw1[i] = db1[i] = dg[i] = splat(0.0f);
-    int64_t gate = 0, gate_end = gated ? first : stop;
-    rows::take_param<MODE>(nullptr, 0, 0, pl, 1.0f, g);
+        dw2[i] = db2[i] = S[i] = T[i] = splat(0.0f);
+    int64_t gate = 0, gate_end = first;
+    bool begun = false;  // acc holds sums
     // What a gate's rows of this unit have given, into place.  Units of kShift share
     // their chunk's gates, of which there are at most two.
     int left = 0;  // which of the unit's two partial rows are written
-    auto flush = [&]() {
-        if (dgate == nullptr)
-            return;
-        if (MODE != rows::kShift && ch.whole(gate, walk.chunk)) {
-            rows::give_param<MODE, E>(dgate, c.g_f32, gate * c.cols, pl, dg);
-        } else {
-            const int to = ch.slot(gate, walk.chunk);
-            left |= 1 << to;
-            rows::give_sums<MODE, E>(ends + (unit * 2 + to) * c.cols, pl, dg);
-        }
+    auto close = [&](bool last) {
+        Param<E, false> w;
+        float2 v[P];
+        if (dgate != nullptr) {
+            rows::take_param<MODE>(c.w_post, c.w_f32, 0, pl, 1.0f, w);
 #pragma unroll
-        for (int i = 0; i < P; ++i)
-            dg[i] = splat(0.0f);
+            for (int i = 0; i < P; ++i)
+                v[i] = __fmul2_rn(S[i], w.pair(i));
+            if (FULL) {
+                rows::take_param<MODE>(c.b_post, c.w_f32, 0, pl, 0.0f, w);
+#pragma unroll
+                for (int i = 0; i < P; ++i)
+                    v[i] = __ffma2_rn(T[i], w.pair(i), v[i]);
+            }
+            if (MODE != rows::kShift && ch.whole(gate, walk.chunk)) {
+                rows::give_param<MODE, E>(dgate, c.g_f32, gate * c.cols, pl, v);
+            } else {
+                const int to = ch.slot(gate, walk.chunk);
+                left |= 1 << to;
+                rows::give_sums<MODE, E>(ends + (unit * 2 + to) * c.cols, pl, v);
+            }
+        }
+        rows::take_param<MODE>(c.gate, c.g_f32, gate * c.cols, pl, 1.0f, w);
+        auto join = [&](float2 (&of)[P], int at, int row) {
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                v[i] = __ffma2_rn(of[i], w.pair(i), begun ? acc_at(at + i) : splat(0.0f));
+                if (!last)
+                    acc_at(at + i) = v[i];
+                of[i] = splat(0.0f);
+            }
+            if (last)
+                rows::give_sums<MODE, E>(p + row * c.cols, pl, v);
+        };
+        join(S, 0, 2);
+        if (FULL)
+            join(T, P, 3);
+        begun = true;
     };
     // statistics of the row in phase two, of the one in phase one, and of the one after
     // that, which are on their way
@@ -711,14 +740,10 @@ bwd_kernel(const Call c, const Chunks ch, const TA *__restrict__ dy, const TR *_
     Stats now, soon = stats_of(first), later = stats_of(first + kStep);
     rows::Cursor cur = slots.first(), ahead = cur;
     int sa = 0, sr = 0, next_sa = 0, next_sr = 0;
-    // A row's two sums depend on one another.  One block to a row takes them in turn, a
-    // barrier each, with what phase one has formed in registers.  In a cluster, where an
-    // exchange takes longer, each carries the second sum of a row and the first one of the
-    // next, and phase two forms phase one's values again from the slot: 8192 columns,
-    // layer norm, 1999 rows 80 us against 95, where 8192 x 4096 in one block takes 84
-    // us so, and 80 with two barriers.
-    constexpr bool kTwo = MODE == rows::kFull || THREADS > kThreads;
-    [[maybe_unused]] float2 kept_h[P], kept_e[P];
+    // A row's two sums depend on one another.  An exchange carries the second sum of a row
+    // and the first one of the next; phase two forms phase one's values again from the slot.
+    // With an exchange for each and the values kept, 8192 x 5120 layer norm took 141 us
+    // against 130, 8192 x 4096 109 against 103, 1999 x 8192 over clusters 95 against 80.
     // Phase one of a row: the sums that D needs, and the gradients of w2 and b2.
     auto one = [&](int64_t row, const Stats &v) {
         slots.wait(ahead, limit_ns, status);
@@ -740,10 +765,6 @@ bwd_kernel(const Call c, const Chunks ch, const TA *__restrict__ dy, const TR *_
             t1 = __ffma2_rn(h[i], e[i], t1);
             if (FULL)
                 t2 = __fadd2_rn(t2, h[i]);
-            if (kTwo) {
-                kept_h[i] = h[i];
-                kept_e[i] = e[i];
-            }
         }
         slots.step(ahead);
         return make_float2(t1.x + t1.y, t2.x + t2.y);
@@ -753,34 +774,31 @@ bwd_kernel(const Call c, const Chunks ch, const TA *__restrict__ dy, const TR *_
         k1 = -v.s2 * (x * inv_c);
         k2 = layer ? -v.s2 * (y * inv_c) : 0.0f;
     };
-    if (!kTwo && first < stop) {
-        const float2 t = one(first, soon), k = sum(t.x, t.y);
+    if (first < stop) {
+        const float2 t = one(first, soon), k = FULL ? sum(t.x, t.y) : make_float2(sum(t.x), 0.0f);
         means(k.x, k.y, soon);
     }
     int64_t at = slots.begin(first);
     for (int64_t row = first; row < stop; row += kStep, at += kStep * c.cols) {
         if (row >= gate_end) {
-            if (row > first)
-                flush();
             gate = ch.gate(row);
             gate_end = min(stop, ch.gate_stop(gate));
+            Param<E, false> g;
+            rows::take_param<MODE>(c.w_post, c.w_f32, 0, pl, 1.0f, gw);
             rows::take_param<MODE>(c.gate, c.g_f32, gate * c.cols, pl, 1.0f, g);
+#pragma unroll
+            for (int i = 0; i < P; ++i)
+                gw.set(i, __fmul2_rn(gw.pair(i), g.pair(i)));
         }
         now = soon;
         soon = later;
         later = stats_of(row + 2 * kStep);
-        if (kTwo) {
-            const float2 t = one(row, now), k = sum(t.x, t.y);
-            means(k.x, k.y, now);
-        }
         sa = next_sa;
         sr = next_sr;
         // h becomes D
         float2 h[P], e[P], o[P];
-        if (!kTwo) {
-            rows::take<MODE, E, TA>(slots.at_a(cur, 0), sa, pl, h);
-            rows::take<MODE, E, TR>(slots.at_r(cur, 1), sr, pl, e);
-        }
+        rows::take<MODE, E, TA>(slots.at_a(cur, 0), sa, pl, h);
+        rows::take<MODE, E, TR>(slots.at_r(cur, 1), sr, pl, e);
         if (dr_out != nullptr) {
             rows::take<MODE, E, TR>(slots.at_r(cur, 0), sr, pl, o);
         } else {
@@ -788,16 +806,12 @@ bwd_kernel(const Call c, const Chunks ch, const TA *__restrict__ dy, const TR *_
             for (int i = 0; i < P; ++i)
                 o[i] = splat(0.0f);
         }
-        [[maybe_unused]] const float s2k1 = now.s2 * k1;
+        const float s2k1 = now.s2 * k1;
 #pragma unroll
         for (int i = 0; i < P; ++i) {
-            if (kTwo) {
-                h[i] = __fadd2_rn(o[i], __ffma2_rn(kept_h[i], splat(now.s2), __ffma2_rn(kept_e[i], splat(k1), splat(k2))));
-            } else {
-                e[i] = __fadd2_rn(e[i], splat(-now.mu2));
-                h[i] = __fmul2_rn(h[i], w2.pair(i));
-                h[i] = __fadd2_rn(o[i], __ffma2_rn(h[i], splat(now.s2), __ffma2_rn(e[i], splat(s2k1), splat(k2))));
-            }
+            e[i] = __fadd2_rn(e[i], splat(-now.mu2));
+            h[i] = __fmul2_rn(h[i], w2.pair(i));
+            h[i] = __fadd2_rn(o[i], __ffma2_rn(h[i], splat(now.s2), __ffma2_rn(e[i], splat(s2k1), splat(k2))));
         }
         rows::take<MODE, E, TA>(slots.at_a(cur, 1), sa, pl, e);
         const bool inside = inside_of<MODE>(at, sl.n, c.rows * c.cols, status);
@@ -807,34 +821,30 @@ bwd_kernel(const Call c, const Chunks ch, const TA *__restrict__ dy, const TR *_
                 o[i] = __fmul2_rn(h[i], splat(c.scale));
             rows::give<MODE, E>(dr + at, pl, o);
         }
-        // e becomes e1 (a without the norm), h du
+        // e becomes e1 (a without the norm), h du w1
         float2 t1 = splat(0.0f), t2 = splat(0.0f);
 #pragma unroll
         for (int i = 0; i < P; ++i) {
             e[i] = __fmul2_rn(__fadd2_rn(e[i], splat(-now.mu1)), splat(now.s1));
-            float2 u = __fmul2_rn(e[i], w1.pair(i));
+            S[i] = __ffma2_rn(h[i], e[i], S[i]);
             if (FULL)
-                u = __fadd2_rn(u, b1.pair(i));
-            dg[i] = __ffma2_rn(h[i], u, dg[i]);
-            h[i] = __fmul2_rn(h[i], g.pair(i));
-            dw1[i] = __ffma2_rn(h[i], e[i], dw1[i]);
-            if (FULL)
-                db1[i] = __fadd2_rn(db1[i], h[i]);
-            h[i] = __fmul2_rn(h[i], w1.pair(i));
+                T[i] = __fadd2_rn(T[i], h[i]);
+            h[i] = __fmul2_rn(h[i], gw.pair(i));
             t1 = __ffma2_rn(h[i], e[i], t1);
             if (FULL)
                 t2 = __fadd2_rn(t2, h[i]);
         }
-        float2 k;
-        if (kTwo) {
-            k = sum(t1.x + t1.y, t2.x + t2.y);
-        } else {
-            float2 t = make_float2(0.0f, 0.0f);
-            if (row + kStep < stop)
-                t = one(row + kStep, soon);
+        float2 k, t = make_float2(0.0f, 0.0f);
+        if (row + kStep < stop)
+            t = one(row + kStep, soon);
+        if constexpr (FULL) {
             const float4 both = sum(t1.x + t1.y, t2.x + t2.y, t.x, t.y);
             k = make_float2(both.x, both.y);
             means(both.z, both.w, soon);
+        } else {
+            const float2 both = sum(t1.x + t1.y, t.x);
+            k = make_float2(both.x, 0.0f);
+            means(both.y, 0.0f, soon);
         }
         // every thread is done with the row: its slot may be filled again
         if (threadIdx.x == 0 && slots.ok && row + stages * kStep < stop)
@@ -848,46 +858,51 @@ bwd_kernel(const Call c, const Chunks ch, const TA *__restrict__ dy, const TR *_
         if (da != nullptr && inside)
             rows::give<MODE, E>(da + at, pl, h);
         slots.step(cur);
+        if (row + kStep >= gate_end)
+            close(row + kStep >= stop);
     }
-    if (gated && first < stop)
-        flush();
-    if (MODE == rows::kShift && gated && dgate != nullptr) {
-        // a unit without rows of one of them: flush left zeros
+    if (first >= stop) {
+        rows::give_sums<MODE, E>(p + 2 * c.cols, pl, S);
+        if (FULL)
+            rows::give_sums<MODE, E>(p + 3 * c.cols, pl, T);
+    }
+    if (MODE == rows::kShift && dgate != nullptr) {
+        // a unit without rows of one of them: close left zeros
         for (int to = 0; to < 2; ++to)
             if ((left & (1 << to)) == 0)
-                rows::give_sums<MODE, E>(ends + (unit * 2 + to) * c.cols, pl, dg);
+                rows::give_sums<MODE, E>(ends + (unit * 2 + to) * c.cols, pl, S);
     }
-    float *p = parts + unit * 4 * c.cols;
     rows::give_sums<MODE, E>(p, pl, dw2);
-    rows::give_sums<MODE, E>(p + 2 * c.cols, pl, dw1);
-    if (FULL) {
+    if (FULL)
         rows::give_sums<MODE, E>(p + c.cols, pl, db2);
-        rows::give_sums<MODE, E>(p + 3 * c.cols, pl, db1);
-    }
     if (threadIdx.x == 0)
         slots.drain();
     if (MODE != rows::kFull && ranks > 1)
         cluster_sync();
 }
 
-// The gradients from the partial rows, in a fixed order: 32 columns a block, 32
-// threads a column, each every 32nd row.  blockIdx.y names a parameter's gradient, or
-// from 4 on gates whose rows may lie in several chunks: gate y - 4 where there are no
-// more gates than borders between chunks, else those that reach over the borders after
-// the 32 chunks from 32 (y - 4) on.  What a chunk has whole it has written, unless its
-// rows are shared by `units` (kShift), which all leave partial rows.
+// The gradients from the partial rows, in a fixed order: 32 columns a block, a lane
+// each, and eight warps that take every eighth row.  blockIdx.y names a parameter's
+// gradient, or from 4 on gates whose rows may lie in several chunks: kEach's gate y - 4,
+// kMany's eight gates from 8 (y - 4) on, a warp each; kBorder's those that reach over the
+// borders after the eight chunks from 8 (y - 4) on.  What a chunk has whole it has written, unless
+// its rows are shared by `units` (kShift), which all leave partial rows.  Of 8192 x 4096
+// with 33 gates, blocks of 1024 threads for each gate took OLDRED us.
+constexpr int kReduceWarps = 8;
+enum GateSums { kEach, kMany, kBorder };
 struct Sums {
     void *out[4];
     void *dgate;
     const float *parts, *ends;
-    int nparts, w_f32, g_f32, by_border, units;
-    int64_t cols;
+    int nparts, w_f32, g_f32, units;
+    GateSums by;
+    int64_t cols, gates;
 };
 
-__global__ void __launch_bounds__(1024)
+__global__ void __launch_bounds__(32 * kReduceWarps)
 reduce_kernel(const __grid_constant__ Sums a, const Chunks ch, unsigned *status)
 {
-    __shared__ float acc[32][33];
+    __shared__ float acc[kReduceWarps][32];
     griddep_wait();
     griddep_launch_dependents();
     const int lane = threadIdx.x & 31, k = threadIdx.x >> 5;
@@ -903,26 +918,23 @@ reduce_kernel(const __grid_constant__ Sums a, const Chunks ch, unsigned *status)
         if (c < cols) {
             const float *p = a.parts + static_cast<int64_t>(blockIdx.y) * cols + c;
 #pragma unroll 8
-            for (int i = k; i < a.nparts; i += 32)
+            for (int i = k; i < a.nparts; i += kReduceWarps)
                 s += p[static_cast<int64_t>(i) * 4 * cols];
         }
     } else {
-        if (a.by_border) {
-            // a thread for each border: its gate reaches into few chunks
-            const int64_t y = (blockIdx.y - 4) * int64_t{32} + k;
-            if (y + 1 >= a.nparts || c >= cols)
+        const int64_t y = blockIdx.y - 4;
+        int64_t g = a.by == kEach ? y : y * kReduceWarps + k;
+        if (a.by == kBorder) {
+            // the gate over the border after chunk g, once: at the first that it reaches over
+            const int64_t border = g;
+            if (border + 1 >= a.nparts)
                 return;
-            const int64_t g = ch.gate(ch.stop(y) - 1), last = (ch.gate_stop(g) - 1) / ch.chunk;
-            if (last == y || ch.gate_first(g) / ch.chunk != y)
+            g = ch.gate(ch.stop(border) - 1);
+            if (ch.gate_first(g) / ch.chunk != border)
                 return;
-            s = a.ends[(y * 2 + ch.slot(g, y)) * cols + c];
-            for (int64_t i = y + 1; i <= last; ++i)
-                s += a.ends[i * 2 * cols + c];
-            if (in_range(g * cols + c, 1, ((ch.rows - 1) / ch.gate_rows + 1) * cols, status))
-                put_param(a.dgate, a.g_f32, g * cols + c, s);
-            return;
         }
-        const int64_t g = blockIdx.y - 4;
+        if (g >= a.gates)
+            return;
         const int64_t first = ch.gate_first(g) / ch.chunk, last = (ch.gate_stop(g) - 1) / ch.chunk;
         if (a.units == 1 && first == last)
             return;
@@ -930,24 +942,32 @@ reduce_kernel(const __grid_constant__ Sums a, const Chunks ch, unsigned *status)
         at = g * cols;
         f32 = a.g_f32;
         // the gate comes first in every chunk but the one that it begins in
+        const int64_t n = a.units, step = a.by == kEach ? kReduceWarps : 1;
         if (c < cols) {
-            const int n = a.units;
-            if (k < n)
-                s = a.ends[((first * n + k) * 2 + ch.slot(g, first)) * cols + c];
+            const float *p = a.ends + (first * n * 2 + ch.slot(g, first)) * cols + c;
 #pragma unroll 8
-            for (int64_t i = (first + 1) * n + k; i < (last + 1) * n; i += 32)
-                s += a.ends[i * 2 * cols + c];
+            for (int64_t i = a.by == kEach ? k : 0; i < n; i += step)
+                s += p[i * 2 * cols];
+            p = a.ends + (first + 1) * n * 2 * cols + c;
+#pragma unroll 8
+            for (int64_t i = a.by == kEach ? k : 0; i < (last - first) * n; i += step)
+                s += p[i * 2 * cols];
+        }
+        if (a.by != kEach) {
+            if (c < cols && in_range(at + c, 1, a.gates * cols, status))
+                put_param(out, f32, at + c, s);
+            return;
         }
     }
     acc[k][lane] = s;
     __syncthreads();
-    s = acc[lane][k];
+    if (k > 0 || c >= cols)
+        return;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-        s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
-    const int64_t col = static_cast<int64_t>(blockIdx.x) * 32 + k;
-    if (lane == 0 && col < cols && in_range(col, 1, cols, status))
-        put_param(out, f32, at + col, s);
+    for (int i = 1; i < kReduceWarps; ++i)
+        s += acc[i][lane];
+    if (in_range(at + c, 1, at + cols, status))
+        put_param(out, f32, at + c, s);
 }
 
 // ------------------------------------------------------------ launches
@@ -958,7 +978,10 @@ constexpr int64_t kRegCols = 16384;  // a cluster's registers hold no more
 // they fill.
 int64_t width_of(int64_t cols) { return cols % 8 == 0 ? cols : cols + 7; }
 bool in_registers(int64_t cols) { return width_of(cols) <= kRegCols; }
-constexpr int kRingBytes = 200 * 1024;
+// Shared memory for a block's ring, of `per_sm` on an SM: beside it lie the sums' and
+// bars' 2.7 KB, and the SM's own 1 KB.
+constexpr int kRingBytes = 224 * 1024;
+int ring_bytes(int per_sm) { return std::min(kRingBytes, (228 / per_sm - 4) * 1024); }
 
 int64_t walk_chunks(int64_t rows, int64_t cols, int sms)
 {
@@ -990,27 +1013,23 @@ Plan plan_of(int64_t cols, int e, int most = kThreads)
 
 Plan fwd_plan(int64_t cols) { return plan_of(cols, kFwdE); }
 
-// Backward, a block of 640 threads (96 registers each) takes rows of up to 5120 columns
-// with bf16 parameters, where a cluster of two would have one row in work on two SMs: 8192
-// x 5120 RMS norm 103 us against 179, layer norm 144 against 213.  Not those of odd widths
-// with the sums of means and biases, which do not fit the registers: 1999 x 5003 layer
-// norm with an fp32 stream 101 us against 93, RMS norm 68 against 76.
+// Backward, a block of 640 threads (96 registers each) takes rows of up to 5120 columns,
+// where a cluster of two would have one row in work on two SMs: 8192 x 5120 RMS norm 103
+// us against 179, layer norm 144 against 213.
 constexpr int kWideThreads = 640;
-bool wide_width(int64_t cols)
+bool wide_block(int64_t cols)
 {
     return width_of(cols) > kThreads * kBwdE && width_of(cols) <= kWideThreads * kBwdE;
 }
-bool wide_block(int64_t cols, bool full, bool bf)
-{
-    return bf && wide_width(cols) && (cols % 8 == 0 || !full);
-}
-Plan bwd_plan(int64_t cols, bool wide) { return plan_of(cols, kBwdE, wide ? kWideThreads : kThreads); }
+Plan bwd_plan(int64_t cols) { return plan_of(cols, kBwdE, wide_block(cols) ? kWideThreads : kThreads); }
 
-// Most units (blocks, or clusters) of the backward pass.
+// Most units (blocks, or clusters) of the backward pass: kShift's may be twice as many
+// as run at once, so that their chunks have at most two gates.
 int64_t bwd_units(int64_t rows, int64_t cols, int sms)
 {
-    const Plan p = bwd_plan(cols, wide_width(cols));
-    return std::max<int64_t>(8, std::min<int64_t>((rows + 7) / 8 * 8, static_cast<int64_t>(sms) * p.per_sm / p.ranks));
+    const Plan p = bwd_plan(cols);
+    const int64_t most = static_cast<int64_t>(sms) * p.per_sm / p.ranks * (cols % 8 != 0 ? 2 : 1);
+    return std::max<int64_t>(8, std::min<int64_t>((rows + 7) / 8 * 8, most));
 }
 
 size_t round256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
@@ -1067,7 +1086,7 @@ struct Shape {
 };
 
 template <auto Kernel>
-cudaError_t shape_of(const Plan &p, uint32_t slot_bytes, const DeviceInfo &dev, Shape *out)
+cudaError_t shape_of(const Plan &p, uint32_t slot_bytes, uint32_t more, const DeviceInfo &dev, Shape *out)
 {
     static std::once_flag once[64];
     static cudaError_t err[64];
@@ -1077,9 +1096,9 @@ cudaError_t shape_of(const Plan &p, uint32_t slot_bytes, const DeviceInfo &dev, 
     });
     if (err[d] != cudaSuccess)
         return err[d];
-    const int fit = kRingBytes / p.per_sm / static_cast<int>(slot_bytes);
+    const int fit = (ring_bytes(p.per_sm) - static_cast<int>(more)) / static_cast<int>(slot_bytes);
     out->stages = std::max(2, std::min(fit, rows::kMaxStages));
-    out->smem = static_cast<size_t>(out->stages) * slot_bytes;
+    out->smem = static_cast<size_t>(out->stages) * slot_bytes + more;
     int64_t units = static_cast<int64_t>(dev.sm_count) * p.per_sm / p.ranks;
     if (p.ranks > 2) {
         // clusters of more than a pair may leave SMs of a group over
@@ -1130,7 +1149,7 @@ cudaError_t fwd_rows(const Call &c, const void *a, const void *r, void *r_out, v
     const Plan p = fwd_plan(c.cols);
     Shape s;
     const cudaError_t e = shape_of<fwd_kernel<TA, TR, MODE, BF>>(
-        p, rows::slice_pitch<TA>(p.slice) + rows::slice_pitch<TR>(p.slice), dev, &s);
+        p, rows::slice_pitch<TA>(p.slice) + rows::slice_pitch<TR>(p.slice), 0, dev, &s);
     if (e != cudaSuccess)
         return e;
     int64_t chunk;
@@ -1159,25 +1178,30 @@ cudaError_t fwd(const Call &c, const void *a, const void *r, void *r_out, void *
                       static_cast<TR *>(r_out), static_cast<TA *>(y), amax, dev.status);
 }
 
-template <typename TA, typename TR, int MODE, bool FULL, bool BF, int THREADS>
+template <typename TA, typename TR, int MODE, bool FULL, int THREADS>
 cudaError_t bwd_rows(const Call &c, Chunks &ch, int *shared, const void *dy, const void *dr_out, const void *a,
                      const void *r_out, const f8_residual_norm_grads &g, float *parts, float *ends,
                      const DeviceInfo &dev, cudaStream_t st)
 {
-    const Plan p = bwd_plan(c.cols, THREADS == kWideThreads);
+    const Plan p = bwd_plan(c.cols);
+    // dw1's and db1's sums over a unit's gates
+    const uint32_t acc = c.gate != nullptr && c.gate_rows < c.rows ? p.threads * kBwdE * (FULL ? 8u : 4u) : 0u;
     Shape s;
-    const cudaError_t e = shape_of<bwd_kernel<TA, TR, MODE, FULL, BF, THREADS>>(
-        p, 2 * (rows::slice_pitch<TA>(p.slice) + rows::slice_pitch<TR>(p.slice)), dev, &s);
+    const cudaError_t e = shape_of<bwd_kernel<TA, TR, MODE, FULL, THREADS>>(
+        p, 2 * (rows::slice_pitch<TA>(p.slice) + rows::slice_pitch<TR>(p.slice)), acc, dev, &s);
     if (e != cudaSuccess)
         return e;
-    const int64_t units = chunk_rows<MODE>(c.rows, s.most, &ch.chunk);
+    int64_t units = chunk_rows<MODE>(c.rows, s.most, &ch.chunk);
     *shared = MODE == rows::kShift ? 8 : 1;
     // kShift's units have room for two gates of their chunk
     if constexpr (MODE == rows::kShift)
         if (c.gate != nullptr && c.gate_rows < ch.chunk)
-            return bwd_rows<TA, TR, rows::kRagged, FULL, BF, THREADS>(c, ch, shared, dy, dr_out, a, r_out, g, parts, ends,
-                                                             dev, st);
-    return launch_pdl_cluster(bwd_kernel<TA, TR, MODE, FULL, BF, THREADS>, dim3(static_cast<unsigned>(units * p.ranks)),
+            units = chunk_rows<MODE>(c.rows, 2 * s.most, &ch.chunk);
+    if constexpr (MODE == rows::kShift)
+        if (c.gate != nullptr && c.gate_rows < ch.chunk)
+            return bwd_rows<TA, TR, rows::kRagged, FULL, THREADS>(c, ch, shared, dy, dr_out, a, r_out, g, parts,
+                                                                  ends, dev, st);
+    return launch_pdl_cluster(bwd_kernel<TA, TR, MODE, FULL, THREADS>, dim3(static_cast<unsigned>(units * p.ranks)),
                               dim3(static_cast<unsigned>(p.threads)), s.smem, st,
                               static_cast<unsigned>(p.ranks), c, ch, static_cast<const TA *>(dy),
                               static_cast<const TR *>(dr_out), static_cast<const TA *>(a),
@@ -1201,23 +1225,19 @@ cudaError_t bwd(const Call &c, const void *dy, const void *dr_out, const void *a
     cudaError_t e;
     if (in_registers(c.cols)) {
         const bool full = c.layer || c.b_post != nullptr || g.db_pre != nullptr || g.db_post != nullptr;
-        auto run = [&](auto mode, auto all, auto bf, auto threads) {
-            return bwd_rows<TA, TR, mode.value, all.value, bf.value, threads.value>(c, ch, &shared, dy, dr_out, a,
-                                                                                   r_out, g, parts, ends, dev, st);
+        const Plan p = bwd_plan(c.cols);
+        auto run = [&](auto all, auto threads) {
+            return by_mode(c.cols, p, kBwdE, true, [&](auto mode) {
+                return bwd_rows<TA, TR, mode.value, all.value, threads.value>(c, ch, &shared, dy, dr_out, a, r_out,
+                                                                              g, parts, ends, dev, st);
+            });
         };
         constexpr std::integral_constant<int, kThreads> usual;
-        constexpr std::integral_constant<int, kWideThreads> more;
-        const bool bf = params_bf16(c), wide = wide_block(c.cols, full, bf);
-        const Plan p = bwd_plan(c.cols, wide);
-        auto modes = [&](auto all, auto bf16, auto threads) {
-            return by_mode(c.cols, p, kBwdE, true, [&](auto m) { return run(m, all, bf16, threads); });
-        };
-        if (wide)
-            e = full ? modes(yes, yes, more) : modes(no, yes, more);
-        else if (bf)
-            e = full ? modes(yes, yes, usual) : modes(no, yes, usual);
+        constexpr std::integral_constant<int, kWideThreads> wide;
+        if (wide_block(c.cols))
+            e = full ? run(yes, wide) : run(no, wide);
         else
-            e = full ? modes(yes, no, usual) : modes(no, no, usual);
+            e = full ? run(yes, usual) : run(no, usual);
     } else {
         float *consts = reinterpret_cast<float *>(ws + w.consts);
         const auto *dy_ = static_cast<const TA *>(dy), *a_ = static_cast<const TA *>(a);
@@ -1251,12 +1271,17 @@ cudaError_t bwd(const Call &c, const void *dy, const void *dr_out, const void *a
     out.w_f32 = c.w_f32;
     out.g_f32 = c.g_f32;
     out.units = shared;
-    out.by_border = shared == 1 && gates > n - 1;
     out.cols = c.cols;
-    const int64_t across = g.dgate == nullptr ? 0 : out.by_border ? (n + 30) / 32 : gates;
+    out.gates = gates;
+    // gates of few partial rows (kMany up to 16: 33 gates of 6 REDA us, kEach REDB)
+    const bool few = (ch.gate_rows / ch.chunk + 2) * shared <= 2 * kReduceWarps;
+    out.by = shared == 1 && gates > n - 1 ? kBorder : few ? kMany : kEach;
+    const int64_t across = g.dgate == nullptr ? 0
+                           : out.by == kEach  ? gates
+                                              : ((out.by == kMany ? gates : n) + kReduceWarps - 1) / kReduceWarps;
     return launch_pdl(reduce_kernel,
                       dim3(static_cast<unsigned>((c.cols + 31) / 32), static_cast<unsigned>(4 + across)),
-                      dim3(1024), 0, st, out, ch, dev.status);
+                      dim3(32 * kReduceWarps), 0, st, out, ch, dev.status);
 }
 
 bool type_ok(f8_dtype t) { return t == F8_BF16 || t == F8_F32; }

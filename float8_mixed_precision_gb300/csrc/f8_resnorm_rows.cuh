@@ -390,81 +390,74 @@ struct Param {
     float2 f[E / 2];
     __device__ __forceinline__ float2 pair(int i) const { return f[i]; }
     __device__ __forceinline__ void set(int i, float2 v) { f[i] = v; }
+    __device__ __forceinline__ void word(int i, uint32_t bf) { f[i] = bf2(bf); }
 };
 template <int E>
 struct Param<E, true> {
     uint32_t w[E / 2];
     __device__ __forceinline__ float2 pair(int i) const { return bf2(w[i]); }
     __device__ __forceinline__ void set(int i, float2 v) { w[i] = pack2(v); }
+    __device__ __forceinline__ void word(int i, uint32_t bf) { w[i] = bf; }
 };
 
-// The slice of a row of parameters in global memory that begins at element `row`, bf16
-// or fp32 (BF: bf16); 0 past the slice, `none` throughout where there is no parameter.
+// The slice of a row of parameters in global memory that begins at element `row`, of
+// type T; 0 past the slice.
+template <int MODE, int E, typename T, typename P>
+__device__ __forceinline__ void take_typed(const T *p, int64_t row, const Place<MODE, E> &pl, P &out)
+{
+    const int64_t at = row + pl.first;
+    if constexpr (MODE == kFull || MODE == kVec) {
+#pragma unroll
+        for (int u = 0; u < E / 8; ++u) {
+            const int c = vec_col(u);
+            if (!vec_in<MODE>(c, pl.n))
+                continue;
+            const uint4 *q = reinterpret_cast<const uint4 *>(p + at + c);
+            const uint4 v = __ldg(q);
+            if constexpr (sizeof(T) == 4) {
+                const uint4 w = __ldg(q + 1);
+                out.set(4 * u, make_float2(__uint_as_float(v.x), __uint_as_float(v.y)));
+                out.set(4 * u + 1, make_float2(__uint_as_float(v.z), __uint_as_float(v.w)));
+                out.set(4 * u + 2, make_float2(__uint_as_float(w.x), __uint_as_float(w.y)));
+                out.set(4 * u + 3, make_float2(__uint_as_float(w.z), __uint_as_float(w.w)));
+            } else {
+                out.word(4 * u, v.x), out.word(4 * u + 1, v.y);
+                out.word(4 * u + 2, v.z), out.word(4 * u + 3, v.w);
+            }
+        }
+    } else {
+        // all loads on their way before the first is used
+        T v[E];
+#pragma unroll
+        for (int j = 0; j < E; ++j) {
+            v[j] = T(0.0f);
+            if constexpr (MODE == kShift) {
+                if (pl.has(j / 8, j & 7))
+                    v[j] = __ldg(p + at + vec_col(j / 8) - pl.s + (j & 7));
+            } else {
+                if (elem_col(j) < pl.n)
+                    v[j] = __ldg(p + at + elem_col(j));
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < E / 2; ++i)
+            out.set(i, make_float2(static_cast<float>(v[2 * i]), static_cast<float>(v[2 * i + 1])));
+    }
+}
+// The same of bf16 or fp32 (BF: bf16); `none` throughout where there is no parameter.
 template <int MODE, int E, bool BF>
 __device__ __forceinline__ void take_param(const void *p, int f32, int64_t row, const Place<MODE, E> &pl,
                                            float none, Param<E, BF> &out)
 {
-    const int n = pl.n;
-    const int64_t at = row + pl.first;
 #pragma unroll
     for (int i = 0; i < E / 2; ++i)
         out.set(i, p == nullptr ? make_float2(none, none) : make_float2(0.0f, 0.0f));
     if (p == nullptr)
         return;
-    if constexpr (MODE == kShift) {
-#pragma unroll
-        for (int u = 0; u < E / 8; ++u) {
-            const int64_t c = at + vec_col(u) - pl.s;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                float v[2] = {0.0f, 0.0f};
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const int e = 2 * i + k;
-                    if (pl.has(u, e))
-                        v[k] = !BF && f32 ? __ldg(static_cast<const float *>(p) + c + e)
-                                          : __bfloat162float(static_cast<const __nv_bfloat16 *>(p)[c + e]);
-                }
-                out.set(4 * u + i, make_float2(v[0], v[1]));
-            }
-        }
-    } else if constexpr (MODE != kRagged) {
-#pragma unroll
-        for (int u = 0; u < E / 8; ++u) {
-            const int c = vec_col(u);
-            if (!vec_in<MODE>(c, n))
-                continue;
-            if (!BF && f32) {
-                const float4 *q = reinterpret_cast<const float4 *>(static_cast<const float *>(p) + at + c);
-                const float4 v = __ldg(q), w = __ldg(q + 1);
-                out.set(4 * u, make_float2(v.x, v.y)), out.set(4 * u + 1, make_float2(v.z, v.w));
-                out.set(4 * u + 2, make_float2(w.x, w.y)), out.set(4 * u + 3, make_float2(w.z, w.w));
-            } else {
-                const uint4 v = __ldg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p) + at + c));
-                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if constexpr (BF)
-                        out.w[4 * u + i] = w[i];
-                    else
-                        out.f[4 * u + i] = bf2(w[i]);
-                }
-            }
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < E / 2; ++i) {
-            float v[2] = {0.0f, 0.0f};
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const int c = elem_col(2 * i + k);
-                if (c < n)
-                    v[k] = !BF && f32 ? __ldg(static_cast<const float *>(p) + at + c)
-                                      : __bfloat162float(static_cast<const __nv_bfloat16 *>(p)[at + c]);
-            }
-            out.set(i, make_float2(v[0], v[1]));
-        }
-    }
+    if (!BF && f32)
+        take_typed<MODE, E>(static_cast<const float *>(p), row, pl, out);
+    else
+        take_typed<MODE, E>(static_cast<const __nv_bfloat16 *>(p), row, pl, out);
 }
 
 // One value to `p`, rounded to T.
