@@ -23,8 +23,8 @@
 //
 // Measured, bf16, gates of 1024 rows: 8192 x 4096 layer norm forward 58 us, 4.6 TB/s;
 // RMS norm backward with every gradient 82 us, 4.9 TB/s; a plain copy runs at 6.8.  1999 x
-// 5003 with an fp32 stream and layer norms, backward, 97 us of 26.5 for the bytes: a row
-// takes a cluster, with one row in work and an exchange of 1 us.
+// 5003 with an fp32 stream and layer norms, backward, 87 us of 26.5 for the bytes: one
+// row is in work an SM, an odd width's on every eighth row.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -618,7 +618,7 @@ cols_walk_kernel(const Call c, const Chunks ch, const TA *__restrict__ dy, const
 // Of a gate's rows only S = sum D e1 and T = sum D are kept: they give dgate = w1 S + b1 T,
 // and g S and g T for dw1 and db1, whose sums over several gates lie in shared memory.
 // With u formed for each row and its three sums, five parameters' columns and five sums
-// a thread, 8192 x 4096 RMS norm took OLDSUM us and 1999 x 5003 layer norm 97.
+// a thread, 8192 x 4999 layer norm took 214 us against 195.
 template <typename TA, typename TR, int MODE, bool FULL, int THREADS>
 __global__ void __launch_bounds__(THREADS, 1)
 bwd_kernel(const Call c, const Chunks ch, const TA *__restrict__ dy, const TR *__restrict__ dr_out,
@@ -882,13 +882,14 @@ bwd_kernel(const Call c, const Chunks ch, const TA *__restrict__ dy, const TR *_
 }
 
 // The gradients from the partial rows, in a fixed order: 32 columns a block, a lane
-// each, and eight warps that take every eighth row.  blockIdx.y names a parameter's
+// each, and W warps that take every W-th row.  blockIdx.y names a parameter's
 // gradient, or from 4 on gates whose rows may lie in several chunks: kEach's gate y - 4,
-// kMany's eight gates from 8 (y - 4) on, a warp each; kBorder's those that reach over the
-// borders after the eight chunks from 8 (y - 4) on.  What a chunk has whole it has written, unless
-// its rows are shared by `units` (kShift), which all leave partial rows.  Of 8192 x 4096
-// with 33 gates, blocks of 1024 threads for each gate took OLDRED us.
-constexpr int kReduceWarps = 8;
+// kMany's W gates from W (y - 4) on, a warp each; kBorder's those that reach over the
+// borders after the W chunks from W (y - 4) on.  What a chunk has whole it has written, unless
+// its rows are shared by `units` (kShift), which all leave partial rows.  W is 8, or
+// 32 where the parameters' blocks would not fill the GPU: 8192 x 4096 with 33 gates 105 us
+// in all against 134, 16384 x 512 RMS norm with one gate 33.5 us against 37.5.
+constexpr int kReduceWarps = 8, kReduceMost = 32;
 enum GateSums { kEach, kMany, kBorder };
 struct Sums {
     void *out[4];
@@ -899,13 +900,13 @@ struct Sums {
     int64_t cols, gates;
 };
 
-__global__ void __launch_bounds__(32 * kReduceWarps)
+__global__ void __launch_bounds__(32 * kReduceMost)
 reduce_kernel(const __grid_constant__ Sums a, const Chunks ch, unsigned *status)
 {
-    __shared__ float acc[kReduceWarps][32];
+    __shared__ float acc[kReduceMost][32];
     griddep_wait();
     griddep_launch_dependents();
-    const int lane = threadIdx.x & 31, k = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31, k = threadIdx.x >> 5, W = blockDim.x >> 5;
     const int64_t cols = a.cols, c = static_cast<int64_t>(blockIdx.x) * 32 + lane;
     void *out;
     int64_t at = 0;
@@ -918,12 +919,12 @@ reduce_kernel(const __grid_constant__ Sums a, const Chunks ch, unsigned *status)
         if (c < cols) {
             const float *p = a.parts + static_cast<int64_t>(blockIdx.y) * cols + c;
 #pragma unroll 8
-            for (int i = k; i < a.nparts; i += kReduceWarps)
+            for (int i = k; i < a.nparts; i += W)
                 s += p[static_cast<int64_t>(i) * 4 * cols];
         }
     } else {
         const int64_t y = blockIdx.y - 4;
-        int64_t g = a.by == kEach ? y : y * kReduceWarps + k;
+        int64_t g = a.by == kEach ? y : y * W + k;
         if (a.by == kBorder) {
             // the gate over the border after chunk g, once: at the first that it reaches over
             const int64_t border = g;
@@ -942,7 +943,7 @@ reduce_kernel(const __grid_constant__ Sums a, const Chunks ch, unsigned *status)
         at = g * cols;
         f32 = a.g_f32;
         // the gate comes first in every chunk but the one that it begins in
-        const int64_t n = a.units, step = a.by == kEach ? kReduceWarps : 1;
+        const int64_t n = a.units, step = a.by == kEach ? W : 1;
         if (c < cols) {
             const float *p = a.ends + (first * n * 2 + ch.slot(g, first)) * cols + c;
 #pragma unroll 8
@@ -963,8 +964,8 @@ reduce_kernel(const __grid_constant__ Sums a, const Chunks ch, unsigned *status)
     __syncthreads();
     if (k > 0 || c >= cols)
         return;
-#pragma unroll
-    for (int i = 1; i < kReduceWarps; ++i)
+#pragma unroll 4
+    for (int i = 1; i < W; ++i)
         s += acc[i][lane];
     if (in_range(at + c, 1, at + cols, status))
         put_param(out, f32, at + c, s);
@@ -1007,7 +1008,7 @@ Plan plan_of(int64_t cols, int e, int most = kThreads)
     const int64_t width = width_of(cols);
     p.slice = static_cast<int>((width + 8 * p.ranks - 1) / (8 * p.ranks)) * 8;
     p.threads = (p.slice + 32 * e - 1) / (32 * e) * 32;
-    p.per_sm = std::max(1, std::min(16, kThreads / p.threads));
+    p.per_sm = std::max(1, std::min(16, most / p.threads));
     return p;
 }
 
@@ -1028,13 +1029,17 @@ Plan fwd_plan(int64_t cols)
     return p;
 }
 
-// Backward, a block of 640 threads (96 registers each) takes rows of up to 5120 columns,
-// where a cluster of two would have one row in work on two SMs: 8192 x 5120 RMS norm 103
-// us against 179, layer norm 144 against 213.
+// Backward, 640 threads of 96 registers an SM where 512 of 128 would hold one block
+// little over half of them, or a row take a cluster: 8192 x 2560 layer norm 74 us against
+// 93, 8192 x 2047 97 against 117, 8192 x 5120 130 against 213.  Elsewhere the registers
+// are worth more: 8192 x 4096 103 us against 111, 8192 x 2048 62 against 68, 8192 x 1536
+// (three blocks instead of two) 56 against 56.
 constexpr int kWideThreads = 640;
 bool wide_block(int64_t cols)
 {
-    return width_of(cols) > kThreads * kBwdE && width_of(cols) <= kWideThreads * kBwdE;
+    const int64_t threads = (width_of(cols) + kBwdE - 1) / kBwdE;
+    return (threads > kThreads / 2 && threads <= kWideThreads / 2) ||
+           (threads > kThreads && threads <= kWideThreads);
 }
 Plan bwd_plan(int64_t cols) { return plan_of(cols, kBwdE, wide_block(cols) ? kWideThreads : kThreads); }
 
@@ -1294,15 +1299,13 @@ cudaError_t bwd(const Call &c, const void *dy, const void *dr_out, const void *a
     out.units = shared;
     out.cols = c.cols;
     out.gates = gates;
-    // gates of few partial rows (kMany up to 16: 33 gates of 6 REDA us, kEach REDB)
-    const bool few = (ch.gate_rows / ch.chunk + 2) * shared <= 2 * kReduceWarps;
+    const unsigned across = static_cast<unsigned>((c.cols + 31) / 32);
+    const int W = across * 4 < 2u * dev.sm_count ? kReduceMost : kReduceWarps;
+    const bool few = (ch.gate_rows / ch.chunk + 2) * shared <= 2 * W;  // partial rows of a gate
     out.by = shared == 1 && gates > n - 1 ? kBorder : few ? kMany : kEach;
-    const int64_t across = g.dgate == nullptr ? 0
-                           : out.by == kEach  ? gates
-                                              : ((out.by == kMany ? gates : n) + kReduceWarps - 1) / kReduceWarps;
-    return launch_pdl(reduce_kernel,
-                      dim3(static_cast<unsigned>((c.cols + 31) / 32), static_cast<unsigned>(4 + across)),
-                      dim3(32 * kReduceWarps), 0, st, out, ch, dev.status);
+    const int64_t down = g.dgate == nullptr ? 0 : out.by == kEach ? gates : ((out.by == kMany ? gates : n) + W - 1) / W;
+    return launch_pdl(reduce_kernel, dim3(across, static_cast<unsigned>(4 + down)), dim3(32 * W), 0, st, out, ch,
+                      dev.status);
 }
 
 bool type_ok(f8_dtype t) { return t == F8_BF16 || t == F8_F32; }
