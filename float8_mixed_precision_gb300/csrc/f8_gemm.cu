@@ -373,10 +373,21 @@ __device__ __forceinline__ void out_row(const uint32_t (&r)[kEpiCols], uint8_t *
 
 // A box of 32 rows x 64 columns between a staging buffer and a row-major tensor
 // whose rows no TMA store takes: a row at a time, two columns a lane, the loads of
-// 16 rows under way together.
+// 16 rows under way together.  Boxes within the tensor move words where a row starts at
+// an even element (every row, or of an odd width every second one: 2k + odd) and need
+// no bounds; what counts is the instructions of two warps a scheduler.  1000 x 5003 x
+// 2064 with a residual, GELU and z 30.5 us, 34 with bounds and single elements throughout;
+// in the tensor's 16-byte vectors, shifted on the way, 36.
 __device__ __forceinline__ uint32_t *box_word(uint8_t *b, int row, int lane)
 {
     return reinterpret_cast<uint32_t *>(b + row * 128 + (((lane >> 2) ^ (row & 7)) << 4) + ((lane & 3) << 2));
+}
+
+__device__ __forceinline__ bool box_inside(int row0, int col0, int M, int N, unsigned *status)
+{
+    return row0 + 32 <= M && col0 + kEpiCols <= N &&
+           in_range(static_cast<int64_t>(row0) * N + col0, static_cast<int64_t>(31) * N + kEpiCols,
+                    static_cast<int64_t>(M) * N, status);
 }
 
 __device__ __forceinline__ void load_box(uint8_t *b, const __nv_bfloat16 *t, int row0, int col0, int M,
@@ -384,6 +395,41 @@ __device__ __forceinline__ void load_box(uint8_t *b, const __nv_bfloat16 *t, int
 {
     const uint16_t *p = reinterpret_cast<const uint16_t *>(t);
     const int64_t mn = static_cast<int64_t>(M) * N;
+    if (box_inside(row0, col0, M, N, status)) {
+        const int64_t o = static_cast<int64_t>(row0) * N + col0;
+        const int odd = static_cast<int>(o & 1);
+        const uint16_t *q = p + o + 2 * lane;
+        if (N % 2 == 0) {
+#pragma unroll 1
+            for (int h = 0; h < 32; h += 16, q += 16 * static_cast<int64_t>(N)) {
+                uint32_t w[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    w[i] = *reinterpret_cast<const uint32_t *>(q + static_cast<int64_t>(i) * N);
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    *box_word(b, h + i, lane) = w[i];
+            }
+            return;
+        }
+        const uint16_t *e = q + odd * static_cast<int64_t>(N), *u = q + (1 - odd) * static_cast<int64_t>(N);
+#pragma unroll 1
+        for (int h = 0; h < 32; h += 16, e += 16 * static_cast<int64_t>(N), u += 16 * static_cast<int64_t>(N)) {
+            uint32_t w[8], lo[8], hi[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                w[i] = *reinterpret_cast<const uint32_t *>(e + static_cast<int64_t>(2 * i) * N);
+                lo[i] = u[static_cast<int64_t>(2 * i) * N];
+                hi[i] = u[static_cast<int64_t>(2 * i) * N + 1];
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                *box_word(b, h + 2 * i + odd, lane) = w[i];
+                *box_word(b, h + 2 * i + 1 - odd, lane) = lo[i] | hi[i] << 16;
+            }
+        }
+        return;
+    }
     const int c = col0 + 2 * lane;
     // places outside the tensor read its last row or column instead: no branch keeps
     // the loads from being issued together
@@ -408,6 +454,26 @@ __device__ __forceinline__ void store_box(uint8_t *b, __nv_bfloat16 *t, int row0
 {
     uint16_t *p = reinterpret_cast<uint16_t *>(t);
     const int64_t mn = static_cast<int64_t>(M) * N;
+    if (box_inside(row0, col0, M, N, status)) {
+        const int64_t o = static_cast<int64_t>(row0) * N + col0;
+        const int odd = static_cast<int>(o & 1);
+        uint16_t *q = p + o + 2 * lane;
+        if (N % 2 == 0) {
+#pragma unroll 8
+            for (int i = 0; i < 32; ++i, q += N)
+                *reinterpret_cast<uint32_t *>(q) = *box_word(b, i, lane);
+            return;
+        }
+        uint16_t *e = q + odd * static_cast<int64_t>(N), *u = q + (1 - odd) * static_cast<int64_t>(N);
+#pragma unroll 4
+        for (int i = 0; i < 32; i += 2, e += 2 * static_cast<int64_t>(N), u += 2 * static_cast<int64_t>(N)) {
+            const uint32_t w = *box_word(b, i + 1 - odd, lane);
+            *reinterpret_cast<uint32_t *>(e) = *box_word(b, i + odd, lane);
+            u[0] = static_cast<uint16_t>(w);
+            u[1] = static_cast<uint16_t>(w >> 16);
+        }
+        return;
+    }
     const int c = col0 + 2 * lane;
 #pragma unroll 8
     for (int i = 0; i < 32; ++i) {
@@ -433,7 +499,7 @@ __device__ __forceinline__ void fetch_residual(const EpiParams<kEpiAct> &ep, uin
 // The Act epilogue of one warp over COLS columns from col_base.  With stores by TMA the
 // two buffers are y's in turn, or y's and z's where z is kept.  A residual comes by TMA
 // into y's buffer while z and the activation are formed; `fetched` says that the
-// caller has asked for the first step's box, `phase` is the parity of the next one.
+// caller has asked for the first step's box (without TMA, has it there), `phase` is the parity of the next one.
 // False if a wait gave up.
 template <int COLS>
 __device__ __forceinline__ bool epilogue_rows_act(uint32_t taddr, int row0, int col_base, int M, int N,
@@ -466,7 +532,7 @@ __device__ __forceinline__ bool epilogue_rows_act(uint32_t taddr, int row0, int 
                 if (res && !(fetched && j == 0))
                     fetch_residual(ep, b, bar, col0, row0);
             }
-        } else if (res) {
+        } else if (res && !(fetched && j == 0)) {
             load_box(b, ep.residual, row0, col0, M, N, lane, status);
         }
         __syncwarp();
@@ -832,8 +898,12 @@ gemm_kernel(const __grid_constant__ GemmSet<NP> set, const __grid_constant__ Epi
             if constexpr (EPI == kEpiAct) {
                 static_assert(kCols <= 128, "a lane's four biases cover the warp's columns");
                 load_bias4(ep.bias, ep.bias_f32, col_base + 4 * lane, pr.N, bias, status);
-                fetched = ep.residual != nullptr && pr.tma_store != 0 && row0 < pr.M && col_base < pr.N;
-                if (fetched && lane == 0) {
+                // the first step's residual is under way while the products are
+                fetched = ep.residual != nullptr && row0 < pr.M && col_base < pr.N;
+                if (fetched && pr.tma_store == 0) {
+                    load_box(my_stage + buf * kEpiBufBytes, ep.residual, row0, col_base, pr.M, pr.N, lane,
+                             status);
+                } else if (fetched && lane == 0) {
                     if (ep.zout != nullptr)
                         bulk_wait_group_read<0>();
                     else
@@ -846,7 +916,7 @@ gemm_kernel(const __grid_constant__ GemmSet<NP> set, const __grid_constant__ Epi
             if (!ok) {
                 if (lane == 0) {
                     note_timeout(abort_flag, status);
-                    if (fetched)
+                    if (fetched && pr.tma_store != 0)
                         mbar_wait(my_bar, phase, nullptr, kDrainLimitNs);
                 }
                 break;
@@ -1249,8 +1319,9 @@ bool few_rows(const GemmDesc &g, const DeviceInfo &dev)
 // pay where they take no more rounds of the pairs: 300 x 4096 x 4096 with bias and SiLU
 // 15.5 us against 17.3, with a residual and z kept too 17.3 against 21.2; 1000 x 4096 x
 // 4096 (two rounds against one) 25 against 18.  Where rows are stored element by
-// element, the epilogue's share makes up for half a round: 1000 x 5003 x 2064 with all
-// of it 35 against 39 (three against two).  F8_GEMM_TILE=128|256 forces one (for
+// element, the epilogue's share makes up for three quarters of a round: 1000 x 5003 x 2064
+// with all of it 30.5 against 35.4 (three against two), 3000 x 5001 x 1024 61 against 64
+// (seven against four), 8192 x 4095 x 4096 158 against 126 (14 against seven).  F8_GEMM_TILE=128|256 forces one (for
 // measurement).
 bool narrow_tiles(const GemmDesc &g, const DeviceInfo &dev)
 {
@@ -1261,7 +1332,7 @@ bool narrow_tiles(const GemmDesc &g, const DeviceInfo &dev)
     const SchedProblem p = sched_problem(g);
     const int64_t wide = (sched_tiles(p, 2 * kBM, 256) + units - 1) / units;
     const int64_t narrow = (sched_tiles(p, 2 * kBM, 128) + units - 1) / units;
-    return g.N % 8 == 0 ? narrow <= wide : narrow * 2 <= wide * 3;
+    return g.N % 8 == 0 ? narrow <= wide : narrow * 4 <= wide * 7;
 }
 
 cudaError_t launch_gemm_act(const GemmDesc &g, const ActEpilogue &e, const DeviceInfo &dev,
