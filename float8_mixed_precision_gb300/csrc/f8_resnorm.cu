@@ -667,7 +667,8 @@ bwd_kernel(const Call c, const Chunks ch, const TA *__restrict__ dy, const TR *_
     const bool post = c.w_post != nullptr, layer = FULL && c.layer;
     float2 *acc = reinterpret_cast<float2 *>(dyn + stages * slots.slot_bytes()) + threadIdx.x;
     auto acc_at = [&](int i) -> float2 & { return acc[i * blockDim.x]; };
-    float *p = parts + unit * 4 * c.cols;
+    const int64_t pitch = rows::sums_pitch(c.cols);
+    float *p = parts + unit * 4 * pitch;
     Param<E, false> w2, gw;  // gw: gate w1
     rows::take_param<MODE>(c.w_pre, c.w_f32, 0, pl, 1.0f, w2);
     float2 dw2[P], db2[P], S[P], T[P];
@@ -693,12 +694,16 @@ bwd_kernel(const Call c, const Chunks ch, const TA *__restrict__ dy, const TR *_
                 for (int i = 0; i < P; ++i)
                     v[i] = __ffma2_rn(T[i], w.pair(i), v[i]);
             }
-            if (MODE != rows::kShift && ch.whole(gate, walk.chunk)) {
-                rows::give_param<MODE, E>(dgate, c.g_f32, gate * c.cols, pl, v);
-            } else {
+            bool whole = false;
+            if constexpr (MODE != rows::kShift) {
+                whole = ch.whole(gate, walk.chunk);
+                if (whole)
+                    rows::give_param<MODE, E>(dgate, c.g_f32, gate * c.cols, pl, v);
+            }
+            if (!whole) {
                 const int to = ch.slot(gate, walk.chunk);
                 left |= 1 << to;
-                rows::give_sums<MODE, E>(ends + (unit * 2 + to) * c.cols, pl, v);
+                rows::give_sums<MODE, E>(ends + (unit * 2 + to) * pitch, pl, v);
             }
         }
         rows::take_param<MODE>(c.gate, c.g_f32, gate * c.cols, pl, 1.0f, w);
@@ -711,7 +716,7 @@ bwd_kernel(const Call c, const Chunks ch, const TA *__restrict__ dy, const TR *_
                 of[i] = splat(0.0f);
             }
             if (last)
-                rows::give_sums<MODE, E>(p + row * c.cols, pl, v);
+                rows::give_sums<MODE, E>(p + row * pitch, pl, v);
         };
         join(S, 0, 2);
         if (FULL)
@@ -862,19 +867,19 @@ bwd_kernel(const Call c, const Chunks ch, const TA *__restrict__ dy, const TR *_
             close(row + kStep >= stop);
     }
     if (first >= stop) {
-        rows::give_sums<MODE, E>(p + 2 * c.cols, pl, S);
+        rows::give_sums<MODE, E>(p + 2 * pitch, pl, S);
         if (FULL)
-            rows::give_sums<MODE, E>(p + 3 * c.cols, pl, T);
+            rows::give_sums<MODE, E>(p + 3 * pitch, pl, T);
     }
     if (MODE == rows::kShift && dgate != nullptr) {
         // a unit without rows of one of them: close left zeros
         for (int to = 0; to < 2; ++to)
             if ((left & (1 << to)) == 0)
-                rows::give_sums<MODE, E>(ends + (unit * 2 + to) * c.cols, pl, S);
+                rows::give_sums<MODE, E>(ends + (unit * 2 + to) * pitch, pl, S);
     }
     rows::give_sums<MODE, E>(p, pl, dw2);
     if (FULL)
-        rows::give_sums<MODE, E>(p + c.cols, pl, db2);
+        rows::give_sums<MODE, E>(p + pitch, pl, db2);
     if (threadIdx.x == 0)
         slots.drain();
     if (MODE != rows::kFull && ranks > 1)
@@ -886,7 +891,8 @@ bwd_kernel(const Call c, const Chunks ch, const TA *__restrict__ dy, const TR *_
 // gradient, or from 4 on gates whose rows may lie in several chunks: kEach's gate y - 4,
 // kMany's W gates from W (y - 4) on, a warp each; kBorder's those that reach over the
 // borders after the W chunks from W (y - 4) on.  What a chunk has whole it has written, unless
-// its rows are shared by `units` (kShift), which all leave partial rows.  W is 8, or
+// its rows are shared by `units` (kShift), which all leave partial rows, by position: unit
+// i's start `shift` i mod 8 floats in.  W is 8, or
 // 32 where the parameters' blocks would not fill the GPU: 8192 x 4096 with 33 gates 105 us
 // in all against 134, 16384 x 512 RMS norm with one gate 33.5 us against 37.5.
 constexpr int kReduceWarps = 8, kReduceMost = 32;
@@ -897,7 +903,8 @@ struct Sums {
     const float *parts, *ends;
     int nparts, w_f32, g_f32, units;
     GateSums by;
-    int64_t cols, gates;
+    int shift;
+    int64_t cols, pitch, gates;
 };
 
 __global__ void __launch_bounds__(32 * kReduceMost)
@@ -917,10 +924,10 @@ reduce_kernel(const __grid_constant__ Sums a, const Chunks ch, unsigned *status)
         if (out == nullptr)
             return;
         if (c < cols) {
-            const float *p = a.parts + static_cast<int64_t>(blockIdx.y) * cols + c;
+            const float *p = a.parts + static_cast<int64_t>(blockIdx.y) * a.pitch + c;
 #pragma unroll 8
             for (int i = k; i < a.nparts; i += W)
-                s += p[static_cast<int64_t>(i) * 4 * cols];
+                s += p[static_cast<int64_t>(i) * 4 * a.pitch + (i * a.shift & 7)];
         }
     } else {
         const int64_t y = blockIdx.y - 4;
@@ -945,14 +952,14 @@ reduce_kernel(const __grid_constant__ Sums a, const Chunks ch, unsigned *status)
         // the gate comes first in every chunk but the one that it begins in
         const int64_t n = a.units, step = a.by == kEach ? W : 1;
         if (c < cols) {
-            const float *p = a.ends + (first * n * 2 + ch.slot(g, first)) * cols + c;
+            const float *p = a.ends + (first * n * 2 + ch.slot(g, first)) * a.pitch + c;
 #pragma unroll 8
             for (int64_t i = a.by == kEach ? k : 0; i < n; i += step)
-                s += p[i * 2 * cols];
-            p = a.ends + (first + 1) * n * 2 * cols + c;
+                s += p[i * 2 * a.pitch + (i * a.shift & 7)];
+            p = a.ends + (first + 1) * n * 2 * a.pitch + c;
 #pragma unroll 8
             for (int64_t i = a.by == kEach ? k : 0; i < (last - first) * n; i += step)
-                s += p[i * 2 * cols];
+                s += p[i * 2 * a.pitch + (i * a.shift & 7)];
         }
         if (a.by != kEach) {
             if (c < cols && in_range(at + c, 1, a.gates * cols, status))
@@ -1064,7 +1071,7 @@ Workspace workspace_of(int64_t rows, int64_t cols, int sms)
 {
     const bool walk = !in_registers(cols);
     const size_t n = static_cast<size_t>(walk ? walk_chunks(rows, cols, sms) : bwd_units(rows, cols, sms));
-    const size_t row = static_cast<size_t>(cols) * sizeof(float);
+    const size_t row = static_cast<size_t>(rows::sums_pitch(cols)) * sizeof(float);
     Workspace w;
     w.consts = 0;
     w.parts = walk ? round256(2 * static_cast<size_t>(rows) * sizeof(float)) : 0;
@@ -1297,7 +1304,9 @@ cudaError_t bwd(const Call &c, const void *dy, const void *dr_out, const void *a
     out.w_f32 = c.w_f32;
     out.g_f32 = c.g_f32;
     out.units = shared;
+    out.shift = shared == 1 ? 0 : static_cast<int>(c.cols & 7);
     out.cols = c.cols;
+    out.pitch = in_registers(c.cols) ? rows::sums_pitch(c.cols) : c.cols;
     out.gates = gates;
     const unsigned across = static_cast<unsigned>((c.cols + 31) / 32);
     const int W = across * 4 < 2u * dev.sm_count ? kReduceMost : kReduceWarps;

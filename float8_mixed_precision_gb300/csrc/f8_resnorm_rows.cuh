@@ -475,9 +475,8 @@ __device__ __forceinline__ void give_one(T *p, float v, uint32_t *seen)
 }
 
 // The thread's columns to `p` (the slice's first element), rounded to T.  `seen`
-// gathers the largest magnitude of the stored bf16 values.  ALIGNED: p lies as the
-// tensors' rows do (else kShift's vectors go element by element).
-template <int MODE, int E, bool ALIGNED = true, typename T>
+// gathers the largest magnitude of the stored bf16 values.
+template <int MODE, int E, typename T>
 __device__ __forceinline__ void give(T *p, const Place<MODE, E> &pl, const float2 (&f)[E / 2],
                                      uint32_t *seen = nullptr)
 {
@@ -489,7 +488,7 @@ __device__ __forceinline__ void give(T *p, const Place<MODE, E> &pl, const float
             if (!vec_in<MODE>(c, n))
                 continue;
             if constexpr (MODE == kShift) {
-                if (!ALIGNED || !pl.whole(u)) {
+                if (!pl.whole(u)) {
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
                         if (pl.has(u, e))
@@ -525,27 +524,42 @@ __device__ __forceinline__ void give(T *p, const Place<MODE, E> &pl, const float
     }
 }
 
-// The thread's columns of a row of sums that begins at `row`, or of one of a gradient of
-// type `f32` (else bf16).
+// Floats from one row of sums to the next: kShift's are laid out by position, which
+// keeps its vectors whole; element by element each 32-byte piece would be written eight
+// times.
+__host__ __device__ __forceinline__ int64_t sums_pitch(int64_t cols)
+{
+    return cols % 8 == 0 ? cols : (cols + 7 + 7) / 8 * 8;
+}
+
+// The thread's columns of a row of sums that begins at `row`.
 template <int MODE, int E>
 __device__ __forceinline__ void give_sums(float *row, const Place<MODE, E> &pl, const float2 (&f)[E / 2])
 {
-    if constexpr (MODE == kShift)
-        give<MODE, E, false>(row + pl.first - pl.s, pl, f);
-    else
+    if constexpr (MODE == kShift) {
+#pragma unroll
+        for (int u = 0; u < E / 8; ++u) {
+            const int c = vec_col(u);
+            if (c < pl.n) {
+                float4 *q = reinterpret_cast<float4 *>(row + pl.first + c);
+                q[0] = make_float4(f[4 * u].x, f[4 * u].y, f[4 * u + 1].x, f[4 * u + 1].y);
+                q[1] = make_float4(f[4 * u + 2].x, f[4 * u + 2].y, f[4 * u + 3].x, f[4 * u + 3].y);
+            }
+        }
+    } else {
         give<MODE, E>(row + pl.first, pl, f);
+    }
 }
+// Or of one of a gradient of type `f32` (else bf16), not of kShift's.
 template <int MODE, int E>
 __device__ __forceinline__ void give_param(void *p, int f32, int64_t row, const Place<MODE, E> &pl,
                                            const float2 (&f)[E / 2])
 {
-    if (f32) {
-        give_sums<MODE, E>(static_cast<float *>(p) + row, pl, f);
-    } else if constexpr (MODE == kShift) {
-        give<MODE, E, false>(static_cast<__nv_bfloat16 *>(p) + row + pl.first - pl.s, pl, f);
-    } else {
+    static_assert(MODE != kShift, "these leave sums");
+    if (f32)
+        give<MODE, E>(static_cast<float *>(p) + row + pl.first, pl, f);
+    else
         give<MODE, E>(static_cast<__nv_bfloat16 *>(p) + row + pl.first, pl, f);
-    }
 }
 
 // Sums over the block, or over the cluster's blocks, in a fixed order; every thread
