@@ -22,8 +22,8 @@
 // arithmetic, some 600 instructions a warp and row forward, with two rows in work an SM.
 //
 // Measured, bf16, gates of 1024 rows: 8192 x 4096 layer norm forward 58 us, 4.6 TB/s;
-// RMS norm backward with every gradient 82 us, 4.9 TB/s; a plain copy runs at 6.8.  1999 x
-// 5003 with an fp32 stream and layer norms, backward, 87 us of 26.5 for the bytes: one
+// RMS norm backward with every gradient 79 us, 5.1 TB/s; a plain copy runs at 6.8.  1999 x
+// 5003 with an fp32 stream and layer norms, backward, 71 us of 26.5 for the bytes: one
 // row is in work an SM, an odd width's on every eighth row.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
