@@ -902,8 +902,8 @@ f8_status f8_rope_frequencies(int64_t rot, double base, f8_rope_scaling scaling,
  *           or NULL; needs x_type F8_BF16; zeroed by the call.  A non-finite y then
  *           sets F8_ERR_NONFINITE.
  * rows, cols >= 0; cols < 2^30, rows * cols < 2^60; eps >= 0; scale finite.  All
- * tensors 16-byte aligned, stats and amax_out 4-byte.  Rows of up to 16384 columns are
- * read once; the fastest widths are 512 times a power of two, forward up to 8192 and
+ * tensors 16-byte aligned, stats and amax_out 4-byte.  Rows of up to 16384 columns (odd
+ * widths: 16377) are read once; the fastest widths are 512 times a power of two, forward up to 8192 and
  * backward up to 4096.  Wider rows (backward above 5120, forward above 8192)
  * take several blocks, and those past 16384 columns are read again for each sum.  Odd
  * widths take up to twice the time of even ones, those with gates of fewer rows than a

@@ -110,6 +110,24 @@ def test_residual_in_place(f8, M, N):
     assert y is res and torch.equal(y, want)
 
 
+@pytest.mark.parametrize("M, N", [(320, 5002), (513, 1003), (300, 66), (4100, 193), (3000, 2001)])
+def test_rows_off_vectors(f8, M, N):
+    """Rows that start anywhere in 16 bytes, over several rounds of tiles: every output, what lies around it, and
+    the residual in place."""
+    _check(f8, M, N, 80, "gelu", M + N)
+    a, sa, b, sb, bias, res = _inputs(M, N, 80, 3)
+    kw = dict(bias=bias, act=f8.F8_ACT_SILU)
+    want, z = f8.f8_gemm_act(a, b, sa, sb, residual=res, want_z=True, **kw)
+    around = 64
+    flat = [torch.full((M * N + 2 * around,), 7.0, dtype=BF, device=DEV) for _ in range(2)]
+    y2, z2 = (f[around:around + M * N].view(M, N) for f in flat)
+    y2.copy_(res)
+    f8.f8_gemm_act(a, b, sa, sb, residual=y2, y=y2, z=z2, **kw)
+    assert torch.equal(y2, want) and torch.equal(z2, z)
+    for f in flat:
+        assert (f[:around] == 7.0).all() and (f[around + M * N:] == 7.0).all()
+
+
 @pytest.mark.parametrize("M, N", [(24, 264), (520, 264), (24, 65), (520, 65)])
 def test_plain_equals_f8_gemm(f8, M, N):
     a, sa, b, sb, _, _ = _inputs(M, N, 512, 19)

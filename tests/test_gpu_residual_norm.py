@@ -135,6 +135,34 @@ def test_wide_blocks(f8, cols, layer, bias):
         _check(f8, s, layer, 0.75, f"{rows}x{cols} by {gate_rows} {rt}")
 
 
+@pytest.mark.parametrize("gate_rows", [137, 100, 72, 71, 50, 8])
+@pytest.mark.parametrize("rows, cols", [(2500, 4099), (3001, 1003), (2500, 2047), (2500, 2052)])
+def test_odd_widths_many_gates(f8, rows, cols, gate_rows):
+    """Gates about as long as the rows that units share, longer and shorter; none of the partial rows lies past the
+    workspace."""
+    s = _inputs(rows, cols, BF, F32, gate_rows=gate_rows, seed=gate_rows)
+    r_out, y, stats, want = _check(f8, s, True, 0.75, f"{rows}x{cols} by {gate_rows}")
+    n = f8.f8_residual_norm_bwd_workspace_bytes(rows, cols)
+    ws = torch.full((n + 4096,), 0x5A, dtype=torch.uint8, device=DEV)
+    got = f8.f8_residual_norm_bwd(s["dy"], s["dr_out"], s["a"], r_out, s["w_pre"], stats, ws=ws[:n], want=_all(s),
+                                  **_kw(f8, s, True, 0.75))
+    assert (ws[n:] == 0x5A).all()
+    for u, v in zip(got, want):
+        assert torch.equal(u, v)
+
+
+@pytest.mark.parametrize("cols", [1000, 1003, 4099, 4104])
+def test_frozen_parts(f8, cols):
+    """Each gradient alone is the one that comes with all others."""
+    s = _inputs(300, cols, gate_rows=40)
+    kw = _kw(f8, s, True, 0.75)
+    r_out, _, stats, want = _check(f8, s, True, 0.75, f"{cols} columns")
+    for i, name in enumerate(GRADS):
+        got = f8.f8_residual_norm_bwd(s["dy"], s["dr_out"], s["a"], r_out, s["w_pre"], stats, want=(name,), **kw)
+        assert [j for j, t in enumerate(got) if t is not None] == [i]
+        assert torch.equal(got[i], want[i]), name
+
+
 def test_one_gate_for_all(f8):
     s = _inputs(40, 256, gate_rows=40)
     want = _check(f8, s, False, 1.0, "rows")
