@@ -16,7 +16,7 @@
 //
 // Both are bound by HBM: four values moved per element forward, six backward.  A row's
 // values stay in registers between the loads and the stores, 16 a thread forward and 8
-// backward (beside the column sums of five gradients), and rows come some ahead through
+// backward (beside four column sums and two parameters), and rows come some ahead through
 // shared memory by bulk copies (f8_resnorm_rows.cuh); with the rows read again for each
 // reduction 8192 x 4096 took 327 us forward and 482 backward.  What is left is the
 // arithmetic, some 600 instructions a warp and row forward, with two rows in work an SM.
