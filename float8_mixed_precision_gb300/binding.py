@@ -276,6 +276,25 @@ def _stream(stream) -> int:
     return int(stream)
 
 
+def _torch_stream(stream, device) -> torch.cuda.Stream:
+    """torch's object for a stream that a call was given."""
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    handle = int(stream)
+    # 0 and 1 name the default stream
+    return (torch.cuda.default_stream(device) if handle in (0, 1) else
+            torch.cuda.ExternalStream(handle, device=device))
+
+
+def _zero(t: torch.Tensor, stream=None) -> None:
+    """Zeros in `t`, in the order of the call's stream."""
+    if stream is None:
+        t.zero_()
+    else:
+        with torch.cuda.stream(_torch_stream(stream, t.device)):
+            t.zero_()
+
+
 def _empty(shape, dtype, device, stream=None) -> torch.Tensor:
     """A new tensor for a call on `stream`.  torch's allocator orders the uses of
     a block by the stream that was current when it was allocated: under any
@@ -289,11 +308,7 @@ def _empty(shape, dtype, device, stream=None) -> torch.Tensor:
     handle = _stream(stream)
     if handle == here.cuda_stream:
         return torch.empty(shape, dtype=dtype, device=device)
-    if not isinstance(stream, torch.cuda.Stream):
-        # 0 and 1 name the default stream
-        stream = (torch.cuda.default_stream(device) if handle in (0, 1) else
-                  torch.cuda.ExternalStream(handle, device=device))
-    with torch.cuda.stream(stream):
+    with torch.cuda.stream(_torch_stream(stream, device)):
         t = torch.empty(shape, dtype=dtype, device=device)
     t.record_stream(here)
     return t

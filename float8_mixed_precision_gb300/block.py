@@ -14,7 +14,7 @@ import struct
 import torch
 
 from . import binding, ops
-from .binding import F8_LAYER_NORM, F8_RMS_NORM, _empty
+from .binding import F8_LAYER_NORM, F8_RMS_NORM, _empty, _zero
 from .ops import _DTYPES, _call, _dtype
 
 _BF16, _F32, _U8 = torch.bfloat16, torch.float32, torch.uint8
@@ -301,4 +301,6 @@ def f8_residual_norm_bwd(dy: torch.Tensor, dr_out: torch.Tensor | None, a: torch
     _call(what, stream, n, _arg(what, "dy", dy, xt, shape, at),
           _arg(what, "dr_out", dr_out, rt, shape, at), binding._ptr(a), _arg(what, "r_out", r_out, rt, shape, at),
           _arg(what, "stats", stats, _F32, (4, shape[0]), at), grads, *space)
+    if shape[0] == 0 and dgate is not None:
+        _zero(dgate, stream)  # a sum over no rows, of as many gates as are given: the C call knows of none
     return da, dr, dw_pre, db_pre, dw_post, db_post, dgate

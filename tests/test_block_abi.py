@@ -286,3 +286,16 @@ def test_no_cpu_path(L):
         block.f8_rope(_bf(8, 4, 64), torch.zeros(8, dtype=torch.int64), torch.zeros(32, dtype=torch.float64))
     with pytest.raises(ValueError, match="device tensors"):
         block.f8_residual_norm_fwd(_bf(8, 64), _bf(8, 64), _bf(64))
+
+
+# ---------------------------------------------------------------- no rows
+def test_no_rows_one_gate(rec):
+    """The gradient of one gate for all rows is 0 where there are none, and not what memory held."""
+    none, w, st = _bf(0, 64), _bf(64), torch.zeros(4, 0)
+    dgate = torch.full((64,), 7.0, dtype=torch.bfloat16)
+    got = block.f8_residual_norm_bwd(none, None, none, none, w, st, w_post=w, gate=w, dgate=dgate)
+    assert got[6] is dgate and not dgate.any()
+    rows = _bf(4, 64)
+    dgate.fill_(7.0)  # with rows it is the C call's
+    block.f8_residual_norm_bwd(rows, None, rows, rows, w, torch.zeros(4, 4), w_post=w, gate=w, dgate=dgate)
+    assert (dgate == 7.0).all()
