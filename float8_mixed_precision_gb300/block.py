@@ -216,7 +216,9 @@ def _residual_norm(what: str, a, r, w_pre, b_pre, w_post, b_post, gate, gate_row
         if gate_rows < 1:
             raise ValueError(f"{what}: gate_rows must be at least 1")
         whole = gate.dim() == 1 and rows <= gate_rows  # one gate for all rows
-        gp, gt = _typed(what, "gate", gate, shape if whole else (-(-rows // gate_rows), cols), at)
+        # no rows are those of any number of gates
+        groups = gate.shape[0] if rows == 0 and gate.dim() == 2 else -(-rows // gate_rows)
+        gp, gt = _typed(what, "gate", gate, shape if whole else (groups, cols), at)
     try:
         types = _DTYPES[a.dtype], _DTYPES[r.dtype], _DTYPES[wt]
     except KeyError:
@@ -237,7 +239,7 @@ def f8_residual_norm_fwd(a: torch.Tensor, r: torch.Tensor, w_pre: torch.Tensor,
     a: r_out = scale r + gate norm(a; w_post, b_post) and y = norm(r_out; w_pre,
     b_pre), the next block's input.  Without w_post a is not normed.  gate [ceil(rows
     / gate_rows), cols], one row for each gate_rows rows (default: one, or [cols], for
-    all).  r may be fp32 beside a bf16 a.  stats fp32 [4, rows] is the backward's."""
+    all; any number for no rows).  r may be fp32 beside a bf16 a.  stats fp32 [4, rows] is the backward's."""
     what = "f8_residual_norm_fwd"
     n = _residual_norm(what, a, r, w_pre, b_pre, w_post, b_post, gate, gate_rows, scale, kind, eps)
     shape, at, xt, rt = a.shape, a.get_device(), a.dtype, r.dtype

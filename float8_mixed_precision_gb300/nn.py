@@ -774,9 +774,9 @@ class ResidualNorm(torch.nn.Module):
             if gate.dim() < 1 or gate.shape[-1] != self.dim:
                 raise ValueError(f"the gate must have {self.dim} features")
             groups = gate.numel() // self.dim
-            if groups < 1 or rows % groups:
+            if rows > 0 and (groups < 1 or rows % groups):
                 raise ValueError("the rows must be a multiple of the gates")
-            gate_rows = max(rows // groups, 1)
+            gate_rows = max(rows // max(groups, 1), 1)
         return _ResidualNormFn.apply(a, r, gate, self.weight, self.bias, self.post_weight, self.post_bias,
                                      gate_rows, self.scale, self.kind, self.eps)
 

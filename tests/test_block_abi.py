@@ -299,3 +299,33 @@ def test_no_rows_one_gate(rec):
     dgate.fill_(7.0)  # with rows it is the C call's
     block.f8_residual_norm_bwd(rows, None, rows, rows, w, torch.zeros(4, 4), w_post=w, gate=w, dgate=dgate)
     assert (dgate == 7.0).all()
+
+
+@pytest.mark.parametrize("gate", [(64,), (1, 64), (0, 64), (3, 64)])
+def test_no_rows_any_gates(rec, gate):
+    """A call of no rows takes gates of any number, as it takes none, and its gradients for them are 0."""
+    none, w, st, g = _bf(0, 64), _bf(64), torch.zeros(4, 0), _bf(*gate)
+    r_out, y, stats = block.f8_residual_norm_fwd(none, none, w, gate=g)
+    assert r_out.shape == y.shape == (0, 64) and stats.shape == (4, 0)
+    block.f8_residual_norm_fwd(none, none, w, gate=g, gate_rows=2)
+    got = block.f8_residual_norm_bwd(none, none, none, none, w, st, gate=g, dgate=torch.full(gate, 7.0).bfloat16())
+    assert got[6].shape == gate and not got[6].any()
+    with pytest.raises(ValueError):
+        block.f8_residual_norm_fwd(none, none, w, gate=_bf(3, 63))
+    with pytest.raises(ValueError):
+        block.f8_residual_norm_fwd(_bf(2, 64), _bf(2, 64), w, gate=_bf(0, 64), gate_rows=2)
+
+
+@pytest.mark.parametrize("lead, gate", [((0,), (64,)), ((0,), (0, 64)), ((0, 5), (64,)), ((0, 5), (0, 64)),
+                                        ((0, 5), (0, 1, 64)), ((3, 0), (3, 64)), ((3, 0), (3, 0, 64))])
+def test_no_rows_through_the_module(rec, lead, gate):
+    from float8_mixed_precision_gb300 import nn
+    m = nn.ResidualNorm(64, kind="layer")
+    a, r, g = (_bf(*s).requires_grad_(True) for s in ((*lead, 64), (*lead, 64), gate))
+    r_out, y = m(a, r, g)
+    assert r_out.shape == y.shape == (*lead, 64)
+    (r_out.sum() + y.sum()).backward()
+    for t in (a, r, g):
+        assert t.grad.shape == t.shape and not t.grad.any()
+    with pytest.raises(ValueError):
+        m(_bf(4, 64), _bf(4, 64), _bf(0, 64))

@@ -39,3 +39,19 @@ def test_one_gate_of_no_rows(f8, side):
     torch.cuda.synchronize()
     assert given[6] is dgate and not dgate.any()
     assert new[6].shape == (64,) and all(not t.any() for t in new[2:])
+
+
+@pytest.mark.parametrize("kind", ["rms", "layer"])
+@pytest.mark.parametrize("lead, gate", [((0,), (64,)), ((0,), (0, 64)), ((0, 5), (64,)), ((0, 5), (0, 64)),
+                                        ((0, 5), (0, 1, 64)), ((3, 0), (3, 64)), ((3, 0), (3, 0, 64))])
+def test_gated_norm_of_no_rows(f8, lead, gate, kind):
+    from float8_mixed_precision_gb300 import nn
+    m = nn.ResidualNorm(64, kind=kind, device=DEV)
+    a, r, g = (torch.ones(s, dtype=BF, device=DEV).requires_grad_(True) for s in ((*lead, 64), (*lead, 64), gate))
+    _poison(1)
+    r_out, y = m(a, r, g)
+    assert r_out.shape == y.shape == (*lead, 64)
+    (r_out.float().sum() + y.float().sum()).backward()
+    for t in (a, r, g, *m.parameters()):
+        assert t.grad.shape == t.shape and not t.grad.any()
+    assert f8.f8_last_device_status() == 0
