@@ -836,12 +836,15 @@ class RotaryPositions(torch.nn.Module):
         self.rot, self.scale = rot, float(scale)
         self.layout = binding.F8_ROPE_HALF if layout == "half" else binding.F8_ROPE_INTERLEAVED
         # fp64 and not a buffer: a cast of the module's type must not reach it
-        self._freqs = {None: block.f8_rope_frequencies(rot, base, _SCALINGS[scaling], **more)}
+        with torch.inference_mode(False):  # as in frequencies()
+            self._freqs = {None: block.f8_rope_frequencies(rot, base, _SCALINGS[scaling], **more)}
 
     def frequencies(self, device) -> torch.Tensor:
         device = torch.device(device)
         if device not in self._freqs:
-            self._freqs[device] = self._freqs[None].to(device)
+            # kept for good, so no inference tensor, which no later call could save for its gradient
+            with torch.inference_mode(False):
+                self._freqs[device] = self._freqs[None].to(device)
         return self._freqs[device]
 
     def forward(self, q: torch.Tensor, positions: torch.Tensor, k: torch.Tensor | None = None):

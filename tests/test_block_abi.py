@@ -329,3 +329,18 @@ def test_no_rows_through_the_module(rec, lead, gate):
         assert t.grad.shape == t.shape and not t.grad.any()
     with pytest.raises(ValueError):
         m(_bf(4, 64), _bf(4, 64), _bf(0, 64))
+
+
+# ---------------------------------------------------------------- evaluation first
+def test_rotary_keeps_no_inference_tensor(rec):
+    """What a module keeps of a first use under inference mode serves a later one that trains."""
+    from float8_mixed_precision_gb300 import nn
+    with torch.inference_mode():
+        made = nn.RotaryPositions(64)
+        assert not made.frequencies("meta").is_inference() and not made._freqs[None].is_inference()
+    q, pos = _bf(8, 4, 64).requires_grad_(True), torch.arange(8)
+    for m in (nn.RotaryPositions(64), made):
+        with torch.inference_mode():
+            m(q.detach(), pos)
+        m(q, pos).sum().backward()
+        assert q.grad.shape == q.shape

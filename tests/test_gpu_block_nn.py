@@ -291,3 +291,18 @@ def test_block_captured(f8, f8nn):
         torch.cuda.synchronize()
         for u, v in zip((*outs, *(p.grad for p in leaves)), want):
             assert torch.equal(u, v)
+
+
+def test_rotary_evaluated_then_trained(f8, f8nn):
+    """A module that is first used under inference mode gives the gradients of one that is not."""
+    q, pos, dq = _rnd((40, 4, 64), 1.0, 71).requires_grad_(True), torch.arange(40, device=DEV), _rnd((40, 4, 64), 0.1, 72)
+    grads = []
+    for first in (False, True):
+        m = f8nn.RotaryPositions(64)
+        if first:
+            with torch.inference_mode():
+                m(q.detach(), pos)
+        q.grad = None
+        m(q, pos).backward(dq)
+        grads.append(q.grad.clone())
+    assert torch.equal(grads[0], grads[1])
