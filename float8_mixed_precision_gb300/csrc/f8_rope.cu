@@ -210,8 +210,11 @@ rope_kernel(const __grid_constant__ Args a)
     float *const cosines = turn, *const sines = turn + a.rows_per_block * a.half;
     for (int p = threadIdx.x; p < a.half * nrows; p += kThreads) {
         const int j = static_cast<int>(a.by_half(p));
-        const uint64_t angle = turn_fraction(a.freqs[p - j * a.half]) * static_cast<uint64_t>(at[j]);
-        const float t = static_cast<float>(static_cast<int32_t>(angle >> 32)) * 0x1p-31f;  // half turns
+        const double f = a.freqs[p - j * a.half];
+        const uint64_t angle = turn_fraction(f) * static_cast<uint64_t>(at[j]);
+        float t = static_cast<float>(static_cast<int32_t>(angle >> 32)) * 0x1p-31f;  // half turns
+        if (((__double_as_longlong(f) >> 52) & 0x7FF) == 0x7FF)
+            t = __int_as_float(0x7FC00000);  // infinite or NaN: no angle, and NaN for the pair
         float sn, cs;
         sincospif(t, &sn, &cs);
         cosines[p] = cs * a.scale;

@@ -847,7 +847,8 @@ typedef struct {
  *              position is padding and is copied as it is.
  *   freqs:     device fp64 [rot / 2], radians a position.  Angles are formed as
  *              64-bit fractions of a turn, so a far position loses nothing beyond
- *              freqs' own rounding.
+ *              freqs' own rounding.  A pair whose frequency is NaN or infinite is
+ *              NaN in every row but padding.
  *   rot:       even, 2 <= rot <= dim;  dim <= 1024;  scale finite.
  * x, out aligned to their elements, freqs and positions to 8 bytes.  Rows of whole
  * 16-byte vectors on 16-byte boundaries (with rot / 2 a multiple of a vector's

@@ -203,3 +203,30 @@ def test_past_2_31_elements(f8):
     want, _ = f8.f8_rope(x[-1:].clone(), pos[-1:], freqs)
     got, _ = f8.f8_rope(x, pos, freqs, q_out=x)
     assert x.numel() > 1 << 31 and torch.equal(got[-1:], want) and not got[:-1].any()
+
+
+@pytest.mark.parametrize("layout", [0, 1], ids=["half", "interleaved"])
+@pytest.mark.parametrize("dtype", [BF, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("dim, rot", [(64, 64), (64, 48), (20, 12)])
+def test_frequencies_that_are_no_numbers(f8, layout, dtype, dim, rot):
+    """A pair whose frequency is NaN or infinite is NaN at every position, as sine and cosine of its angle are, 0 times
+    infinity among them; the other pairs and rows of padding are as they are without it.  The largest finite frequency
+    and the smallest turn by a number."""
+    x = _rnd((7, 3, dim), 15, dtype)
+    pos = torch.tensor([0, 1, 5, -1, 900, 1 << 40, 3], device=DEV)
+    freqs = f8.f8_rope_frequencies(rot, device=DEV)
+    half = rot // 2
+    for inverse in (False, True):
+        want, _ = f8.f8_rope(x, pos, freqs, layout=layout, inverse=inverse)
+        bad = freqs.clone()
+        bad[1], bad[half - 2], bad[half - 1] = float("nan"), float("inf"), float("-inf")
+        got, _ = f8.f8_rope(x, pos, bad, layout=layout, inverse=inverse)
+        gone = torch.zeros(dim, dtype=torch.bool, device=DEV)
+        for i in (1, half - 2, half - 1):
+            gone[[i, i + half] if layout == 0 else [2 * i, 2 * i + 1]] = True
+        assert torch.equal(got[:, :, ~gone], want[:, :, ~gone])
+        rows = pos >= 0
+        assert torch.isnan(got[rows][:, :, gone]).all() and torch.equal(got[~rows], x[~rows])
+        ends = freqs.clone()
+        ends[1], ends[half - 1] = 1.7e308, 5e-324
+        assert torch.isfinite(f8.f8_rope(x, pos, ends, layout=layout, inverse=inverse)[0]).all()
