@@ -354,12 +354,17 @@ f8_status f8_rope(const f8_rope_tensor *tensors, int count, f8_dtype type, int64
         heads += t.heads;
         if (some && t.heads > 0 && (t.x == nullptr || t.out == nullptr))
             return F8_ERR_INVALID;
-        // in place means in place: another order of the rows would read what it wrote
-        if (t.x == t.out && (t.x_batch != t.out_batch || t.x_seq != t.out_seq || t.x_head != t.out_head))
-            return F8_ERR_INVALID;
-        // rows of the output lie apart
-        if ((batch > 1 && t.out_batch == 0) || (seq > 1 && t.out_seq == 0) || (t.heads > 1 && t.out_head == 0))
-            return F8_ERR_INVALID;
+        if (some && t.heads > 0) {
+            // strides count where more than one element goes by them
+            const bool b = batch > 1, q = seq > 1, h = t.heads > 1;
+            // in place means in place: another order of the rows would read what it wrote
+            if (t.x == t.out && ((b && t.x_batch != t.out_batch) || (q && t.x_seq != t.out_seq) ||
+                                 (h && t.x_head != t.out_head)))
+                return F8_ERR_INVALID;
+            // rows of the output lie apart
+            if ((b && t.out_batch == 0) || (q && t.out_seq == 0) || (h && t.out_head == 0))
+                return F8_ERR_INVALID;
+        }
         if (!aligned(t.x, esize) || !aligned(t.out, esize))
             return F8_ERR_ALIGN;
     }

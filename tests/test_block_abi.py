@@ -344,3 +344,20 @@ def test_rotary_keeps_no_inference_tensor(rec):
             m(q.detach(), pos)
         m(q, pos).sum().backward()
         assert q.grad.shape == q.shape
+
+
+# ---------------------------------------------------------------- nothing to rotate
+def test_rope_of_nothing(L):
+    """Empty tensors have no address, and views of packed rows strides that their outputs lack: no reason to refuse a call
+    that does nothing, nor strides that no element goes by.  (Without a GPU the call ends at the device.)"""
+    args = lambda t, count, batch, seq: (t, count, 0, batch, seq, 64, 64, 0, P, seq, 1, P, 1.0, 0, None)  # noqa: E731
+    packed = dict(x_batch=3840, x_seq=768, x_head=64, out_batch=2560, out_seq=512, out_head=64)
+    for batch, seq in ((0, 5), (2, 0), (0, 0)):
+        assert L.f8_rope(*args(_rope_args(x=None, out=None, heads=8, **packed), 1, batch, seq)) not in (INVALID, SHAPE, ALIGN)
+    two = (binding._RopeTensor * 2)(binding._RopeTensor(None, None, 0, 3840, 768, 64, 0, 0, 0),
+                                    binding._RopeTensor(P, 2 * P, 2, 3840, 768, 64, 640, 128, 64))
+    if not torch.cuda.is_available():  # the addresses are not to be read
+        assert L.f8_rope(*args(two, 2, 2, 5)) not in (INVALID, SHAPE, ALIGN)
+        one = _rope_args(out=P, heads=1, x_batch=9, out_batch=8, x_head=5, out_head=0, out_seq=512)
+        assert L.f8_rope(*args(one, 1, 1, 5)) not in (INVALID, SHAPE, ALIGN)
+        assert L.f8_rope(*args(one, 1, 2, 5)) == INVALID

@@ -230,3 +230,30 @@ def test_frequencies_that_are_no_numbers(f8, layout, dtype, dim, rot):
         ends = freqs.clone()
         ends[1], ends[half - 1] = 1.7e308, 5e-324
         assert torch.isfinite(f8.f8_rope(x, pos, ends, layout=layout, inverse=inverse)[0]).all()
+
+
+def test_empty_views(f8):
+    """Views of packed rows without a batch, rows or heads: their strides are those of no output, and of no account."""
+    freqs = f8.f8_rope_frequencies(64, device=DEV)
+    for b, s in ((0, 5), (2, 0), (0, 0)):
+        packed = torch.zeros((b, s, 12, 64), dtype=BF, device=DEV)
+        pos = torch.zeros((b, s), dtype=torch.int64, device=DEV)
+        for inverse in (False, True):
+            q, k = f8.f8_rope(packed[:, :, :8], pos, freqs, k=packed[:, :, 8:10], inverse=inverse)
+            assert q.shape == (b, s, 8, 64) and k.shape == (b, s, 2, 64)
+    packed = _rnd((2, 5, 12, 64), 16, BF)
+    pos = torch.arange(5, device=DEV)
+    q, k = f8.f8_rope(packed[:, :, 3:3], pos, freqs, k=packed[:, :, 8:10])  # no queries
+    assert q.shape == (2, 5, 0, 64) and torch.equal(k, f8.f8_rope(packed[:, :, 8:10], pos, freqs)[0])
+    assert f8.f8_last_device_status() == 0
+
+
+def test_in_place_single_rows(f8):
+    """In place where a dimension is of one: the strides that no element goes by may differ."""
+    packed = _rnd((1, 5, 12, 64), 17, BF)
+    pos, freqs = torch.arange(5, device=DEV), f8.f8_rope_frequencies(64, device=DEV)
+    q = packed[:, :, :8]
+    want, _ = f8.f8_rope(q, pos, freqs)
+    out = q.as_strided(q.shape, (7, *q.stride()[1:]), q.storage_offset())
+    f8.f8_rope(q, pos, freqs, q_out=out)
+    assert torch.equal(q, want)
