@@ -156,15 +156,18 @@ act_bwd_kernel(const __nv_bfloat16 *dy, const __nv_bfloat16 *z, int64_t rows, in
                 before += sums[w][j - kCarry + sw];  // column c - kCarry
         }
         if (c < cols) {
-            if (out == nullptr)
-                parts[static_cast<int64_t>(blockIdx.y) * cols + c] = f;
-            else if (out_bf16)
+            const int64_t part = static_cast<int64_t>(blockIdx.y) * cols + c;
+            if (out == nullptr) {
+                if (in_range(part, 1, gridDim.y * cols, status))
+                    parts[part] = f;
+            } else if (out_bf16)
                 static_cast<__nv_bfloat16 *>(out)[c] = __float2bfloat16_rn(f);
             else
                 static_cast<float *>(out)[c] = f;
         }
-        if (!EVEN && j < kCarry)
-            carry[(static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x) * kCarry + j] = before;
+        const int64_t unit = static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x;
+        if (!EVEN && j < kCarry && in_range(unit, 1, static_cast<int64_t>(gridDim.y) * gridDim.x, status))
+            carry[unit * kCarry + j] = before;
     }
     if (amax != nullptr) {
         __syncthreads();
@@ -196,12 +199,15 @@ act_reduce_kernel(const float *__restrict__ parts, const float *__restrict__ car
     if (c < cols) {
 #pragma unroll 4
         for (int i = k; i < nparts; i += 32)
-            s += parts[static_cast<int64_t>(i) * cols + c];
+            if (in_range(static_cast<int64_t>(i) * cols + c, 1, nparts * cols, status))
+                s += parts[static_cast<int64_t>(i) * cols + c];
         const int64_t strip = c / kStrip + 1;
         const int j = static_cast<int>(c - strip * kStrip) + kCarry;
         if (carry != nullptr && j >= 0 && strip < strips)
             for (int i = k; i < nparts; i += 32)
-                s += carry[(static_cast<int64_t>(i) * strips + strip) * kCarry + j];
+                if (in_range(i * int64_t{strips} + strip, 1, nparts * int64_t{strips}, status) &&
+                    in_range(j, 1, kCarry, status))
+                    s += carry[(static_cast<int64_t>(i) * strips + strip) * kCarry + j];
     }
     acc[k][lane] = s;
     __syncthreads();

@@ -48,15 +48,19 @@ __device__ __forceinline__ float elem(const float *p) { return *p; }
 __device__ __forceinline__ void put(__nv_bfloat16 *p, float f) { *p = __float2bfloat16_rn(f); }
 __device__ __forceinline__ void put(float *p, float f) { *p = f; }
 
-// One parameter value, bf16 or fp32.
-__device__ __forceinline__ float param(const void *p, int f32, int64_t i)
+// One parameter value of n, bf16 or fp32.
+__device__ __forceinline__ float param(const void *p, int f32, int64_t i, int64_t n, unsigned *status)
 {
+    if (!in_range(i, 1, n, status))
+        return 0.0f;
     return f32 ? static_cast<const float *>(p)[i]
                : __bfloat162float(static_cast<const __nv_bfloat16 *>(p)[i]);
 }
 
-__device__ __forceinline__ void put_param(void *p, int f32, int64_t i, float v)
+__device__ __forceinline__ void put_param(void *p, int f32, int64_t i, float v, int64_t n, unsigned *status)
 {
+    if (!in_range(i, 1, n, status))
+        return;
     if (f32)
         static_cast<float *>(p)[i] = v;
     else
@@ -71,6 +75,23 @@ struct Call {
     float eps, scale;
     const void *w_pre, *b_pre, *w_post, *b_post, *gate;
     float *stats;        // [4][rows]: mean and 1/deviation of a, then of r'
+
+    __device__ __forceinline__ float stat(int which, int64_t row, unsigned *status) const
+    {
+        const int64_t i = which * rows + row;
+        return in_range(i, 1, 4 * rows, status) ? stats[i] : 0.0f;
+    }
+    __device__ __forceinline__ void put_stat(int which, int64_t row, float v, unsigned *status) const
+    {
+        const int64_t i = which * rows + row;
+        if (in_range(i, 1, 4 * rows, status))
+            stats[i] = v;
+    }
+    // elements of the gates
+    __device__ __forceinline__ int64_t gate_n() const
+    {
+        return gate != nullptr ? ((rows - 1) / gate_rows + 1) * cols : 0;
+    }
 };
 
 // Sum over the block, in a fixed order; every thread gets it.  `red` has two halves
@@ -141,12 +162,12 @@ fwd_walk_kernel(const Call c, const TA *a, const TR *r, TR *r_out, TA *y, unsign
                 return 0.0f;
             float u = elem(a + at + i);
             if (c.w_post != nullptr) {
-                u = (u - mu1) * s1 * param(c.w_post, c.w_f32, i);
+                u = (u - mu1) * s1 * param(c.w_post, c.w_f32, i, c.cols, status);
                 if (c.b_post != nullptr)
-                    u += param(c.b_post, c.w_f32, i);
+                    u += param(c.b_post, c.w_f32, i, c.cols, status);
             }
             if (c.gate != nullptr)
-                u *= param(c.gate, c.g_f32, gat + i);
+                u *= param(c.gate, c.g_f32, gat + i, c.gate_n(), status);
             return fmaf(c.scale, elem(r + at + i), u);
         };
         float mu2 = 0.0f, t = 0.0f;
@@ -164,9 +185,9 @@ fwd_walk_kernel(const Call c, const TA *a, const TR *r, TR *r_out, TA *y, unsign
         // a thread reads its own columns only, so r_out may be r and y may be a
         for (int64_t i = threadIdx.x; i < c.cols; i += kWalkThreads) {
             const float v = stream(i);
-            float o = (v - mu2) * s2 * param(c.w_pre, c.w_f32, i);
+            float o = (v - mu2) * s2 * param(c.w_pre, c.w_f32, i, c.cols, status);
             if (c.b_pre != nullptr)
-                o += param(c.b_pre, c.w_f32, i);
+                o += param(c.b_pre, c.w_f32, i, c.cols, status);
             if (!in_range(at + i, 1, total, status))
                 continue;
             put(r_out + at + i, v);
@@ -177,12 +198,12 @@ fwd_walk_kernel(const Call c, const TA *a, const TR *r, TR *r_out, TA *y, unsign
         if (threadIdx.x == 0) {
             if (c.w_post != nullptr) {
                 if (c.layer)
-                    c.stats[row] = mu1;
-                c.stats[c.rows + row] = s1;
+                    c.put_stat(0, row, mu1, status);
+                c.put_stat(1, row, s1, status);
             }
             if (c.layer)
-                c.stats[2 * c.rows + row] = mu2;
-            c.stats[3 * c.rows + row] = s2;
+                c.put_stat(2, row, mu2, status);
+            c.put_stat(3, row, s2, status);
         }
     }
     if (amax != nullptr) {
@@ -222,14 +243,14 @@ bwd_walk_kernel(const Call c, const TA *__restrict__ dy, const TR *__restrict__ 
     for (int64_t row = blockIdx.x; row < c.rows; row += gridDim.x) {
         const int64_t at = row * c.cols;
         const int64_t gat = c.gate != nullptr ? row / c.gate_rows * c.cols : 0;
-        const float mu1 = post && c.layer ? c.stats[row] : 0.0f;
-        const float s1 = post ? c.stats[c.rows + row] : 1.0f;
-        const float mu2 = c.layer ? c.stats[2 * c.rows + row] : 0.0f;
-        const float s2 = c.stats[3 * c.rows + row];
+        const float mu1 = post && c.layer ? c.stat(0, row, status) : 0.0f;
+        const float s1 = post ? c.stat(1, row, status) : 1.0f;
+        const float mu2 = c.layer ? c.stat(2, row, status) : 0.0f;
+        const float s2 = c.stat(3, row, status);
         float t1 = 0.0f, t2 = 0.0f;
         for (int64_t i = threadIdx.x; i < c.cols; i += kWalkThreads)
             if (in_range(at + i, 1, total, status)) {
-                const float g = elem(dy + at + i) * param(c.w_pre, c.w_f32, i);
+                const float g = elem(dy + at + i) * param(c.w_pre, c.w_f32, i, c.cols, status);
                 t1 = fmaf(g, (elem(r_out + at + i) - mu2) * s2, t1);
                 t2 += g;
             }
@@ -237,7 +258,7 @@ bwd_walk_kernel(const Call c, const TA *__restrict__ dy, const TR *__restrict__ 
         const float k2 = c.layer ? -s2 * (sum(t2) * inv_c) : 0.0f;
         auto grad = [&](int64_t i) {
             return stream_grad(dr_out != nullptr ? elem(dr_out + at + i) : 0.0f,
-                               elem(dy + at + i) * param(c.w_pre, c.w_f32, i),
+                               elem(dy + at + i) * param(c.w_pre, c.w_f32, i, c.cols, status),
                                (elem(r_out + at + i) - mu2) * s2, s2, k1, k2);
         };
         float d1 = 0.0f, d2 = 0.0f;
@@ -245,9 +266,9 @@ bwd_walk_kernel(const Call c, const TA *__restrict__ dy, const TR *__restrict__ 
             t1 = t2 = 0.0f;
             for (int64_t i = threadIdx.x; i < c.cols; i += kWalkThreads)
                 if (in_range(at + i, 1, total, status)) {
-                    float h = grad(i) * param(c.w_post, c.w_f32, i);
+                    float h = grad(i) * param(c.w_post, c.w_f32, i, c.cols, status);
                     if (c.gate != nullptr)
-                        h *= param(c.gate, c.g_f32, gat + i);
+                        h *= param(c.gate, c.g_f32, gat + i, c.gate_n(), status);
                     t1 = fmaf(h, (elem(a + at + i) - mu1) * s1, t1);
                     t2 += h;
                 }
@@ -262,14 +283,14 @@ bwd_walk_kernel(const Call c, const TA *__restrict__ dy, const TR *__restrict__ 
                 put(dr + at + i, c.scale * d);
             if (da == nullptr)
                 continue;
-            float h = c.gate != nullptr ? d * param(c.gate, c.g_f32, gat + i) : d;
+            float h = c.gate != nullptr ? d * param(c.gate, c.g_f32, gat + i, c.gate_n(), status) : d;
             if (post) {
                 const float e1 = (elem(a + at + i) - mu1) * s1;
-                h = s1 * (fmaf(-e1, d1, h * param(c.w_post, c.w_f32, i)) - d2);
+                h = s1 * (fmaf(-e1, d1, h * param(c.w_post, c.w_f32, i, c.cols, status)) - d2);
             }
             put(da + at + i, h);
         }
-        if (threadIdx.x == 0 && consts != nullptr) {
+        if (threadIdx.x == 0 && consts != nullptr && in_range(c.rows + row, 1, 2 * c.rows, status)) {
             consts[row] = k1;
             consts[c.rows + row] = k2;
         }
@@ -401,7 +422,7 @@ fwd_kernel(const Call c, const TA *a, const TR *r, TR *r_out, TA *y, unsigned *a
     rows::Place<MODE, E> pl;
     pl.set(sl.first, sl.n, walk.shift, static_cast<int>(c.cols));
     rows::Slots<TA, 1, TR, 1, MODE> slots;
-    slots.start(dyn, full, stages, c.cols, c.rows, sl, walk.shift);
+    slots.start(dyn, full, stages, c.cols, c.rows, sl, walk.shift, status);
     slots.a[0] = a;
     slots.r[0] = r;
     zero_sums(red);
@@ -428,10 +449,10 @@ fwd_kernel(const Call c, const TA *a, const TR *r, TR *r_out, TA *y, unsigned *a
     const bool post = c.w_post != nullptr, gated = c.gate != nullptr, layer = c.layer != 0;
     Param<E, BF> w1, b1, g, w2, b2;
     if (BF) {
-        rows::take_param<MODE>(c.w_post, 0, 0, pl, 1.0f, w1);
-        rows::take_param<MODE>(c.b_post, 0, 0, pl, 0.0f, b1);
-        rows::take_param<MODE>(c.w_pre, 0, 0, pl, 1.0f, w2);
-        rows::take_param<MODE>(c.b_pre, 0, 0, pl, 0.0f, b2);
+        rows::take_param<MODE>(c.w_post, 0, 0, pl, 1.0f, w1, c.cols, status);
+        rows::take_param<MODE>(c.b_post, 0, 0, pl, 0.0f, b1, c.cols, status);
+        rows::take_param<MODE>(c.w_pre, 0, 0, pl, 1.0f, w2, c.cols, status);
+        rows::take_param<MODE>(c.b_pre, 0, 0, pl, 0.0f, b2, c.cols, status);
     }
     int64_t gate = gated ? first / c.gate_rows : 0;
     int64_t gate_end = gated ? first : stop, gate_at = 0;
@@ -442,7 +463,7 @@ fwd_kernel(const Call c, const TA *a, const TR *r, TR *r_out, TA *y, unsigned *a
         if (gated && row >= gate_end) {
             gate = MODE == rows::kShift ? row / c.gate_rows : gate;
             if (BF)
-                rows::take_param<MODE>(c.gate, 0, gate * c.cols, pl, 1.0f, g);
+                rows::take_param<MODE>(c.gate, 0, gate * c.cols, pl, 1.0f, g, c.gate_n(), status);
             gate_at = gate * c.cols;
             ++gate;
             gate_end = min(stop, gate * c.gate_rows);  // within rows + gate_rows
@@ -459,16 +480,16 @@ fwd_kernel(const Call c, const TA *a, const TR *r, TR *r_out, TA *y, unsigned *a
         if (post) {
             row_stats<MODE, E>(x, pl, layer, inv_c, c.eps, sum, mu1, s1);
             if (!BF)
-                rows::take_param<MODE>(c.w_post, c.w_f32, 0, pl, 1.0f, w1);
+                rows::take_param<MODE>(c.w_post, c.w_f32, 0, pl, 1.0f, w1, c.cols, status);
             if (!BF)
-                rows::take_param<MODE>(c.b_post, c.w_f32, 0, pl, 0.0f, b1);
+                rows::take_param<MODE>(c.b_post, c.w_f32, 0, pl, 0.0f, b1, c.cols, status);
 #pragma unroll
             for (int i = 0; i < P; ++i)
                 x[i] = __ffma2_rn(__fmul2_rn(x[i], splat(s1)), w1.pair(i), b1.pair(i));
         }
         if (gated) {
             if (!BF)
-                rows::take_param<MODE>(c.gate, c.g_f32, gate_at, pl, 1.0f, g);
+                rows::take_param<MODE>(c.gate, c.g_f32, gate_at, pl, 1.0f, g, c.gate_n(), status);
 #pragma unroll
             for (int i = 0; i < P; ++i)
                 x[i] = __fmul2_rn(x[i], g.pair(i));
@@ -489,18 +510,18 @@ fwd_kernel(const Call c, const TA *a, const TR *r, TR *r_out, TA *y, unsigned *a
             if (rank == 0) {
                 if (post) {
                     if (layer)
-                        c.stats[row] = mu1;
-                    c.stats[c.rows + row] = s1;
+                        c.put_stat(0, row, mu1, status);
+                    c.put_stat(1, row, s1, status);
                 }
                 if (layer)
-                    c.stats[2 * c.rows + row] = mu2;
-                c.stats[3 * c.rows + row] = s2;
+                    c.put_stat(2, row, mu2, status);
+                c.put_stat(3, row, s2, status);
             }
         }
         if (!BF)
-            rows::take_param<MODE>(c.w_pre, c.w_f32, 0, pl, 1.0f, w2);
+            rows::take_param<MODE>(c.w_pre, c.w_f32, 0, pl, 1.0f, w2, c.cols, status);
         if (!BF)
-            rows::take_param<MODE>(c.b_pre, c.w_f32, 0, pl, 0.0f, b2);
+            rows::take_param<MODE>(c.b_pre, c.w_f32, 0, pl, 0.0f, b2, c.cols, status);
 #pragma unroll
         for (int i = 0; i < P; ++i)
             x[i] = __ffma2_rn(__fmul2_rn(x[i], splat(s2)), w2.pair(i), b2.pair(i));
@@ -530,6 +551,7 @@ fwd_kernel(const Call c, const TA *a, const TR *r, TR *r_out, TA *y, unsigned *a
 // chunks only at the chunk's ends.
 struct Chunks {
     int64_t rows, gate_rows, chunk;
+    int64_t room;  // units that the workspace has partial rows for
     __host__ __device__ int64_t first(int64_t i) const { return i * chunk; }
     __host__ __device__ int64_t stop(int64_t i) const
     {
@@ -568,9 +590,9 @@ cols_walk_kernel(const Call c, const Chunks ch, const TA *__restrict__ dy, const
     const int64_t chunk = blockIdx.y, first = ch.first(chunk), stop = ch.stop(chunk);
     const int64_t total = c.rows * c.cols;
     const bool post = c.w_post != nullptr, gated = c.gate != nullptr;
-    const float w2 = param(c.w_pre, c.w_f32, i);
-    const float w1 = post ? param(c.w_post, c.w_f32, i) : 1.0f;
-    const float b1 = c.b_post != nullptr ? param(c.b_post, c.w_f32, i) : 0.0f;
+    const float w2 = param(c.w_pre, c.w_f32, i, c.cols, status);
+    const float w1 = post ? param(c.w_post, c.w_f32, i, c.cols, status) : 1.0f;
+    const float b1 = c.b_post != nullptr ? param(c.b_post, c.w_f32, i, c.cols, status) : 0.0f;
     float dw2 = 0.0f, db2 = 0.0f, dw1 = 0.0f, db1 = 0.0f;
     for (int64_t row = first; row < stop;) {
         // rows of one gate: S = sum D e1, T = sum D
@@ -579,12 +601,12 @@ cols_walk_kernel(const Call c, const Chunks ch, const TA *__restrict__ dy, const
         float S = 0.0f, T = 0.0f;
         for (; row < end; ++row) {
             const int64_t at = row * c.cols + i;
-            if (!in_range(at, 1, total, status))
+            if (!in_range(at, 1, total, status) || !in_range(c.rows + row, 1, 2 * c.rows, status))
                 continue;
-            const float mu1 = post && c.layer ? c.stats[row] : 0.0f;
-            const float s1 = post ? c.stats[c.rows + row] : 1.0f;
-            const float mu2 = c.layer ? c.stats[2 * c.rows + row] : 0.0f;
-            const float s2 = c.stats[3 * c.rows + row];
+            const float mu1 = post && c.layer ? c.stat(0, row, status) : 0.0f;
+            const float s1 = post ? c.stat(1, row, status) : 1.0f;
+            const float mu2 = c.layer ? c.stat(2, row, status) : 0.0f;
+            const float s2 = c.stat(3, row, status);
             const float v = elem(dy + at), e2 = (elem(r_out + at) - mu2) * s2;
             const float d = stream_grad(dr_out != nullptr ? elem(dr_out + at) : 0.0f, v * w2, e2, s2,
                                         consts[row], consts[c.rows + row]);
@@ -594,17 +616,20 @@ cols_walk_kernel(const Call c, const Chunks ch, const TA *__restrict__ dy, const
             S = fmaf(d, e1, S);
             T += d;
         }
-        const float gate = gated ? param(c.gate, c.g_f32, g * c.cols + i) : 1.0f;
+        const float gate = gated ? param(c.gate, c.g_f32, g * c.cols + i, c.gate_n(), status) : 1.0f;
         dw1 = fmaf(gate, S, dw1);
         db1 = fmaf(gate, T, db1);
         if (dgate != nullptr) {
             const float dg = fmaf(S, w1, T * b1);
+            const int64_t end_at = (chunk * 2 + ch.slot(g, chunk)) * c.cols + i;
             if (ch.whole(g, chunk))
-                put_param(dgate, c.g_f32, g * c.cols + i, dg);
-            else
-                ends[(chunk * 2 + ch.slot(g, chunk)) * c.cols + i] = dg;
+                put_param(dgate, c.g_f32, g * c.cols + i, dg, c.gate_n(), status);
+            else if (in_range(end_at, 1, 2 * ch.room * c.cols, status))
+                ends[end_at] = dg;
         }
     }
+    if (!in_range(chunk * 4 * c.cols + i, 3 * c.cols + 1, 4 * ch.room * c.cols, status))
+        return;
     float *p = parts + chunk * 4 * c.cols + i;
     p[0] = dw2;
     p[c.cols] = db2;
@@ -639,7 +664,7 @@ bwd_kernel(const Call c, const Chunks ch, const TA *__restrict__ dy, const TR *_
     rows::Place<MODE, E> pl;
     pl.set(sl.first, sl.n, walk.shift, static_cast<int>(c.cols));
     rows::Slots<TA, 2, TR, 2, MODE> slots;
-    slots.start(dyn, full, stages, c.cols, c.rows, sl, walk.shift);
+    slots.start(dyn, full, stages, c.cols, c.rows, sl, walk.shift, status);
     slots.a[0] = dy;
     slots.a[1] = a;
     slots.r[0] = dr_out;
@@ -668,9 +693,9 @@ bwd_kernel(const Call c, const Chunks ch, const TA *__restrict__ dy, const TR *_
     float2 *acc = reinterpret_cast<float2 *>(dyn + stages * slots.slot_bytes()) + threadIdx.x;
     auto acc_at = [&](int i) -> float2 & { return acc[i * blockDim.x]; };
     const int64_t pitch = rows::sums_pitch(c.cols);
-    float *p = parts + unit * 4 * pitch;
+    const int64_t parts_n = 4 * ch.room * pitch, ends_n = 2 * ch.room * pitch, mine = unit * 4 * pitch;
     Param<E, false> w2, gw;  // gw: gate w1
-    rows::take_param<MODE>(c.w_pre, c.w_f32, 0, pl, 1.0f, w2);
+    rows::take_param<MODE>(c.w_pre, c.w_f32, 0, pl, 1.0f, w2, c.cols, status);
     float2 dw2[P], db2[P], S[P], T[P];
 #pragma unroll
     for (int i = 0; i < P; ++i)
@@ -684,12 +709,12 @@ bwd_kernel(const Call c, const Chunks ch, const TA *__restrict__ dy, const TR *_
         Param<E, false> w;
         float2 v[P];
         if (dgate != nullptr) {
-            rows::take_param<MODE>(c.w_post, c.w_f32, 0, pl, 1.0f, w);
+            rows::take_param<MODE>(c.w_post, c.w_f32, 0, pl, 1.0f, w, c.cols, status);
 #pragma unroll
             for (int i = 0; i < P; ++i)
                 v[i] = __fmul2_rn(S[i], w.pair(i));
             if (FULL) {
-                rows::take_param<MODE>(c.b_post, c.w_f32, 0, pl, 0.0f, w);
+                rows::take_param<MODE>(c.b_post, c.w_f32, 0, pl, 0.0f, w, c.cols, status);
 #pragma unroll
                 for (int i = 0; i < P; ++i)
                     v[i] = __ffma2_rn(T[i], w.pair(i), v[i]);
@@ -698,15 +723,15 @@ bwd_kernel(const Call c, const Chunks ch, const TA *__restrict__ dy, const TR *_
             if constexpr (MODE != rows::kShift) {
                 whole = ch.whole(gate, walk.chunk);
                 if (whole)
-                    rows::give_param<MODE, E>(dgate, c.g_f32, gate * c.cols, pl, v);
+                    rows::give_param<MODE, E>(dgate, c.g_f32, gate * c.cols, pl, v, c.gate_n(), status);
             }
             if (!whole) {
                 const int to = ch.slot(gate, walk.chunk);
                 left |= 1 << to;
-                rows::give_sums<MODE, E>(ends + (unit * 2 + to) * pitch, pl, v);
+                rows::give_sums<MODE, E>(ends, (unit * 2 + to) * pitch, ends_n, pl, v, status);
             }
         }
-        rows::take_param<MODE>(c.gate, c.g_f32, gate * c.cols, pl, 1.0f, w);
+        rows::take_param<MODE>(c.gate, c.g_f32, gate * c.cols, pl, 1.0f, w, c.gate_n(), status);
         auto join = [&](float2 (&of)[P], int at, int row) {
 #pragma unroll
             for (int i = 0; i < P; ++i) {
@@ -716,7 +741,7 @@ bwd_kernel(const Call c, const Chunks ch, const TA *__restrict__ dy, const TR *_
                 of[i] = splat(0.0f);
             }
             if (last)
-                rows::give_sums<MODE, E>(p + row * pitch, pl, v);
+                rows::give_sums<MODE, E>(parts, mine + row * pitch, parts_n, pl, v, status);
         };
         join(S, 0, 2);
         if (FULL)
@@ -733,13 +758,13 @@ bwd_kernel(const Call c, const Chunks ch, const TA *__restrict__ dy, const TR *_
         if (row >= stop)
             return v;
         if (post) {
-            v.s1 = c.stats[c.rows + row];
+            v.s1 = c.stat(1, row, status);
             if (layer)
-                v.mu1 = c.stats[row];
+                v.mu1 = c.stat(0, row, status);
         }
-        v.s2 = c.stats[3 * c.rows + row];
+        v.s2 = c.stat(3, row, status);
         if (layer)
-            v.mu2 = c.stats[2 * c.rows + row];
+            v.mu2 = c.stat(2, row, status);
         return v;
     };
     Stats now, soon = stats_of(first), later = stats_of(first + kStep);
@@ -789,8 +814,8 @@ bwd_kernel(const Call c, const Chunks ch, const TA *__restrict__ dy, const TR *_
             gate = ch.gate(row);
             gate_end = min(stop, ch.gate_stop(gate));
             Param<E, false> g;
-            rows::take_param<MODE>(c.w_post, c.w_f32, 0, pl, 1.0f, gw);
-            rows::take_param<MODE>(c.gate, c.g_f32, gate * c.cols, pl, 1.0f, g);
+            rows::take_param<MODE>(c.w_post, c.w_f32, 0, pl, 1.0f, gw, c.cols, status);
+            rows::take_param<MODE>(c.gate, c.g_f32, gate * c.cols, pl, 1.0f, g, c.gate_n(), status);
 #pragma unroll
             for (int i = 0; i < P; ++i)
                 gw.set(i, __fmul2_rn(gw.pair(i), g.pair(i)));
@@ -867,19 +892,19 @@ bwd_kernel(const Call c, const Chunks ch, const TA *__restrict__ dy, const TR *_
             close(row + kStep >= stop);
     }
     if (first >= stop) {
-        rows::give_sums<MODE, E>(p + 2 * pitch, pl, S);
+        rows::give_sums<MODE, E>(parts, mine + 2 * pitch, parts_n, pl, S, status);
         if (FULL)
-            rows::give_sums<MODE, E>(p + 3 * pitch, pl, T);
+            rows::give_sums<MODE, E>(parts, mine + 3 * pitch, parts_n, pl, T, status);
     }
     if (MODE == rows::kShift && dgate != nullptr) {
         // a unit without rows of one of them: close left zeros
         for (int to = 0; to < 2; ++to)
             if ((left & (1 << to)) == 0)
-                rows::give_sums<MODE, E>(ends + (unit * 2 + to) * pitch, pl, S);
+                rows::give_sums<MODE, E>(ends, (unit * 2 + to) * pitch, ends_n, pl, S, status);
     }
-    rows::give_sums<MODE, E>(p, pl, dw2);
+    rows::give_sums<MODE, E>(parts, mine, parts_n, pl, dw2, status);
     if (FULL)
-        rows::give_sums<MODE, E>(p + pitch, pl, db2);
+        rows::give_sums<MODE, E>(parts, mine + pitch, parts_n, pl, db2, status);
     if (threadIdx.x == 0)
         slots.drain();
     if (MODE != rows::kFull && ranks > 1)
@@ -927,7 +952,8 @@ reduce_kernel(const __grid_constant__ Sums a, const Chunks ch, unsigned *status)
             const float *p = a.parts + static_cast<int64_t>(blockIdx.y) * a.pitch + c;
 #pragma unroll 8
             for (int i = k; i < a.nparts; i += W)
-                s += p[static_cast<int64_t>(i) * 4 * a.pitch + (i * a.shift & 7)];
+                if (in_range((4ll * i + blockIdx.y) * a.pitch + c + (i * a.shift & 7), 1, 4 * ch.room * a.pitch, status))
+                    s += p[static_cast<int64_t>(i) * 4 * a.pitch + (i * a.shift & 7)];
         }
     } else {
         const int64_t y = blockIdx.y - 4;
@@ -952,18 +978,23 @@ reduce_kernel(const __grid_constant__ Sums a, const Chunks ch, unsigned *status)
         // the gate comes first in every chunk but the one that it begins in
         const int64_t n = a.units, step = a.by == kEach ? W : 1;
         if (c < cols) {
+            auto held = [&](const float *p, int64_t i) {
+                return in_range(p - a.ends + i * 2 * a.pitch + (i * a.shift & 7), 1, 2 * ch.room * a.pitch, status);
+            };
             const float *p = a.ends + (first * n * 2 + ch.slot(g, first)) * a.pitch + c;
 #pragma unroll 8
             for (int64_t i = a.by == kEach ? k : 0; i < n; i += step)
-                s += p[i * 2 * a.pitch + (i * a.shift & 7)];
+                if (held(p, i))
+                    s += p[i * 2 * a.pitch + (i * a.shift & 7)];
             p = a.ends + (first + 1) * n * 2 * a.pitch + c;
 #pragma unroll 8
             for (int64_t i = a.by == kEach ? k : 0; i < (last - first) * n; i += step)
-                s += p[i * 2 * a.pitch + (i * a.shift & 7)];
+                if (held(p, i))
+                    s += p[i * 2 * a.pitch + (i * a.shift & 7)];
         }
         if (a.by != kEach) {
-            if (c < cols && in_range(at + c, 1, a.gates * cols, status))
-                put_param(out, f32, at + c, s);
+            if (c < cols)
+                put_param(out, f32, at + c, s, a.gates * cols, status);
             return;
         }
     }
@@ -974,8 +1005,7 @@ reduce_kernel(const __grid_constant__ Sums a, const Chunks ch, unsigned *status)
 #pragma unroll 4
     for (int i = 1; i < W; ++i)
         s += acc[i][lane];
-    if (in_range(at + c, 1, at + cols, status))
-        put_param(out, f32, at + c, s);
+    put_param(out, f32, at + c, s, blockIdx.y < 4 ? cols : a.gates * cols, status);
 }
 
 // ------------------------------------------------------------ launches
@@ -1065,6 +1095,7 @@ size_t round256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
 // parameters' gradients, and of the gates at the chunks' ends.
 struct Workspace {
     size_t consts, parts, ends, bytes;
+    int64_t room;  // units that have partial rows
 };
 
 Workspace workspace_of(int64_t rows, int64_t cols, int sms)
@@ -1077,6 +1108,7 @@ Workspace workspace_of(int64_t rows, int64_t cols, int sms)
     w.parts = walk ? round256(2 * static_cast<size_t>(rows) * sizeof(float)) : 0;
     w.ends = w.parts + round256(4 * n * row);
     w.bytes = w.ends + round256(2 * n * row);
+    w.room = static_cast<int64_t>(n);
     return w;
 }
 
@@ -1253,7 +1285,7 @@ cudaError_t bwd(const Call &c, const void *dy, const void *dr_out, const void *a
     float *parts = reinterpret_cast<float *>(ws + w.parts);
     float *ends = reinterpret_cast<float *>(ws + w.ends);
     const unsigned strips = static_cast<unsigned>((c.cols + 255) / 256);
-    Chunks ch{c.rows, c.gate != nullptr ? c.gate_rows : c.rows, 0};
+    Chunks ch{c.rows, c.gate != nullptr ? c.gate_rows : c.rows, 0, w.room};
     int shared = 1;  // units that share a chunk
     cudaError_t e;
     if (in_registers(c.cols)) {

@@ -152,10 +152,12 @@ struct Slots {
     uint32_t issued;
     int next;
     bool ok;  // no wait has run out
+    unsigned *status;
 
     __device__ __forceinline__ void start(uint8_t *memory, uint64_t *bars, int n, int64_t columns, int64_t rows,
-                                          const Slice &s, int s0)
+                                          const Slice &s, int s0, unsigned *word)
     {
+        status = word;
         shift = s0;
         mem = memory;
         full = bars;
@@ -207,6 +209,10 @@ struct Slots {
             ba = whole<TA>(b) * sizeof(TA);
             br = whole<TR>(b) * sizeof(TR);
         }
+        if (ba > 0 && !in_range(fa, ba / sizeof(TA), total, status))
+            ba = 0u;
+        if (br > 0 && !in_range(fr, br / sizeof(TR), total, status))
+            br = 0u;
         uint32_t bytes = 0;
 #pragma unroll
         for (int i = 0; i < NA; ++i)
@@ -263,14 +269,14 @@ struct Slots {
             const int64_t e = end - wa.tail + t;
 #pragma unroll
             for (int i = 0; i < NA; ++i)
-                if (a[i] != nullptr)
+                if (a[i] != nullptr && in_range(e, 1, total, status))
                     reinterpret_cast<TA *>(at_a(c, i))[e - wa.first] = a[i][e];
         }
         if (t < wr.tail) {
             const int64_t e = end - wr.tail + t;
 #pragma unroll
             for (int i = 0; i < NR; ++i)
-                if (r[i] != nullptr)
+                if (r[i] != nullptr && in_range(e, 1, total, status))
                     reinterpret_cast<TR *>(at_r(c, i))[e - wr.first] = r[i][e];
         }
         __syncthreads();
@@ -287,13 +293,13 @@ struct Slots {
         if (wa + t < end) {
 #pragma unroll
             for (int i = 0; i < NA; ++i)
-                if (a[i] != nullptr)
+                if (a[i] != nullptr && in_range(b + wa + t, 1, total, status))
                     reinterpret_cast<TA *>(at_a(c, i))[wa + t] = a[i][b + wa + t];
         }
         if (wr + t < end) {
 #pragma unroll
             for (int i = 0; i < NR; ++i)
-                if (r[i] != nullptr)
+                if (r[i] != nullptr && in_range(b + wr + t, 1, total, status))
                     reinterpret_cast<TR *>(at_r(c, i))[wr + t] = r[i][b + wr + t];
         }
         __syncthreads();
@@ -400,17 +406,18 @@ struct Param<E, true> {
     __device__ __forceinline__ void word(int i, uint32_t bf) { w[i] = bf; }
 };
 
-// The slice of a row of parameters in global memory that begins at element `row`, of
-// type T; 0 past the slice.
+// The slice of a row of parameters in global memory that begins at element `row` of
+// `total`, of type T; 0 past the slice.
 template <int MODE, int E, typename T, typename P>
-__device__ __forceinline__ void take_typed(const T *p, int64_t row, const Place<MODE, E> &pl, P &out)
+__device__ __forceinline__ void take_typed(const T *p, int64_t row, const Place<MODE, E> &pl, P &out, int64_t total,
+                                           unsigned *status)
 {
     const int64_t at = row + pl.first;
     if constexpr (MODE == kFull || MODE == kVec) {
 #pragma unroll
         for (int u = 0; u < E / 8; ++u) {
             const int c = vec_col(u);
-            if (!vec_in<MODE>(c, pl.n))
+            if (!vec_in<MODE>(c, pl.n) || !in_range(at + c, 8, total, status))
                 continue;
             const uint4 *q = reinterpret_cast<const uint4 *>(p + at + c);
             const uint4 v = __ldg(q);
@@ -432,10 +439,10 @@ __device__ __forceinline__ void take_typed(const T *p, int64_t row, const Place<
         for (int j = 0; j < E; ++j) {
             v[j] = T(0.0f);
             if constexpr (MODE == kShift) {
-                if (pl.has(j / 8, j & 7))
+                if (pl.has(j / 8, j & 7) && in_range(at + vec_col(j / 8) - pl.s + (j & 7), 1, total, status))
                     v[j] = __ldg(p + at + vec_col(j / 8) - pl.s + (j & 7));
             } else {
-                if (elem_col(j) < pl.n)
+                if (elem_col(j) < pl.n && in_range(at + elem_col(j), 1, total, status))
                     v[j] = __ldg(p + at + elem_col(j));
             }
         }
@@ -447,7 +454,7 @@ __device__ __forceinline__ void take_typed(const T *p, int64_t row, const Place<
 // The same of bf16 or fp32 (BF: bf16); `none` throughout where there is no parameter.
 template <int MODE, int E, bool BF>
 __device__ __forceinline__ void take_param(const void *p, int f32, int64_t row, const Place<MODE, E> &pl,
-                                           float none, Param<E, BF> &out)
+                                           float none, Param<E, BF> &out, int64_t total, unsigned *status)
 {
 #pragma unroll
     for (int i = 0; i < E / 2; ++i)
@@ -455,9 +462,9 @@ __device__ __forceinline__ void take_param(const void *p, int f32, int64_t row, 
     if (p == nullptr)
         return;
     if (!BF && f32)
-        take_typed<MODE, E>(static_cast<const float *>(p), row, pl, out);
+        take_typed<MODE, E>(static_cast<const float *>(p), row, pl, out, total, status);
     else
-        take_typed<MODE, E>(static_cast<const __nv_bfloat16 *>(p), row, pl, out);
+        take_typed<MODE, E>(static_cast<const __nv_bfloat16 *>(p), row, pl, out, total, status);
 }
 
 // One value to `p`, rounded to T.
@@ -532,10 +539,14 @@ __host__ __device__ __forceinline__ int64_t sums_pitch(int64_t cols)
     return cols % 8 == 0 ? cols : (cols + 7 + 7) / 8 * 8;
 }
 
-// The thread's columns of a row of sums that begins at `row`.
+// The thread's columns of a row of sums that begins at element `at` of `total`.
 template <int MODE, int E>
-__device__ __forceinline__ void give_sums(float *row, const Place<MODE, E> &pl, const float2 (&f)[E / 2])
+__device__ __forceinline__ void give_sums(float *sums, int64_t at, int64_t total, const Place<MODE, E> &pl,
+                                          const float2 (&f)[E / 2], unsigned *status)
 {
+    if (pl.n > 0 && !in_range(at + pl.first, pl.n, total, status))
+        return;
+    float *row = sums + at;
     if constexpr (MODE == kShift) {
 #pragma unroll
         for (int u = 0; u < E / 8; ++u) {
@@ -550,12 +561,14 @@ __device__ __forceinline__ void give_sums(float *row, const Place<MODE, E> &pl, 
         give<MODE, E>(row + pl.first, pl, f);
     }
 }
-// Or of one of a gradient of type `f32` (else bf16), not of kShift's.
+// Or of one of a gradient of `total` elements, of type `f32` (else bf16), not of kShift's.
 template <int MODE, int E>
 __device__ __forceinline__ void give_param(void *p, int f32, int64_t row, const Place<MODE, E> &pl,
-                                           const float2 (&f)[E / 2])
+                                           const float2 (&f)[E / 2], int64_t total, unsigned *status)
 {
     static_assert(MODE != kShift, "these leave sums");
+    if (pl.n > 0 && !in_range(row + pl.first, pl.n, total, status))
+        return;
     if (f32)
         give<MODE, E>(static_cast<float *>(p) + row + pl.first, pl, f);
     else

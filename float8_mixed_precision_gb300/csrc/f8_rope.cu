@@ -19,6 +19,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <cstdlib>
 
 #include "f8_internal.h"
 #include "f8_ptx.cuh"
@@ -41,10 +42,32 @@ struct Div {
     }
 };
 
+// The elements that a call may touch, around its pointer: for the checked build.
+struct Span {
+    int64_t lo, n;
+    __device__ __forceinline__ bool holds(int64_t i, int len, unsigned *status) const
+    {
+        return in_range(i - lo, len, n, status);
+    }
+};
+
+// Of up to three dimensions, `last` dense elements in each place.
+Span span_of(const int64_t (&sizes)[3], const int64_t (&strides)[3], int64_t last)
+{
+    Span s{0, last};
+    for (int i = 0; i < 3; ++i) {
+        const int64_t far = (sizes[i] - 1) * strides[i];
+        s.lo += std::min<int64_t>(far, 0);
+        s.n += std::abs(far);
+    }
+    return s;
+}
+
 struct Tensor {
     const void *x;
     void *out;
     int64_t x_batch, x_seq, x_head, out_batch, out_seq, out_head;
+    Span x_span, out_span;
 };
 
 struct Args {
@@ -62,6 +85,8 @@ struct Args {
     const double *freqs;
     float scale;
     int inverse;
+    Span pos_span;
+    unsigned *status;
     Div by_units, by_heads, by_half;  // by_units of min(units, threads)
 };
 
@@ -199,7 +224,8 @@ rope_kernel(const __grid_constant__ Args a)
     const int nrows = static_cast<int>(min(static_cast<int64_t>(a.rows_per_block), a.rows - row0));
     if (threadIdx.x < nrows) {
         const int64_t row = row0 + threadIdx.x, b = row / a.seq, s = row - b * a.seq;
-        at[threadIdx.x] = a.pos[b * a.pos_batch + s * a.pos_seq];
+        const int64_t p = b * a.pos_batch + s * a.pos_seq;
+        at[threadIdx.x] = a.pos_span.holds(p, 1, a.status) ? a.pos[p] : -1;
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
             base[threadIdx.x][2 * k] = b * a.t[k].x_batch + s * a.t[k].x_seq;
@@ -210,6 +236,8 @@ rope_kernel(const __grid_constant__ Args a)
     float *const cosines = turn, *const sines = turn + a.rows_per_block * a.half;
     for (int p = threadIdx.x; p < a.half * nrows; p += kThreads) {
         const int j = static_cast<int>(a.by_half(p));
+        if (!in_range(p - j * a.half, 1, a.half, a.status) || !in_range(j, 1, nrows, a.status))
+            continue;
         const double f = a.freqs[p - j * a.half];
         const uint64_t angle = turn_fraction(f) * static_cast<uint64_t>(at[j]);
         float t = static_cast<float>(static_cast<int32_t>(angle >> 32)) * 0x1p-31f;  // half turns
@@ -237,8 +265,15 @@ rope_kernel(const __grid_constant__ Args a)
             const int k = h >= a.heads0 ? 1 : 0;
             h -= k ? a.heads0 : 0;
             const Tensor &t = a.t[k];
-            const T *x = static_cast<const T *>(t.x) + base[j][2 * k] + h * t.x_head;
-            T *o = static_cast<T *>(t.out) + base[j][2 * k + 1] + h * t.out_head;
+            const int64_t xo = base[j][2 * k] + h * t.x_head, oo = base[j][2 * k + 1] + h * t.out_head;
+            const T *x = static_cast<const T *>(t.x) + xo;
+            T *o = static_cast<T *>(t.out) + oo;
+            if (!in_range(c0, VEC, a.dim, a.status) || !t.x_span.holds(xo + c0, VEC, a.status) ||
+                !t.out_span.holds(oo + c0, VEC, a.status))
+                continue;
+            if (second && (!in_range(c1, VEC, a.dim, a.status) || !t.x_span.holds(xo + c1, VEC, a.status) ||
+                           !t.out_span.holds(oo + c1, VEC, a.status)))
+                continue;
             V v0 = *reinterpret_cast<const V *>(x + c0), v1 = v0;
             if (second)
                 v1 = *reinterpret_cast<const V *>(x + c1);
@@ -382,7 +417,10 @@ f8_status f8_rope(const f8_rope_tensor *tensors, int count, f8_dtype type, int64
     Args a = {};
     for (int i = 0; i < count; ++i) {
         const f8_rope_tensor &t = tensors[i];
-        a.t[i] = Tensor{t.x, t.out, t.x_batch, t.x_seq, t.x_head, t.out_batch, t.out_seq, t.out_head};
+        const int64_t sizes[3] = {batch, seq, std::max<int64_t>(t.heads, 1)};
+        a.t[i] = Tensor{t.x, t.out, t.x_batch, t.x_seq, t.x_head, t.out_batch, t.out_seq, t.out_head,
+                        span_of(sizes, {t.x_batch, t.x_seq, t.x_head}, dim),
+                        span_of(sizes, {t.out_batch, t.out_seq, t.out_head}, dim)};
     }
     a.heads0 = static_cast<int>(tensors[0].heads);
     a.heads = static_cast<int>(heads);
@@ -396,6 +434,8 @@ f8_status f8_rope(const f8_rope_tensor *tensors, int count, f8_dtype type, int64
     a.freqs = freqs;
     a.scale = scale;
     a.inverse = inverse != 0;
+    a.pos_span = span_of({batch, seq, 1}, {pos_batch, pos_seq, 0}, 1);
+    a.status = dev->status;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const bool half = layout == F8_ROPE_HALF;
     if (type == F8_BF16)
