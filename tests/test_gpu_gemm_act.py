@@ -335,3 +335,44 @@ def test_bwd_empty(f8):
     assert dz.shape == (0, 64) and torch.equal(db, torch.zeros_like(db))
     e = torch.zeros((4, 0), dtype=BF, device=DEV)
     assert f8.f8_act_bwd(e, e, f8.F8_ACT_SILU)[1].shape == (0,)
+
+
+# ---------------------------------------------------------------- past 2^31 elements
+def test_past_2_31_elements_odd_rows(f8):
+    """Outputs, residual and kept input past 2^31 elements, of rows that no TMA box takes: the last rows are those of a
+    call of their own."""
+    M, N, K = 16400, 131077, 16
+    a, sa, b, sb, bias, _ = _inputs(M, N, K, 81)
+    y = torch.empty((M, N), dtype=BF, device=DEV)
+    z = torch.empty_like(y)
+    gen = torch.Generator(device=DEV).manual_seed(82)
+    last = torch.randn((300, N), generator=gen, device=DEV).to(BF)
+    y.zero_()
+    y[-300:] = last
+    f8.f8_gemm_act(a, b, sa, sb, bias=bias, act=f8.F8_ACT_GELU, residual=y, y=y, z=z)   # in place
+    assert y.numel() > 1 << 31
+    y1, z1 = f8.f8_gemm_act(a[-300:].contiguous(), b, sa, sb, bias=bias, act=f8.F8_ACT_GELU, residual=last, want_z=True)
+    assert torch.equal(y[-300:], y1) and torch.equal(z[-300:], z1)
+    y0, z0 = f8.f8_gemm_act(a[:300].contiguous(), b, sa, sb, bias=bias, act=f8.F8_ACT_GELU, residual=torch.zeros_like(last),
+                            want_z=True)
+    assert torch.equal(y[:300], y0) and torch.equal(z[:300], z0)
+    assert f8.f8_last_device_status() == 0
+
+
+@pytest.mark.parametrize("cols", [8200, 8195])
+def test_bwd_past_2_31_elements(f8, cols):
+    """The gradient's last rows are those of a call of their own, and the bias's is theirs: the others' dy is 0."""
+    rows = (1 << 18) + 77
+    gen = torch.Generator(device=DEV).manual_seed(83)
+    z, dy = torch.empty((rows, cols), dtype=BF, device=DEV), torch.zeros((rows, cols), dtype=BF, device=DEV)
+    z.fill_(0.5)
+    for t in (z, dy):
+        t[-200:] = torch.randn((200, cols), generator=gen, device=DEV).to(BF)
+    assert z.numel() > 1 << 31
+    want, _ = f8.f8_act_bwd(dy[-200:].clone(), z[-200:].clone(), f8.F8_ACT_GELU)
+    _, _, _, bound = ref.act_bwd(dy[-200:], z[-200:], "gelu")
+    exact = ref.act_bwd(dy[-200:], z[-200:], "gelu")[1]
+    dz, db = f8.f8_act_bwd(dy, z, f8.F8_ACT_GELU, dz=dy, bias_dtype=torch.float32)
+    assert torch.equal(dz[-200:], want) and not dz[:-200].any()
+    check(db, exact, bound + rounding(exact, torch.float32), "dbias")
+    assert f8.f8_last_device_status() == 0

@@ -341,3 +341,43 @@ def test_past_2_31_elements(f8):
     want = f8.f8_residual_norm_fwd(s["a"], s["r"], s["w_pre"], b_pre=s["b_pre"], **kw)
     got = f8.f8_residual_norm_fwd(a, r, s["w_pre"], b_pre=s["b_pre"], r_out=r, y=a, **kw)
     assert a.numel() > 1 << 31 and torch.equal(got[0][-1:], want[0]) and torch.equal(got[1][-1:], want[1])
+
+
+@pytest.mark.parametrize("layer", [True, False], ids=["layer", "rms"])
+@pytest.mark.parametrize("cols, rt", [(4100, F32), (4099, BF), (4097, F32), (16391, BF)])
+def test_past_2_31_elements_both_passes(f8, cols, rt, layer):
+    """Rows of both passes past 2^31 elements, odd widths and those past the register path among them: the last rows are
+    the definition's, and as the gradients of the others are 0, so are the sums.  (The order in which a row of an odd width
+    is summed goes by where it starts in the tensor's vectors, so a call of these rows alone may differ in a last bit.)"""
+    rows, some = (1 << 31) // cols + 77, 50
+    s = _inputs(some, cols, BF, rt, gate_rows=some, seed=cols)
+    kw = _kw(f8, s, layer, 0.75)
+
+    def long(t, fill):
+        v = torch.full((rows, cols), fill, dtype=t.dtype, device=DEV)
+        v[-some:] = t
+        return v
+    a, r = long(s["a"], 0.25), long(s["r"], -1.0)
+    assert a.numel() > 1 << 31
+    one = kw | {"gate_rows": rows}
+    y = torch.empty_like(a)
+    r_out, y, stats = f8.f8_residual_norm_fwd(a, r, s["w_pre"], b_pre=s["b_pre"], eps=EPS, r_out=r, y=y, **one)
+    want = ref.residual_norm_fwd(s["a"], s["r"], s["w_pre"], s["b_pre"], s["w_post"], s["b_post"], s["gate"], some, 0.75,
+                                 layer, EPS)
+    for name, got in (("r_out", r_out), ("y", y)):
+        v, b = want[name]
+        check(got[-some:], v, b + rounding(v, got.dtype), name)
+    for i, name in enumerate(STATS):
+        if layer or not name.startswith("mean"):
+            check(stats[i, -some:], *want[name], name)
+    dy, dr_out = long(s["dy"], 0.0), long(s["dr_out"], 0.0)
+    grads = f8.f8_residual_norm_bwd(dy, dr_out, a, r_out, s["w_pre"], stats, want=_all(s), da=y, **one)
+    want = ref.residual_norm_bwd(s["dy"], s["dr_out"], s["a"], r_out[-some:], stats[:, -some:], s["w_pre"], s["w_post"],
+                                 s["b_post"], s["gate"], some, 0.75, layer)
+    for name, got in zip(GRADS, grads):
+        v, b = want[name]
+        if name in ("da", "dr"):
+            assert not got[:-some].any(), name
+            got = got[-some:]
+        check(got, v.reshape(got.shape), (b + rounding(v, got.dtype)).reshape(got.shape), name)
+    assert f8.f8_last_device_status() == 0
