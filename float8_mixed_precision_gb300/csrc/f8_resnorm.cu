@@ -1121,14 +1121,12 @@ Call call_of(const f8_residual_norm &n, float *stats)
 constexpr std::true_type yes;
 constexpr std::false_type no;
 
-// f(mode) for the rows' width.
-template <typename F>
-cudaError_t by_mode(int64_t cols, const Plan &p, int e, bool shift, F f)
+// f(mode) for the rows' width, ODD that of a width of no whole vectors.
+template <int ODD, typename F>
+cudaError_t by_mode(int64_t cols, const Plan &p, int e, F f)
 {
-    if (cols % 8 != 0 && shift)
-        return f(std::integral_constant<int, rows::kShift>());
     if (cols % 8 != 0)
-        return f(std::integral_constant<int, rows::kRagged>());
+        return f(std::integral_constant<int, ODD>());
     if (p.ranks == 1 && cols == static_cast<int64_t>(p.threads) * e)
         return f(std::integral_constant<int, rows::kFull>());
     return f(std::integral_constant<int, rows::kVec>());
@@ -1220,6 +1218,13 @@ cudaError_t fwd_rows(const Call &c, const void *a, const void *r, void *r_out, v
                               amax, chunk, p.ranks, p.slice, s.stages, wait_limit_ns(), dev.status);
 }
 
+// Widths of no whole vectors go by the tensors' own vectors (kShift) where all parameters
+// are bf16 and stay in registers over the rows, element by element (kRagged) where one is
+// fp32: each row then reads them again, which kShift's lanes do in eight scattered pieces.
+// RMS / layer norm, fp32 weights, element by element against vectors: 8192 x 4095 181 / 225
+// us against 174 / 246, 1999 x 5003 53 / 64 against 55 / 76, 8192 x 1001 45 / 57 against 42 /
+// 64, 1999 x 12001 150 / 189 against 153 / 243; bf16 weights in vectors 102 / 127, 33 / 40, 27
+// / 33 and 92 / 132.
 template <typename TA, typename TR>
 cudaError_t fwd(const Call &c, const void *a, const void *r, void *r_out, void *y, unsigned *amax,
                 const DeviceInfo &dev, cudaStream_t st)
@@ -1227,7 +1232,7 @@ cudaError_t fwd(const Call &c, const void *a, const void *r, void *r_out, void *
     if (in_registers(c.cols)) {
         const Plan p = fwd_plan(c.cols);
         auto run = [&](auto bf, auto threads) {
-            return by_mode(c.cols, p, kFwdE, bf.value, [&](auto mode) {
+            return by_mode<bf.value ? rows::kShift : rows::kRagged>(c.cols, p, kFwdE, [&](auto mode) {
                 return fwd_rows<TA, TR, mode.value, bf.value, threads.value>(c, a, r, r_out, y, amax, dev, st);
             });
         };
@@ -1292,7 +1297,7 @@ cudaError_t bwd(const Call &c, const void *dy, const void *dr_out, const void *a
         const bool full = c.layer || c.b_post != nullptr || g.db_pre != nullptr || g.db_post != nullptr;
         const Plan p = bwd_plan(c.cols);
         auto run = [&](auto all, auto threads) {
-            return by_mode(c.cols, p, kBwdE, true, [&](auto mode) {
+            return by_mode<rows::kShift>(c.cols, p, kBwdE, [&](auto mode) {
                 return bwd_rows<TA, TR, mode.value, all.value, threads.value>(c, ch, &shared, dy, dr_out, a, r_out,
                                                                               g, parts, ends, dev, st);
             });

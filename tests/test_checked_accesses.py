@@ -81,3 +81,12 @@ def test_statistics_go_through_their_checks():
     with open(os.path.join(CSRC, "f8_resnorm.cu")) as f:
         text = f.read()
     assert re.search(r"\bc\.stats\[", text) is None and text.count("c.stat(") >= 12 and text.count("c.put_stat(") == 8
+
+
+def test_forward_kernels_that_no_call_reaches():
+    """The residual norm's rule for widths of no whole vectors is a template argument: a mode chosen at run time would
+    build the kernels of both for every kind of parameter, half of them never launched."""
+    with open(os.path.join(CSRC, "f8_resnorm.cu")) as f:
+        text = f.read()
+    assert "by_mode<bf.value ? rows::kShift : rows::kRagged>" in text and "by_mode<rows::kShift>" in text
+    assert re.search(r"by_mode\(", re.sub(r"by_mode\(int64_t cols", "", text)) is None
