@@ -31,6 +31,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <iterator>
 #include <mutex>
 #include <type_traits>
 
@@ -1445,6 +1446,13 @@ f8_status f8_residual_norm_bwd(const f8_residual_norm *n, const void *dy, const 
         !aligned(g.db_pre, 16) || !aligned(g.dw_post, 16) || !aligned(g.db_post, 16) ||
         !aligned(g.dgate, 16) || !aligned(workspace, 16))
         return F8_ERR_ALIGN;
+    // rows are read again for several sums, and partial sums are joined after the rows: an
+    // output in the place of an input or of another output would be read or lost
+    const void *const outs[] = {g.da, g.dr, g.dw_pre, g.db_pre, g.dw_post, g.db_post, g.dgate};
+    const void *const ins[] = {dy, dr_out, a, r_out, stats, n->w_pre, n->b_pre, n->w_post, n->b_post, n->gate};
+    for (const void *const *o = outs; some && o != std::end(outs); ++o)
+        if (*o != nullptr && (std::find(ins, std::end(ins), *o) != std::end(ins) || std::find(outs, o, *o) != o))
+            return F8_ERR_INVALID;
     const DeviceInfo *dev;
     F8_TRY(get_device(&dev));
     cudaStream_t st = static_cast<cudaStream_t>(stream);

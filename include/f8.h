@@ -931,8 +931,9 @@ f8_status f8_residual_norm_fwd(const f8_residual_norm *n, const void *a, const v
  * (means over the row, without mean(dy w_pre) and mean(du w_post) for F8_RMS_NORM).
  *   dy, a, da: of x_type;  dr_out, r_out, dr: of r_type;  dw_*, db_*: [cols] of
  *   w_type;  dgate: as gate.  Every output may be NULL (dw_post, db_post only
- *   without w_post, dgate only without gate).  No output may be an input.  For no
- *   rows the parameters' gradients are 0, and dgate, then of no rows, is not touched.
+ *   without w_post, dgate only without gate).  No output may be an input or another
+ *   output.  For no rows the parameters' gradients are 0, and dgate, then of no rows,
+ *   is not touched.
  *   workspace: f8_residual_norm_bwd_workspace_bytes(rows, cols) bytes, 16-byte
  *   aligned.
  * Sums over rows are formed in a fixed order: equal inputs give equal bits.

@@ -361,3 +361,18 @@ def test_rope_of_nothing(L):
         one = _rope_args(out=P, heads=1, x_batch=9, out_batch=8, x_head=5, out_head=0, out_seq=512)
         assert L.f8_rope(*args(one, 1, 1, 5)) not in (INVALID, SHAPE, ALIGN)
         assert L.f8_rope(*args(one, 1, 2, 5)) == INVALID
+
+
+def test_gradients_in_one_place_are_refused(L):
+    """No gradient may lie in the place of an input or of another gradient."""
+    grads = lambda **kw: ctypes.byref(binding._ResidualNormGrads(**kw))  # noqa: E731
+    n = _norm_args(w_pre=11 * P, b_pre=12 * P, w_post=13 * P, b_post=14 * P, gate=15 * P)
+    every = {k: (20 + i) * P for i, k in enumerate(("da", "dr", "dw_pre", "db_pre", "dw_post", "db_post", "dgate"))}
+    call = lambda **kw: L.f8_residual_norm_bwd(n, P, 2 * P, 3 * P, 4 * P, 5 * P, grads(**(every | kw)), 6 * P, 1 << 30, None)  # noqa: E731
+    inputs = [i * P for i in (1, 2, 3, 4, 5, 11, 12, 13, 14, 15)]
+    for i, name in enumerate(every):
+        for place in inputs + [v for k, v in every.items() if k != name]:
+            assert call(**{name: place}) == INVALID, (name, place // P)
+    if not torch.cuda.is_available():  # the addresses are not to be read
+        assert call() not in (INVALID, SHAPE, ALIGN)
+        assert call(da=None, dr=None, dw_post=None, db_post=None) not in (INVALID, SHAPE, ALIGN)
