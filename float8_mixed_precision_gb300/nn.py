@@ -745,8 +745,9 @@ class ResidualNorm(torch.nn.Module):
     next block's input, in one pass.  kind "rms" or "layer" for both norms;
     `post` False leaves a as it is; layer norms have biases.  The gate is given
     with each call: [dim], or [groups, dim] where each gate is that of as many
-    consecutive rows (a [batch, seq, dim] with a gate [batch, dim]).  r may be fp32
-    beside a bf16 a."""
+    consecutive rows (a [batch, seq, dim] with a gate [batch, dim], or [batch, 1, dim];
+    a gate for each place of every sequence, [1, seq, dim], is to be expanded).  r may
+    be fp32 beside a bf16 a."""
 
     def __init__(self, dim: int, kind: str = "rms", post: bool = True, scale: float = 1.0, eps: float = 1e-5,
                  device=None, dtype=torch.bfloat16):
@@ -773,6 +774,12 @@ class ResidualNorm(torch.nn.Module):
         if gate is not None:
             if gate.dim() < 1 or gate.shape[-1] != self.dim:
                 raise ValueError(f"the gate must have {self.dim} features")
+            lead = list(gate.shape[:-1])
+            while lead and lead[-1] == 1:
+                lead.pop()
+            # a gate of one for all of a's leading dimensions but some ahead would go by other rows than its own
+            if min(gate.dim(), a.dim()) > 2 and tuple(lead) != tuple(a.shape[:len(lead)]):
+                raise ValueError("a gate's leading dimensions must be a's first ones, with ones behind them")
             groups = gate.numel() // self.dim
             if rows > 0 and (groups < 1 or rows % groups):
                 raise ValueError("the rows must be a multiple of the gates")

@@ -376,3 +376,22 @@ def test_gradients_in_one_place_are_refused(L):
     if not torch.cuda.is_available():  # the addresses are not to be read
         assert call() not in (INVALID, SHAPE, ALIGN)
         assert call(da=None, dr=None, dw_post=None, db_post=None) not in (INVALID, SHAPE, ALIGN)
+
+
+@pytest.mark.parametrize("lead, gate, ok", [
+    ((3, 10), (3, 1), True), ((3, 10), (3, 10), True), ((3, 10), (1, 1), True), ((3, 10), (3,), True), ((3, 10), (), True),
+    ((2, 3, 4), (2, 3), True), ((2, 3, 4), (2, 1, 1), True), ((2, 3, 4), (2, 3, 1), True), ((30,), (10,), True),
+    ((3, 10), (1, 10), False), ((10, 10), (1, 10), False), ((2, 3, 4), (1, 3, 4), False), ((2, 3, 4), (2, 1, 4), False),
+    ((2, 3, 4), (3, 4), False), ((4, 4), (2, 2), False)])
+def test_gates_that_broadcast_otherwise_are_refused(rec, lead, gate, ok):
+    """Each gate is that of consecutive rows: a gate whose dimensions would stand for other rows (one for each place of
+    every sequence, [1, seq, dim]) is refused, not taken as one for each group of rows."""
+    from float8_mixed_precision_gb300 import nn
+    m, a, g = nn.ResidualNorm(64), _bf(*lead, 64), _bf(*gate, 64)
+    if ok:
+        m(a, a, g)
+    else:
+        with pytest.raises(ValueError, match="leading dimensions"):
+            m(a, a, g)
+    if len(gate) == len(lead) and all(n in (1, k) for n, k in zip(gate, lead)):
+        m(a, a, g.expand(*lead, 64))
