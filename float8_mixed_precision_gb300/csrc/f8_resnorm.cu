@@ -21,10 +21,11 @@
 // reduction 8192 x 4096 took 327 us forward and 482 backward.  What is left is the
 // arithmetic, some 600 instructions a warp and row forward, with two rows in work an SM.
 //
-// Measured, bf16, gates of 1024 rows: 8192 x 4096 layer norm forward 58 us, 4.6 TB/s;
-// RMS norm backward with every gradient 79 us, 5.1 TB/s; a plain copy runs at 6.8.  1999 x
-// 5003 with an fp32 stream and layer norms, backward, 71 us of 26.5 for the bytes: one
-// row is in work an SM, an odd width's on every eighth row.
+// Measured, bf16: 8192 x 4096 layer norm forward, gates of 1024 rows, 60 us, 4.5 TB/s;
+// RMS norm backward with every gradient 79 us, 5.1 TB/s, with one gate for all rows, and 82
+// with gates of 1024; a plain copy runs at 6.8.  1999 x 5003 with an fp32 stream, layer
+// norms and gates of 250 rows, backward, 71 us of 26.5 for the bytes: one row is in work an
+// SM, and where 8 does not divide the width, of a unit's every eighth row.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -1053,7 +1054,8 @@ Plan plan_of(int64_t cols, int e, int most = kThreads)
 
 // Forward, rows of 4097 to 5120 columns go by two blocks of 320 threads an SM at 96
 // registers, not one at 128: 8192 x 5120 layer norm 82 us against 109, RMS norm 66 against
-// 72, 8192 x 4095 131 against 174.
+// 72, 8192 x 4095 131 against 174 (some 5 us of each are the measuring's).  At 96 registers
+// whole vectors' kernels spill 48 to 56 bytes, kShift's 176 to 264.
 constexpr int kPairThreads = 320;
 bool pair_blocks(int64_t cols)
 {
@@ -1071,7 +1073,7 @@ Plan fwd_plan(int64_t cols)
 // little over half of them, or a row take a cluster: 8192 x 2560 layer norm 74 us against
 // 93, 8192 x 2047 97 against 117, 8192 x 5120 130 against 213.  Elsewhere the registers
 // are worth more: 8192 x 4096 103 us against 111, 8192 x 2048 62 against 68, 8192 x 1536
-// (three blocks instead of two) 56 against 56.
+// (three blocks instead of two) 56 against 56 (some 5 us of each are the measuring's).
 constexpr int kWideThreads = 640;
 bool wide_block(int64_t cols)
 {

@@ -6,7 +6,10 @@
 // and walks the rows' heads, moving two vectors of VEC elements that hold VEC whole
 // pairs.  Addresses are the larger part of its instructions: with a place and a head
 // worked out per unit, and the rows' starts by division, 8192 rows of 32 + 8 heads of 128
-// (96 turned, out of a packed projection) took 34.6 us; so 30.0, 5.6 TB/s.
+// (96 turned, out of a packed projection) took 34.6 us; so 30.3, 5.5 TB/s.  Dense, halves
+// of whole heads 38 us against 31 interleaved.  Units are as wide as rot / 2 lets them be: 8
+// bytes for heads of 96 with 24 turned (31 us halves, 27 interleaved, of 18.5 for the
+// bytes), 4 for heads of 80 with 20 turned (41 of 15.5).
 //
 // The angle: a frequency becomes a fraction of a turn in 64-bit fixed point, so
 // position * fraction mod 2^64 is the angle's fraction of a turn, exactly; its upper

@@ -903,12 +903,16 @@ f8_status f8_rope_frequencies(int64_t rot, double base, f8_rope_scaling scaling,
  *           or NULL; needs x_type F8_BF16; zeroed by the call.  A non-finite y then
  *           sets F8_ERR_NONFINITE.
  * rows, cols >= 0; cols < 2^30, rows * cols < 2^60; eps >= 0; scale finite.  All
- * tensors 16-byte aligned, stats and amax_out 4-byte.  Rows of up to 16384 columns (odd
- * widths: 16377) are read once; the fastest widths are 512 times a power of two, forward up to 8192 and
- * backward up to 4096.  Wider rows (backward above 5120, forward above 8192)
- * take several blocks, and those past 16384 columns are read again for each sum.  Odd
- * widths take up to twice the time of even ones, those with gates of fewer rows than a
- * block walks (rows / 300 or so) backward up to three times.
+ * tensors 16-byte aligned, stats and amax_out 4-byte.  Rows of up to 16384 columns
+ * (16377 where 8 does not divide them) are read once; the fastest widths are 512 times a
+ * power of two, forward up to 8192 and backward up to 4096.  Wider rows (backward above
+ * 5120, forward above 8192) take several blocks, and those past 16384 columns are read
+ * again for each sum, at about four times the time.  Widths that are no multiple of 8
+ * take 2.1 times the time of the fastest forward and 1.6 times backward (1.5 and 1.25
+ * times that of their neighbours); forward with an fp32 weight or gate 3.8 times, and
+ * backward with gates of less than some 38th of the rows 2.2 times what those gates take
+ * at a multiple of 8.  The order of a row's sums goes by row * cols mod 8 at such widths:
+ * equal rows may differ in a last bit.
  */
 typedef struct {
     f8_norm kind;
