@@ -239,7 +239,8 @@ def f8_residual_norm_fwd(a: torch.Tensor, r: torch.Tensor, w_pre: torch.Tensor,
     a: r_out = scale r + gate norm(a; w_post, b_post) and y = norm(r_out; w_pre,
     b_pre), the next block's input.  Without w_post a is not normed.  gate [ceil(rows
     / gate_rows), cols], one row for each gate_rows rows (default: one, or [cols], for
-    all; any number for no rows).  r may be fp32 beside a bf16 a.  stats fp32 [4, rows] is the backward's."""
+    all; any number for no rows).  r may be fp32 beside a bf16 a.  stats fp32 [4, rows]
+    is the backward's."""
     what = "f8_residual_norm_fwd"
     n = _residual_norm(what, a, r, w_pre, b_pre, w_post, b_post, gate, gate_rows, scale, kind, eps)
     shape, at, xt, rt = a.shape, a.get_device(), a.dtype, r.dtype
